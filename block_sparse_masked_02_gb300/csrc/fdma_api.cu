@@ -188,6 +188,8 @@ int classify_into_workspace(const fdma_args* a, int8_t* user_map, cudaStream_t s
 
 }  // namespace
 
+int* paged_error_word() { return device_error_word(); }
+
 WorkspaceLayout workspace_layout(int B, int Nq, int Nk, int Hq, int Hkv, int d) {
   WorkspaceLayout w{};
   const size_t nTq = static_cast<size_t>(cdiv(Nq, kTile)), nTk = static_cast<size_t>(cdiv(Nk, kTile));

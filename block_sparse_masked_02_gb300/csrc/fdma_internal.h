@@ -141,6 +141,8 @@ struct TopkParams {
   uint8_t* mask_u8;        // (B,Hkv,Nq,Nk) contiguous, or nullptr
 };
 
+// The current device's error word, for the entry points outside fdma_api.cu (nullptr on failure).
+int* paged_error_word();
 cudaError_t launch_classify(const ClassifyParams& p, cudaStream_t stream);
 // bf16 masks through a tensor map of the mask (4D, 64 x 128 box, 128-byte swizzle).
 cudaError_t launch_classify_tma1(const CUtensorMap& tm, const ClassifyParams& p, cudaStream_t stream);

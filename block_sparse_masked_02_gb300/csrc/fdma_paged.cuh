@@ -1,0 +1,297 @@
+// What the kernels over a paged key/value cache share: their parameter block, the
+// key tiles that a group of query rows sees, and the division of all those tiles
+// into equal runs, one per CTA.
+//
+// An item is one (sequence, kv head, block of ROWS packed query rows); a packed row
+// is (token, head of the group), the group's heads of one token next to each other,
+// so that one token's heads share the keys that are fetched for them.  An item's key
+// tiles are kKeyTile wide and aligned to multiples of it: first the tiles that hold
+// visible sinks, then the tiles from the window's lower edge (or 0) to the last
+// visible key.  All items' tiles, in the order (sequence, kv head, row block, tile),
+// form one line that is cut into runs of equal length, one for each CTA: ragged
+// batches, causal chunks and one very long sequence all load the machine evenly, and
+// what is needed of the workspace does not depend on any length.  A CTA's run ends
+// inside an item at most twice (its first item may have begun in an earlier CTA, its
+// last may go on in the next ones); those pieces go to the workspace as fp32 sums with
+// their running maximum and weight and are joined by a second kernel.
+#pragma once
+
+#include "../../include/fdma_paged.h"
+#include "fdma_internal.h"
+#include "fdma_ptx.cuh"
+
+namespace fdma {
+
+constexpr int kKeyTile = 128;
+constexpr int kPagedCtas = 152;  // one CTA per SM
+constexpr float kPLog2e = 1.4426950408889634f;
+constexpr float kPLn2 = 0.6931471805599453f;
+
+struct CacheView {
+  const uint8_t* k;  // strides in bytes: page, token, head
+  const uint8_t* v;
+  int64_t ks[3], vs[3];
+  const uint8_t* ke;
+  const uint8_t* ve;
+  int64_t kes[3], ves[3];
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* k_len;
+  int B, Hkv, d, page_shift, num_pages, max_pages;
+};
+
+struct PagedParams {
+  CacheView c;
+  const uint16_t* q;
+  int64_t q_t, q_h;  // elements
+  const int32_t* cu;
+  int T, max_q, Hq, G;
+  int causal, window, sinks;
+  float scale_log2;
+  uint16_t* out;  // (T, Hq, d)
+  float* lse;     // (Hq, T)
+  float* part_o;  // [cta][2][ROWS][D]
+  float2* part_ml;  // [cta][2][ROWS]: running maximum (log2 units) and weight sum
+  int4* desc;     // [cta]: the split item that begins in this CTA: (sequence, kv head, row block, slot | pieces << 1)
+  int* err;
+  int min_run;  // least tiles of a run
+};
+
+// One sequence as the kernels use it: every value inside its bounds whatever the arrays hold.
+struct Seq {
+  int q0;    // first packed token
+  int nq;    // new tokens
+  int klen;  // keys, the new tokens among them
+  int pos0;  // position of the first new token (negative: that row is before the first key)
+};
+
+__device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report) {
+  Seq s;
+  const int a = p.cu[b], e = p.cu[b + 1], kl = p.c.k_len[b];
+  const int cap = p.c.max_pages << p.c.page_shift;
+  s.q0 = min(max(a, 0), p.T);
+  s.nq = min(max(min(e, p.T) - s.q0, 0), p.max_q);
+  s.klen = min(max(kl, 0), cap);
+  s.pos0 = s.klen - s.nq;
+  if (report && (a != s.q0 || e != s.q0 + s.nq || kl != s.klen)) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+  return s;
+}
+
+struct Span {
+  int lo, hi;   // visible to some row: keys lo .. hi-1 ...
+  int sink_hi;  // ... and 0 .. sink_hi-1 (sink_hi <= lo)
+  int sink_tiles, main0, tiles;
+};
+
+// Keys seen by the tokens [i0, i1) of a sequence (i1 > i0).
+__device__ __forceinline__ Span key_span(const PagedParams& p, const Seq& s, int i0, int i1) {
+  Span r;
+  const int first = max(s.pos0 + i0, 0);
+  r.hi = p.causal ? max(s.pos0 + i1, 0) : s.klen;
+  r.lo = p.window > 0 ? max(first - p.window + 1, 0) : 0;
+  r.sink_hi = p.window > 0 ? min(p.sinks, r.lo) : 0;
+  if (r.hi <= 0) {
+    r.sink_tiles = r.main0 = r.tiles = 0;
+    r.lo = r.hi = r.sink_hi = 0;
+    return r;
+  }
+  r.sink_tiles = (r.sink_hi + kKeyTile - 1) / kKeyTile;
+  r.main0 = max(r.lo / kKeyTile, r.sink_tiles);
+  r.tiles = r.sink_tiles + (r.hi + kKeyTile - 1) / kKeyTile - r.main0;
+  return r;
+}
+
+__device__ __forceinline__ int tile_key0(const Span& r, int t) {
+  return (t < r.sink_tiles ? t : r.main0 + (t - r.sink_tiles)) * kKeyTile;
+}
+
+// The keys that the row at position pos sees: j < hi and (j >= lo or j < sinks).
+struct RowKeys {
+  int lo, hi;
+};
+__device__ __forceinline__ RowKeys row_keys(const PagedParams& p, const Seq& s, int pos) {
+  RowKeys r;
+  r.hi = p.causal ? pos + 1 : s.klen;
+  r.lo = p.window > 0 ? pos - p.window + 1 : 0;
+  return r;
+}
+
+// Position on the line of tiles.
+template <int ROWS>
+struct Cursor {
+  int b, g, rt, t;
+  Seq s;
+  Span r;
+
+  __device__ __forceinline__ int row_blocks(const PagedParams& p) const { return (s.nq * p.G + ROWS - 1) / ROWS; }
+  __device__ __forceinline__ void span(const PagedParams& p) {
+    const int i0 = rt * ROWS / p.G, i1 = min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq);
+    r = key_span(p, s, i0, i1);
+  }
+  __device__ __forceinline__ int key0() const { return tile_key0(r, t); }
+  __device__ __forceinline__ bool last_tile() const { return t + 1 == r.tiles; }
+  // The next tile of the line; the caller knows that there is one.
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    if (++t < r.tiles) return;
+    t = 0;
+    for (;;) {
+      if ((rt + 1) * ROWS < s.nq * p.G) {
+        ++rt;
+        span(p);
+      } else {
+        const bool had_one_block = rt == 0;
+        rt = 0;
+        if (g + 1 < p.c.Hkv) {
+          ++g;
+          if (!had_one_block) span(p);
+        } else {
+          g = 0;
+          do {
+            if (++b >= p.c.B) return;  // not reached while tiles are left
+            s = load_seq(p, b, false);
+          } while (s.nq == 0);
+          span(p);
+        }
+      }
+      if (r.tiles > 0) return;
+    }
+  }
+};
+
+// Tiles of one sequence for one kv head.
+template <int ROWS>
+__device__ __forceinline__ int seq_tiles(const PagedParams& p, const Seq& s) {
+  int n = 0;
+  for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS)
+    n += key_span(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
+  return n;
+}
+
+struct PlanSmem {
+  int64_t warp_sum[16];
+  int64_t total;
+  int b, g, rt, t;
+};
+
+// Finds this CTA's run: every thread of the CTA calls it (NT threads).  Returns the number
+// of tiles (0: none); c stands on the first of them.  quota: the run length of all CTAs.
+template <int ROWS, int NT>
+__device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS>& c, int& quota) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.c.B + NT - 1) / NT;
+  const int b0 = min(tid * per, p.c.B), b1 = min(b0 + per, p.c.B);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = load_seq(p, b, blockIdx.x == 0);
+    mine += static_cast<int64_t>(seq_tiles<ROWS>(p, s)) * p.c.Hkv;
+  }
+  int64_t x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sm->warp_sum[warp] = x;
+  __syncthreads();
+  int64_t before = x - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += sm->warp_sum[w];
+    total += sm->warp_sum[w];
+  }
+  quota = static_cast<int>(max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(p.min_run)));
+  const int64_t start = static_cast<int64_t>(blockIdx.x) * quota;
+  if (start >= before && start < before + mine) {
+    int64_t left = start - before;
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = load_seq(p, b, false);
+      const int n = seq_tiles<ROWS>(p, s);
+      if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
+        left -= static_cast<int64_t>(n) * p.c.Hkv;
+        continue;
+      }
+      sm->b = b;
+      sm->g = static_cast<int>(left / n);
+      int t = static_cast<int>(left % n), rt = 0;
+      for (;; ++rt) {
+        const int k = key_span(p, s, rt * ROWS / p.G, min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq)).tiles;
+        if (t < k) break;
+        t -= k;
+      }
+      sm->rt = rt;
+      sm->t = t;
+      break;
+    }
+  }
+  __syncthreads();
+  if (start >= total) return 0;
+  c.b = sm->b;
+  c.g = sm->g;
+  c.rt = sm->rt;
+  c.t = sm->t;
+  c.s = load_seq(p, c.b, false);
+  c.span(p);
+  return static_cast<int>(min(static_cast<int64_t>(quota), total - start));
+}
+
+// Rows that see no key at all because their row block has no tiles: out = 0, lse = -inf.
+// Called by every thread of every CTA; the sequences are dealt out over the CTAs.
+template <int ROWS>
+__device__ __forceinline__ void write_empty_blocks(const PagedParams& p) {
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    const Seq s = load_seq(p, b, false);
+    for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS) {
+      const int i0 = r0 / p.G, i1 = min((r0 + ROWS - 1) / p.G + 1, s.nq);
+      if (key_span(p, s, i0, i1).tiles > 0) continue;
+      const int r1 = min(r0 + ROWS, s.nq * p.G), nr = (r1 - r0) * p.c.Hkv, vec = p.c.d >> 3;
+      for (int e = threadIdx.x; e < nr * vec; e += blockDim.x) {
+        const int x = e / vec, r = r0 + x % (r1 - r0), h = x / (r1 - r0) * p.G + r % p.G, t = s.q0 + r / p.G;
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(t) * p.Hq + h) * p.c.d + (e % vec) * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+        if (e % vec == 0) p.lse[static_cast<int64_t>(h) * p.T + t] = -__int_as_float(0x7f800000);
+      }
+    }
+  }
+}
+
+// Page of key j, or -1 where the table names none (reported).
+__device__ __forceinline__ int key_page(const PagedParams& p, int b, int j) {
+  const int pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (j >> p.c.page_shift)];
+  if (pg < 0 || pg >= p.c.num_pages) {
+    atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+    return -1;
+  }
+  return pg;
+}
+
+__device__ __forceinline__ float paged_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^(e - 127) of a scale byte
+__device__ __forceinline__ float exp_scale(uint32_t e) { return __uint_as_float(e == 0 ? 0x00400000u : e << 23); }
+
+// Two e4m3 codes (low byte first) as f16, exact (NaN stays NaN).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// cp.async of 16 bytes; src_bytes 0 fills with zeros and reads nothing.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+int validate_cache(const fdma_kv_cache* c);
+CacheView cache_view(const fdma_kv_cache& c);
+cudaError_t launch_paged_token(bool fp8, const PagedParams& p, cudaStream_t stream);
+
+}  // namespace fdma

@@ -1,0 +1,255 @@
+"""ctypes binding of libfdma's paged key/value cache (include/fdma_paged.h).
+
+`kv_append` writes new tokens' K and V rows into the pages of a cache, `kv_gather` reads sequences
+back and `fwd` is the attention of every sequence's newest tokens (one, a few, or a chunk of a
+prompt) over its pages.  Like `fdma`, it marshals pointers and strides only: every step runs in the
+CUDA kernels of libfdma.so, and there is no CPU path.
+
+One set of plan tensors serves the three of them, all int32 on the cache's device:
+
+  page_table (B, max_pages)  page of each page_size positions of a sequence; entries behind the last
+                             page that k_lens needs are not read
+  k_lens (B,)                keys of each sequence, its new tokens among them
+  cu_q (B + 1,)              where each sequence's new tokens begin in the packed token axis
+
+so new token i of the n of sequence b is at position k_lens[b] - n + i.  Their contents stay on the
+device: a captured CUDA graph follows them when they change in place.  Page numbers, lengths or
+offsets out of range are left out by the kernels and reported by `fdma.device_error()`.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import fdma as _fdma
+
+FDMA_CACHE_BF16 = 0
+FDMA_CACHE_E4M3 = 1
+
+EXPORTED = ("fdma_kv_append", "fdma_kv_gather", "fdma_paged_workspace_size", "fdma_paged_fwd")
+
+_I64x2 = ctypes.c_int64 * 2
+_I64x3 = ctypes.c_int64 * 3
+
+
+class FdmaKvCache(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("d", ctypes.c_int32), ("cache_type", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("k_stride", _I64x3),
+        ("v", ctypes.c_void_p), ("v_stride", _I64x3),
+        ("k_exp", ctypes.c_void_p), ("k_exp_stride", _I64x3),
+        ("v_exp", ctypes.c_void_p), ("v_exp_stride", _I64x3),
+        ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("k_len", ctypes.c_void_p),
+    ]
+
+
+class FdmaPagedArgs(ctypes.Structure):
+    _fields_ = [
+        ("cache", FdmaKvCache), ("T", ctypes.c_int32), ("Hq", ctypes.c_int32),
+        ("q", ctypes.c_void_p), ("q_stride", _I64x2), ("cu_q", ctypes.c_void_p), ("max_q", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_float),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+_LIB = None
+
+
+def load() -> ctypes.CDLL:
+    global _LIB
+    if _LIB is None:
+        lib = _fdma.load()
+        C, P, I = ctypes.POINTER(FdmaKvCache), ctypes.c_void_p, ctypes.c_int
+        lib.fdma_kv_append.argtypes = [C, P, ctypes.POINTER(ctypes.c_int64), P, ctypes.POINTER(ctypes.c_int64), P, I, P]
+        lib.fdma_kv_append.restype = I
+        lib.fdma_kv_gather.argtypes = [C, P, P, I, P, P, P]
+        lib.fdma_kv_gather.restype = I
+        lib.fdma_paged_workspace_size.argtypes = [ctypes.POINTER(FdmaPagedArgs)]
+        lib.fdma_paged_workspace_size.restype = ctypes.c_size_t
+        lib.fdma_paged_fwd.argtypes = [ctypes.POINTER(FdmaPagedArgs), P, P, P]
+        lib.fdma_paged_fwd.restype = I
+        _LIB = lib
+    return _LIB
+
+
+def _check_device(first, *ts):
+    if not first.is_cuda:
+        raise ValueError("libfdma takes CUDA tensors only (no CPU path)")
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors of a call are on one device")
+
+
+def _check_int(name, t, shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or (t.dim() and t.numel() > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be int32 {shape} with a contiguous last dimension")
+
+
+def _on(device, stream):
+    """(guard that makes `device` and the launch stream current, stream pointer): what is allocated
+    for the call then belongs to the stream that it runs on."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream), stream.cuda_stream
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
+    return None, torch.cuda.current_stream(device).cuda_stream
+
+
+def _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp) -> FdmaKvCache:
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, Hkv, d)")
+    dt = k_cache.dtype
+    if dt not in (torch.bfloat16, torch.float8_e4m3fn) or v_cache.dtype != dt:
+        raise ValueError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
+    n, ps, h, d = k_cache.shape
+    sk, sv = k_cache.stride(), v_cache.stride()
+    if d > 1 and (sk[3] != 1 or sv[3] != 1):
+        raise ValueError("k_cache and v_cache need a contiguous head dim")
+    B = page_table.shape[0]
+    _check_int("page_table", page_table, (B, page_table.shape[1] if page_table.dim() == 2 else -1))
+    _check_int("k_lens", k_lens, (B,))
+    if dt == torch.bfloat16:
+        if k_exp is not None or v_exp is not None:
+            raise ValueError("k_exp and v_exp belong to float8_e4m3fn caches")
+        kind, ke, kes, ve, ves = FDMA_CACHE_BF16, None, _I64x3(), None, _I64x3()
+    else:
+        for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if t is None or t.dtype != torch.uint8 or tuple(t.shape) != (n, ps, h):
+                raise ValueError(f"{name} must be uint8 (num_pages, page_size, Hkv) for a float8_e4m3fn cache")
+        kind, ke, kes, ve, ves = (FDMA_CACHE_E4M3, k_exp.data_ptr(), _I64x3(*k_exp.stride()), v_exp.data_ptr(),
+                                  _I64x3(*v_exp.stride()))
+    return FdmaKvCache(B, h, d, kind, n, ps, page_table.shape[1], k_cache.data_ptr(), _I64x3(*sk[:3]),
+                       v_cache.data_ptr(), _I64x3(*sv[:3]), ke, kes, ve, ves, page_table.data_ptr(),
+                       page_table.stride(0), k_lens.data_ptr())
+
+
+def empty_cache(num_pages, page_size, Hkv, d, *, dtype=torch.bfloat16, device="cuda"):
+    """An uninitialised cache: (k_cache, v_cache, k_exp, v_exp), the caches (num_pages, page_size, Hkv, d)
+    and, for dtype float8_e4m3fn, the scale bytes (num_pages, page_size, Hkv) (else None).  A page's rows
+    of one head lie together in memory: attention reads whole pages of one head."""
+    def one(dt, *tail):
+        x = torch.empty((num_pages, Hkv, page_size) + tail, dtype=dt, device=device)
+        return x.transpose(1, 2)
+    if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("dtype must be torch.bfloat16 or torch.float8_e4m3fn")
+    exp = (one(torch.uint8), one(torch.uint8)) if dtype == torch.float8_e4m3fn else (None, None)
+    return (one(dtype, d), one(dtype, d)) + exp
+
+
+def kv_append(k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, k_exp=None, v_exp=None, stream=None):
+    """Write the new tokens' rows k, v (T, Hkv, d) bf16 (contiguous head dim) into the cache, quantised
+    (with their scale bytes into k_exp, v_exp) where it is float8_e4m3fn.  Rows behind cu_q[B] are ignored.
+    The slots of one call must be distinct."""
+    _check_device(k, v, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp)
+    c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
+    _check_int("cu_q", cu_q, (c.B + 1,))
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (c.Hkv, c.d) or t.shape[0] != k.shape[0] or \
+                t.stride(2) != 1:
+            raise ValueError(f"{name} must be bf16 (T, Hkv, d) with a contiguous head dim")
+    guard, sp = _on(k.device, stream)
+    args = (ctypes.byref(c), k.data_ptr(), _I64x2(k.stride(0), k.stride(1)), v.data_ptr(),
+            _I64x2(v.stride(0), v.stride(1)), cu_q.data_ptr(), k.shape[0], sp)
+    if guard is None:
+        st = load().fdma_kv_append(*args)
+    else:
+        with guard:
+            st = load().fdma_kv_append(*args)
+    _fdma._raise(st, "fdma_kv_append")
+
+
+def kv_gather(k_cache, v_cache, page_table, k_lens, cu_k, total, *, first=None, k_exp=None, v_exp=None, k_out=None,
+              v_out=None, stream=None):
+    """Read positions first[b] + i (first: int32 (B,), default 0) of every sequence into rows cu_k[b] + i of
+    (k, v), each (total, Hkv, d) bf16.  Positions outside [0, k_lens[b]) read as zeros, so with cu_k = b * N
+    and total = B * N the result views as the (B, N, Hkv, d) that `fdma.fwd` takes.  Rows behind cu_k[B] are
+    left as they are (uninitialised where the outputs are allocated here)."""
+    _check_device(k_cache, v_cache, page_table, k_lens, cu_k, first, k_exp, v_exp, k_out, v_out)
+    c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
+    _check_int("cu_k", cu_k, (c.B + 1,))
+    if first is not None:
+        _check_int("first", first, (c.B,))
+    shape = (int(total), c.Hkv, c.d)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous bf16 {shape}")
+
+    def call():
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k_out is None else k_out
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v_out is None else v_out
+        return ko, vo, load().fdma_kv_gather(ctypes.byref(c), cu_k.data_ptr(), None if first is None else first.data_ptr(),
+                                             shape[0], ko.data_ptr(), vo.data_ptr(), sp)
+
+    guard, sp = _on(k_cache.device, stream)
+    if guard is None:
+        ko, vo, st = call()
+    else:
+        with guard:
+            ko, vo, st = call()
+    _fdma._raise(st, "fdma_kv_gather")
+    return ko, vo
+
+
+def make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0,
+              sinks=0, scale=None, workspace=None) -> FdmaPagedArgs:
+    """Fill fdma_paged_args from tensors (see `fwd`)."""
+    c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
+    _check_int("cu_q", cu_q, (c.B + 1,))
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != c.d or q.stride(2) != 1:
+        raise ValueError("q must be bf16 (T, Hq, d) with a contiguous head dim")
+    T, Hq, d = q.shape
+    a = FdmaPagedArgs(c, T, Hq, q.data_ptr(), _I64x2(q.stride(0), q.stride(1)), cu_q.data_ptr(), int(max_q),
+                      1 if causal else 0, int(window), int(sinks), float(scale) if scale is not None else d ** -0.5)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return a
+
+
+def workspace_size(args: FdmaPagedArgs) -> int:
+    return int(load().fdma_paged_workspace_size(ctypes.byref(args)))
+
+
+def alloc_workspace(args: FdmaPagedArgs, device) -> torch.Tensor:
+    # (the caching allocator's blocks are 512-byte aligned)
+    return torch.empty(workspace_size(args), dtype=torch.uint8, device=device)
+
+
+def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0, sinks=0,
+        scale=None, workspace: Optional[torch.Tensor] = None, out=None, lse=None, stream=None):
+    """Attention of the packed new tokens q (T, Hq, d) over the cache: (out (T, Hq, d) bf16, lse (Hq, T) fp32).
+
+    The row at position p sees keys j <= p (all of k_lens[b] with causal=False); with window=W > 0 only those
+    with j > p - W or j < sinks.  max_q (a host int) bounds the new tokens of a sequence.  scale defaults to
+    d ** -0.5.  A row without keys gets out = 0 and lse = -inf; rows behind cu_q[B] are left as they are
+    (uninitialised where out and lse are allocated here).  A workspace passed in serves one call at a time."""
+    _check_device(q, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp, workspace, out, lse)
+    a = make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp=k_exp, v_exp=v_exp, causal=causal,
+                  window=window, sinks=sinks, scale=scale, workspace=workspace)
+    T, Hq, d = q.shape
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
+        raise ValueError("out must be contiguous bf16 (T, Hq, d)")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 (Hq, T)")
+
+    def call():
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device) if out is None else out
+        s = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = workspace
+        if ws is None:
+            ws = alloc_workspace(a, q.device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        return o, s, load().fdma_paged_fwd(ctypes.byref(a), o.data_ptr(), s.data_ptr(), sp)
+
+    guard, sp = _on(q.device, stream)
+    if guard is None:
+        o, s, st = call()
+    else:
+        with guard:
+            o, s, st = call()
+    _fdma._raise(st, "fdma_paged_fwd")
+    return o, s
