@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfdma.so")
 SOURCES = ["fdma_api.cu", "fdma_classify.cu", "fdma_fwd.cu", "fdma_bwd.cu", "fdma_bwd_wide.cu", "fdma_noalloc.cu",
-           "fdma_topk.cu", "fdma_cache.cu", "fdma_paged.cu"]
+           "fdma_topk.cu", "fdma_cache.cu", "fdma_paged.cu",
+           "fdma_paged_chunk.cu"]
 HEADERS = ["fdma_internal.h", "fdma_ptx.cuh", "fdma_paged.cuh", os.path.join("..", "..", "include", "fdma.h"),
            os.path.join("..", "..", "include", "fdma_paged.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

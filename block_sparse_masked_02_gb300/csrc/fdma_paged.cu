@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kTokWarps = 8;
 constexpr int kTokThreads = kTokWarps * 32;
+constexpr int kTokenRows = 32;  // packed rows up to which the token kernel runs
 constexpr float kNInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -492,31 +493,30 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
   }
 }
 
-// Joins the pieces of the items that more than one CTA worked on.  blockIdx.x: the CTA in which
-// the item begins; blockIdx.y: which RPB of its rows.  RPB = 1: the block's eight warps share
-// the pieces of one row (one sequence spread over the machine has up to kPagedCtas of them);
-// RPB = 8: a warp a row.
-template <int D, int ROWS, int RPB>
+// Joins the pieces of the items that more than one CTA of the token kernel worked on.  blockIdx.x:
+// the CTA in which the item begins; blockIdx.y: its row.  The block's eight warps share the row's
+// pieces (one sequence spread over the machine has up to kPagedCtas of them).
+template <int D, int ROWS>
 __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   constexpr int V = D / 32;
-  __shared__ float sacc[RPB == 1 ? 8 : 1][D];
+  __shared__ float sacc[8][D];
   __shared__ float2 sml[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 ds = p.desc[blockIdx.x];
   const int pieces = ds.w >> 1;
   if (pieces == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int pr = RPB == 1 ? blockIdx.y : blockIdx.y * RPB + warp;
+  const int pr = blockIdx.y;
   const Seq s = load_seq(p, ds.x, false);
   const int r = ds.z * ROWS + pr;
-  if (r >= s.nq * p.G) return;  // the whole block where RPB = 1, else the whole warp
+  if (r >= s.nq * p.G) return;
   const int64_t first = (static_cast<int64_t>(blockIdx.x) * 2 + (ds.w & 1)) * ROWS + pr;
   const int64_t rest = static_cast<int64_t>(blockIdx.x) * 2 * ROWS + pr;  // piece i > 0: + i * 2 * ROWS
   float m = kNInf, l = 0.f, a[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) a[e] = 0.f;
 #pragma unroll 4
-  for (int i = RPB == 1 ? warp : 0; i < pieces; i += RPB == 1 ? 8 : 1) {
+  for (int i = warp; i < pieces; i += 8) {
     const int64_t at = i == 0 ? first : rest + static_cast<int64_t>(i) * 2 * ROWS;
     const float2 ml = p.part_ml[at];
     float x[V];
@@ -534,26 +534,24 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
     for (int e = 0; e < V; ++e) a[e] = a[e] * fa + x[e] * fb;
     m = mn;
   }
-  if (RPB == 1) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) sacc[RPB == 1 ? warp : 0][lane * V + e] = a[e];
-    if (lane == 0) sml[warp] = make_float2(m, l);
-    __syncthreads();
-    if (warp > 0) return;
-    m = kNInf;
+  for (int e = 0; e < V; ++e) sacc[warp][lane * V + e] = a[e];
+  if (lane == 0) sml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp > 0) return;
+  m = kNInf;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) m = fmaxf(m, sml[w].x);
-    const float base = m == kNInf ? 0.f : m;
-    l = 0.f;
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, sml[w].x);
+  const float base = m == kNInf ? 0.f : m;
+  l = 0.f;
 #pragma unroll
-    for (int e = 0; e < V; ++e) a[e] = 0.f;
+  for (int e = 0; e < V; ++e) a[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      const float f = paged_ex2(sml[w].x - base);
-      l += sml[w].y * f;
+  for (int w = 0; w < 8; ++w) {
+    const float f = paged_ex2(sml[w].x - base);
+    l += sml[w].y * f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) a[e] += sacc[RPB == 1 ? w : 0][lane * V + e] * f;
-    }
+    for (int e = 0; e < V; ++e) a[e] += sacc[w][lane * V + e] * f;
   }
   const int i = r / p.G, h = ds.y * p.G + r - i * p.G, t = s.q0 + i;
   const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
@@ -567,19 +565,57 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const PagedParams p) {
   if (lane == 0) p.lse[static_cast<int64_t>(h) * p.T + t] = l == 0.f ? kNInf : (m + log2f(l)) * kPLn2;
 }
 
-// The join starts while the main kernel's last CTAs still run and waits for them on the device.
-template <int D, int ROWS, int RPB>
-cudaError_t launch_join(const PagedParams& p, int ctas, int rows, cudaStream_t stream) {
+// Joins the chunk kernel's pieces, which are [column / 4][row] float4: a block takes eight rows, so
+// that eight threads next to each other read 128 contiguous bytes.
+template <int D>
+__global__ void __launch_bounds__(D * 2) paged_chunk_join_kernel(const PagedParams p) {
+  constexpr int ROWS = kChunkItemRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 ds = p.desc[blockIdx.x];
+  const int pieces = ds.w >> 1;
+  if (pieces == 0) return;
+  const int pr = blockIdx.y * 8 + (threadIdx.x & 7), col = threadIdx.x >> 3;
+  const Seq s = load_seq(p, ds.x, false);
+  const int r = ds.z * ROWS + pr;
+  if (r >= s.nq * p.G) return;
+  const float4* o = reinterpret_cast<const float4*>(p.part_o);
+  float m = kNInf, l = 0.f;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < pieces; ++i) {
+    const int64_t pb = ((static_cast<int64_t>(blockIdx.x) + i) * 2 + (i == 0 ? ds.w & 1 : 0)) * ROWS;
+    const float2 ml = p.part_ml[pb + pr];
+    const float4 x = o[pb * (D / 4) + col * ROWS + pr];
+    const float mn = fmaxf(m, ml.x), base = mn == kNInf ? 0.f : mn;
+    const float fa = paged_ex2(m - base), fb = paged_ex2(ml.x - base);
+    l = l * fa + ml.y * fb;
+    a.x = a.x * fa + x.x * fb;
+    a.y = a.y * fa + x.y * fb;
+    a.z = a.z * fa + x.z * fb;
+    a.w = a.w * fa + x.w * fb;
+    m = mn;
+  }
+  const int i = r / p.G, h = ds.y * p.G + r - i * p.G, t = s.q0 + i;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  if (col * 4 < p.c.d)
+    *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(t) * p.Hq + h) * p.c.d + col * 4) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+  if (col == 0) p.lse[static_cast<int64_t>(h) * p.T + t] = l == 0.f ? kNInf : (m + log2f(l)) * kPLn2;
+}
+
+// A join starts while the main kernel's last CTAs still run and waits for them on the device.
+cudaError_t launch_join(void (*kern)(PagedParams), const PagedParams& p, int blocks_y, int threads,
+                        cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, (rows + RPB - 1) / RPB);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(kPagedCtas, blocks_y);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, ROWS, RPB>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <int D, bool FP8, int MT>
@@ -592,7 +628,7 @@ cudaError_t launch_token(const PagedParams& p, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-  return launch_join<D, 16 * MT, 1>(p, kPagedCtas, static_cast<int>(rows < 16 * MT ? rows : 16 * MT), stream);
+  return launch_join(paged_join_kernel<D, 16 * MT>, p, static_cast<int>(rows < 16 * MT ? rows : 16 * MT), 256, stream);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -602,10 +638,10 @@ struct PagedLayout {
   size_t desc, ml, o, total;
 };
 
-// Rows of an item: 16 or 32.
+// Rows of an item: 16 or 32 on the token kernel, else the chunk kernel's.
 int item_rows(const fdma_paged_args* a) {
   const int64_t rows = static_cast<int64_t>(a->max_q) * (a->Hq / a->cache.Hkv);
-  return rows <= 16 ? 16 : 32;
+  return rows <= 16 ? 16 : rows <= kTokenRows ? 32 : kChunkItemRows;
 }
 
 PagedLayout paged_layout(const fdma_paged_args* a) {
@@ -690,7 +726,15 @@ int fdma_paged_fwd(const fdma_paged_args* a, void* out, float* lse, void* stream
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
   const bool fp8 = a->cache.cache_type == FDMA_CACHE_E4M3;
-  return launch_paged_token(fp8, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (item_rows(a) < kChunkItemRows) return launch_paged_token(fp8, p, st_) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  p.min_run = 2;
+  if (launch_paged_chunk(fp8, p, st_) != cudaSuccess) return FDMA_ERR_CUDA;
+  const int64_t rows = static_cast<int64_t>(a->max_q) * p.G;
+  const int by = static_cast<int>(((rows < kChunkItemRows ? rows : kChunkItemRows) + 7) / 8);
+  const cudaError_t e = p.c.d <= 64 ? launch_join(paged_chunk_join_kernel<64>, p, by, 128, st_)
+                                    : launch_join(paged_chunk_join_kernel<128>, p, by, 256, st_);
+  return e == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -292,6 +292,11 @@ __device__ __forceinline__ void cp_async_wait() {
 
 int validate_cache(const fdma_kv_cache* c);
 CacheView cache_view(const fdma_kv_cache& c);
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Attention kernels: the token kernel with its join, and the chunk kernel without.
+constexpr int kChunkItemRows = 256;
 cudaError_t launch_paged_token(bool fp8, const PagedParams& p, cudaStream_t stream);
+cudaError_t launch_paged_chunk(bool fp8, const PagedParams& p, cudaStream_t stream);
 
 }  // namespace fdma

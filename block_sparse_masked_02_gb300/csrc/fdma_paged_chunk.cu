@@ -1,0 +1,496 @@
+// Attention of a chunk of new tokens (more packed query rows than the token kernel takes)
+// over a paged cache, on the tensor cores.
+//
+// An item is 256 packed rows (token, head of the group) of one sequence and kv head, as two
+// slots of 128 rows that share every K and V tile.  With 2 * 128 rows a tile of 128 keys costs
+// 4 * 128 * 128 * d multiply-adds, 2048 cycles of the tensor pipe at d = 128, against about 1400
+// cycles for its K and V from HBM and less from L2: the products bound it, so everything
+// else is arranged to keep them fed.  One CTA an SM, 16 warps:
+//   warp 0          issues tcgen05.mma: S_w = Q_w K^T into TMEM, then O_w += P_w V with P_w read
+//                   from TMEM over the columns of S_w; the order PV0, S0, PV1, S1 lets each slot's
+//                   softmax run under the other slot's products;
+//   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: S is read from TMEM once,
+//   warps 8..11     masked only in tiles that some row of the warp sees in part, exponentiated
+//                   with a running maximum that is raised only when it grows by 2^8 or more;
+//   warps 12..15    bring Q, K and V: page by page with cp.async into 128-byte-swizzled tiles
+//                   (a ring of five), keys that no row of the item sees as zeros; e4m3 rows come
+//                   through registers, are multiplied by their scale and stored as bf16 (exact).
+// The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
+// a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
+#include "fdma_paged.cuh"
+
+namespace fdma {
+namespace {
+
+constexpr int kChunkRows = kChunkItemRows;
+constexpr int kChunkThreads = 512;
+constexpr int kRing = 5;
+constexpr int kLag = 2;  // cp.async groups in flight behind the one being issued
+constexpr uint32_t kRegsMma = 48, kRegsLoad = 96, kRegsSoft = 184;
+constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
+constexpr float kNInf = -__builtin_huge_valf();
+constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
+
+enum ChunkBar : int {
+  cFull = 0,             // + ring slot: 128 arrivals of the loading threads
+  cEmpty = kRing,        // + ring slot: the products that read it are done
+  cQEmpty = 2 * kRing,   // the item's last S product is done
+  cSFull,                // + slot
+  cPReady = cSFull + 2,  // + 2 * slot + key half
+  cOFinal = cPReady + 4,  // + slot: the item's last PV is done
+  cOFree = cOFinal + 2,   // + slot: the softmax threads have read O
+  cDrain = cOFree + 2,
+  kChunkBars
+};
+
+template <int D>
+struct ChunkSmem {
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kOffRing = 2 * kTile;
+  static constexpr int kOffBar = kOffRing + kRing * kTile;
+  static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
+  static constexpr int kOffPlan = kOffMisc + 16;
+  static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
+  static_assert(kTotal <= 232448, "shared memory of one CTA");
+};
+
+// Byte offset of 16-byte chunk c of row r in a K-major tile of 64-column blocks, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// A CTA's part of one item: the tiles [t0, t0 + n) of the item under the cursor.
+struct Part {
+  int n;
+  bool whole;
+  int slot;  // of the workspace
+};
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const PagedParams p) {
+  using L = ChunkSmem<D>;
+  constexpr int ROWS = kChunkRows;
+  constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t IDESC_O = idesc_bf16(128, D, false, true);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  PlanSmem* plan = reinterpret_cast<PlanSmem*>(smem + L::kOffPlan);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if ((smem_u32(smem) & 1023u) != 0) {
+    if (tid == 0) atomicCAS(p.err, 0, kDevErrAlign);
+    return;
+  }
+  Cursor<ROWS> c;
+  int quota;
+  const int run = plan_run<ROWS, kChunkThreads>(p, plan, c, quota);
+  if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+  write_empty_blocks<ROWS>(p);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (run == 0) return;
+
+  if (tid == 0) {
+    for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
+    for (int i = 0; i < kRing; ++i) mbar_init(&bars[cFull + i], 128);
+    for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
+    for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
+    misc[1] = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(misc, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = misc[0];
+  uint8_t* sQ = smem;
+  uint8_t* sR = smem + L::kOffRing;
+  auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag); };
+
+  // The part at the cursor, with `left` tiles of the run to go.  index: parts before it.
+  auto part_at = [&](int left, int index) {
+    Part s;
+    s.n = min(c.r.tiles - c.t, left);
+    s.whole = s.n == c.r.tiles;
+    s.slot = index == 0 ? 0 : 1;
+    return s;
+  };
+  // From the part's first tile to the next part's.
+  auto next_part = [&](const Part& s, int left) {
+    c.t += s.n - 1;
+    if (left > s.n) c.next(p);
+  };
+  auto slots_of = [&]() { return c.s.nq * p.G - c.rt * ROWS > 128 ? 2 : 1; };
+
+  if (warp >= 12) {
+    // ------------------------------------------------------------------ loads
+    regs_decrease<kRegsLoad>();
+    const int lt = tid - 384;
+    const int pmask = (1 << p.c.page_shift) - 1;
+    int it = 0;        // ring items issued
+    int qfills = 0;    // items begun
+    bool ok = true;
+    int signalled = 0;  // ring items whose arrival was announced
+    auto announce = [&](int upto) {
+      fence_proxy_async_smem();
+      for (; signalled < upto; ++signalled) mbar_arrive(&bars[cFull + signalled % kRing]);
+    };
+    for (int left = run, idx = 0; ok && left > 0; ++idx) {
+      const Part s = part_at(left, idx);
+      // Q of both slots, announced with the item's first K tile
+      if (qfills > 0) {
+        cp_async_wait_all();  // the products before the wait need all that was issued
+        announce(it);
+        if (!(ok = wait(cQEmpty, (qfills - 1) & 1))) break;
+      }
+      ++qfills;
+      {
+        constexpr int CPR = D / 8;
+        const int chunk = lt % CPR;
+        const int rows = c.s.nq * p.G - c.rt * ROWS;
+#pragma unroll 4
+        for (int r = lt / CPR; r < 256; r += 128 / CPR) {
+          const int R = c.rt * ROWS + r, i = R / p.G;
+          const uint32_t nb = r < rows && chunk * 8 < p.c.d ? 16u : 0u;
+          const uint16_t* src = p.q + (c.s.q0 + i) * p.q_t + (c.g * p.G + R - i * p.G) * p.q_h + chunk * 8;
+          cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, chunk), nb ? src : p.q, nb);
+        }
+      }
+      for (int k = 0; ok && k < s.n; ++k) {
+        const int j0 = tile_key0(c.r, c.t + k);
+        // lanes 0..7 of every warp look up the pages of the tile's eight groups of 16 keys
+        int pg = -1;
+        if (lane < 8) {
+          const int j = j0 + lane * 16;
+          if (j < c.r.sink_hi || (j < c.r.hi && j + 16 > c.r.lo)) pg = key_page(p, c.b, j);
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint8_t* base = (kv ? p.c.v : p.c.k) + c.g * (kv ? p.c.vs[2] : p.c.ks[2]);
+          const int64_t sp = kv ? p.c.vs[0] : p.c.ks[0], st = kv ? p.c.vs[1] : p.c.ks[1];
+          const int slot = it % kRing;
+          if (it >= kRing && !(ok = wait(cEmpty + slot, (it / kRing - 1) & 1))) break;
+          const uint32_t dst = smem_u32(sR) + slot * L::kTile;
+          if (!FP8) {
+            constexpr int CPR = D / 8, RPP = 128 / CPR;
+            const int chunk = lt % CPR;
+            const uint32_t cb = chunk * 8 < p.c.d ? 16u : 0u;
+#pragma unroll 4
+            for (int i = 0; i < CPR; ++i) {
+              const int r = i * RPP + lt / CPR, j = j0 + r;
+              const int g = __shfl_sync(0xffffffffu, pg, r >> 4);
+              const bool in = g >= 0 && (j < c.r.sink_hi || (j >= c.r.lo && j < c.r.hi));
+              const uint32_t nb = in ? cb : 0u;
+              cp_async16(dst + tile_off(r, chunk), nb ? base + g * sp + (j & pmask) * st + chunk * 16 : p.c.k, nb);
+            }
+            cp_async_commit();
+            ++it;
+            if (it > kLag) {
+              cp_async_wait<kLag>();
+              announce(it - kLag);
+            }
+          } else {
+            constexpr int CPR = D / 16, RPP = 128 / CPR;
+            const int chunk = lt % CPR;
+            const int64_t* es = kv ? p.c.ves : p.c.kes;
+            const uint8_t* eb = (kv ? p.c.ve : p.c.ke) + c.g * es[2];
+            uint4 x[CPR];
+            uint32_t e[CPR];
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              const int r = i * RPP + lt / CPR, j = j0 + r;
+              const int g = __shfl_sync(0xffffffffu, pg, r >> 4);
+              const bool in = g >= 0 && (j < c.r.sink_hi || (j >= c.r.lo && j < c.r.hi));
+              x[i] = make_uint4(0u, 0u, 0u, 0u);
+              e[i] = 127;
+              if (in) {
+                e[i] = eb[g * es[0] + (j & pmask) * es[1]];
+                if (chunk * 16 < p.c.d)
+                  x[i] = __ldg(reinterpret_cast<const uint4*>(base + g * sp + (j & pmask) * st + chunk * 16));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              const int r = i * RPP + lt / CPR;
+              const float sc = exp_scale(e[i]);
+              const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int h = 0; h < 8; ++h) {
+                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+                float lo, hi;
+                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+                    : "=f"(lo), "=f"(hi)
+                    : "r"(f));
+                o[h] = pack_bf16x2(lo * sc, hi * sc);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4*>(sR + slot * L::kTile + tile_off(r, chunk * 2 + h)) =
+                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+            }
+            ++it;
+            cp_async_wait_all();  // the item's Q
+            announce(it);
+          }
+        }
+      }
+      left -= s.n;
+      next_part(s, left + s.n);
+    }
+    cp_async_wait_all();
+    if (ok) announce(it);
+  } else if (warp < 4) {
+    regs_decrease<kRegsMma>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------------- products
+      const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);      // K-major view of ring slot 0
+      const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16384, 1024);   // MN-major view
+      constexpr uint64_t step = static_cast<uint64_t>(L::kTile >> 4);
+      int it = 0;                // ring items before this part
+      int np[2] = {0, 0};        // P tiles consumed by each slot
+      int parts[2] = {0, 0};     // parts begun by each slot
+      bool ok = true;
+      auto full = [&](int item) {
+        if (!wait(cFull + item % kRing, (item / kRing) & 1)) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto issue_s = [&](int w, int item) {
+        const uint64_t kd = kd0 + (item % kRing) * step, qd = qd0 + w * step;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t off = static_cast<uint64_t>(((k >> 2) * 16384u + (k & 3) * 32u) >> 4);
+          umma_ss(tbase + w * 128, qd + off, kd + off, IDESC_S, k > 0);
+        }
+        umma_commit(&bars[cSFull + w]);
+      };
+      auto pv = [&](int w, int item, bool start) {
+        if (start && parts[w] > 1) {  // O_w still holds the previous part until its rows have read it
+          if (!wait(cOFree + w, (parts[w] - 2) & 1)) return false;
+        }
+        const uint64_t vd = vd0 + (item % kRing) * step;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (!wait(cPReady + 2 * w + hf, np[w] & 1)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k = hf * 4; k < hf * 4 + 4; ++k)
+            umma_ts(tbase + 256 + w * 128, tbase + w * 128 + k * 8, vd + static_cast<uint64_t>((k * 2048) >> 4), IDESC_O,
+                    (!start || k > 0) ? 1u : 0u);
+        }
+        ++np[w];
+        return true;
+      };
+      for (int left = run, idx = 0; ok && left > 0; ++idx) {
+        const Part s = part_at(left, idx);
+        const int ns = slots_of();
+        for (int w = 0; w < ns; ++w) ++parts[w];
+        for (int k = 0; ok && k <= s.n; ++k) {
+          const int ik = it + 2 * k, iv = it + 2 * (k - 1) + 1;
+          if (k > 0 && !(ok = full(iv))) break;
+          for (int w = 0; ok && w < ns; ++w) {
+            if (k > 0) {
+              if (!(ok = pv(w, iv, k == 1))) break;
+              if (w == ns - 1) umma_commit(&bars[cEmpty + iv % kRing]);
+              if (k == s.n) umma_commit(&bars[cOFinal + w]);
+            }
+            if (k < s.n) {
+              if (w == 0 && !(ok = full(ik))) break;
+              issue_s(w, ik);
+            }
+          }
+          if (ok && k < s.n) umma_commit(&bars[cEmpty + ik % kRing]);
+          if (ok && k == s.n - 1) umma_commit(&bars[cQEmpty]);
+        }
+        it += 2 * s.n;
+        left -= s.n;
+        next_part(s, left + s.n);
+      }
+      umma_commit(&bars[cDrain]);
+      mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
+    }
+  } else {
+    // -------------------------------------------------------------------- softmax
+    regs_increase<kRegsSoft>();
+    const int w = (warp >> 2) - 1, quad = warp & 3, row = w * 128 + quad * 32 + lane;
+    const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
+    const uint32_t scol = w * 128, ocol = 256 + w * 128;
+    const float cexp = p.scale_log2, raise = kRaise / cexp;
+    const uint64_t c2 = f2(cexp, cexp);
+    int ns = 0, parts = 0;
+    bool ok = true;
+    for (int left = run, idx = 0; ok && left > 0; ++idx) {
+      const Part s = part_at(left, idx);
+      if (w < slots_of()) {
+        const int R = c.rt * ROWS + row;
+        const bool real = R < c.s.nq * p.G;
+        const int tok = real ? R / p.G : 0;
+        const RowKeys rk = row_keys(p, c.s, c.s.pos0 + (real ? tok : c.s.nq - 1));
+        float m = kNInf, l = 0.f;
+        for (int k = 0; k < s.n; ++k, ++ns) {
+          const int j0 = tile_key0(c.r, c.t + k);
+          const int hi = rk.hi - j0, lo = rk.lo - j0, sk = p.sinks - j0;
+          const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
+          if (!(ok = wait(cSFull + w, ns & 1))) break;
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) tmem_ld32(tl + scol + a * 32, x[a]);
+          tmem_ld_wait(x[0]);
+          tmem_ld_tie(x[1]);
+          tmem_ld_tie(x[2]);
+          tmem_ld_tie(x[3]);
+          if (masked) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+              auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+              const uint32_t see = below(hi - a * 32) & (~below(lo - a * 32) | below(sk - a * 32));
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((see >> e) & 1u)) x[a][e] = 0xff800000u;
+            }
+          }
+          float mx4[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            mx4[a] = __uint_as_float(x[a][0]);
+            asm("max.f32 %0, %0, %1;" : "+f"(mx4[a]) : "f"(__uint_as_float(x[a][1])));
+#pragma unroll
+            for (int e = 2; e < 32; e += 2)
+              asm("max.f32 %0, %0, %1, %2;"
+                  : "+f"(mx4[a])
+                  : "f"(__uint_as_float(x[a][e])), "f"(__uint_as_float(x[a][e + 1])));
+          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          const float mn = fmaxf(m, mx);
+          float alpha = 1.f;
+          if (mn > m + raise) {  // (also from -inf)
+            alpha = m == kNInf ? 0.f : paged_ex2((m - mn) * cexp);
+            l *= alpha;
+            m = mn;
+          }
+          if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            // S_w of this tile was issued after the PV_w of the last one, and the next PV_w waits
+            // for the arrivals below: O_w is at rest
+#pragma unroll
+            for (int a = 0; a < D / 16; ++a) {
+              uint32_t o16[16];
+              tmem_ld16(tl + ocol + a * 16, o16);
+              tmem_ld_wait(o16);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o16[e] = __float_as_uint(__uint_as_float(o16[e]) * alpha);
+              tmem_st16(tl + ocol + a * 16, o16);
+            }
+          }
+          const float nm = m == kNInf ? 0.f : -(m * cexp);
+          const uint64_t nm2 = f2(nm, nm);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int a = 0; a < 4; ++a) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float e0, e1;
+              f2split(fma2(f2(__uint_as_float(x[a][2 * e]), __uint_as_float(x[a][2 * e + 1])), c2, nm2), e0, e1);
+              e0 = paged_ex2(e0);
+              e1 = paged_ex2(e1);
+              sum[e & 1] = add2(sum[e & 1], f2(e0, e1));
+              pk[e] = pack_bf16x2(e0, e1);
+            }
+            tmem_st16(tl + scol + a * 16, pk);
+            if (a & 1) {  // keys 0..63, then 64..127
+              tmem_st_wait();
+              tc_fence_before();
+              mbar_arrive(&bars[cPReady + 2 * w + (a >> 1)]);
+            }
+          }
+          float s0, s1;
+          f2split(add2(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+        }
+        if (!ok) break;
+        // ---- the part's end
+        if (!(ok = wait(cOFinal + w, parts & 1))) break;
+        ++parts;
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        const int64_t pb = (static_cast<int64_t>(blockIdx.x) * 2 + s.slot) * ROWS;
+        const int h = c.g * p.G + R - tok * p.G;
+        const int64_t t = c.s.q0 + tok;
+#pragma unroll
+        for (int a = 0; a < D / 32; ++a) {
+          uint32_t o[32];
+          tmem_ld32(tl + ocol + a * 32, o);
+          tmem_ld_wait(o);
+          if (s.whole) {
+            uint16_t* dst = p.out + (t * p.Hq + h) * p.c.d + a * 32;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                pk[i] = pack_bf16x2(__uint_as_float(o[e * 8 + 2 * i]) * inv, __uint_as_float(o[e * 8 + 2 * i + 1]) * inv);
+              if (real && a * 32 + e * 8 < p.c.d)
+                *reinterpret_cast<uint4*>(dst + e * 8) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else {
+            // [column / 4][row]: a warp's stores are contiguous
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              reinterpret_cast<uint4*>(p.part_o)[pb * (D / 4) + (a * 8 + e) * ROWS + row] =
+                  make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&bars[cOFree + w]);
+        if (s.whole) {
+          if (real) p.lse[static_cast<int64_t>(h) * p.T + t] = l == 0.f ? kNInf : (m * cexp + log2f(l)) * kPLn2;
+        } else {
+          p.part_ml[pb + row] = make_float2(m == kNInf ? m : m * cexp, l);
+        }
+      }
+      if (tid == 128 && c.t == 0 && !s.whole) {
+        const int rest = c.r.tiles - s.n;
+        p.desc[blockIdx.x] = make_int4(c.b, c.g, c.rt, s.slot | (1 + (rest + quota - 1) / quota) << 1);
+      }
+      left -= s.n;
+      next_part(s, left + s.n);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tbase, 512);
+  }
+}
+
+template <int D, bool FP8>
+cudaError_t launch_chunk(const PagedParams& p, cudaStream_t stream) {
+  using L = ChunkSmem<D>;
+  auto kern = paged_chunk_kernel<D, FP8>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs < kChunkLaunchRegs) return cudaErrorInvalidConfiguration;  // the setmaxnreg split must fit
+  kern<<<kPagedCtas, kChunkThreads, L::kTotal, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(bool fp8, const PagedParams& p, cudaStream_t stream) {
+  if (p.c.d <= 64) return fp8 ? launch_chunk<64, true>(p, stream) : launch_chunk<64, false>(p, stream);
+  return fp8 ? launch_chunk<128, true>(p, stream) : launch_chunk<128, false>(p, stream);
+}
+
+}  // namespace fdma
