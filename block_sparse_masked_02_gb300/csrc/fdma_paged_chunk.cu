@@ -9,6 +9,9 @@
 //   warp 0          issues tcgen05.mma: S_w = Q_w K^T into TMEM, then O_w += P_w V with P_w read
 //                   from TMEM over the columns of S_w; the order PV0, S0, PV1, S1 lets each slot's
 //                   softmax run under the other slot's products;
+//   warp 3          walks the CTA's run and publishes its parts, one item or piece of an item
+//                   each, in shared memory for the other roles (which keeps the walk's
+//                   state out of their registers: spilled there it cost more than half the time);
 //   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: S is read from TMEM once,
 //   warps 8..11     masked only in tiles that some row of the warp sees in part, exponentiated
 //                   with a running maximum that is raised only when it grows by 2^8 or more;
@@ -25,8 +28,9 @@ namespace {
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kChunkThreads = 512;
 constexpr int kRing = 5;
+constexpr int kParts = 4;  // published parts
 constexpr int kLag = 2;  // cp.async groups in flight behind the one being issued
-constexpr uint32_t kRegsMma = 48, kRegsLoad = 96, kRegsSoft = 184;
+constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
 constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
@@ -39,8 +43,43 @@ enum ChunkBar : int {
   cPReady = cSFull + 2,  // + 2 * slot + key half
   cOFinal = cPReady + 4,  // + slot: the item's last PV is done
   cOFree = cOFinal + 2,   // + slot: the softmax threads have read O
-  cDrain = cOFree + 2,
+  cPart = cOFree + 2,     // + part slot: the part is published
+  cPartFree = cPart + kParts,  // + part slot: every reader is done with it
+  cDrain = cPartFree + kParts,
   kChunkBars
+};
+
+// Byte offset of 16-byte chunk c of row r in a K-major tile of 64-column blocks, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_off(int r, int c) {
+  return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// A CTA's part of one item: its tiles t0 .. t0 + n - 1.
+struct Part {
+  int n;      // 0: the run is over
+  int whole;  // the item's tiles are all here: the result is final
+  int slot;   // else: where its sums go in the workspace
+  int slots;  // row slots in use
+  int t0, sink_tiles, main0;
+  int lo, hi, sink_hi;
+  int b, g, row0;  // row0: first packed row
+  int q0, nq, pos0, klen;
+  int pad;
+};
+__device__ __forceinline__ int part_key0(const Part& s, int t) {
+  return (t < s.sink_tiles ? t : s.main0 + (t - s.sink_tiles)) * kKeyTile;
+}
+
+// A place in the K / V ring and the parity of its current fill.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void step() {
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 template <int D>
@@ -49,21 +88,10 @@ struct ChunkSmem {
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffBar = kOffRing + kRing * kTile;
   static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
-  static constexpr int kOffPlan = kOffMisc + 16;
+  static constexpr int kOffParts = kOffMisc + 16;
+  static constexpr int kOffPlan = kOffParts + kParts * static_cast<int>(sizeof(Part));
   static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
   static_assert(kTotal <= 232448, "shared memory of one CTA");
-};
-
-// Byte offset of 16-byte chunk c of row r in a K-major tile of 64-column blocks, 128-byte swizzle.
-__device__ __forceinline__ uint32_t tile_off(int r, int c) {
-  return (c >> 3) * 16384 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
-// A CTA's part of one item: the tiles [t0, t0 + n) of the item under the cursor.
-struct Part {
-  int n;
-  bool whole;
-  int slot;  // of the workspace
 };
 
 template <int D, bool FP8>
@@ -96,6 +124,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
     for (int i = 0; i < kRing; ++i) mbar_init(&bars[cFull + i], 128);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
+    for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], 128 + 1 + 256);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -111,84 +140,101 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
   uint8_t* sR = smem + L::kOffRing;
   auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag); };
 
-  // The part at the cursor, with `left` tiles of the run to go.  index: parts before it.
-  auto part_at = [&](int left, int index) {
-    Part s;
-    s.n = min(c.r.tiles - c.t, left);
-    s.whole = s.n == c.r.tiles;
-    s.slot = index == 0 ? 0 : 1;
-    return s;
-  };
-  // From the part's first tile to the next part's.
-  auto next_part = [&](const Part& s, int left) {
-    c.t += s.n - 1;
-    if (left > s.n) c.next(p);
-  };
-  auto slots_of = [&]() { return c.s.nq * p.G - c.rt * ROWS > 128 ? 2 : 1; };
+  Part* parts = reinterpret_cast<Part*>(smem + L::kOffParts);
+  // The idx-th part of the run; false on a time-out.
+  auto part_ready = [&](int idx) { return wait(cPart + idx % kParts, (idx / kParts) & 1); };
+  auto part_done = [&](int idx) { mbar_arrive(&bars[cPartFree + idx % kParts]); };
 
   if (warp >= 12) {
     // ------------------------------------------------------------------ loads
     regs_decrease<kRegsLoad>();
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
-    int it = 0;        // ring items issued
-    int qfills = 0;    // items begun
+    int it = 0;             // ring items issued
+    RingPos at, said;       // the next item's place; the next to announce
+    int signalled = 0;      // ring items announced
     bool ok = true;
-    int signalled = 0;  // ring items whose arrival was announced
     auto announce = [&](int upto) {
       fence_proxy_async_smem();
-      for (; signalled < upto; ++signalled) mbar_arrive(&bars[cFull + signalled % kRing]);
+      for (; signalled < upto; ++signalled, said.step()) mbar_arrive(&bars[cFull + said.slot]);
     };
-    for (int left = run, idx = 0; ok && left > 0; ++idx) {
-      const Part s = part_at(left, idx);
+    for (int idx = 0;; ++idx) {
+      if (!(ok = part_ready(idx))) break;
+      const Part& s = parts[idx % kParts];
+      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
+      if (n == 0) break;
       // Q of both slots, announced with the item's first K tile
-      if (qfills > 0) {
+      if (idx > 0) {
         cp_async_wait_all();  // the products before the wait need all that was issued
         announce(it);
-        if (!(ok = wait(cQEmpty, (qfills - 1) & 1))) break;
+        if (!(ok = wait(cQEmpty, (idx - 1) & 1))) break;
       }
-      ++qfills;
       {
         constexpr int CPR = D / 8;
         const int chunk = lt % CPR;
-        const int rows = c.s.nq * p.G - c.rt * ROWS;
+        const int row0 = s.row0, q0 = s.q0, g0 = s.g * p.G, rows = s.nq * p.G - row0;
 #pragma unroll 4
         for (int r = lt / CPR; r < 256; r += 128 / CPR) {
-          const int R = c.rt * ROWS + r, i = R / p.G;
+          const int R = row0 + r, i = R / p.G;
           const uint32_t nb = r < rows && chunk * 8 < p.c.d ? 16u : 0u;
-          const uint16_t* src = p.q + (c.s.q0 + i) * p.q_t + (c.g * p.G + R - i * p.G) * p.q_h + chunk * 8;
+          const uint16_t* src = p.q + (q0 + i) * p.q_t + (g0 + R - i * p.G) * p.q_h + chunk * 8;
           cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, chunk), nb ? src : p.q, nb);
         }
       }
-      for (int k = 0; ok && k < s.n; ++k) {
-        const int j0 = tile_key0(c.r, c.t + k);
-        // lanes 0..7 of every warp look up the pages of the tile's eight groups of 16 keys
+      // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
+      // ahead of their use; -1: no row sees a key of the group.
+      auto look_up = [&](int k) {
         int pg = -1;
-        if (lane < 8) {
-          const int j = j0 + lane * 16;
-          if (j < c.r.sink_hi || (j < c.r.hi && j + 16 > c.r.lo)) pg = key_page(p, c.b, j);
+        if (lane < 8 && k < n) {
+          const int j = part_key0(s, s.t0 + k) + lane * 16;
+          if (j < sink_hi || (j < hi && j + 16 > lo)) pg = key_page(p, b, j);
         }
+        return pg;
+      };
+      int pg_next = look_up(0);
+      for (int k = 0; ok && k < n; ++k) {
+        const int j0 = part_key0(s, s.t0 + k);
+        const int pg = pg_next;
+        pg_next = look_up(k + 1);
+        // every key of the tile is seen by some row and has a page
+        const bool all = j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const uint8_t* base = (kv ? p.c.v : p.c.k) + c.g * (kv ? p.c.vs[2] : p.c.ks[2]);
+          const uint8_t* base = (kv ? p.c.v : p.c.k) + s.g * (kv ? p.c.vs[2] : p.c.ks[2]);
           const int64_t sp = kv ? p.c.vs[0] : p.c.ks[0], st = kv ? p.c.vs[1] : p.c.ks[1];
-          const int slot = it % kRing;
-          if (it >= kRing && !(ok = wait(cEmpty + slot, (it / kRing - 1) & 1))) break;
-          const uint32_t dst = smem_u32(sR) + slot * L::kTile;
+          const int slot = at.slot;
+          if (it >= kRing && !(ok = wait(cEmpty + slot, at.phase ^ 1))) break;
           if (!FP8) {
-            constexpr int CPR = D / 8, RPP = 128 / CPR;
-            const int chunk = lt % CPR;
+            // a thread copies one 16-byte column of rows i * RPP + lt / CPR: its place in the
+            // swizzled tile moves by whole eights of rows, its address with the group's page
+            constexpr int CPR = D / 8, RPP = 128 / CPR, PER = 16 / RPP;  // PER copies a group of 16 keys
+            const int chunk = lt % CPR, r0 = lt / CPR;
+            const uint32_t dst = smem_u32(sR) + slot * L::kTile + tile_off(r0, chunk);
+            const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+            const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
+            const uint8_t* mine = base + r0 * st + chunk * 16;
             const uint32_t cb = chunk * 8 < p.c.d ? 16u : 0u;
-#pragma unroll 4
-            for (int i = 0; i < CPR; ++i) {
-              const int r = i * RPP + lt / CPR, j = j0 + r;
-              const int g = __shfl_sync(0xffffffffu, pg, r >> 4);
-              const bool in = g >= 0 && (j < c.r.sink_hi || (j >= c.r.lo && j < c.r.hi));
-              const uint32_t nb = in ? cb : 0u;
-              cp_async16(dst + tile_off(r, chunk), nb ? base + g * sp + (j & pmask) * st + chunk * 16 : p.c.k, nb);
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const int64_t off = static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
+                                  static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32;
+              if (all) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                  cp_async16(dst + (g * PER + i) * RPP * 128, mine + off + i * RPP * st, cb);
+              } else {
+                const bool paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                  const int j = j0 + g * 16 + i * RPP + r0;
+                  const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
+                  cp_async16(dst + (g * PER + i) * RPP * 128, in ? mine + off + i * RPP * st : p.c.k, in ? cb : 0u);
+                }
+              }
             }
             cp_async_commit();
             ++it;
+            at.step();
             if (it > kLag) {
               cp_async_wait<kLag>();
               announce(it - kLag);
@@ -197,14 +243,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
             constexpr int CPR = D / 16, RPP = 128 / CPR;
             const int chunk = lt % CPR;
             const int64_t* es = kv ? p.c.ves : p.c.kes;
-            const uint8_t* eb = (kv ? p.c.ve : p.c.ke) + c.g * es[2];
+            const uint8_t* eb = (kv ? p.c.ve : p.c.ke) + s.g * es[2];
             uint4 x[CPR];
             uint32_t e[CPR];
 #pragma unroll
             for (int i = 0; i < CPR; ++i) {
               const int r = i * RPP + lt / CPR, j = j0 + r;
               const int g = __shfl_sync(0xffffffffu, pg, r >> 4);
-              const bool in = g >= 0 && (j < c.r.sink_hi || (j >= c.r.lo && j < c.r.hi));
+              const bool in = g >= 0 && (j < sink_hi || (j >= lo && j < hi));
               x[i] = make_uint4(0u, 0u, 0u, 0u);
               e[i] = 127;
               if (in) {
@@ -234,13 +280,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
                     make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
             ++it;
+            at.step();
             cp_async_wait_all();  // the item's Q
             announce(it);
           }
         }
       }
-      left -= s.n;
-      next_part(s, left + s.n);
+      if (!ok) break;
+      part_done(idx);
     }
     cp_async_wait_all();
     if (ok) announce(it);
@@ -252,17 +299,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
       const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);      // K-major view of ring slot 0
       const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16384, 1024);   // MN-major view
       constexpr uint64_t step = static_cast<uint64_t>(L::kTile >> 4);
-      int it = 0;                // ring items before this part
-      int np[2] = {0, 0};        // P tiles consumed by each slot
-      int parts[2] = {0, 0};     // parts begun by each slot
+      RingPos at;          // the next item to arrive: K_0, V_0, K_1, V_1, ...
+      int np[2] = {0, 0};  // P tiles consumed by each slot
+      int nparts[2] = {0, 0};
       bool ok = true;
-      auto full = [&](int item) {
-        if (!wait(cFull + item % kRing, (item / kRing) & 1)) return false;
+      auto arrived = [&]() {
+        if (!wait(cFull + at.slot, at.phase)) return false;
         tc_fence_after();
         return true;
       };
-      auto issue_s = [&](int w, int item) {
-        const uint64_t kd = kd0 + (item % kRing) * step, qd = qd0 + w * step;
+      auto issue_s = [&](int w, int slot) {
+        const uint64_t kd = kd0 + slot * step, qd = qd0 + w * step;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           const uint64_t off = static_cast<uint64_t>(((k >> 2) * 16384u + (k & 3) * 32u) >> 4);
@@ -270,11 +317,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         }
         umma_commit(&bars[cSFull + w]);
       };
-      auto pv = [&](int w, int item, bool start) {
-        if (start && parts[w] > 1) {  // O_w still holds the previous part until its rows have read it
-          if (!wait(cOFree + w, (parts[w] - 2) & 1)) return false;
-        }
-        const uint64_t vd = vd0 + (item % kRing) * step;
+      auto pv = [&](int w, int slot, bool start) {
+        // O_w holds the slot's previous part until its rows have read it
+        if (start && nparts[w] > 1 && !wait(cOFree + w, nparts[w] & 1)) return false;
+        const uint64_t vd = vd0 + slot * step;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           if (!wait(cPReady + 2 * w + hf, np[w] & 1)) return false;
@@ -287,33 +333,77 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         ++np[w];
         return true;
       };
-      for (int left = run, idx = 0; ok && left > 0; ++idx) {
-        const Part s = part_at(left, idx);
-        const int ns = slots_of();
-        for (int w = 0; w < ns; ++w) ++parts[w];
-        for (int k = 0; ok && k <= s.n; ++k) {
-          const int ik = it + 2 * k, iv = it + 2 * (k - 1) + 1;
-          if (k > 0 && !(ok = full(iv))) break;
-          for (int w = 0; ok && w < ns; ++w) {
+      for (int idx = 0; ok; ++idx) {
+        if (!(ok = part_ready(idx))) break;
+        const int n = parts[idx % kParts].n, ns = parts[idx % kParts].slots;
+        part_done(idx);
+        if (n == 0) break;
+        ++nparts[0];
+        if (ns == 2) ++nparts[1];
+        for (int k = 0; ok && k <= n; ++k) {
+          int vslot = 0, kslot = 0;
+          if (k > 0) {
+            if (!(ok = arrived())) break;
+            vslot = at.slot;
+            at.step();
+          }
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w >= ns) break;
             if (k > 0) {
-              if (!(ok = pv(w, iv, k == 1))) break;
-              if (w == ns - 1) umma_commit(&bars[cEmpty + iv % kRing]);
-              if (k == s.n) umma_commit(&bars[cOFinal + w]);
+              if (!(ok = pv(w, vslot, k == 1))) break;
+              if (w == ns - 1) umma_commit(&bars[cEmpty + vslot]);
+              if (k == n) umma_commit(&bars[cOFinal + w]);
             }
-            if (k < s.n) {
-              if (w == 0 && !(ok = full(ik))) break;
-              issue_s(w, ik);
+            if (k < n) {
+              if (w == 0) {
+                if (!(ok = arrived())) break;
+                kslot = at.slot;
+                at.step();
+              }
+              issue_s(w, kslot);
             }
           }
-          if (ok && k < s.n) umma_commit(&bars[cEmpty + ik % kRing]);
-          if (ok && k == s.n - 1) umma_commit(&bars[cQEmpty]);
+          if (ok && k < n) umma_commit(&bars[cEmpty + kslot]);
+          if (ok && k == n - 1) umma_commit(&bars[cQEmpty]);
         }
-        it += 2 * s.n;
-        left -= s.n;
-        next_part(s, left + s.n);
       }
       umma_commit(&bars[cDrain]);
       mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
+    } else if (warp == 3 && lane == 0) {
+      // ---------------------------------------------------------------- walk
+      for (int left = run, idx = 0;; ++idx) {
+        if (idx >= kParts && !wait(cPartFree + idx % kParts, (idx / kParts - 1) & 1)) break;
+        Part& s = parts[idx % kParts];
+        s.n = min(c.r.tiles - c.t, left);
+        if (left > 0) {
+          s.whole = s.n == c.r.tiles;
+          s.slot = idx == 0 ? 0 : 1;
+          s.row0 = c.rt * ROWS;
+          s.slots = c.s.nq * p.G - s.row0 > 128 ? 2 : 1;
+          s.t0 = c.t;
+          s.sink_tiles = c.r.sink_tiles;
+          s.main0 = c.r.main0;
+          s.lo = c.r.lo;
+          s.hi = c.r.hi;
+          s.sink_hi = c.r.sink_hi;
+          s.b = c.b;
+          s.g = c.g;
+          s.q0 = c.s.q0;
+          s.nq = c.s.nq;
+          s.pos0 = c.s.pos0;
+          s.klen = c.s.klen;
+        }
+        mbar_arrive(&bars[cPart + idx % kParts]);
+        if (left == 0) break;
+        if (c.t == 0 && !s.whole)
+          p.desc[blockIdx.x] =
+              make_int4(c.b, c.g, c.rt, s.slot | (1 + (c.r.tiles - s.n + quota - 1) / quota) << 1);
+        const int n = s.n;
+        left -= n;
+        c.t += n - 1;
+        if (left > 0) c.next(p);
+      }
     }
   } else {
     // -------------------------------------------------------------------- softmax
@@ -323,19 +413,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
     const float cexp = p.scale_log2, raise = kRaise / cexp;
     const uint64_t c2 = f2(cexp, cexp);
-    int ns = 0, parts = 0;
+    int ns = 0, ended = 0;  // S tiles and parts of this slot so far
     bool ok = true;
-    for (int left = run, idx = 0; ok && left > 0; ++idx) {
-      const Part s = part_at(left, idx);
-      if (w < slots_of()) {
-        const int R = c.rt * ROWS + row;
-        const bool real = R < c.s.nq * p.G;
-        const int tok = real ? R / p.G : 0;
-        const RowKeys rk = row_keys(p, c.s, c.s.pos0 + (real ? tok : c.s.nq - 1));
+    for (int idx = 0; ok; ++idx) {
+      if (!(ok = part_ready(idx))) break;
+      const Part& s = parts[idx % kParts];
+      const int n = s.n;
+      if (n == 0) break;
+      if (w < s.slots) {
+        // (a row past the item's last one is treated like the last: nothing is stored for it)
+        const int R = s.row0 + row, last = s.nq * p.G - 1;
+        const int pos = s.pos0 + min(R, last) / p.G;
+        const int rhi = p.causal ? pos + 1 : s.klen, rlo = p.window > 0 ? pos - p.window + 1 : 0;
         float m = kNInf, l = 0.f;
-        for (int k = 0; k < s.n; ++k, ++ns) {
-          const int j0 = tile_key0(c.r, c.t + k);
-          const int hi = rk.hi - j0, lo = rk.lo - j0, sk = p.sinks - j0;
+        for (int k = 0; k < n; ++k, ++ns) {
+          const int j0 = part_key0(s, s.t0 + k);
+          const int hi = rhi - j0, lo = rlo - j0, sk = p.sinks - j0;
           const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
           if (!(ok = wait(cSFull + w, ns & 1))) break;
           tc_fence_after();
@@ -416,19 +509,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         }
         if (!ok) break;
         // ---- the part's end
-        if (!(ok = wait(cOFinal + w, parts & 1))) break;
-        ++parts;
+        if (!(ok = wait(cOFinal + w, ended & 1))) break;
+        ++ended;
         tc_fence_after();
+        const bool real = R <= last, whole = s.whole;
+        const int tok = real ? R / p.G : 0;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int64_t pb = (static_cast<int64_t>(blockIdx.x) * 2 + s.slot) * ROWS;
-        const int h = c.g * p.G + R - tok * p.G;
-        const int64_t t = c.s.q0 + tok;
+        const int h = s.g * p.G + R - tok * p.G;
+        const int64_t t = s.q0 + tok;
 #pragma unroll
         for (int a = 0; a < D / 32; ++a) {
           uint32_t o[32];
           tmem_ld32(tl + ocol + a * 32, o);
           tmem_ld_wait(o);
-          if (s.whole) {
+          if (whole) {
             uint16_t* dst = p.out + (t * p.Hq + h) * p.c.d + a * 32;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -449,18 +544,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         }
         tc_fence_before();
         mbar_arrive(&bars[cOFree + w]);
-        if (s.whole) {
+        if (whole) {
           if (real) p.lse[static_cast<int64_t>(h) * p.T + t] = l == 0.f ? kNInf : (m * cexp + log2f(l)) * kPLn2;
         } else {
           p.part_ml[pb + row] = make_float2(m == kNInf ? m : m * cexp, l);
         }
       }
-      if (tid == 128 && c.t == 0 && !s.whole) {
-        const int rest = c.r.tiles - s.n;
-        p.desc[blockIdx.x] = make_int4(c.b, c.g, c.rt, s.slot | (1 + (rest + quota - 1) / quota) << 1);
-      }
-      left -= s.n;
-      next_part(s, left + s.n);
+      part_done(idx);
     }
   }
   tc_fence_before();
