@@ -70,6 +70,13 @@ __device__ __forceinline__ int part_key0(const Part& s, int t) {
   return (t < s.sink_tiles ? t : s.main0 + (t - s.sink_tiles)) * kKeyTile;
 }
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // A place in the K / V ring and the parity of its current fill.
 struct RingPos {
   int slot = 0;
@@ -293,8 +300,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
     if (ok) announce(it);
   } else if (warp < 4) {
     regs_decrease<kRegsMma>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
       // ---------------------------------------------------------------- products
+      // The whole warp runs the loop and one elected lane issues: the descriptors then stay in
+      // uniform registers (with one lane running it all, a product took twice as long to issue).
+      const bool one = elect_one();
       const uint64_t qd0 = sdesc_sw128(smem_u32(sQ), 16, 1024);
       const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);      // K-major view of ring slot 0
       const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16384, 1024);   // MN-major view
@@ -309,6 +319,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         return true;
       };
       auto issue_s = [&](int w, int slot) {
+        if (!one) return;
         const uint64_t kd = kd0 + slot * step, qd = qd0 + w * step;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -325,6 +336,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         for (int hf = 0; hf < 2; ++hf) {
           if (!wait(cPReady + 2 * w + hf, np[w] & 1)) return false;
           tc_fence_after();
+          if (!one) continue;
 #pragma unroll
           for (int k = hf * 4; k < hf * 4 + 4; ++k)
             umma_ts(tbase + 256 + w * 128, tbase + w * 128 + k * 8, vd + static_cast<uint64_t>((k * 2048) >> 4), IDESC_O,
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
       for (int idx = 0; ok; ++idx) {
         if (!(ok = part_ready(idx))) break;
         const int n = parts[idx % kParts].n, ns = parts[idx % kParts].slots;
-        part_done(idx);
+        if (one) part_done(idx);
         if (n == 0) break;
         ++nparts[0];
         if (ns == 2) ++nparts[1];
@@ -352,8 +364,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
             if (w >= ns) break;
             if (k > 0) {
               if (!(ok = pv(w, vslot, k == 1))) break;
-              if (w == ns - 1) umma_commit(&bars[cEmpty + vslot]);
-              if (k == n) umma_commit(&bars[cOFinal + w]);
+              if (w == ns - 1 && one) umma_commit(&bars[cEmpty + vslot]);
+              if (k == n && one) umma_commit(&bars[cOFinal + w]);
             }
             if (k < n) {
               if (w == 0) {
@@ -364,11 +376,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
               issue_s(w, kslot);
             }
           }
-          if (ok && k < n) umma_commit(&bars[cEmpty + kslot]);
-          if (ok && k == n - 1) umma_commit(&bars[cQEmpty]);
+          if (ok && k < n && one) umma_commit(&bars[cEmpty + kslot]);
+          if (ok && k == n - 1 && one) umma_commit(&bars[cQEmpty]);
         }
       }
-      umma_commit(&bars[cDrain]);
+      __syncwarp();
+      if (one) umma_commit(&bars[cDrain]);
       mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------------- walk
