@@ -16,8 +16,8 @@
 //   warps 8..11     masked only in tiles that some row of the warp sees in part, exponentiated
 //                   with a running maximum that is raised only when it grows by 2^8 or more;
 //   warps 12..15    bring Q, K and V: page by page with cp.async into 128-byte-swizzled tiles
-//                   (a ring of five), keys that no row of the item sees as zeros; e4m3 rows come
-//                   through registers, are multiplied by their scale and stored as bf16 (exact).
+//                   (a ring of five), keys that no row of the item sees as zeros; e4m3 rows are copied
+//                   raw, then multiplied by their scale and stored as bf16 (exact).
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 #include "fdma_paged.cuh"
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kChunkThreads = 512;
-constexpr int kRing = 5;
+constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
 constexpr int kLag = 2;  // cp.async groups in flight behind the one being issued
 constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
@@ -37,8 +37,8 @@ constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises
 
 enum ChunkBar : int {
   cFull = 0,             // + ring slot: 128 arrivals of the loading threads
-  cEmpty = kRing,        // + ring slot: the products that read it are done
-  cQEmpty = 2 * kRing,   // the item's last S product is done
+  cEmpty = kRingTiles,   // + ring slot: the products that read it are done
+  cQEmpty = 2 * kRingTiles,   // the item's last S product is done
   cSFull,                // + slot
   cPReady = cSFull + 2,  // + 2 * slot + key half
   cOFinal = cPReady + 4,  // + slot: the item's last PV is done
@@ -77,23 +77,26 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// A place in the K / V ring and the parity of its current fill.
+// A place in a ring of N tiles and the parity of its current fill.
+template <int N>
 struct RingPos {
   int slot = 0;
   uint32_t phase = 0;
   __device__ __forceinline__ void step() {
-    if (++slot == kRing) {
+    if (++slot == N) {
       slot = 0;
       phase ^= 1;
     }
   }
 };
 
-template <int D>
+template <int D, bool FP8>
 struct ChunkSmem {
   static constexpr int kTile = 128 * D * 2;
+  static constexpr int kRing = FP8 ? 4 : kRingTiles;
   static constexpr int kOffRing = 2 * kTile;
-  static constexpr int kOffBar = kOffRing + kRing * kTile;
+  static constexpr int kOffRaw = kOffRing + kRing * kTile;  // e4m3: [2] items as they lie in the cache
+  static constexpr int kOffBar = kOffRaw + (FP8 ? kTile : 0);
   static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
   static constexpr int kOffParts = kOffMisc + 16;
   static constexpr int kOffPlan = kOffParts + kParts * static_cast<int>(sizeof(Part));
@@ -103,7 +106,8 @@ struct ChunkSmem {
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const PagedParams p) {
-  using L = ChunkSmem<D>;
+  using L = ChunkSmem<D, FP8>;
+  using Ring = RingPos<L::kRing>;
   constexpr int ROWS = kChunkRows;
   constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
   constexpr uint32_t IDESC_O = idesc_bf16(128, D, false, true);
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 
   if (tid == 0) {
     for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < kRing; ++i) mbar_init(&bars[cFull + i], 128);
+    for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], 128);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
     for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], 128 + 1 + 256);
@@ -154,40 +158,70 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 
   if (warp >= 12) {
     // ------------------------------------------------------------------ loads
+    // Items (K_0, V_0, K_1, V_1, ... of every part in turn) are issued ahead of the products as far
+    // as the ring goes, across parts.  An item is announced once this thread's copies of it have
+    // landed; a part's first items wait there for its Q, which can be loaded only when the
+    // products of the previous part's last S are done.  Before a wait for those, everything of
+    // earlier parts is announced, so the products can always reach them.
     regs_decrease<kRegsLoad>();
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
-    int it = 0;             // ring items issued
-    RingPos at, said;       // the next item's place; the next to announce
-    int signalled = 0;      // ring items announced
+    Ring at, said;      // the place of the next item to be stored; of the next to be announced
+    int it = 0;         // items issued
+    int announced = 0;
+    int q_item = -1, q_base = 0;  // the item whose copies bring the newest part's Q, that part's first item
     bool ok = true;
     auto announce = [&](int upto) {
+      if (announced >= upto) return;
       fence_proxy_async_smem();
-      for (; signalled < upto; ++signalled, said.step()) mbar_arrive(&bars[cFull + said.slot]);
+      for (; announced < upto; ++announced, said.step()) mbar_arrive(&bars[cFull + said.slot]);
+    };
+    auto slot_free = [&](int item) { return item < L::kRing || wait(cEmpty + at.slot, at.phase ^ 1); };
+    // A thread copies one 16-byte column (of the cache's row) of rows i * RPP + lt / CPR.
+    constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = 128 / CPR;
+    const int chunk = lt % CPR, r0 = lt / CPR;
+    const uint32_t cb = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
+    // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
+    const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
+    uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
+    bool held = false;  // e4m3: the item before the next one is still raw
+    auto convert = [&](int item) {  // (its copies have landed)
+      if (!slot_free(item)) return false;
+      const uint32_t src = raw + (item & 1) * (CPR * 2048);
+#pragma unroll
+      for (int i = 0; i < CPR; ++i) {
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(src + i * 2048)
+                     : "memory");
+        const float sc = exp_scale(e_old[FP8 ? i : 0]);
+        const uint64_t sc2 = f2(sc, sc);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t o[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+          const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+          float a, b;
+          asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+              : "=f"(a), "=f"(b)
+              : "r"(f));
+          f2split(mul2(f2(a, b), sc2), a, b);
+          o[h] = pack_bf16x2(a, b);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
+              make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+      }
+      at.step();
+      return true;
     };
     for (int idx = 0;; ++idx) {
       if (!(ok = part_ready(idx))) break;
       const Part& s = parts[idx % kParts];
-      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
+      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, base = it;
       if (n == 0) break;
-      // Q of both slots, announced with the item's first K tile
-      if (idx > 0) {
-        cp_async_wait_all();  // the products before the wait need all that was issued
-        announce(it);
-        if (!(ok = wait(cQEmpty, (idx - 1) & 1))) break;
-      }
-      {
-        constexpr int CPR = D / 8;
-        const int chunk = lt % CPR;
-        const int row0 = s.row0, q0 = s.q0, g0 = s.g * p.G, rows = s.nq * p.G - row0;
-#pragma unroll 4
-        for (int r = lt / CPR; r < 256; r += 128 / CPR) {
-          const int R = row0 + r, i = R / p.G;
-          const uint32_t nb = r < rows && chunk * 8 < p.c.d ? 16u : 0u;
-          const uint16_t* src = p.q + (q0 + i) * p.q_t + (g0 + R - i * p.G) * p.q_h + chunk * 8;
-          cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, chunk), nb ? src : p.q, nb);
-        }
-      }
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; -1: no row sees a key of the group.
       auto look_up = [&](int k) {
@@ -198,105 +232,110 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         }
         return pg;
       };
-      int pg_next = look_up(0);
-      for (int k = 0; ok && k < n; ++k) {
-        const int j0 = part_key0(s, s.t0 + k);
-        const int pg = pg_next;
-        pg_next = look_up(k + 1);
+      int pg = -1, pg_next = look_up(0);
+#pragma unroll 1
+      for (int i2 = 0; i2 < 2 * n; ++i2) {
+        const bool is_v = i2 & 1;
+        const int j0 = part_key0(s, s.t0 + (i2 >> 1));
+        if (!is_v) {
+          pg = pg_next;
+          pg_next = look_up((i2 >> 1) + 1);
+        }
+        // ---- this item's rows
+        const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
+        const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
+        const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+        const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
+        const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
         // every key of the tile is seen by some row and has a page
         const bool all = j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
+        uint32_t dst = raw + (it & 1) * (CPR * 2048);
+        if (!FP8) {
+          if (!(ok = slot_free(it))) break;
+          dst = smem_u32(sR) + at.slot * L::kTile + tile_off(r0, chunk);
+          at.step();
+        }
+        const int64_t* es = is_v ? p.c.ves : p.c.kes;
+        const uint8_t* efrom = nullptr;
+        int64_t egroup = 0;
+        if (FP8) {
+          efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
+          egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
+        }
+        int64_t off = 0, eoff = 0;
+        bool paged = true;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const uint8_t* base = (kv ? p.c.v : p.c.k) + s.g * (kv ? p.c.vs[2] : p.c.ks[2]);
-          const int64_t sp = kv ? p.c.vs[0] : p.c.ks[0], st = kv ? p.c.vs[1] : p.c.ks[1];
-          const int slot = at.slot;
-          if (it >= kRing && !(ok = wait(cEmpty + slot, at.phase ^ 1))) break;
-          if (!FP8) {
-            // a thread copies one 16-byte column of rows i * RPP + lt / CPR: its place in the
-            // swizzled tile moves by whole eights of rows, its address with the group's page
-            constexpr int CPR = D / 8, RPP = 128 / CPR, PER = 16 / RPP;  // PER copies a group of 16 keys
-            const int chunk = lt % CPR, r0 = lt / CPR;
-            const uint32_t dst = smem_u32(sR) + slot * L::kTile + tile_off(r0, chunk);
-            const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-            const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
-            const uint8_t* mine = base + r0 * st + chunk * 16;
-            const uint32_t cb = chunk * 8 < p.c.d ? 16u : 0u;
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const int64_t off = static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
-                                  static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32;
-              if (all) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                  cp_async16(dst + (g * PER + i) * RPP * 128, mine + off + i * RPP * st, cb);
-              } else {
-                const bool paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                  const int j = j0 + g * 16 + i * RPP + r0;
-                  const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
-                  cp_async16(dst + (g * PER + i) * RPP * 128, in ? mine + off + i * RPP * st : p.c.k, in ? cb : 0u);
-                }
-              }
-            }
-            cp_async_commit();
-            ++it;
-            at.step();
-            if (it > kLag) {
-              cp_async_wait<kLag>();
-              announce(it - kLag);
-            }
-          } else {
-            constexpr int CPR = D / 16, RPP = 128 / CPR;
-            const int chunk = lt % CPR;
-            const int64_t* es = kv ? p.c.ves : p.c.kes;
-            const uint8_t* eb = (kv ? p.c.ve : p.c.ke) + s.g * es[2];
-            uint4 x[CPR];
-            uint32_t e[CPR];
-#pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-              const int r = i * RPP + lt / CPR, j = j0 + r;
-              const int g = __shfl_sync(0xffffffffu, pg, r >> 4);
-              const bool in = g >= 0 && (j < sink_hi || (j >= lo && j < hi));
-              x[i] = make_uint4(0u, 0u, 0u, 0u);
-              e[i] = 127;
-              if (in) {
-                e[i] = eb[g * es[0] + (j & pmask) * es[1]];
-                if (chunk * 16 < p.c.d)
-                  x[i] = __ldg(reinterpret_cast<const uint4*>(base + g * sp + (j & pmask) * st + chunk * 16));
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-              const int r = i * RPP + lt / CPR;
-              const float sc = exp_scale(e[i]);
-              const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int h = 0; h < 8; ++h) {
-                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
-                float lo, hi;
-                asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
-                    : "=f"(lo), "=f"(hi)
-                    : "r"(f));
-                o[h] = pack_bf16x2(lo * sc, hi * sc);
-              }
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4*>(sR + slot * L::kTile + tile_off(r, chunk * 2 + h)) =
-                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-            }
-            ++it;
-            at.step();
-            cp_async_wait_all();  // the item's Q
-            announce(it);
+        for (int i = 0; i < CPR; ++i) {
+          // group of 16 keys of row i * RPP + r0, and the part of the row in it that the thread's r0 leaves
+          constexpr bool kMany = RPP > 16;
+          const int g = ((i * RPP) >> 4) + (kMany ? r0 >> 4 : 0), in_g = (i * RPP) & 15;
+          if (in_g == 0) {
+            off = static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
+                  static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32;
+            if (FP8) eoff = __shfl_sync(0xffffffffu, egroup, g);
+            if (!all) paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
           }
+          const uint32_t to = dst + i * (FP8 ? 2048 : RPP * 128);
+          const int j = j0 + i * RPP + r0;
+          if (all) {
+            cp_async16(to, mine + off + in_g * st, cb);
+            if (FP8) e_new[FP8 ? i : 0] = efrom[eoff];
+          } else {
+            const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
+            cp_async16(to, in ? mine + off + in_g * st : p.c.k, in ? cb : 0u);
+            if (FP8) {
+              e_new[FP8 ? i : 0] = 127;
+              if (in) e_new[FP8 ? i : 0] = efrom[eoff];
+            }
+          }
+        }
+        ++it;
+        // ---- the part's Q, with the third item (or the last, or the first of an e4m3 cache)
+        if (i2 == (FP8 ? 0 : min(2, 2 * n - 1))) {
+          if (idx > 0) {
+            cp_async_wait_all();
+            if (FP8 && held) {
+              if (!(ok = convert(it - 2))) break;
+              held = false;
+            }
+            announce(base);
+            if (!(ok = wait(cQEmpty, (idx - 1) & 1))) break;
+          }
+          q_item = it - 1;
+          q_base = base;
+          constexpr int QCPR = D / 8;
+          const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
+          const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
+#pragma unroll 4
+          for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
+            const int R = row0 + r, i = R / p.G;
+            const uint32_t nb = r < rows ? qb : 0u;
+            cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
+                       nb ? p.q + (q0 + i) * p.q_t + (h0 + R - i * p.G) * p.q_h + qc * 8 : p.q, nb);
+          }
+        }
+        cp_async_commit();
+        if (FP8) {
+          if (held) {
+            cp_async_wait<1>();
+            if (!(ok = convert(it - 2))) break;
+            announce(it - 1);
+          }
+          held = true;
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
+        } else {
+          cp_async_wait<kLag>();
+          // (nothing of a part is announced before the group that brings its Q)
+          const int landed = it - kLag;
+          announce(landed > q_item ? landed : min(landed, q_base));
         }
       }
       if (!ok) break;
       part_done(idx);
     }
     cp_async_wait_all();
+    if (ok && FP8 && held) ok = convert(it - 1);
     if (ok) announce(it);
   } else if (warp < 4) {
     regs_decrease<kRegsMma>();
@@ -309,7 +348,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
       const uint64_t kd0 = sdesc_sw128(smem_u32(sR), 16, 1024);      // K-major view of ring slot 0
       const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16384, 1024);   // MN-major view
       constexpr uint64_t step = static_cast<uint64_t>(L::kTile >> 4);
-      RingPos at;          // the next item to arrive: K_0, V_0, K_1, V_1, ...
+      Ring at;             // the next item to arrive: K_0, V_0, K_1, V_1, ...
       int np[2] = {0, 0};  // P tiles consumed by each slot
       int nparts[2] = {0, 0};
       bool ok = true;
@@ -577,7 +616,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 
 template <int D, bool FP8>
 cudaError_t launch_chunk(const PagedParams& p, cudaStream_t stream) {
-  using L = ChunkSmem<D>;
+  using L = ChunkSmem<D, FP8>;
   auto kern = paged_chunk_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
   if (e != cudaSuccess) return e;
