@@ -184,44 +184,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
     // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
     const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
     uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
-    bool held = false;  // e4m3: the item before the next one is still raw
-    auto convert = [&](int item) {  // (its copies have landed)
-      if (!slot_free(item)) return false;
-      const uint32_t src = raw + (item & 1) * (CPR * 2048);
-#pragma unroll
-      for (int i = 0; i < CPR; ++i) {
-        uint4 x;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                     : "r"(src + i * 2048)
-                     : "memory");
-        const float sc = exp_scale(e_old[FP8 ? i : 0]);
-        const uint64_t sc2 = f2(sc, sc);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t o[8];
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
-          float a, b;
-          asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
-              : "=f"(a), "=f"(b)
-              : "r"(f));
-          f2split(mul2(f2(a, b), sc2), a, b);
-          o[h] = pack_bf16x2(a, b);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
-              make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-      }
-      at.step();
-      return true;
-    };
-    for (int idx = 0;; ++idx) {
+    // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
+    // code fell out of the instruction cache and everything ran at half speed.)
+    for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
       const Part& s = parts[idx % kParts];
       const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, base = it;
-      if (n == 0) break;
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; -1: no row sees a key of the group.
       auto look_up = [&](int k) {
@@ -233,72 +201,115 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         return pg;
       };
       int pg = -1, pg_next = look_up(0);
+      // (one turn without loads at the end of the run, for the last raw item)
+      const int turns = n > 0 ? 2 * n : FP8 ? 1 : 0;
 #pragma unroll 1
-      for (int i2 = 0; i2 < 2 * n; ++i2) {
-        const bool is_v = i2 & 1;
-        const int j0 = part_key0(s, s.t0 + (i2 >> 1));
-        if (!is_v) {
-          pg = pg_next;
-          pg_next = look_up((i2 >> 1) + 1);
-        }
-        // ---- this item's rows
-        const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
-        const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
-        const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-        const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
-        const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
-        // every key of the tile is seen by some row and has a page
-        const bool all = j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
-        uint32_t dst = raw + (it & 1) * (CPR * 2048);
-        if (!FP8) {
-          if (!(ok = slot_free(it))) break;
-          dst = smem_u32(sR) + at.slot * L::kTile + tile_off(r0, chunk);
-          at.step();
-        }
-        const int64_t* es = is_v ? p.c.ves : p.c.kes;
-        const uint8_t* efrom = nullptr;
-        int64_t egroup = 0;
+      for (int i2 = 0; i2 < turns; ++i2) {
         if (FP8) {
-          efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
-          egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
-        }
-        int64_t off = 0, eoff = 0;
-        bool paged = true;
 #pragma unroll
-        for (int i = 0; i < CPR; ++i) {
-          // group of 16 keys of row i * RPP + r0, and the part of the row in it that the thread's r0 leaves
-          constexpr bool kMany = RPP > 16;
-          const int g = ((i * RPP) >> 4) + (kMany ? r0 >> 4 : 0), in_g = (i * RPP) & 15;
-          if (in_g == 0) {
-            off = static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
-                  static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32;
-            if (FP8) eoff = __shfl_sync(0xffffffffu, egroup, g);
-            if (!all) paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
+          for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
+        }
+        if (n > 0) {
+          // ---- this item's rows
+          const bool is_v = i2 & 1;
+          const int j0 = part_key0(s, s.t0 + (i2 >> 1));
+          if (!is_v) {
+            pg = pg_next;
+            pg_next = look_up((i2 >> 1) + 1);
           }
-          const uint32_t to = dst + i * (FP8 ? 2048 : RPP * 128);
-          const int j = j0 + i * RPP + r0;
-          if (all) {
-            cp_async16(to, mine + off + in_g * st, cb);
-            if (FP8) e_new[FP8 ? i : 0] = efrom[eoff];
+          const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
+          const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
+          const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+          const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
+          const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
+          // every key of the tile is seen by some row and has a page
+          const bool all =
+              j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
+          auto key_in = [&](int j, int g) {
+            return __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
+          };
+          auto row_group = [&](int64_t v, int g) { return __shfl_sync(0xffffffffu, v, g); };
+          if (!FP8) {
+            if (!(ok = slot_free(it))) break;
+            constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
+            uint32_t dst = smem_u32(sR) + at.slot * L::kTile + tile_off(r0, chunk);
+            at.step();
+#pragma unroll 2
+            for (int g = 0; g < 8; ++g) {
+              const uint8_t* src = mine + (static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
+                                           static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32);
+#pragma unroll
+              for (int i = 0; i < PER; ++i) {
+                const bool in = all || key_in(j0 + g * 16 + i * RPP + r0, g);
+                cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
+                src += RPP * st;
+                dst += RPP * 128;
+              }
+            }
           } else {
-            const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
-            cp_async16(to, in ? mine + off + in_g * st : p.c.k, in ? cb : 0u);
-            if (FP8) {
+            const int64_t* es = is_v ? p.c.ves : p.c.kes;
+            const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
+            const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
+            const uint32_t dst = raw + (it & 1) * (CPR * 2048);
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              const int g = ((i * RPP) >> 4) + (RPP > 16 ? r0 >> 4 : 0);
+              const int64_t off = row_group(group, g), eoff = row_group(egroup, g);
+              const bool in = all || key_in(j0 + i * RPP + r0, g);
+              cp_async16(dst + i * 2048, in ? mine + off : p.c.k, in ? cb : 0u);
               e_new[FP8 ? i : 0] = 127;
               if (in) e_new[FP8 ? i : 0] = efrom[eoff];
             }
           }
+          ++it;
+          cp_async_commit();
         }
-        ++it;
-        // ---- the part's Q, with the third item (or the last, or the first of an e4m3 cache)
-        if (i2 == (FP8 ? 0 : min(2, 2 * n - 1))) {
-          if (idx > 0) {
-            cp_async_wait_all();
-            if (FP8 && held) {
-              if (!(ok = convert(it - 2))) break;
-              held = false;
+        if (FP8) {
+          // ---- the item before becomes bf16
+          const int item = n > 0 ? it - 2 : it - 1;
+          if (n > 0) cp_async_wait<1>();
+          else cp_async_wait_all();
+          if (item >= announced) {
+            if (!(ok = slot_free(item))) break;
+            const uint32_t src = raw + (item & 1) * (CPR * 2048);
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              uint4 x;
+              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                           : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                           : "r"(src + i * 2048)
+                           : "memory");
+              const float sc = exp_scale(e_old[FP8 ? i : 0]);
+              const uint64_t sc2 = f2(sc, sc);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int h = 0; h < 8; ++h) {
+                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+                float a, c;
+                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                    : "=f"(a), "=f"(c)
+                    : "r"(f));
+                f2split(mul2(f2(a, c), sc2), a, c);
+                o[h] = pack_bf16x2(a, c);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
+                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
-            announce(base);
+            at.step();
+            announce(item + 1);
+          }
+        }
+        // ---- the part's Q: its copies join those of the third item (or, e4m3, follow the first's), so
+        // that the part's first item is announced before the ring is full of them
+        if (n > 0 && i2 == (FP8 ? 0 : 1)) {
+          if (idx > 0) {
+            if (!FP8) {
+              cp_async_wait_all();
+              announce(base);
+            }
             if (!(ok = wait(cQEmpty, (idx - 1) & 1))) break;
           }
           q_item = it - 1;
@@ -306,36 +317,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
           const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
-#pragma unroll 4
+#pragma unroll 2
           for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
             const int R = row0 + r, i = R / p.G;
             const uint32_t nb = r < rows ? qb : 0u;
             cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
                        nb ? p.q + (q0 + i) * p.q_t + (h0 + R - i * p.G) * p.q_h + qc * 8 : p.q, nb);
           }
+          if (FP8) cp_async_commit();  // (its own group: the next item's conversion waits for it)
         }
-        cp_async_commit();
-        if (FP8) {
-          if (held) {
-            cp_async_wait<1>();
-            if (!(ok = convert(it - 2))) break;
-            announce(it - 1);
-          }
-          held = true;
-#pragma unroll
-          for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
-        } else {
+        if (!FP8) {
+          // (nothing of a part is announced before the copies that bring its Q have landed)
           cp_async_wait<kLag>();
-          // (nothing of a part is announced before the group that brings its Q)
           const int landed = it - kLag;
-          announce(landed > q_item ? landed : min(landed, q_base));
+          announce(landed > q_item + 1 ? landed : min(landed, q_base));
         }
       }
-      if (!ok) break;
+      if (!ok || n == 0) break;
       part_done(idx);
     }
     cp_async_wait_all();
-    if (ok && FP8 && held) ok = convert(it - 1);
     if (ok) announce(it);
   } else if (warp < 4) {
     regs_decrease<kRegsMma>();
