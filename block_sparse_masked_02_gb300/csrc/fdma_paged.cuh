@@ -55,6 +55,7 @@ struct PagedParams {
   int4* desc;     // [cta]: the split item that begins in this CTA: (sequence, kv head, row block, slot | pieces << 1)
   int* err;
   int min_run;  // least tiles of a run
+  int box;      // chunk kernel: rows of a TMA box of the cache (0: no TMA)
 };
 
 // One sequence as the kernels use it: every value inside its bounds whatever the arrays hold.

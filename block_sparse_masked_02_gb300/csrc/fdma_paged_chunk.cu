@@ -29,16 +29,16 @@ constexpr int kChunkRows = kChunkItemRows;
 constexpr int kChunkThreads = 512;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
-constexpr int kLag = 2;  // cp.async groups in flight behind the one being issued
 constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
 constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
 
 enum ChunkBar : int {
-  cFull = 0,             // + ring slot: 128 arrivals of the loading threads
+  cFull = 0,             // + ring slot: the loading warps
   cEmpty = kRingTiles,   // + ring slot: the products that read it are done
-  cQEmpty = 2 * kRingTiles,   // the item's last S product is done
+  cQFull = 2 * kRingTiles,  // the part's Q is in shared memory
+  cQEmpty,                  // the part's last S product is done
   cSFull,                // + slot
   cPReady = cSFull + 2,  // + 2 * slot + key half
   cOFinal = cPReady + 4,  // + slot: the item's last PV is done
@@ -105,7 +105,9 @@ struct ChunkSmem {
 };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 1)
+    paged_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const PagedParams p) {
   using L = ChunkSmem<D, FP8>;
   using Ring = RingPos<L::kRing>;
   constexpr int ROWS = kChunkRows;
@@ -132,7 +134,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 
   if (tid == 0) {
     for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], 128);
+    for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], 4);
+    mbar_init(&bars[cQFull], 4);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
     for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], 128 + 1 + 256);
@@ -158,23 +161,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 
   if (warp >= 12) {
     // ------------------------------------------------------------------ loads
-    // Items (K_0, V_0, K_1, V_1, ... of every part in turn) are issued ahead of the products as far
-    // as the ring goes, across parts.  An item is announced once this thread's copies of it have
-    // landed; a part's first items wait there for its Q, which can be loaded only when the
-    // products of the previous part's last S are done.  Before a wait for those, everything of
-    // earlier parts is announced, so the products can always reach them.
+    // Items (K_0, V_0, K_1, V_1, ... of every part in turn) are brought ahead of the products as far
+    // as the ring goes, across parts.  bf16 tiles that are seen whole come by TMA, a box a page;
+    // tiles with keys that no row sees (and layouts that TMA cannot address) by cp.async, which
+    // fills those with zeros.
     regs_decrease<kRegsLoad>();
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
-    Ring at, said;      // the place of the next item to be stored; of the next to be announced
-    int it = 0;         // items issued
-    int announced = 0;
-    int q_item = -1, q_base = 0;  // the item whose copies bring the newest part's Q, that part's first item
+    Ring at;     // the place of the next item
+    int it = 0;  // items issued
     bool ok = true;
-    auto announce = [&](int upto) {
-      if (announced >= upto) return;
+    // every thread of the warp has stored its part of what `bar` announces
+    auto announce = [&](int bar) {
       fence_proxy_async_smem();
-      for (; announced < upto; ++announced, said.step()) mbar_arrive(&bars[cFull + said.slot]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto slot_free = [&](int item) { return item < L::kRing || wait(cEmpty + at.slot, at.phase ^ 1); };
     // A thread copies one 16-byte column (of the cache's row) of rows i * RPP + lt / CPR.
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
     for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
       const Part& s = parts[idx % kParts];
-      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, base = it;
+      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; -1: no row sees a key of the group.
       auto look_up = [&](int k) {
@@ -220,7 +221,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
           const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
           const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
           const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-          const int glo = static_cast<int>(group), ghi = static_cast<int>(group >> 32);
           const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
           // every key of the tile is seen by some row and has a page
           const bool all =
@@ -231,21 +231,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
           auto row_group = [&](int64_t v, int g) { return __shfl_sync(0xffffffffu, v, g); };
           if (!FP8) {
             if (!(ok = slot_free(it))) break;
-            constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
-            uint32_t dst = smem_u32(sR) + at.slot * L::kTile + tile_off(r0, chunk);
-            at.step();
-#pragma unroll 2
-            for (int g = 0; g < 8; ++g) {
-              const uint8_t* src = mine + (static_cast<int64_t>(static_cast<uint32_t>(__shfl_sync(0xffffffffu, glo, g))) |
-                                           static_cast<int64_t>(__shfl_sync(0xffffffffu, ghi, g)) << 32);
+            const int bar = cFull + at.slot;
+            uint8_t* to = sR + at.slot * L::kTile;
+            if (all && p.box > 0) {
+              if (warp == 12) {
+                // lane g brings the page of its group of 16 keys, if that group begins a box
+                if (lane == 0) mbar_arrive_expect_tx(&bars[bar], L::kTile);
+                __syncwarp();
+                if (lane < 8 && ((lane * 16) & (p.box - 1)) == 0) {
+                  const CUtensorMap* tm = is_v ? &tmV : &tmK;
 #pragma unroll
-              for (int i = 0; i < PER; ++i) {
-                const bool in = all || key_in(j0 + g * 16 + i * RPP + r0, g);
-                cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
-                src += RPP * st;
-                dst += RPP * 128;
+                  for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(to + c * 16384 + lane * 2048, tm, &bars[bar], c * 64, (j0 + lane * 16) & pmask, s.g, pg);
+                }
+              } else if (lane == 0) {
+                mbar_arrive(&bars[bar]);
               }
+            } else {
+              constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
+              uint32_t dst = smem_u32(to) + tile_off(r0, chunk);
+#pragma unroll 1
+              for (int g = 0; g < 8; ++g) {
+                const uint8_t* src = mine + row_group(group, g);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                  const bool in = key_in(j0 + g * 16 + i * RPP + r0, g);
+                  cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
+                  src += RPP * st;
+                  dst += RPP * 128;
+                }
+              }
+              cp_async_wait_all();
+              announce(bar);
             }
+            at.step();
           } else {
             const int64_t* es = is_v ? p.c.ves : p.c.kes;
             const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
@@ -262,14 +281,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
             }
           }
           ++it;
-          cp_async_commit();
+          if (FP8) cp_async_commit();
         }
         if (FP8) {
           // ---- the item before becomes bf16
           const int item = n > 0 ? it - 2 : it - 1;
           if (n > 0) cp_async_wait<1>();
           else cp_async_wait_all();
-          if (item >= announced) {
+          if (item >= 0 && (n > 0 || it > 0)) {
             if (!(ok = slot_free(item))) break;
             const uint32_t src = raw + (item & 1) * (CPR * 2048);
 #pragma unroll
@@ -298,22 +317,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
                 *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
                     make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
             }
+            announce(cFull + at.slot);
             at.step();
-            announce(item + 1);
           }
         }
-        // ---- the part's Q: its copies join those of the third item (or, e4m3, follow the first's), so
-        // that the part's first item is announced before the ring is full of them
+        // ---- the part's Q, behind its first loads
         if (n > 0 && i2 == (FP8 ? 0 : 1)) {
-          if (idx > 0) {
-            if (!FP8) {
-              cp_async_wait_all();
-              announce(base);
-            }
-            if (!(ok = wait(cQEmpty, (idx - 1) & 1))) break;
-          }
-          q_item = it - 1;
-          q_base = base;
+          if (idx > 0 && !(ok = wait(cQEmpty, (idx - 1) & 1))) break;
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
           const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
@@ -324,20 +334,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
             cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
                        nb ? p.q + (q0 + i) * p.q_t + (h0 + R - i * p.G) * p.q_h + qc * 8 : p.q, nb);
           }
-          if (FP8) cp_async_commit();  // (its own group: the next item's conversion waits for it)
-        }
-        if (!FP8) {
-          // (nothing of a part is announced before the copies that bring its Q have landed)
-          cp_async_wait<kLag>();
-          const int landed = it - kLag;
-          announce(landed > q_item + 1 ? landed : min(landed, q_base));
+          cp_async_wait_all();
+          announce(cQFull);
         }
       }
       if (!ok || n == 0) break;
       part_done(idx);
     }
     cp_async_wait_all();
-    if (ok) announce(it);
+    // (after a time-out: the TMA boxes in flight land before the CTA ends)
+    if (!FP8 && *abort_flag && warp == 12) {
+      for (int i = 0; i < L::kRing && i < it; ++i) {
+        at.phase ^= at.slot == 0 ? 1u : 0u;
+        at.slot = at.slot == 0 ? L::kRing - 1 : at.slot - 1;
+        mbar_wait(&bars[cFull + at.slot], at.phase, p.err, kDevErrTimeout, nullptr);
+      }
+    }
   } else if (warp < 4) {
     regs_decrease<kRegsMma>();
     if (warp == 0) {
@@ -392,6 +404,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
         if (n == 0) break;
         ++nparts[0];
         if (ns == 2) ++nparts[1];
+        if (!(ok = wait(cQFull, idx & 1))) break;
         for (int k = 0; ok && k <= n; ++k) {
           int vslot = 0, kslot = 0;
           if (k > 0) {
@@ -616,7 +629,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) paged_chunk_kernel(const Pag
 }
 
 template <int D, bool FP8>
-cudaError_t launch_chunk(const PagedParams& p, cudaStream_t stream) {
+cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
   using L = ChunkSmem<D, FP8>;
   auto kern = paged_chunk_kernel<D, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
@@ -625,7 +638,14 @@ cudaError_t launch_chunk(const PagedParams& p, cudaStream_t stream) {
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
   if (fa.numRegs < kChunkLaunchRegs) return cudaErrorInvalidConfiguration;  // the setmaxnreg split must fit
-  kern<<<kPagedCtas, kChunkThreads, L::kTotal, stream>>>(p);
+  CUtensorMap tk{}, tv{};
+  const int page = 1 << p.c.page_shift, rows = page < 128 ? page : 128;
+  // (a cache that broadcasts an axis with stride 0 goes by cp.async)
+  p.box = !FP8 && paged_map(&tk, p.c.k, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.ks, rows) &&
+                  paged_map(&tv, p.c.v, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, rows)
+              ? rows
+              : 0;
+  kern<<<kPagedCtas, kChunkThreads, L::kTotal, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
