@@ -622,7 +622,8 @@ template <int D, bool FP8, int MT>
 cudaError_t launch_token(const PagedParams& p, cudaStream_t stream) {
   using L = TokSmem<D, FP8, MT>;
   auto kern = paged_token_kernel<D, FP8, MT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = set_up_once(ready, kern, L::kTotal, 0);
   if (e != cudaSuccess) return e;
   kern<<<kPagedCtas, kTokThreads, L::kTotal, stream>>>(p);
   e = cudaGetLastError();

@@ -16,6 +16,8 @@
 // their running maximum and weight and are joined by a second kernel.
 #pragma once
 
+#include <atomic>
+
 #include "../../include/fdma_paged.h"
 #include "fdma_internal.h"
 #include "fdma_ptx.cuh"
@@ -294,6 +296,25 @@ __device__ __forceinline__ void cp_async_wait() {
 int validate_cache(const fdma_kv_cache* c);
 CacheView cache_view(const fdma_kv_cache& c);
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Lets a kernel use smem_bytes of shared memory on the current device and checks that it was compiled
+// with at least min_regs registers; done once for each kernel and device (bit `device` of ready).
+template <typename K>
+inline cudaError_t set_up_once(std::atomic<uint64_t>& ready, K* kern, int smem_bytes, int min_regs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (fa.numRegs < min_regs) return cudaErrorInvalidConfiguration;
+  ready.fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
+}
 
 // Attention kernels: the token kernel with its join, and the chunk kernel without.
 constexpr int kChunkItemRows = 256;

@@ -632,12 +632,9 @@ template <int D, bool FP8>
 cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
   using L = ChunkSmem<D, FP8>;
   auto kern = paged_chunk_kernel<D, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kTotal);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = set_up_once(ready, kern, L::kTotal, kChunkLaunchRegs);  // (the setmaxnreg split must fit)
   if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs < kChunkLaunchRegs) return cudaErrorInvalidConfiguration;  // the setmaxnreg split must fit
   CUtensorMap tk{}, tv{};
   const int page = 1 << p.c.page_shift, rows = page < 128 ? page : 128;
   // (a cache that broadcasts an axis with stride 0 goes by cp.async)

@@ -19,6 +19,7 @@ offsets out of range are left out by the kernels and reported by `fdma.device_er
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
@@ -55,6 +56,12 @@ class FdmaPagedArgs(ctypes.Structure):
     ]
 
 
+# The same two structs as packed bytes (native alignment): filling them is a good part of a small
+# call's time, and one struct.pack takes a quarter of what the ctypes fields take.
+_CACHE_FMT = "7iP3qP3qP3qP3qPqP"
+_PACK_CACHE = struct.Struct(_CACHE_FMT).pack
+_PACK_ARGS = struct.Struct(_CACHE_FMT + "2iP2qP4ifPN").pack
+
 _LIB = None
 
 
@@ -62,70 +69,77 @@ def load() -> ctypes.CDLL:
     global _LIB
     if _LIB is None:
         lib = _fdma.load()
-        C, P, I = ctypes.POINTER(FdmaKvCache), ctypes.c_void_p, ctypes.c_int
-        lib.fdma_kv_append.argtypes = [C, P, ctypes.POINTER(ctypes.c_int64), P, ctypes.POINTER(ctypes.c_int64), P, I, P]
+        # (structs go as the address of their packed bytes)
+        S, P, I = ctypes.c_char_p, ctypes.c_void_p, ctypes.c_int
+        lib.fdma_kv_append.argtypes = [S, P, S, P, S, P, I, P]
         lib.fdma_kv_append.restype = I
-        lib.fdma_kv_gather.argtypes = [C, P, P, I, P, P, P]
+        lib.fdma_kv_gather.argtypes = [S, P, P, I, P, P, P]
         lib.fdma_kv_gather.restype = I
-        lib.fdma_paged_workspace_size.argtypes = [ctypes.POINTER(FdmaPagedArgs)]
+        lib.fdma_paged_workspace_size.argtypes = [S]
         lib.fdma_paged_workspace_size.restype = ctypes.c_size_t
-        lib.fdma_paged_fwd.argtypes = [ctypes.POINTER(FdmaPagedArgs), P, P, P]
+        lib.fdma_paged_fwd.argtypes = [S, P, P, P]
         lib.fdma_paged_fwd.restype = I
         _LIB = lib
     return _LIB
 
 
 def _check_device(first, *ts):
-    if not first.is_cuda:
+    dev = first.device
+    if dev.type != "cuda":
         raise ValueError("libfdma takes CUDA tensors only (no CPU path)")
     for t in ts:
-        if t is not None and t.device != first.device:
+        if t is not None and t.device != dev:
             raise ValueError("all tensors of a call are on one device")
+    return dev
 
 
-def _check_int(name, t, shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or (t.dim() and t.numel() > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be int32 {shape} with a contiguous last dimension")
+def _check_int(name, t, n):
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be int32 ({n},) and contiguous")
 
 
-def _on(device, stream):
-    """(guard that makes `device` and the launch stream current, stream pointer): what is allocated
-    for the call then belongs to the stream that it runs on."""
+def _on(dev, stream):
+    """(guard that makes the device and the launch stream current, or None; stream pointer): what is
+    allocated for the call then belongs to the stream that it runs on."""
     if stream is not None:
-        if stream.device != device:
+        if stream.device != dev:
             raise ValueError("the stream belongs to another device than the tensors")
         return torch.cuda.stream(stream), stream.cuda_stream
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device), torch.cuda.current_stream(device).cuda_stream
-    return None, torch.cuda.current_stream(device).cuda_stream
+    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    return guard, torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp) -> FdmaKvCache:
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+def _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp):
+    """The fields of fdma_kv_cache, in order."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be (num_pages, page_size, Hkv, d)")
+    n, ps, h, d = shape
     dt = k_cache.dtype
-    if dt not in (torch.bfloat16, torch.float8_e4m3fn) or v_cache.dtype != dt:
-        raise ValueError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
-    n, ps, h, d = k_cache.shape
     sk, sv = k_cache.stride(), v_cache.stride()
     if d > 1 and (sk[3] != 1 or sv[3] != 1):
         raise ValueError("k_cache and v_cache need a contiguous head dim")
-    B = page_table.shape[0]
-    _check_int("page_table", page_table, (B, page_table.shape[1] if page_table.dim() == 2 else -1))
-    _check_int("k_lens", k_lens, (B,))
-    if dt == torch.bfloat16:
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be int32 (B, max_pages)")
+    B, mp = page_table.shape
+    ts, tc = page_table.stride()
+    if mp > 1 and tc != 1:
+        raise ValueError("page_table must have a contiguous last dimension")
+    _check_int("k_lens", k_lens, B)
+    head = (B, h, d)
+    tail = (page_table.data_ptr(), ts, k_lens.data_ptr())
+    rows = (n, ps, mp, k_cache.data_ptr(), sk[0], sk[1], sk[2], v_cache.data_ptr(), sv[0], sv[1], sv[2])
+    if dt is torch.bfloat16 and v_cache.dtype is dt:
         if k_exp is not None or v_exp is not None:
             raise ValueError("k_exp and v_exp belong to float8_e4m3fn caches")
-        kind, ke, kes, ve, ves = FDMA_CACHE_BF16, None, _I64x3(), None, _I64x3()
-    else:
+        return head + (FDMA_CACHE_BF16,) + rows + (0, 0, 0, 0, 0, 0, 0, 0) + tail
+    if dt is torch.float8_e4m3fn and v_cache.dtype is dt:
         for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-            if t is None or t.dtype != torch.uint8 or tuple(t.shape) != (n, ps, h):
+            if t is None or t.dtype is not torch.uint8 or t.shape != shape[:3]:
                 raise ValueError(f"{name} must be uint8 (num_pages, page_size, Hkv) for a float8_e4m3fn cache")
-        kind, ke, kes, ve, ves = (FDMA_CACHE_E4M3, k_exp.data_ptr(), _I64x3(*k_exp.stride()), v_exp.data_ptr(),
-                                  _I64x3(*v_exp.stride()))
-    return FdmaKvCache(B, h, d, kind, n, ps, page_table.shape[1], k_cache.data_ptr(), _I64x3(*sk[:3]),
-                       v_cache.data_ptr(), _I64x3(*sv[:3]), ke, kes, ve, ves, page_table.data_ptr(),
-                       page_table.stride(0), k_lens.data_ptr())
+        return head + (FDMA_CACHE_E4M3,) + rows + (k_exp.data_ptr(), *k_exp.stride(), v_exp.data_ptr(),
+                                                   *v_exp.stride()) + tail
+    raise ValueError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
 
 
 def empty_cache(num_pages, page_size, Hkv, d, *, dtype=torch.bfloat16, device="cuda"):
@@ -141,20 +155,24 @@ def empty_cache(num_pages, page_size, Hkv, d, *, dtype=torch.bfloat16, device="c
     return (one(dtype, d), one(dtype, d)) + exp
 
 
+_PACK_2Q = struct.Struct("2q").pack
+
+
 def kv_append(k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, k_exp=None, v_exp=None, stream=None):
     """Write the new tokens' rows k, v (T, Hkv, d) bf16 (contiguous head dim) into the cache, quantised
     (with their scale bytes into k_exp, v_exp) where it is float8_e4m3fn.  Rows behind cu_q[B] are ignored.
     The slots of one call must be distinct."""
-    _check_device(k, v, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp)
+    dev = _check_device(k, v, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp)
     c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
-    _check_int("cu_q", cu_q, (c.B + 1,))
-    for name, t in (("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (c.Hkv, c.d) or t.shape[0] != k.shape[0] or \
-                t.stride(2) != 1:
-            raise ValueError(f"{name} must be bf16 (T, Hkv, d) with a contiguous head dim")
-    guard, sp = _on(k.device, stream)
-    args = (ctypes.byref(c), k.data_ptr(), _I64x2(k.stride(0), k.stride(1)), v.data_ptr(),
-            _I64x2(v.stride(0), v.stride(1)), cu_q.data_ptr(), k.shape[0], sp)
+    B, Hkv, d = c[:3]
+    _check_int("cu_q", cu_q, B + 1)
+    sk, sv = k.stride(), v.stride()
+    if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or v.shape != k.shape or len(sk) != 3 or \
+            k.shape[1] != Hkv or k.shape[2] != d or sk[2] != 1 or sv[2] != 1:
+        raise ValueError("k and v must be bf16 (T, Hkv, d) with a contiguous head dim")
+    guard, sp = _on(dev, stream)
+    args = (_PACK_CACHE(*c), k.data_ptr(), _PACK_2Q(sk[0], sk[1]), v.data_ptr(), _PACK_2Q(sv[0], sv[1]),
+            cu_q.data_ptr(), k.shape[0], sp)
     if guard is None:
         st = load().fdma_kv_append(*args)
     else:
@@ -169,23 +187,24 @@ def kv_gather(k_cache, v_cache, page_table, k_lens, cu_k, total, *, first=None, 
     (k, v), each (total, Hkv, d) bf16.  Positions outside [0, k_lens[b]) read as zeros, so with cu_k = b * N
     and total = B * N the result views as the (B, N, Hkv, d) that `fdma.fwd` takes.  Rows behind cu_k[B] are
     left as they are (uninitialised where the outputs are allocated here)."""
-    _check_device(k_cache, v_cache, page_table, k_lens, cu_k, first, k_exp, v_exp, k_out, v_out)
+    dev = _check_device(k_cache, v_cache, page_table, k_lens, cu_k, first, k_exp, v_exp, k_out, v_out)
     c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
-    _check_int("cu_k", cu_k, (c.B + 1,))
+    B, Hkv, d = c[:3]
+    _check_int("cu_k", cu_k, B + 1)
     if first is not None:
-        _check_int("first", first, (c.B,))
-    shape = (int(total), c.Hkv, c.d)
+        _check_int("first", first, B)
+    shape = (int(total), Hkv, d)
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is not None and (t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not t.is_contiguous()):
+        if t is not None and (t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous bf16 {shape}")
+    guard, sp = _on(dev, stream)
 
     def call():
-        ko = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if k_out is None else k_out
-        vo = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device) if v_out is None else v_out
-        return ko, vo, load().fdma_kv_gather(ctypes.byref(c), cu_k.data_ptr(), None if first is None else first.data_ptr(),
+        ko = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+        vo = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+        return ko, vo, load().fdma_kv_gather(_PACK_CACHE(*c), cu_k.data_ptr(), None if first is None else first.data_ptr(),
                                              shape[0], ko.data_ptr(), vo.data_ptr(), sp)
 
-    guard, sp = _on(k_cache.device, stream)
     if guard is None:
         ko, vo, st = call()
     else:
@@ -195,23 +214,28 @@ def kv_gather(k_cache, v_cache, page_table, k_lens, cu_k, total, *, first=None, 
     return ko, vo
 
 
-def make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0,
-              sinks=0, scale=None, workspace=None) -> FdmaPagedArgs:
-    """Fill fdma_paged_args from tensors (see `fwd`)."""
+def _fields(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp, v_exp, causal, window, sinks, scale):
+    """The fields of fdma_paged_args up to the workspace, in order."""
     c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
-    _check_int("cu_q", cu_q, (c.B + 1,))
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != c.d or q.stride(2) != 1:
+    _check_int("cu_q", cu_q, c[0] + 1)
+    sq = q.stride()
+    if q.dtype is not torch.bfloat16 or len(sq) != 3 or q.shape[2] != c[2] or sq[2] != 1:
         raise ValueError("q must be bf16 (T, Hq, d) with a contiguous head dim")
     T, Hq, d = q.shape
-    a = FdmaPagedArgs(c, T, Hq, q.data_ptr(), _I64x2(q.stride(0), q.stride(1)), cu_q.data_ptr(), int(max_q),
-                      1 if causal else 0, int(window), int(sinks), float(scale) if scale is not None else d ** -0.5)
-    if workspace is not None:
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    return a
+    return c + (T, Hq, q.data_ptr(), sq[0], sq[1], cu_q.data_ptr(), int(max_q), 1 if causal else 0, int(window),
+                int(sinks), d ** -0.5 if scale is None else float(scale))
+
+
+def make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0,
+              sinks=0, scale=None, workspace=None) -> FdmaPagedArgs:
+    """fdma_paged_args of a call (see `fwd`)."""
+    f = _fields(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp, v_exp, causal, window, sinks, scale)
+    ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return FdmaPagedArgs.from_buffer_copy(_PACK_ARGS(*f, *ws))
 
 
 def workspace_size(args: FdmaPagedArgs) -> int:
-    return int(load().fdma_paged_workspace_size(ctypes.byref(args)))
+    return int(load().fdma_paged_workspace_size(bytes(args)))
 
 
 def alloc_workspace(args: FdmaPagedArgs, device) -> torch.Tensor:
@@ -227,25 +251,25 @@ def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_e
     with j > p - W or j < sinks.  max_q (a host int) bounds the new tokens of a sequence.  scale defaults to
     d ** -0.5.  A row without keys gets out = 0 and lse = -inf; rows behind cu_q[B] are left as they are
     (uninitialised where out and lse are allocated here).  A workspace passed in serves one call at a time."""
-    _check_device(q, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp, workspace, out, lse)
-    a = make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp=k_exp, v_exp=v_exp, causal=causal,
-                  window=window, sinks=sinks, scale=scale, workspace=workspace)
+    dev = _check_device(q, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp, workspace, out, lse)
+    f = _fields(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp, v_exp, causal, window, sinks, scale)
     T, Hq, d = q.shape
-    if out is not None and (out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
+    if out is not None and (out.dtype is not torch.bfloat16 or out.shape != q.shape or not out.is_contiguous()):
         raise ValueError("out must be contiguous bf16 (T, Hq, d)")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (Hq, T) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 (Hq, T)")
+    guard, sp = _on(dev, stream)
 
     def call():
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device) if out is None else out
-        s = torch.empty((Hq, T), dtype=torch.float32, device=q.device) if lse is None else lse
+        lib = load()
+        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if out is None else out
+        s = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
         ws = workspace
         if ws is None:
-            ws = alloc_workspace(a, q.device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-        return o, s, load().fdma_paged_fwd(ctypes.byref(a), o.data_ptr(), s.data_ptr(), sp)
+            ws = torch.empty(lib.fdma_paged_workspace_size(_PACK_ARGS(*f, 0, 0)), dtype=torch.uint8, device=dev)
+        args = _PACK_ARGS(*f, ws.data_ptr(), ws.numel() * ws.element_size())
+        return o, s, lib.fdma_paged_fwd(args, o.data_ptr(), s.data_ptr(), sp)
 
-    guard, sp = _on(q.device, stream)
     if guard is None:
         o, s, st = call()
     else:
