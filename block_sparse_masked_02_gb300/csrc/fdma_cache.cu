@@ -2,10 +2,11 @@
 //
 // Both move rows of d values between packed tokens and cache slots and are bound by
 // memory traffic (or, for a few tokens, by the latency of token -> sequence -> page ->
-// row).  One warp serves one token and up to kHeadsPerWarp kv heads: the search for the
-// token's sequence and its page is made once for all of them, lanes 0..15 then move the
-// K rows and lanes 16..31 the V rows, eight values a lane, every row's load issued before
-// the first is used.
+// row).  All rows of a call, T tokens times Hkv heads times K and V, form one line of which
+// a warp takes kPasses times the two or four that its lanes move at once (LPR = 16 or 8 lanes
+// a row, eight values a lane): the sequence is searched once for them, and every row's load
+// is issued before the first is used.  (Four passes: eight, with fewer warps on an SM, took
+// 60 instead of 52 us for 82 thousand tokens of four bf16 heads.)
 //
 // e4m3: with m = max |x| of a row, e is the least integer with m <= 448 * 2^e, taken from
 // m's bits: 448 = 1.75 * 2^8, so e = E - 8 where m = f * 2^E has f <= 1.75 and E - 7
@@ -15,8 +16,8 @@
 namespace fdma {
 namespace {
 
-constexpr int kHeadsPerWarp = 4;
-constexpr int kCacheThreads = 256;
+constexpr int kPasses = 4;
+constexpr int kCacheThreads = 128;
 
 struct MoveParams {
   CacheView c;
@@ -52,13 +53,20 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int B, int t, int lan
   return lo - 1 < B ? lo - 1 : -1;
 }
 
-// Byte offset of (page of position pos, slot in it) for strides st (page, token, head) and
-// head g; pg: the page.
-__device__ __forceinline__ int64_t slot_offset(const CacheView& c, const int64_t* st, int pg, int pos, int g) {
-  return pg * st[0] + (pos & ((1 << c.page_shift) - 1)) * st[1] + g * st[2];
+// The same for one lane, by halving.
+__device__ __forceinline__ int find_from_start(const int32_t* cu, int B, int t) {
+  if (cu[0] > t) return -1;
+  int lo = 0, hi = B;  // cu[lo] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo < B ? lo : -1;
 }
 
-// Quantises eight values of a row whose 16 lanes hold it all; returns the codes, e + 127 in `be`.
+// Quantises eight values of a row that LPR lanes hold; returns the codes, e + 127 in `be`.
+template <int LPR>
 __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t m = 0;  // largest finite magnitude, as bf16 bits
@@ -68,7 +76,7 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
     m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   // m = (1 + mant / 128) * 2^(E - 127), 1.75 = 1 + 96 / 128 (bf16 subnormals fall to the clamp)
   const int E = static_cast<int>(m >> 7), up = (m & 0x7fu) > 96u ? 1 : 0;
   const int b = min(max(E - 8 + up, 1), 246);
@@ -101,114 +109,234 @@ __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t be) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// One row of the line: which token, kv head and tensor.
+struct Row {
+  int64_t tok;
+  int g;
+  bool is_v, real;
+};
+
+// The i-th row of a warp whose first is row rem of the 2 * Hkv of token tok0.  ONE: a warp's rows
+// are always one token's.
+template <bool ONE>
+__device__ __forceinline__ Row warp_row(const MoveParams& p, int64_t tok0, int rem, int i) {
+  Row r;
+  int x = rem + i, t = 0;
+  const int per = 2 * p.c.Hkv;
+  if (!ONE && x >= per) {
+    t = x / per;
+    x -= t * per;
+  }
+  r.tok = tok0 + t;
+  r.real = ONE || r.tok < p.T;
+  r.is_v = x >= p.c.Hkv;
+  r.g = r.is_v ? x - p.c.Hkv : x;
+  return r;
+}
+
+// The sequence of token t, which is not before one of sequence b (of token b's search); -1: none.
+__device__ __forceinline__ int seq_from(const MoveParams& p, int b, int t) {
+  if (b < 0) return find_from_start(p.cu, p.c.B, t);
+  while (b < p.c.B && p.cu[b + 1] <= t) ++b;
+  return b < p.c.B ? b : -1;
+}
+
+// Page of position pos of sequence b, or -1 (reported).
+__device__ __forceinline__ int page_at(const MoveParams& p, int b, int pos) {
+  const int pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (pos >> p.c.page_shift)];
+  if (pg >= 0 && pg < p.c.num_pages) return pg;
+  atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+  return -1;
+}
+
+// Where a token's rows lie in the cache, as byte offsets of kv head 0.
+struct Slot {
+  int64_t tok = -1;
+  bool owned = false;  // a sequence has the token
+  bool paged = false;  // and its position has a slot
+  int64_t k, v, ke, ve;
+};
+
 template <bool FP8>
-__global__ void __launch_bounds__(kCacheThreads) kv_append_kernel(const MoveParams p) {
+__device__ __forceinline__ void set_slot(const MoveParams& p, Slot& s, int pg, int pos) {
+  const int64_t at = pos & ((1 << p.c.page_shift) - 1);
+  s.paged = true;
+  s.k = pg * p.c.ks[0] + at * p.c.ks[1];
+  s.v = pg * p.c.vs[0] + at * p.c.vs[1];
+  if (FP8) {
+    s.ke = pg * p.c.kes[0] + at * p.c.kes[1];
+    s.ve = pg * p.c.ves[0] + at * p.c.ves[1];
+  }
+}
+
+template <bool FP8, int LPR, bool ONE>
+__global__ void __launch_bounds__(kCacheThreads) kv_append_kernel(const __grid_constant__ MoveParams p) {
+  constexpr int RPP = 32 / LPR, PASSES = kPasses;
   const int lane = threadIdx.x & 31;
-  const int groups = (p.c.Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x) >> 5;
-  const int64_t tok = w / groups;
-  if (tok >= p.T) return;
-  const int t = static_cast<int>(tok), g0 = static_cast<int>(w % groups) * kHeadsPerWarp;
-  const bool is_v = lane >= 16;
-  const int col = (lane & 15) * 8;
+  const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  int64_t tok0;
+  int rem;
+  if (ONE) {  // a warp's rows divide a token's
+    const uint32_t per = static_cast<uint32_t>(2 * p.c.Hkv) / (RPP * PASSES), t = w / per;
+    tok0 = t;
+    rem = static_cast<int>(w - t * per) * (RPP * PASSES);
+  } else {
+    const int64_t first = static_cast<int64_t>(w) * (RPP * PASSES);
+    tok0 = first / (2 * p.c.Hkv);
+    rem = static_cast<int>(first - tok0 * (2 * p.c.Hkv));
+  }
+  if (tok0 >= p.T) return;
+  const int col = (lane % LPR) * 8;
   const bool in = col < p.c.d;
   // the rows themselves do not depend on the slot: load them while it is looked up
-  const uint16_t* src = (is_v ? p.v_new : p.k_new) + t * (is_v ? p.vn[0] : p.kn[0]) + col;
-  const int64_t sh = is_v ? p.vn[1] : p.kn[1];
-  uint4 x[kHeadsPerWarp];
+  uint4 x[PASSES];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i) {
+  for (int i = 0; i < PASSES; ++i) {
+    const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
     x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && g0 + i < p.c.Hkv) x[i] = __ldg(reinterpret_cast<const uint4*>(src + (g0 + i) * sh));
+    if (in && r.real)
+      x[i] = __ldg(reinterpret_cast<const uint4*>((r.is_v ? p.v_new : p.k_new) + r.tok * (r.is_v ? p.vn[0] : p.kn[0]) +
+                                                  r.g * (r.is_v ? p.vn[1] : p.kn[1]) + col));
   }
-  const int b = find_seq(p.cu, p.c.B, t, lane);
-  if (b < 0) return;  // behind the last sequence
-  const int pos = p.c.k_len[b] - (p.cu[b + 1] - t);
-  int pg = -1;
-  if (pos >= 0 && (pos >> p.c.page_shift) < p.c.max_pages)
-    pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (pos >> p.c.page_shift)];
-  if (pg < 0 || pg >= p.c.num_pages) {
-    if (lane == 0) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
-    return;
-  }
-  uint8_t* dst = const_cast<uint8_t*>(is_v ? p.c.v : p.c.k);
-  const int64_t* st = is_v ? p.c.vs : p.c.ks;
+  const int b0 = find_seq(p.cu, p.c.B, static_cast<int>(tok0), lane);
+  Slot s;
+  auto look_up = [&](int64_t tok) {
+    s = Slot{};
+    s.tok = tok;
+    const int t = static_cast<int>(tok), b = seq_from(p, b0, t);
+    if (b < 0) return;  // behind the last sequence
+    const int pos = p.c.k_len[b] - (p.cu[b + 1] - t);
+    if (pos < 0 || (pos >> p.c.page_shift) >= p.c.max_pages) {
+      atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+      return;
+    }
+    const int pg = page_at(p, b, pos);
+    if (pg >= 0) set_slot<FP8>(p, s, pg, pos);
+  };
+  look_up(tok0);
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i) {
-    const int g = g0 + i;
-    if (g >= p.c.Hkv) break;
+  for (int i = 0; i < PASSES; ++i) {
+    const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
+    uint32_t be = 0;
+    uint2 q = make_uint2(0u, 0u);
+    if (FP8) q = quantise8<LPR>(x[i], be);
+    if (!r.real) continue;
+    if (!ONE && r.tok != s.tok) look_up(r.tok);
+    if (!s.paged) continue;
+    uint8_t* dst = const_cast<uint8_t*>(r.is_v ? p.c.v : p.c.k) + (r.is_v ? s.v : s.k) +
+                   r.g * (r.is_v ? p.c.vs[2] : p.c.ks[2]);
     if (FP8) {
-      uint32_t be;
-      const uint2 q = quantise8(x[i], be);
-      if (in) *reinterpret_cast<uint2*>(dst + slot_offset(p.c, st, pg, pos, g) + col) = q;
-      if ((lane & 15) == 0)
-        const_cast<uint8_t*>(is_v ? p.c.ve : p.c.ke)[slot_offset(p.c, is_v ? p.c.ves : p.c.kes, pg, pos, g)] =
+      if (in) *reinterpret_cast<uint2*>(dst + col) = q;
+      if (col == 0)
+        const_cast<uint8_t*>(r.is_v ? p.c.ve : p.c.ke)[(r.is_v ? s.ve : s.ke) + r.g * (r.is_v ? p.c.ves[2] : p.c.kes[2])] =
             static_cast<uint8_t>(be);
     } else if (in) {
-      *reinterpret_cast<uint4*>(dst + slot_offset(p.c, st, pg, pos, g) + col * 2) = x[i];
+      *reinterpret_cast<uint4*>(dst + col * 2) = x[i];
     }
   }
 }
 
-template <bool FP8>
-__global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const MoveParams p) {
+template <bool FP8, int LPR, bool ONE>
+__global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_constant__ MoveParams p) {
+  constexpr int RPP = 32 / LPR, PASSES = kPasses;
   const int lane = threadIdx.x & 31;
-  const int groups = (p.c.Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  const int64_t w = (static_cast<int64_t>(blockIdx.x) * kCacheThreads + threadIdx.x) >> 5;
-  const int64_t tok = w / groups;
-  if (tok >= p.T) return;
-  const int t = static_cast<int>(tok), g0 = static_cast<int>(w % groups) * kHeadsPerWarp;
-  const bool is_v = lane >= 16;
-  const int col = (lane & 15) * 8;
-  const int b = find_seq(p.cu, p.c.B, t, lane);
-  if (b < 0) return;
-  const int64_t pos64 = static_cast<int64_t>(p.first != nullptr ? p.first[b] : 0) + (t - p.cu[b]);
-  const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
-  const int kl = p.c.k_len[b];
-  if ((kl < 0 || kl > cap) && lane == 0) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
-  int pg = -1;
-  const int pos = static_cast<int>(pos64);
-  if (pos64 >= 0 && pos64 < min(static_cast<int64_t>(kl), cap)) {
-    pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (pos >> p.c.page_shift)];
-    if (pg < 0 || pg >= p.c.num_pages) {
-      if (lane == 0) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
-      pg = -1;
-    }
+  const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  int64_t tok0;
+  int rem;
+  if (ONE) {  // a warp's rows divide a token's
+    const uint32_t per = static_cast<uint32_t>(2 * p.c.Hkv) / (RPP * PASSES), t = w / per;
+    tok0 = t;
+    rem = static_cast<int>(w - t * per) * (RPP * PASSES);
+  } else {
+    const int64_t first = static_cast<int64_t>(w) * (RPP * PASSES);
+    tok0 = first / (2 * p.c.Hkv);
+    rem = static_cast<int>(first - tok0 * (2 * p.c.Hkv));
   }
-  if (col >= p.c.d) return;
-  const uint8_t* src = is_v ? p.c.v : p.c.k;
-  const uint8_t* ex = is_v ? p.c.ve : p.c.ke;
-  const int64_t* st = is_v ? p.c.vs : p.c.ks;
-  const int64_t* es = is_v ? p.c.ves : p.c.kes;
-  uint16_t* dst = (is_v ? p.v_out : p.k_out) + (tok * p.c.Hkv + g0) * p.c.d + col;
-  uint4 x[kHeadsPerWarp];
-  uint32_t be[kHeadsPerWarp];
+  if (tok0 >= p.T) return;
+  const int col = (lane % LPR) * 8;
+  const bool in = col < p.c.d;
+  const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
+  const int b0 = find_seq(p.cu, p.c.B, static_cast<int>(tok0), lane);
+  uint4 x[PASSES];
+  uint32_t be[PASSES];
+  uint32_t store = 0;  // bit i: pass i has a row to write
+  Slot s;
+  auto look_up = [&](int64_t tok) {
+    s = Slot{};
+    s.tok = tok;
+    const int t = static_cast<int>(tok), b = seq_from(p, b0, t);
+    if (b < 0) return;
+    s.owned = true;
+    const int64_t at = static_cast<int64_t>(p.first != nullptr ? p.first[b] : 0) + (t - p.cu[b]);
+    const int kl = p.c.k_len[b];
+    if (kl < 0 || kl > cap) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+    if (at < 0 || at >= min(static_cast<int64_t>(kl), cap)) return;
+    const int pg = page_at(p, b, static_cast<int>(at));
+    if (pg >= 0) set_slot<FP8>(p, s, pg, static_cast<int>(at));
+  };
+  look_up(tok0);
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i) {
+  for (int i = 0; i < PASSES; ++i) {
+    const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
     x[i] = make_uint4(0u, 0u, 0u, 0u);
     be[i] = 127;
-    if (pg >= 0 && g0 + i < p.c.Hkv) {
-      const uint8_t* a = src + slot_offset(p.c, st, pg, pos, g0 + i);
-      if (FP8) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(a + col));
-        x[i].x = q.x;
-        x[i].y = q.y;
-        be[i] = ex[slot_offset(p.c, es, pg, pos, g0 + i)];
-      } else {
-        x[i] = __ldg(reinterpret_cast<const uint4*>(a + col * 2));
-      }
+    if (!r.real) continue;
+    if (!ONE && r.tok != s.tok) look_up(r.tok);
+    if (!s.owned) continue;
+    store |= 1u << i;
+    if (!s.paged || !in) continue;
+    const uint8_t* src = (r.is_v ? p.c.v : p.c.k) + (r.is_v ? s.v : s.k) + r.g * (r.is_v ? p.c.vs[2] : p.c.ks[2]);
+    if (FP8) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(src + col));
+      x[i].x = q.x;
+      x[i].y = q.y;
+      be[i] = (r.is_v ? p.c.ve : p.c.ke)[(r.is_v ? s.ve : s.ke) + r.g * (r.is_v ? p.c.ves[2] : p.c.kes[2])];
+    } else {
+      x[i] = __ldg(reinterpret_cast<const uint4*>(src + col * 2));
     }
   }
+  if (!in) return;
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp; ++i) {
-    if (g0 + i >= p.c.Hkv) break;
-    *reinterpret_cast<uint4*>(dst + i * p.c.d) = FP8 ? dequantise8(make_uint2(x[i].x, x[i].y), be[i]) : x[i];
+  for (int i = 0; i < PASSES; ++i) {
+    if (!((store >> i) & 1u)) continue;
+    const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
+    *reinterpret_cast<uint4*>((r.is_v ? p.v_out : p.k_out) + (r.tok * p.c.Hkv + r.g) * p.c.d + col) =
+        FP8 ? dequantise8(make_uint2(x[i].x, x[i].y), be[i]) : x[i];
   }
 }
 
-int64_t move_blocks(int T, int Hkv) {
-  const int64_t warps = static_cast<int64_t>(T) * ((Hkv + kHeadsPerWarp - 1) / kHeadsPerWarp);
-  return (warps * 32 + kCacheThreads - 1) / kCacheThreads;
+struct Append {
+  template <bool FP8, int LPR, bool ONE>
+  static auto kernel() {
+    return kv_append_kernel<FP8, LPR, ONE>;
+  }
+};
+struct Gather {
+  template <bool FP8, int LPR, bool ONE>
+  static auto kernel() {
+    return kv_gather_kernel<FP8, LPR, ONE>;
+  }
+};
+
+// A warp's rows are one token's where they divide its 2 * Hkv (the usual head counts); that form needs
+// no division a row and one lookup a warp.
+template <typename K>
+void launch_move(bool fp8, int d, int Hkv, unsigned blocks, const MoveParams& p, cudaStream_t stream, K) {
+  const int lpr = d > 64 ? 16 : 8;
+  const bool one = 2 * Hkv % (kPasses * (32 / lpr)) == 0;
+  void (*kern)(MoveParams);
+  if (lpr == 16)
+    kern = fp8 ? (one ? K::template kernel<true, 16, true>() : K::template kernel<true, 16, false>())
+               : (one ? K::template kernel<false, 16, true>() : K::template kernel<false, 16, false>());
+  else
+    kern = fp8 ? (one ? K::template kernel<true, 8, true>() : K::template kernel<true, 8, false>())
+               : (one ? K::template kernel<false, 8, true>() : K::template kernel<false, 8, false>());
+  kern<<<blocks, kCacheThreads, 0, stream>>>(p);
+}
+
+int64_t move_blocks(int T, int Hkv, int d) {
+  const int64_t rows = static_cast<int64_t>(T) * 2 * Hkv, per = kPasses * (kCacheThreads / (d > 64 ? 16 : 8));
+  return (rows + per - 1) / per;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -295,8 +423,8 @@ int fdma_kv_append(const fdma_kv_cache* c, const void* k_new, const int64_t kn[2
     if (n > 1 && c->cache_type == FDMA_CACHE_E4M3 && (c->k_exp_stride[i] == 0 || c->v_exp_stride[i] == 0))
       return FDMA_ERR_INVALID;
   }
-  const int64_t blocks = move_blocks(T, c->Hkv);
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  const int64_t blocks = move_blocks(T, c->Hkv, c->d);
+  if (blocks > 0x1fffffff) return FDMA_ERR_UNSUPPORTED;
   MoveParams p{};
   p.c = cache_view(*c);
   p.k_new = static_cast<const uint16_t*>(k_new);
@@ -309,8 +437,8 @@ int fdma_kv_append(const fdma_kv_cache* c, const void* k_new, const int64_t kn[2
   p.T = T;
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
-  auto kern = c->cache_type == FDMA_CACHE_E4M3 ? kv_append_kernel<true> : kv_append_kernel<false>;
-  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  launch_move(c->cache_type == FDMA_CACHE_E4M3, c->d, c->Hkv, static_cast<unsigned>(blocks), p,
+              static_cast<cudaStream_t>(stream), Append{});
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
@@ -322,8 +450,8 @@ int fdma_kv_gather(const fdma_kv_cache* c, const int32_t* cu, const int32_t* fir
   if (T == 0 || c->B == 0) return FDMA_OK;
   if (cu == nullptr || k_out == nullptr || v_out == nullptr) return FDMA_ERR_INVALID;
   if (!aligned16(k_out) || !aligned16(v_out)) return FDMA_ERR_UNSUPPORTED;
-  const int64_t blocks = move_blocks(T, c->Hkv);
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  const int64_t blocks = move_blocks(T, c->Hkv, c->d);
+  if (blocks > 0x1fffffff) return FDMA_ERR_UNSUPPORTED;
   MoveParams p{};
   p.c = cache_view(*c);
   p.cu = cu;
@@ -333,8 +461,8 @@ int fdma_kv_gather(const fdma_kv_cache* c, const int32_t* cu, const int32_t* fir
   p.v_out = static_cast<uint16_t*>(v_out);
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
-  auto kern = c->cache_type == FDMA_CACHE_E4M3 ? kv_gather_kernel<true> : kv_gather_kernel<false>;
-  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  launch_move(c->cache_type == FDMA_CACHE_E4M3, c->d, c->Hkv, static_cast<unsigned>(blocks), p,
+              static_cast<cudaStream_t>(stream), Gather{});
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
