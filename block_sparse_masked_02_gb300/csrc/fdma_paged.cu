@@ -1,26 +1,29 @@
 // Attention of few new tokens a sequence (decoding, a handful of drafted tokens) over a
 // paged cache, and the host side of fdma_paged_fwd.
 //
-// An item is a kv head's query rows of one sequence, at most 16 * MT of them.  Every key
-// and value is read from HBM once and takes part in 4 * d flops a row, so with few rows the
-// kernel is bound by memory, and its work is to keep enough loads in flight: each of the
-// eight warps of a CTA runs its own ring of kStages cp.async stages of 16 keys' K and V rows
-// (192 or 160 KB in flight on an SM at d = 128), with no barrier between warps inside the loop, and
-// the ring runs on across items, so that a batch of short sequences streams like one long one.
-// A tile of 128 keys is 16 keys a warp; page_size is a multiple of 16, so a warp's keys lie in
-// one page.
+// An item is a kv head's query rows of one sequence, at most 8 * NT of them.  Every key and
+// value is read from HBM once and takes part in 4 * d flops a row, so with few rows the kernel
+// is bound by memory, and its work is to keep enough loads in flight with few instructions:
+// each warp of the one CTA on an SM runs its own ring of cp.async stages of 16 keys' K and V
+// rows (192 KB on an SM at d = 128), with no barrier between warps inside the loop, and the
+// ring runs on across items, so that a batch of short sequences streams like one long one.
+// page_size is a multiple of 16, so a warp's keys lie in one page.
 //
 // Each warp keeps its own running maximum, weight sum and output for its keys (online
-// softmax), and the eight are joined at the end of the item.  The products are
-// mma.sync.m16n8k16: at 16 rows the tensor pipe is idle most of the time whichever
-// instruction feeds it, and this one takes the keys as they lie in shared memory and P straight
-// from registers.
+// softmax), and they are joined at the end of the item.  The products are mma.sync with the
+// keys (then the head dim) as the 16 rows of A and eight query rows as the columns of B:
+//   S^T = K Q^T,    O^T += V^T P^T,
+// so eight rows, the usual group of one token, waste nothing; P^T becomes the B operand by one
+// 8 x 8 transpose of 16-bit values in registers.  At so few rows the tensor pipe is idle most of
+// the time whichever instruction feeds it, and this one takes K and V as they lie in shared
+// memory.
 //
 // e4m3 caches: codes become f16 exactly (one conversion for two), so the products run in f16.
 // q is scaled by a power of two per row to [2^14, 2^15), which is exact but for parts below
 // 2^-38 of the row's largest.  The key's scale multiplies S; the value's scale multiplies P,
 // as 2^(e - r + 15) with r the largest e so far (the output is kept in units of 2^(r - 15)), so
 // that P stays in f16's range and a weight keeps all 11 bits down to 2^-29 of the largest.
+// Half the bytes a key and the conversions on top leave less time for latency: 16 warps.
 #include <cmath>
 
 #include "fdma_paged.cuh"
@@ -29,8 +32,6 @@ namespace fdma {
 
 namespace {
 
-constexpr int kTokWarps = 8;
-constexpr int kTokThreads = kTokWarps * 32;
 constexpr int kTokenRows = 32;  // packed rows up to which the token kernel runs
 constexpr float kNInf = -__builtin_huge_valf();
 
@@ -68,26 +69,43 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float quad_max(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+// Over the eight lanes that hold a query row (lane & 3 the same).
+__device__ __forceinline__ float row_max(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// The 8 x 8 matrix of 16-bit values that the warp holds as (row lane / 4, columns 2 * (lane & 3) + {0, 1}),
+// transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-// D: 64 or 128, the head dim's padded width (columns past d are read as zeros).
-template <int D, bool FP8, int MT>
-struct TokSmem {
-  static constexpr int kRowB = FP8 ? D : 2 * D;        // bytes of a row in shared memory
-  static constexpr int kHalfB = 16 * kRowB;            // 16 keys of K (or V)
-  static constexpr int kStages = kRowB == 256 ? 3 : FP8 ? 5 : 6;
+// D: 64 or 128, the head dim's padded width (columns past d are read as zeros); NT: eights of rows.
+template <int D, bool FP8, int NT>
+struct TokCfg {
+  static constexpr int kWarps = FP8 && NT == 1 ? 16 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kKeys = kWarps * 16;         // keys of a tile
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRowB = FP8 ? D : 2 * D;     // bytes of a row in shared memory
+  static constexpr int kHalfB = 16 * kRowB;         // 16 keys of K (or V)
+  static constexpr int kStages = kRowB == 256 ? 3 : kWarps == 16 ? 3 : FP8 ? 5 : 6;
   static constexpr int kWarpB = kStages * 2 * kHalfB;
-  static constexpr int kOffMerge = kTokWarps * kWarpB;     // [8][16][64] fp32
-  static constexpr int kOffMl = kOffMerge + 8 * 16 * 64 * 4;  // [8][16 * MT] (maximum, sum)
-  static constexpr int kOffExp = kOffMl + 8 * 16 * MT * 8;    // [8][kStages][32] scale bytes (e4m3)
-  static constexpr int kOffPlan = kOffExp + (FP8 ? 8 * kStages * 32 : 0);
+  // columns joined at a time: [kWarps][kRows][kCols] fp32 within 32 KB
+  static constexpr int kFit = 32768 / (kWarps * kRows * 4);
+  static constexpr int kCols = kFit >= D ? D : kFit >= 64 ? 64 : 32;
+  static constexpr int kOffMerge = kWarps * kWarpB;
+  static constexpr int kOffMl = kOffMerge + kWarps * kRows * kCols * 4;  // [kWarps][kRows] (maximum, sum)
+  static constexpr int kOffExp = kOffMl + kWarps * kRows * 8;            // [kWarps][kStages][32] scale bytes (e4m3)
+  static constexpr int kOffPlan = kOffExp + (FP8 ? kWarps * kStages * 32 : 0);
   static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
@@ -99,12 +117,13 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return r * ROWB + ((ROWB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7)) << 4);
 }
 
-template <int D, bool FP8, int MT>
-__global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const PagedParams p) {
-  using L = TokSmem<D, FP8, MT>;
-  constexpr int ROWS = 16 * MT, NST = L::kStages, ROWB = L::kRowB;
-  constexpr int CPR = ROWB / 16;           // 16-byte chunks of a row
-  constexpr int RPP = 32 / CPR;            // rows that a warp copies at a time
+template <int D, bool FP8, int NT>
+__global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
+    paged_token_kernel(const __grid_constant__ PagedParams p) {
+  using L = TokCfg<D, FP8, NT>;
+  constexpr int ROWS = L::kRows, NST = L::kStages, ROWB = L::kRowB, W = L::kWarps;
+  constexpr int CPR = ROWB / 16;  // 16-byte chunks of a row
+  constexpr int RPP = 32 / CPR;   // rows that a warp copies at a time
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = lane & 3, n8 = lane >> 2;
   PlanSmem* plan = reinterpret_cast<PlanSmem*>(smem + L::kOffPlan);
@@ -113,76 +132,88 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
   uint8_t* sexp = smem + L::kOffExp + warp * NST * 32;
   const uint32_t ring = smem_u32(smem) + warp * L::kWarpB;
 
-  Cursor<ROWS> lc;  // the tile that is loaded next
+  Cursor<ROWS, L::kKeys> lc;  // the tile that is loaded next
   int quota;
-  const int run = plan_run<ROWS, kTokThreads>(p, plan, lc, quota);
+  const int run = plan_run<ROWS, L::kKeys, L::kThreads>(p, plan, lc, quota);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   write_empty_blocks<ROWS>(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up; it waits for the end
   if (run == 0) return;
-  Cursor<ROWS> cc = lc;  // the tile that is computed next
+  Cursor<ROWS, L::kKeys> cc = lc;  // the tile that is computed next
 
   // ---- loads: stage (x mod NST) of this warp's ring takes its 16 keys of tile x
   const int chunk = lane % CPR, crow = lane / CPR;
   const uint32_t cbytes = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
   const int pmask = (1 << p.c.page_shift) - 1;
   uint32_t exp_pend = 127;
-  auto page_of = [&](const Cursor<ROWS>& c) {
-    const int j0 = c.key0() + warp * 16;
-    // a warp's keys are looked up only where some row sees one of them
-    return j0 < c.r.sink_hi || (j0 < c.r.hi && j0 + 16 > c.r.lo) ? key_page(p, c.b, j0) : -1;
-  };
-  int lpage = page_of(lc);
-  auto issue = [&](int x) {
-    const int st = x % NST;
-    const uint32_t dst = ring + st * 2 * L::kHalfB;
+  auto some_seen = [&](const Span& r, int j0) { return j0 < r.sink_hi || (j0 < r.hi && j0 + 16 > r.lo); };
+  // a warp's keys are looked up only where some row sees one of them
+  auto page_of = [&]() {
     const int j0 = lc.key0() + warp * 16;
-    if (FP8 && x > 0) sexp[((x - 1) % NST) * 32 + lane] = static_cast<uint8_t>(exp_pend);
-    const int64_t pg = lpage < 0 ? 0 : lpage;
-    const uint8_t* kb = p.c.k + pg * p.c.ks[0] + (j0 & pmask) * p.c.ks[1] + lc.g * p.c.ks[2] + chunk * 16;
-    const uint8_t* vb = p.c.v + pg * p.c.vs[0] + (j0 & pmask) * p.c.vs[1] + lc.g * p.c.vs[2] + chunk * 16;
-#pragma unroll
-    for (int i = 0; i < 16 / RPP; ++i) {
-      const int r = i * RPP + crow, j = j0 + r;
-      const bool ok = lpage >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi));
-      const uint32_t nb = ok ? cbytes : 0u;
-      cp_async16(dst + swz<ROWB>(r, chunk), nb ? kb + r * p.c.ks[1] : p.c.k, nb);
-      cp_async16(dst + L::kHalfB + swz<ROWB>(r, chunk), nb ? vb + r * p.c.vs[1] : p.c.v, nb);
-    }
-    if (FP8) {
-      const int r = lane & 15, j = j0 + r;
-      exp_pend = 0;
-      if (lpage >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi))) {
-        const int64_t* es = lane < 16 ? p.c.kes : p.c.ves;
-        exp_pend = (lane < 16 ? p.c.ke : p.c.ve)[pg * es[0] + (j & pmask) * es[1] + lc.g * es[2]];
-      }
-    }
+    return some_seen(lc.r, j0) ? key_page(p, lc.b, j0) : -1;
   };
-  int loaded = 0;
+  int lpage = page_of(), lstage = 0, loaded = 0;
   auto load_next = [&]() {
+    if (FP8 && loaded > 0 && loaded <= run) sexp[(lstage == 0 ? NST - 1 : lstage - 1) * 32 + lane] = static_cast<uint8_t>(exp_pend);
     if (loaded < run) {
-      issue(loaded);
-      if (++loaded < run) {
-        lc.next(p);
-        lpage = page_of(lc);
+      const uint32_t dst = ring + lstage * 2 * L::kHalfB;
+      const int j0 = lc.key0() + warp * 16;
+      const int64_t pg = lpage;
+      const uint8_t* kb = p.c.k + pg * p.c.ks[0] + ((j0 & pmask) + crow) * p.c.ks[1] + lc.g * p.c.ks[2] + chunk * 16;
+      const uint8_t* vb = p.c.v + pg * p.c.vs[0] + ((j0 & pmask) + crow) * p.c.vs[1] + lc.g * p.c.vs[2] + chunk * 16;
+      if (lpage >= 0 && j0 >= lc.r.lo && j0 + 16 <= lc.r.hi) {  // all 16 keys
+#pragma unroll
+        for (int i = 0; i < 16 / RPP; ++i) {
+          cp_async16(dst + swz<ROWB>(i * RPP + crow, chunk), kb, cbytes);
+          cp_async16(dst + L::kHalfB + swz<ROWB>(i * RPP + crow, chunk), vb, cbytes);
+          kb += RPP * p.c.ks[1];
+          vb += RPP * p.c.vs[1];
+        }
+      } else if (lpage >= 0) {
+#pragma unroll 1
+        for (int i = 0; i < 16 / RPP; ++i) {
+          const int r = i * RPP + crow, j = j0 + r;
+          const bool ok = j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi);
+          cp_async16(dst + swz<ROWB>(r, chunk), ok ? kb : p.c.k, ok ? cbytes : 0u);
+          cp_async16(dst + L::kHalfB + swz<ROWB>(r, chunk), ok ? vb : p.c.v, ok ? cbytes : 0u);
+          kb += RPP * p.c.ks[1];
+          vb += RPP * p.c.vs[1];
+        }
+      } else if (some_seen(lc.r, j0)) {  // no page: keys of zeros
+#pragma unroll 1
+        for (int i = 0; i < 2 * L::kHalfB / 512; ++i)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512 + lane * 16), "r"(0) : "memory");
       }
-    } else if (FP8 && loaded == run) {
-      sexp[((run - 1) % NST) * 32 + lane] = static_cast<uint8_t>(exp_pend);
+      if (FP8) {
+        const int r = lane & 15, j = j0 + r;
+        exp_pend = 0;
+        if (lpage >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi))) {
+          const int64_t* es = lane < 16 ? p.c.kes : p.c.ves;
+          exp_pend = (lane < 16 ? p.c.ke : p.c.ve)[pg * es[0] + (j & pmask) * es[1] + lc.g * es[2]];
+        }
+      }
+      lstage = lstage + 1 == NST ? 0 : lstage + 1;
+      if (loaded + 1 < run) {
+        lc.next(p);
+        lpage = page_of();
+      }
     }
+    ++loaded;
     cp_async_commit();
   };
 #pragma unroll 1
   for (int i = 0; i < NST - 1; ++i) load_next();
 
-  uint32_t qf[MT][D / 16][4];  // Q as A fragments
-  float rowfac[MT][2];         // log2(e) * scale (and the row's power of two) of rows n8, n8 + 8
-  RowKeys rk[MT][2];
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];
-  int ref = 0;  // e4m3: the largest value scale byte so far
-  int seg0 = 0;             // tile of the item at which this CTA began
-  bool first_seg = true;
-  bool begin = true;
+  uint32_t qf[NT][D / 16][2];  // Q^T as B operands: rows n8 of each eight
+  float rowfac[NT][2];         // log2(e) * scale (and the row's power of two) of rows 2 * q4 + {0, 1}
+  int rlo[NT][2], rhi[NT][2];  // their keys
+  float o[NT][D / 16][4];      // O^T: head dim n8 (+ 8; e4m3: 2 * n8 + {0, 1}) of each 16, rows 2 * q4 + {0, 1}
+  float m[NT][2], l[NT][2];
+  int full_lo = 0, full_hi = 0;  // keys that every row sees
+  int ref = 0;                   // e4m3: the largest value scale byte so far
+  int seg0 = 0;                  // tile of the item at which this CTA began
+  int stage = 0;
+  bool first_seg = true, begin = true;
 
 #pragma unroll 1
   for (int x = 0; x < run; ++x) {
@@ -190,59 +221,65 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
       // ---- a new item: its query rows, and an empty softmax
       begin = false;
       seg0 = cc.t;
+      const int rows = cc.s.nq * p.G - cc.rt * ROWS;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int nt = 0; nt < NT; ++nt) {
+        const int pr = nt * 8 + n8, R = cc.rt * ROWS + pr;
+        const bool in = pr < rows;
+        const int i = in ? R / p.G : 0;
+        const uint16_t* src = p.q + (cc.s.q0 + i) * p.q_t + (cc.g * p.G + (in ? R - i * p.G : 0)) * p.q_h;
+        uint32_t top = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = cc.rt * ROWS + mt * 16 + h * 8 + n8;
-          const bool in = r < cc.s.nq * p.G;
-          const int i = in ? r / p.G : 0;
-          const uint16_t* src = p.q + (cc.s.q0 + i) * p.q_t + (cc.g * p.G + (in ? r - i * p.G : 0)) * p.q_h;
-          rk[mt][h] = row_keys(p, cc.s, cc.s.pos0 + i);
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // the pair's columns: with e4m3 a lane's key bytes are D / 4 adjacent ones, so the
+            // order of the columns inside the product is that of those bytes
+            const int col = FP8 ? q4 * (D / 4) + s * 4 + e * 2 : s * 16 + e * 8 + q4 * 2;
+            const uint32_t w = in && col < p.c.d ? __ldg(reinterpret_cast<const uint32_t*>(src + col)) : 0u;
+            qf[nt][s][e] = w;
+            top = max(top, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+          }
+        float fac = p.scale_log2;
+        if (FP8) {
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          // q * 2^up has its largest part in [2^14, 2^15)
+          const int E = static_cast<int>(top >> 7);
+          const int up = E == 0 || E == 255 ? 0 : 14 + 127 - E;
+          const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up / 2) << 23);
+          const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
+          fac = p.scale_log2 / f1 / f2;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              // the pair's columns: with e4m3 a lane's key bytes are D / 4 adjacent ones, so the
-              // order of the columns inside the product is that of those bytes
-              const int col = FP8 ? q4 * (D / 4) + s * 4 + e * 2 : s * 16 + e * 8 + q4 * 2;
-              qf[mt][s][h + 2 * e] =
-                  in && col < p.c.d ? __ldg(reinterpret_cast<const uint32_t*>(src + col)) : 0u;
+              const uint32_t w = qf[nt][s][e];
+              qf[nt][s][e] =
+                  pack_f16x2(__uint_as_float(w << 16) * f1 * f2, __uint_as_float(w & 0xffff0000u) * f1 * f2);
             }
-          rowfac[mt][h] = p.scale_log2;
-          if (FP8) {
-            uint32_t top = 0;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t w = qf[mt][s][h + 2 * e];
-                top = max(top, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
-              }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // q * 2^up has its largest part in [2^14, 2^15)
-            const int E = static_cast<int>(top >> 7);
-            const int up = E == 0 || E == 255 ? 0 : 14 + 127 - E;
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up / 2) << 23);
-            const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
-            rowfac[mt][h] = p.scale_log2 / f1 / f2;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t w = qf[mt][s][h + 2 * e];
-                qf[mt][s][h + 2 * e] = pack_f16x2(__uint_as_float(w << 16) * f1 * f2,
-                                                  __uint_as_float(w & 0xffff0000u) * f1 * f2);
-              }
-          }
-          m[mt][h] = kNInf;
-          l[mt][h] = 0.f;
         }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c)
+        for (int e = 0; e < 2; ++e) {
+          // (row 2 * q4 + e of this eight is row n8 of lane 4 * (2 * q4 + e))
+          rowfac[nt][e] = FP8 ? __shfl_sync(0xffffffffu, fac, 4 * (2 * q4 + e)) : fac;
+          const int pe = nt * 8 + 2 * q4 + e, Re = cc.rt * ROWS + pe;
+          // (a row past the last is treated like the last: nothing is stored for it)
+          const RowKeys rk = row_keys(p, cc.s, cc.s.pos0 + (pe < rows ? Re / p.G : cc.s.nq - 1));
+          rlo[nt][e] = rk.lo;
+          rhi[nt][e] = rk.hi;
+          m[nt][e] = kNInf;
+          l[nt][e] = 0.f;
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][c][e] = 0.f;
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][c][e] = 0.f;
+      }
+      {
+        const int i0 = cc.rt * ROWS / p.G, i1 = min((cc.rt * ROWS + ROWS - 1) / p.G, cc.s.nq - 1);
+        full_hi = row_keys(p, cc.s, cc.s.pos0 + i0).hi;
+        full_lo = row_keys(p, cc.s, cc.s.pos0 + i1).lo;
       }
       ref = 0;
     }
@@ -251,116 +288,98 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
     load_next();
 
     const int j0 = cc.key0() + warp * 16;
-    if (j0 < cc.r.sink_hi || (j0 < cc.r.hi && j0 + 16 > cc.r.lo)) {
-      const int st = x % NST;
-      const uint32_t sk = ring + st * 2 * L::kHalfB, sv = sk + L::kHalfB;
-      // ---- S = Q K^T: rows n8 (+8), keys j0 + 8 * nt + 2 * q4 + {0, 1}
-      float s[MT][2][4];
+    if (some_seen(cc.r, j0)) {
+      const uint32_t sk = ring + stage * 2 * L::kHalfB, sv = sk + L::kHalfB;
+      // ---- S^T = K Q^T: keys j0 + n8 (+ 8), rows 2 * q4 + {0, 1} of each eight
+      float s[NT][4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
       if (FP8) {
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
+        for (int c = 0; c < D / 64; ++c) {
+          const uint4 wa = lds128(sk + swz<ROWB>(n8, q4 * (D / 64) + c));
+          const uint4 wb = lds128(sk + swz<ROWB>(n8 + 8, q4 * (D / 64) + c));
+          const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 w = lds128(sk + swz<ROWB>(nt * 8 + n8, q4 * (D / 64) + c));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2(aw[e]), e4m3x2_to_f16x2(bw[e]), e4m3x2_to_f16x2(aw[e] >> 16),
+                                   e4m3x2_to_f16x2(bw[e] >> 16)};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t b0 = e4m3x2_to_f16x2(ww[e]), b1 = e4m3x2_to_f16x2(ww[e] >> 16);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<true>(s[mt][nt], qf[mt][c * 4 + e], b0, b1);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[nt], a, qf[nt][c * 4 + e][0], qf[nt][c * 4 + e][1]);
           }
+        }
       } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t b[4];
-          ldsm4(b, sk + swz<ROWB>((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+          uint32_t a[4];
+          ldsm4(a, sk + swz<ROWB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<false>(s[mt][0], qf[mt][ks], b[0], b[1]);
-            mma16816<false>(s[mt][1], qf[mt][ks], b[2], b[3]);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
         }
       }
-      float kf[2][2], vf[2][2];  // scales of the lane's four keys
+      float kf[2], vf[2];  // scales of keys n8, n8 + 8
       float oscale = 1.f;
       if (FP8) {
-        const uint8_t* ex = sexp + st * 32;
+        const uint8_t* ex = sexp + stage * 32;
         const int mx = __reduce_max_sync(0xffffffffu, lane >= 16 ? static_cast<int>(ex[lane]) : 0);
         if (mx > ref) {  // the output's unit grows
           oscale = ref == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(max(127 - (mx - ref), 0)) << 23);
           ref = mx;
         }
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k = nt * 8 + q4 * 2 + e;
-            kf[nt][e] = exp_scale(ex[k]);
-            const int ve = ex[16 + k];
-            vf[nt][e] = __uint_as_float(static_cast<uint32_t>(max(127 + 15 - (ref - ve), 0)) << 23);
-          }
+        for (int e = 0; e < 2; ++e) {
+          kf[e] = exp_scale(ex[n8 + 8 * e]);
+          const int ve = ex[16 + n8 + 8 * e];
+          vf[e] = __uint_as_float(static_cast<uint32_t>(max(127 + 15 - (ref - ve), 0)) << 23);
+        }
       }
       // ---- softmax of these 16 keys
-      uint32_t pa[MT][4];
+      const bool masked = j0 < full_lo || j0 + 16 > full_hi;
+      uint32_t pb[NT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+      for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float mx = kNInf;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = j0 + nt * 8 + q4 * 2 + e;
-              float u = s[mt][nt][2 * h + e] * rowfac[mt][h];
-              if (FP8) u *= kf[nt][e];
-              if (!(j < rk[mt][h].hi && (j >= rk[mt][h].lo || j < p.sinks))) u = kNInf;
-              s[mt][nt][2 * h + e] = u;
-              mx = fmaxf(mx, u);
-            }
-          mx = fmaxf(m[mt][h], quad_max(mx));
+        for (int r = 0; r < 2; ++r) {  // row 2 * q4 + r
+          float u0 = s[nt][r] * rowfac[nt][r], u1 = s[nt][2 + r] * rowfac[nt][r];
+          if (FP8) {
+            u0 *= kf[0];
+            u1 *= kf[1];
+          }
+          if (masked) {
+            const int ja = j0 + n8, jb = ja + 8;
+            if (!(ja < rhi[nt][r] && (ja >= rlo[nt][r] || ja < p.sinks))) u0 = kNInf;
+            if (!(jb < rhi[nt][r] && (jb >= rlo[nt][r] || jb < p.sinks))) u1 = kNInf;
+          }
+          const float mx = fmaxf(m[nt][r], row_max(fmaxf(u0, u1)));
           const float base = mx == kNInf ? 0.f : mx;
-          alpha[h] = paged_ex2(m[mt][h] - base);
-          m[mt][h] = mx;
-          float sum = 0.f;
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float w = paged_ex2(s[mt][nt][2 * h + e] - base);
-              sum += w;
-              s[mt][nt][2 * h + e] = FP8 ? w * vf[nt][e] : w;
-            }
-          l[mt][h] = l[mt][h] * alpha[h] + sum;
-          alpha[h] *= oscale;
+          alpha[r] = paged_ex2(m[nt][r] - base);
+          m[nt][r] = mx;
+          const float w0 = paged_ex2(u0 - base), w1 = paged_ex2(u1 - base);
+          l[nt][r] = l[nt][r] * alpha[r] + (w0 + w1);
+          s[nt][r] = FP8 ? w0 * vf[0] : w0;
+          s[nt][2 + r] = FP8 ? w1 * vf[1] : w1;
+          alpha[r] *= oscale;
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) {
-            o[mt][c][0] *= alpha[0];
-            o[mt][c][1] *= alpha[0];
-            o[mt][c][2] *= alpha[1];
-            o[mt][c][3] *= alpha[1];
+          for (int c = 0; c < D / 16; ++c) {
+            o[nt][c][0] *= alpha[0];
+            o[nt][c][1] *= alpha[1];
+            o[nt][c][2] *= alpha[0];
+            o[nt][c][3] *= alpha[1];
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            pa[mt][nt * 2 + h] = FP8 ? pack_f16x2(s[mt][nt][2 * h], s[mt][nt][2 * h + 1])
-                                     : pack_bf16x2(s[mt][nt][2 * h], s[mt][nt][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+          pb[nt][h] = transpose8(FP8 ? pack_f16x2(s[nt][2 * h], s[nt][2 * h + 1])
+                                     : pack_bf16x2(s[nt][2 * h], s[nt][2 * h + 1]));
       }
-      // ---- O += P V
-      const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
+      // ---- O^T += V^T P^T
       if (FP8) {
+        const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
 #pragma unroll
         for (int c = 0; c < D / 16; c += 2) {
           // 16-byte chunks c and c + 1, read as pairs of columns: a register holds key 2q's and key
@@ -368,31 +387,28 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
           uint32_t w[4];
           ldsm4_t(w, sv + swz<ROWB>(vr, c + vc));
 #pragma unroll
-          for (int cc2 = 0; cc2 < 2; ++cc2)
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0020)),
+                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0031)),
+                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0020)),
+                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0031))};
 #pragma unroll
-            for (int par = 0; par < 2; ++par) {
-              const uint32_t sel = par ? 0x0031u : 0x0020u;
-              const uint32_t b0 = e4m3x2_to_f16x2(__byte_perm(w[2 * cc2], 0u, sel));
-              const uint32_t b1 = e4m3x2_to_f16x2(__byte_perm(w[2 * cc2 + 1], 0u, sel));
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mma16816<true>(o[mt][2 * (c + cc2) + par], pa[mt], b0, b1);
-            }
+            for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][c + h], a, pb[nt][0], pb[nt][1]);
+          }
         }
       } else {
 #pragma unroll
-        for (int c = 0; c < D / 8; c += 2) {
-          uint32_t b[4];
-          ldsm4_t(b, sv + swz<ROWB>(vr, c + vc));
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t a[4];
+          ldsm4_t(a, sv + swz<ROWB>((lane & 7) + (lane >> 4) * 8, 2 * c + ((lane >> 3) & 1)));
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816<false>(o[mt][c], pa[mt], b[0], b[1]);
-            mma16816<false>(o[mt][c + 1], pa[mt], b[2], b[3]);
-          }
+          for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][c], a, pb[nt][0], pb[nt][1]);
         }
       }
     }
+    stage = stage + 1 == NST ? 0 : stage + 1;
 
-    // ---- the end of the item, or of this CTA's part of it: join the eight warps
+    // ---- the end of the item, or of this CTA's part of it: join the warps
     if (cc.last_tile() || x + 1 == run) {
       const bool whole = seg0 == 0 && cc.last_tile();
       const int slot = first_seg ? 0 : 1;
@@ -401,11 +417,11 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
         p.desc[blockIdx.x] = make_int4(cc.b, cc.g, cc.rt, slot | (1 + (left + quota - 1) / quota) << 1);
       }
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float sum = quad_sum(l[mt][h]);
-          if (q4 == 0) sml[warp * ROWS + mt * 16 + h * 8 + n8] = make_float2(m[mt][h], sum);
+        for (int r = 0; r < 2; ++r) {
+          const float sum = row_sum(l[nt][r]);
+          if (n8 == 0) sml[warp * ROWS + nt * 8 + 2 * q4 + r] = make_float2(m[nt][r], sum);
         }
       // 2^(ref - 127 - 15) as two factors, both normal numbers
       const int u = ref - 142, u1 = u / 2;
@@ -413,78 +429,73 @@ __global__ void __launch_bounds__(kTokThreads, 1) paged_token_kernel(const Paged
       const float unit2 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u - u1) << 23) : 1.f;
       __syncthreads();
       const int64_t pbase = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS;
+      float f[NT][2];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float f[2];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int r = 0; r < 2; ++r) {
           float top = kNInf;
 #pragma unroll
-          for (int w = 0; w < kTokWarps; ++w) top = fmaxf(top, sml[w * ROWS + mt * 16 + h * 8 + n8].x);
-          f[h] = paged_ex2(m[mt][h] - (top == kNInf ? 0.f : top));
-          if (FP8) f[h] *= unit1;
+          for (int w = 0; w < W; ++w) top = fmaxf(top, sml[w * ROWS + nt * 8 + 2 * q4 + r].x);
+          f[nt][r] = paged_ex2(m[nt][r] - (top == kNInf ? 0.f : top)) * unit1;
         }
+      // columns of a row are exchanged by eights so that the four row pairs of a store differ in bank
+      constexpr int COLS = L::kCols, PC = COLS / 16;
 #pragma unroll
-        for (int half = 0; half < D / 64; ++half) {
-          float* mw = merge + warp * 1024;
-          if (FP8) {
-            // columns 16c + 4 * q4 + {0, 1, 2, 3} of rows n8, n8 + 8
+      for (int pass = 0; pass < D / COLS; ++pass) {
+        float* mw = merge + warp * ROWS * COLS;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float* a = o[mt][2 * (half * 4 + c)];
-                const float* b = o[mt][2 * (half * 4 + c) + 1];
-                *reinterpret_cast<float4*>(mw + (n8 + 8 * h) * 64 + ((16 * c + 4 * q4) ^ ((n8 & 1) << 4))) =
-                    make_float4(a[2 * h] * f[h] * unit2, b[2 * h] * f[h] * unit2, a[2 * h + 1] * f[h] * unit2,
-                                b[2 * h + 1] * f[h] * unit2);
-              }
-          } else {
+          for (int c = 0; c < PC; ++c) {
+            const float* v = o[nt][pass * PC + c];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<float2*>(mw + (n8 + 8 * h) * 64 + ((8 * c + 2 * q4) ^ ((n8 & 3) << 3))) =
-                    make_float2(o[mt][half * 8 + c][2 * h] * f[h], o[mt][half * 8 + c][2 * h + 1] * f[h]);
-          }
-          __syncthreads();
-          {
-            const int row = tid >> 4, col = (tid & 15) * 4;
-            const int pc = FP8 ? col ^ ((row & 1) << 4) : col ^ ((row & 3) << 3);
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-            float top = kNInf, sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kTokWarps; ++w) {
-              const float4 v = *reinterpret_cast<const float4*>(merge + w * 1024 + row * 64 + pc);
-              a.x += v.x;
-              a.y += v.y;
-              a.z += v.z;
-              a.w += v.w;
-              top = fmaxf(top, sml[w * ROWS + mt * 16 + row].x);
-            }
-#pragma unroll
-            for (int w = 0; w < kTokWarps; ++w) {
-              const float2 t = sml[w * ROWS + mt * 16 + row];
-              sum += t.y * paged_ex2(t.x - (top == kNInf ? 0.f : top));
-            }
-            const int pr = mt * 16 + row, r = cc.rt * ROWS + pr, d0 = half * 64 + col;
-            if (r < cc.s.nq * p.G) {
-              if (whole) {
-                const int i = r / p.G, h = cc.g * p.G + r - i * p.G, t = cc.s.q0 + i;
-                const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-                if (d0 < p.c.d)
-                  *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(t) * p.Hq + h) * p.c.d + d0) =
-                      make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-                if (half == 0 && (tid & 15) == 0)
-                  p.lse[static_cast<int64_t>(h) * p.T + t] = sum == 0.f ? kNInf : (top + log2f(sum)) * kPLn2;
+            for (int r = 0; r < 2; ++r) {
+              float* row = mw + (nt * 8 + 2 * q4 + r) * COLS;
+              const float fa = f[nt][r];
+              if (FP8) {
+                *reinterpret_cast<float2*>(row + ((16 * c + 2 * n8) ^ (q4 << 3 & (COLS - 1)))) =
+                    make_float2(v[r] * fa * unit2, v[2 + r] * fa * unit2);
               } else {
-                *reinterpret_cast<float4*>(p.part_o + (pbase + pr) * D + d0) = a;
-                if (half == 0 && (tid & 15) == 0) p.part_ml[pbase + pr] = make_float2(top, sum);
+                row[(16 * c + n8) ^ (q4 << 3 & (COLS - 1))] = v[r] * fa;
+                row[(16 * c + 8 + n8) ^ (q4 << 3 & (COLS - 1))] = v[2 + r] * fa;
               }
             }
           }
-          __syncthreads();
+        __syncthreads();
+        for (int e = tid; e < ROWS * (COLS / 4); e += L::kThreads) {
+          const int pr = e / (COLS / 4), col = e % (COLS / 4) * 4, pc = col ^ ((pr >> 1 & 3) << 3 & (COLS - 1));
+          const int R = cc.rt * ROWS + pr, d0 = pass * COLS + col;
+          if (R >= cc.s.nq * p.G) continue;
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          float top = kNInf, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(merge + (w * ROWS + pr) * COLS + pc);
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+            top = fmaxf(top, sml[w * ROWS + pr].x);
+          }
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float2 t = sml[w * ROWS + pr];
+            sum += t.y * paged_ex2(t.x - (top == kNInf ? 0.f : top));
+          }
+          if (whole) {
+            const int i = R / p.G, h = cc.g * p.G + R - i * p.G, t = cc.s.q0 + i;
+            const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+            if (d0 < p.c.d)
+              *reinterpret_cast<uint2*>(p.out + (static_cast<int64_t>(t) * p.Hq + h) * p.c.d + d0) =
+                  make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+            if (d0 == 0) p.lse[static_cast<int64_t>(h) * p.T + t] = sum == 0.f ? kNInf : (top + log2f(sum)) * kPLn2;
+          } else {
+            *reinterpret_cast<float4*>(p.part_o + (pbase + pr) * D + d0) = a;
+            if (d0 == 0) p.part_ml[pbase + pr] = make_float2(top, sum);
+          }
         }
+        __syncthreads();
       }
       first_seg = false;
       begin = true;
@@ -618,18 +629,27 @@ cudaError_t launch_join(void (*kern)(PagedParams), const PagedParams& p, int blo
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, bool FP8, int MT>
+template <int D, bool FP8, int NT>
 cudaError_t launch_token(const PagedParams& p, cudaStream_t stream) {
-  using L = TokSmem<D, FP8, MT>;
-  auto kern = paged_token_kernel<D, FP8, MT>;
+  using L = TokCfg<D, FP8, NT>;
+  auto kern = paged_token_kernel<D, FP8, NT>;
   static std::atomic<uint64_t> ready{0};
   cudaError_t e = set_up_once(ready, kern, L::kTotal, 0);
   if (e != cudaSuccess) return e;
-  kern<<<kPagedCtas, kTokThreads, L::kTotal, stream>>>(p);
+  kern<<<kPagedCtas, L::kThreads, L::kTotal, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
-  return launch_join(paged_join_kernel<D, 16 * MT>, p, static_cast<int>(rows < 16 * MT ? rows : 16 * MT), 256, stream);
+  return launch_join(paged_join_kernel<D, 8 * NT>, p, static_cast<int>(rows < 8 * NT ? rows : 8 * NT), 256, stream);
+}
+
+template <int D, bool FP8>
+cudaError_t launch_token_rows(const PagedParams& p, cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
+  if (rows <= 8) return launch_token<D, FP8, 1>(p, stream);
+  if (rows <= 16) return launch_token<D, FP8, 2>(p, stream);
+  if (rows <= 24) return launch_token<D, FP8, 3>(p, stream);
+  return launch_token<D, FP8, 4>(p, stream);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -639,10 +659,10 @@ struct PagedLayout {
   size_t desc, ml, o, total;
 };
 
-// Rows of an item: 16 or 32 on the token kernel, else the chunk kernel's.
+// Rows of an item: the next multiple of eight on the token kernel, else the chunk kernel's.
 int item_rows(const fdma_paged_args* a) {
   const int64_t rows = static_cast<int64_t>(a->max_q) * (a->Hq / a->cache.Hkv);
-  return rows <= 16 ? 16 : rows <= kTokenRows ? 32 : kChunkItemRows;
+  return rows <= kTokenRows ? (rows <= 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8)) : kChunkItemRows;
 }
 
 PagedLayout paged_layout(const fdma_paged_args* a) {
@@ -670,13 +690,8 @@ int validate_paged(const fdma_paged_args* a) {
 }  // namespace
 
 cudaError_t launch_paged_token(bool fp8, const PagedParams& p, cudaStream_t stream) {
-  const bool two = static_cast<int64_t>(p.max_q) * p.G > 16;
-  if (p.c.d <= 64) {
-    if (fp8) return two ? launch_token<64, true, 2>(p, stream) : launch_token<64, true, 1>(p, stream);
-    return two ? launch_token<64, false, 2>(p, stream) : launch_token<64, false, 1>(p, stream);
-  }
-  if (fp8) return two ? launch_token<128, true, 2>(p, stream) : launch_token<128, true, 1>(p, stream);
-  return two ? launch_token<128, false, 2>(p, stream) : launch_token<128, false, 1>(p, stream);
+  if (p.c.d <= 64) return fp8 ? launch_token_rows<64, true>(p, stream) : launch_token_rows<64, false>(p, stream);
+  return fp8 ? launch_token_rows<128, true>(p, stream) : launch_token_rows<128, false>(p, stream);
 }
 
 }  // namespace fdma

@@ -24,7 +24,6 @@
 
 namespace fdma {
 
-constexpr int kKeyTile = 128;
 constexpr int kPagedCtas = 152;  // one CTA per SM
 constexpr float kPLog2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
@@ -87,6 +86,7 @@ struct Span {
 };
 
 // Keys seen by the tokens [i0, i1) of a sequence (i1 > i0).
+template <int KT>
 __device__ __forceinline__ Span key_span(const PagedParams& p, const Seq& s, int i0, int i1) {
   Span r;
   const int first = max(s.pos0 + i0, 0);
@@ -98,14 +98,10 @@ __device__ __forceinline__ Span key_span(const PagedParams& p, const Seq& s, int
     r.lo = r.hi = r.sink_hi = 0;
     return r;
   }
-  r.sink_tiles = (r.sink_hi + kKeyTile - 1) / kKeyTile;
-  r.main0 = max(r.lo / kKeyTile, r.sink_tiles);
-  r.tiles = r.sink_tiles + (r.hi + kKeyTile - 1) / kKeyTile - r.main0;
+  r.sink_tiles = (r.sink_hi + KT - 1) / KT;
+  r.main0 = max(r.lo / KT, r.sink_tiles);
+  r.tiles = r.sink_tiles + (r.hi + KT - 1) / KT - r.main0;
   return r;
-}
-
-__device__ __forceinline__ int tile_key0(const Span& r, int t) {
-  return (t < r.sink_tiles ? t : r.main0 + (t - r.sink_tiles)) * kKeyTile;
 }
 
 // The keys that the row at position pos sees: j < hi and (j >= lo or j < sinks).
@@ -120,7 +116,7 @@ __device__ __forceinline__ RowKeys row_keys(const PagedParams& p, const Seq& s, 
 }
 
 // Position on the line of tiles.
-template <int ROWS>
+template <int ROWS, int KT>
 struct Cursor {
   int b, g, rt, t;
   Seq s;
@@ -129,9 +125,9 @@ struct Cursor {
   __device__ __forceinline__ int row_blocks(const PagedParams& p) const { return (s.nq * p.G + ROWS - 1) / ROWS; }
   __device__ __forceinline__ void span(const PagedParams& p) {
     const int i0 = rt * ROWS / p.G, i1 = min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq);
-    r = key_span(p, s, i0, i1);
+    r = key_span<KT>(p, s, i0, i1);
   }
-  __device__ __forceinline__ int key0() const { return tile_key0(r, t); }
+  __device__ __forceinline__ int key0() const { return (t < r.sink_tiles ? t : r.main0 + (t - r.sink_tiles)) * KT; }
   __device__ __forceinline__ bool last_tile() const { return t + 1 == r.tiles; }
   // The next tile of the line; the caller knows that there is one.
   __device__ __forceinline__ void next(const PagedParams& p) {
@@ -162,11 +158,11 @@ struct Cursor {
 };
 
 // Tiles of one sequence for one kv head.
-template <int ROWS>
+template <int ROWS, int KT>
 __device__ __forceinline__ int seq_tiles(const PagedParams& p, const Seq& s) {
   int n = 0;
   for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS)
-    n += key_span(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
+    n += key_span<KT>(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
   return n;
 }
 
@@ -178,15 +174,15 @@ struct PlanSmem {
 
 // Finds this CTA's run: every thread of the CTA calls it (NT threads).  Returns the number
 // of tiles (0: none); c stands on the first of them.  quota: the run length of all CTAs.
-template <int ROWS, int NT>
-__device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS>& c, int& quota) {
+template <int ROWS, int KT, int NT>
+__device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS, KT>& c, int& quota) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.c.B + NT - 1) / NT;
   const int b0 = min(tid * per, p.c.B), b1 = min(b0 + per, p.c.B);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = load_seq(p, b, blockIdx.x == 0);
-    mine += static_cast<int64_t>(seq_tiles<ROWS>(p, s)) * p.c.Hkv;
+    mine += static_cast<int64_t>(seq_tiles<ROWS, KT>(p, s)) * p.c.Hkv;
   }
   int64_t x = mine;
 #pragma unroll
@@ -208,7 +204,7 @@ __device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Curs
     int64_t left = start - before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b, false);
-      const int n = seq_tiles<ROWS>(p, s);
+      const int n = seq_tiles<ROWS, KT>(p, s);
       if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
         left -= static_cast<int64_t>(n) * p.c.Hkv;
         continue;
@@ -217,7 +213,7 @@ __device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Curs
       sm->g = static_cast<int>(left / n);
       int t = static_cast<int>(left % n), rt = 0;
       for (;; ++rt) {
-        const int k = key_span(p, s, rt * ROWS / p.G, min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq)).tiles;
+        const int k = key_span<KT>(p, s, rt * ROWS / p.G, min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq)).tiles;
         if (t < k) break;
         t -= k;
       }
@@ -245,7 +241,7 @@ __device__ __forceinline__ void write_empty_blocks(const PagedParams& p) {
     const Seq s = load_seq(p, b, false);
     for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS) {
       const int i0 = r0 / p.G, i1 = min((r0 + ROWS - 1) / p.G + 1, s.nq);
-      if (key_span(p, s, i0, i1).tiles > 0) continue;
+      if (key_span<128>(p, s, i0, i1).tiles > 0) continue;
       const int r1 = min(r0 + ROWS, s.nq * p.G), nr = (r1 - r0) * p.c.Hkv, vec = p.c.d >> 3;
       for (int e = threadIdx.x; e < nr * vec; e += blockDim.x) {
         const int x = e / vec, r = r0 + x % (r1 - r0), h = x / (r1 - r0) * p.G + r % p.G, t = s.q0 + r / p.G;

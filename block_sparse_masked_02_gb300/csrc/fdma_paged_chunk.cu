@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kChunkThreads = 512;
+constexpr int kKeyTile = 128;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
 constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
@@ -124,9 +125,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (tid == 0) atomicCAS(p.err, 0, kDevErrAlign);
     return;
   }
-  Cursor<ROWS> c;
+  Cursor<ROWS, kKeyTile> c;
   int quota;
-  const int run = plan_run<ROWS, kChunkThreads>(p, plan, c, quota);
+  const int run = plan_run<ROWS, kKeyTile, kChunkThreads>(p, plan, c, quota);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   write_empty_blocks<ROWS>(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
