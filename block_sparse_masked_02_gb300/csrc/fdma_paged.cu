@@ -4,7 +4,7 @@
 // An item is a kv head's query rows of one sequence, at most 8 * NT of them.  Every key and
 // value is read from HBM once and takes part in 4 * d flops a row, so with few rows the kernel
 // is bound by memory, and its work is to keep enough loads in flight with few instructions:
-// each warp of the one CTA on an SM runs its own ring of cp.async stages of 16 keys' K and V
+// each warp of the one CTA on an SM runs its own ring of cp.async stages of 16 or 32 keys' K and V
 // rows (192 KB on an SM at d = 128), with no barrier between warps inside the loop, and the
 // ring runs on across items, so that a batch of short sequences streams like one long one.
 // page_size is a multiple of 16, so a warp's keys lie in one page.
@@ -23,7 +23,8 @@
 // 2^-38 of the row's largest.  The key's scale multiplies S; the value's scale multiplies P,
 // as 2^(e - r + 15) with r the largest e so far (the output is kept in units of 2^(r - 15)), so
 // that P stays in f16's range and a weight keeps all 11 bits down to 2^-29 of the largest.
-// Half the bytes a key and the conversions on top leave less time for latency: 16 warps.
+// A key is half the bytes and has the conversions on top, so a warp takes 32 keys a step: two
+// independent chains of products and half the bookkeeping a key.
 #include <cmath>
 
 #include "fdma_paged.cuh"
@@ -32,7 +33,7 @@ namespace fdma {
 
 namespace {
 
-constexpr int kTokenRows = 32;  // packed rows up to which the token kernel runs
+constexpr int kTokenRows = 24;  // packed rows up to which the token kernel runs
 constexpr float kNInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -91,21 +92,23 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // D: 64 or 128, the head dim's padded width (columns past d are read as zeros); NT: eights of rows.
 template <int D, bool FP8, int NT>
 struct TokCfg {
-  static constexpr int kWarps = FP8 && NT == 1 ? 16 : 8;
+  static constexpr int kWarps = 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kKeys = kWarps * 16;         // keys of a tile
+  static constexpr int kGroups = FP8 ? 2 : 1;       // 16-key groups of a warp's step
+  static constexpr int kStep = 16 * kGroups;        // keys of a warp's step
+  static constexpr int kKeys = kWarps * kStep;      // keys of a tile
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowB = FP8 ? D : 2 * D;     // bytes of a row in shared memory
-  static constexpr int kHalfB = 16 * kRowB;         // 16 keys of K (or V)
-  static constexpr int kStages = kRowB == 256 ? 3 : kWarps == 16 ? 3 : FP8 ? 5 : 6;
+  static constexpr int kHalfB = kStep * kRowB;      // a step's K (or V)
+  static constexpr int kStages = kHalfB == 4096 ? 3 : 5;
   static constexpr int kWarpB = kStages * 2 * kHalfB;
   // columns joined at a time: [kWarps][kRows][kCols] fp32 within 32 KB
   static constexpr int kFit = 32768 / (kWarps * kRows * 4);
   static constexpr int kCols = kFit >= D ? D : kFit >= 64 ? 64 : 32;
   static constexpr int kOffMerge = kWarps * kWarpB;
   static constexpr int kOffMl = kOffMerge + kWarps * kRows * kCols * 4;  // [kWarps][kRows] (maximum, sum)
-  static constexpr int kOffExp = kOffMl + kWarps * kRows * 8;            // [kWarps][kStages][32] scale bytes (e4m3)
-  static constexpr int kOffPlan = kOffExp + (FP8 ? kWarps * kStages * 32 : 0);
+  static constexpr int kOffExp = kOffMl + kWarps * kRows * 8;            // [kWarps][kStages][2][kStep] scale bytes (e4m3)
+  static constexpr int kOffPlan = kOffExp + (FP8 ? kWarps * kStages * 2 * kStep : 0);
   static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
@@ -121,7 +124,7 @@ template <int D, bool FP8, int NT>
 __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
     paged_token_kernel(const __grid_constant__ PagedParams p) {
   using L = TokCfg<D, FP8, NT>;
-  constexpr int ROWS = L::kRows, NST = L::kStages, ROWB = L::kRowB, W = L::kWarps;
+  constexpr int ROWS = L::kRows, NST = L::kStages, ROWB = L::kRowB, W = L::kWarps, KG = L::kGroups, STEP = L::kStep;
   constexpr int CPR = ROWB / 16;  // 16-byte chunks of a row
   constexpr int RPP = 32 / CPR;   // rows that a warp copies at a time
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   PlanSmem* plan = reinterpret_cast<PlanSmem*>(smem + L::kOffPlan);
   float* merge = reinterpret_cast<float*>(smem + L::kOffMerge);
   float2* sml = reinterpret_cast<float2*>(smem + L::kOffMl);
-  uint8_t* sexp = smem + L::kOffExp + warp * NST * 32;
+  uint8_t* sexp = smem + L::kOffExp + warp * NST * 2 * STEP;
   const uint32_t ring = smem_u32(smem) + warp * L::kWarpB;
 
   Cursor<ROWS, L::kKeys> lc;  // the tile that is loaded next
@@ -141,61 +144,78 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   if (run == 0) return;
   Cursor<ROWS, L::kKeys> cc = lc;  // the tile that is computed next
 
-  // ---- loads: stage (x mod NST) of this warp's ring takes its 16 keys of tile x
+  // ---- loads: stage (x mod NST) of this warp's ring takes its step's keys of tile x
   const int chunk = lane % CPR, crow = lane / CPR;
   const uint32_t cbytes = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
   const int pmask = (1 << p.c.page_shift) - 1;
-  uint32_t exp_pend = 127;
-  auto some_seen = [&](const Span& r, int j0) { return j0 < r.sink_hi || (j0 < r.hi && j0 + 16 > r.lo); };
-  // a warp's keys are looked up only where some row sees one of them
-  auto page_of = [&]() {
-    const int j0 = lc.key0() + warp * 16;
-    return some_seen(lc.r, j0) ? key_page(p, lc.b, j0) : -1;
-  };
-  int lpage = page_of(), lstage = 0, loaded = 0;
-  auto load_next = [&]() {
-    if (FP8 && loaded > 0 && loaded <= run) sexp[(lstage == 0 ? NST - 1 : lstage - 1) * 32 + lane] = static_cast<uint8_t>(exp_pend);
-    if (loaded < run) {
-      const uint32_t dst = ring + lstage * 2 * L::kHalfB;
-      const int j0 = lc.key0() + warp * 16;
-      const int64_t pg = lpage;
-      const uint8_t* kb = p.c.k + pg * p.c.ks[0] + ((j0 & pmask) + crow) * p.c.ks[1] + lc.g * p.c.ks[2] + chunk * 16;
-      const uint8_t* vb = p.c.v + pg * p.c.vs[0] + ((j0 & pmask) + crow) * p.c.vs[1] + lc.g * p.c.vs[2] + chunk * 16;
-      if (lpage >= 0 && j0 >= lc.r.lo && j0 + 16 <= lc.r.hi) {  // all 16 keys
+  uint32_t exp_pend[2] = {127, 127};
+  auto some_seen = [&](const Span& r, int j0, int n) { return j0 < r.sink_hi || (j0 < r.hi && j0 + n > r.lo); };
+  // a group's page is looked up (a step ahead) only where some row sees one of its keys
+  int lentry[KG];
+  auto look_up = [&]() {
 #pragma unroll
-        for (int i = 0; i < 16 / RPP; ++i) {
-          cp_async16(dst + swz<ROWB>(i * RPP + crow, chunk), kb, cbytes);
-          cp_async16(dst + L::kHalfB + swz<ROWB>(i * RPP + crow, chunk), vb, cbytes);
-          kb += RPP * p.c.ks[1];
-          vb += RPP * p.c.vs[1];
-        }
-      } else if (lpage >= 0) {
+    for (int g = 0; g < KG; ++g) {
+      const int j0 = lc.key0() + warp * STEP + g * 16;
+      lentry[g] = some_seen(lc.r, j0, 16) ? table_entry(p, lc.b, j0) : kNoKeys;
+    }
+  };
+  look_up();
+  int lstage = 0, loaded = 0;
+  auto load_next = [&]() {
+    if (FP8 && loaded > 0 && loaded <= run) {
+      uint8_t* e = sexp + (lstage == 0 ? NST - 1 : lstage - 1) * 2 * STEP;
+      e[lane] = static_cast<uint8_t>(exp_pend[0]);
+      e[STEP + lane] = static_cast<uint8_t>(exp_pend[1]);
+    }
+    if (loaded < run) {
+      const int js = lc.key0() + warp * STEP;
+      int pgs[KG];
+#pragma unroll
+      for (int g = 0; g < KG; ++g) pgs[g] = checked_page(p, lentry[g]);
+      if (some_seen(lc.r, js, STEP)) {
+#pragma unroll
+        for (int g = 0; g < KG; ++g) {
+          const int j0 = js + g * 16;
+          const int64_t pg = pgs[g];
+          const uint32_t dst = ring + lstage * 2 * L::kHalfB;
+          const uint8_t* kb = p.c.k + pg * p.c.ks[0] + ((j0 & pmask) + crow) * p.c.ks[1] + lc.g * p.c.ks[2] + chunk * 16;
+          const uint8_t* vb = p.c.v + pg * p.c.vs[0] + ((j0 & pmask) + crow) * p.c.vs[1] + lc.g * p.c.vs[2] + chunk * 16;
+          if (pg >= 0 && j0 >= lc.r.lo && j0 + 16 <= lc.r.hi) {  // all 16 keys
+#pragma unroll
+            for (int i = 0; i < 16 / RPP; ++i) {
+              const uint32_t at = swz<ROWB>(g * 16 + i * RPP + crow, chunk);
+              cp_async16(dst + at, kb, cbytes);
+              cp_async16(dst + L::kHalfB + at, vb, cbytes);
+              kb += RPP * p.c.ks[1];
+              vb += RPP * p.c.vs[1];
+            }
+          } else {  // some, or none (zeros)
 #pragma unroll 1
-        for (int i = 0; i < 16 / RPP; ++i) {
-          const int r = i * RPP + crow, j = j0 + r;
-          const bool ok = j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi);
-          cp_async16(dst + swz<ROWB>(r, chunk), ok ? kb : p.c.k, ok ? cbytes : 0u);
-          cp_async16(dst + L::kHalfB + swz<ROWB>(r, chunk), ok ? vb : p.c.v, ok ? cbytes : 0u);
-          kb += RPP * p.c.ks[1];
-          vb += RPP * p.c.vs[1];
+            for (int i = 0; i < 16 / RPP; ++i) {
+              const int j = j0 + i * RPP + crow;
+              const uint32_t at = swz<ROWB>(g * 16 + i * RPP + crow, chunk);
+              const bool ok = pg >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi));
+              cp_async16(dst + at, ok ? kb : p.c.k, ok ? cbytes : 0u);
+              cp_async16(dst + L::kHalfB + at, ok ? vb : p.c.v, ok ? cbytes : 0u);
+              kb += RPP * p.c.ks[1];
+              vb += RPP * p.c.vs[1];
+            }
+          }
         }
-      } else if (some_seen(lc.r, j0)) {  // no page: keys of zeros
-#pragma unroll 1
-        for (int i = 0; i < 2 * L::kHalfB / 512; ++i)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * 512 + lane * 16), "r"(0) : "memory");
       }
-      if (FP8) {
-        const int r = lane & 15, j = j0 + r;
-        exp_pend = 0;
-        if (lpage >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi))) {
-          const int64_t* es = lane < 16 ? p.c.kes : p.c.ves;
-          exp_pend = (lane < 16 ? p.c.ke : p.c.ve)[pg * es[0] + (j & pmask) * es[1] + lc.g * es[2]];
+      if (FP8) {  // (a step has a lane for each of its keys)
+        const int j = js + lane;
+        const int64_t pg = lane < 16 ? pgs[0] : pgs[KG - 1];
+        exp_pend[0] = exp_pend[1] = 0;
+        if (pg >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi))) {
+          exp_pend[0] = p.c.ke[pg * p.c.kes[0] + (j & pmask) * p.c.kes[1] + lc.g * p.c.kes[2]];
+          exp_pend[1] = p.c.ve[pg * p.c.ves[0] + (j & pmask) * p.c.ves[1] + lc.g * p.c.ves[2]];
         }
       }
       lstage = lstage + 1 == NST ? 0 : lstage + 1;
       if (loaded + 1 < run) {
         lc.next(p);
-        lpage = page_of();
+        look_up();
       }
     }
     ++loaded;
@@ -287,80 +307,98 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
     __syncwarp();
     load_next();
 
-    const int j0 = cc.key0() + warp * 16;
-    if (some_seen(cc.r, j0)) {
+    const int j0 = cc.key0() + warp * STEP;
+    if (some_seen(cc.r, j0, STEP)) {
       const uint32_t sk = ring + stage * 2 * L::kHalfB, sv = sk + L::kHalfB;
-      // ---- S^T = K Q^T: keys j0 + n8 (+ 8), rows 2 * q4 + {0, 1} of each eight
-      float s[NT][4];
+      // ---- S^T = K Q^T: keys j0 + 16 * g + n8 (+ 8), rows 2 * q4 + {0, 1} of each eight
+      float s[KG][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int g = 0; g < KG; ++g)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[g][nt][e] = 0.f;
       if (FP8) {
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          const uint4 wa = lds128(sk + swz<ROWB>(n8, q4 * (D / 64) + c));
-          const uint4 wb = lds128(sk + swz<ROWB>(n8 + 8, q4 * (D / 64) + c));
-          const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
+        for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(aw[e]), e4m3x2_to_f16x2(bw[e]), e4m3x2_to_f16x2(aw[e] >> 16),
-                                   e4m3x2_to_f16x2(bw[e] >> 16)};
+          for (int g = 0; g < KG; ++g) {
+            const uint4 wa = lds128(sk + swz<ROWB>(g * 16 + n8, q4 * (D / 64) + c));
+            const uint4 wb = lds128(sk + swz<ROWB>(g * 16 + n8 + 8, q4 * (D / 64) + c));
+            const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[nt], a, qf[nt][c * 4 + e][0], qf[nt][c * 4 + e][1]);
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t a[4] = {e4m3x2_to_f16x2(aw[e]), e4m3x2_to_f16x2(bw[e]), e4m3x2_to_f16x2(aw[e] >> 16),
+                                     e4m3x2_to_f16x2(bw[e] >> 16)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[g][nt], a, qf[nt][c * 4 + e][0], qf[nt][c * 4 + e][1]);
+            }
           }
-        }
       } else {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          uint32_t a[4];
-          ldsm4(a, sk + swz<ROWB>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
+        for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[nt], a, qf[nt][ks][0], qf[nt][ks][1]);
-        }
+          for (int g = 0; g < KG; ++g) {
+            uint32_t a[4];
+            ldsm4(a, sk + swz<ROWB>(g * 16 + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * ks + (lane >> 4)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[g][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
+          }
       }
-      float kf[2], vf[2];  // scales of keys n8, n8 + 8
+      float kf[KG][2], vf[KG][2];  // scales of keys n8, n8 + 8 of each group
       float oscale = 1.f;
       if (FP8) {
-        const uint8_t* ex = sexp + stage * 32;
-        const int mx = __reduce_max_sync(0xffffffffu, lane >= 16 ? static_cast<int>(ex[lane]) : 0);
+        const uint8_t* ex = sexp + stage * 2 * STEP;
+        const int mx = __reduce_max_sync(0xffffffffu, static_cast<int>(ex[STEP + lane]));
         if (mx > ref) {  // the output's unit grows
           oscale = ref == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(max(127 - (mx - ref), 0)) << 23);
           ref = mx;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          kf[e] = exp_scale(ex[n8 + 8 * e]);
-          const int ve = ex[16 + n8 + 8 * e];
-          vf[e] = __uint_as_float(static_cast<uint32_t>(max(127 + 15 - (ref - ve), 0)) << 23);
-        }
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            kf[g][e] = exp_scale(ex[g * 16 + n8 + 8 * e]);
+            const int ve = ex[STEP + g * 16 + n8 + 8 * e];
+            vf[g][e] = __uint_as_float(static_cast<uint32_t>(max(127 + 15 - (ref - ve), 0)) << 23);
+          }
       }
-      // ---- softmax of these 16 keys
-      const bool masked = j0 < full_lo || j0 + 16 > full_hi;
-      uint32_t pb[NT][2];
+      // ---- softmax of these keys
+      const bool masked = j0 < full_lo || j0 + STEP > full_hi;
+      uint32_t pb[KG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // row 2 * q4 + r
-          float u0 = s[nt][r] * rowfac[nt][r], u1 = s[nt][2 + r] * rowfac[nt][r];
-          if (FP8) {
-            u0 *= kf[0];
-            u1 *= kf[1];
-          }
-          if (masked) {
-            const int ja = j0 + n8, jb = ja + 8;
-            if (!(ja < rhi[nt][r] && (ja >= rlo[nt][r] || ja < p.sinks))) u0 = kNInf;
-            if (!(jb < rhi[nt][r] && (jb >= rlo[nt][r] || jb < p.sinks))) u1 = kNInf;
-          }
-          const float mx = fmaxf(m[nt][r], row_max(fmaxf(u0, u1)));
+          float mx = kNInf;
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float u = s[g][nt][2 * e + r] * rowfac[nt][r];
+              if (FP8) u *= kf[g][e];
+              if (masked) {
+                const int j = j0 + g * 16 + n8 + 8 * e;
+                if (!(j < rhi[nt][r] && (j >= rlo[nt][r] || j < p.sinks))) u = kNInf;
+              }
+              s[g][nt][2 * e + r] = u;
+              mx = fmaxf(mx, u);
+            }
+          mx = fmaxf(m[nt][r], row_max(mx));
           const float base = mx == kNInf ? 0.f : mx;
           alpha[r] = paged_ex2(m[nt][r] - base);
           m[nt][r] = mx;
-          const float w0 = paged_ex2(u0 - base), w1 = paged_ex2(u1 - base);
-          l[nt][r] = l[nt][r] * alpha[r] + (w0 + w1);
-          s[nt][r] = FP8 ? w0 * vf[0] : w0;
-          s[nt][2 + r] = FP8 ? w1 * vf[1] : w1;
+          float sum = 0.f;
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float w = paged_ex2(s[g][nt][2 * e + r] - base);
+              sum += w;
+              s[g][nt][2 * e + r] = FP8 ? w * vf[g][e] : w;
+            }
+          l[nt][r] = l[nt][r] * alpha[r] + sum;
           alpha[r] *= oscale;
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
@@ -373,37 +411,43 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          pb[nt][h] = transpose8(FP8 ? pack_f16x2(s[nt][2 * h], s[nt][2 * h + 1])
-                                     : pack_bf16x2(s[nt][2 * h], s[nt][2 * h + 1]));
+        for (int g = 0; g < KG; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            pb[g][nt][h] = transpose8(FP8 ? pack_f16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1])
+                                          : pack_bf16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1]));
       }
       // ---- O^T += V^T P^T
       if (FP8) {
         const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
 #pragma unroll
-        for (int c = 0; c < D / 16; c += 2) {
-          // 16-byte chunks c and c + 1, read as pairs of columns: a register holds key 2q's and key
-          // 2q + 1's codes of columns 2 * n8 and 2 * n8 + 1
-          uint32_t w[4];
-          ldsm4_t(w, sv + swz<ROWB>(vr, c + vc));
+        for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0020)),
-                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0031)),
-                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0020)),
-                                   e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0031))};
+          for (int g = 0; g < KG; ++g) {
+            // 16-byte chunks c and c + 1, read as pairs of columns: a register holds key 2q's and key
+            // 2q + 1's codes of columns 2 * n8 and 2 * n8 + 1
+            uint32_t w[4];
+            ldsm4_t(w, sv + swz<ROWB>(g * 16 + vr, c + vc));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][c + h], a, pb[nt][0], pb[nt][1]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t a[4] = {e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0020)),
+                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0031)),
+                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0020)),
+                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0031))};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][c + h], a, pb[g][nt][0], pb[g][nt][1]);
+            }
           }
-        }
       } else {
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t a[4];
-          ldsm4_t(a, sv + swz<ROWB>((lane & 7) + (lane >> 4) * 8, 2 * c + ((lane >> 3) & 1)));
+        for (int c = 0; c < D / 16; ++c)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][c], a, pb[nt][0], pb[nt][1]);
-        }
+          for (int g = 0; g < KG; ++g) {
+            uint32_t a[4];
+            ldsm4_t(a, sv + swz<ROWB>(g * 16 + (lane & 7) + (lane >> 4) * 8, 2 * c + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816<false>(o[nt][c], a, pb[g][nt][0], pb[g][nt][1]);
+          }
       }
     }
     stage = stage + 1 == NST ? 0 : stage + 1;
@@ -648,8 +692,7 @@ cudaError_t launch_token_rows(const PagedParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
   if (rows <= 8) return launch_token<D, FP8, 1>(p, stream);
   if (rows <= 16) return launch_token<D, FP8, 2>(p, stream);
-  if (rows <= 24) return launch_token<D, FP8, 3>(p, stream);
-  return launch_token<D, FP8, 4>(p, stream);
+  return launch_token<D, FP8, 3>(p, stream);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

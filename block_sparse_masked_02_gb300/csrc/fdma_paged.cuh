@@ -253,14 +253,17 @@ __device__ __forceinline__ void write_empty_blocks(const PagedParams& p) {
   }
 }
 
-// Page of key j, or -1 where the table names none (reported).
-__device__ __forceinline__ int key_page(const PagedParams& p, int b, int j) {
-  const int pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (j >> p.c.page_shift)];
-  if (pg < 0 || pg >= p.c.num_pages) {
-    atomicCAS(p.err, 0, FDMA_ERR_INVALID);
-    return -1;
-  }
-  return pg;
+// The table's entry for key j: looked up a step ahead of its use, so nothing may depend on it yet.
+__device__ __forceinline__ int table_entry(const PagedParams& p, int b, int j) {
+  return p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (j >> p.c.page_shift)];
+}
+constexpr int kNoKeys = -0x7fffffff - 1;  // in place of an entry that is not needed
+
+// The page that an entry names, or -1 where it names none (reported) or is not needed.
+__device__ __forceinline__ int checked_page(const PagedParams& p, int entry) {
+  if (entry >= 0 && entry < p.c.num_pages) return entry;
+  if (entry != kNoKeys) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
+  return -1;
 }
 
 __device__ __forceinline__ float paged_ex2(float x) {

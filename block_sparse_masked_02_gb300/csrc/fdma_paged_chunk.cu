@@ -195,12 +195,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; -1: no row sees a key of the group.
       auto look_up = [&](int k) {
-        int pg = -1;
+        int entry = kNoKeys;
         if (lane < 8 && k < n) {
           const int j = part_key0(s, s.t0 + k) + lane * 16;
-          if (j < sink_hi || (j < hi && j + 16 > lo)) pg = key_page(p, b, j);
+          if (j < sink_hi || (j < hi && j + 16 > lo)) entry = table_entry(p, b, j);
         }
-        return pg;
+        return entry;
       };
       int pg = -1, pg_next = look_up(0);
       // (one turn without loads at the end of the run, for the last raw item)
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool is_v = i2 & 1;
           const int j0 = part_key0(s, s.t0 + (i2 >> 1));
           if (!is_v) {
-            pg = pg_next;
+            pg = checked_page(p, pg_next);
             pg_next = look_up((i2 >> 1) + 1);
           }
           const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
