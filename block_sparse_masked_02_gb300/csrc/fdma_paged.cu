@@ -137,11 +137,11 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
 
   Cursor<ROWS, L::kKeys> lc;  // the tile that is loaded next
   int quota;
-  const int run = plan_run<ROWS, L::kKeys, L::kThreads>(p, plan, lc, quota);
+  const bool any = plan_run<ROWS, L::kKeys, L::kThreads>(p, plan, lc, quota);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   write_empty_blocks<ROWS>(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be set up; it waits for the end
-  if (run == 0) return;
+  if (!any) return;
   Cursor<ROWS, L::kKeys> cc = lc;  // the tile that is computed next
 
   // ---- loads: stage (x mod NST) of this warp's ring takes its step's keys of tile x
@@ -160,14 +160,16 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
     }
   };
   look_up();
-  int lstage = 0, loaded = 0;
+  int lstage = 0;
+  bool more = true, pending = false;  // tiles to load; scale bytes still in registers
   auto load_next = [&]() {
-    if (FP8 && loaded > 0 && loaded <= run) {
+    if (FP8 && pending) {
       uint8_t* e = sexp + (lstage == 0 ? NST - 1 : lstage - 1) * 2 * STEP;
       e[lane] = static_cast<uint8_t>(exp_pend[0]);
       e[STEP + lane] = static_cast<uint8_t>(exp_pend[1]);
     }
-    if (loaded < run) {
+    pending = more;
+    if (more) {
       const int js = lc.key0() + warp * STEP;
       int pgs[KG];
 #pragma unroll
@@ -213,16 +215,15 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         }
       }
       lstage = lstage + 1 == NST ? 0 : lstage + 1;
-      if (loaded + 1 < run) {
+      lc.left = lc.left_after(1);
+      more = lc.left > 0;
+      if (more) {
         lc.next(p);
         look_up();
       }
     }
-    ++loaded;
     cp_async_commit();
   };
-#pragma unroll 1
-  for (int i = 0; i < NST - 1; ++i) load_next();
 
   uint32_t qf[NT][D / 16][2];  // Q^T as B operands: rows n8 of each eight
   float rowfac[NT][2];         // log2(e) * scale (and the row's power of two) of rows 2 * q4 + {0, 1}
@@ -235,8 +236,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   int stage = 0;
   bool first_seg = true, begin = true;
 
+  // (the first NST - 1 turns only load: the item's query rows come in at the same time)
 #pragma unroll 1
-  for (int x = 0; x < run; ++x) {
+  for (int x = 1 - NST;; ++x) {
     if (begin) {
       // ---- a new item: its query rows, and an empty softmax
       begin = false;
@@ -303,9 +305,10 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
       }
       ref = 0;
     }
-    cp_async_wait<NST - 2>();
+    if (x >= 0) cp_async_wait<NST - 2>();
     __syncwarp();
     load_next();
+    if (x < 0) continue;
 
     const int j0 = cc.key0() + warp * STEP;
     if (some_seen(cc.r, j0, STEP)) {
@@ -453,7 +456,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
     stage = stage + 1 == NST ? 0 : stage + 1;
 
     // ---- the end of the item, or of this CTA's part of it: join the warps
-    if (cc.last_tile() || x + 1 == run) {
+    cc.left = cc.left_after(1);
+    const bool done = cc.left <= 0;
+    if (cc.last_tile() || done) {
       const bool whole = seg0 == 0 && cc.last_tile();
       const int slot = first_seg ? 0 : 1;
       if (tid == 0 && seg0 == 0 && !whole) {
@@ -544,7 +549,8 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
       first_seg = false;
       begin = true;
     }
-    if (x + 1 < run) cc.next(p);
+    if (done) break;
+    cc.next(p);
   }
 }
 

@@ -28,6 +28,8 @@ constexpr int kPagedCtas = 152;  // one CTA per SM
 constexpr float kPLog2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
 
+constexpr int kItemCost = 2;
+
 struct CacheView {
   const uint8_t* k;  // strides in bytes: page, token, head
   const uint8_t* v;
@@ -55,7 +57,7 @@ struct PagedParams {
   float2* part_ml;  // [cta][2][ROWS]: running maximum (log2 units) and weight sum
   int4* desc;     // [cta]: the split item that begins in this CTA: (sequence, kv head, row block, slot | pieces << 1)
   int* err;
-  int min_run;  // least tiles of a run
+  int min_run;  // least length of a run
   int box;      // chunk kernel: rows of a TMA box of the cache (0: no TMA)
 };
 
@@ -119,17 +121,19 @@ __device__ __forceinline__ RowKeys row_keys(const PagedParams& p, const Seq& s, 
 template <int ROWS, int KT>
 struct Cursor {
   int b, g, rt, t;
+  int left;  // places of the run from this tile on
   Seq s;
   Span r;
 
-  __device__ __forceinline__ int row_blocks(const PagedParams& p) const { return (s.nq * p.G + ROWS - 1) / ROWS; }
   __device__ __forceinline__ void span(const PagedParams& p) {
     const int i0 = rt * ROWS / p.G, i1 = min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq);
     r = key_span<KT>(p, s, i0, i1);
   }
   __device__ __forceinline__ int key0() const { return (t < r.sink_tiles ? t : r.main0 + (t - r.sink_tiles)) * KT; }
   __device__ __forceinline__ bool last_tile() const { return t + 1 == r.tiles; }
-  // The next tile of the line; the caller knows that there is one.
+  // Places of the run that are left when the current tile is done (the tiles t .. t + n - 1 of the item).
+  __device__ __forceinline__ int left_after(int n) const { return left - n - (t + n == r.tiles ? kItemCost : 0); }
+  // The next tile of the line; the caller knows that the run goes on.
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (++t < r.tiles) return;
     t = 0;
@@ -157,12 +161,14 @@ struct Cursor {
   }
 };
 
-// Tiles of one sequence for one kv head.
+// Places of one sequence's items of one kv head.
 template <int ROWS, int KT>
-__device__ __forceinline__ int seq_tiles(const PagedParams& p, const Seq& s) {
+__device__ __forceinline__ int seq_places(const PagedParams& p, const Seq& s) {
   int n = 0;
-  for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS)
-    n += key_span<KT>(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
+  for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS) {
+    const int k = key_span<KT>(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
+    if (k > 0) n += k + kItemCost;
+  }
   return n;
 }
 
@@ -172,17 +178,17 @@ struct PlanSmem {
   int b, g, rt, t;
 };
 
-// Finds this CTA's run: every thread of the CTA calls it (NT threads).  Returns the number
-// of tiles (0: none); c stands on the first of them.  quota: the run length of all CTAs.
+// Finds this CTA's run: every thread of the CTA calls it (NT threads).  False where it has no
+// tiles; else c stands on the first of them.  quota: the run length of all CTAs.
 template <int ROWS, int KT, int NT>
-__device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS, KT>& c, int& quota) {
+__device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS, KT>& c, int& quota) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.c.B + NT - 1) / NT;
   const int b0 = min(tid * per, p.c.B), b1 = min(b0 + per, p.c.B);
   int64_t mine = 0;
   for (int b = b0; b < b1; ++b) {
     const Seq s = load_seq(p, b, blockIdx.x == 0);
-    mine += static_cast<int64_t>(seq_tiles<ROWS, KT>(p, s)) * p.c.Hkv;
+    mine += static_cast<int64_t>(seq_places<ROWS, KT>(p, s)) * p.c.Hkv;
   }
   int64_t x = mine;
 #pragma unroll
@@ -204,7 +210,7 @@ __device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Curs
     int64_t left = start - before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b, false);
-      const int n = seq_tiles<ROWS, KT>(p, s);
+      const int n = seq_places<ROWS, KT>(p, s);
       if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
         left -= static_cast<int64_t>(n) * p.c.Hkv;
         continue;
@@ -214,8 +220,9 @@ __device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Curs
       int t = static_cast<int>(left % n), rt = 0;
       for (;; ++rt) {
         const int k = key_span<KT>(p, s, rt * ROWS / p.G, min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq)).tiles;
-        if (t < k) break;
-        t -= k;
+        if (k == 0) continue;
+        if (t < k + kItemCost) break;
+        t -= k + kItemCost;
       }
       sm->rt = rt;
       sm->t = t;
@@ -223,14 +230,21 @@ __device__ __forceinline__ int plan_run(const PagedParams& p, PlanSmem* sm, Curs
     }
   }
   __syncthreads();
-  if (start >= total) return 0;
+  if (start >= total) return false;
   c.b = sm->b;
   c.g = sm->g;
   c.rt = sm->rt;
   c.t = sm->t;
   c.s = load_seq(p, c.b, false);
   c.span(p);
-  return static_cast<int>(min(static_cast<int64_t>(quota), total - start));
+  c.left = static_cast<int>(min(static_cast<int64_t>(quota), total - start));
+  if (c.t >= c.r.tiles) {  // between two items: the run's tiles begin with the next
+    c.left -= c.r.tiles + kItemCost - c.t;
+    c.t = c.r.tiles - 1;
+    if (c.left <= 0) return false;
+    c.next(p);
+  }
+  return true;
 }
 
 // Rows that see no key at all because their row block has no tiles: out = 0, lse = -inf.

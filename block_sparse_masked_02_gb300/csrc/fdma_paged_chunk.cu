@@ -127,11 +127,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   Cursor<ROWS, kKeyTile> c;
   int quota;
-  const int run = plan_run<ROWS, kKeyTile, kChunkThreads>(p, plan, c, quota);
+  const bool any = plan_run<ROWS, kKeyTile, kChunkThreads>(p, plan, c, quota);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   write_empty_blocks<ROWS>(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (run == 0) return;
+  if (!any) return;
 
   if (tid == 0) {
     for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
@@ -439,10 +439,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------------- walk
-      for (int left = run, idx = 0;; ++idx) {
+      for (int left = c.left, idx = 0;; ++idx) {
         if (idx >= kParts && !wait(cPartFree + idx % kParts, (idx / kParts - 1) & 1)) break;
         Part& s = parts[idx % kParts];
-        s.n = min(c.r.tiles - c.t, left);
+        s.n = max(min(c.r.tiles - c.t, left), 0);
         if (left > 0) {
           s.whole = s.n == c.r.tiles;
           s.slot = idx == 0 ? 0 : 1;
@@ -462,12 +462,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           s.klen = c.s.klen;
         }
         mbar_arrive(&bars[cPart + idx % kParts]);
-        if (left == 0) break;
+        if (left <= 0) break;
         if (c.t == 0 && !s.whole)
           p.desc[blockIdx.x] =
               make_int4(c.b, c.g, c.rt, s.slot | (1 + (c.r.tiles - s.n + quota - 1) / quota) << 1);
         const int n = s.n;
-        left -= n;
+        left -= n + (c.t + n == c.r.tiles ? kItemCost : 0);
         c.t += n - 1;
         if (left > 0) c.next(p);
       }
