@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   int seg0 = 0;                  // tile of the item at which this CTA began
   int stage = 0;
   bool first_seg = true, begin = true;
+  bool odd = false;  // this warp cleared values that are not finite
 
   // (the first NST - 1 turns only load: the item's query rows come in at the same time)
 #pragma unroll 1
@@ -304,6 +305,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         full_lo = row_keys(p, cc.s, cc.s.pos0 + i1).lo;
       }
       ref = 0;
+      odd = false;
     }
     if (x >= 0) cp_async_wait<NST - 2>();
     __syncwarp();
@@ -420,6 +422,25 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             pb[g][nt][h] = transpose8(FP8 ? pack_f16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1])
                                           : pack_bf16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1]));
       }
+      if (masked && cc.s.nq > 1) {
+        bool found = false;
+#pragma unroll 1
+        for (int i = lane; i < L::kHalfB / 16; i += 32) {
+          const int r = i / CPR, j = j0 + r;
+          if (j < full_hi && (j >= full_lo || j < p.sinks)) continue;  // all rows see it
+          const uint32_t at = sv + swz<ROWB>(r, i % CPR);
+          uint4 v = lds128(at);
+          bool hit;
+          if (FP8) hit = clear_odd_e4m3x4(v.x) | clear_odd_e4m3x4(v.y) | clear_odd_e4m3x4(v.z) | clear_odd_e4m3x4(v.w);
+          else hit = clear_odd_bf16x2(v.x) | clear_odd_bf16x2(v.y) | clear_odd_bf16x2(v.z) | clear_odd_bf16x2(v.w);
+          if (!hit) continue;
+          found = true;
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        odd |= __any_sync(0xffffffffu, found);
+        __syncwarp();
+      }
       // ---- O^T += V^T P^T
       if (FP8) {
         const int vr = (lane & 7) + ((lane >> 3) & 1) * 8, vc = lane >> 4;
@@ -476,7 +497,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
       const int u = ref - 142, u1 = u / 2;
       const float unit1 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u1) << 23) : 1.f;
       const float unit2 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u - u1) << 23) : 1.f;
-      __syncthreads();
+      const bool any_odd = __syncthreads_or(odd) != 0;
       const int64_t pbase = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS;
       float f[NT][2];
 #pragma unroll
@@ -531,6 +552,16 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           for (int w = 0; w < W; ++w) {
             const float2 t = sml[w * ROWS + pr];
             sum += t.y * paged_ex2(t.x - (top == kNInf ? 0.f : top));
+          }
+          if (any_odd) {
+            const RowKeys rk = row_keys(p, cc.s, cc.s.pos0 + R / p.G);
+            float v[4] = {a.x, a.y, a.z, a.w};
+            const int mid = min(full_lo, cc.r.hi), from = max(max(full_hi, cc.r.lo), mid);
+            for (int j = cc.r.lo < mid ? cc.r.lo : from; j < cc.r.hi; j = j + 1 == mid ? from : j + 1)
+              if (const int t = tile_of<L::kKeys>(cc.r.sink_tiles, cc.r.main0, j);
+                  t >= seg0 && t <= cc.t && j < rk.hi && (j >= rk.lo || j < p.sinks))
+                add_odd_values<FP8, 4>(p, cc.b, cc.g, j, d0, v);
+            a = make_float4(v[0], v[1], v[2], v[3]);
           }
           if (whole) {
             const int i = R / p.G, h = cc.g * p.G + R - i * p.G, t = cc.s.q0 + i;

@@ -117,6 +117,13 @@ __device__ __forceinline__ RowKeys row_keys(const PagedParams& p, const Seq& s, 
   return r;
 }
 
+// The tile of the span that holds key j, which some row sees.
+template <int KT>
+__device__ __forceinline__ int tile_of(int sink_tiles, int main0, int j) {
+  const int t = j / KT;
+  return t < sink_tiles ? t : t - main0 + sink_tiles;
+}
+
 // Position on the line of tiles.
 template <int ROWS, int KT>
 struct Cursor {
@@ -294,6 +301,46 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
   return r;
+}
+
+// ---- Values that are not finite, in keys that only some rows of a block see.  In the product with
+// V their weight 0 would still make the other rows NaN, so they are set to zero in shared memory, and
+// at the end of the item the rows that do see them add them (a weight is positive, so an infinity
+// or NaN is all that is left of the sum).  A CTA adds those of its own tiles only: its sums enter the
+// join with the weight of the keys it saw, which is 0 where a row saw none of them.
+
+// Clears what is not finite in two bf16; true if there was anything.
+__device__ __forceinline__ bool clear_odd_bf16x2(uint32_t& w) {
+  uint32_t keep = 0xffffffffu;
+  if ((w & 0x7f80u) == 0x7f80u) keep &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) keep &= 0x0000ffffu;
+  w &= keep;
+  return keep != 0xffffffffu;
+}
+// Clears NaN codes (0x7f, 0xff) in four e4m3; true if there was any.
+__device__ __forceinline__ bool clear_odd_e4m3x4(uint32_t& w) {
+  const uint32_t nan = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+  w &= ~(nan * 0xffu);
+  return nan != 0;
+}
+
+// Adds the values of columns col .. col + N - 1 of key j that are not finite to o.
+template <bool FP8, int N>
+__device__ __forceinline__ void add_odd_values(const PagedParams& p, int b, int g, int j, int col, float* o) {
+  const int pg = p.c.table[static_cast<int64_t>(b) * p.c.table_stride + (j >> p.c.page_shift)];
+  if (pg < 0 || pg >= p.c.num_pages) return;
+  const int64_t at = j & ((1 << p.c.page_shift) - 1);
+  const uint8_t* src = p.c.v + pg * p.c.vs[0] + at * p.c.vs[1] + g * p.c.vs[2];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (col + e >= p.c.d) return;
+    if (FP8) {
+      if ((src[col + e] & 0x7fu) == 0x7fu) o[e] = __uint_as_float(0x7fffffffu);
+    } else {
+      const uint32_t w = reinterpret_cast<const uint16_t*>(src)[col + e];
+      if ((w & 0x7f80u) == 0x7f80u) o[e] += __uint_as_float(w << 16);
+    }
+  }
 }
 
 // cp.async of 16 bytes; src_bytes 0 fills with zeros and reads nothing.

@@ -64,8 +64,9 @@ struct Part {
   int t0, sink_tiles, main0;
   int lo, hi, sink_hi;
   int b, g, row0;  // row0: first packed row
+  int all_lo, all_hi;  // keys j < all_hi with j >= all_lo or j < sinks are seen by every row
   int q0, nq, pos0, klen;
-  int pad;
+  int odd;  // set by the loads: values that are not finite were cleared
 };
 __device__ __forceinline__ int part_key0(const Part& s, int t) {
   return (t < s.sink_tiles ? t : s.main0 + (t - s.sink_tiles)) * kKeyTile;
@@ -186,11 +187,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
     const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
     uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
+    int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: V of keys that only some rows see, as above
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
     // code fell out of the instruction cache and everything ran at half speed.)
     for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
-      const Part& s = parts[idx % kParts];
+      Part& s = parts[idx % kParts];
       const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; -1: no row sees a key of the group.
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (FP8) {
 #pragma unroll
           for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
+          look_j0 = look_next;
         }
         if (n > 0) {
           // ---- this item's rows
@@ -234,7 +237,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             if (!(ok = slot_free(it))) break;
             const int bar = cFull + at.slot;
             uint8_t* to = sR + at.slot * L::kTile;
-            if (all && p.box > 0) {
+            // (V of keys that only some rows see is looked through for values that are not finite)
+            const bool look = is_v && !(j0 >= s.all_lo && j0 + 128 <= s.all_hi);
+            if (all && !look && p.box > 0) {
               if (warp == 12) {
                 // lane g brings the page of its group of 16 keys, if that group begins a box
                 if (lane == 0) mbar_arrive_expect_tx(&bars[bar], L::kTile);
@@ -263,6 +268,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
               }
               cp_async_wait_all();
+              if (look) {
+                uint8_t* own = to + tile_off(r0, chunk);
+#pragma unroll 1
+                for (int r = r0; r < 128; r += RPP, own += RPP * 128) {
+                  const int j = j0 + r;
+                  if (j < s.all_hi && (j >= s.all_lo || j < p.sinks)) continue;
+                  uint4 v = *reinterpret_cast<uint4*>(own);
+                  if (clear_odd_bf16x2(v.x) | clear_odd_bf16x2(v.y) | clear_odd_bf16x2(v.z) | clear_odd_bf16x2(v.w)) {
+                    *reinterpret_cast<uint4*>(own) = v;
+                    s.odd = 1;
+                  }
+                }
+              }
               announce(bar);
             }
             at.step();
@@ -271,6 +289,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
             const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
             const uint32_t dst = raw + (it & 1) * (CPR * 2048);
+            look_next = is_v && !(j0 >= s.all_lo && j0 + 128 <= s.all_hi) ? j0 : -1;
 #pragma unroll
             for (int i = 0; i < CPR; ++i) {
               const int g = ((i * RPP) >> 4) + (RPP > 16 ? r0 >> 4 : 0);
@@ -299,6 +318,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                            : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                            : "r"(src + i * 2048)
                            : "memory");
+              if (look_j0 >= 0) {
+                Part& sp = parts[look_part % kParts];
+                const int j = look_j0 + i * RPP + r0;
+                if (!(j < sp.all_hi && (j >= sp.all_lo || j < p.sinks)) &&
+                    (clear_odd_e4m3x4(x.x) | clear_odd_e4m3x4(x.y) | clear_odd_e4m3x4(x.z) | clear_odd_e4m3x4(x.w)))
+                  sp.odd = 1;
+              }
               const float sc = exp_scale(e_old[FP8 ? i : 0]);
               const uint64_t sc2 = f2(sc, sc);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -321,6 +347,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             announce(cFull + at.slot);
             at.step();
           }
+          look_part = idx;
         }
         // ---- the part's Q, behind its first loads
         if (n > 0 && i2 == (FP8 ? 0 : 1)) {
@@ -460,6 +487,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           s.nq = c.s.nq;
           s.pos0 = c.s.pos0;
           s.klen = c.s.klen;
+          const int i0 = s.row0 / p.G, i1 = min((s.row0 + ROWS - 1) / p.G, s.nq - 1);
+          s.all_hi = row_keys(p, c.s, c.s.pos0 + i0).hi;
+          s.all_lo = row_keys(p, c.s, c.s.pos0 + i1).lo;
+          s.odd = 0;
         }
         mbar_arrive(&bars[cPart + idx % kParts]);
         if (left <= 0) break;
@@ -478,7 +509,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int w = (warp >> 2) - 1, quad = warp & 3, row = w * 128 + quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
-    const float cexp = p.scale_log2, raise = kRaise / cexp;
+    const float cexp = p.scale_log2;
     const uint64_t c2 = f2(cexp, cexp);
     int ns = 0, ended = 0;  // S tiles and parts of this slot so far
     bool ok = true;
@@ -530,7 +561,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float mn = fmaxf(m, mx);
           float alpha = 1.f;
-          if (mn > m + raise) {  // (also from -inf)
+          if ((mn - m) * cexp > kRaise) {  // (also from -inf)
             alpha = m == kNInf ? 0.f : paged_ex2((m - mn) * cexp);
             l *= alpha;
             m = mn;
@@ -579,7 +610,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!(ok = wait(cOFinal + w, ended & 1))) break;
         ++ended;
         tc_fence_after();
-        const bool real = R <= last, whole = s.whole;
+        const bool real = R <= last, whole = s.whole, odd = *const_cast<volatile int*>(&s.odd) != 0;
         const int tok = real ? R / p.G : 0;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int64_t pb = (static_cast<int64_t>(blockIdx.x) * 2 + s.slot) * ROWS;
@@ -590,6 +621,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + ocol + a * 32, o);
           tmem_ld_wait(o);
+          if (odd && real) {
+            const int mid = min(s.all_lo, s.hi), from = max(max(s.all_hi, s.lo), mid);
+#pragma unroll 1
+            for (int j = s.lo < mid ? s.lo : from; j < s.hi; j = j + 1 == mid ? from : j + 1)
+              if (const int kt = tile_of<kKeyTile>(s.sink_tiles, s.main0, j);
+                  kt >= s.t0 && kt < s.t0 + n && j < rhi && (j >= rlo || j < p.sinks))
+                add_odd_values<FP8, 32>(p, s.b, s.g, j, a * 32, reinterpret_cast<float*>(o));
+          }
           if (whole) {
             uint16_t* dst = p.out + (t * p.Hq + h) * p.c.d + a * 32;
 #pragma unroll

@@ -258,3 +258,401 @@ def test_attention_matches_the_oracle(P, case, fp8):
     q = _queries(sum(news), Hq, d)
     out, lse = P.fwd(q, *s.at, _cu(news), max(news), window=window, sinks=sinks, causal=causal, **s.ex)
     _check_attention(s, q, news, out, lse, causal, window, sinks)
+
+
+# ------------------------------------------------------------------------------------------------ masked values
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("news,lens,Hq,Hkv,window,sinks", [
+    ([5], [300], 4, 1, 0, 0), ([3, 6], [40, 257], 8, 4, 20, 4), ([200, 70], [700, 70], 4, 2, 0, 0),
+    ([260], [900], 2, 1, 100, 7), ([40], [129], 4, 1, 0, 0)])
+def test_values_of_unseen_keys_reach_no_row(P, fp8, news, lens, Hq, Hkv, window, sinks):
+    """NaN and infinities in K and V of keys that only some rows of a chunk see: the rows that do not see
+    them are as if they were not there, the rows that do get what they make of the sum."""
+    d, page = 128, 16
+    s = Setup(P, lens, Hkv, d, page, fp8, seed=11)
+    q = _queries(sum(news), Hq, d)
+    kw = dict(window=window, sinks=sinks, **s.ex)
+    cu = _cu(news)
+    clean, clean_lse = P.fwd(q, *s.at, cu, max(news), **kw)
+    at = 0
+    for b, n in enumerate(news):
+        # the last new token's V (seen by one row only), one in the middle, and one at the window's lower edge
+        nk = lens[b]
+        spots = {nk - 1, nk - 1 - n // 2}
+        if window and nk - n - window // 2 >= sinks:
+            spots.add(max(nk - n - window + 1 + n // 2, sinks))
+        for x, j in enumerate(sorted(spots)):
+            pg, sl = int(s.table[b, j // page]), j % page
+            if fp8:
+                s.vc.view(torch.uint8)[pg, sl, :, 5 + x] = 0x7F
+            else:
+                s.vc[pg, sl, :, 5 + x] = float("nan") if x % 2 else float("inf")
+        out, lse = P.fwd(q, *s.at, cu, max(news), **kw)
+        assert torch.equal(lse[:, at:at + n], clean_lse[:, at:at + n])
+        for i in range(n):
+            keep = orc.visible(nk - n + i, nk, True, window, sinks)
+            row, ref = out[at + i].float(), clean[at + i].float()
+            for x, j in enumerate(sorted(spots)):
+                c = 5 + x
+                if keep[j]:
+                    bad = ~torch.isfinite(row[:, c])
+                    assert bad.all()
+                    if not fp8 and x % 2 == 0:
+                        # (a weight below 2^-126 is 0 in fp32, and 0 * inf is NaN: looked at down to 2^-100)
+                        for h in range(Hq):
+                            sc = d ** -0.5 * float(s.K[b][j, h // (Hq // Hkv)] @ _np(q[at + i, h]))
+                            if sc - float(clean_lse[h, at + i]) > -100 * np.log(2):
+                                assert row[h, c] == float("inf")
+                else:
+                    assert torch.isfinite(row[:, c]).all()
+            cols = [c for c in range(d) if c - 5 not in range(len(spots))]
+            # (a run may be cut elsewhere for nothing else: the sums are the same ones)
+            assert torch.equal(row[:, cols], ref[:, cols])
+        at += n
+        # K: a NaN in the last key reaches the last row alone
+        pg, sl = int(s.table[b, (nk - 1) // page]), (nk - 1) % page
+        if fp8:
+            s.kc.view(torch.uint8)[pg, sl, :, 3] = 0x7F
+        else:
+            s.kc[pg, sl, :, 3] = float("nan")
+        out, lse = P.fwd(q, *s.at, cu, max(news), **kw)
+        if n > 1:
+            assert torch.isfinite(lse[:, at - n:at - 1]).all()
+            cols = [c for c in range(d) if c > 9]
+            assert torch.equal(out[at - n:at - 1, :, cols], clean[at - n:at - 1, :, cols])
+        assert torch.isnan(lse[:, at - 1]).all() and torch.isnan(out[at - 1]).all()
+        clean, clean_lse = out, lse  # the next sequence's rows have not changed
+
+
+def test_rows_of_lowest_and_largest_scores(P):
+    """Scores of +-1e4 and a chunk whose first tiles are far below its last: the running maximum holds."""
+    s = Setup(P, [600, 600], 1, 64, 16, False, seed=4, scale=6.0)
+    q = _queries(2 * 40, 4, 64, gain=20.0)
+    for news in ([40, 40], [1, 2]):
+        T = sum(news)
+        out, lse = P.fwd(q[:T], *s.at, _cu(news), max(news), scale=1.0)
+        _check_attention(s, q[:T], news, out, lse, scale=1.0)
+    out, lse = P.fwd(q[:3], *s.at, _cu([1, 2]), 2, scale=1e-30)
+    _check_attention(s, q[:3], [1, 2], out, lse, scale=1e-30)
+    out, lse = P.fwd(q, *s.at, _cu([40, 40]), 40, scale=1e-30)
+    _check_attention(s, q, [40, 40], out, lse, scale=1e-30)
+
+
+def test_e4m3_scales_from_end_to_end(P):
+    """Rows whose scale bytes span the range: tiny, huge and zero rows in one sequence."""
+    d, n = 128, 200
+    g = torch.Generator().manual_seed(8)
+    s = Setup(P, [n], 2, d, 16, True, seed=2)
+    x = torch.randn(n, 2, d, generator=g)
+    k = (x * torch.exp2(torch.randint(-8, 2, (n, 2, 1), generator=g).float())).bfloat16()
+    v = (torch.randn(n, 2, d, generator=g) * torch.exp2(torch.randint(-10, 3, (n, 2, 1), generator=g).float())).bfloat16()
+    v[7] = 0
+    k[9] = 0
+    P.kv_append(k.cuda(), v.cuda(), *s.at, _cu([n]), **s.ex)
+    s.K = [orc.dequantise(*orc.quantise(_np(k)))]
+    s.V = [orc.dequantise(*orc.quantise(_np(v)))]
+    for new in (1, 5, 60):
+        q = _queries(new, 8, d, seed=new)
+        out, lse = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
+        _check_attention(s, q, [new], out, lse)
+    # all values a factor 2^100 larger: the same sums, scaled
+    big = Setup(P, [n], 2, d, 16, True, seed=2)
+    big.kc.view(torch.uint8).copy_(s.kc.view(torch.uint8)), big.vc.view(torch.uint8).copy_(s.vc.view(torch.uint8))
+    big.ke.copy_(s.ke)
+    big.ve.copy_(torch.where(s.ve == 255, s.ve, s.ve + 90))
+    big.table.copy_(s.table)
+    for new in (1, 60):
+        q = _queries(new, 8, d, seed=new)
+        a, b = P.fwd(q, *s.at, _cu([new]), new, **s.ex), P.fwd(q, *big.at, _cu([new]), new, **big.ex)
+        assert torch.equal(a[1], b[1]) and torch.equal(torch.ldexp(a[0].float(), torch.tensor(90)), b[0].float())
+
+
+# ------------------------------------------------------------------------------------------------ as they are used
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_then_decode_like_one_long_call(P, fp8):
+    """A prompt in two chunks and then single tokens, every step written to the cache first: the rows are those
+    of attention over the whole sequence at once (the float64 oracle on what the cache holds)."""
+    Hq, Hkv, d, page, total = 8, 2, 128, 16, 150
+    steps = [90, 57] + [1] * 3
+    g = torch.Generator().manual_seed(1)
+    k, v = ((torch.randn(2, total + 11 * b, Hkv, d, generator=g)).bfloat16() for b in (0, 0))
+    kc, vc, ke, ve = P.empty_cache(32, page, Hkv, d, dtype=E4M3 if fp8 else torch.bfloat16)
+    ex = dict(k_exp=ke, v_exp=ve)
+    table = torch.randperm(32, generator=g)[:24].view(2, 12).int().cuda()
+    q = torch.randn(2, total, Hq, d, generator=g).bfloat16()
+    outs, done = [], 0
+    for n in steps:
+        # the second sequence is a token behind until the last step
+        lens = torch.tensor([done + n, done + n], dtype=torch.int32, device="cuda")
+        cu = _cu([n, n])
+        pack = lambda t: torch.cat([t[0, done:done + n], t[1, done:done + n]]).cuda()  # noqa: E731
+        P.kv_append(pack(k), pack(v), kc, vc, table, lens, cu, **ex)
+        outs.append(P.fwd(pack(q), kc, vc, table, lens, cu, n, window=64, sinks=3, **ex))
+        done += n
+    for b in range(2):
+        K, V = (_np(t[b]) for t in (k, v))
+        if fp8:
+            K, V = (orc.dequantise(*orc.quantise(t)) for t in (K, V))
+        ref, rl, A, D = orc.attend(_np(q[b]), K, V, d ** -0.5, True, 64, 3)
+        got = torch.cat([o[0][n * b:n * (b + 1)] for (o, n) in zip(outs, steps)])
+        w = 2.0 ** -22 * (8 + d * D)[..., None]
+        assert (np.abs(_np(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * w) * A + 1e-30).all()
+        gl = torch.cat([o[1][:, n * b:n * (b + 1)] for (o, n) in zip(outs, steps)], 1)
+        assert (np.abs(_np(gl).T - rl) <= w[..., 0] + 2.0 ** -22 * np.abs(rl)).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_gathered_keys_feed_the_masked_forward(P, fp8):
+    """kv_gather's padded rows through fdma.fwd (the masked, biased path) give the paged forward's rows."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    lens, new, Hq, Hkv, d, N = [300, 384], 128, 4, 2, 128, 384
+    s = Setup(P, lens, Hkv, d, 64, fp8, seed=9)
+    q = _queries(2 * new, Hq, d)
+    out, lse = P.fwd(q, *s.at, _cu([new, new]), new, **s.ex)
+    cu = torch.tensor([0, N, 2 * N], dtype=torch.int32, device="cuda")
+    k, v = P.kv_gather(*s.at, cu, 2 * N, **s.ex)
+    k, v = k.view(2, N, Hkv, d), v.view(2, N, Hkv, d)
+    for b in range(2):
+        o, z = fdma.fwd(q.view(2, new, Hq, d)[b:b + 1], k[b:b + 1], v[b:b + 1], causal_offset=lens[b] - new)
+        # both round the weights to bf16 and the result to bf16; fdma's lse carries the rounded weights (1.95e-3)
+        assert float((o[0].float() - out[b * new:(b + 1) * new].float()).norm() / o[0].float().norm()) < 2.0 ** -7
+        assert float((z[0] - lse[:, b * new:(b + 1) * new]).abs().max()) < 4e-3
+
+
+def test_rows_behind_the_last_sequence_and_given_outputs(P):
+    s = Setup(P, [40, 500], 2, 64, 16, False, seed=6)
+    for news in ([1, 1], [3, 70]):
+        T = sum(news)
+        q = _queries(T + 5, 4, 64)
+        q[T:] = float("nan")
+        out = torch.full((T + 5, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((4, T + 5), 3.0, device="cuda")
+        a = P.make_args(q, *s.at, _cu(news), max(news) + 9)
+        ws = P.alloc_workspace(a, "cuda")
+        ws.fill_(255)
+        o, z = P.fwd(q, *s.at, _cu(news), max(news) + 9, out=out, lse=lse, workspace=ws)
+        assert o is out and z is lse
+        assert (out[T:] == 3).all() and (lse[:, T:] == 3).all()
+        _check_attention(s, q[:T], news, out[:T], lse[:, :T])
+
+
+def test_strided_queries_and_wide_batches(P):
+    """Queries as a slice of a fused projection; 200 sequences of 0 to 40 keys (more than SMs and than a warp)."""
+    g = np.random.default_rng(3)
+    lens = g.integers(0, 41, 200).tolist()
+    s = Setup(P, lens, 2, 64, 16, False, seed=5)
+    for news in ([min(1, n) for n in lens], [min(n, 17) for n in lens]):
+        T = sum(news)
+        big = torch.randn(T, 3, 6, 64, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+        q = big[:, 1, 1:5]
+        out, lse = P.fwd(q, *s.at, _cu(news), max(news))
+        _check_attention(s, q, news, out, lse)
+
+
+def test_repeats_bit_for_bit(P):
+    s = Setup(P, [3000, 70, 900], 2, 128, 16, True, seed=7)
+    for news in ([1, 1, 1], [300, 70, 5]):
+        q = _queries(sum(news), 8, 128)
+        a = P.fwd(q, *s.at, _cu(news), max(news), **s.ex)
+        for _ in range(5):
+            b = P.fwd(q, *s.at, _cu(news), max(news), **s.ex)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_step_replays_from_a_cuda_graph(P, fp8):
+    """A decoding step (append, attention) captured once: replays follow the lengths, pages, offsets and
+    tokens that change in place."""
+    Hq, Hkv, d, page = 8, 2, 128, 16
+    s = Setup(P, [200, 31], Hkv, d, page, fp8, seed=3, extra_pages=10)
+    s.table[:, -2:] = torch.tensor([[s.num - 1, s.num - 2]], dtype=torch.int32).cuda()  # (not used by any sequence)
+    used = set(s.table[0, :13].tolist() + s.table[1, :2].tolist())
+    free = [i for i in range(s.num) if i not in used]
+    s.table[0, 13], s.table[1, 2] = free[0], free[1]
+    k, v, q = (torch.randn(2, h, d, device="cuda").bfloat16() for h in (Hkv, Hkv, Hq))
+    cu = _cu([1, 1])
+    out, lse = torch.empty_like(q), torch.empty(Hq, 2, device="cuda")
+
+    def step():
+        P.kv_append(k, v, *s.at, cu, **s.ex)
+        P.fwd(q, *s.at, cu, 1, out=out, lse=lse, **s.ex)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in range(12):  # crosses into a new page
+        s.k_lens += 1
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=torch.Generator().manual_seed(i)).bfloat16())
+        graph.replay()
+        got = out.clone(), lse.clone()
+        step()
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+    K, V = P.kv_gather(*s.at, _cu(s.k_lens.tolist()), int(s.k_lens.sum()), **s.ex)
+    n = int(s.k_lens[0])
+    s.K, s.V = ([_np(t[:n]), _np(t[n:])] for t in (K, V))
+    _check_attention(s, q, [1, 1], out, lse)
+
+
+def test_two_streams_at_once(P):
+    """Calls on two side streams, outputs and workspaces allocated by the calls, inputs ready."""
+    s = Setup(P, [2000, 900], 2, 128, 16, False, seed=8)
+    cases = [([1, 1], _queries(2, 8, 128, 1)), ([200, 33], _queries(233, 8, 128, 2))]
+    want = [P.fwd(q, *s.at, _cu(n), max(n)) for n, q in cases]
+    cus = [_cu(n) for n, _ in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, (n, q) in enumerate(cases):
+            got[i].append(P.fwd(q, *s.at, cus[i], max(n), stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, z in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(z, want[i][1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(P, fp8):
+    """A cache of more than 2^32 bytes a tensor whose used pages lie at its end."""
+    Hkv, d, page = 8, 128, 64
+    per = page * Hkv * d * (1 if fp8 else 2)
+    num = (1 << 32) // per + 70
+    kc, vc, ke, ve = P.empty_cache(num, page, Hkv, d, dtype=E4M3 if fp8 else torch.bfloat16)
+    ex = dict(k_exp=ke, v_exp=ve)
+    n = 300
+    g = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(n, Hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    table = torch.tensor([[num - 1, 0, num - 3, num - 2, num - 5]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    at = (kc, vc, table, lens)
+    P.kv_append(k, v, *at, _cu([n]), **ex)
+    kk, vv = P.kv_gather(*at, _cu([n]), n, **ex)
+    if fp8:
+        K, V = (orc.dequantise(*orc.quantise(_np(t))) for t in (k, v))
+        assert np.array_equal(_np(kk), K) and np.array_equal(_np(vv), V)
+    else:
+        assert torch.equal(kk, k) and torch.equal(vv, v)
+    s = Setup.__new__(Setup)
+    s.d, s.Hkv, s.fp8, s.K, s.V = d, Hkv, fp8, [_np(kk)], [_np(vv)]
+    for new in (1, 64):
+        q = _queries(new, Hkv * 2, d)
+        out, lse = P.fwd(q, *at, _cu([new]), new, **ex)
+        _check_attention(s, q, [new], out, lse)
+
+
+def test_broadcast_heads_of_a_cache(P):
+    """kv heads that share one row (stride 0): read like any other cache, refused as a target."""
+    s = Setup(P, [500], 1, 64, 16, False, seed=3)
+    kc, vc = s.kc.expand(-1, -1, 4, -1), s.vc.expand(-1, -1, 4, -1)
+    at = (kc, vc, s.table, s.k_lens)
+    t = Setup.__new__(Setup)
+    t.d, t.Hkv, t.fp8 = 64, 4, False
+    t.K, t.V = [np.repeat(s.K[0], 4, 1)], [np.repeat(s.V[0], 4, 1)]
+    for new in (1, 100):
+        q = _queries(new, 8, 64)
+        out, lse = P.fwd(q, *at, _cu([new]), new)
+        _check_attention(t, q, [new], out, lse)
+    k = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    from block_sparse_masked_02_gb300 import fdma
+
+    with pytest.raises(fdma.FdmaError):
+        P.kv_append(k, k, *at, _cu([1]))
+
+
+# ------------------------------------------------------------------------------------------------ refusals
+def test_bad_device_arrays_are_reported_and_not_followed(P):
+    """Page numbers, lengths and offsets out of range: nothing is read or written there, the rest is right,
+    and the device error says so."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    s = Setup(P, [40, 200], 2, 64, 16, False, seed=1)
+    bad = s.table.clone()
+    bad[0, 1] = s.num  # one past the last page
+    at = (s.kc, s.vc, bad, s.k_lens)
+    kk, _ = P.kv_gather(*at, _cu([40, 200]), 240)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    want = np.concatenate([s.K[0], s.K[1]])
+    want[16:32] = 0
+    assert np.array_equal(_np(kk), want)
+    for news in ([1, 1], [30, 100]):
+        q = _queries(sum(news), 4, 64)
+        out, lse = P.fwd(q, *at, _cu(news), max(news))
+        assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+        assert torch.isfinite(out).all()
+        ref, rl = P.fwd(q, *s.at, _cu(news), max(news))
+        assert torch.equal(out[news[0]:], ref[news[0]:])  # the other sequence
+        # more new tokens than max_q: the rest is left out
+        part = torch.full_like(out, 5.0)
+        P.fwd(q, *s.at, _cu(news), max(news) - 1 if max(news) > 1 else 1, out=part)
+        if max(news) > 1:
+            assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+            assert (part[-1] == 5).all()
+    # a length past the table: keys of the whole table, reported
+    far = s.k_lens.clone()
+    far[1] = 1 << 30
+    full = s.table.clamp(min=0)
+    P.fwd(_queries(2, 4, 64), s.kc, s.vc, full, far, _cu([1, 1]), 1)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    P.kv_gather(s.kc, s.vc, full, far, _cu([40, 10]), 50)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    # an append to a position before the first key, past the table, or to a page that is not there
+    k = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    before = s.kc.clone()
+    P.kv_append(k, k, s.kc, s.vc, bad, torch.tensor([18, 1], dtype=torch.int32, device="cuda"), _cu([1, 2]))
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    pg = int(s.table[1, 0])
+    before[pg, 0] = 1
+    assert torch.equal(torch.nan_to_num(s.kc, nan=9.0), torch.nan_to_num(before, nan=9.0))
+    # offsets that run backwards or past the tokens
+    q = _queries(4, 4, 64)
+    cu = torch.tensor([0, 3, 9], dtype=torch.int32, device="cuda")
+    P.fwd(q, *s.at, cu, 3)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    cu = torch.tensor([3, 1, 2], dtype=torch.int32, device="cuda")
+    P.fwd(q, *s.at, cu, 3)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+
+
+def test_empty_calls_do_nothing(P):
+    s = Setup(P, [20], 2, 64, 16, False)
+    none = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    P.kv_append(none, none, *s.at, _cu([0]))
+    out, lse = P.fwd(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda"), *s.at, _cu([0]), 0)
+    assert out.shape == (0, 4, 64) and lse.shape == (4, 0)
+    k, v = P.kv_gather(*s.at, _cu([0]), 0)
+    assert k.shape == (0, 2, 64)
+
+
+def test_tensors_of_a_call_are_checked(P):
+    from block_sparse_masked_02_gb300 import fdma
+
+    s = Setup(P, [40], 2, 64, 16, False)
+    q = _queries(1, 4, 64)
+    cu = _cu([1])
+    with pytest.raises(ValueError):
+        P.fwd(q.float(), *s.at, cu, 1)
+    with pytest.raises(ValueError):
+        P.fwd(q, s.kc, s.vc, s.table.cpu(), s.k_lens, cu, 1)
+    with pytest.raises(ValueError):
+        P.fwd(q, s.kc, s.vc, s.table.long(), s.k_lens, cu, 1)
+    with pytest.raises(ValueError):
+        P.fwd(q, *s.at, _cu([1, 1]), 1)
+    with pytest.raises(ValueError):
+        P.fwd(q, *s.at, cu, 1, k_exp=torch.zeros(1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        P.fwd(q, s.kc.to(E4M3), s.vc.to(E4M3), s.table, s.k_lens, cu, 1)
+    with pytest.raises(ValueError):
+        P.fwd(q, *s.at, cu, 1, lse=torch.zeros(1, 4, device="cuda"))
+    with pytest.raises(fdma.FdmaError):
+        P.fwd(q, *s.at, cu, 1, window=8, causal=False)
+    with pytest.raises(fdma.FdmaError):
+        P.fwd(q, *s.at, cu, 1, scale=float("nan"))
+    with pytest.raises(fdma.FdmaError):
+        P.fwd(q, *s.at, cu, 1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
