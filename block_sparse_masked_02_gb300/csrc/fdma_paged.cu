@@ -423,20 +423,15 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
                                           : pack_bf16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1]));
       }
       if (masked && cc.s.nq > 1) {
+        // a lane's column of 16-byte pieces (rows eight apart have theirs exchanged alike)
         bool found = false;
-#pragma unroll 1
-        for (int i = lane; i < L::kHalfB / 16; i += 32) {
-          const int r = i / CPR, j = j0 + r;
-          if (j < full_hi && (j >= full_lo || j < p.sinks)) continue;  // all rows see it
-          const uint32_t at = sv + swz<ROWB>(r, i % CPR);
-          uint4 v = lds128(at);
-          bool hit;
-          if (FP8) hit = clear_odd_e4m3x4(v.x) | clear_odd_e4m3x4(v.y) | clear_odd_e4m3x4(v.z) | clear_odd_e4m3x4(v.w);
-          else hit = clear_odd_bf16x2(v.x) | clear_odd_bf16x2(v.y) | clear_odd_bf16x2(v.z) | clear_odd_bf16x2(v.w);
-          if (!hit) continue;
-          found = true;
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
+        const SeenKeys seen{cc.r.lo, cc.r.hi, cc.r.sink_hi, full_lo, full_hi, p.sinks};
+        if (STEP == 32) {
+          for (int r = crow; r < 8; r += RPP)
+            found |= mend_pieces_apart<FP8>(sv + swz<ROWB>(r, chunk), 8 * ROWB, 4, j0 + r, 8, seen);
+        } else {
+          for (int r = crow; r < 16; r += RPP)  // (four times the same piece)
+            found |= mend_pieces_apart<FP8>(sv + swz<ROWB>(r, chunk), 0, 4, j0 + r, 0, seen);
         }
         odd |= __any_sync(0xffffffffu, found);
         __syncwarp();
@@ -553,16 +548,6 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             const float2 t = sml[w * ROWS + pr];
             sum += t.y * paged_ex2(t.x - (top == kNInf ? 0.f : top));
           }
-          if (any_odd) {
-            const RowKeys rk = row_keys(p, cc.s, cc.s.pos0 + R / p.G);
-            float v[4] = {a.x, a.y, a.z, a.w};
-            const int mid = min(full_lo, cc.r.hi), from = max(max(full_hi, cc.r.lo), mid);
-            for (int j = cc.r.lo < mid ? cc.r.lo : from; j < cc.r.hi; j = j + 1 == mid ? from : j + 1)
-              if (const int t = tile_of<L::kKeys>(cc.r.sink_tiles, cc.r.main0, j);
-                  t >= seg0 && t <= cc.t && j < rk.hi && (j >= rk.lo || j < p.sinks))
-                add_odd_values<FP8, 4>(p, cc.b, cc.g, j, d0, v);
-            a = make_float4(v[0], v[1], v[2], v[3]);
-          }
           if (whole) {
             const int i = R / p.G, h = cc.g * p.G + R - i * p.G, t = cc.s.q0 + i;
             const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
@@ -573,6 +558,16 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           } else {
             *reinterpret_cast<float4*>(p.part_o + (pbase + pr) * D + d0) = a;
             if (d0 == 0) p.part_ml[pbase + pr] = make_float2(top, sum);
+          }
+          if (any_odd) {
+            const int i = R / p.G, h = cc.g * p.G + R - i * p.G, mid = min(full_lo, cc.r.hi);
+            const RowKeys rk = row_keys(p, cc.s, cc.s.pos0 + i);
+            const OddKeys k{cc.b,    cc.g, cc.r.lo, mid, max(max(full_hi, cc.r.lo), mid), cc.r.hi, cc.r.sink_tiles, cc.r.main0,
+                            seg0, cc.t};
+            add_odd_values<FP8, L::kKeys>(
+                p, k, rk.lo, rk.hi, d0, 4,
+                whole ? p.out + (static_cast<int64_t>(cc.s.q0 + i) * p.Hq + h) * p.c.d : nullptr,
+                p.part_o + (pbase + pr) * D, 4);
           }
         }
         __syncthreads();

@@ -12,6 +12,9 @@
 //   warp 3          walks the CTA's run and publishes its parts, one item or piece of an item
 //                   each, in shared memory for the other roles (which keeps the walk's
 //                   state out of their registers: spilled there it cost more than half the time);
+//   warps 1 and 2   look through the V tiles (by TMA) whose keys not every row sees: rows that nobody
+//                   sees become zeros, values that are not finite are cleared (fdma_paged.cuh);
+//                   the loads stay ahead meanwhile;
 //   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: S is read from TMEM once,
 //   warps 8..11     masked only in tiles that some row of the warp sees in part, exponentiated
 //                   with a running maximum that is raised only when it grows by 2^8 or more;
@@ -30,8 +33,11 @@ constexpr int kChunkThreads = 512;
 constexpr int kKeyTile = 128;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
+constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
 constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
+constexpr uint32_t kRegsLoad8 = 96, kRegsSoft8 = 176;  // e4m3: the conversion needs more
 constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
+static_assert(kRegsMma + kRegsLoad8 + 2 * kRegsSoft8 == 4 * kChunkLaunchRegs, "the registers of the launch");
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
 
@@ -46,7 +52,8 @@ enum ChunkBar : int {
   cOFree = cOFinal + 2,   // + slot: the softmax threads have read O
   cPart = cOFree + 2,     // + part slot: the part is published
   cPartFree = cPart + kParts,  // + part slot: every reader is done with it
-  cDrain = cPartFree + kParts,
+  cLook = cPartFree + kParts,  // + entry: a V tile to be looked through has landed
+  cDrain = cLook + kLooks,
   kChunkBars
 };
 
@@ -68,15 +75,31 @@ struct Part {
   int q0, nq, pos0, klen;
   int odd;  // set by the loads: values that are not finite were cleared
 };
-__device__ __forceinline__ int part_key0(const Part& s, int t) {
-  return (t < s.sink_tiles ? t : s.main0 + (t - s.sink_tiles)) * kKeyTile;
-}
+// First key of the k-th tile of a part.
+struct PartTiles {
+  int t0, sink_tiles, skip;
+  __device__ __forceinline__ explicit PartTiles(const Part& s)
+      : t0(s.t0), sink_tiles(s.sink_tiles), skip(s.main0 - s.sink_tiles) {}
+  __device__ __forceinline__ int key0(int k) const {
+    const int t = t0 + k;
+    return (t < sink_tiles ? t : t + skip) * kKeyTile;
+  }
+};
 
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+
+struct Look {
+  int slot;  // of the ring; -1: the run is over
+  int j0, part;
+};
+
+__device__ __forceinline__ SeenKeys part_seen(const Part& s, int sinks) {
+  return SeenKeys{s.lo, s.hi, s.sink_hi, s.all_lo, s.all_hi, sinks};
 }
 
 // A place in a ring of N tiles and the parity of its current fill.
@@ -101,7 +124,8 @@ struct ChunkSmem {
   static constexpr int kOffBar = kOffRaw + (FP8 ? kTile : 0);
   static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
   static constexpr int kOffParts = kOffMisc + 16;
-  static constexpr int kOffPlan = kOffParts + kParts * static_cast<int>(sizeof(Part));
+  static constexpr int kOffLooks = kOffParts + kParts * static_cast<int>(sizeof(Part));
+  static constexpr int kOffPlan = (kOffLooks + kLooks * static_cast<int>(sizeof(Look)) + 7) / 8 * 8;
   static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
@@ -109,7 +133,7 @@ struct ChunkSmem {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                       const PagedParams p) {
+                       const __grid_constant__ PagedParams p) {
   using L = ChunkSmem<D, FP8>;
   using Ring = RingPos<L::kRing>;
   constexpr int ROWS = kChunkRows;
@@ -157,6 +181,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag); };
 
   Part* parts = reinterpret_cast<Part*>(smem + L::kOffParts);
+  Look* look_at = reinterpret_cast<Look*>(smem + L::kOffLooks);
   // The idx-th part of the run; false on a time-out.
   auto part_ready = [&](int idx) { return wait(cPart + idx % kParts, (idx / kParts) & 1); };
   auto part_done = [&](int idx) { mbar_arrive(&bars[cPartFree + idx % kParts]); };
@@ -167,7 +192,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // as the ring goes, across parts.  bf16 tiles that are seen whole come by TMA, a box a page;
     // tiles with keys that no row sees (and layouts that TMA cannot address) by cp.async, which
     // fills those with zeros.
-    regs_decrease<kRegsLoad>();
+    regs_decrease<FP8 ? kRegsLoad8 : kRegsLoad>();
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
     Ring at;     // the place of the next item
@@ -187,24 +212,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
     const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
     uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
-    int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: V of keys that only some rows see, as above
+    int looks = 0;                                      // bf16: V tiles given to the looking warps
+    int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: the same, looked through here as they are converted
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
     // code fell out of the instruction cache and everything ran at half speed.)
     for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
       Part& s = parts[idx % kParts];
-      const int n = s.n, b = s.b, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
+      // (copies: what lies in shared memory is read again after every barrier)
+      const int n = s.n, b = s.b, g_kv = s.g, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, all_lo = s.all_lo, all_hi = s.all_hi;
+      const PartTiles tiles(s);
       // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
-      // ahead of their use; -1: no row sees a key of the group.
+      // ahead of their use; none where no row sees a key of the group (of its box).
+      const int unit = max(p.box, 16);
       auto look_up = [&](int k) {
         int entry = kNoKeys;
         if (lane < 8 && k < n) {
-          const int j = part_key0(s, s.t0 + k) + lane * 16;
-          if (j < sink_hi || (j < hi && j + 16 > lo)) entry = table_entry(p, b, j);
+          const int j = tiles.key0(k) + lane * 16, jb = j & -unit;
+          if (jb < sink_hi || (jb < hi && jb + unit > lo)) entry = table_entry(p, b, j);
         }
         return entry;
       };
       int pg = -1, pg_next = look_up(0);
+      bool missing = false;  // a page that is needed is not there
       // (one turn without loads at the end of the run, for the last raw item)
       const int turns = n > 0 ? 2 * n : FP8 ? 1 : 0;
 #pragma unroll 1
@@ -217,84 +247,90 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (n > 0) {
           // ---- this item's rows
           const bool is_v = i2 & 1;
-          const int j0 = part_key0(s, s.t0 + (i2 >> 1));
+          const int j0 = tiles.key0(i2 >> 1);
           if (!is_v) {
-            pg = checked_page(p, pg_next);
+            const int entry = pg_next;
+            pg = checked_page(p, entry);
+            missing = __any_sync(0xffffffffu, entry != kNoKeys && pg < 0);
             pg_next = look_up((i2 >> 1) + 1);
           }
-          const uint8_t* from = (is_v ? p.c.v : p.c.k) + s.g * (is_v ? p.c.vs[2] : p.c.ks[2]);
-          const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
-          const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-          const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
-          // every key of the tile is seen by some row and has a page
-          const bool all =
-              j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
-          auto key_in = [&](int j, int g) {
-            return __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
-          };
-          auto row_group = [&](int64_t v, int g) { return __shfl_sync(0xffffffffu, v, g); };
           if (!FP8) {
             if (!(ok = slot_free(it))) break;
             const int bar = cFull + at.slot;
             uint8_t* to = sR + at.slot * L::kTile;
-            // (V of keys that only some rows see is looked through for values that are not finite)
-            const bool look = is_v && !(j0 >= s.all_lo && j0 + 128 <= s.all_hi);
-            if (all && !look && p.box > 0) {
+            // V of keys that not every row sees goes by the looking warps.  (K needs no care: scores of
+            // unseen keys are replaced, whatever they are.)
+            const bool look = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi);
+            if (p.box > 0 && !missing) {
               if (warp == 12) {
                 // lane g brings the page of its group of 16 keys, if that group begins a box
-                if (lane == 0) mbar_arrive_expect_tx(&bars[bar], L::kTile);
+                const bool mine_box = lane < 8 && ((lane * 16) & (p.box - 1)) == 0 && pg >= 0;
+                const unsigned boxes = __ballot_sync(0xffffffffu, mine_box);
+                uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
+                if (lane == 0) {
+                  if (look) look_at[looks % kLooks] = Look{at.slot, j0, idx};
+                  mbar_arrive_expect_tx(to_bar, __popc(boxes) * p.box * (2 * D));
+                }
                 __syncwarp();
-                if (lane < 8 && ((lane * 16) & (p.box - 1)) == 0) {
+                if (mine_box) {
                   const CUtensorMap* tm = is_v ? &tmV : &tmK;
 #pragma unroll
                   for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(to + c * 16384 + lane * 2048, tm, &bars[bar], c * 64, (j0 + lane * 16) & pmask, s.g, pg);
+                    tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
                 }
-              } else if (lane == 0) {
+                looks += look;
+              } else if (lane == 0 && !look) {
                 mbar_arrive(&bars[bar]);
               }
             } else {
+              const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
+              const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
+              const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+              const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
               constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
               uint32_t dst = smem_u32(to) + tile_off(r0, chunk);
 #pragma unroll 1
               for (int g = 0; g < 8; ++g) {
-                const uint8_t* src = mine + row_group(group, g);
+                const uint8_t* src = mine + __shfl_sync(0xffffffffu, group, g);
+                const bool paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                  const bool in = key_in(j0 + g * 16 + i * RPP + r0, g);
+                  const int j = j0 + g * 16 + i * RPP + r0;
+                  const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
                   cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
                   src += RPP * st;
                   dst += RPP * 128;
                 }
               }
               cp_async_wait_all();
-              if (look) {
-                uint8_t* own = to + tile_off(r0, chunk);
-#pragma unroll 1
-                for (int r = r0; r < 128; r += RPP, own += RPP * 128) {
-                  const int j = j0 + r;
-                  if (j < s.all_hi && (j >= s.all_lo || j < p.sinks)) continue;
-                  uint4 v = *reinterpret_cast<uint4*>(own);
-                  if (clear_odd_bf16x2(v.x) | clear_odd_bf16x2(v.y) | clear_odd_bf16x2(v.z) | clear_odd_bf16x2(v.w)) {
-                    *reinterpret_cast<uint4*>(own) = v;
-                    s.odd = 1;
-                  }
-                }
-              }
+              if (look && mend_pieces_apart<false>(smem_u32(to) + tile_off(r0, chunk), RPP * 128, CPR, j0 + r0, RPP,
+                                             part_seen(s, p.sinks)))
+                s.odd = 1;
               announce(bar);
             }
             at.step();
           } else {
+            const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
+            const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
+            const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+            const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
+            // every key of the tile is seen by some row and has a page
+            const bool all =
+                j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
             const int64_t* es = is_v ? p.c.ves : p.c.kes;
-            const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + s.g * es[2] + (r0 & 15) * es[1];
+            const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + g_kv * es[2] + (r0 & 15) * es[1];
             const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
             const uint32_t dst = raw + (it & 1) * (CPR * 2048);
-            look_next = is_v && !(j0 >= s.all_lo && j0 + 128 <= s.all_hi) ? j0 : -1;
+            look_next = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi) ? j0 : -1;
 #pragma unroll
             for (int i = 0; i < CPR; ++i) {
               const int g = ((i * RPP) >> 4) + (RPP > 16 ? r0 >> 4 : 0);
-              const int64_t off = row_group(group, g), eoff = row_group(egroup, g);
-              const bool in = all || key_in(j0 + i * RPP + r0, g);
+              const int64_t off = __shfl_sync(0xffffffffu, group, g), eoff = __shfl_sync(0xffffffffu, egroup, g);
+              bool in = true;
+              if (!all) {
+                const int j = j0 + i * RPP + r0;
+                in = __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
+              }
               cp_async16(dst + i * 2048, in ? mine + off : p.c.k, in ? cb : 0u);
               e_new[FP8 ? i : 0] = 127;
               if (in) e_new[FP8 ? i : 0] = efrom[eoff];
@@ -311,6 +347,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (item >= 0 && (n > 0 || it > 0)) {
             if (!(ok = slot_free(item))) break;
             const uint32_t src = raw + (item & 1) * (CPR * 2048);
+            if (look_j0 >= 0) {
+              Part& sp = parts[look_part % kParts];
+              if (mend_pieces_apart<true>(src, 2048, CPR, look_j0 + r0, RPP, part_seen(sp, p.sinks))) sp.odd = 1;
+            }
 #pragma unroll
             for (int i = 0; i < CPR; ++i) {
               uint4 x;
@@ -318,13 +358,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                            : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
                            : "r"(src + i * 2048)
                            : "memory");
-              if (look_j0 >= 0) {
-                Part& sp = parts[look_part % kParts];
-                const int j = look_j0 + i * RPP + r0;
-                if (!(j < sp.all_hi && (j >= sp.all_lo || j < p.sinks)) &&
-                    (clear_odd_e4m3x4(x.x) | clear_odd_e4m3x4(x.y) | clear_odd_e4m3x4(x.z) | clear_odd_e4m3x4(x.w)))
-                  sp.odd = 1;
-              }
               const float sc = exp_scale(e_old[FP8 ? i : 0]);
               const uint64_t sc2 = f2(sc, sc);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -370,8 +403,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       part_done(idx);
     }
     cp_async_wait_all();
+    if (!FP8 && ok && lt == 0) {
+      look_at[looks % kLooks] = Look{-1, 0, 0};
+      mbar_arrive(&bars[cLook + looks % kLooks]);
+    }
     // (after a time-out: the TMA boxes in flight land before the CTA ends)
     if (!FP8 && *abort_flag && warp == 12) {
+      for (int i = max(looks - kLooks, 0); i < looks; ++i)
+        mbar_wait(&bars[cLook + i % kLooks], (i / kLooks) & 1, p.err, kDevErrTimeout, nullptr);
       for (int i = 0; i < L::kRing && i < it; ++i) {
         at.phase ^= at.slot == 0 ? 1u : 0u;
         at.slot = at.slot == 0 ? L::kRing - 1 : at.slot - 1;
@@ -464,6 +503,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       __syncwarp();
       if (one) umma_commit(&bars[cDrain]);
       mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
+    } else if (!FP8 && warp < 3) {
+      // ---------------------------------------------------------------- looking
+      constexpr int CPR = D / 8, RPP = 64 / CPR;
+      const int chunk = (tid - 32) % CPR, r0 = (tid - 32) / CPR;
+      // (rows eight apart have a column of pieces at equal distances)
+      for (int i = 0;; ++i) {
+        if (!wait(cLook + i % kLooks, (i / kLooks) & 1)) break;
+        const Look k = look_at[i % kLooks];
+        if (k.slot < 0) break;
+        Part& s = parts[k.part % kParts];
+        const SeenKeys seen = part_seen(s, p.sinks);
+        bool found = false;
+#pragma unroll 1
+        for (int r = r0; r < 8; r += RPP)
+          found |= mend_pieces<false>(smem_u32(sR) + k.slot * L::kTile + tile_off(r, chunk), 1024, 16, k.j0 + r, 8, seen);
+        if (found) s.odd = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars[cFull + k.slot]);
+          mbar_arrive(&bars[cFull + k.slot]);
+        }
+      }
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------------- walk
       for (int left = c.left, idx = 0;; ++idx) {
@@ -505,7 +567,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------- softmax
-    regs_increase<kRegsSoft>();
+    regs_increase<FP8 ? kRegsSoft8 : kRegsSoft>();
     const int w = (warp >> 2) - 1, quad = warp & 3, row = w * 128 + quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
@@ -523,9 +585,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int R = s.row0 + row, last = s.nq * p.G - 1;
         const int pos = s.pos0 + min(R, last) / p.G;
         const int rhi = p.causal ? pos + 1 : s.klen, rlo = p.window > 0 ? pos - p.window + 1 : 0;
+        const PartTiles tiles(s);
         float m = kNInf, l = 0.f;
         for (int k = 0; k < n; ++k, ++ns) {
-          const int j0 = part_key0(s, s.t0 + k);
+          const int j0 = tiles.key0(k);
           const int hi = rhi - j0, lo = rlo - j0, sk = p.sinks - j0;
           const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
           if (!(ok = wait(cSFull + w, ns & 1))) break;
@@ -621,14 +684,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + ocol + a * 32, o);
           tmem_ld_wait(o);
-          if (odd && real) {
-            const int mid = min(s.all_lo, s.hi), from = max(max(s.all_hi, s.lo), mid);
-#pragma unroll 1
-            for (int j = s.lo < mid ? s.lo : from; j < s.hi; j = j + 1 == mid ? from : j + 1)
-              if (const int kt = tile_of<kKeyTile>(s.sink_tiles, s.main0, j);
-                  kt >= s.t0 && kt < s.t0 + n && j < rhi && (j >= rlo || j < p.sinks))
-                add_odd_values<FP8, 32>(p, s.b, s.g, j, a * 32, reinterpret_cast<float*>(o));
-          }
           if (whole) {
             uint16_t* dst = p.out + (t * p.Hq + h) * p.c.d + a * 32;
 #pragma unroll
@@ -650,6 +705,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         tc_fence_before();
         mbar_arrive(&bars[cOFree + w]);
+        if (odd && real) {
+          const int mid = min(s.all_lo, s.hi);
+          const OddKeys k{s.b,  s.g,  s.lo, mid, max(max(s.all_hi, s.lo), mid), s.hi, s.sink_tiles, s.main0,
+                          s.t0, s.t0 + n - 1};
+          add_odd_values<FP8, kKeyTile>(p, k, rlo, rhi, 0, p.c.d, whole ? p.out + (t * p.Hq + h) * p.c.d : nullptr,
+                                        p.part_o + (pb * (D / 4) + row) * 4, ROWS * 4);
+        }
         if (whole) {
           if (real) p.lse[static_cast<int64_t>(h) * p.T + t] = l == 0.f ? kNInf : (m * cexp + log2f(l)) * kPLn2;
         } else {
