@@ -351,13 +351,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               Part& sp = parts[look_part % kParts];
               if (mend_pieces_apart<true>(src, 2048, CPR, look_j0 + r0, RPP, part_seen(sp, p.sinks))) sp.odd = 1;
             }
+            // (loads of four pieces together: one after the other, each waited for the last one's store)
 #pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-              uint4 x;
-              asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                           : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                           : "r"(src + i * 2048)
-                           : "memory");
+            for (int i4 = 0; i4 < CPR; i4 += 4) {
+             uint4 x4[4];
+#pragma unroll
+             for (int i = 0; i < 4; ++i)
+               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                            : "=r"(x4[i].x), "=r"(x4[i].y), "=r"(x4[i].z), "=r"(x4[i].w)
+                            : "r"(src + (i4 + i) * 2048)
+                            : "memory");
+#pragma unroll
+             for (int i = i4; i < i4 + 4; ++i) {
+              const uint4 x = x4[i - i4];
               const float sc = exp_scale(e_old[FP8 ? i : 0]);
               const uint64_t sc2 = f2(sc, sc);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -376,6 +382,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
                     make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+             }
             }
             announce(cFull + at.slot);
             at.step();
