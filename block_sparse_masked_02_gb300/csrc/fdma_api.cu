@@ -190,7 +190,7 @@ int classify_into_workspace(const fdma_args* a, int8_t* user_map, cudaStream_t s
 
 int* paged_error_word() { return device_error_word(); }
 
-bool paged_map(CUtensorMap* m, const void* base, int bytes_wide, int d, int page, int Hkv, int num_pages, const int64_t st[3],
+bool paged_map(CUtensorMap* m, const void* base, int d, int page, int Hkv, int num_pages, const int64_t st[3],
                int rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || base == nullptr) return false;
@@ -201,12 +201,10 @@ bool paged_map(CUtensorMap* m, const void* base, int bytes_wide, int d, int page
     if (gs[i] == 0 && gd[i + 1] > 1) return false;
     if (gs[i] == 0) gs[i] = 16;  // an axis of one element: any stride
   }
-  const bool raw = bytes_wide > 0;
-  const cuuint32_t box[4] = {raw ? static_cast<cuuint32_t>(bytes_wide) : 64u, static_cast<cuuint32_t>(rows), 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  return enc(m, raw ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, raw ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 WorkspaceLayout workspace_layout(int B, int Nq, int Nk, int Hq, int Hkv, int d) {

@@ -31,11 +31,8 @@ namespace {
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kChunkThreads = 512;
 constexpr int kKeyTile = 128;
-constexpr int kRingTiles = 5;  // K and V tiles in shared memory (e4m3: three, and kRawItems raw ones)
-constexpr int kRawItems = 4;
-constexpr int kLead = kRawItems - 1;  // turns between an item's copy and its conversion
+constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
-constexpr int kRefs = 8;   // tiles whose scale references are kept: more than the loads are ahead
 constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
 constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
 constexpr uint32_t kRegsLoad8 = 96, kRegsSoft8 = 176;  // e4m3: the conversion needs more
@@ -56,9 +53,7 @@ enum ChunkBar : int {
   cPart = cOFree + 2,     // + part slot: the part is published
   cPartFree = cPart + kParts,  // + part slot: every reader is done with it
   cLook = cPartFree + kParts,  // + entry: a V tile to be looked through has landed
-  cMax = cLook + kLooks,    // e4m3: the loading warps' maxima of a tile's scales
-  cRaw,                     // + place (e4m3): the raw item has landed
-  cDrain = cRaw + kRawItems,
+  cDrain = cLook + kLooks,
   kChunkBars
 };
 
@@ -123,22 +118,15 @@ struct RingPos {
 template <int D, bool FP8>
 struct ChunkSmem {
   static constexpr int kTile = 128 * D * 2;
-  static constexpr int kRing = FP8 ? 3 : kRingTiles;
+  static constexpr int kRing = FP8 ? 4 : kRingTiles;
   static constexpr int kOffRing = 2 * kTile;
-  static constexpr int kOffRaw = kOffRing + kRing * kTile;  // e4m3: [kRawItems] items as they lie in the cache
-  static constexpr int kOffBar = kOffRaw + (FP8 ? kRawItems * 64 * D * 2 : 0);
+  static constexpr int kOffRaw = kOffRing + kRing * kTile;  // e4m3: [2] items as they lie in the cache
+  static constexpr int kOffBar = kOffRaw + (FP8 ? kTile : 0);
   static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
   static constexpr int kOffParts = kOffMisc + 16;
   static constexpr int kOffLooks = kOffParts + kParts * static_cast<int>(sizeof(Part));
   static constexpr int kOffPlan = (kOffLooks + kLooks * static_cast<int>(sizeof(Look)) + 7) / 8 * 8;
-  // e4m3: [2][256] power of two of a row of Q, [kRefs] references of a tile's K and V scales, [2][4] their maxima
-  // by warp, [4][2][128] the tile's scale bytes
-  static constexpr int kOffFac = (kOffPlan + static_cast<int>(sizeof(PlanSmem)) + 7) / 8 * 8;
-  static constexpr int kOffRef = kOffFac + (FP8 ? 1024 : 0);
-  static constexpr int kOffMax = kOffRef + (FP8 ? kRefs * 8 : 0);
-  static constexpr int kOffExp = kOffMax + (FP8 ? 64 : 0);
-  static constexpr int kOffInfo = kOffExp + (FP8 ? 1024 : 0);  // [kRawItems] (first key to look from, part)
-  static constexpr int kTotal = kOffInfo + (FP8 ? kRawItems * 8 : 0);
+  static constexpr int kTotal = kOffPlan + static_cast<int>(sizeof(PlanSmem));
   static_assert(kTotal <= 232448, "shared memory of one CTA");
 };
 
@@ -149,8 +137,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   using L = ChunkSmem<D, FP8>;
   using Ring = RingPos<L::kRing>;
   constexpr int ROWS = kChunkRows;
-  constexpr uint32_t IDESC_S = FP8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
-  constexpr uint32_t IDESC_O = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
+  constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
+  constexpr uint32_t IDESC_O = idesc_bf16(128, D, false, true);
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
@@ -174,12 +162,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
     for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], 4);
     mbar_init(&bars[cQFull], 4);
-    mbar_init(&bars[cMax], 4);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
     for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], 128 + 1 + 256);
     misc[1] = 0;
-    misc[2] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -196,11 +182,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   Part* parts = reinterpret_cast<Part*>(smem + L::kOffParts);
   Look* look_at = reinterpret_cast<Look*>(smem + L::kOffLooks);
-  int16_t* row_up = reinterpret_cast<int16_t*>(smem + L::kOffFac);
-  uint8_t* tile_exp = smem + L::kOffExp;
-  int2* raw_info = reinterpret_cast<int2*>(smem + L::kOffInfo);
-  int2* refs = reinterpret_cast<int2*>(smem + L::kOffRef);
-  int2* ref_max = reinterpret_cast<int2*>(smem + L::kOffMax);
   // The idx-th part of the run; false on a time-out.
   auto part_ready = [&](int idx) { return wait(cPart + idx % kParts, (idx / kParts) & 1); };
   auto part_done = [&](int idx) { mbar_arrive(&bars[cPartFree + idx % kParts]); };
@@ -215,7 +196,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
     Ring at;     // the place of the next item
-    Ring prev;   // e4m3: of the item kRawItems before the next one
     int it = 0;  // items issued
     bool ok = true;
     // every thread of the warp has stored its part of what `bar` announces
@@ -229,12 +209,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = 128 / CPR;
     const int chunk = lt % CPR, r0 = lt / CPR;
     const uint32_t cb = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
-    // e4m3: two items as they lie in the cache; a thread converts rows r0 + i * RPP of a column of pieces
-    const uint32_t raw = smem_u32(smem) + L::kOffRaw;
-    constexpr int kRaw = 128 * D;
-    uint32_t e_k = 0, e_v = 0;         // scale bytes of row lt of the newest tile, as they come in
-    int kref[2] = {0, 0}, vref[2] = {0, 0}, tile = 0;  // the largest of the last two tiles'; tiles so far
+    // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
+    const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
+    uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
     int looks = 0;                                      // bf16: V tiles given to the looking warps
+    int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: the same, looked through here as they are converted
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
     // code fell out of the instruction cache and everything ran at half speed.)
     for (int idx = 0; ok; ++idx) {
@@ -256,33 +235,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       };
       int pg = -1, pg_next = look_up(0);
       bool missing = false;  // a page that is needed is not there
-      unsigned boxes = 0;
-      bool mine_box = false;
-      // (turns without loads at the end of the run, for the last raw items)
-      const int turns = n > 0 ? 2 * n : FP8 ? kLead : 0;
+      // (one turn without loads at the end of the run, for the last raw item)
+      const int turns = n > 0 ? 2 * n : FP8 ? 1 : 0;
 #pragma unroll 1
       for (int i2 = 0; i2 < turns; ++i2) {
-        if (FP8 && (i2 & 1)) {
-          kref[1] = kref[0];
-          vref[1] = vref[0];
-          if (n > 0) {
-            // the tile's scale bytes have come in during the last turn: to shared memory, and their maxima
-            uint8_t* te = tile_exp + (tile & 3) * 256;
-            te[lt] = static_cast<uint8_t>(e_k);
-            te[128 + lt] = static_cast<uint8_t>(e_v);
-            const uint32_t mk = __reduce_max_sync(0xffffffffu, e_k), mv = __reduce_max_sync(0xffffffffu, e_v);
-            __syncwarp();
-            int2* box = ref_max + (tile & 1) * 4;
-            if (lane == 0) {
-              box[warp - 12] = make_int2(static_cast<int>(mk), static_cast<int>(mv));
-              mbar_arrive(&bars[cMax]);
-            }
-            if (!(ok = wait(cMax, tile & 1))) break;
-            kref[0] = max(max(box[0].x, box[1].x), max(box[2].x, box[3].x));
-            vref[0] = max(max(box[0].y, box[1].y), max(box[2].y, box[3].y));
-            if (lt == 0) refs[tile % kRefs] = make_int2(kref[0], vref[0]);
-            ++tile;
-          }
+        if (FP8) {
+#pragma unroll
+          for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
+          look_j0 = look_next;
         }
         if (n > 0) {
           // ---- this item's rows
@@ -293,11 +253,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             pg = checked_page(p, entry);
             missing = __any_sync(0xffffffffu, entry != kNoKeys && pg < 0);
             pg_next = look_up((i2 >> 1) + 1);
-            // lane g brings the page of its group of 16 keys, if that group begins a box; the boxes are dealt
-            // out over the four warps (a warp's boxes go one after the other, some 150 cycles each)
-            const bool begins = lane < 8 && ((lane * 16) & (unit - 1)) == 0 && pg >= 0;
-            boxes = __ballot_sync(0xffffffffu, begins);
-            mine_box = begins && ((lane * 16 / unit) & 3) == warp - 12;
           }
           if (!FP8) {
             if (!(ok = slot_free(it))) break;
@@ -307,23 +262,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // unseen keys are replaced, whatever they are.)
             const bool look = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi);
             if (p.box > 0 && !missing) {
-              uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
-              if (lane == 0) {
-                if (warp == 12) {
+              if (warp == 12) {
+                // lane g brings the page of its group of 16 keys, if that group begins a box
+                const bool mine_box = lane < 8 && ((lane * 16) & (p.box - 1)) == 0 && pg >= 0;
+                const unsigned boxes = __ballot_sync(0xffffffffu, mine_box);
+                uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
+                if (lane == 0) {
                   if (look) look_at[looks % kLooks] = Look{at.slot, j0, idx};
                   mbar_arrive_expect_tx(to_bar, __popc(boxes) * p.box * (2 * D));
-                } else if (!look) {
-                  mbar_arrive(to_bar);
                 }
-              }
-              if (mine_box) {
-                const CUtensorMap* tm = is_v ? &tmV : &tmK;
+                __syncwarp();
+                if (mine_box) {
+                  const CUtensorMap* tm = is_v ? &tmV : &tmK;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                  tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
+                  for (int c = 0; c < D / 64; ++c)
+                    tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
+                }
+                looks += look;
+              } else if (lane == 0 && !look) {
+                mbar_arrive(&bars[bar]);
               }
-              __syncwarp();
-              looks += look;
             } else {
               const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
               const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
@@ -352,62 +310,46 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             }
             at.step();
           } else {
-            const int place = it % kRawItems;
-            // V of keys that not every row sees is looked through before it is converted
-            if (lt == 0) raw_info[place] = make_int2(is_v && !(j0 >= all_lo && j0 + 128 <= all_hi) ? j0 : -1, idx);
-            if (!is_v) {  // a tile's K turn also fetches the scale bytes of both, which the next turn needs
-              const int page = __shfl_sync(0xffffffffu, pg, lt >> 4), j = j0 + lt;
-              e_k = e_v = 0;
-              if (page >= 0 && (j < sink_hi || (j >= lo && j < hi))) {
-                const int64_t slot = j & pmask;
-                e_k = p.c.ke[page * p.c.kes[0] + slot * p.c.kes[1] + g_kv * p.c.kes[2]];
-                e_v = p.c.ve[page * p.c.ves[0] + slot * p.c.ves[1] + g_kv * p.c.ves[2]];
+            const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
+            const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
+            const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
+            const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
+            // every key of the tile is seen by some row and has a page
+            const bool all =
+                j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
+            const int64_t* es = is_v ? p.c.ves : p.c.kes;
+            const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + g_kv * es[2] + (r0 & 15) * es[1];
+            const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
+            const uint32_t dst = raw + (it & 1) * (CPR * 2048);
+            look_next = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi) ? j0 : -1;
+#pragma unroll
+            for (int i = 0; i < CPR; ++i) {
+              const int g = ((i * RPP) >> 4) + (RPP > 16 ? r0 >> 4 : 0);
+              const int64_t off = __shfl_sync(0xffffffffu, group, g), eoff = __shfl_sync(0xffffffffu, egroup, g);
+              bool in = true;
+              if (!all) {
+                const int j = j0 + i * RPP + r0;
+                in = __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
               }
+              cp_async16(dst + i * 2048, in ? mine + off : p.c.k, in ? cb : 0u);
+              e_new[FP8 ? i : 0] = 127;
+              if (in) e_new[FP8 ? i : 0] = efrom[eoff];
             }
-            if (p.box > 0 && !missing) {
-              // (the item that was there has been converted by all loading warps)
-              if (it >= kRawItems && !(ok = wait(cFull + prev.slot, prev.phase))) break;
-              if (lt == 0) mbar_arrive_expect_tx(&bars[cRaw + place], __popc(boxes) * p.box * D);
-              if (mine_box)
-                tma_load_4d(smem + L::kOffRaw + place * kRaw + lane * 16 * D, is_v ? &tmV : &tmK, &bars[cRaw + place], 0,
-                            (j0 + lane * 16) & pmask, g_kv, pg);
-              __syncwarp();
-            } else {
-              const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
-              const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
-              const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-              if (it >= kRawItems && !(ok = wait(cFull + prev.slot, prev.phase))) break;
-#pragma unroll 1
-              for (int r = r0; r < 128; r += RPP) {
-                const int64_t off = __shfl_sync(0xffffffffu, group, r >> 4);
-                const bool in = __shfl_sync(0xffffffffu, pg, r >> 4) >= 0 &&
-                                (j0 + r < sink_hi || (j0 + r >= lo && j0 + r < hi));
-                cp_async16(raw + place * kRaw + r * D + chunk * 16, in ? from + off + (r & 15) * st + chunk * 16 : p.c.k, in ? cb : 0u);
-              }
-              cp_async_wait_all();
-              fence_proxy_async_smem();
-              __syncwarp();
-              // (all four warps: the barrier counts one arrival, the last warp's)
-              __threadfence_block();
-              if (lane == 0 && atomicAdd(reinterpret_cast<int*>(misc + 2), 1) % 4 == 3) mbar_arrive(&bars[cRaw + place]);
-            }
-            if (it >= kRawItems) prev.step();
           }
           ++it;
+          if (FP8) cp_async_commit();
         }
         if (FP8) {
-          // ---- the item kLead before this turn's becomes f16
-          const int item = (n > 0 ? it - 1 : it + i2) - kLead;
-          if (item >= 0) {
-            const int place = item % kRawItems;
-            if (!(ok = slot_free(item) && wait(cRaw + place, (item / kRawItems) & 1))) break;
-            const uint32_t src = raw + place * kRaw + r0 * D + chunk * 16;
-            // (in a V turn that is the last tile's K, in a K turn the V of the tile before that)
-            const uint8_t* eb = tile_exp + ((item >> 1) & 3) * 256 + (item & 1) * 128 + r0;
-            const int ref = item & 1 ? vref[1] : kref[1];
-            if (const int2 look = raw_info[place]; look.x >= 0) {
-              Part& sp = parts[look.y % kParts];
-              if (mend_pieces_apart<true>(src, RPP * D, CPR, look.x + r0, RPP, part_seen(sp, p.sinks))) sp.odd = 1;
+          // ---- the item before becomes bf16
+          const int item = n > 0 ? it - 2 : it - 1;
+          if (n > 0) cp_async_wait<1>();
+          else cp_async_wait_all();
+          if (item >= 0 && (n > 0 || it > 0)) {
+            if (!(ok = slot_free(item))) break;
+            const uint32_t src = raw + (item & 1) * (CPR * 2048);
+            if (look_j0 >= 0) {
+              Part& sp = parts[look_part % kParts];
+              if (mend_pieces_apart<true>(src, 2048, CPR, look_j0 + r0, RPP, part_seen(sp, p.sinks))) sp.odd = 1;
             }
             // (loads of four pieces together: one after the other, each waited for the last one's store)
 #pragma unroll
@@ -417,19 +359,25 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
              for (int i = 0; i < 4; ++i)
                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                             : "=r"(x4[i].x), "=r"(x4[i].y), "=r"(x4[i].z), "=r"(x4[i].w)
-                            : "r"(src + (i4 + i) * RPP * D)
+                            : "r"(src + (i4 + i) * 2048)
                             : "memory");
 #pragma unroll
              for (int i = i4; i < i4 + 4; ++i) {
               const uint4 x = x4[i - i4];
-              // code * 2^(e - ref) in f16: exact down to 2^-14 of the tile's largest scale, nothing below 2^-24
-              const int down = ref - static_cast<int>(eb[i * RPP]);
-              const uint32_t by = (down <= 14 ? (15 - down) << 10 : down <= 24 ? 1 << (24 - down) : 0) * 0x00010001u;
+              const float sc = exp_scale(e_old[FP8 ? i : 0]);
+              const uint64_t sc2 = f2(sc, sc);
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               uint32_t o[8];
 #pragma unroll
-              for (int h = 0; h < 8; ++h)
-                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(o[h]) : "r"(e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)))), "r"(by));
+              for (int h = 0; h < 8; ++h) {
+                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+                float a, c;
+                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                    : "=f"(a), "=f"(c)
+                    : "r"(f));
+                f2split(mul2(f2(a, c), sc2), a, c);
+                o[h] = pack_bf16x2(a, c);
+              }
 #pragma unroll
               for (int h = 0; h < 2; ++h)
                 *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
@@ -439,48 +387,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             announce(cFull + at.slot);
             at.step();
           }
+          look_part = idx;
         }
         // ---- the part's Q, behind its first loads
-        if (n > 0 && i2 == 1) {
+        if (n > 0 && i2 == (FP8 ? 0 : 1)) {
           if (idx > 0 && !(ok = wait(cQEmpty, (idx - 1) & 1))) break;
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
           const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
-          // row row0 + r is (token, head) number first + r from the token of row0: a small number, so
-          // the quotient by the group's size comes from one fp32 product (exact below 2^20)
-          const int tok0 = row0 / p.G, first = row0 - tok0 * p.G;
-          const float by_g = 1.f / static_cast<float>(p.G);
-#pragma unroll 4
+#pragma unroll 2
           for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
-            const int x = first + r, i = p.G < 4096 ? static_cast<int>((static_cast<float>(x) + 0.5f) * by_g) : x / p.G;
+            const int R = row0 + r, i = R / p.G;
             const uint32_t nb = r < rows ? qb : 0u;
             cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
-                       nb ? p.q + (q0 + tok0 + i) * p.q_t + (h0 + x - i * p.G) * p.q_h + qc * 8 : p.q, nb);
+                       nb ? p.q + (q0 + i) * p.q_t + (h0 + R - i * p.G) * p.q_h + qc * 8 : p.q, nb);
           }
           cp_async_wait_all();
-          if (FP8) {
-            // to f16: each row times the power of two that brings its largest part to [2^14, 2^15)
-#pragma unroll 4
-            for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
-              uint4* at_q = reinterpret_cast<uint4*>(sQ + (r >> 7) * L::kTile + tile_off(r & 127, qc));
-              const uint4 v = *at_q;
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, top = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-#pragma unroll
-              for (int o = QCPR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-              const int E = static_cast<int>(top >> 7), up = E == 0 || E == 255 ? 0 : 14 + 127 - E;
-              const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up / 2) << 23);
-              const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(w[e] << 16) * f1 * f2, c = __uint_as_float(w[e] & 0xffff0000u) * f1 * f2;
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(c), "f"(a));
-              }
-              *at_q = make_uint4(w[0], w[1], w[2], w[3]);
-              if (qc == 0) row_up[(idx & 1) * 256 + r] = static_cast<int16_t>(up);
-            }
-          }
           announce(cQFull);
         }
       }
@@ -492,9 +414,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       look_at[looks % kLooks] = Look{-1, 0, 0};
       mbar_arrive(&bars[cLook + looks % kLooks]);
     }
-    if (FP8 && *abort_flag && warp == 12)
-      for (int i = max(it - kRawItems, 0); i < it; ++i)
-        mbar_wait(&bars[cRaw + i % kRawItems], (i / kRawItems) & 1, p.err, kDevErrTimeout, nullptr);
     // (after a time-out: the TMA boxes in flight land before the CTA ends)
     if (!FP8 && *abort_flag && warp == 12) {
       for (int i = max(looks - kLooks, 0); i < looks; ++i)
@@ -659,9 +578,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int w = (warp >> 2) - 1, quad = warp & 3, row = w * 128 + quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
-    float cexp = p.scale_log2;
+    const float cexp = p.scale_log2;
+    const uint64_t c2 = f2(cexp, cexp);
     int ns = 0, ended = 0;  // S tiles and parts of this slot so far
-    int tile = 0;           // e4m3: tiles of all parts so far
     bool ok = true;
     for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
@@ -675,7 +594,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int rhi = p.causal ? pos + 1 : s.klen, rlo = p.window > 0 ? pos - p.window + 1 : 0;
         const PartTiles tiles(s);
         float m = kNInf, l = 0.f;
-        int vref = 0;  // e4m3: O is in units of 2^(vref - 127 - 7)
         for (int k = 0; k < n; ++k, ++ns) {
           const int j0 = tiles.key0(k);
           const int hi = rhi - j0, lo = rlo - j0, sk = p.sinks - j0;
@@ -710,35 +628,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                   : "+f"(mx4[a])
                   : "f"(__uint_as_float(x[a][e])), "f"(__uint_as_float(x[a][e + 1])));
           }
-          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          float alpha = 1.f, ct = cexp, shift = 0.f, back = 1.f;
-          if (FP8) {
-            // scores are in units of the tile's K reference, weights leave in units of its V reference
-            const int2 ref = refs[(tile + k) % kRefs];
-            if (k == 0) {
-              const int up = row_up[(idx & 1) * 256 + row];  // scale * log2(e) * 2^-up, in two steps of normal numbers
-              cexp = fmaxf(p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up / 2) << 23) *
-                               __uint_as_float(static_cast<uint32_t>(127 - (up - up / 2)) << 23),
-                           1e-37f);
-              vref = ref.y;
-            }
-            // (below 2^-87 every score is 0 all the same; a factor of 0 would make NaN of -inf)
-            const float kf = exp_scale(max(ref.x, 40));
-            mx *= kf;
-            ct = fmaxf(cexp * kf, 1e-37f);
-            if (ref.y > vref) {
-              alpha = __uint_as_float(static_cast<uint32_t>(max(127 + vref - ref.y, 0)) << 23);
-              vref = ref.y;
-            }
-            const int by = max(7 + ref.y - vref, -60);
-            shift = static_cast<float>(by);
-            back = __uint_as_float(static_cast<uint32_t>(127 - by) << 23);
-          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float mn = fmaxf(m, mx);
+          float alpha = 1.f;
           if ((mn - m) * cexp > kRaise) {  // (also from -inf)
-            const float a = m == kNInf ? 0.f : paged_ex2((m - mn) * cexp);
-            alpha *= a;
-            l *= a;
+            alpha = m == kNInf ? 0.f : paged_ex2((m - mn) * cexp);
+            l *= alpha;
             m = mn;
           }
           if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -754,8 +649,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tmem_st16(tl + ocol + a * 16, o16);
             }
           }
-          const float nm = (m == kNInf ? 0.f : -(m * cexp)) + shift;
-          const uint64_t nm2 = f2(nm, nm), c2 = f2(ct, ct);
+          const float nm = m == kNInf ? 0.f : -(m * cexp);
+          const uint64_t nm2 = f2(nm, nm);
           uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
@@ -767,8 +662,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               e0 = paged_ex2(e0);
               e1 = paged_ex2(e1);
               sum[e & 1] = add2(sum[e & 1], f2(e0, e1));
-              if (FP8) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e]) : "f"(e1), "f"(e0));
-              else pk[e] = pack_bf16x2(e0, e1);
+              pk[e] = pack_bf16x2(e0, e1);
             }
             tmem_st16(tl + scol + a * 16, pk);
             if (a & 1) {  // keys 0..63, then 64..127
@@ -779,7 +673,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           float s0, s1;
           f2split(add2(sum[0], sum[1]), s0, s1);
-          l += (s0 + s1) * back;
+          l += s0 + s1;
         }
         if (!ok) break;
         // ---- the part's end
@@ -788,11 +682,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
         const bool real = R <= last, whole = s.whole, odd = *const_cast<volatile int*>(&s.odd) != 0;
         const int tok = real ? R / p.G : 0;
-        // (e4m3: O's unit as two factors, both normal numbers)
-        const int u = vref - 134, u1 = u / 2;
-        const float unit1 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u1) << 23) : 1.f;
-        const float unit2 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u - u1) << 23) : 1.f;
-        const float inv = (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) * unit1;
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
         const int64_t pb = (static_cast<int64_t>(blockIdx.x) * 2 + s.slot) * ROWS;
         const int h = s.g * p.G + R - tok * p.G;
         const int64_t t = s.q0 + tok;
@@ -801,11 +691,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           uint32_t o[32];
           tmem_ld32(tl + ocol + a * 32, o);
           tmem_ld_wait(o);
-          if (FP8) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              o[e] = __float_as_uint(__uint_as_float(o[e]) * (whole ? unit2 : unit1 * unit2));
-          }
           if (whole) {
             uint16_t* dst = p.out + (t * p.Hq + h) * p.c.d + a * 32;
 #pragma unroll
@@ -840,7 +725,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           p.part_ml[pb + row] = make_float2(m == kNInf ? m : m * cexp, l);
         }
       }
-      tile += n;
       part_done(idx);
     }
   }
@@ -863,8 +747,8 @@ cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
   CUtensorMap tk{}, tv{};
   const int page = 1 << p.c.page_shift, rows = page < 128 ? page : 128;
   // (a cache that broadcasts an axis with stride 0 goes by cp.async)
-  p.box = paged_map(&tk, p.c.k, FP8 ? D : 0, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.ks, rows) &&
-                  paged_map(&tv, p.c.v, FP8 ? D : 0, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, rows)
+  p.box = !FP8 && paged_map(&tk, p.c.k, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.ks, rows) &&
+                  paged_map(&tv, p.c.v, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, rows)
               ? rows
               : 0;
   kern<<<kPagedCtas, kChunkThreads, L::kTotal, stream>>>(tk, tv, p);
