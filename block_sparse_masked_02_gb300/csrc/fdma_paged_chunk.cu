@@ -235,6 +235,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       };
       int pg = -1, pg_next = look_up(0);
       bool missing = false;  // a page that is needed is not there
+      unsigned boxes = 0;
+      bool mine_box = false;
       // (one turn without loads at the end of the run, for the last raw item)
       const int turns = n > 0 ? 2 * n : FP8 ? 1 : 0;
 #pragma unroll 1
@@ -253,6 +255,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             pg = checked_page(p, entry);
             missing = __any_sync(0xffffffffu, entry != kNoKeys && pg < 0);
             pg_next = look_up((i2 >> 1) + 1);
+            // lane g brings the page of its group of 16 keys, if that group begins a box; the boxes are dealt
+            // out over the four warps (a warp's boxes go one after the other)
+            const bool begins = lane < 8 && ((lane * 16) & (unit - 1)) == 0 && pg >= 0;
+            boxes = __ballot_sync(0xffffffffu, begins);
+            mine_box = begins && ((lane * 16 / unit) & 3) == warp - 12;
           }
           if (!FP8) {
             if (!(ok = slot_free(it))) break;
@@ -262,26 +269,23 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             // unseen keys are replaced, whatever they are.)
             const bool look = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi);
             if (p.box > 0 && !missing) {
-              if (warp == 12) {
-                // lane g brings the page of its group of 16 keys, if that group begins a box
-                const bool mine_box = lane < 8 && ((lane * 16) & (p.box - 1)) == 0 && pg >= 0;
-                const unsigned boxes = __ballot_sync(0xffffffffu, mine_box);
-                uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
-                if (lane == 0) {
+              uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
+              if (lane == 0) {
+                if (warp == 12) {
                   if (look) look_at[looks % kLooks] = Look{at.slot, j0, idx};
                   mbar_arrive_expect_tx(to_bar, __popc(boxes) * p.box * (2 * D));
+                } else if (!look) {
+                  mbar_arrive(to_bar);
                 }
-                __syncwarp();
-                if (mine_box) {
-                  const CUtensorMap* tm = is_v ? &tmV : &tmK;
-#pragma unroll
-                  for (int c = 0; c < D / 64; ++c)
-                    tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
-                }
-                looks += look;
-              } else if (lane == 0 && !look) {
-                mbar_arrive(&bars[bar]);
               }
+              if (mine_box) {
+                const CUtensorMap* tm = is_v ? &tmV : &tmK;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
+              }
+              __syncwarp();
+              looks += look;
             } else {
               const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
               const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
@@ -395,12 +399,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
           const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
-#pragma unroll 2
+          // row row0 + r is (token, head) number first + r from the token of row0: a small number, so
+          // the quotient by the group's size comes from one fp32 product (exact: checked for every
+          // group size below 4096)
+          const int tok0 = row0 / p.G, first = row0 - tok0 * p.G;
+          const float by_g = 1.f / static_cast<float>(p.G);
+#pragma unroll 4
           for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
-            const int R = row0 + r, i = R / p.G;
+            const int x = first + r, i = p.G < 4096 ? static_cast<int>((static_cast<float>(x) + 0.5f) * by_g) : x / p.G;
             const uint32_t nb = r < rows ? qb : 0u;
             cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
-                       nb ? p.q + (q0 + i) * p.q_t + (h0 + R - i * p.G) * p.q_h + qc * 8 : p.q, nb);
+                       nb ? p.q + (q0 + tok0 + i) * p.q_t + (h0 + x - i * p.G) * p.q_h + qc * 8 : p.q, nb);
           }
           cp_async_wait_all();
           announce(cQFull);
