@@ -38,6 +38,7 @@ constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
 constexpr uint32_t kRegsLoad8 = 96, kRegsSoft8 = 176;  // e4m3: the conversion needs more
 constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
 static_assert(kRegsMma + kRegsLoad8 + 2 * kRegsSoft8 == 4 * kChunkLaunchRegs, "the registers of the launch");
+constexpr uint64_t kIdleWaitNs = 300ull * kWaitLimitNs;
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
 
@@ -179,6 +180,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   uint8_t* sQ = smem;
   uint8_t* sR = smem + L::kOffRing;
   auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag); };
+
+  // For the roles that have nothing to do for most of a run, however long it is; a time-out of
+  // another role ends these waits too.
+  auto idle_wait = [&](int bar, uint32_t parity) {
+    return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag, kIdleWaitNs);
+  };
 
   Part* parts = reinterpret_cast<Part*>(smem + L::kOffParts);
   Look* look_at = reinterpret_cast<Look*>(smem + L::kOffLooks);
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int chunk = (tid - 32) % CPR, r0 = (tid - 32) / CPR;
       // (rows eight apart have a column of pieces at equal distances)
       for (int i = 0;; ++i) {
-        if (!wait(cLook + i % kLooks, (i / kLooks) & 1)) break;
+        if (!idle_wait(cLook + i % kLooks, (i / kLooks) & 1)) break;
         const Look k = look_at[i % kLooks];
         if (k.slot < 0) break;
         Part& s = parts[k.part % kParts];
@@ -545,7 +552,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     } else if (warp == 3 && lane == 0) {
       // ---------------------------------------------------------------- walk
       for (int left = c.left, idx = 0;; ++idx) {
-        if (idx >= kParts && !wait(cPartFree + idx % kParts, (idx / kParts - 1) & 1)) break;
+        if (idx >= kParts && !idle_wait(cPartFree + idx % kParts, (idx / kParts - 1) & 1)) break;
         Part& s = parts[idx % kParts];
         s.n = max(min(c.r.tiles - c.t, left), 0);
         if (left > 0) {

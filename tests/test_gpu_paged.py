@@ -10,6 +10,8 @@ w = 2^-22 * (8 + d * D) for both numerator and denominator, every output element
     2^-8 |out|  +  (u + 2 w) * A,      A = sum_j P_j |v_j|,
 and lse by at most w + 2^-22 |lse|.  Quantised rows and rows read back are exact.
 """
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -257,6 +259,33 @@ def test_attention_matches_the_oracle(P, case, fp8):
     s = Setup(P, lens, Hkv, d, page, fp8, layout, seed=sum(lens) + d)
     q = _queries(sum(news), Hq, d)
     out, lse = P.fwd(q, *s.at, _cu(news), max(news), window=window, sinks=sinks, causal=causal, **s.ex)
+    _check_attention(s, q, news, out, lse, causal, window, sinks)
+
+
+@pytest.mark.parametrize("seed", range(int(os.environ.get("FDMA_PAGED_FUZZ", "30"))))
+def test_random_batches_match_the_oracle(P, seed):
+    """Seeded draws over batch, lengths, heads, head dims, page sizes, layouts, types, windows and sinks:
+    the rows are read back, then attended to (FDMA_PAGED_FUZZ=n draws n batches)."""
+    g = np.random.default_rng(1000 + seed)
+    fp8 = bool(g.integers(2))
+    B, Hkv = int(g.integers(1, 6)), int(g.choice([1, 2, 3, 5]))
+    G = int(g.choice([1, 2, 3, 4, 7, 8, 13]))
+    d = int(g.choice([16, 32, 48, 64, 80, 96, 112, 128, 128])) if fp8 else int(g.choice([8, 24, 64, 72, 104, 120, 128, 128]))
+    page, layout = int(g.choice([16, 32, 64, 128, 512])), str(g.choice(["head", "token"]))
+    if layout == "token" and d % 16:
+        d += 8
+    most = int(g.choice([1, 1, 4, 20, 90, 300]))
+    news = [int(n) for n in g.integers(0, most + 1, B)]
+    news[int(g.integers(B))] = most
+    lens = [int(n + k) for n, k in zip(news, g.integers(0, int(g.choice([1, 40, 300, 1500])), B))]
+    causal = bool(g.random() < 0.85)
+    window = int(g.integers(1, 400)) if causal and g.random() < 0.5 else 0
+    sinks = int(g.choice([0, 1, 5, 130, 200]))
+    s = Setup(P, lens, Hkv, d, page, fp8, layout, seed=seed)
+    k, v = P.kv_gather(*s.at, _cu(lens), sum(lens), **s.ex)
+    assert np.array_equal(_np(k), np.concatenate(s.K)) and np.array_equal(_np(v), np.concatenate(s.V))
+    q = _queries(sum(news), Hkv * G, d, seed)
+    out, lse = P.fwd(q, *s.at, _cu(news), most, window=window, sinks=sinks, causal=causal, **s.ex)
     _check_attention(s, q, news, out, lse, causal, window, sinks)
 
 
