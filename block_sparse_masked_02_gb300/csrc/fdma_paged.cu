@@ -33,7 +33,10 @@ namespace fdma {
 
 namespace {
 
-constexpr int kTokenRows = 24;  // packed rows up to which the token kernel runs
+// Packed rows up to which the token kernel runs.  With 17 to 24 rows (8 kv heads, d 128) of 16
+// sequences of 4096 keys it took 69 us and the chunk kernel 59 (e4m3: 81 and 77; of one sequence of
+// 32768 keys 41 and 41, e4m3 42 and 46), with 9 to 16 rows 57 and 59 (e4m3 54 and 76).
+constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -723,8 +726,7 @@ template <int D, bool FP8>
 cudaError_t launch_token_rows(const PagedParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.G;
   if (rows <= 8) return launch_token<D, FP8, 1>(p, stream);
-  if (rows <= 16) return launch_token<D, FP8, 2>(p, stream);
-  return launch_token<D, FP8, 3>(p, stream);
+  return launch_token<D, FP8, 2>(p, stream);
 }
 
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -737,7 +739,7 @@ struct PagedLayout {
 // Rows of an item: the next multiple of eight on the token kernel, else the chunk kernel's.
 int item_rows(const fdma_paged_args* a) {
   const int64_t rows = static_cast<int64_t>(a->max_q) * (a->Hq / a->cache.Hkv);
-  return rows <= kTokenRows ? (rows <= 8 ? 8 : static_cast<int>((rows + 7) / 8 * 8)) : kChunkItemRows;
+  return rows <= 8 ? 8 : rows <= kTokenRows ? kTokenRows : kChunkItemRows;
 }
 
 PagedLayout paged_layout(const fdma_paged_args* a) {

@@ -180,7 +180,7 @@ __device__ __forceinline__ int seq_places(const PagedParams& p, const Seq& s) {
 }
 
 struct PlanSmem {
-  int64_t warp_sum[16];
+  int64_t warp_sum[32];
   int64_t total;
   int b, g, rt, t;
 };
@@ -330,17 +330,17 @@ struct SeenKeys {
   int lo, hi, sink_hi, all_lo, all_hi, sinks;
 };
 
-// Clears them in `count` (a multiple of four) 16-byte pieces of shared memory, `step` bytes and `dj` keys
+// Clears them in `count` (a multiple of N) 16-byte pieces of shared memory, `step` bytes and `dj` keys
 // apart, of keys that not every row sees, and zeroes those of keys that no row sees; true if values
 // were cleared that some row sees.
-template <bool FP8>
+template <bool FP8, int N = 4>
 __device__ __forceinline__ bool mend_pieces(uint32_t at, int step, int count, int j, int dj, const SeenKeys s) {
   bool found = false;
 #pragma unroll 1
-  for (int i = 0; i < count; i += 4, at += 4 * step, j += 4 * dj) {
-    uint32_t v[4][4], sum[4];
+  for (int i = 0; i < count; i += N, at += N * step, j += N * dj) {
+    uint32_t v[N][4], sum[N];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {  // (count is a multiple of four)
+    for (int e = 0; e < N; ++e) {
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                    : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3])
                    : "r"(at + e * step)
@@ -348,7 +348,7 @@ __device__ __forceinline__ bool mend_pieces(uint32_t at, int step, int count, in
     }
     uint32_t any = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < N; ++e) {
       sum[e] = 0;
       // an exponent (a code) of all ones carries into the sign bit's place
 #pragma unroll
@@ -366,7 +366,7 @@ __device__ __forceinline__ bool mend_pieces(uint32_t at, int step, int count, in
     if (any == 0) continue;
     found |= any > 1u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < N; ++e) {
       if (sum[e] == 0) continue;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
@@ -381,9 +381,9 @@ __device__ __forceinline__ bool mend_pieces(uint32_t at, int step, int count, in
   return found;
 }
 
-template <bool FP8>
+template <bool FP8, int N = 4>
 __device__ __noinline__ bool mend_pieces_apart(uint32_t at, int step, int count, int j, int dj, const SeenKeys s) {
-  return mend_pieces<FP8>(at, step, count, j, dj, s);
+  return mend_pieces<FP8, N>(at, step, count, j, dj, s);
 }
 
 // What a row adds: keys lo .. hi-1 but those between mid and from, in the tiles t0 .. t1 of KT keys.

@@ -5,7 +5,7 @@
 // slots of 128 rows that share every K and V tile.  With 2 * 128 rows a tile of 128 keys costs
 // 4 * 128 * 128 * d multiply-adds, 2048 cycles of the tensor pipe at d = 128, against about 1400
 // cycles for its K and V from HBM and less from L2: the products bound it, so everything
-// else is arranged to keep them fed.  One CTA an SM, 16 warps:
+// else is arranged to keep them fed.  One CTA an SM, 16 warps (20 with an e4m3 cache):
 //   warp 0          issues tcgen05.mma: S_w = Q_w K^T into TMEM, then O_w += P_w V with P_w read
 //                   from TMEM over the columns of S_w; the order PV0, S0, PV1, S1 lets each slot's
 //                   softmax run under the other slot's products;
@@ -15,12 +15,13 @@
 //   warps 1 and 2   look through the V tiles (by TMA) whose keys not every row sees: rows that nobody
 //                   sees become zeros, values that are not finite are cleared (fdma_paged.cuh);
 //                   the loads stay ahead meanwhile;
-//   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: S is read from TMEM once,
-//   warps 8..11     masked only in tiles that some row of the warp sees in part, exponentiated
-//                   with a running maximum that is raised only when it grows by 2^8 or more;
-//   warps 12..15    bring Q, K and V: page by page with cp.async into 128-byte-swizzled tiles
-//                   (a ring of five), keys that no row of the item sees as zeros; e4m3 rows are copied
-//                   raw, then multiplied by their scale and stored as bf16 (exact).
+//   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: masked only in tiles that some
+//   warps 8..11     row of the warp sees in part, exponentiated with a running maximum that is
+//                   raised only when it grows by 2^8 or more;
+//   warps 12..      bring Q, K and V into 128-byte-swizzled tiles: a ring of five bf16 tiles by TMA, a
+//                   box a page, or by cp.async where TMA cannot address the cache's layout or a page
+//                   is not there; of an e4m3 cache (a ring of four and two raw ones) the codes by
+//                   cp.async, which are then multiplied by their scale and stored as bf16 (exact).
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 #include "fdma_paged.cuh"
@@ -29,15 +30,22 @@ namespace fdma {
 namespace {
 
 constexpr int kChunkRows = kChunkItemRows;
-constexpr int kChunkThreads = 512;
 constexpr int kKeyTile = 128;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
 constexpr int kParts = 4;  // published parts
 constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
-constexpr uint32_t kRegsMma = 64, kRegsLoad = 80, kRegsSoft = 184;
-constexpr uint32_t kRegsLoad8 = 96, kRegsSoft8 = 176;  // e4m3: the conversion needs more
-constexpr int kChunkLaunchRegs = (kRegsMma + kRegsLoad + 2 * kRegsSoft) / 4;  // 128
-static_assert(kRegsMma + kRegsLoad8 + 2 * kRegsSoft8 == 4 * kChunkLaunchRegs, "the registers of the launch");
+// Loading warps and the division of the registers (setmaxnreg).  An e4m3 cache has eight loading warps,
+// because the conversion of its tiles to bf16 bounds it, and the softmax keeps less in registers for
+// it: two chunks of 333 to 1024 tokens over 4097 to 8192 keys, 32 heads, took 158 us with four warps, 133 with eight.
+template <bool FP8>
+struct ChunkRoles {
+  static constexpr int kLoadWarps = FP8 ? 8 : 4;
+  static constexpr int kThreads = 384 + 32 * kLoadWarps;
+  static constexpr uint32_t kRegsMma = 64, kRegsLoad = FP8 ? 96 : 80, kRegsSoft = FP8 ? 112 : 184;
+  static constexpr int kLaunchRegs = FP8 ? 96 : 128;
+  static_assert(kRegsMma + kRegsLoad * (kLoadWarps / 4) + 2 * kRegsSoft == kLaunchRegs * (kThreads / 128),
+                "the registers of the launch");
+};
 constexpr uint64_t kIdleWaitNs = 300ull * kWaitLimitNs;
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kRaise = 8.f;  // log2 units: P stays at most 2^8 between raises of the maximum
@@ -132,10 +140,12 @@ struct ChunkSmem {
 };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kChunkThreads, 1)
+__global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ PagedParams p) {
   using L = ChunkSmem<D, FP8>;
+  using Roles = ChunkRoles<FP8>;
+  constexpr int LT = 32 * Roles::kLoadWarps;  // loading threads
   using Ring = RingPos<L::kRing>;
   constexpr int ROWS = kChunkRows;
   constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
@@ -153,7 +163,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   Cursor<ROWS, kKeyTile> c;
   int quota;
-  const bool any = plan_run<ROWS, kKeyTile, kChunkThreads>(p, plan, c, quota);
+  const bool any = plan_run<ROWS, kKeyTile, Roles::kThreads>(p, plan, c, quota);
   if (tid == 0) p.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
   write_empty_blocks<ROWS>(p);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -161,11 +171,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kChunkBars; ++i) mbar_init(&bars[i], 1);
-    for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], 4);
-    mbar_init(&bars[cQFull], 4);
+    for (int i = 0; i < kRingTiles; ++i) mbar_init(&bars[cFull + i], Roles::kLoadWarps);
+    mbar_init(&bars[cQFull], Roles::kLoadWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
-    for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], 128 + 1 + 256);
+    for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], LT + 1 + 256);
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -196,10 +206,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (warp >= 12) {
     // ------------------------------------------------------------------ loads
     // Items (K_0, V_0, K_1, V_1, ... of every part in turn) are brought ahead of the products as far
-    // as the ring goes, across parts.  bf16 tiles that are seen whole come by TMA, a box a page;
-    // tiles with keys that no row sees (and layouts that TMA cannot address) by cp.async, which
-    // fills those with zeros.
-    regs_decrease<FP8 ? kRegsLoad8 : kRegsLoad>();
+    // as the ring goes, across parts.
+    regs_decrease<Roles::kRegsLoad>();
     const int lt = tid - 384;
     const int pmask = (1 << p.c.page_shift) - 1;
     Ring at;     // the place of the next item
@@ -212,13 +220,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto slot_free = [&](int item) { return item < L::kRing || wait(cEmpty + at.slot, at.phase ^ 1); };
-    // A thread copies one 16-byte column (of the cache's row) of rows i * RPP + lt / CPR.
-    constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = 128 / CPR;
+    // A thread copies one 16-byte column (of the cache's row) of NP rows i * RPP + lt / CPR.
+    constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = LT / CPR, NP = 128 / RPP, NB = NP < 4 ? NP : 4;
     const int chunk = lt % CPR, r0 = lt / CPR;
     const uint32_t cb = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
     // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
+    // (piece i of item x at (x & 1) * 128 * D + i * LT * 16)
     const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
-    uint32_t e_old[FP8 ? CPR : 1], e_new[FP8 ? CPR : 1];
+    uint32_t e_old[FP8 ? NP : 1], e_new[FP8 ? NP : 1];
     int looks = 0;                                      // bf16: V tiles given to the looking warps
     int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: the same, looked through here as they are converted
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
@@ -250,7 +259,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int i2 = 0; i2 < turns; ++i2) {
         if (FP8) {
 #pragma unroll
-          for (int i = 0; i < CPR; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
+          for (int i = 0; i < NP; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
           look_j0 = look_next;
         }
         if (n > 0) {
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                 }
               }
               cp_async_wait_all();
-              if (look && mend_pieces_apart<false>(smem_u32(to) + tile_off(r0, chunk), RPP * 128, CPR, j0 + r0, RPP,
+              if (look && mend_pieces_apart<false>(smem_u32(to) + tile_off(r0, chunk), RPP * 128, NP, j0 + r0, RPP,
                                              part_seen(s, p.sinks)))
                 s.odd = 1;
               announce(bar);
@@ -331,18 +340,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int64_t* es = is_v ? p.c.ves : p.c.kes;
             const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + g_kv * es[2] + (r0 & 15) * es[1];
             const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
-            const uint32_t dst = raw + (it & 1) * (CPR * 2048);
+            const uint32_t dst = raw + (it & 1) * (128 * D);
             look_next = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi) ? j0 : -1;
 #pragma unroll
-            for (int i = 0; i < CPR; ++i) {
-              const int g = ((i * RPP) >> 4) + (RPP > 16 ? r0 >> 4 : 0);
+            for (int i = 0; i < NP; ++i) {
+              const int g = ((i * RPP) >> 4) + (r0 >> 4);
               const int64_t off = __shfl_sync(0xffffffffu, group, g), eoff = __shfl_sync(0xffffffffu, egroup, g);
               bool in = true;
               if (!all) {
                 const int j = j0 + i * RPP + r0;
                 in = __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
               }
-              cp_async16(dst + i * 2048, in ? mine + off : p.c.k, in ? cb : 0u);
+              cp_async16(dst + i * (LT * 16), in ? mine + off : p.c.k, in ? cb : 0u);
               e_new[FP8 ? i : 0] = 127;
               if (in) e_new[FP8 ? i : 0] = efrom[eoff];
             }
@@ -357,43 +366,44 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           else cp_async_wait_all();
           if (item >= 0 && (n > 0 || it > 0)) {
             if (!(ok = slot_free(item))) break;
-            const uint32_t src = raw + (item & 1) * (CPR * 2048);
+            const uint32_t src = raw + (item & 1) * (128 * D);
             if (look_j0 >= 0) {
               Part& sp = parts[look_part % kParts];
-              if (mend_pieces_apart<true>(src, 2048, CPR, look_j0 + r0, RPP, part_seen(sp, p.sinks))) sp.odd = 1;
+              if (mend_pieces_apart<true, NB>(src, LT * 16, NP, look_j0 + r0, RPP, part_seen(sp, p.sinks)))
+                sp.odd = 1;
             }
             // (loads of four pieces together: one after the other, each waited for the last one's store)
 #pragma unroll
-            for (int i4 = 0; i4 < CPR; i4 += 4) {
-             uint4 x4[4];
+            for (int i4 = 0; i4 < NP; i4 += NB) {
+              uint4 x4[NB];
 #pragma unroll
-             for (int i = 0; i < 4; ++i)
-               asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                            : "=r"(x4[i].x), "=r"(x4[i].y), "=r"(x4[i].z), "=r"(x4[i].w)
-                            : "r"(src + (i4 + i) * 2048)
-                            : "memory");
+              for (int i = 0; i < NB; ++i)
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x4[i].x), "=r"(x4[i].y), "=r"(x4[i].z), "=r"(x4[i].w)
+                             : "r"(src + (i4 + i) * (LT * 16))
+                             : "memory");
 #pragma unroll
-             for (int i = i4; i < i4 + 4; ++i) {
-              const uint4 x = x4[i - i4];
-              const float sc = exp_scale(e_old[FP8 ? i : 0]);
-              const uint64_t sc2 = f2(sc, sc);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-              uint32_t o[8];
+              for (int i = i4; i < i4 + NB; ++i) {
+                const uint4 x = x4[i - i4];
+                const float sc = exp_scale(e_old[FP8 ? i : 0]);
+                const uint64_t sc2 = f2(sc, sc);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t o[8];
 #pragma unroll
-              for (int h = 0; h < 8; ++h) {
-                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
-                float a, c;
-                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
-                    : "=f"(a), "=f"(c)
-                    : "r"(f));
-                f2split(mul2(f2(a, c), sc2), a, c);
-                o[h] = pack_bf16x2(a, c);
+                for (int h = 0; h < 8; ++h) {
+                  const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+                  float a, c;
+                  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                      : "=f"(a), "=f"(c)
+                      : "r"(f));
+                  f2split(mul2(f2(a, c), sc2), a, c);
+                  o[h] = pack_bf16x2(a, c);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
+                      make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
               }
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
-                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-             }
             }
             announce(cFull + at.slot);
             at.step();
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int tok0 = row0 / p.G, first = row0 - tok0 * p.G;
           const float by_g = 1.f / static_cast<float>(p.G);
 #pragma unroll 4
-          for (int r = lt / QCPR; r < 256; r += 128 / QCPR) {
+          for (int r = lt / QCPR; r < 256; r += LT / QCPR) {
             const int x = first + r, i = p.G < 4096 ? static_cast<int>((static_cast<float>(x) + 0.5f) * by_g) : x / p.G;
             const uint32_t nb = r < rows ? qb : 0u;
             cp_async16(smem_u32(sQ) + (r >> 7) * L::kTile + tile_off(r & 127, qc),
@@ -441,7 +451,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
   } else if (warp < 4) {
-    regs_decrease<kRegsMma>();
+    regs_decrease<Roles::kRegsMma>();
     if (warp == 0) {
       // ---------------------------------------------------------------- products
       // The whole warp runs the loop and one elected lane issues: the descriptors then stay in
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------- softmax
-    regs_increase<FP8 ? kRegsSoft8 : kRegsSoft>();
+    regs_increase<Roles::kRegsSoft>();
     const int w = (warp >> 2) - 1, quad = warp & 3, row = w * 128 + quad * 32 + lane;
     const uint32_t tl = tbase + (static_cast<uint32_t>(quad * 32) << 16);
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
@@ -616,35 +626,48 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
           if (!(ok = wait(cSFull + w, ns & 1))) break;
           tc_fence_after();
-          uint32_t x[4][32];
+          auto mask32 = [&](int a, uint32_t (&x)[32]) {
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+            const uint32_t see = below(hi - a * 32) & (~below(lo - a * 32) | below(sk - a * 32));
 #pragma unroll
-          for (int a = 0; a < 4; ++a) tmem_ld32(tl + scol + a * 32, x[a]);
-          tmem_ld_wait(x[0]);
-          tmem_ld_tie(x[1]);
-          tmem_ld_tie(x[2]);
-          tmem_ld_tie(x[3]);
-          if (masked) {
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-              auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-              const uint32_t see = below(hi - a * 32) & (~below(lo - a * 32) | below(sk - a * 32));
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see >> e) & 1u)) x[a][e] = 0xff800000u;
-            }
-          }
-          float mx4[4];
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
-            mx4[a] = __uint_as_float(x[a][0]);
-            asm("max.f32 %0, %0, %1;" : "+f"(mx4[a]) : "f"(__uint_as_float(x[a][1])));
+            for (int e = 0; e < 32; ++e)
+              if (!((see >> e) & 1u)) x[e] = 0xff800000u;
+          };
+          auto max32 = [](const uint32_t (&x)[32]) {
+            float t = __uint_as_float(x[0]);
+            asm("max.f32 %0, %0, %1;" : "+f"(t) : "f"(__uint_as_float(x[1])));
 #pragma unroll
             for (int e = 2; e < 32; e += 2)
-              asm("max.f32 %0, %0, %1, %2;"
-                  : "+f"(mx4[a])
-                  : "f"(__uint_as_float(x[a][e])), "f"(__uint_as_float(x[a][e + 1])));
+              asm("max.f32 %0, %0, %1, %2;" : "+f"(t) : "f"(__uint_as_float(x[e])), "f"(__uint_as_float(x[e + 1])));
+            return t;
+          };
+          // bf16: the row's 128 scores stay in registers.  e4m3: they are read from TMEM twice, 32 at a
+          // time, which leaves registers for more loading warps.
+          uint32_t x[FP8 ? 1 : 4][32];
+          float mx = kNInf;
+          if (FP8) {
+#pragma unroll 1
+            for (int a = 0; a < 4; ++a) {
+              tmem_ld32(tl + scol + a * 32, x[0]);
+              tmem_ld_wait(x[0]);
+              if (masked) mask32(a, x[0]);
+              mx = fmaxf(mx, max32(x[0]));
+            }
+          } else {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) tmem_ld32(tl + scol + a * 32, x[FP8 ? 0 : a]);
+            tmem_ld_wait(x[0]);
+#pragma unroll
+            for (int a = 1; a < 4; ++a) tmem_ld_tie(x[FP8 ? 0 : a]);
+            if (masked) {
+#pragma unroll
+              for (int a = 0; a < 4; ++a) mask32(a, x[FP8 ? 0 : a]);
+            }
+            float mx4[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) mx4[a] = max32(x[FP8 ? 0 : a]);
+            mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float mn = fmaxf(m, mx);
           float alpha = 1.f;
           if ((mn - m) * cexp > kRaise) {  // (also from -inf)
@@ -668,13 +691,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const float nm = m == kNInf ? 0.f : -(m * cexp);
           const uint64_t nm2 = f2(nm, nm);
           uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int a = 0; a < 4; ++a) {
+          auto weights32 = [&](int a, const uint32_t (&x)[32]) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float e0, e1;
-              f2split(fma2(f2(__uint_as_float(x[a][2 * e]), __uint_as_float(x[a][2 * e + 1])), c2, nm2), e0, e1);
+              f2split(fma2(f2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), c2, nm2), e0, e1);
               e0 = paged_ex2(e0);
               e1 = paged_ex2(e1);
               sum[e & 1] = add2(sum[e & 1], f2(e0, e1));
@@ -686,6 +708,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
               tc_fence_before();
               mbar_arrive(&bars[cPReady + 2 * w + (a >> 1)]);
             }
+          };
+          if (FP8) {
+#pragma unroll 1
+            for (int a = 0; a < 4; ++a) {
+              tmem_ld32(tl + scol + a * 32, x[0]);
+              tmem_ld_wait(x[0]);
+              if (masked) mask32(a, x[0]);
+              weights32(a, x[0]);
+            }
+          } else {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) weights32(a, x[FP8 ? 0 : a]);
           }
           float s0, s1;
           f2split(add2(sum[0], sum[1]), s0, s1);
@@ -758,7 +792,7 @@ cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
   using L = ChunkSmem<D, FP8>;
   auto kern = paged_chunk_kernel<D, FP8>;
   static std::atomic<uint64_t> ready{0};
-  cudaError_t e = set_up_once(ready, kern, L::kTotal, kChunkLaunchRegs);  // (the setmaxnreg split must fit)
+  cudaError_t e = set_up_once(ready, kern, L::kTotal, ChunkRoles<FP8>::kLaunchRegs);  // (the setmaxnreg split must fit)
   if (e != cudaSuccess) return e;
   CUtensorMap tk{}, tv{};
   const int page = 1 << p.c.page_shift, rows = page < 128 ? page : 128;
@@ -767,7 +801,7 @@ cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
                   paged_map(&tv, p.c.v, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, rows)
               ? rows
               : 0;
-  kern<<<kPagedCtas, kChunkThreads, L::kTotal, stream>>>(tk, tv, p);
+  kern<<<kPagedCtas, ChunkRoles<FP8>::kThreads, L::kTotal, stream>>>(tk, tv, p);
   return cudaGetLastError();
 }
 

@@ -82,7 +82,7 @@ typedef struct fdma_paged_args {
   int64_t q_stride[2];
   const int32_t* cu_q; /* (B + 1) */
   int32_t max_q;       /* at least the longest sequence's new tokens (rows past it are left out and
-                          reported as FDMA_ERR_INVALID by fdma_get_device_error) */
+                          reported as FDMA_ERR_INVALID by fdma_get_device_error; 0: nothing is done) */
 
   int32_t causal; /* 1: the row at position p sees keys j <= p; 0: all k_len[b] keys */
   int32_t window; /* > 0 (causal only): of those, j > p - window or j < sinks; 0: no window */
@@ -118,7 +118,8 @@ FDMA_API size_t fdma_paged_workspace_size(const fdma_paged_args* args);
      lse = log sum exp S  (fp32 (Hq, T) contiguous).
    A row that sees no key gets out = 0 and lse = -inf.  Keys that a row does not see do not reach
    it, whatever they hold.  Precision: products in fp32 from the bf16 (or exact e4m3) values, the
-   softmax in fp32; the weights are rounded to 16 bits (8 or more of mantissa) for the product with V.
+   softmax in fp32; for the product with V the weights are rounded to bf16 (to f16, which keeps 11 bits, for
+   an e4m3 cache and at most 16 rows, max_q * Hq / Hkv).
    Deterministic: the same call gives the same bits. */
 FDMA_API int fdma_paged_fwd(const fdma_paged_args* args, void* out, float* lse, void* stream);
 

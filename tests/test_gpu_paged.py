@@ -2,7 +2,7 @@
 
 Bounds.  Let u be half a step of the type that the softmax weights are held in for the product with V,
 relative to the value: 2^-8 for bf16 (bf16 caches, and every cache in the chunk kernel, whose values
-are bf16 in shared memory), 2^-11 for f16 (e4m3 caches in the token kernel: up to 24 rows (new tokens
+are bf16 in shared memory), 2^-11 for f16 (e4m3 caches in the token kernel: up to 16 rows (new tokens
 times heads of a group) a sequence).  A weight P_j carries its own rounding (u) and the error of its score: a sum of d products in
 fp32 is off by at most d * 2^-24 * sum |q_c k_c| (times scale: d 2^-24 D), the exponent's argument
 S * log2(e) - max and the exponential itself by a few 2^-22 relative to the score's size.  With
@@ -111,7 +111,7 @@ def _queries(T, Hq, d, seed=1, gain=1.0):
 def _check_attention(s, q, news, out, lse, causal=True, window=0, sinks=0, scale=None):
     d = s.d
     scale = d ** -0.5 if scale is None else scale
-    f16 = s.fp8 and max(news) * (q.shape[1] // s.Hkv) <= 24
+    f16 = s.fp8 and max(news) * (q.shape[1] // s.Hkv) <= 16
     at, worst = 0, 0.0
     out, lse, q = _np(out), _np(lse), _np(q)
     for b, n in enumerate(news):
