@@ -190,8 +190,8 @@ int classify_into_workspace(const fdma_args* a, int8_t* user_map, cudaStream_t s
 
 int* paged_error_word() { return device_error_word(); }
 
-bool paged_map(CUtensorMap* m, const void* base, int d, int page, int Hkv, int num_pages, const int64_t st[3],
-               int rows) {
+bool paged_map(CUtensorMap* m, bool e4m3, const void* base, int d, int page, int Hkv, int num_pages,
+               const int64_t st[3], int cols, int rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || base == nullptr) return false;
   const cuuint64_t gd[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(Hkv),
@@ -201,9 +201,10 @@ bool paged_map(CUtensorMap* m, const void* base, int d, int page, int Hkv, int n
     if (gs[i] == 0 && gd[i + 1] > 1) return false;
     if (gs[i] == 0) gs[i] = 16;  // an axis of one element: any stride
   }
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd, gs, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols), static_cast<cuuint32_t>(rows), 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gd,
+             gs, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -143,9 +143,11 @@ struct TopkParams {
 
 // The current device's error word, for the entry points outside fdma_api.cu (nullptr on failure).
 int* paged_error_word();
-// bf16 cache rows (d, page, Hkv, num_pages; strides in bytes: page, token, head) as a map of boxes of
-// 64 columns by `rows` tokens, 128-byte swizzle; false where such a map cannot be made.
-bool paged_map(CUtensorMap* m, const void* base, int d, int page, int Hkv, int num_pages, const int64_t st[3], int rows);
+// Cache rows (d, page, Hkv, num_pages; strides in bytes: page, token, head) as a map of boxes of `cols`
+// columns by `rows` tokens, bf16 with a 128-byte swizzle or e4m3 codes without; false where such a map
+// cannot be made.
+bool paged_map(CUtensorMap* m, bool e4m3, const void* base, int d, int page, int Hkv, int num_pages,
+               const int64_t st[3], int cols, int rows);
 cudaError_t launch_classify(const ClassifyParams& p, cudaStream_t stream);
 // bf16 masks through a tensor map of the mask (4D, 64 x 128 box, 128-byte swizzle).
 cudaError_t launch_classify_tma1(const CUtensorMap& tm, const ClassifyParams& p, cudaStream_t stream);

@@ -816,6 +816,8 @@ int fdma_paged_fwd(const fdma_paged_args* a, void* out, float* lse, void* stream
   p.part_ml = reinterpret_cast<float2*>(ws + w.ml);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.min_run = 1;
+  const int64_t blocks = (static_cast<int64_t>(a->max_q) * p.G + item_rows(a) - 1) / item_rows(a);
+  for (p.plan_lanes = 1; p.plan_lanes < 32 && p.plan_lanes < blocks;) p.plan_lanes *= 2;
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
   const bool fp8 = a->cache.cache_type == FDMA_CACHE_E4M3;

@@ -58,6 +58,7 @@ struct PagedParams {
   int4* desc;     // [cta]: the split item that begins in this CTA: (sequence, kv head, row block, slot | pieces << 1)
   int* err;
   int min_run;  // least length of a run
+  int plan_lanes;  // lanes that share a sequence when the line is laid out: a power of two, at most 32
   int box;      // chunk kernel: rows of a TMA box of the cache (0: no TMA)
 };
 
@@ -168,15 +169,13 @@ struct Cursor {
   }
 };
 
-// Places of one sequence's items of one kv head.
+// Places of the rt-th item of a kv head.
 template <int ROWS, int KT>
-__device__ __forceinline__ int seq_places(const PagedParams& p, const Seq& s) {
-  int n = 0;
-  for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS) {
-    const int k = key_span<KT>(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
-    if (k > 0) n += k + kItemCost;
-  }
-  return n;
+__device__ __forceinline__ int item_places(const PagedParams& p, const Seq& s, int rt) {
+  const int r0 = rt * ROWS;
+  if (r0 >= s.nq * p.G) return 0;
+  const int k = key_span<KT>(p, s, r0 / p.G, min((r0 + ROWS - 1) / p.G + 1, s.nq)).tiles;
+  return k > 0 ? k + kItemCost : 0;
 }
 
 struct PlanSmem {
@@ -187,17 +186,25 @@ struct PlanSmem {
 
 // Finds this CTA's run: every thread of the CTA calls it (NT threads).  False where it has no
 // tiles; else c stands on the first of them.  quota: the run length of all CTAs.
+// A sequence's items are counted by plan_lanes lanes together (by one, a chunk's 16 to 32 row blocks took
+// 6 us before the first load).
 template <int ROWS, int KT, int NT>
 __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS, KT>& c, int& quota) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (p.c.B + NT - 1) / NT;
-  const int b0 = min(tid * per, p.c.B), b1 = min(b0 + per, p.c.B);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = p.plan_lanes, sub = lane & (L - 1);
+  const unsigned group = (L == 32 ? 0xffffffffu : (1u << L) - 1u) << (lane & -L);
+  const int per = (p.c.B + NT / L - 1) / (NT / L);
+  const int b0 = min(tid / L * per, p.c.B), b1 = min(b0 + per, p.c.B);
+  // places of a kv head of a sequence, in every lane of the group
+  auto seq_places = [&](const Seq& s) {
+    int n = 0;
+    for (int rt = sub; rt * ROWS < s.nq * p.G; rt += L) n += item_places<ROWS, KT>(p, s, rt);
+    for (int o = 1; o < L; o <<= 1) n += __shfl_xor_sync(group, n, o);
+    return n;
+  };
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) {
-    const Seq s = load_seq(p, b, blockIdx.x == 0);
-    mine += static_cast<int64_t>(seq_places<ROWS, KT>(p, s)) * p.c.Hkv;
-  }
-  int64_t x = mine;
+  for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(seq_places(load_seq(p, b, blockIdx.x == 0))) * p.c.Hkv;
+  __syncwarp();
+  int64_t x = sub == 0 ? mine : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -205,7 +212,7 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
   }
   if (lane == 31) sm->warp_sum[warp] = x;
   __syncthreads();
-  int64_t before = x - mine, total = 0;
+  int64_t before = x - mine, total = 0;  // (x holds the group's places in every lane of it)
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += sm->warp_sum[w];
@@ -213,26 +220,34 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
   }
   quota = static_cast<int>(max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(p.min_run)));
   const int64_t start = static_cast<int64_t>(blockIdx.x) * quota;
-  if (start >= before && start < before + mine) {
+  if (start >= before && start < before + mine) {  // (one group of lanes)
     int64_t left = start - before;
     for (int b = b0; b < b1; ++b) {
       const Seq s = load_seq(p, b, false);
-      const int n = seq_places<ROWS, KT>(p, s);
+      const int n = seq_places(s);
       if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
         left -= static_cast<int64_t>(n) * p.c.Hkv;
         continue;
       }
-      sm->b = b;
-      sm->g = static_cast<int>(left / n);
-      int t = static_cast<int>(left % n), rt = 0;
-      for (;; ++rt) {
-        const int k = key_span<KT>(p, s, rt * ROWS / p.G, min((rt * ROWS + ROWS - 1) / p.G + 1, s.nq)).tiles;
-        if (k == 0) continue;
-        if (t < k + kItemCost) break;
-        t -= k + kItemCost;
+      const int g = static_cast<int>(left / n);
+      int t = static_cast<int>(left % n);
+      for (int rt = sub;; rt += L) {
+        const int k = item_places<ROWS, KT>(p, s, rt);
+        int sum = k;
+        for (int o = 1; o < L; o <<= 1) {
+          const int y = __shfl_up_sync(group, sum, o, L);
+          if (sub >= o) sum += y;
+        }
+        if (t >= sum - k && t < sum) {
+          sm->b = b;
+          sm->g = g;
+          sm->rt = rt;
+          sm->t = t - (sum - k);
+        }
+        const int all = __shfl_sync(group, sum, L - 1, L);
+        if (t < all) break;
+        t -= all;
       }
-      sm->rt = rt;
-      sm->t = t;
       break;
     }
   }
@@ -260,6 +275,7 @@ template <int ROWS>
 __device__ __forceinline__ void write_empty_blocks(const PagedParams& p) {
   for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
     const Seq s = load_seq(p, b, false);
+    if (p.causal ? s.pos0 >= 0 : s.klen > 0) continue;  // every row sees a key
     for (int r0 = 0; r0 < s.nq * p.G; r0 += ROWS) {
       const int i0 = r0 / p.G, i1 = min((r0 + ROWS - 1) / p.G + 1, s.nq);
       if (key_span<128>(p, s, i0, i1).tiles > 0) continue;

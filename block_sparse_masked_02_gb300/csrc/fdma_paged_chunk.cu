@@ -31,7 +31,9 @@ namespace {
 
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kKeyTile = 128;
-constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four and two raw ones with e4m3)
+constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four, and kRaw raw ones, with e4m3)
+constexpr int kRaw = 2;
+constexpr int kScales = 4;  // tiles' scale bytes
 constexpr int kParts = 4;  // published parts
 constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
 // Loading warps and the division of the registers (setmaxnreg).  An e4m3 cache has eight loading warps,
@@ -63,7 +65,11 @@ enum ChunkBar : int {
   cPartFree = cPart + kParts,  // + part slot: every reader is done with it
   cLook = cPartFree + kParts,  // + entry: a V tile to be looked through has landed
   cDrain = cLook + kLooks,
-  kChunkBars
+  cRaw,  // + place: an e4m3 item's codes are in shared memory
+  cRawFree = cRaw + kRaw,  // + place: they have been converted
+  cScale = cRawFree + kRaw,  // + place: the scale bytes of a tile's K and V rows
+  cScaleFree = cScale + kScales,
+  kChunkBars = cScaleFree + kScales
 };
 
 // Byte offset of 16-byte chunk c of row r in a K-major tile of 64-column blocks, 128-byte swizzle.
@@ -129,8 +135,10 @@ struct ChunkSmem {
   static constexpr int kTile = 128 * D * 2;
   static constexpr int kRing = FP8 ? 4 : kRingTiles;
   static constexpr int kOffRing = 2 * kTile;
-  static constexpr int kOffRaw = kOffRing + kRing * kTile;  // e4m3: [2] items as they lie in the cache
-  static constexpr int kOffBar = kOffRaw + (FP8 ? kTile : 0);
+  static constexpr int kOffRaw = kOffRing + kRing * kTile;  // e4m3: [kRaw] items' rows of d codes
+  static constexpr int kOffScale = kOffRaw + (FP8 ? kRaw * (kTile / 2) : 0);  // [kScales][K, V][128]
+  static constexpr int kOffAbsent = kOffScale + (FP8 ? kScales * 256 : 0);    // [kRaw]: groups of 16 rows that are not there
+  static constexpr int kOffBar = kOffAbsent + (FP8 ? kRaw * 4 : 0);
   static constexpr int kOffMisc = kOffBar + kChunkBars * 8;
   static constexpr int kOffParts = kOffMisc + 16;
   static constexpr int kOffLooks = kOffParts + kParts * static_cast<int>(sizeof(Part));
@@ -175,7 +183,9 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
     mbar_init(&bars[cQFull], Roles::kLoadWarps);
     for (int i = 0; i < 4; ++i) mbar_init(&bars[cPReady + i], 128);
     for (int i = 0; i < 2; ++i) mbar_init(&bars[cOFree + i], 128);
-    for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], LT + 1 + 256);
+    for (int i = 0; i < kRaw; ++i) mbar_init(&bars[cRawFree + i], Roles::kLoadWarps);
+    for (int i = 0; i < kScales; ++i) mbar_init(&bars[cScaleFree + i], Roles::kLoadWarps);
+    for (int i = 0; i < kParts; ++i) mbar_init(&bars[cPartFree + i], LT + 1 + 256 + (FP8 ? 2 : 0));
     misc[1] = 0;
     fence_mbar_init();
   }
@@ -220,16 +230,16 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
     auto slot_free = [&](int item) { return item < L::kRing || wait(cEmpty + at.slot, at.phase ^ 1); };
-    // A thread copies one 16-byte column (of the cache's row) of NP rows i * RPP + lt / CPR.
-    constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = LT / CPR, NP = 128 / RPP, NB = NP < 4 ? NP : 4;
-    const int chunk = lt % CPR, r0 = lt / CPR;
+    // A thread has one 16-byte column (of the cache's row) of NP rows r0 + i * RPP; with an e4m3 cache these
+    // are of the warp's group of 16 keys.
+    constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = (FP8 ? 32 : LT) / CPR, NP = (FP8 ? 16 : 128) / RPP;
+    constexpr int NB = NP < 4 ? NP : 4;
+    static_assert(!FP8 || Roles::kLoadWarps == 8, "a warp for each 16 of a tile's 128 keys");
+    const int chunk = lt % CPR, r0 = FP8 ? (warp - 12) * 16 + lane / CPR : lt / CPR;
     const uint32_t cb = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
-    // e4m3: this thread's raw 16-byte pieces of two items, and the scale bytes of their rows
-    // (piece i of item x at (x & 1) * 128 * D + i * LT * 16)
-    const uint32_t raw = smem_u32(smem) + L::kOffRaw + lt * 16;
-    uint32_t e_old[FP8 ? NP : 1], e_new[FP8 ? NP : 1];
-    int looks = 0;                                      // bf16: V tiles given to the looking warps
-    int look_j0 = -1, look_next = -1, look_part = 0;  // e4m3: the same, looked through here as they are converted
+    // e4m3: this thread's first piece of the item at place 0; piece i lies i * 512 on
+    const uint32_t raw = smem_u32(smem) + L::kOffRaw + (warp - 12) * 16 * D + lane * 16;
+    int looks = 0;  // bf16: V tiles given to the looking warps
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
     // code fell out of the instruction cache and everything ran at half speed.)
     for (int idx = 0; ok; ++idx) {
@@ -238,12 +248,12 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       // (copies: what lies in shared memory is read again after every barrier)
       const int n = s.n, b = s.b, g_kv = s.g, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, all_lo = s.all_lo, all_hi = s.all_hi;
       const PartTiles tiles(s);
-      // Lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
+      // bf16: lanes 0..7 of every warp look up the pages of a tile's eight groups of 16 keys, one tile
       // ahead of their use; none where no row sees a key of the group (of its box).
       const int unit = max(p.box, 16);
       auto look_up = [&](int k) {
         int entry = kNoKeys;
-        if (lane < 8 && k < n) {
+        if (!FP8 && lane < 8 && k < n) {
           const int j = tiles.key0(k) + lane * 16, jb = j & -unit;
           if (jb < sink_hi || (jb < hi && jb + unit > lo)) entry = table_entry(p, b, j);
         }
@@ -253,19 +263,14 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       bool missing = false;  // a page that is needed is not there
       unsigned boxes = 0;
       bool mine_box = false;
-      // (one turn without loads at the end of the run, for the last raw item)
-      const int turns = n > 0 ? 2 * n : FP8 ? 1 : 0;
 #pragma unroll 1
-      for (int i2 = 0; i2 < turns; ++i2) {
-        if (FP8) {
-#pragma unroll
-          for (int i = 0; i < NP; ++i) e_old[FP8 ? i : 0] = e_new[FP8 ? i : 0];
-          look_j0 = look_next;
-        }
-        if (n > 0) {
-          // ---- this item's rows
-          const bool is_v = i2 & 1;
-          const int j0 = tiles.key0(i2 >> 1);
+      for (int i2 = 0; i2 < 2 * n; ++i2) {
+        const bool is_v = i2 & 1;
+        const int j0 = tiles.key0(i2 >> 1);
+        // V of keys that not every row sees is looked through.  (K needs no care: scores of unseen keys are
+        // replaced, whatever they are.)
+        const bool look = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi);
+        if (!FP8) {
           if (!is_v) {
             const int entry = pg_next;
             pg = checked_page(p, entry);
@@ -277,141 +282,113 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
             boxes = __ballot_sync(0xffffffffu, begins);
             mine_box = begins && ((lane * 16 / unit) & 3) == warp - 12;
           }
-          if (!FP8) {
-            if (!(ok = slot_free(it))) break;
-            const int bar = cFull + at.slot;
-            uint8_t* to = sR + at.slot * L::kTile;
-            // V of keys that not every row sees goes by the looking warps.  (K needs no care: scores of
-            // unseen keys are replaced, whatever they are.)
-            const bool look = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi);
-            if (p.box > 0 && !missing) {
-              uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
-              if (lane == 0) {
-                if (warp == 12) {
-                  if (look) look_at[looks % kLooks] = Look{at.slot, j0, idx};
-                  mbar_arrive_expect_tx(to_bar, __popc(boxes) * p.box * (2 * D));
-                } else if (!look) {
-                  mbar_arrive(to_bar);
-                }
+          if (!(ok = slot_free(it))) break;
+          const int bar = cFull + at.slot;
+          uint8_t* to = sR + at.slot * L::kTile;
+          if (p.box > 0 && !missing) {
+            uint64_t* to_bar = &bars[look ? cLook + looks % kLooks : bar];
+            if (lane == 0) {
+              if (warp == 12) {
+                if (look) look_at[looks % kLooks] = Look{at.slot, j0, idx};
+                mbar_arrive_expect_tx(to_bar, __popc(boxes) * p.box * (2 * D));
+              } else if (!look) {
+                mbar_arrive(to_bar);
               }
-              if (mine_box) {
-                const CUtensorMap* tm = is_v ? &tmV : &tmK;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                  tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
-              }
-              __syncwarp();
-              looks += look;
-            } else {
-              const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
-              const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
-              const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
-              const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
-              constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
-              uint32_t dst = smem_u32(to) + tile_off(r0, chunk);
-#pragma unroll 1
-              for (int g = 0; g < 8; ++g) {
-                const uint8_t* src = mine + __shfl_sync(0xffffffffu, group, g);
-                const bool paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                  const int j = j0 + g * 16 + i * RPP + r0;
-                  const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
-                  cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
-                  src += RPP * st;
-                  dst += RPP * 128;
-                }
-              }
-              cp_async_wait_all();
-              if (look && mend_pieces_apart<false>(smem_u32(to) + tile_off(r0, chunk), RPP * 128, NP, j0 + r0, RPP,
-                                             part_seen(s, p.sinks)))
-                s.odd = 1;
-              announce(bar);
             }
-            at.step();
+            if (mine_box) {
+              const CUtensorMap* tm = is_v ? &tmV : &tmK;
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(to + c * 16384 + lane * 2048, tm, to_bar, c * 64, (j0 + lane * 16) & pmask, g_kv, pg);
+            }
+            __syncwarp();
+            looks += look;
           } else {
             const uint8_t* from = (is_v ? p.c.v : p.c.k) + g_kv * (is_v ? p.c.vs[2] : p.c.ks[2]);
             const int64_t sp = is_v ? p.c.vs[0] : p.c.ks[0], st = is_v ? p.c.vs[1] : p.c.ks[1];
             const int64_t group = static_cast<int64_t>(pg) * sp + ((j0 + (lane & 7) * 16) & pmask) * st;
             const uint8_t* mine = from + (r0 & 15) * st + chunk * 16;
-            // every key of the tile is seen by some row and has a page
-            const bool all =
-                j0 >= lo && j0 + 128 <= hi && (__ballot_sync(0xffffffffu, pg >= 0) & 0xffu) == 0xffu;
-            const int64_t* es = is_v ? p.c.ves : p.c.kes;
-            const uint8_t* efrom = (is_v ? p.c.ve : p.c.ke) + g_kv * es[2] + (r0 & 15) * es[1];
-            const int64_t egroup = static_cast<int64_t>(pg) * es[0] + ((j0 + (lane & 7) * 16) & pmask) * es[1];
-            const uint32_t dst = raw + (it & 1) * (128 * D);
-            look_next = is_v && !(j0 >= all_lo && j0 + 128 <= all_hi) ? j0 : -1;
+            constexpr int PER = 16 / RPP;  // copies of a group of 16 keys
+            uint32_t dst = smem_u32(to) + tile_off(r0, chunk);
+#pragma unroll 1
+            for (int g = 0; g < 8; ++g) {
+              const uint8_t* src = mine + __shfl_sync(0xffffffffu, group, g);
+              const bool paged = __shfl_sync(0xffffffffu, pg, g) >= 0;
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-              const int g = ((i * RPP) >> 4) + (r0 >> 4);
-              const int64_t off = __shfl_sync(0xffffffffu, group, g), eoff = __shfl_sync(0xffffffffu, egroup, g);
-              bool in = true;
-              if (!all) {
-                const int j = j0 + i * RPP + r0;
-                in = __shfl_sync(0xffffffffu, pg, g) >= 0 && (j < sink_hi || (j >= lo && j < hi));
+              for (int i = 0; i < PER; ++i) {
+                const int j = j0 + g * 16 + i * RPP + r0;
+                const bool in = paged && (j < sink_hi || (j >= lo && j < hi));
+                cp_async16(dst, in ? src : p.c.k, in ? cb : 0u);
+                src += RPP * st;
+                dst += RPP * 128;
               }
-              cp_async16(dst + i * (LT * 16), in ? mine + off : p.c.k, in ? cb : 0u);
-              e_new[FP8 ? i : 0] = 127;
-              if (in) e_new[FP8 ? i : 0] = efrom[eoff];
             }
+            cp_async_wait_all();
+            if (look && mend_pieces_apart<false>(smem_u32(to) + tile_off(r0, chunk), RPP * 128, NP, j0 + r0, RPP,
+                                           part_seen(s, p.sinks)))
+              s.odd = 1;
+            announce(bar);
           }
-          ++it;
-          if (FP8) cp_async_commit();
-        }
-        if (FP8) {
-          // ---- the item before becomes bf16
-          const int item = n > 0 ? it - 2 : it - 1;
-          if (n > 0) cp_async_wait<1>();
-          else cp_async_wait_all();
-          if (item >= 0 && (n > 0 || it > 0)) {
-            if (!(ok = slot_free(item))) break;
-            const uint32_t src = raw + (item & 1) * (128 * D);
-            if (look_j0 >= 0) {
-              Part& sp = parts[look_part % kParts];
-              if (mend_pieces_apart<true, NB>(src, LT * 16, NP, look_j0 + r0, RPP, part_seen(sp, p.sinks)))
-                sp.odd = 1;
-            }
-            // (loads of four pieces together: one after the other, each waited for the last one's store)
+          at.step();
+        } else {
+          // ---- the warp's 16 rows become bf16
+          const int tile = it >> 1, place = it % kRaw;
+          if (!is_v && !(ok = wait(cScale + tile % kScales, (tile / kScales) & 1))) break;
+          if (!(ok = wait(cRaw + place, (it / kRaw) & 1) && slot_free(it))) break;
+          const uint32_t src = raw + place * (128 * D);
+          const uint8_t* exps = smem + L::kOffScale + tile % kScales * 256 + is_v * 128 + r0;
+          const bool here = !((reinterpret_cast<const int*>(smem + L::kOffAbsent)[place] >> (warp - 12)) & 1);
+          if (look && here && mend_pieces_apart<true, NB>(src, 512, NP, j0 + r0, RPP, part_seen(s, p.sinks))) s.odd = 1;
+          // (loads of four pieces together: one after the other, each waited for the last one's store)
 #pragma unroll
-            for (int i4 = 0; i4 < NP; i4 += NB) {
-              uint4 x4[NB];
+          for (int i4 = 0; i4 < NP; i4 += NB) {
+            uint4 x4[NB];
 #pragma unroll
-              for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < NB; ++i) {
+              x4[i] = make_uint4(0u, 0u, 0u, 0u);
+              if (here)
                 asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(x4[i].x), "=r"(x4[i].y), "=r"(x4[i].z), "=r"(x4[i].w)
-                             : "r"(src + (i4 + i) * (LT * 16))
+                             : "r"(src + (i4 + i) * 512)
                              : "memory");
-#pragma unroll
-              for (int i = i4; i < i4 + NB; ++i) {
-                const uint4 x = x4[i - i4];
-                const float sc = exp_scale(e_old[FP8 ? i : 0]);
-                const uint64_t sc2 = f2(sc, sc);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t o[8];
-#pragma unroll
-                for (int h = 0; h < 8; ++h) {
-                  const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
-                  float a, c;
-                  asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
-                      : "=f"(a), "=f"(c)
-                      : "r"(f));
-                  f2split(mul2(f2(a, c), sc2), a, c);
-                  o[h] = pack_bf16x2(a, c);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + h)) =
-                      make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
-              }
             }
-            announce(cFull + at.slot);
-            at.step();
+#pragma unroll
+            for (int i = i4; i < i4 + NB; ++i) {
+              // (the lanes of one row that lie 128 bytes apart in the tile's row store their halves in
+              // opposite order: else every store would meet a second one in its banks)
+              const bool turn = chunk >= 4;
+              uint4 x = x4[i - i4];
+              if (turn) x = make_uint4(x.z, x.w, x.x, x.y);
+              const float sc = exp_scale(exps[i * RPP]);
+              const uint64_t sc2 = f2(sc, sc);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int h = 0; h < 8; ++h) {
+                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
+                float a, c;
+                asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
+                    : "=f"(a), "=f"(c)
+                    : "r"(f));
+                f2split(mul2(f2(a, c), sc2), a, c);
+                o[h] = pack_bf16x2(a, c);
+              }
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                *reinterpret_cast<uint4*>(sR + at.slot * L::kTile + tile_off(i * RPP + r0, chunk * 2 + (h ^ turn))) =
+                    make_uint4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
+            }
           }
-          look_part = idx;
+          announce(cFull + at.slot);
+          if (lane == 0) {
+            mbar_arrive(&bars[cRawFree + place]);
+            if (is_v) mbar_arrive(&bars[cScaleFree + tile % kScales]);
+          }
+          at.step();
         }
+        ++it;
         // ---- the part's Q, behind its first loads
-        if (n > 0 && i2 == (FP8 ? 0 : 1)) {
+        if (i2 == (FP8 ? 0 : 1)) {
           if (idx > 0 && !(ok = wait(cQEmpty, (idx - 1) & 1))) break;
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
@@ -536,6 +513,102 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       __syncwarp();
       if (one) umma_commit(&bars[cDrain]);
       mbar_wait(&bars[cDrain], 0, p.err, kDevErrTimeout, nullptr);
+    } else if (FP8 && warp < 3) {
+      // ------------------------------------------------- e4m3: codes (warp 1) and scale bytes (warp 2)
+      const int pmask = (1 << p.c.page_shift) - 1, sub = warp == 1 ? (lane & 7) * 16 : lane * 4;
+      uint8_t* const raw = smem + L::kOffRaw;
+      int tile = 0, issued = 0;  // tiles so far in the run; items on their way
+      bool ok = true;
+      for (int idx = 0; ok; ++idx) {
+        if (!(ok = part_ready(idx))) break;
+        const Part& s = parts[idx % kParts];
+        const int n = s.n, b = s.b, g = s.g, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
+        const PartTiles tiles(s);
+        __syncwarp();
+        if (lane == 0) part_done(idx);
+        if (n == 0) break;
+        // the page of this lane's keys of a tile, looked up one tile ahead; none where no row sees a key
+        // of the group of 16
+        auto look_up = [&](int k) {
+          int entry = kNoKeys;
+          if (k < n) {
+            const int j = tiles.key0(k) + (sub & -16);
+            if (j < sink_hi || (j < hi && j + 16 > lo)) entry = table_entry(p, b, j);
+          }
+          return entry;
+        };
+        int next = look_up(0);
+#pragma unroll 1
+        for (int k = 0; ok && k < n; ++k, ++tile) {
+          const int j = tiles.key0(k) + sub, pg = checked_page(p, next);
+          next = look_up(k + 1);
+          if (warp == 1) {
+            const unsigned here = __ballot_sync(0xffffffffu, lane < 8 && pg >= 0);
+#pragma unroll 1
+            for (int is_v = 0; is_v < 2; ++is_v) {
+              const int it = 2 * tile + is_v, place = it % kRaw;
+              if (it >= kRaw && !(ok = wait(cRawFree + place, (it / kRaw - 1) & 1))) break;
+              uint8_t* to = raw + place * (128 * D);
+              uint64_t* bar = &bars[cRaw + place];
+              if (lane == 0) {
+                reinterpret_cast<unsigned*>(smem + L::kOffAbsent)[place] = ~here;
+                if (p.box > 0) mbar_arrive_expect_tx(bar, __popc(here) * 16 * D);
+              }
+              __syncwarp();
+              if (p.box > 0) {
+                if ((here >> lane) & 1u) tma_load_4d(to + lane * 16 * D, is_v ? &tmV : &tmK, bar, 0, j & pmask, g, pg);
+              } else {
+                constexpr int CPR = D / 16;
+                const int64_t* st = is_v ? p.c.vs : p.c.ks;
+                const uint8_t* from = (is_v ? p.c.v : p.c.k) + g * st[2];
+#pragma unroll 1
+                for (int i = lane; i < 128 * CPR; i += 32) {
+                  const int grp = i / (16 * CPR), page = __shfl_sync(0xffffffffu, pg, grp);
+                  const int slot = (__shfl_sync(0xffffffffu, j, grp) & pmask) + i / CPR % 16, c = i % CPR * 16;
+                  if (page >= 0)
+                    cp_async16(smem_u32(to) + i * 16, c < p.c.d ? from + page * st[0] + slot * st[1] + c : p.c.k,
+                               c < p.c.d ? 16u : 0u);
+                }
+                cp_async_wait_all();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+              }
+              ++issued;
+            }
+          } else {
+            uint32_t e[2] = {0x7f7f7f7fu, 0x7f7f7f7fu};
+            if (pg >= 0) {
+              uint32_t x[2][4];
+#pragma unroll
+              for (int is_v = 0; is_v < 2; ++is_v) {
+                const int64_t* st = is_v ? p.c.ves : p.c.kes;
+                const uint8_t* from = (is_v ? p.c.ve : p.c.ke) + g * st[2] + pg * st[0] + (j & pmask) * st[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  x[is_v][i] = 127;
+                  if (j + i < sink_hi || (j + i >= lo && j + i < hi)) x[is_v][i] = from[i * st[1]];
+                }
+              }
+#pragma unroll
+              for (int is_v = 0; is_v < 2; ++is_v)
+                e[is_v] = x[is_v][0] | x[is_v][1] << 8 | x[is_v][2] << 16 | x[is_v][3] << 24;
+            }
+            const int place = tile % kScales;
+            if (tile >= kScales && !(ok = wait(cScaleFree + place, (tile / kScales - 1) & 1))) break;
+            uint32_t* to = reinterpret_cast<uint32_t*>(smem + L::kOffScale + place * 256) + lane;
+            to[0] = e[0];
+            to[32] = e[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[cScale + place]);
+          }
+        }
+      }
+      cp_async_wait_all();
+      // (the boxes in flight land before the CTA ends, after a time-out too)
+      if (warp == 1) {
+        for (int i = max(issued - kRaw, 0); i < issued; ++i)
+          mbar_wait(&bars[cRaw + i % kRaw], (i / kRaw) & 1, p.err, kDevErrTimeout, nullptr);
+      }
     } else if (!FP8 && warp < 3) {
       // ---------------------------------------------------------------- looking
       constexpr int CPR = D / 8, RPP = 64 / CPR;
@@ -641,17 +714,25 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
               asm("max.f32 %0, %0, %1, %2;" : "+f"(t) : "f"(__uint_as_float(x[e])), "f"(__uint_as_float(x[e + 1])));
             return t;
           };
-          // bf16: the row's 128 scores stay in registers.  e4m3: they are read from TMEM twice, 32 at a
+          // bf16: the row's 128 scores stay in registers.  e4m3: they are read from TMEM twice, 64 at a
           // time, which leaves registers for more loading warps.
-          uint32_t x[FP8 ? 1 : 4][32];
+          uint32_t x[FP8 ? 2 : 4][32];
           float mx = kNInf;
+          auto load64 = [&](int a) {
+            tmem_ld32(tl + scol + a * 32, x[0]);
+            tmem_ld32(tl + scol + a * 32 + 32, x[1]);
+            tmem_ld_wait(x[0]);
+            tmem_ld_tie(x[1]);
+            if (masked) {
+              mask32(a, x[0]);
+              mask32(a + 1, x[1]);
+            }
+          };
           if (FP8) {
 #pragma unroll 1
-            for (int a = 0; a < 4; ++a) {
-              tmem_ld32(tl + scol + a * 32, x[0]);
-              tmem_ld_wait(x[0]);
-              if (masked) mask32(a, x[0]);
-              mx = fmaxf(mx, max32(x[0]));
+            for (int a = 0; a < 4; a += 2) {
+              load64(a);
+              mx = fmaxf(mx, fmaxf(max32(x[0]), max32(x[1])));
             }
           } else {
 #pragma unroll
@@ -711,11 +792,10 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
           };
           if (FP8) {
 #pragma unroll 1
-            for (int a = 0; a < 4; ++a) {
-              tmem_ld32(tl + scol + a * 32, x[0]);
-              tmem_ld_wait(x[0]);
-              if (masked) mask32(a, x[0]);
+            for (int a = 0; a < 4; a += 2) {
+              load64(a);
               weights32(a, x[0]);
+              weights32(a + 1, x[1]);
             }
           } else {
 #pragma unroll
@@ -795,10 +875,10 @@ cudaError_t launch_chunk(PagedParams p, cudaStream_t stream) {
   cudaError_t e = set_up_once(ready, kern, L::kTotal, ChunkRoles<FP8>::kLaunchRegs);  // (the setmaxnreg split must fit)
   if (e != cudaSuccess) return e;
   CUtensorMap tk{}, tv{};
-  const int page = 1 << p.c.page_shift, rows = page < 128 ? page : 128;
+  const int page = 1 << p.c.page_shift, rows = FP8 ? 16 : page < 128 ? page : 128, cols = FP8 ? D : 64;
   // (a cache that broadcasts an axis with stride 0 goes by cp.async)
-  p.box = !FP8 && paged_map(&tk, p.c.k, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.ks, rows) &&
-                  paged_map(&tv, p.c.v, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, rows)
+  p.box = paged_map(&tk, FP8, p.c.k, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.ks, cols, rows) &&
+                  paged_map(&tv, FP8, p.c.v, p.c.d, page, p.c.Hkv, p.c.num_pages, p.c.vs, cols, rows)
               ? rows
               : 0;
   kern<<<kPagedCtas, ChunkRoles<FP8>::kThreads, L::kTotal, stream>>>(tk, tv, p);
