@@ -65,27 +65,44 @@ __device__ __forceinline__ int find_from_start(const int32_t* cu, int B, int t) 
   return lo < B ? lo : -1;
 }
 
-// Quantises eight values of a row that LPR lanes hold; returns the codes, e + 127 in `be`.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Quantises eight values of a row that LPR lanes hold; returns the codes, e + 127 in `be`.  Every lane of
+// the warp calls it.
 template <int LPR>
 __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t m = 0;  // largest finite magnitude, as bf16 bits
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  // largest magnitude of the row, as bf16 bits, two values at a time
+  uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & kAbs, w[1] & kAbs), __vmaxu2(w[2] & kAbs, w[3] & kAbs));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-    m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+  for (int o = LPR / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+  uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+  if (__any_sync(0xffffffffu, m >= 0x7f80u)) {  // a row with infinities or NaN: its largest finite one
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
+      m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   }
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   // m = (1 + mant / 128) * 2^(E - 127), 1.75 = 1 + 96 / 128 (bf16 subnormals fall to the clamp)
   const int E = static_cast<int>(m >> 7), up = (m & 0x7fu) > 96u ? 1 : 0;
   const int b = min(max(E - 8 + up, 1), 246);
   be = static_cast<uint32_t>(b);
-  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);  // 2^-(b - 127)
+  // 2^-(b - 127): exact in bf16 but for products below 2^-126, which become codes of zero either way
+  const uint32_t inv = static_cast<uint32_t>(254 - b) * 0x00800080u;
   uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(w[i] << 16) * inv, hi = __uint_as_float(w[i] & 0xffff0000u) * inv;
+    const uint32_t y = mul_bf16x2(w[i], inv);
+    const float lo = __uint_as_float(y << 16), hi = __uint_as_float(y & 0xffff0000u);
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     h[i] = r;
@@ -93,8 +110,9 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// (code -> f16 -> bf16 are exact, and so is the product with a power of two, above bf16's subnormals.)
 __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t be) {
-  const float s = exp_scale(be);
+  const uint32_t s = (__float_as_uint(exp_scale(be)) >> 16) * 0x10001u;
   const uint32_t h[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
   uint32_t r[4];
 #pragma unroll
@@ -104,7 +122,7 @@ __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t be) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
         : "r"(f));
-    r[i] = pack_bf16x2(lo * s, hi * s);
+    r[i] = mul_bf16x2(pack_bf16x2(lo, hi), s);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
