@@ -3,10 +3,11 @@
 // Both move rows of d values between packed tokens and cache slots and are bound by
 // memory traffic (or, for a few tokens, by the latency of token -> sequence -> page ->
 // row).  All rows of a call, T tokens times Hkv heads times K and V, form one line of which
-// a warp takes kPasses times the two or four that its lanes move at once (LPR = 16 or 8 lanes
-// a row, eight values a lane): the sequence is searched once for them, and every row's load
-// is issued before the first is used.  (Four passes: eight, with fewer warps on an SM, took
-// 60 instead of 52 us for 82 thousand tokens of four bf16 heads.)
+// a warp takes PASSES times those that its lanes move at once: bf16 four times two or four rows
+// (LPR = 16 or 8 lanes a row, eight values a lane), e4m3 twice four or eight (8 or 4 lanes a row, 16
+// values a lane, so that codes too move 16 bytes at a time).  The sequence is searched once for them,
+// and every row's load is issued before the first is used.  (Four passes: eight, with fewer warps
+// on an SM, took 60 instead of 52 us for 82 thousand tokens of four bf16 heads.)
 //
 // e4m3: with m = max |x| of a row, e is the least integer with m <= 448 * 2^e, taken from
 // m's bits: 448 = 1.75 * 2^8, so e = E - 8 where m = f * 2^E has f <= 1.75 and E - 7
@@ -16,7 +17,10 @@
 namespace fdma {
 namespace {
 
-constexpr int kPasses = 4;
+template <bool FP8>
+struct Move {
+  static constexpr int kPasses = FP8 ? 2 : 4, kValues = FP8 ? 16 : 8, kVec = kValues / 8;
+};
 constexpr int kCacheThreads = 128;
 
 struct MoveParams {
@@ -71,21 +75,23 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Quantises eight values of a row that LPR lanes hold; returns the codes, e + 127 in `be`.  Every lane of
+// Quantises 16 values of a row that LPR lanes hold; returns the codes, e + 127 in `be`.  Every lane of
 // the warp calls it.
 template <int LPR>
-__device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+__device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint32_t& be) {
+  const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
   constexpr uint32_t kAbs = 0x7fff7fffu;
   // largest magnitude of the row, as bf16 bits, two values at a time
-  uint32_t m2 = __vmaxu2(__vmaxu2(w[0] & kAbs, w[1] & kAbs), __vmaxu2(w[2] & kAbs, w[3] & kAbs));
+  uint32_t m2 = w[0] & kAbs;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, w[i] & kAbs);
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
   uint32_t m = max(m2 & 0xffffu, m2 >> 16);
   if (__any_sync(0xffffffffu, m >= 0x7f80u)) {  // a row with infinities or NaN: its largest finite one
     m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
       m = max(m, max(a < 0x7f80u ? a : 0u, b < 0x7f80u ? b : 0u));
     }
@@ -98,16 +104,16 @@ __device__ __forceinline__ uint2 quantise8(uint4 x, uint32_t& be) {
   be = static_cast<uint32_t>(b);
   // 2^-(b - 127): exact in bf16 but for products below 2^-126, which become codes of zero either way
   const uint32_t inv = static_cast<uint32_t>(254 - b) * 0x00800080u;
-  uint32_t h[4];
+  uint32_t h[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {
     const uint32_t y = mul_bf16x2(w[i], inv);
     const float lo = __uint_as_float(y << 16), hi = __uint_as_float(y & 0xffff0000u);
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     h[i] = r;
   }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
 }
 
 // (code -> f16 -> bf16 are exact, and so is the product with a power of two, above bf16's subnormals.)
@@ -189,7 +195,7 @@ __device__ __forceinline__ void set_slot(const MoveParams& p, Slot& s, int pg, i
 
 template <bool FP8, int LPR, bool ONE>
 __global__ void __launch_bounds__(kCacheThreads) kv_append_kernel(const __grid_constant__ MoveParams p) {
-  constexpr int RPP = 32 / LPR, PASSES = kPasses;
+  constexpr int RPP = 32 / LPR, PASSES = Move<FP8>::kPasses, VEC = Move<FP8>::kVec;
   const int lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   int64_t tok0;
@@ -204,17 +210,17 @@ __global__ void __launch_bounds__(kCacheThreads) kv_append_kernel(const __grid_c
     rem = static_cast<int>(first - tok0 * (2 * p.c.Hkv));
   }
   if (tok0 >= p.T) return;
-  const int col = (lane % LPR) * 8;
+  const int col = (lane % LPR) * Move<FP8>::kValues;
   const bool in = col < p.c.d;
   // the rows themselves do not depend on the slot: load them while it is looked up
-  uint4 x[PASSES];
+  uint4 x[PASSES][VEC];
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
-    x[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (in && r.real)
-      x[i] = __ldg(reinterpret_cast<const uint4*>((r.is_v ? p.v_new : p.k_new) + r.tok * (r.is_v ? p.vn[0] : p.kn[0]) +
-                                                  r.g * (r.is_v ? p.vn[1] : p.kn[1]) + col));
+    const uint4* src = reinterpret_cast<const uint4*>((r.is_v ? p.v_new : p.k_new) + r.tok * (r.is_v ? p.vn[0] : p.kn[0]) +
+                                                      r.g * (r.is_v ? p.vn[1] : p.kn[1]) + col);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) x[i][e] = in && r.real ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
   }
   const int b0 = find_seq(p.cu, p.c.B, static_cast<int>(tok0), lane);
   Slot s;
@@ -236,27 +242,25 @@ __global__ void __launch_bounds__(kCacheThreads) kv_append_kernel(const __grid_c
   for (int i = 0; i < PASSES; ++i) {
     const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
     uint32_t be = 0;
-    uint2 q = make_uint2(0u, 0u);
-    if (FP8) q = quantise8<LPR>(x[i], be);
+    uint4 q = x[i][0];
+    if constexpr (FP8) q = quantise16<LPR>(x[i], be);
     if (!r.real) continue;
     if (!ONE && r.tok != s.tok) look_up(r.tok);
     if (!s.paged) continue;
     uint8_t* dst = const_cast<uint8_t*>(r.is_v ? p.c.v : p.c.k) + (r.is_v ? s.v : s.k) +
                    r.g * (r.is_v ? p.c.vs[2] : p.c.ks[2]);
+    if (in) *reinterpret_cast<uint4*>(dst + col * (FP8 ? 1 : 2)) = q;
     if (FP8) {
-      if (in) *reinterpret_cast<uint2*>(dst + col) = q;
       if (col == 0)
         const_cast<uint8_t*>(r.is_v ? p.c.ve : p.c.ke)[(r.is_v ? s.ve : s.ke) + r.g * (r.is_v ? p.c.ves[2] : p.c.kes[2])] =
             static_cast<uint8_t>(be);
-    } else if (in) {
-      *reinterpret_cast<uint4*>(dst + col * 2) = x[i];
     }
   }
 }
 
 template <bool FP8, int LPR, bool ONE>
 __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_constant__ MoveParams p) {
-  constexpr int RPP = 32 / LPR, PASSES = kPasses;
+  constexpr int RPP = 32 / LPR, PASSES = Move<FP8>::kPasses;
   const int lane = threadIdx.x & 31;
   const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   int64_t tok0;
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_c
     rem = static_cast<int>(first - tok0 * (2 * p.c.Hkv));
   }
   if (tok0 >= p.T) return;
-  const int col = (lane % LPR) * 8;
+  const int col = (lane % LPR) * Move<FP8>::kValues;
   const bool in = col < p.c.d;
   const int64_t cap = static_cast<int64_t>(p.c.max_pages) << p.c.page_shift;
   const int b0 = find_seq(p.cu, p.c.B, static_cast<int>(tok0), lane);
@@ -304,22 +308,18 @@ __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_c
     store |= 1u << i;
     if (!s.paged || !in) continue;
     const uint8_t* src = (r.is_v ? p.c.v : p.c.k) + (r.is_v ? s.v : s.k) + r.g * (r.is_v ? p.c.vs[2] : p.c.ks[2]);
-    if (FP8) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(src + col));
-      x[i].x = q.x;
-      x[i].y = q.y;
+    x[i] = __ldg(reinterpret_cast<const uint4*>(src + col * (FP8 ? 1 : 2)));
+    if (FP8)
       be[i] = (r.is_v ? p.c.ve : p.c.ke)[(r.is_v ? s.ve : s.ke) + r.g * (r.is_v ? p.c.ves[2] : p.c.kes[2])];
-    } else {
-      x[i] = __ldg(reinterpret_cast<const uint4*>(src + col * 2));
-    }
   }
   if (!in) return;
 #pragma unroll
   for (int i = 0; i < PASSES; ++i) {
     if (!((store >> i) & 1u)) continue;
     const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
-    *reinterpret_cast<uint4*>((r.is_v ? p.v_out : p.k_out) + (r.tok * p.c.Hkv + r.g) * p.c.d + col) =
-        FP8 ? dequantise8(make_uint2(x[i].x, x[i].y), be[i]) : x[i];
+    uint4* dst = reinterpret_cast<uint4*>((r.is_v ? p.v_out : p.k_out) + (r.tok * p.c.Hkv + r.g) * p.c.d + col);
+    dst[0] = FP8 ? dequantise8(make_uint2(x[i].x, x[i].y), be[i]) : x[i];
+    if (FP8) dst[1] = dequantise8(make_uint2(x[i].z, x[i].w), be[i]);
   }
 }
 
@@ -340,20 +340,20 @@ struct Gather {
 // no division a row and one lookup a warp.
 template <typename K>
 void launch_move(bool fp8, int d, int Hkv, unsigned blocks, const MoveParams& p, cudaStream_t stream, K) {
-  const int lpr = d > 64 ? 16 : 8;
-  const bool one = 2 * Hkv % (kPasses * (32 / lpr)) == 0;
+  const int rows = d > 64 ? 8 : 16;  // of a warp
+  const bool one = 2 * Hkv % rows == 0;
   void (*kern)(MoveParams);
-  if (lpr == 16)
-    kern = fp8 ? (one ? K::template kernel<true, 16, true>() : K::template kernel<true, 16, false>())
+  if (d > 64)
+    kern = fp8 ? (one ? K::template kernel<true, 8, true>() : K::template kernel<true, 8, false>())
                : (one ? K::template kernel<false, 16, true>() : K::template kernel<false, 16, false>());
   else
-    kern = fp8 ? (one ? K::template kernel<true, 8, true>() : K::template kernel<true, 8, false>())
+    kern = fp8 ? (one ? K::template kernel<true, 4, true>() : K::template kernel<true, 4, false>())
                : (one ? K::template kernel<false, 8, true>() : K::template kernel<false, 8, false>());
   kern<<<blocks, kCacheThreads, 0, stream>>>(p);
 }
 
 int64_t move_blocks(int T, int Hkv, int d) {
-  const int64_t rows = static_cast<int64_t>(T) * 2 * Hkv, per = kPasses * (kCacheThreads / (d > 64 ? 16 : 8));
+  const int64_t rows = static_cast<int64_t>(T) * 2 * Hkv, per = (d > 64 ? 8 : 16) * (kCacheThreads / 32);
   return (rows + per - 1) / per;
 }
 
