@@ -14,16 +14,22 @@
 //                   state out of their registers: spilled there it cost more than half the time);
 //   warps 1 and 2   look through the V tiles (by TMA) whose keys not every row sees: rows that nobody
 //                   sees become zeros, values that are not finite are cleared (fdma_paged.cuh);
-//                   the loads stay ahead meanwhile;
+//                   the loads stay ahead meanwhile; with an e4m3 cache they bring its codes (a box
+//                   for 16 keys) and its scale bytes instead, and the converting warps look;
 //   warps 4..7,     softmax of slot 0 and slot 1, one thread a row: masked only in tiles that some
 //   warps 8..11     row of the warp sees in part, exponentiated with a running maximum that is
 //                   raised only when it grows by 2^8 or more;
 //   warps 12..      bring Q, K and V into 128-byte-swizzled tiles: a ring of five bf16 tiles by TMA, a
 //                   box a page, or by cp.async where TMA cannot address the cache's layout or a page
-//                   is not there; of an e4m3 cache (a ring of four and two raw ones) the codes by
-//                   cp.async, which are then multiplied by their scale and stored as bf16 (exact).
+//                   is not there; or turn an e4m3 cache's codes into a ring of four tiles: multiplied
+//                   by their scale and stored as bf16 (exact).
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
+//
+// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 178 us, 1.45 PFLOP/s.  A slot's softmax
+// waits for its S and its next S for its P, about 3300 cycles a tile with the other slot's
+// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 130 us;
+// the conversion, 1300 cycles an item, and the longer softmax share the issue slots.
 #include "fdma_paged.cuh"
 
 namespace fdma {
@@ -32,13 +38,13 @@ namespace {
 constexpr int kChunkRows = kChunkItemRows;
 constexpr int kKeyTile = 128;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four, and kRaw raw ones, with e4m3)
-constexpr int kRaw = 2;
+constexpr int kRaw = 2;     // (four, and a ring of three, took 133 instead of 130 us below)
 constexpr int kScales = 4;  // tiles' scale bytes
 constexpr int kParts = 4;  // published parts
 constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
 // Loading warps and the division of the registers (setmaxnreg).  An e4m3 cache has eight loading warps,
 // because the conversion of its tiles to bf16 bounds it, and the softmax keeps less in registers for
-// it: two chunks of 333 to 1024 tokens over 4097 to 8192 keys, 32 heads, took 158 us with four warps, 133 with eight.
+// it: the e4m3 case above took 199 us with four such warps (and each row's scores in registers), 131 with eight.
 template <bool FP8>
 struct ChunkRoles {
   static constexpr int kLoadWarps = FP8 ? 8 : 4;

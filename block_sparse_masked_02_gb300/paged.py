@@ -109,6 +109,11 @@ def _on(dev, stream):
     return guard, torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _check_workspace(ws):
+    if ws is not None and not ws.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp):
     """The fields of fdma_kv_cache, in order."""
     shape = k_cache.shape
@@ -230,6 +235,7 @@ def make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=Non
               sinks=0, scale=None, workspace=None) -> FdmaPagedArgs:
     """fdma_paged_args of a call (see `fwd`)."""
     f = _fields(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp, v_exp, causal, window, sinks, scale)
+    _check_workspace(workspace)
     ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return FdmaPagedArgs.from_buffer_copy(_PACK_ARGS(*f, *ws))
 
@@ -258,6 +264,7 @@ def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_e
         raise ValueError("out must be contiguous bf16 (T, Hq, d)")
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (Hq, T) or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous fp32 (Hq, T)")
+    _check_workspace(workspace)
     guard, sp = _on(dev, stream)
 
     def call():

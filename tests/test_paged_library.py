@@ -144,3 +144,14 @@ def test_binding_refuses_cpu_tensors(P):
         P.empty_cache(4, 16, 2, 64, dtype=torch.float16, device="cpu")
     kc, vc, ke, ve = P.empty_cache(4, 16, 2, 64, dtype=torch.float8_e4m3fn, device="cpu")
     assert kc.shape == (4, 16, 2, 64) and ke.shape == (4, 16, 2) and kc.stride(3) == 1 and kc.stride(1) == 64
+
+
+def test_workspace_must_be_contiguous(P):
+    torch = pytest.importorskip("torch")
+    kc, vc, _, _ = P.empty_cache(4, 16, 2, 64, device="cpu")
+    table, lens, cu = torch.zeros(1, 2, dtype=torch.int32), torch.tensor([5], dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    P.make_args(q, kc, vc, table, lens, cu, 1, workspace=torch.empty(64, dtype=torch.uint8))
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 30), torch.empty(64, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            P.make_args(q, kc, vc, table, lens, cu, 1, workspace=ws)
