@@ -26,9 +26,9 @@
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 //
-// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 178 us, 1.45 PFLOP/s.  A slot's softmax
+// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 173 us, 1.49 PFLOP/s.  A slot's softmax
 // waits for its S and its next S for its P, about 3300 cycles a tile with the other slot's
-// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 130 us;
+// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 127 us;
 // the conversion, 1300 cycles an item, and the longer softmax share the issue slots.
 #include "fdma_paged.cuh"
 
@@ -39,7 +39,7 @@ constexpr int kChunkRows = kChunkItemRows;
 constexpr int kKeyTile = 128;
 constexpr int kRingTiles = 5;  // K and V tiles in shared memory (four, and kRaw raw ones, with e4m3)
 constexpr int kRaw = 2;     // (four, and a ring of three, took 133 instead of 130 us below)
-constexpr int kScales = 4;  // tiles' scale bytes
+constexpr int kScales = 2;  // tiles' scale bytes
 constexpr int kParts = 4;  // published parts
 constexpr int kLooks = 4;  // V tiles to be looked through: an entry is free again when the ring has gone round
 // Loading warps and the division of the registers (setmaxnreg).  An e4m3 cache has eight loading warps,
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       const uint64_t vd0 = sdesc_sw128(smem_u32(sR), 16384, 1024);   // MN-major view
       constexpr uint64_t step = static_cast<uint64_t>(L::kTile >> 4);
       Ring at;             // the next item to arrive: K_0, V_0, K_1, V_1, ...
-      int np[2] = {0, 0};  // P tiles consumed by each slot
+      uint32_t np = 0;  // parity of the P tiles consumed by each slot
       int nparts[2] = {0, 0};
       bool ok = true;
       auto arrived = [&]() {
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         const uint64_t vd = vd0 + slot * step;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          if (!wait(cPReady + 2 * w + hf, np[w] & 1)) return false;
+          if (!wait(cPReady + 2 * w + hf, (np >> w) & 1u)) return false;
           tc_fence_after();
           if (!one) continue;
 #pragma unroll
@@ -477,43 +477,63 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
             umma_ts(tbase + 256 + w * 128, tbase + w * 128 + k * 8, vd + static_cast<uint64_t>((k * 2048) >> 4), IDESC_O,
                     (!start || k > 0) ? 1u : 0u);
         }
-        ++np[w];
+        np ^= 1u << w;
         return true;
       };
       for (int idx = 0; ok; ++idx) {
         if (!(ok = part_ready(idx))) break;
-        const int n = parts[idx % kParts].n, ns = parts[idx % kParts].slots;
+        const int n = parts[idx % kParts].n;
+        const bool both = parts[idx % kParts].slots == 2;
         if (one) part_done(idx);
         if (n == 0) break;
         ++nparts[0];
-        if (ns == 2) ++nparts[1];
         if (!(ok = wait(cQFull, idx & 1))) break;
-        for (int k = 0; ok && k <= n; ++k) {
-          int vslot = 0, kslot = 0;
-          if (k > 0) {
-            if (!(ok = arrived())) break;
-            vslot = at.slot;
-            at.step();
-          }
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w >= ns) break;
+        // (a loop for each number of slots: with one for both, a 2048-token chunk took 177 instead of 173 us)
+        if (both) {
+          ++nparts[1];
+          for (int k = 0; ok && k <= n; ++k) {
+            int vslot = 0, kslot = 0;
             if (k > 0) {
-              if (!(ok = pv(w, vslot, k == 1))) break;
-              if (w == ns - 1 && one) umma_commit(&bars[cEmpty + vslot]);
-              if (k == n && one) umma_commit(&bars[cOFinal + w]);
+              if (!(ok = arrived())) break;
+              vslot = at.slot;
+              at.step();
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (k > 0) {
+                if (!(ok = pv(w, vslot, k == 1))) break;
+                if (w == 1 && one) umma_commit(&bars[cEmpty + vslot]);
+                if (k == n && one) umma_commit(&bars[cOFinal + w]);
+              }
+              if (k < n) {
+                if (w == 0) {
+                  if (!(ok = arrived())) break;
+                  kslot = at.slot;
+                  at.step();
+                }
+                issue_s(w, kslot);
+              }
+            }
+            if (ok && k < n && one) umma_commit(&bars[cEmpty + kslot]);
+            if (ok && k == n - 1 && one) umma_commit(&bars[cQEmpty]);
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; ok && k <= n; ++k) {
+            if (k > 0) {
+              if (!(ok = arrived() && pv(0, at.slot, k == 1))) break;
+              if (one) umma_commit(&bars[cEmpty + at.slot]);
+              if (k == n && one) umma_commit(&bars[cOFinal]);
+              at.step();
             }
             if (k < n) {
-              if (w == 0) {
-                if (!(ok = arrived())) break;
-                kslot = at.slot;
-                at.step();
-              }
-              issue_s(w, kslot);
+              if (!(ok = arrived())) break;
+              issue_s(0, at.slot);
+              if (one) umma_commit(&bars[cEmpty + at.slot]);
+              if (k == n - 1 && one) umma_commit(&bars[cQEmpty]);
+              at.step();
             }
           }
-          if (ok && k < n && one) umma_commit(&bars[cEmpty + kslot]);
-          if (ok && k == n - 1 && one) umma_commit(&bars[cQEmpty]);
         }
       }
       __syncwarp();
@@ -685,7 +705,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
     const uint32_t scol = w * 128, ocol = 256 + w * 128;
     const float cexp = p.scale_log2;
     const uint64_t c2 = f2(cexp, cexp);
-    int ns = 0, ended = 0;  // S tiles and parts of this slot so far
+    uint32_t parity = 0;  // of this slot's S tiles (bit 0) and parts (bit 1) so far
     bool ok = true;
     for (int idx = 0; ok; ++idx) {
       if (!(ok = part_ready(idx))) break;
@@ -697,13 +717,12 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         const int R = s.row0 + row, last = s.nq * p.G - 1;
         const int pos = s.pos0 + min(R, last) / p.G;
         const int rhi = p.causal ? pos + 1 : s.klen, rlo = p.window > 0 ? pos - p.window + 1 : 0;
-        const PartTiles tiles(s);
         float m = kNInf, l = 0.f;
-        for (int k = 0; k < n; ++k, ++ns) {
-          const int j0 = tiles.key0(k);
+        for (int k = 0; k < n; ++k, parity ^= 1u) {
+          const int j0 = PartTiles(s).key0(k);  // (not kept: there is no register to spare here)
           const int hi = rhi - j0, lo = rlo - j0, sk = p.sinks - j0;
           const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
-          if (!(ok = wait(cSFull + w, ns & 1))) break;
+          if (!(ok = wait(cSFull + w, parity & 1u))) break;
           tc_fence_after();
           auto mask32 = [&](int a, uint32_t (&x)[32]) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
@@ -813,8 +832,8 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         }
         if (!ok) break;
         // ---- the part's end
-        if (!(ok = wait(cOFinal + w, ended & 1))) break;
-        ++ended;
+        if (!(ok = wait(cOFinal + w, parity >> 1))) break;
+        parity ^= 2u;
         tc_fence_after();
         const bool real = R <= last, whole = s.whole, odd = *const_cast<volatile int*>(&s.odd) != 0;
         const int tok = real ? R / p.G : 0;
