@@ -178,10 +178,16 @@ __device__ __forceinline__ int item_places(const PagedParams& p, const Seq& s, i
   return k > 0 ? k + kItemCost : 0;
 }
 
+// a / b, a >= 0 and b > 0.  (A 64-bit division takes 400 cycles, and every CTA waits for these.)
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+  return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 struct PlanSmem {
   int64_t warp_sum[32];
   int64_t total;
   int b, g, rt, t;
+  Seq s;
 };
 
 // Finds this CTA's run: every thread of the CTA calls it (NT threads).  False where it has no
@@ -202,7 +208,13 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
     return n;
   };
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += static_cast<int64_t>(seq_places(load_seq(p, b, blockIdx.x == 0))) * p.c.Hkv;
+  Seq s{};  // the last one, and its places: usually a group has one sequence
+  int n = 0;
+  for (int b = b0; b < b1; ++b) {
+    s = load_seq(p, b, blockIdx.x == 0);
+    n = seq_places(s);
+    mine += static_cast<int64_t>(n) * p.c.Hkv;
+  }
   __syncwarp();
   int64_t x = sub == 0 ? mine : 0;
 #pragma unroll
@@ -218,19 +230,21 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
     if (w < warp) before += sm->warp_sum[w];
     total += sm->warp_sum[w];
   }
-  quota = static_cast<int>(max((total + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(p.min_run)));
+  quota = static_cast<int>(max(quotient(total + kPagedCtas - 1, kPagedCtas), static_cast<int64_t>(p.min_run)));
   const int64_t start = static_cast<int64_t>(blockIdx.x) * quota;
   if (start >= before && start < before + mine) {  // (one group of lanes)
     int64_t left = start - before;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq(p, b, false);
-      const int n = seq_places(s);
+      if (b1 - b0 > 1) {
+        s = load_seq(p, b, false);
+        n = seq_places(s);
+      }
       if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
         left -= static_cast<int64_t>(n) * p.c.Hkv;
         continue;
       }
-      const int g = static_cast<int>(left / n);
-      int t = static_cast<int>(left % n);
+      const int g = static_cast<int>(quotient(left, n));
+      int t = static_cast<int>(left - static_cast<int64_t>(g) * n);
       for (int rt = sub;; rt += L) {
         const int k = item_places<ROWS, KT>(p, s, rt);
         int sum = k;
@@ -243,6 +257,7 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
           sm->g = g;
           sm->rt = rt;
           sm->t = t - (sum - k);
+          sm->s = s;
         }
         const int all = __shfl_sync(group, sum, L - 1, L);
         if (t < all) break;
@@ -257,7 +272,7 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
   c.g = sm->g;
   c.rt = sm->rt;
   c.t = sm->t;
-  c.s = load_seq(p, c.b, false);
+  c.s = sm->s;
   c.span(p);
   c.left = static_cast<int>(min(static_cast<int64_t>(quota), total - start));
   if (c.t >= c.r.tiles) {  // between two items: the run's tiles begin with the next

@@ -61,6 +61,7 @@ class FdmaPagedArgs(ctypes.Structure):
 _CACHE_FMT = "7iP3qP3qP3qP3qPqP"
 _PACK_CACHE = struct.Struct(_CACHE_FMT).pack
 _PACK_ARGS = struct.Struct(_CACHE_FMT + "2iP2qP4ifPN").pack
+_PACK_WORKSPACE = struct.Struct("PN").pack  # the last two fields
 
 _LIB = None
 
@@ -271,10 +272,11 @@ def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_e
         lib = load()
         o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if out is None else out
         s = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+        args = _PACK_ARGS(*f, 0, 0)
         ws = workspace
         if ws is None:
-            ws = torch.empty(lib.fdma_paged_workspace_size(_PACK_ARGS(*f, 0, 0)), dtype=torch.uint8, device=dev)
-        args = _PACK_ARGS(*f, ws.data_ptr(), ws.numel() * ws.element_size())
+            ws = torch.empty(lib.fdma_paged_workspace_size(args), dtype=torch.uint8, device=dev)
+        args = args[:-16] + _PACK_WORKSPACE(ws.data_ptr(), ws.numel() * ws.element_size())
         return o, s, lib.fdma_paged_fwd(args, o.data_ptr(), s.data_ptr(), sp)
 
     if guard is None:

@@ -45,6 +45,7 @@ def test_packed_bytes_are_the_structs(P):
     assert (a.T, a.Hq, a.q, list(a.q_stride), a.cu_q) == (61, 62, 63, [64, 65], 66)
     assert (a.max_q, a.causal, a.window, a.sinks, a.scale, a.workspace, a.workspace_bytes) == (67, 1, 69, 70, 0.5, 72, 73)
     assert len(P._PACK_ARGS(*c, *([0] * 10), 0.0, 0, 0)) == ctypes.sizeof(P.FdmaPagedArgs)
+    assert bytes(a)[-16:] == P._PACK_WORKSPACE(72, 73)
 
 
 FAKE = 1 << 20  # never dereferenced: the arguments are refused first
