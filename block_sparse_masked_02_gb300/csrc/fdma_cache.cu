@@ -120,15 +120,15 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint32_t& be) {
 // (code -> f16 -> bf16 are exact, and so is the product with a power of two, above bf16's subnormals.)
 __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t be) {
   const uint32_t s = (__float_as_uint(exp_scale(be)) >> 16) * 0x10001u;
-  const uint32_t h[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
-  uint32_t r[4];
+  uint32_t f[4], r[4];
+  e4m3x4_to_f16x4(q.x, f[0], f[1]);
+  e4m3x4_to_f16x4(q.y, f[2], f[3]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t f = e4m3x2_to_f16x2(h[i]);
     float lo, hi;
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
         : "=f"(lo), "=f"(hi)
-        : "r"(f));
+        : "r"(f[i]));
     r[i] = mul_bf16x2(pack_bf16x2(lo, hi), s);
   }
   return make_uint4(r[0], r[1], r[2], r[3]);

@@ -35,8 +35,8 @@ namespace fdma {
 namespace {
 
 // Packed rows up to which the token kernel runs.  With 17 to 24 rows (8 kv heads, d 128) of 16
-// sequences of 4096 keys it took 69 us and the chunk kernel 59 (e4m3: 81 and 77; of one sequence of
-// 32768 keys 41 and 41, e4m3 42 and 46), with 9 to 16 rows 57 and 59 (e4m3 54 and 76).
+// sequences of 4096 keys it took 69 us and the chunk kernel 59 (e4m3: 81 and 73; of one sequence of
+// 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 53 and 73).
 constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
 
@@ -337,8 +337,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const uint32_t a[4] = {e4m3x2_to_f16x2(aw[e]), e4m3x2_to_f16x2(bw[e]), e4m3x2_to_f16x2(aw[e] >> 16),
-                                     e4m3x2_to_f16x2(bw[e] >> 16)};
+              uint32_t a[4];
+              e4m3x4_to_f16x4(aw[e], a[0], a[2]);
+              e4m3x4_to_f16x4(bw[e], a[1], a[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816<true>(s[g][nt], a, qf[nt][c * 4 + e][0], qf[nt][c * 4 + e][1]);
             }
@@ -453,10 +454,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             ldsm4_t(w, sv + swz<ROWB>(g * 16 + vr, c + vc));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a[4] = {e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0020)),
-                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h], 0u, 0x0031)),
-                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0020)),
-                                     e4m3x2_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x0031))};
+              uint32_t a[4];
+              e4m3x4_to_f16x4(__byte_perm(w[2 * h], 0u, 0x3120), a[0], a[1]);
+              e4m3x4_to_f16x4(__byte_perm(w[2 * h + 1], 0u, 0x3120), a[2], a[3]);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma16816<true>(o[nt][c + h], a, pb[g][nt][0], pb[g][nt][1]);
             }

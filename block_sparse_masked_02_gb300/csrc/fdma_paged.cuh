@@ -327,11 +327,11 @@ __device__ __forceinline__ float paged_ex2(float x) {
 // 2^(e - 127) of a scale byte
 __device__ __forceinline__ float exp_scale(uint32_t e) { return __uint_as_float(e == 0 ? 0x00400000u : e << 23); }
 
-// Two e4m3 codes (low byte first) as f16, exact (NaN stays NaN).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
+// Four e4m3 codes (low byte first) as f16, exact (NaN stays NaN).
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 // ---- Values that are not finite, in keys that only some rows of a block see.  In the product with

@@ -26,9 +26,9 @@
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 //
-// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 173 us, 1.49 PFLOP/s.  A slot's softmax
+// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 169 us, 1.52 PFLOP/s.  A slot's softmax
 // waits for its S and its next S for its P, about 3300 cycles a tile with the other slot's
-// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 127 us;
+// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 124 us;
 // the conversion, 1300 cycles an item, and the longer softmax share the issue slots.
 #include "fdma_paged.cuh"
 
@@ -370,12 +370,13 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
               uint32_t o[8];
 #pragma unroll
+              for (int h = 0; h < 4; ++h) e4m3x4_to_f16x4(w[h], o[2 * h], o[2 * h + 1]);
+#pragma unroll
               for (int h = 0; h < 8; ++h) {
-                const uint32_t f = e4m3x2_to_f16x2(w[h >> 1] >> (16 * (h & 1)));
                 float a, c;
                 asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.f32.f16 %0, x;\n\tcvt.f32.f16 %1, y;\n\t}"
                     : "=f"(a), "=f"(c)
-                    : "r"(f));
+                    : "r"(o[h]));
                 f2split(mul2(f2(a, c), sc2), a, c);
                 o[h] = pack_bf16x2(a, c);
               }
