@@ -595,6 +595,40 @@ def test_broadcast_heads_of_a_cache(P):
         P.kv_append(k, k, *at, _cu([1]))
 
 
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_broadcast_heads_of_an_e4m3_cache(P, d):
+    """Rows and scale bytes that kv heads share (stride 0), for single tokens and chunks of one and two slots of rows."""
+    s = Setup(P, [500, 77], 1, d, 16, True, seed=4)
+    heads = lambda x: x.expand(*x.shape[:2], 4, *x.shape[3:])
+    t = Setup.__new__(Setup)
+    t.d, t.Hkv, t.fp8 = d, 4, True
+    t.K, t.V = [np.repeat(x, 4, 1) for x in s.K], [np.repeat(x, 4, 1) for x in s.V]
+    for news in ([1, 1], [30, 7], [150, 77]):
+        q = _queries(sum(news), 8, d)
+        out, lse = P.fwd(q, heads(s.kc), heads(s.vc), s.table, s.k_lens, _cu(news), max(news), k_exp=heads(s.ke),
+                         v_exp=heads(s.ve))
+        _check_attention(t, q, news, out, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window", [0, 100])
+def test_keys_of_a_page_that_is_not_there_read_as_zeros(P, fp8, window):
+    from block_sparse_masked_02_gb300 import fdma
+
+    s = Setup(P, [600, 333], 2, 128, 16, fp8, seed=6)
+    table = s.table.clone()
+    table[0, 3], table[0, 36], table[1, 20] = -1, s.num, 1 << 30
+    for b, pages in ((0, (3, 36)), (1, (20,))):
+        for x in pages:
+            s.K[b][16 * x:16 * x + 16] = 0
+            s.V[b][16 * x:16 * x + 16] = 0
+    for news in ([1, 1], [5, 20], [40, 333]):
+        q = _queries(sum(news), 8, 128)
+        out, lse = P.fwd(q, s.kc, s.vc, table, s.k_lens, _cu(news), max(news), window=window, sinks=9 if window else 0, **s.ex)
+        assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+        _check_attention(s, q, news, out, lse, window=window, sinks=9 if window else 0)
+
+
 # ------------------------------------------------------------------------------------------------ refusals
 def test_bad_device_arrays_are_reported_and_not_followed(P):
     """Page numbers, lengths and offsets out of range: nothing is read or written there, the rest is right,
