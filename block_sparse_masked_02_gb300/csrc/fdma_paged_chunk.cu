@@ -26,9 +26,9 @@
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 //
-// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 169 us, 1.52 PFLOP/s.  A slot's softmax
+// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 172 us, 1.50 PFLOP/s.  A slot's softmax
 // waits for its S and its next S for its P, about 3300 cycles a tile with the other slot's
-// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 124 us;
+// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 126 us;
 // the conversion, 1300 cycles an item, and the longer softmax share the issue slots.
 #include "fdma_paged.cuh"
 
@@ -207,6 +207,9 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
   uint8_t* sR = smem + L::kOffRing;
   auto wait = [&](int bar, uint32_t parity) { return mbar_wait(&bars[bar], parity, p.err, kDevErrTimeout, abort_flag); };
 
+  // For whole warps that go on to warp-wide instructions: every lane gets the same answer, whichever of them
+  // saw the time-out, so that none waits for lanes that have left (1 % of the time of a call).
+  auto wait_all = [&](int bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   // For the roles that have nothing to do for most of a run, however long it is; a time-out of
   // another role ends these waits too.
   auto idle_wait = [&](int bar, uint32_t parity) {
@@ -217,6 +220,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
   Look* look_at = reinterpret_cast<Look*>(smem + L::kOffLooks);
   // The idx-th part of the run; false on a time-out.
   auto part_ready = [&](int idx) { return wait(cPart + idx % kParts, (idx / kParts) & 1); };
+  auto part_ready_all = [&](int idx) { return wait_all(cPart + idx % kParts, (idx / kParts) & 1); };
   auto part_done = [&](int idx) { mbar_arrive(&bars[cPartFree + idx % kParts]); };
 
   if (warp >= 12) {
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[bar]);
     };
-    auto slot_free = [&](int item) { return item < L::kRing || wait(cEmpty + at.slot, at.phase ^ 1); };
+    auto slot_free = [&](int item) { return item < L::kRing || wait_all(cEmpty + at.slot, at.phase ^ 1); };
     // A thread has one 16-byte column (of the cache's row) of NP rows r0 + i * RPP; with an e4m3 cache these
     // are of the warp's group of 16 keys.
     constexpr int CPR = FP8 ? D / 16 : D / 8, RPP = (FP8 ? 32 : LT) / CPR, NP = (FP8 ? 16 : 128) / RPP;
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
     // (Rolled loops and one copy of each step: with the steps unrolled and inlined twice the roles'
     // code fell out of the instruction cache and everything ran at half speed.)
     for (int idx = 0; ok; ++idx) {
-      if (!(ok = part_ready(idx))) break;
+      if (!(ok = part_ready_all(idx))) break;
       Part& s = parts[idx % kParts];
       // (copies: what lies in shared memory is read again after every barrier)
       const int n = s.n, b = s.b, g_kv = s.g, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi, all_lo = s.all_lo, all_hi = s.all_hi;
@@ -339,8 +343,8 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         } else {
           // ---- the warp's 16 rows become bf16
           const int tile = it >> 1, place = it % kRaw;
-          if (!is_v && !(ok = wait(cScale + tile % kScales, (tile / kScales) & 1))) break;
-          if (!(ok = wait(cRaw + place, (it / kRaw) & 1) && slot_free(it))) break;
+          if (!is_v && !(ok = wait_all(cScale + tile % kScales, (tile / kScales) & 1))) break;
+          if (!(ok = wait_all(cRaw + place, (it / kRaw) & 1) && slot_free(it))) break;
           const uint32_t src = raw + place * (128 * D);
           const uint8_t* exps = smem + L::kOffScale + tile % kScales * 256 + is_v * 128 + r0;
           const bool here = !((reinterpret_cast<const int*>(smem + L::kOffAbsent)[place] >> (warp - 12)) & 1);
@@ -396,7 +400,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         ++it;
         // ---- the part's Q, behind its first loads
         if (i2 == (FP8 ? 0 : 1)) {
-          if (idx > 0 && !(ok = wait(cQEmpty, (idx - 1) & 1))) break;
+          if (idx > 0 && !(ok = wait_all(cQEmpty, (idx - 1) & 1))) break;
           constexpr int QCPR = D / 8;
           const int qc = lt % QCPR, row0 = s.row0, q0 = s.q0, h0 = s.g * p.G, rows = s.nq * p.G - row0;
           const uint32_t qb = qc * 8 < p.c.d ? 16u : 0u;
@@ -547,7 +551,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       int tile = 0, issued = 0;  // tiles so far in the run; items on their way
       bool ok = true;
       for (int idx = 0; ok; ++idx) {
-        if (!(ok = part_ready(idx))) break;
+        if (!(ok = part_ready_all(idx))) break;
         const Part& s = parts[idx % kParts];
         const int n = s.n, b = s.b, g = s.g, lo = s.lo, hi = s.hi, sink_hi = s.sink_hi;
         const PartTiles tiles(s);
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
 #pragma unroll 1
             for (int is_v = 0; is_v < 2; ++is_v) {
               const int it = 2 * tile + is_v, place = it % kRaw;
-              if (it >= kRaw && !(ok = wait(cRawFree + place, (it / kRaw - 1) & 1))) break;
+              if (it >= kRaw && !(ok = wait_all(cRawFree + place, (it / kRaw - 1) & 1))) break;
               uint8_t* to = raw + place * (128 * D);
               uint64_t* bar = &bars[cRaw + place];
               if (lane == 0) {
@@ -621,7 +625,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
                 e[is_v] = x[is_v][0] | x[is_v][1] << 8 | x[is_v][2] << 16 | x[is_v][3] << 24;
             }
             const int place = tile % kScales;
-            if (tile >= kScales && !(ok = wait(cScaleFree + place, (tile / kScales - 1) & 1))) break;
+            if (tile >= kScales && !(ok = wait_all(cScaleFree + place, (tile / kScales - 1) & 1))) break;
             uint32_t* to = reinterpret_cast<uint32_t*>(smem + L::kOffScale + place * 256) + lane;
             to[0] = e[0];
             to[32] = e[1];
@@ -642,7 +646,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
       const int chunk = (tid - 32) % CPR, r0 = (tid - 32) / CPR;
       // (rows eight apart have a column of pieces at equal distances)
       for (int i = 0;; ++i) {
-        if (!idle_wait(cLook + i % kLooks, (i / kLooks) & 1)) break;
+        if (!__all_sync(0xffffffffu, idle_wait(cLook + i % kLooks, (i / kLooks) & 1))) break;
         const Look k = look_at[i % kLooks];
         if (k.slot < 0) break;
         Part& s = parts[k.part % kParts];
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
     uint32_t parity = 0;  // of this slot's S tiles (bit 0) and parts (bit 1) so far
     bool ok = true;
     for (int idx = 0; ok; ++idx) {
-      if (!(ok = part_ready(idx))) break;
+      if (!(ok = part_ready_all(idx))) break;
       const Part& s = parts[idx % kParts];
       const int n = s.n;
       if (n == 0) break;
@@ -723,7 +727,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
           const int j0 = PartTiles(s).key0(k);  // (not kept: there is no register to spare here)
           const int hi = rhi - j0, lo = rlo - j0, sk = p.sinks - j0;
           const bool masked = !__all_sync(0xffffffffu, hi >= 128 && (lo <= 0 || sk >= 128));
-          if (!(ok = wait(cSFull + w, parity & 1u))) break;
+          if (!(ok = wait_all(cSFull + w, parity & 1u))) break;
           tc_fence_after();
           auto mask32 = [&](int a, uint32_t (&x)[32]) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
         }
         if (!ok) break;
         // ---- the part's end
-        if (!(ok = wait(cOFinal + w, parity >> 1))) break;
+        if (!(ok = wait_all(cOFinal + w, parity >> 1))) break;
         parity ^= 2u;
         tc_fence_after();
         const bool real = R <= last, whole = s.whole, odd = *const_cast<volatile int*>(&s.odd) != 0;
