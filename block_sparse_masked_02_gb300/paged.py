@@ -132,19 +132,17 @@ def _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp):
     if mp > 1 and tc != 1:
         raise ValueError("page_table must have a contiguous last dimension")
     _check_int("k_lens", k_lens, B)
-    head = (B, h, d)
-    tail = (page_table.data_ptr(), ts, k_lens.data_ptr())
     rows = (n, ps, mp, k_cache.data_ptr(), sk[0], sk[1], sk[2], v_cache.data_ptr(), sv[0], sv[1], sv[2])
     if dt is torch.bfloat16 and v_cache.dtype is dt:
         if k_exp is not None or v_exp is not None:
             raise ValueError("k_exp and v_exp belong to float8_e4m3fn caches")
-        return head + (FDMA_CACHE_BF16,) + rows + (0, 0, 0, 0, 0, 0, 0, 0) + tail
+        return (B, h, d, FDMA_CACHE_BF16, *rows, 0, 0, 0, 0, 0, 0, 0, 0, page_table.data_ptr(), ts, k_lens.data_ptr())
     if dt is torch.float8_e4m3fn and v_cache.dtype is dt:
         for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
             if t is None or t.dtype is not torch.uint8 or t.shape != shape[:3]:
                 raise ValueError(f"{name} must be uint8 (num_pages, page_size, Hkv) for a float8_e4m3fn cache")
-        return head + (FDMA_CACHE_E4M3,) + rows + (k_exp.data_ptr(), *k_exp.stride(), v_exp.data_ptr(),
-                                                   *v_exp.stride()) + tail
+        return (B, h, d, FDMA_CACHE_E4M3, *rows, k_exp.data_ptr(), *k_exp.stride(), v_exp.data_ptr(), *v_exp.stride(),
+                page_table.data_ptr(), ts, k_lens.data_ptr())
     raise ValueError("k_cache and v_cache must both be bfloat16 or both float8_e4m3fn")
 
 
@@ -228,8 +226,8 @@ def _fields(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, k_exp, v_exp, 
     if q.dtype is not torch.bfloat16 or len(sq) != 3 or q.shape[2] != c[2] or sq[2] != 1:
         raise ValueError("q must be bf16 (T, Hq, d) with a contiguous head dim")
     T, Hq, d = q.shape
-    return c + (T, Hq, q.data_ptr(), sq[0], sq[1], cu_q.data_ptr(), int(max_q), 1 if causal else 0, int(window),
-                int(sinks), d ** -0.5 if scale is None else float(scale))
+    return (*c, T, Hq, q.data_ptr(), sq[0], sq[1], cu_q.data_ptr(), int(max_q), 1 if causal else 0, int(window),
+            int(sinks), d ** -0.5 if scale is None else float(scale))
 
 
 def make_args(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0,
@@ -250,6 +248,22 @@ def alloc_workspace(args: FdmaPagedArgs, device) -> torch.Tensor:
     return torch.empty(workspace_size(args), dtype=torch.uint8, device=device)
 
 
+def _launch_fwd(f, T, Hq, d, dev, sp, ws, out, lse):
+    lib = load()
+    args = _PACK_ARGS(*f, 0, 0)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = torch.empty(lib.fdma_paged_workspace_size(args), dtype=torch.uint8, device=dev)
+    st = lib.fdma_paged_fwd(args[:-16] + _PACK_WORKSPACE(ws.data_ptr(), ws.numel() * ws.element_size()), out.data_ptr(),
+                            lse.data_ptr(), sp)
+    if st:
+        _fdma._raise(st, "fdma_paged_fwd")
+    return out, lse
+
+
 def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_exp=None, causal=True, window=0, sinks=0,
         scale=None, workspace: Optional[torch.Tensor] = None, out=None, lse=None, stream=None):
     """Attention of the packed new tokens q (T, Hq, d) over the cache: (out (T, Hq, d) bf16, lse (Hq, T) fp32).
@@ -267,22 +281,7 @@ def fwd(q, k_cache, v_cache, page_table, k_lens, cu_q, max_q, *, k_exp=None, v_e
         raise ValueError("lse must be contiguous fp32 (Hq, T)")
     _check_workspace(workspace)
     guard, sp = _on(dev, stream)
-
-    def call():
-        lib = load()
-        o = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev) if out is None else out
-        s = torch.empty((Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-        args = _PACK_ARGS(*f, 0, 0)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib.fdma_paged_workspace_size(args), dtype=torch.uint8, device=dev)
-        args = args[:-16] + _PACK_WORKSPACE(ws.data_ptr(), ws.numel() * ws.element_size())
-        return o, s, lib.fdma_paged_fwd(args, o.data_ptr(), s.data_ptr(), sp)
-
     if guard is None:
-        o, s, st = call()
-    else:
-        with guard:
-            o, s, st = call()
-    _fdma._raise(st, "fdma_paged_fwd")
-    return o, s
+        return _launch_fwd(f, T, Hq, d, dev, sp, workspace, out, lse)
+    with guard:
+        return _launch_fwd(f, T, Hq, d, dev, sp, workspace, out, lse)
