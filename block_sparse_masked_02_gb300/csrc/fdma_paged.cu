@@ -22,11 +22,19 @@
 // e4m3 caches: codes become f16 exactly (one conversion for two), so the products run in f16.
 // q is scaled by a power of two per row to [2^14, 2^15), which is exact but for parts below
 // 2^-38 of the row's largest.  The key's scale multiplies S; the value's scale multiplies P,
-// as 2^(e - r + 15) with r the largest e so far (the output is kept in units of 2^(r - 15)), so
-// that P stays in f16's range and a weight keeps all 11 bits down to 2^-29 of the largest.
+// as 2^(e - r + 15) with r the largest e so far of the keys that the row sees (its output is kept in
+// units of 2^(r - 15)), so that P stays in f16's range: a weight keeps 11 bits, or 2^(r - e - 40) where
+// that is more, at most 2^-24 because e and r are at most 16 apart.  A row that sees scales further
+// apart ("wide") goes on in fp32 products of its own, in units of 1: with f16 weights a large value would
+// take the weights of all others away, in columns where it is 0 and where its own weight is 0 too.
+// What a row gets so depends on the keys that it sees alone.  Value rows of zeros do not make it wide.
+// (Keeping a unit for each row costs 4 to 5 % with several tokens a sequence and nothing with one; all rows wide,
+// two sequences of 65 thousand keys take 2.5 times as long.)
 // A key is half the bytes and has the conversions on top, so a warp takes 32 keys a step: two
 // independent chains of products and half the bookkeeping a key.
 #include <cmath>
+
+#include <cuda_fp16.h>
 
 #include "fdma_paged.cuh"
 
@@ -39,6 +47,39 @@ namespace {
 // 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 53 and 73).
 constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
+constexpr int kNarrow = 16;  // value scales of an f16 row are at most 2^16 apart
+
+// The largest value scale byte that a row has seen in the low half, 255 less the least one in the high half (0: none):
+// both grow, so a maximum by halves takes more keys in.
+__device__ __forceinline__ uint32_t scale_span(uint32_t most, uint32_t least) { return most | (255u - least) << 16; }
+__device__ __forceinline__ bool wide_span(uint32_t s) { return (s & 0xffffu) + (s >> 16) > 255u + kNarrow; }
+
+// (The following two hardly ever run: out of line, so that the loop stays in the instruction cache.)
+// True if the `pieces` 16-byte pieces of codes at `at` are zeros.
+__device__ __noinline__ bool zero_row(uint32_t at, int pieces) {
+  uint32_t any = 0;
+#pragma unroll 1
+  for (int c = 0; c < pieces; ++c) {
+    uint32_t x, y, z, w;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x), "=r"(y), "=r"(z), "=r"(w) : "r"(at + c * 16) : "memory");
+    any |= x | y | z | w;
+  }
+  return (any & 0x7f7f7f7fu) == 0;
+}
+// Of 32 keys' scale bytes, those that a row with these first and last keys sees, but for those in `none`.  The
+// eight lanes of a row (lane & 3 the same) call it together.
+__device__ __noinline__ uint32_t seen_span(const uint8_t* bytes, int first, int end, int sinks, unsigned none) {
+  uint32_t x = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = static_cast<int>(lane_id() >> 2) + 8 * i;
+    const uint32_t b = bytes[k];
+    if (b != 0 && !((none >> k) & 1u) && k < end && (k >= first || k < sinks)) x = __vmaxu2(x, scale_span(b, b));
+  }
+#pragma unroll
+  for (int i = 4; i < 32; i <<= 1) x = __vmaxu2(x, __shfl_xor_sync(0xffffffffu, x, i));
+  return x;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -235,7 +276,8 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   float o[NT][D / 16][4];      // O^T: head dim n8 (+ 8; e4m3: 2 * n8 + {0, 1}) of each 16, rows 2 * q4 + {0, 1}
   float m[NT][2], l[NT][2];
   int full_lo = 0, full_hi = 0;  // keys that every row sees
-  int ref = 0;                   // e4m3: the largest value scale byte so far
+  bool any_wide = false;         // e4m3: some row of the warp is wide
+  uint32_t span[NT][2];          // e4m3: value scales of the keys that the row has seen (scale_span)
   int seg0 = 0;                  // tile of the item at which this CTA began
   int stage = 0;
   bool first_seg = true, begin = true;
@@ -297,6 +339,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           rhi[nt][e] = rk.hi;
           m[nt][e] = kNInf;
           l[nt][e] = 0.f;
+          span[nt][e] = 0;
         }
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -308,8 +351,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         full_hi = row_keys(p, cc.s, cc.s.pos0 + i0).hi;
         full_lo = row_keys(p, cc.s, cc.s.pos0 + i1).lo;
       }
-      ref = 0;
-      odd = false;
+      odd = any_wide = false;
     }
     if (x >= 0) cp_async_wait<NST - 2>();
     __syncwarp();
@@ -319,6 +361,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
     const int j0 = cc.key0() + warp * STEP;
     if (some_seen(cc.r, j0, STEP)) {
       const uint32_t sk = ring + stage * 2 * L::kHalfB, sv = sk + L::kHalfB;
+      const bool masked = j0 < full_lo || j0 + STEP > full_hi;
       // ---- S^T = K Q^T: keys j0 + 16 * g + n8 (+ 8), rows 2 * q4 + {0, 1} of each eight
       float s[KG][NT][4];
 #pragma unroll
@@ -355,26 +398,103 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             for (int nt = 0; nt < NT; ++nt) mma16816<false>(s[g][nt], a, qf[nt][ks][0], qf[nt][ks][1]);
           }
       }
-      float kf[KG][2], vf[KG][2];  // scales of keys n8, n8 + 8 of each group
-      float oscale = 1.f;
+      float kf[KG][2];    // scales of keys n8, n8 + 8 of each group
+      uint32_t vx[KG][2];  // and their values' scale bytes (0: not there, or a row of zeros)
+      const uint8_t* ex = sexp + stage * 2 * STEP;
+      float grow[NT][2];   // what the output's unit changes by
+      bool plain = false;  // every key is there and no larger than any row's unit, no row is wide
       if (FP8) {
-        const uint8_t* ex = sexp + stage * 2 * STEP;
-        const int mx = __reduce_max_sync(0xffffffffu, static_cast<int>(ex[STEP + lane]));
-        if (mx > ref) {  // the output's unit grows
-          oscale = ref == 0 ? 0.f : __uint_as_float(static_cast<uint32_t>(max(127 - (mx - ref), 0)) << 23);
-          ref = mx;
+        uint32_t ve = ex[STEP + lane];
+        uint32_t least = __reduce_min_sync(0xffffffffu, ve);
+        plain = least > 1;
+        if (least <= 1) {  // 1: what rows of zeros are written with, which never count
+          if (ve == 1 && zero_row(sv + lane * ROWB, CPR)) sexp[stage * 2 * STEP + STEP + lane] = static_cast<uint8_t>(ve = 0);
+          __syncwarp();
+          least = __reduce_min_sync(0xffffffffu, ve != 0 ? ve : 255u);
         }
+        const uint32_t step_span = scale_span(__reduce_max_sync(0xffffffffu, ve), least);
 #pragma unroll
         for (int g = 0; g < KG; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             kf[g][e] = exp_scale(ex[g * 16 + n8 + 8 * e]);
-            const int ve = ex[STEP + g * 16 + n8 + 8 * e];
-            vf[g][e] = __uint_as_float(static_cast<uint32_t>(max(127 + 15 - (ref - ve), 0)) << 23);
+            vx[g][e] = ex[STEP + g * 16 + n8 + 8 * e];
           }
+        bool grows = false, widens = false;
+        uint32_t now[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            now[nt][r] = __vmaxu2(span[nt][r], step_span);
+            grows |= now[nt][r] != span[nt][r];
+            widens |= wide_span(now[nt][r]);
+            grow[nt][r] = 1.f;
+          }
+        if (__any_sync(0xffffffffu, grows)) {
+          // A row's keys have the step's span where those that every row sees have it.  (Keys that a single token does
+          // not see are not there.)
+          if (masked && cc.s.nq > 1) {
+            const int j = j0 + lane;
+            if (!(j < full_hi && (j >= full_lo || j < p.sinks))) ve = 0;
+            widens |= step_span != scale_span(__reduce_max_sync(0xffffffffu, ve),
+                                              __reduce_min_sync(0xffffffffu, ve != 0 ? ve : 255u));
+          }
+          if (__builtin_expect(!__any_sync(0xffffffffu, widens), 1)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {  // the output's unit grows
+                const int up = static_cast<int>((now[nt][r] & 0xffffu) - (span[nt][r] & 0xffffu));
+                grow[nt][r] = __uint_as_float(static_cast<uint32_t>(127 - min(up, 127)) << 23);
+                span[nt][r] = now[nt][r];
+              }
+          } else {
+            unsigned none = 0;
+#pragma unroll 1
+            for (int pass = 0; pass < 2; ++pass) {
+              widens = false;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const uint32_t x = seen_span(ex + STEP, rlo[nt][r] - j0, rhi[nt][r] - j0, p.sinks - j0, none);
+                  if (pass == 0 || (wide_span(now[nt][r]) && !wide_span(span[nt][r])))
+                    now[nt][r] = __vmaxu2(span[nt][r], x);
+                  widens |= wide_span(now[nt][r]) && !wide_span(span[nt][r]);
+                }
+              // (rows of zeros with any other scale make no row wide)
+              if (pass == 1 || !__any_sync(0xffffffffu, widens)) break;
+              none = __ballot_sync(0xffffffffu, zero_row(sv + lane * ROWB, CPR));
+            }
+            bool wide = false, over = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                // the output's unit grows, or becomes 1 (two factors: 2^-141 is not a normal number)
+                const uint32_t old = span[nt][r], to = now[nt][r];
+                const int up = static_cast<int>(old & 0xffffu) - (wide_span(to) ? 142 : static_cast<int>(to & 0xffffu));
+                const int x = wide_span(old) ? 0 : max(up, -200);
+                grow[nt][r] = __uint_as_float((127 + x / 2) << 23) * __uint_as_float((127 + x - x / 2) << 23);
+                span[nt][r] = to;
+                wide |= wide_span(to);
+                over |= __vmaxu2(to, step_span) != to;  // unseen keys, rows of zeros that did not count
+              }
+            any_wide = __any_sync(0xffffffffu, wide);
+            plain &= !__any_sync(0xffffffffu, over);
+          }
+        }
+        plain &= !any_wide;
+      }
+      uint32_t up[NT][2];
+      if (FP8) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) up[nt][r] = (142u - (span[nt][r] & 0xffffu)) << 23;
       }
       // ---- softmax of these keys
-      const bool masked = j0 < full_lo || j0 + STEP > full_hi;
       uint32_t pb[KG][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -406,10 +526,10 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const float w = paged_ex2(s[g][nt][2 * e + r] - base);
               sum += w;
-              s[g][nt][2 * e + r] = FP8 ? w * vf[g][e] : w;
+              s[g][nt][2 * e + r] = w;
             }
           l[nt][r] = l[nt][r] * alpha[r] + sum;
-          alpha[r] *= oscale;
+          if (FP8) alpha[r] *= grow[nt][r];
         }
         if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
@@ -423,9 +543,72 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
 #pragma unroll
         for (int g = 0; g < KG; ++g)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            pb[g][nt][h] = transpose8(FP8 ? pack_f16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1])
-                                          : pack_bf16x2(s[g][nt][2 * h], s[g][nt][2 * h + 1]));
+          for (int h = 0; h < 2; ++h) {
+            float a = s[g][nt][2 * h], b = s[g][nt][2 * h + 1];
+            if (FP8) {  // times 2^(e - r + 15), at most 2^15
+              const uint32_t e = vx[g][h] << 23;
+              a *= __uint_as_float(e + up[nt][0]);
+              b *= __uint_as_float(e + up[nt][1]);
+            }
+            pb[g][nt][h] = FP8 ? pack_f16x2(a, b) : transpose8(pack_bf16x2(a, b));
+          }
+      }
+      if (FP8) {
+        if (!plain) {  // (keys that a row does not see have weight 0 and any scale, rows of zeros any scale too)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int g = 0; g < KG; ++g)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float f[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                  const int e = static_cast<int>(vx[g][h]) + 142 - static_cast<int>(span[nt][r] & 0xffffu);
+                  f[r] = wide_span(span[nt][r]) ? 0.f : __uint_as_float(static_cast<uint32_t>(min(max(e, 0), 142)) << 23);
+                }
+                pb[g][nt][h] = pack_f16x2(s[g][nt][2 * h] * f[0], s[g][nt][2 * h + 1] * f[1]);
+              }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int g = 0; g < KG; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) pb[g][nt][h] = transpose8(pb[g][nt][h]);
+      }
+      if (FP8 && any_wide) {
+        // ---- the wide rows' part of O: weights, scales and products in fp32, key by key (of weight 0: not
+        // seen, where some keys are not; their values may be NaN here)
+#pragma unroll 1
+        for (int k = 0; k < STEP; ++k) {
+          const float sc = exp_scale(ex[STEP + k]);
+          float wr[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float a = k & 8 ? s[0][nt][2 + r] : s[0][nt][r], b = k & 8 ? s[KG - 1][nt][2 + r] : s[KG - 1][nt][r];
+              wr[nt][r] = __shfl_sync(0xffffffffu, k & 16 ? b : a, (k & 7) * 4 + q4);
+              if (!wide_span(span[nt][r])) wr[nt][r] = 0.f;
+            }
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint16_t code;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(code) : "r"(sv + swz<ROWB>(k, c) + 2 * n8) : "memory");
+            uint32_t f16, none;
+            e4m3x4_to_f16x4(code, f16, none);
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f16));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const bool skip = masked && wr[nt][r] == 0.f;
+                o[nt][c][r] += skip ? 0.f : wr[nt][r] * (v.x * sc);
+                o[nt][c][2 + r] += skip ? 0.f : wr[nt][r] * (v.y * sc);
+              }
+          }
+        }
       }
       if (masked && cc.s.nq > 1) {
         // a lane's column of 16-byte pieces (rows eight apart have theirs exchanged alike)
@@ -492,17 +675,18 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           const float sum = row_sum(l[nt][r]);
           if (n8 == 0) sml[warp * ROWS + nt * 8 + 2 * q4 + r] = make_float2(m[nt][r], sum);
         }
-      // 2^(ref - 127 - 15) as two factors, both normal numbers
-      const int u = ref - 142, u1 = u / 2;
-      const float unit1 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u1) << 23) : 1.f;
-      const float unit2 = FP8 ? __uint_as_float(static_cast<uint32_t>(127 + u - u1) << 23) : 1.f;
       const bool any_odd = __syncthreads_or(odd) != 0;
       const int64_t pbase = (static_cast<int64_t>(blockIdx.x) * 2 + slot) * ROWS;
-      float f[NT][2];
+      float f[NT][2], unit2[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
+          // 2^(r - 127 - 15) as two factors, both normal numbers
+          const uint32_t sp = FP8 ? span[nt][r] : 0u;
+          const int u = FP8 && !wide_span(sp) ? static_cast<int>(sp & 0xffffu) - 142 : 0, u1 = u / 2;
+          const float unit1 = __uint_as_float(static_cast<uint32_t>(127 + u1) << 23);
+          unit2[nt][r] = __uint_as_float(static_cast<uint32_t>(127 + u - u1) << 23);
           float top = kNInf;
 #pragma unroll
           for (int w = 0; w < W; ++w) top = fmaxf(top, sml[w * ROWS + nt * 8 + 2 * q4 + r].x);
@@ -524,7 +708,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
               const float fa = f[nt][r];
               if (FP8) {
                 *reinterpret_cast<float2*>(row + ((16 * c + 2 * n8) ^ (q4 << 3 & (COLS - 1)))) =
-                    make_float2(v[r] * fa * unit2, v[2 + r] * fa * unit2);
+                    make_float2(v[r] * fa * unit2[nt][r], v[2 + r] * fa * unit2[nt][r]);
               } else {
                 row[(16 * c + n8) ^ (q4 << 3 & (COLS - 1))] = v[r] * fa;
                 row[(16 * c + 8 + n8) ^ (q4 << 3 & (COLS - 1))] = v[2 + r] * fa;

@@ -118,8 +118,9 @@ FDMA_API size_t fdma_paged_workspace_size(const fdma_paged_args* args);
      lse = log sum exp S  (fp32 (Hq, T) contiguous).
    A row that sees no key gets out = 0 and lse = -inf.  Keys that a row does not see do not reach
    it, whatever they hold.  Precision: products in fp32 from the bf16 (or exact e4m3) values, the
-   softmax in fp32; for the product with V the weights are rounded to bf16 (to f16, which keeps 11 bits, for
-   an e4m3 cache and at most 16 rows, max_q * Hq / Hkv).
+   softmax in fp32; for the product with V the weights are rounded to bf16.  With an e4m3 cache and at most 16 rows
+   (max_q * Hq / Hkv) they are rounded to f16, relative to the row's largest: to 11 bits or 2^-24; or, for a row that
+   sees value scales more than 2^16 apart, not at all.
    Deterministic: the same call gives the same bits. */
 FDMA_API int fdma_paged_fwd(const fdma_paged_args* args, void* out, float* lse, void* stream);
 

@@ -719,3 +719,114 @@ def test_tensors_of_a_call_are_checked(P):
         P.fwd(q, *s.at, cu, 1, scale=float("nan"))
     with pytest.raises(fdma.FdmaError):
         P.fwd(q, *s.at, cu, 1, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------------------------------------------ scales far apart
+# e4m3 caches, at most 16 rows: a weight is an f16 number in units of the row's largest value scale, so its own error
+# is 2^-11 of it or, where it gets subnormal (step 2^-24, scales at most 2^16 apart, the largest unit 2^15), at most
+# 2^-25 * 2^-15 * 2^16 = 2^-24.  Rows whose scales lie further apart take weights in fp32.  So the bound above
+# grows by 2^-24 sum_j |v_j| / (sum of the weights, which is at least 1).
+def _plant_scale(s, b, j, delta, kind):
+    """Key j of sequence b with a value scale `delta` powers of two above the sequence's largest."""
+    pg, sl = int(s.table[b, j // s.page]), j % s.page
+    top = int(np.log2(np.abs(s.V[b]).max() / 448).max()) + 128
+    code = s.vc.view(torch.uint8)[pg, sl].clone()
+    if kind == "column":  # one value, and seven eighths of the others' columns are its zeros
+        code[:, s.d // 8:] = 0
+        s.vc.view(torch.uint8)[pg, sl] = code
+    if kind == "light":  # far below the others' scores: queries have 8 in column 0
+        kcode, kbyte = orc.quantise(np.where(np.arange(s.d) == 0, -8.0 * s.d ** 0.5, s.K[b][j]))
+        s.kc.view(torch.uint8)[pg, sl], s.ke[pg, sl] = torch.from_numpy(kcode).cuda(), torch.from_numpy(kbyte).cuda()
+        s.K[b][j] = orc.dequantise(kcode, kbyte)
+    s.ve[pg, sl] = top + delta
+    s.V[b][j] = orc.dequantise(code.cpu().numpy(), np.full(s.Hkv, top + delta))
+
+
+@pytest.mark.parametrize("delta", [12, 30, 40, 100])
+@pytest.mark.parametrize("kind", ["unseen", "light", "column"])
+@pytest.mark.parametrize("new,G,d", [(1, 1, 128), (2, 1, 64), (3, 2, 128), (4, 4, 128), (16, 1, 64), (5, 4, 128)])
+def test_a_large_value_leaves_the_other_keys_their_weights(P, new, G, d, kind, delta):
+    if kind == "unseen" and new == 1:
+        pytest.skip("a single token sees every key")
+    for n in (20, 300, 3000):
+        s = Setup(P, [n], 2, d, 16, True, seed=n + d)
+        q = _queries(new, 2 * G, d, seed=delta)
+        q[..., 0] = 8
+        cu = _cu([new])
+        if kind == "light":  # (its score is -64 nats, the others within some of 0)
+            s.kc.view(torch.uint8)[..., 0] = 0
+            s.K[0][..., 0] = 0
+        clean, clean_lse = P.fwd(q, *s.at, cu, new, **s.ex)
+        j = n - 1 if kind == "unseen" else n - new - 3
+        _plant_scale(s, 0, j, delta, kind)
+        out, lse = P.fwd(q, *s.at, cu, new, **s.ex)
+        ref, rl, A, D = orc.attend(_np(q), s.K[0], s.V[0], d ** -0.5)
+        w = 2.0 ** -22 * (8 + d * D)[..., None]
+        others = np.repeat(np.abs(np.delete(s.V[0], j, 0)).sum(0), G, 0)[None]
+        u = 2.0 ** -11 if new * G <= 16 else 2.0 ** -8
+        tol = 2.0 ** -8 * np.abs(ref) + (u + 2 * w) * A + 2.0 ** -24 * others
+        if delta <= 16:
+            tol = tol + 2.0 ** -40 * np.repeat(np.abs(s.V[0][j]), G, 0)[None]
+        err = np.abs(_np(out) - ref)
+        assert (err <= tol).all(), (n, (err / tol).max())
+        assert (np.abs(_np(lse).T - rl) <= w[..., 0] + 2.0 ** -22 * np.abs(rl)).all()
+        if kind == "unseen":  # the rows that do not see it have not changed
+            assert torch.equal(out[:-1], clean[:-1]) and torch.equal(lse[:, :-1], clean_lse[:, :-1])
+
+
+@pytest.mark.parametrize("order", ["shuffled", "rising", "falling"])
+@pytest.mark.parametrize("news,G", [([1], 1), ([2], 4), ([4], 4), ([1, 3], 8), ([6], 4)])
+def test_value_scales_over_the_whole_range(P, news, G, order):
+    """Scale bytes 20 to 240 in one sequence, each octave of bytes with columns of its own: every column has to
+    be right by itself, however small beside the others."""
+    d, lens = 128, [700 + 31 * b for b in range(len(news))]
+    s = Setup(P, lens, 1, d, 16, True, seed=len(lens))
+    g = np.random.default_rng(G)
+    for b, n in enumerate(lens):
+        byte = np.sort(g.integers(20, 241, n))
+        byte = byte[::-1].copy() if order == "falling" else g.permutation(byte) if order == "shuffled" else byte
+        code = g.integers(8, 120, (n, 1, d)).astype(np.uint8) | (g.integers(0, 2, (n, 1, d)) << 7).astype(np.uint8)
+        band = np.arange(d)[None, None] // 8 == (byte // 16)[:, None, None]
+        code = np.where(band, code, 0).astype(np.uint8)
+        pos = torch.arange(n)
+        pg, sl = s.table[b, (pos // 16).cuda()].long(), (pos % 16).cuda()
+        s.vc.view(torch.uint8)[pg, sl] = torch.from_numpy(code).cuda()
+        s.ve[pg, sl] = torch.from_numpy(byte[:, None].astype(np.uint8)).cuda()
+        s.V[b] = orc.dequantise(code, byte[:, None])
+    q = _queries(sum(news), G, d, seed=4)
+    out, lse = P.fwd(q, *s.at, _cu(news), max(news), **s.ex)
+    out, lse, at = _np(out), _np(lse), 0
+    u = 2.0 ** -11 if max(news) * G <= 16 else 2.0 ** -8
+    for b, n in enumerate(news):
+        ref, rl, A, D = orc.attend(_np(q[at:at + n]), s.K[b], s.V[b], d ** -0.5)
+        w = 2.0 ** -22 * (8 + d * D)[..., None]
+        # 2^-130: bf16's least step is 2^-133, fp32's 2^-149.  The f16 term of above: a warp whose keys' scales are at most
+        # 2^16 apart has f16 weights; beside a largest unit of 2^15 key j's is 2^(15 - x), x <= 16, half a step of a
+        # subnormal f16 2^-25, so w_j is off by at most 2^-25 / 2^(15 - x) = 2^(x - 40) <= 2^-24.  Some heads' weights
+        # of a whole band are below that (2^-36 of the row's largest), and only keys of the band have the column.
+        tol = 2.0 ** -8 * np.abs(ref) + (u + 2 * w) * A + 2.0 ** -130
+        if max(news) * G <= 16:
+            tol = tol + 2.0 ** -24 * np.abs(s.V[b][:, 0]).sum(0)
+        err = np.abs(out[at:at + n] - ref)
+        assert (err <= tol).all(), (err / tol).max()
+        assert (np.abs(lse[:, at:at + n].T - rl) <= w[..., 0] + 2.0 ** -22 * np.abs(rl)).all()
+        at += n
+
+
+def test_zero_value_rows_do_not_disturb_the_others(P):
+    """Rows of zeros (scale byte 1) beside ordinary ones: the same rows as with any other scale byte."""
+    s = Setup(P, [500], 2, 128, 16, True, seed=3)
+    for j in (0, 33, 250, 499):
+        pg, sl = int(s.table[0, j // 16]), j % 16
+        s.vc.view(torch.uint8)[pg, sl] = torch.tensor([0, 0x80], dtype=torch.uint8, device="cuda").repeat(64)
+        s.ve[pg, sl] = 1
+        s.V[0][j] = 0
+    for new in (1, 4, 30):
+        q = _queries(new, 8, 128, new)
+        a = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
+        _check_attention(s, q, [new], *a)
+        for byte in (110, 20, 240):
+            ve = s.ve.clone()
+            ve[ve == 1] = byte
+            b = P.fwd(q, *s.at, _cu([new]), new, k_exp=s.ke, v_exp=ve)
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
