@@ -62,22 +62,25 @@ struct PagedParams {
   int box;      // chunk kernel: rows of a TMA box of the cache (0: no TMA)
 };
 
-// One sequence as the kernels use it: every value inside its bounds whatever the arrays hold.
+// One sequence as the kernels use it: every value inside its bounds whatever the arrays hold.  Tokens that are left
+// out (outside [0, T), behind max_q) do not move the others: packed token t stays at position
+// k_len - (cu[b + 1] - t).  A sequence whose k_len is out of range has no rows.
 struct Seq {
   int q0;    // first packed token
   int nq;    // new tokens
   int klen;  // keys, the new tokens among them
-  int pos0;  // position of the first new token (negative: that row is before the first key)
+  int pos0;  // position of token q0 (negative: that row is before the first key); pos0 + nq <= klen
 };
 
 __device__ __forceinline__ Seq load_seq(const PagedParams& p, int b, bool report) {
   Seq s;
   const int a = p.cu[b], e = p.cu[b + 1], kl = p.c.k_len[b];
   const int cap = p.c.max_pages << p.c.page_shift;
-  s.q0 = min(max(a, 0), p.T);
-  s.nq = min(max(min(e, p.T) - s.q0, 0), p.max_q);
   s.klen = min(max(kl, 0), cap);
-  s.pos0 = s.klen - s.nq;
+  s.q0 = min(max(a, 0), p.T);
+  s.nq = kl == s.klen ? min(max(min(e, p.T) - s.q0, 0), p.max_q) : 0;
+  // (far below the first key, as far as a row's number reaches, is the same as further)
+  s.pos0 = s.nq > 0 ? max(s.klen - (e - s.q0), -(1 << 30)) : 0;
   if (report && (a != s.q0 || e != s.q0 + s.nq || kl != s.klen)) atomicCAS(p.err, 0, FDMA_ERR_INVALID);
   return s;
 }

@@ -31,7 +31,8 @@
  * What only the device sees (cu, k_len, page_table) is checked there: a page
  * number outside [0, num_pages), a k_len outside [0, max_pages * page_size], a
  * token range outside [0, T) or a position outside the sequence's pages is never
- * dereferenced; the tokens it stands for are left out, keys of a page that is not
+ * dereferenced; the tokens it stands for are left out (their rows or slots stay as they are, all
+ * other tokens keep their positions), keys of a page that is not
  * there read as zeros, and fdma_get_device_error() returns FDMA_ERR_INVALID.  Entries of page_table that
  * no position below k_len needs are not looked at.
  */

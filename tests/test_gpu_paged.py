@@ -830,3 +830,82 @@ def test_zero_value_rows_do_not_disturb_the_others(P):
             ve[ve == 1] = byte
             b = P.fwd(q, *s.at, _cu([new]), new, k_exp=s.ke, v_exp=ve)
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------------------------------------------ parts left out
+def _check_kept_rows(s, q, news, keep, out, lse, window=0, sinks=0, f16=False):
+    """Rows `keep` (a number for each sequence) of the sequences' first, as with nothing left out; the others as they were (5)."""
+    at = 0
+    for b, n in enumerate(news):
+        ref, rl, A, D = orc.attend(_np(q[at:at + n]), s.K[b], s.V[b], s.d ** -0.5, True, window, sinks)
+        m = keep[b]
+        w = 2.0 ** -22 * (8 + s.d * D)[..., None]
+        tol = (2.0 ** -8 * np.abs(ref) + ((2.0 ** -11 if f16 else 2.0 ** -8) + 2 * w) * A + 1e-30)[:m]
+        o, z = _np(out[at:at + n]), _np(lse[:, at:at + n]).T
+        assert (np.abs(o[:m] - ref[:m]) <= tol).all(), (b, (np.abs(o[:m] - ref[:m]) / tol).max())
+        assert (np.abs(z[:m] - rl[:m]) <= w[:m, :, 0] + 2.0 ** -22 * np.abs(rl[:m])).all()
+        assert (o[m:] == 5).all() and (z[m:] == 5).all()
+        at += n
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (30, 4)])
+@pytest.mark.parametrize("max_q", [1, 4, 20, 150])
+def test_rows_past_max_q_are_left_out_and_the_others_keep_their_positions(P, fp8, window, sinks, max_q):
+    from block_sparse_masked_02_gb300 import fdma
+
+    news, lens = [6, 1, 200], [50, 77, 500]
+    s = Setup(P, lens, 2, 64, 16, fp8, seed=5)
+    T = sum(news)
+    q = _queries(T, 4, 64)
+    out, lse = torch.full((T, 4, 64), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, T), 5.0, device="cuda")
+    P.fwd(q, *s.at, _cu(news), max_q, window=window, sinks=sinks, out=out, lse=lse, **s.ex)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    _check_kept_rows(s, q, news, [min(n, max_q) for n in news], out, lse, window, sinks, fp8 and 2 * max_q <= 16)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("news", [[3, 4], [30, 100]])
+def test_tokens_behind_the_packed_axis_are_left_out(P, fp8, news):
+    """cu_q[B] past T by two: the last two tokens are not there, the others keep their positions."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    s = Setup(P, [40, 300], 2, 128, 16, fp8, seed=6)
+    T = sum(news)
+    q = _queries(T, 4, 128)
+    out, lse = torch.full((T, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, T), 5.0, device="cuda")
+    short, z = out[:T - 2], torch.full((4, T - 2), 5.0, device="cuda")
+    P.fwd(q[:T - 2], *s.at, _cu(news), max(news), out=short, lse=z, **s.ex)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    lse[:, :T - 2] = z
+    _check_kept_rows(s, q, news, [news[0], news[1] - 2], out, lse, f16=fp8 and max(news) * 2 <= 16)
+    # ranges that begin before the first token: those tokens are left out
+    cu = _cu(news) - 2
+    P.fwd(q[:T - 2], *s.at, cu, max(news), out=short, lse=z, **s.ex)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    full = torch.cat([q[:2], q[:T - 2]])
+    o = torch.cat([torch.zeros_like(out[:2]), short])
+    for b, (a, n) in enumerate(((2, news[0] - 2), (news[0], news[1]))):
+        ref, _, A, D = orc.attend(_np(full[a + n - news[b]:a + n]), s.K[b], s.V[b], 128 ** -0.5)
+        w = 2.0 ** -22 * (8 + 128 * D)[..., None]
+        err = np.abs(_np(o[a:a + n]) - ref[-n:])
+        assert (err <= (2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2 * w) * A + 1e-30)[-n:]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("news", [[3, 4, 2], [30, 100, 1]])
+@pytest.mark.parametrize("bad", [-1, -(1 << 31), "past", 1 << 30, (1 << 31) - 1])
+def test_sequences_with_a_length_out_of_range_are_left_out(P, fp8, news, bad):
+    """fwd leaves their rows, append their slots as they were; the others are right."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    s = Setup(P, [40, 300, 25], 2, 128, 16, fp8, seed=6, spare=0)
+    lens = s.k_lens.clone()
+    lens[0] = s.table.shape[1] * 16 + 1 if bad == "past" else bad
+    at = (s.kc, s.vc, s.table, lens)
+    T = sum(news)
+    q = _queries(T, 4, 128)
+    out, lse = torch.full((T, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda"), torch.full((4, T), 5.0, device="cuda")
+    P.fwd(q, *at, _cu(news), max(news), out=out, lse=lse, **s.ex)
+    assert fdma.device_error() == fdma.FDMA_ERR_INVALID
+    _check_kept_rows(s, q, news, [0] + news[1:], out, lse, f16=fp8 and max(news) * 2 <= 16)
