@@ -29,6 +29,7 @@ constexpr float kPLog2e = 1.4426950408889634f;
 constexpr float kPLn2 = 0.6931471805599453f;
 
 constexpr int kItemCost = 2;
+constexpr int64_t kMaxRun = 1 << 30;  // places of a CTA's run (of a chunk: a quarter of an hour): more is refused
 
 struct CacheView {
   const uint8_t* k;  // strides in bytes: page, token, head
@@ -182,8 +183,8 @@ __device__ __forceinline__ int item_places(const PagedParams& p, const Seq& s, i
 }
 
 // a / b, a >= 0 and b > 0.  (A 64-bit division takes 400 cycles, and every CTA waits for these.)
-__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
-  return (a >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
 struct PlanSmem {
@@ -196,7 +197,8 @@ struct PlanSmem {
 // Finds this CTA's run: every thread of the CTA calls it (NT threads).  False where it has no
 // tiles; else c stands on the first of them.  quota: the run length of all CTAs.
 // A sequence's items are counted by plan_lanes lanes together (by one, a chunk's 16 to 32 row blocks took
-// 6 us before the first load).
+// 6 us before the first load).  Places are counted in 64 bits: 1.5 million tokens of 64 heads on one kv head over
+// themselves have 2^31.
 template <int ROWS, int KT, int NT>
 __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cursor<ROWS, KT>& c, int& quota) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, L = p.plan_lanes, sub = lane & (L - 1);
@@ -205,18 +207,18 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
   const int b0 = min(tid / L * per, p.c.B), b1 = min(b0 + per, p.c.B);
   // places of a kv head of a sequence, in every lane of the group
   auto seq_places = [&](const Seq& s) {
-    int n = 0;
+    int64_t n = 0;
     for (int rt = sub; rt * ROWS < s.nq * p.G; rt += L) n += item_places<ROWS, KT>(p, s, rt);
     for (int o = 1; o < L; o <<= 1) n += __shfl_xor_sync(group, n, o);
     return n;
   };
   int64_t mine = 0;
   Seq s{};  // the last one, and its places: usually a group has one sequence
-  int n = 0;
+  int64_t n = 0;
   for (int b = b0; b < b1; ++b) {
     s = load_seq(p, b, blockIdx.x == 0);
     n = seq_places(s);
-    mine += static_cast<int64_t>(n) * p.c.Hkv;
+    mine += n * p.c.Hkv;
   }
   __syncwarp();
   int64_t x = sub == 0 ? mine : 0;
@@ -233,7 +235,12 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
     if (w < warp) before += sm->warp_sum[w];
     total += sm->warp_sum[w];
   }
-  quota = static_cast<int>(max(quotient(total + kPagedCtas - 1, kPagedCtas), static_cast<int64_t>(p.min_run)));
+  const int64_t run = max(quotient(total + kPagedCtas - 1, kPagedCtas), static_cast<int64_t>(p.min_run));
+  if (run > kMaxRun) {
+    if (blockIdx.x == 0 && tid == 0) atomicCAS(p.err, 0, FDMA_ERR_UNSUPPORTED);
+    return false;
+  }
+  quota = static_cast<int>(run);
   const int64_t start = static_cast<int64_t>(blockIdx.x) * quota;
   if (start >= before && start < before + mine) {  // (one group of lanes)
     int64_t left = start - before;
@@ -242,27 +249,27 @@ __device__ __forceinline__ bool plan_run(const PagedParams& p, PlanSmem* sm, Cur
         s = load_seq(p, b, false);
         n = seq_places(s);
       }
-      if (left >= static_cast<int64_t>(n) * p.c.Hkv) {
-        left -= static_cast<int64_t>(n) * p.c.Hkv;
+      if (left >= n * p.c.Hkv) {
+        left -= n * p.c.Hkv;
         continue;
       }
       const int g = static_cast<int>(quotient(left, n));
-      int t = static_cast<int>(left - static_cast<int64_t>(g) * n);
+      int64_t t = left - g * n;
       for (int rt = sub;; rt += L) {
         const int k = item_places<ROWS, KT>(p, s, rt);
-        int sum = k;
+        int64_t sum = k;
         for (int o = 1; o < L; o <<= 1) {
-          const int y = __shfl_up_sync(group, sum, o, L);
+          const int64_t y = __shfl_up_sync(group, sum, o, L);
           if (sub >= o) sum += y;
         }
         if (t >= sum - k && t < sum) {
           sm->b = b;
           sm->g = g;
           sm->rt = rt;
-          sm->t = t - (sum - k);
+          sm->t = static_cast<int>(t - (sum - k));
           sm->s = s;
         }
-        const int all = __shfl_sync(group, sum, L - 1, L);
+        const int64_t all = __shfl_sync(group, sum, L - 1, L);
         if (t < all) break;
         t -= all;
       }

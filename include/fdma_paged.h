@@ -122,7 +122,8 @@ FDMA_API size_t fdma_paged_workspace_size(const fdma_paged_args* args);
    softmax in fp32; for the product with V the weights are rounded to bf16.  With an e4m3 cache and at most 16 rows
    (max_q * Hq / Hkv) they are rounded to f16, relative to the row's largest: to 11 bits or 2^-24; or, for a row that
    sees value scales more than 2^16 apart, not at all.
-   Deterministic: the same call gives the same bits. */
+   Deterministic: the same call gives the same bits.  A call of more than 2^30 steps of 128 keys an SM does
+   nothing, and fdma_get_device_error() returns FDMA_ERR_UNSUPPORTED. */
 FDMA_API int fdma_paged_fwd(const fdma_paged_args* args, void* out, float* lse, void* stream);
 
 #ifdef __cplusplus

@@ -909,3 +909,128 @@ def test_sequences_with_a_length_out_of_range_are_left_out(P, fp8, news, bad):
     P.fwd(q, *at, _cu(news), max(news), out=out, lse=lse, **s.ex)
     assert fdma.device_error() == fdma.FDMA_ERR_INVALID
     _check_kept_rows(s, q, news, [0] + news[1:], out, lse, f16=fp8 and max(news) * 2 <= 16)
+
+
+# ------------------------------------------------------------------------------------------------ division of the work
+PLAN_PROBE = r"""
+#include "fdma_paged.cuh"
+template <int ROWS, int NT>
+__global__ void __launch_bounds__(NT) probe(const __grid_constant__ fdma::PagedParams p, int* out) {
+  __shared__ fdma::PlanSmem sm;
+  fdma::Cursor<ROWS, 128> c;
+  int quota = 0;
+  const bool any = fdma::plan_run<ROWS, 128, NT>(p, &sm, c, quota);
+  if (threadIdx.x == 0) {
+    int* o = out + blockIdx.x * 8;
+    o[0] = any;
+    if (any) o[1] = c.b, o[2] = c.g, o[3] = c.rt, o[4] = c.t, o[5] = c.left, o[6] = quota;
+  }
+}
+extern "C" __attribute__((visibility("default"))) int plan_probe(
+    const int* cu, const int* k_len, int B, int Hkv, int G, int T, int max_q, int page_shift, int max_pages, int causal,
+    int window, int sinks, int rows, int lanes, int min_run, int* out, int* err) {
+  fdma::PagedParams p{};
+  p.cu = cu, p.c.k_len = k_len, p.c.B = B, p.c.Hkv = Hkv, p.G = G, p.T = T, p.max_q = max_q, p.c.page_shift = page_shift;
+  p.c.max_pages = max_pages, p.causal = causal, p.window = window, p.sinks = sinks, p.plan_lanes = lanes, p.min_run = min_run;
+  p.err = err;
+  if (rows == 256) probe<256, 512><<<fdma::kPagedCtas, 512>>>(p, out);
+  else if (rows == 8) probe<8, 256><<<fdma::kPagedCtas, 256>>>(p, out);
+  else return -1;
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? static_cast<int>(cudaDeviceSynchronize()) : static_cast<int>(e);
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def plan_probe(P, tmp_path_factory):
+    """The division of the work by itself: what every CTA begins with, without the attention."""
+    import ctypes
+    import subprocess
+
+    from block_sparse_masked_02_gb300 import build
+
+    d = tmp_path_factory.mktemp("plan")
+    src, lib = d / "plan_probe.cu", d / "plan_probe.so"
+    src.write_text(PLAN_PROBE)
+    subprocess.run([build._nvcc(), *build.ARCH, *build.CFLAGS, "-I", build.CSRC, "-shared", str(src), "-o", str(lib)], check=True)
+    return ctypes.CDLL(str(lib)).plan_probe
+
+
+def _line(news, lens, G, Hkv, causal, window, sinks, rows):
+    """Key tiles of every item, (sequence, kv head, row block) in order, as (sequence, tiles of each block)."""
+    for b, (n, kl) in enumerate(zip(news, lens)):
+        r0 = np.arange(0, n * G, rows, dtype=np.int64)
+        i0, i1 = r0 // G, np.minimum((r0 + rows - 1) // G + 1, n)
+        pos0 = kl - n
+        hi = np.maximum(pos0 + i1, 0) if causal else np.full(len(r0), kl)
+        lo = np.maximum(np.maximum(pos0 + i0, 0) - window + 1, 0) if window else np.zeros(len(r0), np.int64)
+        sink = np.minimum(sinks, lo) if window else lo
+        st = -(-sink // 128)
+        yield b, np.where(hi > 0, st - (-hi // 128) - np.maximum(lo // 128, st), 0)
+
+
+@pytest.mark.parametrize("case", [
+    # news, lens, Hkv, G, causal, window, sinks, rows of an item
+    ([1] * 200, list(range(200)), 2, 4, True, 0, 0, 8),
+    ([2, 0, 1], [5000, 7, 70000], 8, 4, True, 0, 0, 8),
+    ([200, 33, 0, 1000], [1500, 33, 9, 4000], 4, 4, True, 0, 0, 256),
+    ([300, 300], [900, 5000], 2, 2, True, 129, 130, 256),
+    ([100, 600], [350, 600], 3, 5, False, 0, 0, 256),
+    ([700, 1], [90, 0], 1, 4, True, 0, 0, 256),  # blocks without a key
+    ([1 << 16, 5], [1 << 20, 999], 2, 8, True, 0, 0, 256),
+    ([5, 1 << 21, 77], [40, 1 << 21, 3000], 1, 64, True, 0, 0, 256),  # 4.3e9 places in one kv head
+    ([1 << 20, 1 << 20], [1 << 20, 1 << 22], 2, 64, True, 0, 0, 256),
+    ([1 << 20], [1 << 24], 1, 64, False, 0, 0, 256),
+], ids=[str(i) for i in range(10)])
+def test_the_work_is_divided_into_equal_runs(plan_probe, case):
+    """Every CTA's first tile and the length of its run, against whole-number arithmetic."""
+    import ctypes
+
+    news, lens, Hkv, G, causal, window, sinks, rows = case
+    blocks, lanes = -(-max(news) * G // rows), 1
+    while lanes < min(32, blocks):
+        lanes *= 2
+    min_run = 1 if rows == 8 else 2
+    cu, kl = _cu(news), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, err = torch.zeros(152, 8, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    args = (ptr(cu), ptr(kl), len(news), Hkv, G, sum(news), max(news), 12, 1 << 18, int(causal), window, sinks, rows, lanes,
+            min_run, ptr(out), ptr(err))
+    assert plan_probe(*args) == 0 and int(err) == 0
+    items = list(_line(news, lens, G, Hkv, causal, window, sinks, rows))
+    places = [np.where(t > 0, t + 2, 0) for _, t in items]  # an item costs two places more than its tiles
+    ends = [np.cumsum(x) for x in places]
+    heads = [int(e[-1]) if len(e) else 0 for e in ends]
+    total = sum(heads) * Hkv
+    quota = max(-(-total // 152), min_run)
+    for i, got in enumerate(out.tolist()):
+        start, left = i * quota, min(quota, total - i * quota)
+        want = None
+        while left > 0:
+            at, x = start, 0
+            while at >= heads[x] * Hkv:
+                at -= heads[x] * Hkv
+                x += 1
+            g, at = divmod(at, heads[x])
+            rt = int(np.searchsorted(ends[x], at, side="right"))
+            t = at - int(ends[x][rt] - places[x][rt])
+            if t < items[x][1][rt]:
+                want = [1, items[x][0], g, rt, t, left, quota]
+                break
+            step = int(places[x][rt]) - t  # the two places behind an item's tiles
+            start, left = start + step, left - step
+        assert got[:7] == want if want else got[0] == 0, (i, got, want)
+
+
+def test_more_work_than_runs_can_hold_is_refused(plan_probe):
+    import ctypes
+
+    from block_sparse_masked_02_gb300 import fdma
+
+    n, kl = 1 << 24, 1 << 30
+    cu, lens = _cu([n]), torch.tensor([kl], dtype=torch.int32, device="cuda")
+    out, err = torch.zeros(152, 8, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    assert plan_probe(ptr(cu), ptr(lens), 1, 1, 64, n, n, 12, 1 << 18, 0, 0, 0, 256, 32, 2, ptr(out), ptr(err)) == 0
+    assert int(err) == fdma.FDMA_ERR_UNSUPPORTED and not out[:, 0].any()
