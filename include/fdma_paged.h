@@ -105,8 +105,8 @@ FDMA_API int fdma_kv_append(const fdma_kv_cache* cache, const void* k_new, const
 
 /* Reads positions first[b] + i (i = 0 .. cu[b+1]-cu[b]-1; first NULL: 0) of every sequence into
    rows cu[b] + i of k_out and v_out, (T, Hkv, d) bf16 contiguous, 16-byte aligned.  Positions
-   outside [0, k_len[b]) read as zeros (so cu = b * N gives sequences padded to N rows); rows behind
-   cu[B] are left as they are. */
+   outside [0, k_len[b]) read as zeros (so cu = b * N gives sequences padded to N rows), as do, where
+   k_len[b] is out of range, positions that the table does not reach; rows behind cu[B] are left as they are. */
 FDMA_API int fdma_kv_gather(const fdma_kv_cache* cache, const int32_t* cu, const int32_t* first, int T, void* k_out,
                             void* v_out, void* stream);
 

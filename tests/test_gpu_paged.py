@@ -1034,3 +1034,65 @@ def test_more_work_than_runs_can_hold_is_refused(plan_probe):
     ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
     assert plan_probe(ptr(cu), ptr(lens), 1, 1, 64, n, n, 12, 1 << 18, 0, 0, 0, 256, 32, 2, ptr(out), ptr(err)) == 0
     assert int(err) == fdma.FDMA_ERR_UNSUPPORTED and not out[:, 0].any()
+
+
+def _appended(P, s, k, cu, lens):
+    """Slots (page, slot) whose K bytes an append changes (k holds no row that the cache had)."""
+    raw = lambda: s.kc.view(torch.uint8 if s.fp8 else torch.int16).clone()  # noqa: E731
+    before = raw()
+    P.kv_append(k, k, s.kc, s.vc, s.table, lens, cu, **s.ex)
+    return {tuple(x) for x in (raw() != before).flatten(2).any(-1).nonzero().tolist()}
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Hkv", [2, 4, 8])
+def test_appends_and_gathers_report_bad_offsets_and_lengths(P, fp8, Hkv):
+    """Token ranges past T, that begin before 0 or run backwards, and lengths past the table: reported, and
+    only slots of tokens that are there are written."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    lens = [40, 300, 25]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    g = torch.Generator().manual_seed(3)
+
+    def slots(s, b, positions):
+        return {(int(s.table[b, p // 16]), p % 16) for p in positions}
+
+    def run(cu, T, k_lens=lens):
+        s = Setup(P, lens, Hkv, 64, 16, fp8, seed=6, spare=0)
+        assert fdma.device_error() == 0
+        k = (3 + torch.rand(T, Hkv, 64, generator=g)).bfloat16().cuda()
+        got = _appended(P, s, k, i32(*cu), i32(*k_lens))
+        return s, got, fdma.device_error()
+
+    bad = fdma.FDMA_ERR_INVALID
+    s, got, err = run((0, 3, 7, 9), 9)
+    assert err == 0 and got == slots(s, 0, range(37, 40)) | slots(s, 1, range(296, 300)) | slots(s, 2, range(23, 25))
+    # past T: inside a sequence, and a sequence that no token belongs to
+    s, got, err = run((0, 3, 7, 9), 5)
+    assert err == bad and got == slots(s, 0, range(37, 40)) | slots(s, 1, range(296, 298))
+    s, got, err = run((0, 3, 5, 9), 5)
+    assert err == bad and got == slots(s, 0, range(37, 40)) | slots(s, 1, range(298, 300))
+    # before the first token
+    s, got, err = run((-2, 1, 2, 3), 3)
+    assert err == bad and got == slots(s, 0, [39]) | slots(s, 1, [299]) | slots(s, 2, [24])
+    # backwards: only slots of tokens in a range that has them
+    s, got, err = run((0, 3, 1, 3), 3)
+    assert err == bad and got <= slots(s, 0, range(37, 40)) | slots(s, 2, range(23, 25))
+    s, got, err = run((3, 1, 2, 2), 4)
+    assert err == bad and got <= slots(s, 1, [299])
+    # lengths: none of that sequence's tokens
+    cap = s.table.shape[1] * 16
+    for n in (cap + 1, cap + 2, 1 << 30, (1 << 31) - 1, -1, -(1 << 31)):
+        s, got, err = run((0, 3, 7, 9), 9, (n, 300, 25))
+        assert err == bad and got == slots(s, 1, range(296, 300)) | slots(s, 2, range(23, 25))
+
+    s = Setup(P, lens, Hkv, 64, 16, fp8, seed=6, spare=0)
+    for cu, T in (((0, 40, 340, 365), 364), ((0, 40, 340, 365), 340), ((-2, 38, 338, 363), 363), ((0, 40, 30, 55), 55)):
+        k, v = P.kv_gather(*s.at, i32(*cu), T, **s.ex)
+        assert fdma.device_error() == bad
+        if cu[2] > cu[1]:
+            want = np.concatenate(s.K)[-cu[0]:][:T]
+            assert np.array_equal(_np(k), want)
+    k, v = P.kv_gather(*s.at, i32(0, 40, 340, 365), 365, **s.ex)
+    assert fdma.device_error() == 0 and np.array_equal(_np(v), np.concatenate(s.V))
