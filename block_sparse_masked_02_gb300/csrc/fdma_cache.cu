@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_c
     if (!((store >> i) & 1u)) continue;
     const Row r = warp_row<ONE>(p, tok0, rem, i * RPP + lane / LPR);
     uint4* dst = reinterpret_cast<uint4*>((r.is_v ? p.v_out : p.k_out) + (r.tok * p.c.Hkv + r.g) * p.c.d + col);
+    if (FP8) be[i] = scale_byte(be[i]);
     dst[0] = FP8 ? dequantise8(make_uint2(x[i].x, x[i].y), be[i]) : x[i];
     if (FP8) dst[1] = dequantise8(make_uint2(x[i].z, x[i].w), be[i]);
   }

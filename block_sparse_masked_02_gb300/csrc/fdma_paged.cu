@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   const uint32_t cbytes = chunk * 16 < p.c.d * (FP8 ? 1 : 2) ? 16u : 0u;
   const int pmask = (1 << p.c.page_shift) - 1;
   uint32_t exp_pend[2] = {127, 127};
+  bool seen_pend = false;
   auto some_seen = [&](const Span& r, int j0, int n) { return j0 < r.sink_hi || (j0 < r.hi && j0 + n > r.lo); };
   // a group's page is looked up (a step ahead) only where some row sees one of its keys
   int lentry[KG];
@@ -210,8 +211,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   auto load_next = [&]() {
     if (FP8 && pending) {
       uint8_t* e = sexp + (lstage == 0 ? NST - 1 : lstage - 1) * 2 * STEP;
-      e[lane] = static_cast<uint8_t>(exp_pend[0]);
-      e[STEP + lane] = static_cast<uint8_t>(exp_pend[1]);
+      // (not when they are loaded: nothing may wait for them there)
+      e[lane] = static_cast<uint8_t>(scale_byte(exp_pend[0]));
+      e[STEP + lane] = static_cast<uint8_t>(seen_pend ? scale_byte(exp_pend[1]) : 0u);
     }
     pending = more;
     if (more) {
@@ -254,9 +256,11 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         const int j = js + lane;
         const int64_t pg = lane < 16 ? pgs[0] : pgs[KG - 1];
         exp_pend[0] = exp_pend[1] = 0;
+        seen_pend = false;
         if (pg >= 0 && (j < lc.r.sink_hi || (j >= lc.r.lo && j < lc.r.hi))) {
           exp_pend[0] = p.c.ke[pg * p.c.kes[0] + (j & pmask) * p.c.kes[1] + lc.g * p.c.kes[2]];
           exp_pend[1] = p.c.ve[pg * p.c.ves[0] + (j & pmask) * p.c.ves[1] + lc.g * p.c.ves[2]];
+          seen_pend = true;
         }
       }
       lstage = lstage + 1 == NST ? 0 : lstage + 1;

@@ -334,6 +334,9 @@ __device__ __forceinline__ float paged_ex2(float x) {
   return y;
 }
 
+// A scale byte as it counts: what no append writes (0, 247 to 255) as the nearest that one does.  So every value is
+// finite in bf16, and in a product with a weight of 0 adds nothing.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t e) { return min(max(e, 1u), 246u); }
 // 2^(e - 127) of a scale byte
 __device__ __forceinline__ float exp_scale(uint32_t e) { return __uint_as_float(e == 0 ? 0x00400000u : e << 23); }
 

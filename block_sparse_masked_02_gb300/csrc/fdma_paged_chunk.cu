@@ -622,7 +622,8 @@ __global__ void __launch_bounds__(ChunkRoles<FP8>::kThreads, 1)
               }
 #pragma unroll
               for (int is_v = 0; is_v < 2; ++is_v)
-                e[is_v] = x[is_v][0] | x[is_v][1] << 8 | x[is_v][2] << 16 | x[is_v][3] << 24;
+                e[is_v] = scale_byte(x[is_v][0]) | scale_byte(x[is_v][1]) << 8 | scale_byte(x[is_v][2]) << 16 |
+                          scale_byte(x[is_v][3]) << 24;
             }
             const int place = tile % kScales;
             if (tile >= kScales && !(ok = wait_all(cScaleFree + place, (tile / kScales - 1) & 1))) break;

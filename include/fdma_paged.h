@@ -20,7 +20,8 @@
  *                     finite |x| where x has infinities, which become
  *                     +-448 * 2^(e - 127); NaN stays NaN), each value rounded
  *                     once, to nearest even.  The scale is a power of two, so
- *                     the values read back are exact in bf16.
+ *                     the values read back are exact in bf16.  Bytes that are not written
+ *                     (0, 247 to 255) read as the nearest one that is.
  *
  * Several sequences are packed along one token axis: sequence b owns tokens
  * cu[b] .. cu[b+1]-1 (cu is non-decreasing, cu[0] >= 0).  k_len[b] counts the

@@ -1096,3 +1096,37 @@ def test_appends_and_gathers_report_bad_offsets_and_lengths(P, fp8, Hkv):
             assert np.array_equal(_np(k), want)
     k, v = P.kv_gather(*s.at, i32(0, 40, 340, 365), 365, **s.ex)
     assert fdma.device_error() == 0 and np.array_equal(_np(v), np.concatenate(s.V))
+
+
+@pytest.mark.parametrize("d", [64, 112, 128])
+def test_scale_bytes_out_of_range_read_as_the_nearest_one(P, d):
+    """Bytes that no append writes (0, and 247 to 255): the nearest of 1 .. 246."""
+    n = 300
+    s = Setup(P, [n], 2, d, 16, True, seed=d)
+    pos = torch.arange(n)
+    pg, sl = s.table[0, (pos // 16).cuda()].long(), (pos % 16).cuda()
+    for x, rows in ((s.ke, s.K), (s.ve, s.V)):
+        byte = torch.tensor([0, 1, 246, 247, 250, 255] * (n // 6), dtype=torch.uint8, device="cuda")
+        x[pg, sl] = byte[:, None].expand(-1, 2)
+        code = (s.kc if x is s.ke else s.vc).view(torch.uint8)[pg, sl].cpu().numpy()
+        rows[0] = orc.dequantise(code, np.clip(byte.cpu().numpy(), 1, 246)[:, None].repeat(2, 1))
+    k, v = P.kv_gather(*s.at, _cu([n]), n, **s.ex)
+    for got, rows in ((k, s.K), (v, s.V)):
+        assert torch.equal(got.cpu(), torch.tensor(rows[0]).bfloat16())
+
+
+@pytest.mark.parametrize("d", [64, 112, 128])
+def test_scale_bytes_of_unseen_keys_reach_no_row(P, d):
+    """Any scale bytes in a key that only the last row sees: the others get the same bits."""
+    n = 300
+    s = Setup(P, [n], 2, d, 16, True, seed=d)
+    clean = s.ke.clone(), s.ve.clone()
+    at = int(s.table[0, (n - 1) // 16]), (n - 1) % 16
+    for new in (2, 4, 40, 150):
+        q = _queries(new, 8, d, new)
+        want = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
+        for byte in (246, 247, 255, 0):
+            s.ke[at], s.ve[at] = byte, byte
+            got = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
+            s.ke.copy_(clean[0]), s.ve.copy_(clean[1])
+            assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1][:, :-1], want[1][:, :-1])
