@@ -118,7 +118,8 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&x)[2], uint32_t& be) {
   return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
 }
 
-// (code -> f16 -> bf16 are exact, and so is the product with a power of two, above bf16's subnormals.)
+// (code -> f16 -> bf16 are exact, and so is the product with a power of two down to bf16's least step, 2^-133;
+// below, with scale bytes 1 and 2, it is rounded once, to nearest even.)
 __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t be) {
   const uint32_t s = (__float_as_uint(exp_scale(be)) >> 16) * 0x10001u;
   uint32_t f[4], r[4];

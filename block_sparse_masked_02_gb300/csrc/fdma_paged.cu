@@ -21,7 +21,7 @@
 //
 // e4m3 caches: codes become f16 exactly (one conversion for two), so the products run in f16.
 // q is scaled by a power of two per row to [2^14, 2^15), which is exact but for parts below
-// 2^-38 of the row's largest.  The key's scale multiplies S; the value's scale multiplies P,
+// 2^-31 of the row's largest (f16's least step, 2^-24, is 2^-38 of 2^14, and a bf16 number has eight bits).  The key's scale multiplies S; the value's scale multiplies P,
 // as 2^(e - r + 15) with r the largest e so far of the keys that the row sees (its output is kept in
 // units of 2^(r - 15)), so that P stays in f16's range: a weight keeps 11 bits, or 2^(r - e - 40) where
 // that is more, at most 2^-24 because e and r are at most 16 apart.  A row that sees scales further

@@ -22,7 +22,7 @@
 //   warps 12..      bring Q, K and V into 128-byte-swizzled tiles: a ring of five bf16 tiles by TMA, a
 //                   box a page, or by cp.async where TMA cannot address the cache's layout or a page
 //                   is not there; or turn an e4m3 cache's codes into a ring of four tiles: multiplied
-//                   by their scale and stored as bf16 (exact).
+//                   by their scale and stored as bf16 (exact down to bf16's least step, 2^-133).
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 //

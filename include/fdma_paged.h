@@ -20,8 +20,9 @@
  *                     finite |x| where x has infinities, which become
  *                     +-448 * 2^(e - 127); NaN stays NaN), each value rounded
  *                     once, to nearest even.  The scale is a power of two, so
- *                     the values read back are exact in bf16.  Bytes that are not written
- *                     (0, 247 to 255) read as the nearest one that is.
+ *                     the values read back are exact in bf16 where they are multiples of its least
+ *                     step, 2^-133, as all are from e = 3 on (else rounded once more).  Bytes that
+ *                     are not written (0, 247 to 255) read as the nearest one that is.
  *
  * Several sequences are packed along one token axis: sequence b owns tokens
  * cu[b] .. cu[b+1]-1 (cu is non-decreasing, cu[0] >= 0).  k_len[b] counts the
@@ -122,7 +123,10 @@ FDMA_API size_t fdma_paged_workspace_size(const fdma_paged_args* args);
    it, whatever they hold.  Precision: products in fp32 from the bf16 (or exact e4m3) values, the
    softmax in fp32; for the product with V the weights are rounded to bf16.  With an e4m3 cache and at most 16 rows
    (max_q * Hq / Hkv) they are rounded to f16, relative to the row's largest: to 11 bits or 2^-24; or, for a row that
-   sees value scales more than 2^16 apart, not at all.
+   sees value scales more than 2^16 apart, not at all.  (A row's largest |q| * scale is to be 0 or between 2^-110 and
+   2^111 there, so that its factor and its products with the codes stay in fp32's range.)
+   Sums of weights (up to 2^8 in a chunk) times values are divided at the end: they have to stay finite in fp32.
+   (A sequence's rounding so depends on max_q, the longest one's tokens in a serving batch.)
    Deterministic: the same call gives the same bits.  A call of more than 2^30 steps of 128 keys an SM does
    nothing, and fdma_get_device_error() returns FDMA_ERR_UNSUPPORTED. */
 FDMA_API int fdma_paged_fwd(const fdma_paged_args* args, void* out, float* lse, void* stream);

@@ -1130,3 +1130,18 @@ def test_scale_bytes_of_unseen_keys_reach_no_row(P, d):
             got = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
             s.ke.copy_(clean[0]), s.ve.copy_(clean[1])
             assert torch.equal(got[0][:-1], want[0][:-1]) and torch.equal(got[1][:, :-1], want[1][:, :-1])
+
+def test_least_codes_at_the_least_scales_read_back_rounded_once(P):
+    """Scale bytes 1 and 2 with subnormal codes lie below bf16's least step, 2^-133: rounded once, to nearest even.
+    From byte 3 on every value is exact."""
+    s = Setup(P, [3], 1, 128, 16, True, seed=1)
+    pg = int(s.table[0, 0])
+    code = torch.arange(128, dtype=torch.uint8)
+    code[127] = 126
+    byte = torch.tensor([1, 2, 3], dtype=torch.uint8)
+    s.vc.view(torch.uint8)[pg, :3, 0] = code.cuda()
+    s.ve[pg, :3, 0] = byte.cuda()
+    want = torch.tensor(orc.dequantise(code.numpy()[None].repeat(3, 0), byte.numpy()))
+    _, v = P.kv_gather(*s.at, _cu([3]), 3, **s.ex)
+    assert torch.equal(v[:, 0].cpu(), want.bfloat16())
+    assert torch.equal(v[2, 0].cpu().double(), want[2]) and not torch.equal(v[0, 0].cpu().double(), want[0])
