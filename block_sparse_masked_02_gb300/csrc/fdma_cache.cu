@@ -7,8 +7,8 @@
 // (LPR = 16 or 8 lanes a row, eight values a lane), e4m3 twice four or eight (8 or 4 lanes a row, 16
 // values a lane, so that codes too move 16 bytes at a time).  The sequence is searched once for them,
 // and every row's load is issued before the first is used.  (Four passes: eight, with fewer warps
-// on an SM, took 60 instead of 52 us for 82 thousand tokens of four bf16 heads, 6.4 TB/s read and
-// written; quantising 19 thousand tokens of eight heads took 23 us, 5.1 TB/s.)
+// on an SM, took 60 instead of 52 us for 82 thousand tokens of four bf16 heads with some of them in L2; with none
+// there it takes 54 us, 6.2 TB/s read and written.  Quantising 19 thousand tokens of eight heads took 23 us, 5.1 TB/s.)
 //
 // e4m3: with m = max |x| of a row, e is the least integer with m <= 448 * 2^e, taken from
 // m's bits: 448 = 1.75 * 2^8, so e = E - 8 where m = f * 2^E has f <= 1.75 and E - 7

@@ -8,7 +8,7 @@
 // rows (192 KB on an SM at d = 128), with no barrier between warps inside the loop, and the
 // ring runs on across items, so that a batch of short sequences streams like one long one.
 // page_size is a multiple of 16, so a group of 16 keys lies in one page.  32 sequences of 257 to 8191 keys,
-// 8 kv heads of 128, bf16, a token each: 95 us, 5.8 TB/s of keys and values, 86 % of a plain copy's rate.
+// 8 kv heads of 128, bf16, a token each: a call of 97 us, 5.7 TB/s of keys and values, 84 % of a plain copy's rate.
 //
 // Each warp keeps its own running maximum, weight sum and output for its keys (online
 // softmax), and they are joined at the end of the item.  The products are mma.sync with the
@@ -28,8 +28,8 @@
 // apart ("wide") goes on in fp32 products of its own, in units of 1: with f16 weights a large value would
 // take the weights of all others away, in columns where it is 0 and where its own weight is 0 too.
 // What a row gets so depends on the keys that it sees alone.  Value rows of zeros do not make it wide.
-// (Keeping a unit for each row costs 4 to 5 % with several tokens a sequence and nothing with one; all rows wide,
-// two sequences of 65 thousand keys take 2.5 times as long.)
+// (A unit for each row instead of one for a warp: 26.1 against 24.8 us for a token over two sequences of 65 thousand keys, 57.6
+// against 54.1 for 16 rows of 16 sequences of 4096 keys, 8 kv heads; the first case with all rows wide: 81 us.)
 // A key is half the bytes and has the conversions on top, so a warp takes 32 keys a step: two
 // independent chains of products and half the bookkeeping a key.
 #include <cmath>
@@ -44,7 +44,7 @@ namespace {
 
 // Packed rows up to which the token kernel runs.  With 17 to 24 rows (8 kv heads, d 128) of 16
 // sequences of 4096 keys it took 69 us and the chunk kernel 59 (e4m3: 81 and 73; of one sequence of
-// 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 53 and 73).
+// 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 58 and 73).
 constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr int kNarrow = 16;  // value scales of an f16 row are at most 2^16 apart

@@ -26,9 +26,10 @@
 // The line of all items' tiles is cut into one run a CTA (fdma_paged.cuh), so a causal chunk or
 // a ragged batch keeps every SM busy to the end; the ring and the barriers run on across items.
 //
-// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 172 us, 1.50 PFLOP/s.  A slot's softmax
+// 2048 tokens over 16384 keys, 16 heads on 4 kv heads of 128, bf16: 171 us, 1.51 PFLOP/s, from a captured graph (184 us, 1.40
+// PFLOP/s, a call).  A slot's softmax
 // waits for its S and its next S for its P, about 3300 cycles a tile with the other slot's
-// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 126 us;
+// products in between.  e4m3 (333 to 1024 tokens of two sequences over 4097 to 8192 keys, 32 heads): 127 us;
 // the conversion, 1300 cycles an item, and the longer softmax share the issue slots.
 #include "fdma_paged.cuh"
 
