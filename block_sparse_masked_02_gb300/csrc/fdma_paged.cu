@@ -47,6 +47,7 @@ namespace {
 // 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 58 and 73).
 constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
+constexpr float kMostF = 3.402823466e38f;  // the largest fp32 number
 constexpr int kNarrow = 16;  // value scales of an f16 row are at most 2^16 apart
 
 // The largest value scale byte that a row has seen in the low half, 255 less the least one in the high half (0: none):
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
   };
 
   uint32_t qf[NT][D / 16][2];  // Q^T as B operands: rows n8 of each eight
-  float rowfac[NT][2];         // log2(e) * scale (and the row's power of two) of rows 2 * q4 + {0, 1}
+  float rowfac[NT][2];         // of rows 2 * q4 + {0, 1}: log2(e) * scale; e4m3: what undoes the row's power of two
   int rlo[NT][2], rhi[NT][2];  // their keys
   float o[NT][D / 16][4];      // O^T: head dim n8 (+ 8; e4m3: 2 * n8 + {0, 1}) of each 16, rows 2 * q4 + {0, 1}
   float m[NT][2], l[NT][2];
@@ -317,12 +318,12 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         if (FP8) {
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          // q * 2^up has its largest part in [2^14, 2^15)
+          // q * 2^up has its largest part in [2^14, 2^15) (below, where that is subnormal)
           const int E = static_cast<int>(top >> 7);
-          const int up = E == 0 || E == 255 ? 0 : 14 + 127 - E;
+          const int up = E == 255 ? 0 : 14 + 127 - max(E, 1);
           const float f1 = __uint_as_float(static_cast<uint32_t>(127 + up / 2) << 23);
           const float f2 = __uint_as_float(static_cast<uint32_t>(127 + up - up / 2) << 23);
-          fac = p.scale_log2 / f1 / f2;
+          fac = 1.f / f1 / f2;
 #pragma unroll
           for (int s = 0; s < D / 16; ++s)
 #pragma unroll
@@ -421,7 +422,7 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
         for (int g = 0; g < KG; ++g)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            kf[g][e] = exp_scale(ex[g * 16 + n8 + 8 * e]);
+            kf[g][e] = exp_scale(ex[g * 16 + n8 + 8 * e]) * p.scale_log2;
             vx[g][e] = ex[STEP + g * 16 + n8 + 8 * e];
           }
         bool grows = false, widens = false;
@@ -510,8 +511,9 @@ __global__ void __launch_bounds__(TokCfg<D, FP8, NT>::kThreads, 1)
           for (int g = 0; g < KG; ++g)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float u = s[g][nt][2 * e + r] * rowfac[nt][r];
-              if (FP8) u *= kf[g][e];
+              // (e4m3: the two factors first, as either alone may take the sum out of fp32's range; together they are too
+              // large only where the score is at least 2^95, or 0)
+              float u = s[g][nt][2 * e + r] * (FP8 ? fminf(kf[g][e] * rowfac[nt][r], kMostF) : rowfac[nt][r]);
               if (masked) {
                 const int j = j0 + g * 16 + n8 + 8 * e;
                 if (!(j < rhi[nt][r] && (j >= rlo[nt][r] || j < p.sinks))) u = kNInf;

@@ -123,8 +123,7 @@ FDMA_API size_t fdma_paged_workspace_size(const fdma_paged_args* args);
    it, whatever they hold.  Precision: products in fp32 from the bf16 (or exact e4m3) values, the
    softmax in fp32; for the product with V the weights are rounded to bf16.  With an e4m3 cache and at most 16 rows
    (max_q * Hq / Hkv) they are rounded to f16, relative to the row's largest: to 11 bits or 2^-24; or, for a row that
-   sees value scales more than 2^16 apart, not at all.  (A row's largest |q| * scale is to be 0 or between 2^-110 and
-   2^111 there, so that its factor and its products with the codes stay in fp32's range.)
+   sees value scales more than 2^16 apart, not at all.
    Sums of weights (up to 2^8 in a chunk) times values are divided at the end: they have to stay finite in fp32.
    (A sequence's rounding so depends on max_q, the longest one's tokens in a serving batch.)
    Deterministic: the same call gives the same bits.  A call of more than 2^30 steps of 128 keys an SM does

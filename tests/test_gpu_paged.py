@@ -1145,3 +1145,44 @@ def test_least_codes_at_the_least_scales_read_back_rounded_once(P):
     _, v = P.kv_gather(*s.at, _cu([3]), 3, **s.ex)
     assert torch.equal(v[:, 0].cpu(), want.bfloat16())
     assert torch.equal(v[2, 0].cpu().double(), want[2]) and not torch.equal(v[0, 0].cpu().double(), want[0])
+
+
+@pytest.mark.parametrize("news,G", [([1], 1), ([2, 1], 4), ([4], 4), ([5], 4)])
+@pytest.mark.parametrize("size", [124, 116, 60, -60, -112, -116, -127])
+def test_queries_of_any_size_meet_keys_that_undo_it(P, news, G, size):
+    """q of 2^size and K of 2^-size: scores of ordinary size, wherever in fp32's range q itself lies (below 2^-126 it is
+    subnormal, and rounded to that when it is made)."""
+    d, lens = 128, [300 + 70 * b for b in range(len(news))]
+    s = Setup(P, lens, 2, d, 16, True, seed=size % 7)
+    for b, n in enumerate(lens):
+        x = torch.randn(n, 2, d, generator=torch.Generator().manual_seed(b)).bfloat16().double().numpy() * 2.0 ** min(-size, 124)
+        code, byte = orc.quantise(x)
+        pos = torch.arange(n)
+        pg, sl = s.table[b, (pos // 16).cuda()].long(), (pos % 16).cuda()
+        s.kc.view(torch.uint8)[pg, sl], s.ke[pg, sl] = torch.from_numpy(code).cuda(), torch.from_numpy(byte).cuda()
+        s.K[b] = orc.dequantise(code, byte)
+    g = torch.Generator().manual_seed(9)
+    q = (torch.randn(sum(news), 2 * G, d, generator=g).bfloat16().double() * 2.0 ** size).bfloat16().cuda()
+    assert torch.isfinite(q).all() and bool((q != 0).any())
+    out, lse = P.fwd(q, *s.at, _cu(news), max(news), **s.ex)
+    _check_attention(s, q, news, out, lse)
+
+
+def test_a_large_key_at_right_angles_scores_zero(P):
+    """Keys of 2^118 in a column where q is zero, beside keys that undo a q of 2^100."""
+    d, n = 128, 200
+    s = Setup(P, [n], 1, d, 16, True, seed=3)
+    x = torch.randn(n, 1, d, generator=torch.Generator().manual_seed(5)).bfloat16().double().numpy() * 2.0 ** -100
+    x[:, :, 0] = 0
+    x[::9] = 0
+    x[::9, :, 0] = 2.0 ** 118
+    code, byte = orc.quantise(x)
+    pos = torch.arange(n)
+    pg, sl = s.table[0, (pos // 16).cuda()].long(), (pos % 16).cuda()
+    s.kc.view(torch.uint8)[pg, sl], s.ke[pg, sl] = torch.from_numpy(code).cuda(), torch.from_numpy(byte).cuda()
+    s.K[0] = orc.dequantise(code, byte)
+    for new in (1, 4, 20):
+        q = (torch.randn(new, 4, d, generator=torch.Generator().manual_seed(new)).double() * 2.0 ** 100).bfloat16().cuda()
+        q[..., 0] = 0
+        out, lse = P.fwd(q, *s.at, _cu([new]), new, **s.ex)
+        _check_attention(s, q, [new], out, lse)
