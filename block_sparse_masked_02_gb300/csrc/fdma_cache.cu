@@ -387,6 +387,7 @@ int validate_cache(const fdma_kv_cache* c) {
   if (c->cache_type != FDMA_CACHE_BF16 && c->cache_type != FDMA_CACHE_E4M3) return FDMA_ERR_INVALID;
   const bool fp8 = c->cache_type == FDMA_CACHE_E4M3;
   if (c->d > 128 || c->d % (fp8 ? 16 : 8) != 0) return FDMA_ERR_UNSUPPORTED;
+  if (c->B > (1 << 30) || c->Hkv > (1 << 20)) return FDMA_ERR_UNSUPPORTED;  // (B + 1 and 2 * Hkv are formed in 32 bits)
   if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FDMA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(c->max_pages) * c->page_size > (1 << 30)) return FDMA_ERR_UNSUPPORTED;
   if (c->B == 0) return FDMA_OK;

@@ -951,7 +951,7 @@ int validate_paged(const fdma_paged_args* a) {
   if (static_cast<int64_t>(a->T) * a->Hq > 0x7fffff00 || a->max_q > (1 << 30) / a->Hq) return FDMA_ERR_UNSUPPORTED;
   if (a->causal != 0 && a->causal != 1) return FDMA_ERR_INVALID;
   if (a->window < 0 || a->sinks < 0 || (a->window > 0 && a->causal == 0)) return FDMA_ERR_INVALID;
-  if (!(std::isfinite(a->scale) && a->scale > 0.f)) return FDMA_ERR_INVALID;
+  if (!(std::isfinite(a->scale * kPLog2e) && a->scale > 0.f)) return FDMA_ERR_INVALID;
   return FDMA_OK;
 }
 

@@ -50,8 +50,8 @@ extern "C" {
 typedef enum { FDMA_CACHE_BF16 = 0, FDMA_CACHE_E4M3 = 1 } fdma_cache_type;
 
 typedef struct fdma_kv_cache {
-  int32_t B;          /* sequences: rows of page_table, entries of k_len */
-  int32_t Hkv, d;     /* kv heads; head dim, a multiple of 8 (bf16) or 16 (e4m3), at most 128 */
+  int32_t B;          /* sequences (at most 2^30): rows of page_table, entries of k_len */
+  int32_t Hkv, d;     /* kv heads (at most 2^20); head dim, a multiple of 8 (bf16) or 16 (e4m3), at most 128 */
   int32_t cache_type; /* fdma_cache_type */
   int32_t num_pages;  /* pages of k and v */
   int32_t page_size;  /* tokens of a page: a power of two, 16 to 4096 */
@@ -90,7 +90,7 @@ typedef struct fdma_paged_args {
   int32_t causal; /* 1: the row at position p sees keys j <= p; 0: all k_len[b] keys */
   int32_t window; /* > 0 (causal only): of those, j > p - window or j < sinks; 0: no window */
   int32_t sinks;  /* first tokens that stay visible to every later row (ignored without a window) */
-  float scale;    /* multiplies q.k; finite and > 0 */
+  float scale;    /* multiplies q.k; > 0, and finite times log2(e) */
 
   void* workspace; /* >= fdma_paged_workspace_size() bytes, 256-byte aligned; holds nothing between
                       calls.  Calls that may run at the same time (two streams, two captured graphs)

@@ -156,3 +156,18 @@ def test_workspace_must_be_contiguous(P):
     for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 30), torch.empty(64, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="contiguous"):
             P.make_args(q, kc, vc, table, lens, cu, 1, workspace=ws)
+
+
+@pytest.mark.parametrize("field,value,status", [("scale", 3e38, 1), ("Hkv", (1 << 20) + 1, 2), ("B", (1 << 30) + 1, 2)])
+def test_sizes_that_32_bit_arithmetic_does_not_hold_are_refused(P, field, value, status):
+    """scale * log2(e) has to be finite in fp32; 2 * Hkv and B + 1 are formed in 32 bits."""
+    kw = {field: value}
+    if field == "Hkv":
+        kw["Hq"] = value
+    a = _args(P, **kw)
+    lib, st = P.load(), struct.pack("2q", 256, 128)
+    assert lib.fdma_paged_fwd(bytes(a), FAKE, FAKE, None) == status
+    assert lib.fdma_paged_workspace_size(bytes(a)) == 0
+    if field != "scale":
+        assert lib.fdma_kv_append(bytes(a.cache), FAKE, st, FAKE, st, FAKE, 4, None) == status
+        assert lib.fdma_kv_gather(bytes(a.cache), FAKE, None, 4, FAKE, FAKE, None) == status
