@@ -28,7 +28,7 @@
 // apart ("wide") goes on in fp32 products of its own, in units of 1: with f16 weights a large value would
 // take the weights of all others away, in columns where it is 0 and where its own weight is 0 too.
 // What a row gets so depends on the keys that it sees alone.  Value rows of zeros do not make it wide.
-// (A unit for each row instead of one for a warp: 26.1 against 24.8 us for a token over two sequences of 65 thousand keys, 57.6
+// (A unit for each row instead of one for a warp: 26.1 against 24.8 us for a token over two sequences of 65 thousand keys, 58.6
 // against 54.1 for 16 rows of 16 sequences of 4096 keys, 8 kv heads; the first case with all rows wide: 81 us.)
 // A key is half the bytes and has the conversions on top, so a warp takes 32 keys a step: two
 // independent chains of products and half the bookkeeping a key.
@@ -44,7 +44,7 @@ namespace {
 
 // Packed rows up to which the token kernel runs.  With 17 to 24 rows (8 kv heads, d 128) of 16
 // sequences of 4096 keys it took 69 us and the chunk kernel 59 (e4m3: 81 and 73; of one sequence of
-// 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 58 and 73).
+// 32768 keys 41 and 40, e4m3 42 and 42), with 9 to 16 rows 57 and 59 (e4m3 59 and 73).
 constexpr int kTokenRows = 16;
 constexpr float kNInf = -__builtin_huge_valf();
 constexpr float kMostF = 3.402823466e38f;  // the largest fp32 number

@@ -165,7 +165,7 @@ _PACK_2Q = struct.Struct("2q").pack
 def kv_append(k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, k_exp=None, v_exp=None, stream=None):
     """Write the new tokens' rows k, v (T, Hkv, d) bf16 (contiguous head dim) into the cache, quantised
     (with their scale bytes into k_exp, v_exp) where it is float8_e4m3fn.  Rows behind cu_q[B] are ignored.
-    The slots of one call must be distinct."""
+    The slots of one call must be distinct, and none may hold a row of k or v itself."""
     dev = _check_device(k, v, k_cache, v_cache, page_table, k_lens, cu_q, k_exp, v_exp)
     c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
     B, Hkv, d = c[:3]

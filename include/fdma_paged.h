@@ -100,7 +100,8 @@ typedef struct fdma_paged_args {
 
 /* Writes k_new and v_new ((T, Hkv, d) bf16; strides (token, head) in elements, multiples of 8, d
    contiguous, bases 16-byte aligned) of the tokens cu[0] .. cu[B]-1 into the cache.  The slots of
-   one call must be distinct (a page that several sequences share is written by none of them).
+   one call must be distinct (a page that several sequences share is written by none of them), and
+   none may hold a row of k_new or v_new.
    All else in the cache is left as it is. */
 FDMA_API int fdma_kv_append(const fdma_kv_cache* cache, const void* k_new, const int64_t k_new_stride[2],
                             const void* v_new, const int64_t v_new_stride[2], const int32_t* cu, int T, void* stream);
