@@ -13,6 +13,10 @@
 // e4m3: with m = max |x| of a row, e is the least integer with m <= 448 * 2^e, taken from
 // m's bits: 448 = 1.75 * 2^8, so e = E - 8 where m = f * 2^E has f <= 1.75 and E - 7
 // otherwise.  x * 2^-e is exact, so each value is rounded once.
+//
+// norm_rope_append_kernel writes keys that it has divided by their root mean square and
+// turned on the way (fdma_norm_rope.cuh), and the queries beside them into their own rows.
+#include "fdma_norm_rope.cuh"
 #include "fdma_paged.cuh"
 
 namespace fdma {
@@ -23,6 +27,7 @@ struct Move {
   static constexpr int kPasses = FP8 ? 2 : 4, kValues = FP8 ? 16 : 8, kVec = kValues / 8;
 };
 constexpr int kCacheThreads = 128;
+constexpr int kNormAppendRows = 4;  // rows of a lane
 
 struct MoveParams {
   CacheView c;
@@ -341,6 +346,127 @@ __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_c
   }
 }
 
+struct NormAppendParams {
+  MoveParams m;  // k_new, v_new are not used
+  NormRopeView v;
+  int H, Hq;  // rows of a token: Hq of q, Hkv of k, Hkv of v
+  RowsView in[3], q_out;
+};
+
+// A row of fp32 values as e4m3 codes of the pieces that a lane holds, and e + 127 in `be`: quantise16's rule, from
+// values that are rounded for the first time.  Every lane of the warp calls it; lanes that hold nothing have zeros.
+template <int LPR, bool ADJ>
+__device__ __forceinline__ uint2 quantise_pairs(const Pairs& x, uint32_t& be) {
+  const float v[8] = {x.a[0], ADJ ? x.b[0] : x.a[1], ADJ ? x.a[1] : x.a[2], ADJ ? x.b[1] : x.a[3],
+                      ADJ ? x.a[2] : x.b[0], ADJ ? x.b[2] : x.b[1], ADJ ? x.a[3] : x.b[2], x.b[3]};
+  uint32_t m = 0;  // largest finite magnitude, as bits
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
+    m = max(m, a < 0x7f800000u ? a : 0u);
+  }
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int E = static_cast<int>(m >> 23), up = (m & 0x7fffffu) > 0x600000u ? 1 : 0;
+  const int b = min(max(E - 8 + up, 1), 246);
+  be = static_cast<uint32_t>(b);
+  const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
+    h[i] = r;
+  }
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+template <bool FP8, int LPR, bool ADJ>
+__global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
+  constexpr int RPW = 32 / LPR, ROWS = kNormAppendRows;
+  const int lane = threadIdx.x & 31, l = lane % LPR;
+  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5)) * (RPW * ROWS);
+  const int64_t tok0 = first / p.H;
+  if (tok0 >= p.m.T) return;  // (never a block's first warp)
+  const int rem = static_cast<int>(first - tok0 * p.H);
+  check_offsets(p.m);
+  const Lane at = lane_of<ADJ>(p.v, l);
+  Raw raw[ROWS];
+  int head[ROWS], side[ROWS];
+  int64_t tok[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    const int x = rem + i * RPW + lane / LPR, t = x / p.H;
+    tok[i] = tok0 + t;
+    head[i] = x - t * p.H;
+    side[i] = head[i] < p.Hq ? 0 : head[i] < p.Hq + p.m.c.Hkv ? 1 : 2;
+    head[i] -= side[i] == 0 ? 0 : side[i] == 1 ? p.Hq : p.Hq + p.m.c.Hkv;
+    raw[i] = Raw{};
+    const RowsView& s = p.in[side[i]];
+    if (at.in && tok[i] < p.m.T) raw[i] = load_raw<ADJ>(s.p + tok[i] * s.st[1] + head[i] * s.st[2], at);
+  }
+  const int b0 = find_seq(p.m.cu, p.m.c.B, static_cast<int>(tok0), lane);
+  Slot s;
+  int pos = -1;  // that the rotation goes by; negative: the token is left out
+  auto look_up = [&](int64_t token) {
+    s = Slot{};
+    s.tok = token;
+    pos = -1;
+    const int t = static_cast<int>(token), b = seq_from(p.m, b0, t);
+    if (b < 0) return;  // behind the last sequence
+    const int kl = p.m.c.k_len[b], at_pos = kl < 0 ? -1 : kl - (p.m.cu[b + 1] - t);
+    if (at_pos < 0 || kl > p.m.c.max_pages << p.m.c.page_shift) {
+      atomicCAS(p.m.err, 0, FDMA_ERR_INVALID);
+      return;
+    }
+    const int turn_pos = checked_position(p.v, p.v.pos != nullptr ? p.v.pos[token * p.v.pos_st[1]] : at_pos, p.m.err);
+    if (turn_pos < 0) return;
+    const int pg = page_at(p.m, b, at_pos);
+    if (pg < 0) return;
+    set_slot<FP8>(p.m, s, pg, at_pos);
+    pos = turn_pos;
+  };
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (tok[i] < p.m.T && tok[i] != s.tok) look_up(tok[i]);
+    const bool left_out = tok[i] >= p.m.T || pos < 0;
+    const bool is_v = side[i] == 2;
+    const Lane n{at.ca, at.cb, at.in, at.turned && !is_v};
+    const Turn t = load_turn(p.v, left_out ? 0 : pos, l, n);
+    const Pairs w = load_weight<ADJ>(p.v, is_v ? 0 : side[i], head[i], n);
+    Pairs x = widen<ADJ>(raw[i]);
+    if (p.v.norm) {
+      Pairs y = x;
+      norm_and_turn<LPR>(p.v, y, w, t, n);
+      if (!is_v) x = y;
+    } else {
+      turn<false>(x, t, n);
+    }
+    uint32_t be = 0;
+    uint2 code = make_uint2(0u, 0u);
+    if constexpr (FP8) code = quantise_pairs<LPR, ADJ>(x, be);
+    if (left_out) continue;
+    const Raw out = is_v ? raw[i] : narrow<ADJ>(x);
+    if (side[i] == 0) {
+      if (at.in) store_raw<ADJ>(p.q_out.p + tok[i] * p.q_out.st[1] + head[i] * p.q_out.st[2], at, out);
+      continue;
+    }
+    uint8_t* dst = const_cast<uint8_t*>(is_v ? p.m.c.v : p.m.c.k) + (is_v ? s.v : s.k) +
+                   head[i] * (is_v ? p.m.c.vs[2] : p.m.c.ks[2]);
+    if (!FP8) {
+      if (at.in) store_raw<ADJ>(reinterpret_cast<uint16_t*>(dst), at, out);
+      continue;
+    }
+    if (at.in) {
+      *reinterpret_cast<uint32_t*>(dst + at.ca) = code.x;
+      *reinterpret_cast<uint32_t*>(dst + at.cb) = code.y;
+    }
+    if (l == 0)
+      const_cast<uint8_t*>(is_v ? p.m.c.ve : p.m.c.ke)[(is_v ? s.ve : s.ke) + head[i] * (is_v ? p.m.c.ves[2] : p.m.c.kes[2])] =
+          static_cast<uint8_t>(be);
+  }
+}
+
 struct Append {
   template <bool FP8, int LPR, bool ONE>
   static auto kernel() {
@@ -376,6 +502,22 @@ int64_t move_blocks(int T, int Hkv, int d) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Whether distinct slots are distinct memory.
+bool distinct_slots(const fdma_kv_cache& c) {
+  for (int i = 0; i < 3; ++i) {
+    const int n = i == 0 ? c.num_pages : i == 1 ? c.page_size : c.Hkv;
+    if (n > 1 && (c.k_stride[i] == 0 || c.v_stride[i] == 0)) return false;
+    if (n > 1 && c.cache_type == FDMA_CACHE_E4M3 && (c.k_exp_stride[i] == 0 || c.v_exp_stride[i] == 0)) return false;
+  }
+  return true;
+}
+
+template <bool FP8>
+auto norm_append_kernel(int d, bool adj) {
+  if (d <= 64) return adj ? norm_rope_append_kernel<FP8, 8, true> : norm_rope_append_kernel<FP8, 8, false>;
+  return adj ? norm_rope_append_kernel<FP8, 16, true> : norm_rope_append_kernel<FP8, 16, false>;
+}
 
 }  // namespace
 
@@ -453,13 +595,7 @@ int fdma_kv_append(const fdma_kv_cache* c, const void* k_new, const int64_t kn[2
     if (kn[i] < 0 || vn[i] < 0) return FDMA_ERR_INVALID;
     if (kn[i] % 8 != 0 || vn[i] % 8 != 0) return FDMA_ERR_UNSUPPORTED;
   }
-  // distinct slots must be distinct memory
-  for (int i = 0; i < 3; ++i) {
-    const int n = i == 0 ? c->num_pages : i == 1 ? c->page_size : c->Hkv;
-    if (n > 1 && (c->k_stride[i] == 0 || c->v_stride[i] == 0)) return FDMA_ERR_INVALID;
-    if (n > 1 && c->cache_type == FDMA_CACHE_E4M3 && (c->k_exp_stride[i] == 0 || c->v_exp_stride[i] == 0))
-      return FDMA_ERR_INVALID;
-  }
+  if (!distinct_slots(*c)) return FDMA_ERR_INVALID;
   const int64_t blocks = move_blocks(T, c->Hkv, c->d);
   if (blocks > 0x1fffffff) return FDMA_ERR_UNSUPPORTED;
   MoveParams p{};
@@ -502,6 +638,46 @@ int fdma_kv_gather(const fdma_kv_cache* c, const int32_t* cu, const int32_t* fir
   if (p.err == nullptr) return FDMA_ERR_CUDA;
   launch_move(c->cache_type == FDMA_CACHE_E4M3, c->d, c->Hkv, static_cast<unsigned>(blocks), p,
               static_cast<cudaStream_t>(stream), Gather{});
+  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+}
+
+int fdma_norm_rope_append(const fdma_norm_rope_args* a, const fdma_kv_cache* c, const fdma_rows* q, const fdma_rows* k,
+                          const fdma_rows* v, const fdma_rows* q_out, const int32_t* cu, void* stream) {
+  int st = validate_norm_rope(a);
+  if (st == FDMA_OK) st = validate_cache(c);
+  if (st != FDMA_OK) return st;
+  if (a->B != 1 || a->Hk != c->Hkv || a->d != c->d) return FDMA_ERR_INVALID;
+  if (a->positions != nullptr && a->pos_stride[1] < 0) return FDMA_ERR_INVALID;
+  const int T = a->N;
+  if (T == 0 || c->B == 0) return FDMA_OK;
+  if (cu == nullptr) return FDMA_ERR_INVALID;
+  const int64_t nq[3] = {1, T, a->Hq}, nk[3] = {1, T, a->Hk};
+  st = validate_rows(q, nq, false);
+  if (st == FDMA_OK) st = validate_rows(k, nk, false);
+  if (st == FDMA_OK) st = validate_rows(v, nk, false);
+  if (st == FDMA_OK) st = validate_rows(q_out, nq, true);
+  if (st != FDMA_OK) return st;
+  if (!distinct_slots(*c)) return FDMA_ERR_INVALID;
+  NormAppendParams p{};
+  p.H = a->Hq + 2 * c->Hkv;
+  const int per = (c->d > 64 ? 2 : 4) * kNormAppendRows * (kCacheThreads / 32);
+  const int64_t blocks = (static_cast<int64_t>(T) * p.H + per - 1) / per;
+  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  p.m.c = cache_view(*c);
+  p.m.cu = cu;
+  p.m.T = T;
+  p.m.check_blocks = (static_cast<unsigned>(c->B) + 31) / 32;
+  p.m.err = paged_error_word();
+  if (p.m.err == nullptr) return FDMA_ERR_CUDA;
+  p.v = norm_rope_view(*a);
+  p.Hq = a->Hq;
+  p.in[0] = rows_view(*q);
+  p.in[1] = rows_view(*k);
+  p.in[2] = rows_view(*v);
+  p.q_out = rows_view(*q_out);
+  const auto kern = c->cache_type == FDMA_CACHE_E4M3 ? norm_append_kernel<true>(c->d, a->interleaved != 0)
+                                                     : norm_append_kernel<false>(c->d, a->interleaved != 0);
+  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
