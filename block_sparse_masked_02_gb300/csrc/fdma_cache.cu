@@ -27,7 +27,6 @@ struct Move {
   static constexpr int kPasses = FP8 ? 2 : 4, kValues = FP8 ? 16 : 8, kVec = kValues / 8;
 };
 constexpr int kCacheThreads = 128;
-constexpr int kNormAppendRows = 4;  // rows of a lane
 
 struct MoveParams {
   CacheView c;
@@ -349,19 +348,25 @@ __global__ void __launch_bounds__(kCacheThreads) kv_gather_kernel(const __grid_c
 struct NormAppendParams {
   MoveParams m;  // k_new, v_new are not used
   NormRopeView v;
-  int H, Hq;  // rows of a token: Hq of q, Hkv of k, Hkv of v
+  int H[3], end[3];  // heads of q, k, v; the passes of each end there
+  PassPlan plan;
   RowsView in[3], q_out;
 };
 
-// A row of fp32 values as e4m3 codes of the pieces that a lane holds, and e + 127 in `be`: quantise16's rule, from
-// values that are rounded for the first time.  Every lane of the warp calls it; lanes that hold nothing have zeros.
-template <int LPR, bool ADJ>
-__device__ __forceinline__ uint2 quantise_pairs(const Pairs& x, uint32_t& be) {
-  const float v[8] = {x.a[0], ADJ ? x.b[0] : x.a[1], ADJ ? x.a[1] : x.a[2], ADJ ? x.b[1] : x.a[3],
-                      ADJ ? x.a[2] : x.b[0], ADJ ? x.b[2] : x.b[1], ADJ ? x.a[3] : x.b[2], x.b[3]};
+// A row of fp32 values as e4m3 codes, e + 127 in `be`: quantise16's rule, for values that are rounded for the first
+// time.  Codes are in the order of the lane's columns.  Every lane of the warp calls it; lanes that hold nothing
+// have zeros.
+template <int LPR, int P, bool ADJ>
+__device__ __forceinline__ void quantise_pairs(const Pairs<P>& x, uint32_t (&code)[P / 2], uint32_t& be) {
+  float v[2 * P];
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    f2split(x.a[i], v[ADJ ? 4 * i : 2 * i], v[ADJ ? 4 * i + 2 : 2 * i + 1]);
+    f2split(x.b[i], v[ADJ ? 4 * i + 1 : P + 2 * i], v[ADJ ? 4 * i + 3 : P + 2 * i + 1]);
+  }
   uint32_t m = 0;  // largest finite magnitude, as bits
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2 * P; ++i) {
     const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
     m = max(m, a < 0x7f800000u ? a : 0u);
   }
@@ -371,99 +376,106 @@ __device__ __forceinline__ uint2 quantise_pairs(const Pairs& x, uint32_t& be) {
   const int b = min(max(E - 8 + up, 1), 246);
   be = static_cast<uint32_t>(b);
   const float inv = __uint_as_float(static_cast<uint32_t>(254 - b) << 23);
-  uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v[2 * i + 1] * inv), "f"(v[2 * i] * inv));
-    h[i] = r;
+  for (int i = 0; i < P / 2; ++i) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * i + 1] * inv), "f"(v[4 * i] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * i + 3] * inv), "f"(v[4 * i + 2] * inv));
+    code[i] = lo | (static_cast<uint32_t>(hi) << 16);
   }
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-template <bool FP8, int LPR, bool ADJ>
-__global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
-  constexpr int RPW = 32 / LPR, ROWS = kNormAppendRows;
-  const int lane = threadIdx.x & 31, l = lane % LPR;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kCacheThreads / 32) + (threadIdx.x >> 5)) * (RPW * ROWS);
-  const int64_t tok0 = first / p.H;
-  if (tok0 >= p.m.T) return;  // (never a block's first warp)
-  const int rem = static_cast<int>(first - tok0 * p.H);
-  check_offsets(p.m);
-  const Lane at = lane_of<ADJ>(p.v, l);
-  Raw raw[ROWS];
-  int head[ROWS], side[ROWS];
-  int64_t tok[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int x = rem + i * RPW + lane / LPR, t = x / p.H;
-    tok[i] = tok0 + t;
-    head[i] = x - t * p.H;
-    side[i] = head[i] < p.Hq ? 0 : head[i] < p.Hq + p.m.c.Hkv ? 1 : 2;
-    head[i] -= side[i] == 0 ? 0 : side[i] == 1 ? p.Hq : p.Hq + p.m.c.Hkv;
-    raw[i] = Raw{};
-    const RowsView& s = p.in[side[i]];
-    if (at.in && tok[i] < p.m.T) raw[i] = load_raw<ADJ>(s.p + tok[i] * s.st[1] + head[i] * s.st[2], at);
+template <int P>
+__device__ __forceinline__ void store_codes(uint8_t* row, const Lane& n, const uint32_t (&c)[P / 2]) {
+  if constexpr (P == 8) {
+    *reinterpret_cast<uint2*>(row + n.ca) = make_uint2(c[0], c[1]);
+    *reinterpret_cast<uint2*>(row + n.cb) = make_uint2(c[2], c[3]);
+  } else {
+    *reinterpret_cast<uint32_t*>(row + n.ca) = c[0];
+    *reinterpret_cast<uint32_t*>(row + n.cb) = c[1];
   }
-  const int b0 = find_seq(p.m.cu, p.m.c.B, static_cast<int>(tok0), lane);
-  Slot s;
-  int pos = -1;  // that the rotation goes by; negative: the token is left out
-  auto look_up = [&](int64_t token) {
-    s = Slot{};
-    s.tok = token;
-    pos = -1;
-    const int t = static_cast<int>(token), b = seq_from(p.m, b0, t);
-    if (b < 0) return;  // behind the last sequence
-    const int kl = p.m.c.k_len[b], at_pos = kl < 0 ? -1 : kl - (p.m.cu[b + 1] - t);
-    if (at_pos < 0 || kl > p.m.c.max_pages << p.m.c.page_shift) {
-      atomicCAS(p.m.err, 0, FDMA_ERR_INVALID);
-      return;
-    }
-    const int turn_pos = checked_position(p.v, p.v.pos != nullptr ? p.v.pos[token * p.v.pos_st[1]] : at_pos, p.m.err);
-    if (turn_pos < 0) return;
-    const int pg = page_at(p.m, b, at_pos);
-    if (pg < 0) return;
-    set_slot<FP8>(p.m, s, pg, at_pos);
-    pos = turn_pos;
-  };
+}
+
+// A warp takes a token, or a run of its passes where there are few tokens: queries, keys, values, in this order.
+template <bool FP8, int P, int LPR, bool ADJ>
+__global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
+  constexpr int RPW = 32 / LPR, R = 16 / P;
+  const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
+  const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+  uint32_t tok = w, c = 0;
+  if (p.plan.chunks > 1) {
+    tok = w / p.plan.chunks;
+    c = w - tok * p.plan.chunks;
+  }
+  if (tok >= static_cast<uint32_t>(p.m.T)) return;  // (never a block's first warp)
+  check_offsets(p.m);
+  const Lane at = lane_of<P, ADJ>(p.v, l);
+  auto side_of = [&](int q) { return q < p.end[0] ? 0 : q < p.end[1] ? 1 : 2; };
+  auto head_of = [&](int q, int side) { return (q - (side > 0 ? p.end[side - 1] : 0)) * RPW + g; };
+  const int q1 = min(static_cast<int>(c + 1) * p.plan.per, p.plan.passes);
+  int q0 = static_cast<int>(c) * p.plan.per;
+  Raw<P> raw[R];
+  // the rows themselves do not depend on the slot: load them while it is looked up
+  auto load = [&] {
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (tok[i] < p.m.T && tok[i] != s.tok) look_up(tok[i]);
-    const bool left_out = tok[i] >= p.m.T || pos < 0;
-    const bool is_v = side[i] == 2;
-    const Lane n{at.ca, at.cb, at.in, at.turned && !is_v};
-    const Turn t = load_turn(p.v, left_out ? 0 : pos, l, n);
-    const Pairs w = load_weight<ADJ>(p.v, is_v ? 0 : side[i], head[i], n);
-    Pairs x = widen<ADJ>(raw[i]);
-    if (p.v.norm) {
-      Pairs y = x;
-      norm_and_turn<LPR>(p.v, y, w, t, n);
-      if (!is_v) x = y;
-    } else {
-      turn<false>(x, t, n);
+    for (int i = 0; i < R; ++i) {
+      const int side = side_of(q0 + i), h = head_of(q0 + i, side);
+      raw[i] = no_raw<P>();
+      if (q0 + i < q1 && at.in && h < p.H[side])
+        raw[i] = load_raw<P>(p.in[side].p + tok * p.in[side].st[1] + h * p.in[side].st[2], at);
     }
-    uint32_t be = 0;
-    uint2 code = make_uint2(0u, 0u);
-    if constexpr (FP8) code = quantise_pairs<LPR, ADJ>(x, be);
-    if (left_out) continue;
-    const Raw out = is_v ? raw[i] : narrow<ADJ>(x);
-    if (side[i] == 0) {
-      if (at.in) store_raw<ADJ>(p.q_out.p + tok[i] * p.q_out.st[1] + head[i] * p.q_out.st[2], at, out);
-      continue;
+  };
+  load();
+  const int b = find_seq(p.m.cu, p.m.c.B, static_cast<int>(tok), lane);
+  if (b < 0) return;  // behind the last sequence
+  const int kl = p.m.c.k_len[b], slot_pos = kl < 0 ? -1 : kl - (p.m.cu[b + 1] - static_cast<int>(tok));
+  if (slot_pos < 0 || kl > p.m.c.max_pages << p.m.c.page_shift) {
+    atomicCAS(p.m.err, 0, FDMA_ERR_INVALID);
+    return;
+  }
+  const int pos = checked_position(p.v, p.v.pos != nullptr ? p.v.pos[tok * p.v.pos_st[1]] : slot_pos, p.m.err);
+  if (pos < 0) return;
+  const int pg = page_at(p.m, b, slot_pos);
+  if (pg < 0) return;
+  Slot s;
+  set_slot<FP8>(p.m, s, pg, slot_pos);
+  const Turn<P> t = load_turn<P>(p.v, pos, l, at);
+  Pairs<P> wt;
+  int have = -1;  // the tensor whose weight wt holds
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (q0 + i >= q1) break;
+      const int side = side_of(q0 + i), h = head_of(q0 + i, side);
+      const bool real = at.in && h < p.H[side];
+      Pairs<P> x = widen<P, ADJ>(raw[i]);
+      if (side < 2) {
+        if (side != have || p.v.w[side].head != 0) {
+          wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
+          have = side;
+        }
+        norm_and_turn<LPR>(p.v, x, wt, t, at);
+      }
+      if (side == 0) {
+        if (real) store_raw<P>(p.q_out.p + tok * p.q_out.st[1] + h * p.q_out.st[2], at, narrow<P, ADJ>(x));
+        continue;
+      }
+      const bool is_v = side == 2;
+      uint8_t* dst = const_cast<uint8_t*>(is_v ? p.m.c.v : p.m.c.k) + (is_v ? s.v : s.k) + h * (is_v ? p.m.c.vs[2] : p.m.c.ks[2]);
+      if constexpr (FP8) {
+        uint32_t code[P / 2], be;
+        quantise_pairs<LPR, P, ADJ>(x, code, be);
+        if (real) store_codes<P>(dst, at, code);
+        if (real && l == 0)
+          const_cast<uint8_t*>(is_v ? p.m.c.ve : p.m.c.ke)[(is_v ? s.ve : s.ke) + h * (is_v ? p.m.c.ves[2] : p.m.c.kes[2])] =
+              static_cast<uint8_t>(be);
+      } else {
+        if (real) store_raw<P>(reinterpret_cast<uint16_t*>(dst), at, is_v ? raw[i] : narrow<P, ADJ>(x));
+      }
     }
-    uint8_t* dst = const_cast<uint8_t*>(is_v ? p.m.c.v : p.m.c.k) + (is_v ? s.v : s.k) +
-                   head[i] * (is_v ? p.m.c.vs[2] : p.m.c.ks[2]);
-    if (!FP8) {
-      if (at.in) store_raw<ADJ>(reinterpret_cast<uint16_t*>(dst), at, out);
-      continue;
-    }
-    if (at.in) {
-      *reinterpret_cast<uint32_t*>(dst + at.ca) = code.x;
-      *reinterpret_cast<uint32_t*>(dst + at.cb) = code.y;
-    }
-    if (l == 0)
-      const_cast<uint8_t*>(is_v ? p.m.c.ve : p.m.c.ke)[(is_v ? s.ve : s.ke) + head[i] * (is_v ? p.m.c.ves[2] : p.m.c.kes[2])] =
-          static_cast<uint8_t>(be);
+    q0 += R;
+    if (q0 >= q1) break;
+    load();
   }
 }
 
@@ -511,12 +523,6 @@ bool distinct_slots(const fdma_kv_cache& c) {
     if (n > 1 && c.cache_type == FDMA_CACHE_E4M3 && (c.k_exp_stride[i] == 0 || c.v_exp_stride[i] == 0)) return false;
   }
   return true;
-}
-
-template <bool FP8>
-auto norm_append_kernel(int d, bool adj) {
-  if (d <= 64) return adj ? norm_rope_append_kernel<FP8, 8, true> : norm_rope_append_kernel<FP8, 8, false>;
-  return adj ? norm_rope_append_kernel<FP8, 16, true> : norm_rope_append_kernel<FP8, 16, false>;
 }
 
 }  // namespace
@@ -659,25 +665,36 @@ int fdma_norm_rope_append(const fdma_norm_rope_args* a, const fdma_kv_cache* c, 
   if (st != FDMA_OK) return st;
   if (!distinct_slots(*c)) return FDMA_ERR_INVALID;
   NormAppendParams p{};
-  p.H = a->Hq + 2 * c->Hkv;
-  const int per = (c->d > 64 ? 2 : 4) * kNormAppendRows * (kCacheThreads / 32);
-  const int64_t blocks = (static_cast<int64_t>(T) * p.H + per - 1) / per;
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  p.v = norm_rope_view(*a);
+  const int rows = pass_rows(c->d, p.v.rot);
+  int at = 0;
+  for (int i = 0; i < 3; ++i) {
+    p.H[i] = i == 0 ? a->Hq : c->Hkv;
+    p.end[i] = at += (p.H[i] + rows - 1) / rows;
+  }
+  p.plan = plan_passes(at, T, 152 * 32);
+  const int64_t per = kCacheThreads / 32, blocks = (static_cast<int64_t>(T) * p.plan.chunks + per - 1) / per;
+  if (blocks * per > 0xffffffffll) return FDMA_ERR_UNSUPPORTED;
   p.m.c = cache_view(*c);
   p.m.cu = cu;
   p.m.T = T;
   p.m.check_blocks = (static_cast<unsigned>(c->B) + 31) / 32;
   p.m.err = paged_error_word();
   if (p.m.err == nullptr) return FDMA_ERR_CUDA;
-  p.v = norm_rope_view(*a);
-  p.Hq = a->Hq;
   p.in[0] = rows_view(*q);
   p.in[1] = rows_view(*k);
   p.in[2] = rows_view(*v);
   p.q_out = rows_view(*q_out);
-  const auto kern = c->cache_type == FDMA_CACHE_E4M3 ? norm_append_kernel<true>(c->d, a->interleaved != 0)
-                                                     : norm_append_kernel<false>(c->d, a->interleaved != 0);
-  kern<<<static_cast<unsigned>(blocks), kCacheThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  with_layout(c->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
+    constexpr int kP = decltype(P)::value, kL = decltype(L)::value;
+    if constexpr (kP * kL <= 64) {  // (a cache's rows are at most 128 wide)
+      if (c->cache_type == FDMA_CACHE_E4M3)
+        norm_rope_append_kernel<true, kP, kL, decltype(A)::value><<<static_cast<unsigned>(blocks), kCacheThreads, 0, cs>>>(p);
+      else
+        norm_rope_append_kernel<false, kP, kL, decltype(A)::value><<<static_cast<unsigned>(blocks), kCacheThreads, 0, cs>>>(p);
+    }
+  });
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 

@@ -1,14 +1,14 @@
 // Norms of queries and keys for each head and the rotation of their positions, forward and
 // backward (include/fdma_inputs.h).
 //
-// Forward.  All rows of a call (token, head of q or k) form one line of which a warp takes
-// ROWS times those that its lanes hold at once; each row is read once and written once.
+// Forward.  A warp takes a token, or a run of its passes where there are few tokens; position,
+// angles and weights are looked up once for all of its rows, and each row is read once and written once.
 //
-// Backward.  With g the gradient of the output turned back, r = 1 / sqrt(mean(x^2) + eps) and
-// S = sum(g w x):  dx = r g w - x r^3 S / d,  dw = sum over tokens of g x r.
-// The rows are dealt to slots, each of which keeps one head and walks over tokens, so
-// that a weight's gradient is summed in registers; a CTA adds its slots in a fixed order and
-// writes one part for each weight row that it has, and a second kernel adds the parts.
+// Backward.  With g the gradient of the output turned back, r = 1 / sqrt(mean(x^2) + eps), xn = x r:
+//   dx = r (g w - xn mean(g w xn)),  dw = sum over tokens (and heads that share it) of g xn.
+// A CTA keeps a chunk of one tensor's heads (one pass where every head has a weight of its own) and its warps walk
+// over tokens, so that a lane has one weight and sums one gradient, in registers; the CTA adds its warps' sums in a
+// fixed order and writes one part, and a second kernel adds the parts of a weight.
 #include <cmath>
 
 #include "fdma_norm_rope.cuh"
@@ -17,34 +17,19 @@ namespace fdma {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRows = 4;     // rows of a lane
 constexpr int kBwdCtas = 304;
 
-struct FwdView {
-  NormRopeView v;
-  int H, Hq, N;  // heads of q and k together
-  int batches;   // 1: tokens are one line
+struct TokenLine {
+  int N, batches;  // batches 1: tokens are one line
   int64_t tokens;
-  RowsView in[2], out[2];
-  int* err;
 };
 
-__device__ __forceinline__ int64_t row_at(const RowsView& r, int b, int n, int h) {
-  return b * r.st[0] + n * r.st[1] + h * r.st[2];
-}
-
-// One row of the line.
-struct RowId {
-  int b, n, h, side;
-  bool real;
-};
-
-__device__ __forceinline__ void split_token(int64_t tok, int N, int batches, int& b, int& n) {
+__device__ __forceinline__ void split_token(const TokenLine& t, int64_t tok, int& b, int& n) {
   b = 0;
   n = static_cast<int>(tok);
-  if (batches > 1) {
-    b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(N));
-    n = static_cast<int>(tok) - b * N;
+  if (t.batches > 1) {
+    b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(t.N));
+    n = static_cast<int>(tok) - b * t.N;
   }
 }
 
@@ -53,159 +38,174 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
   return v.pos != nullptr ? v.pos[b * v.pos_st[0] + n * v.pos_st[1]] : v.first + n;
 }
 
-template <int LPR, bool ADJ>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ FwdView p) {
-  constexpr int RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, l = lane % LPR;
-  const int64_t first = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * (RPW * kRows);
-  const int64_t tok0 = first / p.H;
-  if (tok0 >= p.tokens) return;
-  const int rem = static_cast<int>(first - tok0 * p.H);
-  const Lane at = lane_of<ADJ>(p.v, l);
-  RowId id[kRows];
-  Raw raw[kRows];
-  int pos[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    RowId& r = id[i];
-    const int x = rem + i * RPW + lane / LPR, t = x / p.H;
-    r.h = x - t * p.H;
-    r.side = r.h >= p.Hq ? 1 : 0;
-    if (r.side) r.h -= p.Hq;
-    r.real = tok0 + t < p.tokens;
-    split_token(tok0 + t, p.N, p.batches, r.b, r.n);
-    raw[i] = Raw{};
-    pos[i] = -1;
-    if (!r.real) continue;
-    const RowsView& s = p.in[r.side];
-    if (at.in) raw[i] = load_raw<ADJ>(s.p + row_at(s, r.b, r.n, r.h), at);
-    pos[i] = position_of(p.v, r.b, r.n);
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const RowId& r = id[i];
-    const int q = r.real ? checked_position(p.v, pos[i], p.err) : -1;
-    const Turn t = load_turn(p.v, max(q, 0), l, at);
-    const Pairs w = load_weight<ADJ>(p.v, r.side, r.h, at);
-    Pairs x = widen<ADJ>(raw[i]);
-    norm_and_turn<LPR>(p.v, x, w, t, at);
-    const RowsView& o = p.out[r.side];
-    if (q >= 0 && at.in) store_raw<ADJ>(o.p + row_at(o, r.b, r.n, r.h), at, narrow<ADJ>(x));
-  }
-}
+__device__ __forceinline__ uint16_t* token_rows(const RowsView& r, int b, int n) { return r.p + b * r.st[0] + n * r.st[1]; }
 
-struct BwdView {
+struct FwdView {
   NormRopeView v;
-  int H, Hq, N, batches;
-  int64_t tokens;
-  int par, steps;  // tokens side by side; tokens of a slot
-  RowsView in[2], dout[2], din[2];
-  float* part;  // [cta][rows of a CTA][d]; nullptr: no weight's gradient
-  int part_rows;
-  int by_head;
+  TokenLine line;
+  int H[2], passes_q;
+  PassPlan plan;
+  RowsView in[2], out[2];
   int* err;
 };
 
-// Slots of a CTA: they keep heads (first slot of the CTA + j) % H.
-template <int LPR>
-constexpr int kCtaSlots = kWarps * (32 / LPR) * kRows;
-
-template <int LPR, bool ADJ>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ BwdView p) {
-  constexpr int RPW = 32 / LPR, SLOTS = kCtaSlots<LPR>, COLS = LPR * 8;
-  __shared__ float sums[SLOTS * COLS];
-  const int lane = threadIdx.x & 31, l = lane % LPR, warp = threadIdx.x >> 5;
-  const Lane at = lane_of<ADJ>(p.v, l);
-  const int slot0 = blockIdx.x * SLOTS;
-  Pairs acc[kRows];
+template <int P, int LPR, bool ADJ>
+__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ FwdView p) {
+  constexpr int RPW = 32 / LPR, R = 16 / P;  // rows of a pass; passes whose loads run together
+  const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
+  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  uint32_t tok = w, c = 0;
+  if (p.plan.chunks > 1) {
+    tok = w / p.plan.chunks;
+    c = w - tok * p.plan.chunks;
+  }
+  if (tok >= p.line.tokens) return;
+  int b, n;
+  split_token(p.line, tok, b, n);
+  const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
+  if (pos < 0) return;
+  const Lane at = lane_of<P, ADJ>(p.v, l);
+  const Turn<P> t = load_turn<P>(p.v, pos, l, at);
+  const int q1 = min(static_cast<int>(c + 1) * p.plan.per, p.plan.passes);
+  Pairs<P> wt;
+  int have = -1;  // the tensor whose weight wt holds
+  for (int q0 = static_cast<int>(c) * p.plan.per; q0 < q1; q0 += R) {
+    Raw<P> raw[R];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[i].a[e] = acc[i].b[e] = 0.f;
-  for (int k = 0; k < p.steps; ++k) {
-    RowId id[kRows];
-    Raw xr[kRows], gr[kRows];
-    int pos[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      RowId& r = id[i];
-      const int s = slot0 + (warp * kRows + i) * RPW + lane / LPR, t = s / p.H;
-      const int64_t tok = t + static_cast<int64_t>(k) * p.par;
-      r.h = s - t * p.H;
-      r.side = r.h >= p.Hq ? 1 : 0;
-      if (r.side) r.h -= p.Hq;
-      r.real = t < p.par && tok < p.tokens;
-      split_token(tok, p.N, p.batches, r.b, r.n);
-      xr[i] = gr[i] = Raw{};
-      pos[i] = -1;
-      if (!r.real) continue;
-      const RowsView &sx = p.in[r.side], &sg = p.dout[r.side];
-      if (at.in) {
-        if (p.v.norm) xr[i] = load_raw<ADJ>(sx.p + row_at(sx, r.b, r.n, r.h), at);
-        gr[i] = load_raw<ADJ>(sg.p + row_at(sg, r.b, r.n, r.h), at);
-      }
-      pos[i] = position_of(p.v, r.b, r.n);
+    for (int i = 0; i < R; ++i) {
+      const int side = q0 + i >= p.passes_q, h = (q0 + i - (side ? p.passes_q : 0)) * RPW + g;
+      raw[i] = no_raw<P>();
+      if (q0 + i < q1 && at.in && h < p.H[side])
+        raw[i] = load_raw<P>(token_rows(p.in[side], b, n) + h * p.in[side].st[2], at);
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const RowId& r = id[i];
-      const int q = r.real ? checked_position(p.v, pos[i], p.err) : -1;
-      if (q < 0) gr[i] = xr[i] = Raw{};  // left out: no gradient (not even from values that are not finite)
-      const Turn t = load_turn(p.v, max(q, 0), l, at);
-      Pairs g = widen<ADJ>(gr[i]);
-      turn<true>(g, t, at);
-      if (p.v.norm) {
-        const Pairs w = load_weight<ADJ>(p.v, r.side, r.h, at);
-        Pairs x = widen<ADJ>(xr[i]);
-        float scale;
-        const float rs = row_rsqrt<LPR>(p.v, x, scale);
-        float dot = 0.f;
+    for (int i = 0; i < R; ++i) {
+      if (q0 + i >= q1) break;
+      const int side = q0 + i >= p.passes_q, h = (q0 + i - (side ? p.passes_q : 0)) * RPW + g;
+      const bool real = at.in && h < p.H[side];
+      if (side != have || p.v.w[side].head != 0) {
+        wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
+        have = side;
+      }
+      Pairs<P> x = widen<P, ADJ>(raw[i]);
+      norm_and_turn<LPR>(p.v, x, wt, t, at);
+      if (real) store_raw<P>(token_rows(p.out[side], b, n) + h * p.out[side].st[2], at, narrow<P, ADJ>(x));
+    }
+  }
+}
+
+// How the backward deals out its work: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each
+// with ctas[s] CTAs.
+struct BwdPlan {
+  int per, chunks[2], ctas[2], grid;
+  int rows;  // weight rows of a CTA's part
+  size_t bytes;
+};
+
+struct BwdView {
+  NormRopeView v;
+  TokenLine line;
+  int H[2], passes[2];
+  BwdPlan plan;
+  RowsView in[2], dout[2], din[2];
+  float* part;  // [cta][plan.rows][d]; nullptr: no weight's gradient
+  int* err;
+};
+
+template <int P>
+__device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const Lane& at, bool adj) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x.a[e] *= rs;
-          x.b[e] *= rs;
-          acc[i].a[e] += g.a[e] * x.a[e];
-          acc[i].b[e] += g.b[e] * x.b[e];
-          g.a[e] *= w.a[e];
-          g.b[e] *= w.b[e];
-          dot += g.a[e] * x.a[e] + g.b[e] * x.b[e];
-        }
-        // with xn = x r:  dx = r (g w - xn mean(g w xn))
-        dot = row_sum<LPR>(dot) * p.v.inv_d;
-        const float f = rs * scale;
+  for (int i = 0; i < P / 2; ++i) {
+    float a0, a1, b0, b1;
+    f2split(x.a[i], a0, a1);
+    f2split(x.b[i], b0, b1);
+    s[adj ? at.ca + 4 * i : at.ca + 2 * i] = a0;
+    s[adj ? at.ca + 4 * i + 2 : at.ca + 2 * i + 1] = a1;
+    s[adj ? at.ca + 4 * i + 1 : at.cb + 2 * i] = b0;
+    s[adj ? at.ca + 4 * i + 3 : at.cb + 2 * i + 1] = b1;
+  }
+}
+
+// HEADS: every head has a weight of its own.
+template <int P, int LPR, bool ADJ, bool HEADS>
+__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ BwdView p) {
+  constexpr int RPW = 32 / LPR, R = HEADS ? 1 : 16 / P, COLS = 2 * P * LPR;
+  __shared__ float sums[kWarps][RPW][COLS];
+  const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR, warp = threadIdx.x >> 5;
+  int cta = blockIdx.x;
+  const int side = cta >= p.plan.chunks[0] * p.plan.ctas[0];
+  if (side) cta -= p.plan.chunks[0] * p.plan.ctas[0];
+  const int chunk = cta / p.plan.ctas[side];
+  const int q_first = chunk * p.plan.per, q_last = min(q_first + p.plan.per, p.passes[side]), H = p.H[side];
+  const Lane at = lane_of<P, ADJ>(p.v, l);
+  const RowsView in = p.in[side], dout = p.dout[side], din = p.din[side];
+  const int64_t step = static_cast<int64_t>(p.plan.ctas[side]) * kWarps;
+  Pairs<P> acc;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          g.a[e] = f * (g.a[e] - x.a[e] * dot);
-          g.b[e] = f * (g.b[e] - x.b[e] * dot);
+  for (int e = 0; e < P / 2; ++e) acc.a[e] = acc.b[e] = 0;
+  const Pairs<P> wt = load_weight<P, ADJ>(p.v, side, HEADS ? min(q_first * RPW + g, H - 1) : 0, at);
+  for (int64_t tok = (cta - chunk * p.plan.ctas[side]) * kWarps + warp; tok < p.line.tokens; tok += step) {
+    int b, n;
+    split_token(p.line, tok, b, n);
+    const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
+    const Turn<P> t = load_turn<P>(p.v, max(pos, 0), l, at);
+    const uint16_t *x_at = token_rows(in, b, n), *g_at = token_rows(dout, b, n);
+    uint16_t* o_at = token_rows(din, b, n);
+    for (int q0 = q_first; q0 < q_last; q0 += R) {
+      Raw<P> xr[R], gr[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int h = (q0 + i) * RPW + g;
+        xr[i] = gr[i] = no_raw<P>();  // a token that is left out has no gradient, whatever it holds
+        if (pos >= 0 && q0 + i < q_last && at.in && h < H) {
+          if (p.v.norm) xr[i] = load_raw<P>(x_at + h * in.st[2], at);
+          gr[i] = load_raw<P>(g_at + h * dout.st[2], at);
         }
       }
-      const RowsView& o = p.din[r.side];
-      if (r.real && at.in) store_raw<ADJ>(o.p + row_at(o, r.b, r.n, r.h), at, q < 0 ? Raw{} : narrow<ADJ>(g));
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (q0 + i >= q_last) break;
+        const int h = (q0 + i) * RPW + g;
+        const bool real = at.in && h < H;
+        Pairs<P> d = widen<P, ADJ>(gr[i]);
+        turn<true>(d, t, at);
+        if (p.v.norm) {
+          Pairs<P> x = widen<P, ADJ>(xr[i]);
+          float by;
+          const float r = row_rsqrt<LPR>(p.v, x, by);
+          scale(x, r);
+#pragma unroll
+          for (int e = 0; e < P / 2; ++e) {
+            acc.a[e] = fma2(d.a[e], x.a[e], acc.a[e]);
+            acc.b[e] = fma2(d.b[e], x.b[e], acc.b[e]);
+          }
+          multiply(d, wt);
+          const float m = -row_sum<LPR>(dot(d, x)) * p.v.inv_d;
+          const uint64_t m2 = f2(m, m);
+#pragma unroll
+          for (int e = 0; e < P / 2; ++e) {
+            d.a[e] = fma2(x.a[e], m2, d.a[e]);
+            d.b[e] = fma2(x.b[e], m2, d.b[e]);
+          }
+          scale(d, r * by);
+        }
+        if (real) store_raw<P>(o_at + h * din.st[2], at, pos < 0 ? no_raw<P>() : narrow<P, ADJ>(d));
+      }
     }
   }
   if (p.part == nullptr) return;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float* s = sums + ((warp * kRows + i) * RPW + lane / LPR) * COLS;
-    if (!at.in) continue;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      s[ADJ ? at.ca + 2 * e : at.ca + e] = acc[i].a[e];
-      s[ADJ ? at.ca + 2 * e + 1 : at.cb + e] = acc[i].b[e];
-    }
-  }
+  if (at.in) put_columns(sums[warp][g], acc, at, ADJ);
   __syncthreads();
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.part_rows * p.v.d;
-  for (int x = threadIdx.x; x < p.part_rows * p.v.d; x += kThreads) {
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.plan.rows * p.v.d;
+  for (int x = threadIdx.x; x < p.plan.rows * p.v.d; x += kThreads) {
     const int row = x / p.v.d, c = x - row * p.v.d;
     float sum = 0.f;
-    if (p.by_head) {  // the slots of one head
-      for (int j = row; j < SLOTS; j += p.H) sum += sums[j * COLS + c];
-    } else {  // those of q (row 0) or k
-      int h = slot0 % p.H;
-      for (int j = 0; j < SLOTS; ++j) {
-        if ((h >= p.Hq) == (row == 1)) sum += sums[j * COLS + c];
-        if (++h == p.H) h = 0;
+    for (int j = 0; j < kWarps; ++j) {
+      if (HEADS) {
+        sum += sums[j][row][c];
+      } else {
+#pragma unroll
+        for (int k = 0; k < RPW; ++k) sum += sums[j][k][c];
       }
     }
     out[x] = sum;
@@ -215,66 +215,63 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
 struct WeightSumView {
   const float* part;
   float* dw[2];
-  int ctas, part_rows, slots, d, H, Hq, by_head;
+  BwdPlan plan;
+  int d, H[2], heads, rpw;
 };
 
-// Adds the CTAs' parts: block (row of the weights, 32 columns) of 32 x 8 threads.
-__global__ void __launch_bounds__(256) weight_sum_kernel(const WeightSumView p) {
-  __shared__ float s[8][32];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.y * 32 + tx, row = blockIdx.x;
-  const int side = p.by_head ? row >= p.Hq : row, h = p.by_head ? row - side * p.Hq : 0;
-  if (p.dw[side] == nullptr) return;
-  float sum = 0.f;
-  if (c < p.d) {
-    for (int b = ty; b < p.ctas; b += 8) {
-      int at = row;
-      if (p.by_head) {  // where this CTA has the head
-        at = row - static_cast<int>(static_cast<int64_t>(b) * p.slots % p.H);
-        if (at < 0) at += p.H;
-        if (at >= p.part_rows) continue;
-      }
-      sum += p.part[(static_cast<int64_t>(b) * p.part_rows + at) * p.d + c];
-    }
+// Adds the CTAs' parts: block (row of the weights, 32 columns) of 32 x 32 threads.
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const __grid_constant__ WeightSumView p) {
+  __shared__ float s[32][33];
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.y * 32 + tx;
+  int side, h = 0;
+  if (p.heads) {
+    side = static_cast<int>(blockIdx.x) >= p.H[0];
+    h = blockIdx.x - (side ? p.H[0] : 0);
+  } else {
+    side = blockIdx.x;
   }
+  float* dw = side ? p.dw[1] : p.dw[0];
+  if (dw == nullptr) return;
+  const int heads = p.plan.per * p.rpw, chunk = p.heads ? h / heads : 0, row = p.heads ? h - chunk * heads : 0;
+  const int ctas = p.plan.ctas[side];
+  const int first = (side ? p.plan.chunks[0] * p.plan.ctas[0] : 0) + chunk * ctas, count = p.heads ? ctas : p.plan.chunks[side] * ctas;
+  float sum = 0.f;
+  if (c < p.d)
+    for (int j = ty; j < count; j += 32) sum += p.part[(static_cast<int64_t>(first + j) * p.plan.rows + row) * p.d + c];
   s[ty][tx] = sum;
   __syncthreads();
-  if (ty != 0 || c >= p.d) return;
-  for (int j = 1; j < 8; ++j) sum += s[j][tx];
-  p.dw[side][static_cast<int64_t>(h) * p.d + c] = sum;
+  sum = s[tx][ty];  // column ty of the 32
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (tx == 0 && blockIdx.y * 32 + ty < p.d) dw[static_cast<int64_t>(h) * p.d + blockIdx.y * 32 + ty] = sum;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int lanes_of(int d) { return d <= 64 ? 8 : d <= 128 ? 16 : 32; }
+int passes_of(int H, int rows) { return (H + rows - 1) / rows; }
 
-struct BwdPlan {
-  int par, steps, ctas, slots, part_rows;
-  size_t bytes;
-};
+bool by_head(const fdma_norm_rope_args& a) { return a.q_weight_head != 0 || a.k_weight_head != 0; }
 
 BwdPlan bwd_plan(const fdma_norm_rope_args& a) {
   BwdPlan r{};
-  const int64_t tokens = static_cast<int64_t>(a.B) * a.N, H = a.Hq + a.Hk;
-  r.slots = kWarps * (32 / lanes_of(a.d)) * kRows;
-  int64_t par = kBwdCtas * r.slots / H;
-  par = par < 1 ? 1 : par > tokens ? tokens : par;
-  r.steps = static_cast<int>((tokens + par - 1) / par);
-  r.par = static_cast<int>((tokens + r.steps - 1) / r.steps);
-  r.ctas = static_cast<int>((r.par * H + r.slots - 1) / r.slots);
-  const bool by_head = a.q_weight_head != 0 || a.k_weight_head != 0;
-  r.part_rows = !by_head ? 2 : H < r.slots ? static_cast<int>(H) : r.slots;
-  r.bytes = static_cast<size_t>(r.ctas) * r.part_rows * a.d * sizeof(float);
+  const int rot = a.rope != nullptr ? a.rot : 0, rpw = pass_rows(a.d, rot);
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
+  const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
+  r.per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, kBwdCtas * kWarps).per;
+  int64_t cost = 0;  // of a token, the last chunks counted as whole ones
+  for (int s = 0; s < 2; ++s) {
+    r.chunks[s] = (q[s] + r.per - 1) / r.per;
+    cost += static_cast<int64_t>(r.chunks[s]) * (q[s] < r.per ? q[s] : r.per);
+  }
+  const int64_t most_ctas = (tokens + kWarps - 1) / kWarps;
+  for (int s = 0; s < 2; ++s) {
+    const int64_t n = kBwdCtas * static_cast<int64_t>(q[s] < r.per ? q[s] : r.per) / cost;
+    r.ctas[s] = static_cast<int>(n < 1 ? 1 : n > most_ctas ? most_ctas : n);
+    r.grid += r.chunks[s] * r.ctas[s];
+  }
+  r.rows = by_head(a) ? r.per * rpw : 1;
+  r.bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
   return r;
-}
-
-template <typename F>
-void with_lanes(int d, bool adj, F&& f) {
-  using std::integral_constant;
-  using T = integral_constant<bool, true>;
-  using N = integral_constant<bool, false>;
-  if (d <= 64) adj ? f(integral_constant<int, 8>{}, T{}) : f(integral_constant<int, 8>{}, N{});
-  else if (d <= 128) adj ? f(integral_constant<int, 16>{}, T{}) : f(integral_constant<int, 16>{}, N{});
-  else adj ? f(integral_constant<int, 32>{}, T{}) : f(integral_constant<int, 32>{}, N{});
 }
 
 }  // namespace
@@ -378,24 +375,24 @@ int fdma_norm_rope(const fdma_norm_rope_args* a, const fdma_rows* q, const fdma_
   FwdView p{};
   p.v = norm_rope_view(*a);
   if (a->positions == nullptr && a->rope == nullptr) p.v.first = 0;
-  p.H = a->Hq + a->Hk;
-  p.Hq = a->Hq;
-  p.N = a->N;
-  p.tokens = tokens;
+  p.line = {a->N, a->B, tokens};
+  p.H[0] = a->Hq;
+  p.H[1] = a->Hk;
   p.in[0] = rows_view(*q);
   p.out[0] = rows_view(*q_out);
   if (a->Hk > 0) {
     p.in[1] = rows_view(*k);
     p.out[1] = rows_view(*k_out);
   }
-  p.batches = a->B;
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
-  const int per = kWarps * (32 / lanes_of(a->d)) * kRows;
-  const int64_t blocks = (tokens * p.H + per - 1) / per;
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
-  with_lanes(a->d, a->interleaved != 0, [&](auto L, auto A) {
-    norm_rope_kernel<decltype(L)::value, decltype(A)::value>
+  const int rpw = pass_rows(a->d, p.v.rot);
+  p.passes_q = passes_of(a->Hq, rpw);
+  p.plan = plan_passes(p.passes_q + passes_of(a->Hk, rpw), tokens, 152 * 32);
+  const int64_t blocks = (tokens * p.plan.chunks + kWarps - 1) / kWarps;
+  if (blocks * kWarps > 0xffffffffll) return FDMA_ERR_UNSUPPORTED;
+  with_layout(a->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
+    norm_rope_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value>
         <<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   });
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
@@ -435,13 +432,12 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   BwdView p{};
   p.v = norm_rope_view(*a);
   if (a->positions == nullptr && a->rope == nullptr) p.v.first = 0;
-  p.H = a->Hq + a->Hk;
-  p.Hq = a->Hq;
-  p.N = a->N;
-  p.tokens = tokens;
-  p.batches = a->B;
-  p.par = plan.par;
-  p.steps = plan.steps;
+  p.line = {a->N, a->B, tokens};
+  p.plan = plan;
+  const int rpw = pass_rows(a->d, p.v.rot);
+  p.H[0] = a->Hq;
+  p.H[1] = a->Hk;
+  for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], rpw);
   p.dout[0] = rows_view(*dq_out);
   p.din[0] = rows_view(*dq);
   if (a->norm) p.in[0] = rows_view(*q);
@@ -451,12 +447,12 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
     if (a->norm) p.in[1] = rows_view(*k);
   }
   p.part = want ? static_cast<float*>(workspace) : nullptr;
-  p.part_rows = plan.part_rows;
-  p.by_head = a->q_weight_head != 0 || a->k_weight_head != 0;
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
-  with_lanes(a->d, a->interleaved != 0, [&](auto L, auto A) {
-    norm_rope_bwd_kernel<decltype(L)::value, decltype(A)::value><<<plan.ctas, kThreads, 0, cs>>>(p);
+  const bool heads = by_head(*a);
+  with_layout(a->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
+    if (heads) norm_rope_bwd_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value, true><<<plan.grid, kThreads, 0, cs>>>(p);
+    else norm_rope_bwd_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value, false><<<plan.grid, kThreads, 0, cs>>>(p);
   });
   if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
   if (!want) return FDMA_OK;
@@ -464,15 +460,14 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   w.part = p.part;
   w.dw[0] = dq_weight;
   w.dw[1] = dk_weight;
-  w.ctas = plan.ctas;
-  w.part_rows = plan.part_rows;
-  w.slots = plan.slots;
+  w.plan = plan;
   w.d = a->d;
-  w.H = p.H;
-  w.Hq = p.Hq;
-  w.by_head = p.by_head;
-  const dim3 grid(p.by_head ? p.H : 2, (a->d + 31) / 32);
-  weight_sum_kernel<<<grid, 256, 0, cs>>>(w);
+  w.H[0] = a->Hq;
+  w.H[1] = a->Hk;
+  w.heads = heads;
+  w.rpw = rpw;
+  const dim3 grid(heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
+  weight_sum_kernel<<<grid, 1024, 0, cs>>>(w);
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 

@@ -1,12 +1,16 @@
 // The norm of a row (one token's values of one head) and the rotation of its pairs, as the
 // kernels of fdma_norm_rope.cu and the cache write in fdma_cache.cu share them.
 //
-// A row is held by LPR lanes (a power of two), eight values a lane as four pairs (a[i], b[i]):
-//   halves    lane l of the first rot / 8 holds columns 4 l + i and rot / 2 + 4 l + i, so both values
-//             of a pair are in one lane whatever rot is; the lanes behind hold columns 8 l + i and 8 l + 4 + i;
-//   adjacent  lane l holds columns 8 l + 2 i and 8 l + 2 i + 1.
-// Either way lane l turns its pairs by the angles 4 l + i.  Lanes with 8 l >= d hold zeros.
+// A row is held by LPR lanes (a power of two), 2 P values a lane as P pairs (a[i], b[i]):
+//   halves    lane l of the first rot / (2 P) holds columns P l + i and rot / 2 + P l + i, so both values
+//             of a pair are in one lane; the lanes behind hold columns 2 P l + i and 2 P l + P + i;
+//   adjacent  lane l holds columns 2 P l + 2 i and 2 P l + 2 i + 1.
+// Either way lane l turns its pairs by the angles P l + i.  Lanes with 2 P l >= d hold zeros.  P is 8, pieces
+// of 16 bytes, where d and rot are multiples of 16, else 4.  A warp holds 32 / LPR rows at once, all of one
+// tensor: a pass.  Arithmetic is on pairs of fp32 values, one instruction for two.
 #pragma once
+
+#include <type_traits>
 
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
@@ -42,132 +46,195 @@ NormRopeView norm_rope_view(const fdma_norm_rope_args& a);
 int validate_rows(const fdma_rows* r, const int64_t n[3], bool written);
 RowsView rows_view(const fdma_rows& r);
 
+// Pairs of a lane.
+inline int piece_of(int d, int rot) { return d % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+
+// Calls f(P, LPR, ADJ) with the constants that a row of d values with rot turned ones takes.  (LPR is 4 to 16 with
+// pieces of 8, 8 to 32 with pieces of 4.)
+template <typename F>
+void with_layout(int d, int rot, bool adj, F&& f) {
+  auto with = [&](auto P, auto L) {
+    if (adj) f(P, L, std::true_type{});
+    else f(P, L, std::false_type{});
+  };
+  using std::integral_constant;
+  if (piece_of(d, rot) == 8) {
+    if (d <= 64) with(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+    else if (d <= 128) with(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    else with(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+  } else {
+    if (d <= 64) with(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    else if (d <= 128) with(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+    else with(integral_constant<int, 4>{}, integral_constant<int, 32>{});
+  }
+}
+// Rows of a pass.
+inline int pass_rows(int d, int rot) {
+  const int l = d <= 64 ? 4 : d <= 128 ? 8 : 16;
+  return 32 / (piece_of(d, rot) == 8 ? l : 2 * l);
+}
+
 // Where a lane's values lie in a row.
 struct Lane {
-  int ca, cb;   // columns of the two 4-value pieces
-  bool in;      // 8 l < d
+  int ca, cb;   // columns of its two pieces of P values
+  bool in;      // 2 P l < d
   bool turned;  // its pairs are rotated
 };
 
-template <bool ADJ>
+template <int P, bool ADJ>
 __device__ __forceinline__ Lane lane_of(const NormRopeView& v, int l) {
   Lane r;
-  r.in = 8 * l < v.d;
-  r.turned = 8 * l < v.rot;
-  r.ca = !ADJ && r.turned ? 4 * l : 8 * l;
-  r.cb = !ADJ && r.turned ? (v.rot >> 1) + 4 * l : 8 * l + 4;
+  r.in = 2 * P * l < v.d;
+  r.turned = 2 * P * l < v.rot;
+  r.ca = !ADJ && r.turned ? P * l : 2 * P * l;
+  r.cb = !ADJ && r.turned ? (v.rot >> 1) + P * l : 2 * P * l + P;
   return r;
 }
 
+// A lane's values as they are stored: word i holds two neighbouring columns, the first P / 2 those of piece a.
+template <int P>
 struct Raw {
-  uint2 a, b;
+  uint32_t w[P];
 };
 
-template <bool ADJ>
-__device__ __forceinline__ Raw load_raw(const uint16_t* row, const Lane& n) {
-  Raw r;
-  if (ADJ) {
-    const uint4 v = *reinterpret_cast<const uint4*>(row + n.ca);
-    r.a = make_uint2(v.x, v.y);
-    r.b = make_uint2(v.z, v.w);
+template <int P>
+__device__ __forceinline__ Raw<P> no_raw() {
+  Raw<P> r;
+#pragma unroll
+  for (int i = 0; i < P; ++i) r.w[i] = 0u;
+  return r;
+}
+
+template <int P>
+__device__ __forceinline__ Raw<P> load_raw(const uint16_t* row, const Lane& n) {
+  Raw<P> r;
+  if constexpr (P == 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + n.ca), y = *reinterpret_cast<const uint4*>(row + n.cb);
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w, r.w[4] = y.x, r.w[5] = y.y, r.w[6] = y.z, r.w[7] = y.w;
   } else {
-    r.a = *reinterpret_cast<const uint2*>(row + n.ca);
-    r.b = *reinterpret_cast<const uint2*>(row + n.cb);
+    const uint2 x = *reinterpret_cast<const uint2*>(row + n.ca), y = *reinterpret_cast<const uint2*>(row + n.cb);
+    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = y.x, r.w[3] = y.y;
   }
   return r;
 }
-template <bool ADJ>
-__device__ __forceinline__ void store_raw(uint16_t* row, const Lane& n, const Raw& r) {
-  if (ADJ) {
-    *reinterpret_cast<uint4*>(row + n.ca) = make_uint4(r.a.x, r.a.y, r.b.x, r.b.y);
+template <int P>
+__device__ __forceinline__ void store_raw(uint16_t* row, const Lane& n, const Raw<P>& r) {
+  if constexpr (P == 8) {
+    *reinterpret_cast<uint4*>(row + n.ca) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    *reinterpret_cast<uint4*>(row + n.cb) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
   } else {
-    *reinterpret_cast<uint2*>(row + n.ca) = r.a;
-    *reinterpret_cast<uint2*>(row + n.cb) = r.b;
+    *reinterpret_cast<uint2*>(row + n.ca) = make_uint2(r.w[0], r.w[1]);
+    *reinterpret_cast<uint2*>(row + n.cb) = make_uint2(r.w[2], r.w[3]);
   }
 }
 
-// Values in the order of the pairs.
+// Values in the order of the pairs: a[i] holds those of pairs 2 i and 2 i + 1.
+template <int P>
 struct Pairs {
-  float a[4], b[4];
+  uint64_t a[P / 2], b[P / 2];
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-template <bool ADJ>
-__device__ __forceinline__ Pairs widen(const Raw& r) {
-  Pairs x;
-  if (ADJ) {
-    x.a[0] = bf16_lo(r.a.x), x.b[0] = bf16_hi(r.a.x), x.a[1] = bf16_lo(r.a.y), x.b[1] = bf16_hi(r.a.y);
-    x.a[2] = bf16_lo(r.b.x), x.b[2] = bf16_hi(r.b.x), x.a[3] = bf16_lo(r.b.y), x.b[3] = bf16_hi(r.b.y);
-  } else {
-    x.a[0] = bf16_lo(r.a.x), x.a[1] = bf16_hi(r.a.x), x.a[2] = bf16_lo(r.a.y), x.a[3] = bf16_hi(r.a.y);
-    x.b[0] = bf16_lo(r.b.x), x.b[1] = bf16_hi(r.b.x), x.b[2] = bf16_lo(r.b.y), x.b[3] = bf16_hi(r.b.y);
+template <int P, bool ADJ>
+__device__ __forceinline__ Pairs<P> widen(const Raw<P>& r) {
+  Pairs<P> x;
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    if constexpr (ADJ) {
+      x.a[i] = f2(bf16_lo(r.w[2 * i]), bf16_lo(r.w[2 * i + 1]));
+      x.b[i] = f2(bf16_hi(r.w[2 * i]), bf16_hi(r.w[2 * i + 1]));
+    } else {
+      x.a[i] = bf16x2_to_f2(r.w[i]);
+      x.b[i] = bf16x2_to_f2(r.w[P / 2 + i]);
+    }
   }
   return x;
 }
-template <bool ADJ>
-__device__ __forceinline__ Raw narrow(const Pairs& x) {
-  Raw r;
-  if (ADJ) {
-    r.a = make_uint2(pack_bf16x2(x.a[0], x.b[0]), pack_bf16x2(x.a[1], x.b[1]));
-    r.b = make_uint2(pack_bf16x2(x.a[2], x.b[2]), pack_bf16x2(x.a[3], x.b[3]));
-  } else {
-    r.a = make_uint2(pack_bf16x2(x.a[0], x.a[1]), pack_bf16x2(x.a[2], x.a[3]));
-    r.b = make_uint2(pack_bf16x2(x.b[0], x.b[1]), pack_bf16x2(x.b[2], x.b[3]));
+template <int P, bool ADJ>
+__device__ __forceinline__ Raw<P> narrow(const Pairs<P>& x) {
+  Raw<P> r;
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    float a0, a1, b0, b1;
+    f2split(x.a[i], a0, a1);
+    f2split(x.b[i], b0, b1);
+    if constexpr (ADJ) {
+      r.w[2 * i] = pack_bf16x2(a0, b0);
+      r.w[2 * i + 1] = pack_bf16x2(a1, b1);
+    } else {
+      r.w[i] = pack_bf16x2(a0, a1);
+      r.w[P / 2 + i] = pack_bf16x2(b0, b1);
+    }
   }
   return r;
 }
 
 // The weight of a head in the order of the pairs (ones without a weight).
-template <bool ADJ>
-__device__ __forceinline__ Pairs load_weight(const NormRopeView& v, int side, int head, const Lane& n) {
-  Pairs w;
+template <int P, bool ADJ>
+__device__ __forceinline__ Pairs<P> load_weight(const NormRopeView& v, int side, int head, const Lane& n) {
+  Pairs<P> w;
   const WeightView& f = v.w[side];
   if (f.p == nullptr || !n.in) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w.a[i] = w.b[i] = 1.f;
+    for (int i = 0; i < P / 2; ++i) w.a[i] = w.b[i] = f2(1.f, 1.f);
     return w;
   }
   const int64_t at = head * f.head;
-  if (v.weight_bf16) return widen<ADJ>(load_raw<ADJ>(static_cast<const uint16_t*>(f.p) + at, n));
+  if (v.weight_bf16) return widen<P, ADJ>(load_raw<P>(static_cast<const uint16_t*>(f.p) + at, n));
   const float* p = static_cast<const float*>(f.p) + at;
-  const float4 x = *reinterpret_cast<const float4*>(p + n.ca), y = *reinterpret_cast<const float4*>(p + n.cb);
-  if (ADJ) {
-    w.a[0] = x.x, w.b[0] = x.y, w.a[1] = x.z, w.b[1] = x.w;
-    w.a[2] = y.x, w.b[2] = y.y, w.a[3] = y.z, w.b[3] = y.w;
-  } else {
-    w.a[0] = x.x, w.a[1] = x.y, w.a[2] = x.z, w.a[3] = x.w;
-    w.b[0] = y.x, w.b[1] = y.y, w.b[2] = y.z, w.b[3] = y.w;
+  float x[2 * P];
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    const float4 y = *reinterpret_cast<const float4*>(p + n.ca + i), z = *reinterpret_cast<const float4*>(p + n.cb + i);
+    x[i] = y.x, x[i + 1] = y.y, x[i + 2] = y.z, x[i + 3] = y.w;
+    x[P + i] = z.x, x[P + i + 1] = z.y, x[P + i + 2] = z.z, x[P + i + 3] = z.w;
+  }
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    w.a[i] = ADJ ? f2(x[4 * i], x[4 * i + 2]) : f2(x[2 * i], x[2 * i + 1]);
+    w.b[i] = ADJ ? f2(x[4 * i + 1], x[4 * i + 3]) : f2(x[P + 2 * i], x[P + 2 * i + 1]);
   }
   return w;
 }
 
+// Cosines and sines.
+template <int P>
 struct Turn {
-  float4 c, s;
+  uint64_t c[P / 2], s[P / 2];
 };
-// Cosines and sines of a lane's pairs at a position inside the table.
-__device__ __forceinline__ Turn load_turn(const NormRopeView& v, int pos, int l, const Lane& n) {
-  Turn t{};
-  if (n.turned) {
-    const float* p = v.rope + static_cast<int64_t>(pos) * v.rot + 4 * l;
-    t.c = __ldg(reinterpret_cast<const float4*>(p));
-    t.s = __ldg(reinterpret_cast<const float4*>(p + (v.rot >> 1)));
+// Those of a lane's pairs at a position inside the table.
+template <int P>
+__device__ __forceinline__ Turn<P> load_turn(const NormRopeView& v, int pos, int l, const Lane& n) {
+  Turn<P> t;
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) t.c[i] = t.s[i] = 0;
+  if (!n.turned) return t;
+  const float* p = v.rope + static_cast<int64_t>(pos) * v.rot + P * l;
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    const float4 c = __ldg(reinterpret_cast<const float4*>(p + i)), s = __ldg(reinterpret_cast<const float4*>(p + (v.rot >> 1) + i));
+    t.c[i / 2] = f2(c.x, c.y);
+    t.c[i / 2 + 1] = f2(c.z, c.w);
+    t.s[i / 2] = f2(s.x, s.y);
+    t.s[i / 2 + 1] = f2(s.z, s.w);
   }
   return t;
 }
 
+__device__ __forceinline__ uint64_t neg2(uint64_t x) { return x ^ 0x8000000080000000ull; }
+
 // Turns a lane's pairs (BACK: the other way).  Lanes that are not turned keep their values: a product with
 // a sine of 0 would carry an infinity of one column into another.
-template <bool BACK>
-__device__ __forceinline__ void turn(Pairs& x, const Turn& t, const Lane& n) {
+template <bool BACK, int P>
+__device__ __forceinline__ void turn(Pairs<P>& x, const Turn<P>& t, const Lane& n) {
   if (!n.turned) return;
-  const float c[4] = {t.c.x, t.c.y, t.c.z, t.c.w}, s[4] = {t.s.x, t.s.y, t.s.z, t.s.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = x.a[i], b = x.b[i], z = BACK ? -s[i] : s[i];
-    x.a[i] = a * c[i] - b * z;
-    x.b[i] = b * c[i] + a * z;
+  for (int i = 0; i < P / 2; ++i) {
+    const uint64_t a = x.a[i], b = x.b[i], s = t.s[i], m = neg2(s);
+    x.a[i] = fma2(b, BACK ? s : m, mul2(a, t.c[i]));
+    x.b[i] = fma2(a, BACK ? m : s, mul2(b, t.c[i]));
   }
 }
 
@@ -178,47 +245,64 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-__device__ __forceinline__ float square_sum(const Pairs& x) {
-  float s = 0.f;
+// The sum of a lane's products.
+template <int P>
+__device__ __forceinline__ float dot(const Pairs<P>& x, const Pairs<P>& y) {
+  uint64_t s = mul2(x.a[0], y.a[0]), u = mul2(x.b[0], y.b[0]);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) s += x.a[i] * x.a[i] + x.b[i] * x.b[i];
-  return s;
+  for (int i = 1; i < P / 2; ++i) {
+    s = fma2(x.a[i], y.a[i], s);
+    u = fma2(x.b[i], y.b[i], u);
+  }
+  float lo, hi;
+  f2split(add2(s, u), lo, hi);
+  return lo + hi;
+}
+
+template <int P>
+__device__ __forceinline__ void scale(Pairs<P>& x, float f) {
+  const uint64_t g = f2(f, f);
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    x.a[i] = mul2(x.a[i], g);
+    x.b[i] = mul2(x.b[i], g);
+  }
+}
+template <int P>
+__device__ __forceinline__ void multiply(Pairs<P>& x, const Pairs<P>& w) {
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    x.a[i] = mul2(x.a[i], w.a[i]);
+    x.b[i] = mul2(x.b[i], w.b[i]);
+  }
 }
 
 // 1 / sqrt(mean(x^2) + eps) of the row.  Values above 2^64 have squares that fp32 does not hold: such a row is
-// multiplied by 2^-70 first (its squares then sum to less than 2^125), `scale` says so, and what is returned belongs to
+// multiplied by 2^-70 first (its squares then sum to less than 2^125), `by` says so, and what is returned belongs to
 // the scaled row.  Every lane of the warp calls it.
-template <int LPR>
-__device__ __forceinline__ float row_rsqrt(const NormRopeView& v, Pairs& x, float& scale) {
+template <int LPR, int P>
+__device__ __forceinline__ float row_rsqrt(const NormRopeView& v, Pairs<P>& x, float& by) {
   constexpr float kDown = 0x1p-70f;
-  float s = row_sum<LPR>(square_sum(x));
-  scale = 1.f;
+  float s = row_sum<LPR>(dot(x, x));
+  by = 1.f;
   const bool over = s == __int_as_float(0x7f800000);
   if (__any_sync(0xffffffffu, over)) {
     if (over) {
-      scale = kDown;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x.a[i] *= kDown;
-        x.b[i] *= kDown;
-      }
+      by = kDown;
+      scale(x, kDown);
     }
-    s = row_sum<LPR>(square_sum(x));
+    s = row_sum<LPR>(dot(x, x));
   }
-  return rsqrtf(s * v.inv_d + v.eps * scale * scale);
+  return rsqrtf(s * v.inv_d + v.eps * by * by);
 }
 
 // The forward of a row: x becomes what is stored.  Every lane of the warp calls it.
-template <int LPR>
-__device__ __forceinline__ void norm_and_turn(const NormRopeView& v, Pairs& x, const Pairs& w, const Turn& t, const Lane& n) {
+template <int LPR, int P>
+__device__ __forceinline__ void norm_and_turn(const NormRopeView& v, Pairs<P>& x, const Pairs<P>& w, const Turn<P>& t, const Lane& n) {
   if (v.norm) {
-    float scale;
-    const float r = row_rsqrt<LPR>(v, x, scale);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x.a[i] = x.a[i] * r * w.a[i];
-      x.b[i] = x.b[i] * r * w.b[i];
-    }
+    float by;
+    scale(x, row_rsqrt<LPR>(v, x, by));
+    multiply(x, w);
   }
   turn<false>(x, t, n);
 }
@@ -230,6 +314,20 @@ __device__ __forceinline__ int checked_position(const NormRopeView& v, int pos, 
     return -1;
   }
   return max(pos, -1);
+}
+
+// The line of a token's passes, cut into `chunks` runs of `per` for as many warps.
+struct PassPlan {
+  int passes, per, chunks;
+};
+// Whole tokens a warp where that leaves `warps` of them, else shorter runs: a warp's lookups (position, angles,
+// weights) are then paid for by fewer rows.
+inline PassPlan plan_passes(int passes, int64_t tokens, int64_t warps) {
+  PassPlan r{passes, 1, 1};
+  const int64_t per = passes * tokens / warps;
+  r.per = per < 1 ? 1 : per > passes ? passes : static_cast<int>(per);
+  r.chunks = (passes + r.per - 1) / r.per;
+  return r;
 }
 
 }  // namespace fdma

@@ -277,7 +277,7 @@ RelView view(const fdma_rel_args& a, int64_t batches, int most) {
   }
   return r;
 }
-constexpr int kFwdWalk = 16, kBwdWalk = 64;
+constexpr int kFwdWalk = 4, kBwdWalk = 32;
 
 int64_t units_of(const RelView& r, int64_t batches) { return batches * r.H * r.nrc * r.ncc; }
 
