@@ -398,8 +398,9 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const Lane& n, const u
 
 // A warp takes a token, or a run of its passes where there are few tokens: queries, keys, values, in this order.
 template <bool FP8, int P, int LPR, bool ADJ>
-__global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
-  constexpr int RPW = 32 / LPR, R = 16 / P;
+__global__ void __launch_bounds__(kCacheThreads, 6) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
+  constexpr int RPW = 32 / LPR, SLOTS = 48 / P;
+  __shared__ __align__(16) uint8_t rings[kCacheThreads / 32][SLOTS * Ring<P>::kSlot];
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
   const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
   uint32_t tok = w, c = 0;
@@ -408,58 +409,61 @@ __global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const _
     c = w - tok * p.plan.chunks;
   }
   if (tok >= static_cast<uint32_t>(p.m.T)) return;  // (never a block's first warp)
-  check_offsets(p.m);
   const Lane at = lane_of<P, ADJ>(p.v, l);
+  const Ring<P> ring(smem_u32(rings[threadIdx.x >> 5]), lane);
   auto side_of = [&](int q) { return q < p.end[0] ? 0 : q < p.end[1] ? 1 : 2; };
   auto head_of = [&](int q, int side) { return (q - (side > 0 ? p.end[side - 1] : 0)) * RPW + g; };
-  const int q1 = min(static_cast<int>(c + 1) * p.plan.per, p.plan.passes);
-  int q0 = static_cast<int>(c) * p.plan.per;
-  Raw<P> raw[R];
-  // the rows themselves do not depend on the slot: load them while it is looked up
-  auto load = [&] {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int side = side_of(q0 + i), h = head_of(q0 + i, side);
-      raw[i] = no_raw<P>();
-      if (q0 + i < q1 && at.in && h < p.H[side])
-        raw[i] = load_raw<P>(p.in[side].p + tok * p.in[side].st[1] + h * p.in[side].st[2], at);
+  const int q0 = static_cast<int>(c) * p.plan.per, q1 = min(q0 + p.plan.per, p.plan.passes);
+  auto start = [&](int q, int slot) {
+    if (q < q1) {
+      const int side = side_of(q), h = head_of(q, side);
+      const bool real = at.in && h < p.H[side];
+      ring.copy(slot, p.in[side].p + tok * p.in[side].st[1] + (real ? h * p.in[side].st[2] : 0), at, real);
     }
+    cp_async_commit();
   };
-  load();
+  // the rows themselves do not depend on the slot: they are fetched while it is looked up
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) start(q0 + i, i);
+  check_offsets(p.m);
+  Slot s;
+  int pos = -1;  // that the rotation goes by; negative: the token is left out
   const int b = find_seq(p.m.cu, p.m.c.B, static_cast<int>(tok), lane);
-  if (b < 0) return;  // behind the last sequence
-  const int kl = p.m.c.k_len[b], slot_pos = kl < 0 ? -1 : kl - (p.m.cu[b + 1] - static_cast<int>(tok));
-  if (slot_pos < 0 || kl > p.m.c.max_pages << p.m.c.page_shift) {
-    atomicCAS(p.m.err, 0, FDMA_ERR_INVALID);
+  if (b >= 0) {  // (else behind the last sequence)
+    const int kl = p.m.c.k_len[b], slot_pos = kl < 0 ? -1 : kl - (p.m.cu[b + 1] - static_cast<int>(tok));
+    if (slot_pos < 0 || kl > p.m.c.max_pages << p.m.c.page_shift) {
+      atomicCAS(p.m.err, 0, FDMA_ERR_INVALID);
+    } else {
+      pos = checked_position(p.v, p.v.pos != nullptr ? p.v.pos[tok * p.v.pos_st[1]] : slot_pos, p.m.err);
+      const int pg = pos < 0 ? -1 : page_at(p.m, b, slot_pos);
+      if (pg < 0) pos = -1;
+      else set_slot<FP8>(p.m, s, pg, slot_pos);
+    }
+  }
+  if (pos < 0) {
+    cp_async_wait_all();
     return;
   }
-  const int pos = checked_position(p.v, p.v.pos != nullptr ? p.v.pos[tok * p.v.pos_st[1]] : slot_pos, p.m.err);
-  if (pos < 0) return;
-  const int pg = page_at(p.m, b, slot_pos);
-  if (pg < 0) return;
-  Slot s;
-  set_slot<FP8>(p.m, s, pg, slot_pos);
   const Turn<P> t = load_turn<P>(p.v, pos, l, at);
   Pairs<P> wt;
   int have = -1;  // the tensor whose weight wt holds
-  for (;;) {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (q0 + i >= q1) break;
-      const int side = side_of(q0 + i), h = head_of(q0 + i, side);
-      const bool real = at.in && h < p.H[side];
-      Pairs<P> x = widen<P, ADJ>(raw[i]);
-      if (side < 2) {
-        if (side != have || p.v.w[side].head != 0) {
-          wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
-          have = side;
-        }
-        norm_and_turn<LPR>(p.v, x, wt, t, at);
+  int ready = 0;  // its slot
+  for (int q = q0; q < q1; ++q) {
+    const int side = side_of(q), h = head_of(q, side);
+    const bool real = at.in && h < p.H[side];
+    cp_async_wait<SLOTS - 1>();
+    const Raw<P> raw = ring.get(ready);
+    Pairs<P> x = widen<P, ADJ>(raw);
+    if (side < 2) {
+      if (side != have || p.v.w[side].head != 0) {
+        wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
+        have = side;
       }
-      if (side == 0) {
-        if (real) store_raw<P>(p.q_out.p + tok * p.q_out.st[1] + h * p.q_out.st[2], at, narrow<P, ADJ>(x));
-        continue;
-      }
+      norm_and_turn<LPR>(p.v, x, wt, t, at);
+    }
+    if (side == 0) {
+      if (real) store_raw<P>(p.q_out.p + tok * p.q_out.st[1] + h * p.q_out.st[2], at, narrow<P, ADJ>(x));
+    } else {
       const bool is_v = side == 2;
       uint8_t* dst = const_cast<uint8_t*>(is_v ? p.m.c.v : p.m.c.k) + (is_v ? s.v : s.k) + h * (is_v ? p.m.c.vs[2] : p.m.c.ks[2]);
       if constexpr (FP8) {
@@ -470,12 +474,11 @@ __global__ void __launch_bounds__(kCacheThreads) norm_rope_append_kernel(const _
           const_cast<uint8_t*>(is_v ? p.m.c.ve : p.m.c.ke)[(is_v ? s.ve : s.ke) + h * (is_v ? p.m.c.ves[2] : p.m.c.kes[2])] =
               static_cast<uint8_t>(be);
       } else {
-        if (real) store_raw<P>(reinterpret_cast<uint16_t*>(dst), at, is_v ? raw[i] : narrow<P, ADJ>(x));
+        if (real) store_raw<P>(reinterpret_cast<uint16_t*>(dst), at, is_v ? raw : narrow<P, ADJ>(x));
       }
     }
-    q0 += R;
-    if (q0 >= q1) break;
-    load();
+    start(q + SLOTS, ready);
+    ready = ready + 1 == SLOTS ? 0 : ready + 1;
   }
 }
 

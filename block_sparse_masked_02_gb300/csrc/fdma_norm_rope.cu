@@ -49,11 +49,16 @@ struct FwdView {
   int* err;
 };
 
+// Passes of a warp that are on their way at once: 6 KB.
+template <int P>
+constexpr int kFwdSlots = 48 / P;
+
 template <int P, int LPR, bool ADJ>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_constant__ FwdView p) {
-  constexpr int RPW = 32 / LPR, R = 16 / P;  // rows of a pass; passes whose loads run together
-  const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
-  const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ FwdView p) {
+  constexpr int RPW = 32 / LPR, SLOTS = kFwdSlots<P>;
+  __shared__ __align__(16) uint8_t rings[kWarps][SLOTS * Ring<P>::kSlot];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, g = lane / LPR;
+  const uint32_t w = blockIdx.x * kWarps + warp;
   uint32_t tok = w, c = 0;
   if (p.plan.chunks > 1) {
     tok = w / p.plan.chunks;
@@ -62,35 +67,41 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const __grid_consta
   if (tok >= p.line.tokens) return;
   int b, n;
   split_token(p.line, tok, b, n);
-  const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
-  if (pos < 0) return;
   const Lane at = lane_of<P, ADJ>(p.v, l);
+  const Ring<P> ring(smem_u32(rings[warp]), lane);
+  const int q0 = static_cast<int>(c) * p.plan.per, q1 = min(q0 + p.plan.per, p.plan.passes);
+  auto start = [&](int q, int slot) {
+    if (q < q1) {
+      const int side = q >= p.passes_q, h = (q - (side ? p.passes_q : 0)) * RPW + g;
+      const bool real = at.in && h < p.H[side];
+      ring.copy(slot, token_rows(p.in[side], b, n) + (real ? h * p.in[side].st[2] : 0), at, real);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) start(q0 + i, i);
+  const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
+  if (pos < 0) {
+    cp_async_wait_all();
+    return;
+  }
   const Turn<P> t = load_turn<P>(p.v, pos, l, at);
-  const int q1 = min(static_cast<int>(c + 1) * p.plan.per, p.plan.passes);
   Pairs<P> wt;
   int have = -1;  // the tensor whose weight wt holds
-  for (int q0 = static_cast<int>(c) * p.plan.per; q0 < q1; q0 += R) {
-    Raw<P> raw[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int side = q0 + i >= p.passes_q, h = (q0 + i - (side ? p.passes_q : 0)) * RPW + g;
-      raw[i] = no_raw<P>();
-      if (q0 + i < q1 && at.in && h < p.H[side])
-        raw[i] = load_raw<P>(token_rows(p.in[side], b, n) + h * p.in[side].st[2], at);
+  int slot = 0;
+  for (int q = q0; q < q1; ++q) {
+    const int side = q >= p.passes_q, h = (q - (side ? p.passes_q : 0)) * RPW + g;
+    const bool real = at.in && h < p.H[side];
+    if (side != have || p.v.w[side].head != 0) {
+      wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
+      have = side;
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (q0 + i >= q1) break;
-      const int side = q0 + i >= p.passes_q, h = (q0 + i - (side ? p.passes_q : 0)) * RPW + g;
-      const bool real = at.in && h < p.H[side];
-      if (side != have || p.v.w[side].head != 0) {
-        wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
-        have = side;
-      }
-      Pairs<P> x = widen<P, ADJ>(raw[i]);
-      norm_and_turn<LPR>(p.v, x, wt, t, at);
-      if (real) store_raw<P>(token_rows(p.out[side], b, n) + h * p.out[side].st[2], at, narrow<P, ADJ>(x));
-    }
+    cp_async_wait<SLOTS - 1>();
+    Pairs<P> x = widen<P, ADJ>(ring.get(slot));
+    norm_and_turn<LPR>(p.v, x, wt, t, at);
+    if (real) store_raw<P>(token_rows(p.out[side], b, n) + h * p.out[side].st[2], at, narrow<P, ADJ>(x));
+    start(q + SLOTS, slot);
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
   }
 }
 
@@ -126,11 +137,16 @@ __device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const L
   }
 }
 
+// Steps of a warp (a pass of the gradients and of the rows) that are on their way at once: 6 KB.
+template <int P>
+constexpr int kBwdSlots = 24 / P;
+
 // HEADS: every head has a weight of its own.
 template <int P, int LPR, bool ADJ, bool HEADS>
 __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ BwdView p) {
-  constexpr int RPW = 32 / LPR, R = HEADS ? 1 : 16 / P, COLS = 2 * P * LPR;
-  __shared__ float sums[kWarps][RPW][COLS];
+  constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kBwdSlots<P>;
+  __shared__ __align__(16) uint8_t rings[kWarps][2 * SLOTS * Ring<P>::kSlot];
+  static_assert(sizeof(rings) >= kWarps * RPW * COLS * sizeof(float), "the sums take the rings' place");
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR, warp = threadIdx.x >> 5;
   int cta = blockIdx.x;
   const int side = cta >= p.plan.chunks[0] * p.plan.ctas[0];
@@ -140,61 +156,84 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
   const Lane at = lane_of<P, ADJ>(p.v, l);
   const RowsView in = p.in[side], dout = p.dout[side], din = p.din[side];
   const int64_t step = static_cast<int64_t>(p.plan.ctas[side]) * kWarps;
+  const int64_t tok0 = (cta - chunk * p.plan.ctas[side]) * kWarps + warp;
+  const Ring<P> ring(smem_u32(rings[warp]), lane);
+  // what is fetched next
+  int64_t tok_next = tok0;
+  int q_next = q_first;
+  const uint16_t *x_next = nullptr, *g_next = nullptr;
+  auto start = [&](int slot) {
+    if (tok_next < p.line.tokens) {
+      if (q_next == q_first) {
+        int b, n;
+        split_token(p.line, tok_next, b, n);
+        x_next = token_rows(in, b, n);
+        g_next = token_rows(dout, b, n);
+      }
+      const int h = q_next * RPW + g;
+      const bool real = at.in && h < H;
+      if (p.v.norm) ring.copy(2 * slot, x_next + (real ? h * in.st[2] : 0), at, real);
+      ring.copy(2 * slot + 1, g_next + (real ? h * dout.st[2] : 0), at, real);
+      if (++q_next == q_last) {
+        q_next = q_first;
+        tok_next += step;
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < SLOTS; ++i) start(i);
   Pairs<P> acc;
 #pragma unroll
   for (int e = 0; e < P / 2; ++e) acc.a[e] = acc.b[e] = 0;
   const Pairs<P> wt = load_weight<P, ADJ>(p.v, side, HEADS ? min(q_first * RPW + g, H - 1) : 0, at);
-  for (int64_t tok = (cta - chunk * p.plan.ctas[side]) * kWarps + warp; tok < p.line.tokens; tok += step) {
+  int slot = 0;
+  for (int64_t tok = tok0; tok < p.line.tokens; tok += step) {
     int b, n;
     split_token(p.line, tok, b, n);
     const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
     const Turn<P> t = load_turn<P>(p.v, max(pos, 0), l, at);
-    const uint16_t *x_at = token_rows(in, b, n), *g_at = token_rows(dout, b, n);
     uint16_t* o_at = token_rows(din, b, n);
-    for (int q0 = q_first; q0 < q_last; q0 += R) {
-      Raw<P> xr[R], gr[R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        const int h = (q0 + i) * RPW + g;
-        xr[i] = gr[i] = no_raw<P>();  // a token that is left out has no gradient, whatever it holds
-        if (pos >= 0 && q0 + i < q_last && at.in && h < H) {
-          if (p.v.norm) xr[i] = load_raw<P>(x_at + h * in.st[2], at);
-          gr[i] = load_raw<P>(g_at + h * dout.st[2], at);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (q0 + i >= q_last) break;
-        const int h = (q0 + i) * RPW + g;
-        const bool real = at.in && h < H;
-        Pairs<P> d = widen<P, ADJ>(gr[i]);
+    for (int q = q_first; q < q_last; ++q) {
+      const int h = q * RPW + g;
+      const bool real = at.in && h < H;
+      cp_async_wait<SLOTS - 1>();
+      // a token that is left out has no gradient, whatever it holds
+      Pairs<P> d = widen<P, ADJ>(pos >= 0 ? ring.get(2 * slot + 1) : no_raw<P>());
+      if (p.v.norm) {
+        Pairs<P> x = widen<P, ADJ>(pos >= 0 ? ring.get(2 * slot) : no_raw<P>());
+        float by;
+        const float r = row_rsqrt<LPR>(p.v, x, by);
         turn<true>(d, t, at);
-        if (p.v.norm) {
-          Pairs<P> x = widen<P, ADJ>(xr[i]);
-          float by;
-          const float r = row_rsqrt<LPR>(p.v, x, by);
-          scale(x, r);
+        // e = g r:  dw += e x,  dx = e w - x r^2 mean(e w x)   (of a scaled row: times `by`)
+        scale(d, r);
 #pragma unroll
-          for (int e = 0; e < P / 2; ++e) {
-            acc.a[e] = fma2(d.a[e], x.a[e], acc.a[e]);
-            acc.b[e] = fma2(d.b[e], x.b[e], acc.b[e]);
-          }
-          multiply(d, wt);
-          const float m = -row_sum<LPR>(dot(d, x)) * p.v.inv_d;
-          const uint64_t m2 = f2(m, m);
-#pragma unroll
-          for (int e = 0; e < P / 2; ++e) {
-            d.a[e] = fma2(x.a[e], m2, d.a[e]);
-            d.b[e] = fma2(x.b[e], m2, d.b[e]);
-          }
-          scale(d, r * by);
+        for (int e = 0; e < P / 2; ++e) {
+          acc.a[e] = fma2(d.a[e], x.a[e], acc.a[e]);
+          acc.b[e] = fma2(d.b[e], x.b[e], acc.b[e]);
         }
-        if (real) store_raw<P>(o_at + h * din.st[2], at, pos < 0 ? no_raw<P>() : narrow<P, ADJ>(d));
+        multiply(d, wt);
+        const float m = row_sum<LPR>(dot(d, x)) * p.v.inv_d * (-r * r);
+        const uint64_t m2 = f2(m, m);
+#pragma unroll
+        for (int e = 0; e < P / 2; ++e) {
+          d.a[e] = fma2(x.a[e], m2, d.a[e]);
+          d.b[e] = fma2(x.b[e], m2, d.b[e]);
+        }
+        if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
+      } else {
+        turn<true>(d, t, at);
       }
+      if (real) store_raw<P>(o_at + h * din.st[2], at, pos < 0 ? no_raw<P>() : narrow<P, ADJ>(d));
+      start(slot);
+      slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
   }
+  cp_async_wait_all();
   if (p.part == nullptr) return;
-  if (at.in) put_columns(sums[warp][g], acc, at, ADJ);
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(rings);  // [warp][row of a pass][column]
+  if (at.in) put_columns(sums + (warp * RPW + g) * COLS, acc, at, ADJ);
   __syncthreads();
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.plan.rows * p.v.d;
   for (int x = threadIdx.x; x < p.plan.rows * p.v.d; x += kThreads) {
@@ -202,10 +241,10 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
     float sum = 0.f;
     for (int j = 0; j < kWarps; ++j) {
       if (HEADS) {
-        sum += sums[j][row][c];
+        sum += sums[(j * RPW + row) * COLS + c];
       } else {
 #pragma unroll
-        for (int k = 0; k < RPW; ++k) sum += sums[j][k][c];
+        for (int k = 0; k < RPW; ++k) sum += sums[(j * RPW + k) * COLS + c];
       }
     }
     out[x] = sum;

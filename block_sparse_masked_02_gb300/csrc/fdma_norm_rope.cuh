@@ -14,6 +14,7 @@
 
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
+#include "fdma_paged.cuh"
 #include "fdma_ptx.cuh"
 
 namespace fdma {
@@ -127,6 +128,45 @@ __device__ __forceinline__ void store_raw(uint16_t* row, const Lane& n, const Ra
     *reinterpret_cast<uint2*>(row + n.cb) = make_uint2(r.w[2], r.w[3]);
   }
 }
+
+// Rows on their way, in shared memory: a slot holds a lane's two pieces of a pass, where only this lane writes and reads
+// them, so that a warp has many passes in flight without registers for them and without a barrier.
+template <int P>
+struct Ring {
+  static constexpr int kSlot = 128 * P;  // bytes of a warp's slot
+  uint32_t at;                           // this lane's piece a of slot 0
+
+  __device__ __forceinline__ Ring(uint32_t warp_base, int lane) : at(warp_base + lane * 2 * P) {}
+  // Starts a copy; with real false nothing is read and zeros are written.
+  __device__ __forceinline__ void copy(int slot, const uint16_t* row, const Lane& n, bool real) const {
+    const uint32_t to = at + slot * kSlot, bytes = real ? 2 * P : 0;
+    if constexpr (P == 8) {
+      cp_async16(to, row + n.ca, bytes);
+      cp_async16(to + 64 * P, row + n.cb, bytes);
+    } else {
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(row + n.ca), "r"(bytes) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 64 * P), "l"(row + n.cb), "r"(bytes) : "memory");
+    }
+  }
+  __device__ __forceinline__ Raw<P> get(int slot) const {
+    Raw<P> r;
+    const uint32_t from = at + slot * kSlot;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (P == 8)
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r.w[4 * k]), "=r"(r.w[4 * k + 1]), "=r"(r.w[4 * k + 2]), "=r"(r.w[4 * k + 3])
+                     : "r"(from + k * 64 * P)
+                     : "memory");
+      else
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(r.w[2 * k]), "=r"(r.w[2 * k + 1])
+                     : "r"(from + k * 64 * P)
+                     : "memory");
+    }
+    return r;
+  }
+};
 
 // Values in the order of the pairs: a[i] holds those of pairs 2 i and 2 i + 1.
 template <int P>

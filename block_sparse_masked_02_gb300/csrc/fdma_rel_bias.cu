@@ -2,13 +2,16 @@
 // its table (include/fdma_inputs.h).
 //
 // Both use that the bias depends on j - i alone.  The matrix is cut into blocks of 8 rows by 8
-// columns; a block holds 15 diagonals, and the block one further down and to the right holds the
-// same ones.  So a lane that walks down its diagonal of blocks needs 15 values for all of them: the
-// forward looks them up once and then only stores (16 bytes a row), the backward adds every element to one
-// of 15 sums in registers (one add an element, no atomics) and is done with buckets at the end of its walk.
-// The 32 lanes of a warp hold neighbouring blocks, 512 contiguous bytes a row.  A unit of work is
-// such a walk of a warp over `walk` block rows; units begin walk - 1 block columns to the left of
-// the matrix, so that all of it is covered.
+// columns, one a lane: a block holds 15 diagonals, and the 32 neighbouring blocks of a warp 263 (512
+// contiguous bytes a row).  The forward looks up a block's 15 values and stores 16 bytes a row.
+//
+// Backward.  The block one further down and to the right holds the same diagonals, so a lane that walks down
+// its diagonal of blocks adds every element to one of 15 sums in registers: one add an element, no atomics, and buckets
+// only at the end of the walk.  A band is the 32 neighbouring diagonals of blocks that a warp walks along; its block rows
+// are dealt out to `parts` warps in turn (warp p takes p, p + parts, ...), so that all warps sweep
+// over the matrix together and DRAM sees neighbouring rows.  A CTA's warps have eight parts of a band; it
+// joins their sums, adds up the diagonals of each bucket in a fixed order and writes one number for each bucket
+// that the band touches.  A second kernel adds those.
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
 #include "fdma_ptx.cuh"
@@ -19,34 +22,33 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxLen = 131072;  // as fdma_fwd's
 constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
+constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
 
 struct RelView {
   int H, Nq, Nk, off;
-  int n, two_sided;     // buckets of a side
-  int walk, nrc, ncc;   // block rows of a unit; units along the rows and the columns
+  int n, two_sided;  // buckets of a side
   int starts[FDMA_MAX_BUCKETS];
 
   __host__ __device__ int buckets() const { return two_sided ? 2 * n : n; }
-  // The bucket of a distance.
-  __device__ __forceinline__ int side(int a) const {
+  __host__ __device__ int row_blocks() const { return (Nq + 7) >> 3; }
+  // The bucket of a distance, by its side's first distances.
+  __device__ __forceinline__ int side(const int* first, int a) const {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (starts[mid] <= a) lo = mid;
+      if (first[mid] <= a) lo = mid;
       else hi = mid - 1;
     }
     return lo;
   }
+  __device__ __forceinline__ int side(int a) const { return side(starts, a); }
   // ... of a difference key - query.  It falls as delta rises to 0, and rises (from n, two-sided) or stays behind
   // it: where both ends of an interval have the same bucket, all of it has.
-  __device__ __forceinline__ int bucket(int delta) const {
-    if (delta <= 0) return side(-delta);
-    return two_sided ? n + side(delta) : side(0);
+  __device__ __forceinline__ int bucket(const int* first, int delta) const {
+    if (delta <= 0) return side(first, -delta);
+    return two_sided ? n + side(first, delta) : side(first, 0);
   }
-  // The first diagonal of a unit's first lane.
-  __device__ __forceinline__ int first_delta(int rc, int cc) const {
-    return 8 * (32 * cc - (walk - 1)) - 8 * walk * rc - off - 7;
-  }
+  __device__ __forceinline__ int bucket(int delta) const { return bucket(starts, delta); }
 };
 
 // ---- forward
@@ -58,7 +60,7 @@ struct FwdView {
   int64_t ts[2];
   uint16_t* out;
   int64_t os[2];
-  int64_t units;
+  uint32_t ncc, units;  // warps along the columns; of all rows and heads
 };
 
 __device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, int h) {
@@ -67,40 +69,40 @@ __device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, in
   return pack_bf16x2(static_cast<const float*>(p.table)[at], 0.f) & 0xffffu;
 }
 
+// A warp writes 8 rows of 256 columns: with walks of 1, 2, 4, 8 or 16 blocks down the diagonal, which look up their values
+// once for all of them, four heads of 16384 x 16384 took 285, 310, 319, 330 or 353 us.
 __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView p) {
+  __shared__ int first[FDMA_MAX_BUCKETS];  // (lanes look at different ones, which constant memory serves in turn)
   const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= p.units) return;
-  const int64_t hr = unit / p.r.ncc;
-  const int cc = static_cast<int>(unit - hr * p.r.ncc), h = static_cast<int>(hr / p.r.nrc),
-            rc = static_cast<int>(hr - static_cast<int64_t>(h) * p.r.nrc);
-  const int lo = p.r.first_delta(rc, cc);
-  uint32_t w[14];  // neighbouring diagonals in pairs
+  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const uint32_t hr = unit / p.ncc, nrb = p.r.row_blocks();
+  const int cc = static_cast<int>(unit - hr * p.ncc), h = static_cast<int>(hr / nrb), rb = static_cast<int>(hr - h * nrb);
+  const int lo = 256 * cc - 8 * rb - p.r.off - 7;
   const int b0 = p.r.bucket(lo);
-  if (b0 == p.r.bucket(lo + kSpan - 1)) {
+  const bool one = b0 == p.r.bucket(lo + kSpan - 1) || unit >= p.units;
+  if (__syncthreads_or(!one)) {
+    for (int i = threadIdx.x; i < p.r.n; i += kThreads) first[i] = p.r.starts[i];
+    __syncthreads();
+  }
+  if (unit >= p.units) return;
+  uint32_t w[14];  // neighbouring diagonals in pairs
+  if (one) {
     const uint32_t v = table_value(p, b0, h) * 0x10001u;
 #pragma unroll
     for (int i = 0; i < 14; ++i) w[i] = v;
   } else {
-    uint32_t before = 0;
+    uint32_t v[15];
 #pragma unroll
-    for (int i = 0; i < 15; ++i) {
-      const uint32_t v = table_value(p, p.r.bucket(lo + 8 * lane + i), h);
-      if (i > 0) w[i - 1] = before | (v << 16);
-      before = v;
-    }
-  }
-  const int rb0 = rc * p.r.walk, nkb = p.r.Nk >> 3;
-  int cb = 32 * cc - (p.r.walk - 1) + lane;
-  const int rows = min(p.r.Nq - rb0 * 8, p.r.walk * 8);
-  uint16_t* at = p.out + h * p.os[0] + static_cast<int64_t>(rb0) * 8 * p.os[1] + static_cast<int64_t>(cb) * 8;
-  const int64_t row = p.os[1];
-  for (int i = 0; i < rows; i += 8, ++cb, at += 8 * row + 8) {
-    if (cb < 0 || cb >= nkb) continue;
+    for (int i = 0; i < 15; ++i) v[i] = table_value(p, p.r.bucket(first, lo + 8 * lane + i), h);
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      if (i + r < rows) *reinterpret_cast<uint4*>(at + r * row) = make_uint4(w[7 - r], w[9 - r], w[11 - r], w[13 - r]);
+    for (int i = 0; i < 14; ++i) w[i] = v[i] | (v[i + 1] << 16);
   }
+  const int cb = 32 * cc + lane, rows = min(p.r.Nq - 8 * rb, 8);
+  if (cb >= p.r.Nk >> 3) return;
+  uint16_t* at = p.out + h * p.os[0] + static_cast<int64_t>(8 * rb) * p.os[1] + 8 * cb;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < rows) *reinterpret_cast<uint4*>(at + r * p.os[1]) = make_uint4(w[7 - r], w[9 - r], w[11 - r], w[13 - r]);
 }
 
 // ---- backward
@@ -108,20 +110,22 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
 struct BwdView {
   RelView r;
   int B, causal;
+  int bands, parts;  // bands with anything in them; parts is a multiple of 8
   const uint16_t* db;
   int64_t ds[3];
-  float* part;  // [unit][bucket]: the sums of the buckets that the unit has
+  float* part;  // [cta][bucket]: the sums of the buckets that the band has
   float* dtable;
-  int64_t units;
 };
 
-// Of a unit, or a bucket: the diagonals lo .. hi.
+// Of a band, or a bucket: the diagonals lo .. hi.
 struct Deltas {
   int lo, hi;
 };
-__device__ __forceinline__ Deltas unit_deltas(const BwdView& p, int rc, int cc) {
+// Band 0 begins with the block in the matrix's lower left corner.
+__device__ __forceinline__ int first_delta(const RelView& r) { return -8 * (r.row_blocks() - 1) - r.off - 7; }
+__device__ __forceinline__ Deltas band_deltas(const BwdView& p, int band) {
   Deltas d;
-  d.lo = p.r.first_delta(rc, cc);
+  d.lo = first_delta(p.r) + 256 * band;
   d.hi = d.lo + kSpan - 1;
   if (p.causal) d.hi = min(d.hi, 0);
   return d;
@@ -147,30 +151,40 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads) rel_bias_bwd_kernel(const __grid_constant__ BwdView p) {
+__global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView p) {
   __shared__ float diag[kWarps][kSpan + 1];
+  __shared__ float all[kSpan + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
-  if (unit >= p.units) return;
-  const int64_t hr = unit / p.r.ncc, hb = hr / p.r.nrc;
-  const int cc = static_cast<int>(unit - hr * p.r.ncc), rc = static_cast<int>(hr - hb * p.r.nrc);
-  const int h = static_cast<int>(hb / p.B), b = static_cast<int>(hb - static_cast<int64_t>(h) * p.B);
-  const Deltas d = unit_deltas(p, rc, cc);
-  if (d.lo > d.hi) return;
+  // the bands from right to left: a causal matrix's longest ones come first
+  const uint32_t u = blockIdx.x / p.bands, groups = p.parts / kWarps;
+  const int band = p.bands - 1 - static_cast<int>(blockIdx.x - u * p.bands);
+  const uint32_t hb = u / groups;
+  const int part = static_cast<int>(u - hb * groups) * kWarps + warp;
+  const int h = static_cast<int>(hb / p.B), b = static_cast<int>(hb - h * p.B);
+  const Deltas d = band_deltas(p, band);
+  const int nrb = p.r.row_blocks(), ncb = p.r.Nk >> 3, db0 = 32 * band - (nrb - 1), db = db0 + lane;
   float acc[15];
 #pragma unroll
   for (int i = 0; i < 15; ++i) acc[i] = 0.f;
-  const int rb0 = rc * p.r.walk, nkb = p.r.Nk >> 3;
-  int cb = 32 * cc - (p.r.walk - 1) + lane;
-  const int rows = min(p.r.Nq - rb0 * 8, p.r.walk * 8);
   const int64_t row = p.ds[2];
-  const uint16_t* at = p.db + b * p.ds[0] + h * p.ds[1] + static_cast<int64_t>(rb0) * 8 * row + static_cast<int64_t>(cb) * 8;
+  // block rows in which some lane has a block
+  int rb = max(0, -(db0 + 31));
+  const int end = min(nrb, ncb - db0);
+  rb += (part - rb % p.parts + p.parts) % p.parts;
   const bool any = d.lo + 8 * lane <= d.hi;
-  for (int i = 0; i < rows; i += 8, ++cb, at += 8 * row + 8) {
-    if (!any || cb < 0 || cb >= nkb) continue;
+  const uint16_t* at = p.db + b * p.ds[0] + h * p.ds[1] + static_cast<int64_t>(8 * rb) * row + 8 * (db + rb);
+  const int64_t step = static_cast<int64_t>(8 * p.parts) * row + 8 * p.parts;
+  for (; rb < end; rb += p.parts, at += step) {
+    if (!any || db + rb < 0 || db + rb >= ncb) continue;
     uint4 v[8];
+    if (8 * rb + 8 <= p.r.Nq) {
 #pragma unroll
-    for (int r = 0; r < 8; ++r) v[r] = i + r < rows ? __ldg(reinterpret_cast<const uint4*>(at + r * row)) : make_uint4(0u, 0u, 0u, 0u);
+      for (int r = 0; r < 8; ++r) v[r] = __ldg(reinterpret_cast<const uint4*>(at + r * row));
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        v[r] = 8 * rb + r < p.r.Nq ? __ldg(reinterpret_cast<const uint4*>(at + r * row)) : make_uint4(0u, 0u, 0u, 0u);
+    }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
@@ -181,20 +195,6 @@ __global__ void __launch_bounds__(kThreads) rel_bias_bwd_kernel(const __grid_con
       }
     }
   }
-  // (a diagonal behind the causal one is dropped, not multiplied: it may hold anything)
-#pragma unroll
-  for (int i = 0; i < 15; ++i)
-    if (d.lo + 8 * lane + i > d.hi) acc[i] = 0.f;
-  float* part = p.part + unit * p.r.buckets();
-  const int b_lo = p.r.bucket(d.lo);
-  if (b_lo == p.r.bucket(d.hi)) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < 15; ++i) s += acc[i];
-    s = warp_sum(s);
-    if (lane == 0) part[b_lo] = s;
-    return;
-  }
   // diagonal 8 lane + i of the warp: i >= 7 is this lane's, the others are the lane's before, too
   float* x = diag[warp];
   if (lane == 0)
@@ -204,36 +204,55 @@ __global__ void __launch_bounds__(kThreads) rel_bias_bwd_kernel(const __grid_con
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < 7; ++i) x[8 * lane + i] += acc[i];
-  __syncwarp();
+  __syncthreads();
+  for (int i = threadIdx.x; i < kSpan; i += kThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) s += diag[j][i];
+    all[i] = s;
+  }
+  __syncthreads();
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.r.buckets();
+  // the buckets of the band, dealt out over the warps (diagonals behind d.hi belong to none: they may hold anything)
   auto add_bucket = [&](int k) {
     const Deltas q = bucket_deltas(p.r, k);
     const int from = max(q.lo, d.lo) - d.lo, to = min(q.hi, d.hi) - d.lo;
     if (from > to) return;
     float s = 0.f;
-    for (int i = from + lane; i <= to; i += 32) s += x[i];
+    for (int i = from + lane; i <= to; i += 32) s += all[i];
     s = warp_sum(s);
-    if (lane == 0) part[k] = s;
+    if (lane == 0) out[k] = s;
   };
-  if (d.lo <= 0)
-    for (int k = p.r.side(max(-d.hi, 0)); k <= b_lo; ++k) add_bucket(k);
+  if (d.lo <= 0) {
+    const int last = p.r.side(-d.lo);
+    for (int k = p.r.side(max(-d.hi, 0)) + warp; k <= last; k += kWarps) add_bucket(k);
+  } else if (!p.r.two_sided && warp == 0) {
+    add_bucket(p.r.side(0));
+  }
   if (d.hi > 0 && p.r.two_sided) {
     const int last = p.r.side(d.hi);
-    for (int k = p.r.side(max(d.lo, 1)); k <= last; ++k) add_bucket(p.r.n + k);
+    for (int k = p.r.side(max(d.lo, 1)) + warp; k <= last; k += kWarps) add_bucket(p.r.n + k);
   }
 }
 
-// Adds the units' sums of one bucket and head.
+// Adds the CTAs' sums of one bucket and head.
 __global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView p) {
   __shared__ double s[kThreads];
   const int k = blockIdx.x % p.r.buckets(), h = blockIdx.x / p.r.buckets();
   const Deltas q = bucket_deltas(p.r, k);
-  const int64_t per = static_cast<int64_t>(p.B) * p.r.nrc * p.r.ncc;
-  const float* part = p.part + h * per * p.r.buckets() + k;
+  // the bands that have some of it
+  const int64_t base = first_delta(p.r), hi = p.causal ? min(q.hi, 0) : q.hi;
+  const int64_t lo_band = max(int64_t{0}, (max(static_cast<int64_t>(q.lo), base) - base - (kSpan - 1) + 255) / 256);
+  const int64_t hi_band = hi < base ? -1 : min(static_cast<int64_t>(p.bands - 1), (hi - base) / 256);
   double sum = 0.;
-  for (int64_t u = threadIdx.x; u < per; u += kThreads) {
-    const int64_t r = u / p.r.ncc;
-    const Deltas d = unit_deltas(p, static_cast<int>(r % p.r.nrc), static_cast<int>(u - r * p.r.ncc));
-    if (max(d.lo, q.lo) <= min(d.hi, q.hi)) sum += part[u * p.r.buckets()];
+  if (q.lo <= hi && lo_band <= hi_band) {
+    const uint32_t n = static_cast<uint32_t>(hi_band - lo_band + 1);
+    const int64_t first = static_cast<int64_t>(h) * p.B * (p.parts / kWarps), count = n * static_cast<int64_t>(p.B) * (p.parts / kWarps);
+    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
+      const int64_t u = i / n;
+      const int64_t cta = (first + u) * p.bands + (p.bands - 1 - (lo_band + (i - u * n)));
+      sum += p.part[cta * p.r.buckets() + k];
+    }
   }
   s[threadIdx.x] = sum;
   __syncthreads();
@@ -259,8 +278,7 @@ int validate(const fdma_rel_args* a) {
   return FDMA_OK;
 }
 
-// Units of `most` block rows, fewer where that leaves too few warps for the machine.
-RelView view(const fdma_rel_args& a, int64_t batches, int most) {
+RelView view(const fdma_rel_args& a) {
   RelView r{};
   r.H = a.H;
   r.Nq = a.Nq;
@@ -269,17 +287,32 @@ RelView view(const fdma_rel_args& a, int64_t batches, int most) {
   r.n = a.num_starts;
   r.two_sided = a.two_sided;
   for (int i = 0; i < r.n; ++i) r.starts[i] = a.starts[i];
-  const int nqb = (a.Nq + 7) / 8, nkb = a.Nk / 8;
-  for (r.walk = most;; r.walk /= 2) {
-    r.nrc = (nqb + r.walk - 1) / r.walk;
-    r.ncc = (nkb + r.walk - 1 + 31) / 32;
-    if (r.walk == 1 || batches * a.H * r.nrc * r.ncc >= 152 * 16) break;
-  }
   return r;
 }
-constexpr int kFwdWalk = 4, kBwdWalk = 32;
 
-int64_t units_of(const RelView& r, int64_t batches) { return batches * r.H * r.nrc * r.ncc; }
+struct BwdPlan {
+  int bands, parts;
+  int64_t ctas;
+};
+// Bands and parts of a call; what it needs of the workspace does not depend on `causal`.
+BwdPlan bwd_plan(const RelView& r, int64_t B, bool causal) {
+  BwdPlan p;
+  const int nrb = r.row_blocks(), ncb = r.Nk / 8, bands = (nrb + ncb - 1 + 31) / 32;
+  // groups of eight warps that share a band: walks of about kBwdSteps block rows, shorter ones where that is too few
+  // CTAs for the machine
+  const int64_t fill = (kBwdCtas + B * r.H * bands - 1) / (B * r.H * bands), most = (nrb + kWarps - 1) / kWarps;
+  int64_t groups = (nrb + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps);
+  if (groups < fill) groups = fill < most ? fill : most;
+  p.parts = kWarps * static_cast<int>(groups);
+  p.bands = bands;
+  if (causal) {  // those that begin at a key that some query sees
+    const int64_t lo = -8ll * (nrb - 1) - r.off - 7;
+    const int64_t n = lo > 0 ? 0 : -lo / 256 + 1;
+    if (n < bands) p.bands = static_cast<int>(n);
+  }
+  p.ctas = B * r.H * (p.parts / kWarps) * p.bands;
+  return p;
+}
 
 }  // namespace
 }  // namespace fdma
@@ -302,7 +335,7 @@ int fdma_rel_bias(const fdma_rel_args* a, const void* table, int table_type, con
   if (a->H > 1 && a->Nq == 1 && os[0] < a->Nk) return FDMA_ERR_INVALID;
   if (!aligned16(out) || (a->H > 1 && os[0] % 8 != 0) || (a->Nq > 1 && os[1] % 8 != 0)) return FDMA_ERR_UNSUPPORTED;
   FwdView p{};
-  p.r = view(*a, 1, kFwdWalk);
+  p.r = view(*a);
   p.table = table;
   p.table_bf16 = table_type == FDMA_BF16;
   p.out = static_cast<uint16_t*>(out);
@@ -310,17 +343,20 @@ int fdma_rel_bias(const fdma_rel_args* a, const void* table, int table_type, con
     p.ts[i] = ts[i];
     p.os[i] = os[i];
   }
-  p.units = units_of(p.r, 1);
-  const int64_t blocks = (p.units + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  p.ncc = (a->Nk / 8 + 31) / 32;
+  const int64_t units = static_cast<int64_t>(p.ncc) * p.r.row_blocks() * a->H;
+  if (units > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  p.units = static_cast<uint32_t>(units);
+  const int64_t blocks = (units + kWarps - 1) / kWarps;
   rel_bias_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* a, int B) {
   if (validate(a) != FDMA_OK || B <= 0 || B > (1 << 20) || a->Nq == 0 || a->Nk == 0) return 0;
-  const RelView r = view(*a, B, kBwdWalk);
-  return static_cast<size_t>(units_of(r, B)) * r.buckets() * sizeof(float);
+  const RelView r = view(*a);
+  const BwdPlan plan = bwd_plan(r, B, false);
+  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * r.buckets() * sizeof(float);
 }
 
 int fdma_rel_bias_bwd(const fdma_rel_args* a, int B, const void* dbias, const int64_t ds[3], int causal, float* dtable,
@@ -343,21 +379,24 @@ int fdma_rel_bias_bwd(const fdma_rel_args* a, int B, const void* dbias, const in
   }
   if (!aligned16(dbias)) return FDMA_ERR_UNSUPPORTED;
   BwdView p{};
-  p.r = view(*a, B, kBwdWalk);
-  p.units = units_of(p.r, B);
+  p.r = view(*a);
+  const BwdPlan whole = bwd_plan(p.r, B, false), plan = bwd_plan(p.r, B, causal != 0);
+  if (whole.ctas > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < static_cast<size_t>(p.units) * buckets * sizeof(float))
+      workspace_bytes < static_cast<size_t>(whole.ctas) * buckets * sizeof(float))
     return FDMA_ERR_WORKSPACE;
+  p.bands = plan.bands;
+  p.parts = plan.parts;
   p.B = B;
   p.causal = causal;
   p.db = static_cast<const uint16_t*>(dbias);
   for (int i = 0; i < 3; ++i) p.ds[i] = ds[i];
   p.part = static_cast<float*>(workspace);
   p.dtable = dtable;
-  const int64_t blocks = (p.units + kWarps - 1) / kWarps;
-  if (blocks > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
-  rel_bias_bwd_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, cs>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
+  if (plan.ctas > 0) {
+    rel_bias_bwd_kernel<<<static_cast<unsigned>(plan.ctas), kThreads, 0, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
+  }
   rel_bias_join_kernel<<<static_cast<unsigned>(buckets * a->H), kThreads, 0, cs>>>(p);
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
