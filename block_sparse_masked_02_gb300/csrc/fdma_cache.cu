@@ -386,13 +386,13 @@ __device__ __forceinline__ void quantise_pairs(const Pairs<P>& x, uint32_t (&cod
 }
 
 template <int P>
-__device__ __forceinline__ void store_codes(uint8_t* row, const Lane& n, const uint32_t (&c)[P / 2]) {
+__device__ __forceinline__ void store_codes(uint8_t* piece, int apart, const uint32_t (&c)[P / 2]) {
   if constexpr (P == 8) {
-    *reinterpret_cast<uint2*>(row + n.ca) = make_uint2(c[0], c[1]);
-    *reinterpret_cast<uint2*>(row + n.cb) = make_uint2(c[2], c[3]);
+    *reinterpret_cast<uint2*>(piece) = make_uint2(c[0], c[1]);
+    *reinterpret_cast<uint2*>(piece + apart) = make_uint2(c[2], c[3]);
   } else {
-    *reinterpret_cast<uint32_t*>(row + n.ca) = c[0];
-    *reinterpret_cast<uint32_t*>(row + n.cb) = c[1];
+    *reinterpret_cast<uint32_t*>(piece) = c[0];
+    *reinterpret_cast<uint32_t*>(piece + apart) = c[1];
   }
 }
 
@@ -411,20 +411,31 @@ __global__ void __launch_bounds__(kCacheThreads, 6) norm_rope_append_kernel(cons
   if (tok >= static_cast<uint32_t>(p.m.T)) return;  // (never a block's first warp)
   const Lane at = lane_of<P, ADJ>(p.v, l);
   const Ring<P> ring(smem_u32(rings[threadIdx.x >> 5]), lane);
-  auto side_of = [&](int q) { return q < p.end[0] ? 0 : q < p.end[1] ? 1 : 2; };
-  auto head_of = [&](int q, int side) { return (q - (side > 0 ? p.end[side - 1] : 0)) * RPW + g; };
   const int q0 = static_cast<int>(c) * p.plan.per, q1 = min(q0 + p.plan.per, p.plan.passes);
-  auto start = [&](int q, int slot) {
-    if (q < q1) {
-      const int side = side_of(q), h = head_of(q, side);
-      const bool real = at.in && h < p.H[side];
-      ring.copy(slot, p.in[side].p + tok * p.in[side].st[1] + (real ? h * p.in[side].st[2] : 0), at, real);
+  // what is fetched next: pass q_next, whose row of this lane is head h_next of the tensor that ends at pass q_turn
+  int q_next = q0, q_turn = 0, h_next = 0, h_end = 0;
+  int64_t by_next = 0;
+  const uint16_t* from = nullptr;
+  auto start = [&](int slot) {
+    if (q_next < q1) {
+      if (q_next >= q_turn) {
+        const int side = q_next < p.end[0] ? 0 : q_next < p.end[1] ? 1 : 2;
+        q_turn = p.end[side];
+        h_next = (q_next - (side > 0 ? p.end[side - 1] : 0)) * RPW + g;
+        h_end = at.in ? p.H[side] : 0;
+        by_next = RPW * p.in[side].st[2];
+        from = p.in[side].p + tok * p.in[side].st[1] + h_next * p.in[side].st[2] + at.ca;
+      }
+      ring.copy(slot, from, at.apart, h_next < h_end);
+      h_next += RPW;
+      from += by_next;
+      ++q_next;
     }
     cp_async_commit();
   };
   // the rows themselves do not depend on the slot: they are fetched while it is looked up
 #pragma unroll
-  for (int i = 0; i < SLOTS; ++i) start(q0 + i, i);
+  for (int i = 0; i < SLOTS; ++i) start(i);
   check_offsets(p.m);
   Slot s;
   int pos = -1;  // that the rotation goes by; negative: the token is left out
@@ -445,40 +456,41 @@ __global__ void __launch_bounds__(kCacheThreads, 6) norm_rope_append_kernel(cons
     return;
   }
   const Turn<P> t = load_turn<P>(p.v, pos, l, at);
-  Pairs<P> wt;
-  int have = -1;  // the tensor whose weight wt holds
-  int ready = 0;  // its slot
-  for (int q = q0; q < q1; ++q) {
-    const int side = side_of(q), h = head_of(q, side);
-    const bool real = at.in && h < p.H[side];
-    cp_async_wait<SLOTS - 1>();
-    const Raw<P> raw = ring.get(ready);
-    Pairs<P> x = widen<P, ADJ>(raw);
-    if (side < 2) {
-      if (side != have || p.v.w[side].head != 0) {
-        wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
-        have = side;
-      }
-      norm_and_turn<LPR>(p.v, x, wt, t, at);
-    }
-    if (side == 0) {
-      if (real) store_raw<P>(p.q_out.p + tok * p.q_out.st[1] + h * p.q_out.st[2], at, narrow<P, ADJ>(x));
-    } else {
-      const bool is_v = side == 2;
-      uint8_t* dst = const_cast<uint8_t*>(is_v ? p.m.c.v : p.m.c.k) + (is_v ? s.v : s.k) + h * (is_v ? p.m.c.vs[2] : p.m.c.ks[2]);
-      if constexpr (FP8) {
+  int slot = 0;
+#pragma unroll 1
+  for (int side = 0; side < 3; ++side) {
+    const int first = side > 0 ? p.end[side - 1] : 0, qa = max(q0, first), qb = min(q1, p.end[side]);
+    if (qa >= qb) continue;
+    const bool is_q = side == 0, is_v = side == 2, heads = side < 2 && p.v.w[side].head != 0;
+    const int end = at.in ? p.H[side] : 0;
+    int h = (qa - first) * RPW + g;
+    // bytes between the rows of neighbouring heads; where this lane's first row begins
+    const int64_t by = is_q ? 2 * p.q_out.st[2] : is_v ? p.m.c.vs[2] : p.m.c.ks[2];
+    uint8_t* to = is_q ? reinterpret_cast<uint8_t*>(p.q_out.p + tok * p.q_out.st[1])
+                       : const_cast<uint8_t*>(is_v ? p.m.c.v + s.v : p.m.c.k + s.k);
+    to += h * by + at.ca * (FP8 && !is_q ? 1 : 2);
+    Pairs<P> wt;
+    if (!is_v && !heads) wt = load_weight<P, ADJ>(p.v, side, 0, at);
+#pragma unroll 1
+    for (int q = qa; q < qb; ++q, h += RPW, to += RPW * by) {
+      if (heads) wt = load_weight<P, ADJ>(p.v, side, min(h, p.H[side] - 1), at);
+      cp_async_wait<SLOTS - 1>();
+      const Raw<P> raw = ring.get(slot);
+      Pairs<P> x = widen<P, ADJ>(raw);
+      if (!is_v) norm_and_turn<LPR>(p.v, x, wt, t, at);
+      if (!FP8 || is_q) {
+        if (h < end) store_raw<P>(reinterpret_cast<uint16_t*>(to), at.apart, is_v ? raw : narrow<P, ADJ>(x));
+      } else {
         uint32_t code[P / 2], be;
         quantise_pairs<LPR, P, ADJ>(x, code, be);
-        if (real) store_codes<P>(dst, at, code);
-        if (real && l == 0)
+        if (h < end) store_codes<P>(to, at.apart, code);
+        if (h < end && l == 0)
           const_cast<uint8_t*>(is_v ? p.m.c.ve : p.m.c.ke)[(is_v ? s.ve : s.ke) + h * (is_v ? p.m.c.ves[2] : p.m.c.kes[2])] =
               static_cast<uint8_t>(be);
-      } else {
-        if (real) store_raw<P>(reinterpret_cast<uint16_t*>(dst), at, is_v ? raw : narrow<P, ADJ>(x));
       }
+      start(slot);
+      slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
-    start(q + SLOTS, ready);
-    ready = ready + 1 == SLOTS ? 0 : ready + 1;
   }
 }
 

@@ -1,14 +1,16 @@
 // Norms of queries and keys for each head and the rotation of their positions, forward and
 // backward (include/fdma_inputs.h).
 //
-// Forward.  A warp takes a token, or a run of its passes where there are few tokens; position,
-// angles and weights are looked up once for all of its rows, and each row is read once and written once.
+// With x a row, r = 1 / sqrt(mean(x^2) + eps) and g the gradient of the output turned back:
+//   forward   y = turned(x r w)
+//   backward  e = g r,  dx = e w - x r^2 mean(e w x),  dw = sum over tokens (and heads that share it) of e x.
 //
-// Backward.  With g the gradient of the output turned back, r = 1 / sqrt(mean(x^2) + eps), xn = x r:
-//   dx = r (g w - xn mean(g w xn)),  dw = sum over tokens (and heads that share it) of g xn.
-// A CTA keeps a chunk of one tensor's heads (one pass where every head has a weight of its own) and its warps walk
-// over tokens, so that a lane has one weight and sums one gradient, in registers; the CTA adds its warps' sums in a
-// fixed order and writes one part, and a second kernel adds the parts of a weight.
+// One kernel does either.  Bound by memory traffic, it keeps it going: a CTA has a chunk of one tensor's
+// heads (one pass where every head has a weight of its own) and its warps walk over tokens, a pass a step, with
+// the rows of the next steps and the angles of the next tokens on their way into shared memory; a lane's
+// weight lies there too, which leaves registers for three CTAs an SM.  The backward sums a weight's gradient in
+// registers; at the end the CTA adds its warps' sums in a fixed order and writes one part, and a second kernel
+// adds the parts of a weight.
 #include <cmath>
 
 #include "fdma_norm_rope.cuh"
@@ -17,19 +19,25 @@ namespace fdma {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kBwdCtas = 304;
+constexpr int kSmemPerSm = 227 * 1024;
+// CTAs of an SM that registers allow.
+constexpr int ctas_per_sm(int piece, bool back) { return back && piece == 8 ? 2 : 3; }
 
 struct TokenLine {
   int N, batches;  // batches 1: tokens are one line
   int64_t tokens;
 };
 
-__device__ __forceinline__ void split_token(const TokenLine& t, int64_t tok, int& b, int& n) {
-  b = 0;
-  n = static_cast<int>(tok);
-  if (t.batches > 1) {
-    b = static_cast<int>(static_cast<uint32_t>(tok) / static_cast<uint32_t>(t.N));
-    n = static_cast<int>(tok) - b * t.N;
+// A token of a warp's walk.
+struct Token {
+  uint32_t n;
+  int b;
+};
+__device__ __forceinline__ void wrap(const TokenLine& t, Token& k) {
+  if (t.batches > 1 && k.n >= static_cast<uint32_t>(t.N)) {
+    const uint32_t more = k.n / t.N;
+    k.b += more;
+    k.n -= more * t.N;
   }
 }
 
@@ -38,88 +46,22 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
   return v.pos != nullptr ? v.pos[b * v.pos_st[0] + n * v.pos_st[1]] : v.first + n;
 }
 
-__device__ __forceinline__ uint16_t* token_rows(const RowsView& r, int b, int n) { return r.p + b * r.st[0] + n * r.st[1]; }
-
-struct FwdView {
-  NormRopeView v;
-  TokenLine line;
-  int H[2], passes_q;
-  PassPlan plan;
-  RowsView in[2], out[2];
-  int* err;
-};
-
-// Passes of a warp that are on their way at once: 6 KB.
-template <int P>
-constexpr int kFwdSlots = 48 / P;
-
-template <int P, int LPR, bool ADJ>
-__global__ void __launch_bounds__(kThreads, 3) norm_rope_kernel(const __grid_constant__ FwdView p) {
-  constexpr int RPW = 32 / LPR, SLOTS = kFwdSlots<P>;
-  __shared__ __align__(16) uint8_t rings[kWarps][SLOTS * Ring<P>::kSlot];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % LPR, g = lane / LPR;
-  const uint32_t w = blockIdx.x * kWarps + warp;
-  uint32_t tok = w, c = 0;
-  if (p.plan.chunks > 1) {
-    tok = w / p.plan.chunks;
-    c = w - tok * p.plan.chunks;
-  }
-  if (tok >= p.line.tokens) return;
-  int b, n;
-  split_token(p.line, tok, b, n);
-  const Lane at = lane_of<P, ADJ>(p.v, l);
-  const Ring<P> ring(smem_u32(rings[warp]), lane);
-  const int q0 = static_cast<int>(c) * p.plan.per, q1 = min(q0 + p.plan.per, p.plan.passes);
-  auto start = [&](int q, int slot) {
-    if (q < q1) {
-      const int side = q >= p.passes_q, h = (q - (side ? p.passes_q : 0)) * RPW + g;
-      const bool real = at.in && h < p.H[side];
-      ring.copy(slot, token_rows(p.in[side], b, n) + (real ? h * p.in[side].st[2] : 0), at, real);
-    }
-    cp_async_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < SLOTS; ++i) start(q0 + i, i);
-  const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
-  if (pos < 0) {
-    cp_async_wait_all();
-    return;
-  }
-  const Turn<P> t = load_turn<P>(p.v, pos, l, at);
-  Pairs<P> wt;
-  int have = -1;  // the tensor whose weight wt holds
-  int slot = 0;
-  for (int q = q0; q < q1; ++q) {
-    const int side = q >= p.passes_q, h = (q - (side ? p.passes_q : 0)) * RPW + g;
-    const bool real = at.in && h < p.H[side];
-    if (side != have || p.v.w[side].head != 0) {
-      wt = load_weight<P, ADJ>(p.v, side, real ? h : 0, at);
-      have = side;
-    }
-    cp_async_wait<SLOTS - 1>();
-    Pairs<P> x = widen<P, ADJ>(ring.get(slot));
-    norm_and_turn<LPR>(p.v, x, wt, t, at);
-    if (real) store_raw<P>(token_rows(p.out[side], b, n) + h * p.out[side].st[2], at, narrow<P, ADJ>(x));
-    start(q + SLOTS, slot);
-    slot = slot + 1 == SLOTS ? 0 : slot + 1;
-  }
-}
-
-// How the backward deals out its work: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each
-// with ctas[s] CTAs.
-struct BwdPlan {
+// How the work is dealt out: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each with ctas[s]
+// CTAs.
+struct WalkPlan {
   int per, chunks[2], ctas[2], grid;
   int rows;  // weight rows of a CTA's part
-  size_t bytes;
+  size_t part_bytes;
+  int smem, table;  // of a CTA; of a warp's row of angles
 };
 
-struct BwdView {
+struct WalkView {
   NormRopeView v;
   TokenLine line;
   int H[2], passes[2];
-  BwdPlan plan;
-  RowsView in[2], dout[2], din[2];
-  float* part;  // [cta][plan.rows][d]; nullptr: no weight's gradient
+  WalkPlan plan;
+  RowsView x[2], g[2], out[2];  // g: backward
+  float* part;  // backward: [cta][plan.rows][d]; nullptr: no weight's gradient
   int* err;
 };
 
@@ -137,16 +79,18 @@ __device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const L
   }
 }
 
-// Steps of a warp (a pass of the gradients and of the rows) that are on their way at once: 6 KB.
-template <int P>
-constexpr int kBwdSlots = 24 / P;
+// Steps of a warp that are on their way at once: 4 KB of rows, backward 6 KB.  Angles of a token more than steps.
+template <int P, bool BACK>
+constexpr int kSlots = BACK ? 24 / P : 32 / P;
+template <int P, bool BACK>
+constexpr int kRingBytes = kSlots<P, BACK> * (BACK ? 2 : 1) * Ring<P>::kSlot;
 
 // HEADS: every head has a weight of its own.
-template <int P, int LPR, bool ADJ, bool HEADS>
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid_constant__ BwdView p) {
-  constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kBwdSlots<P>;
-  __shared__ __align__(16) uint8_t rings[kWarps][2 * SLOTS * Ring<P>::kSlot];
-  static_assert(sizeof(rings) >= kWarps * RPW * COLS * sizeof(float), "the sums take the rings' place");
+template <int P, int LPR, bool ADJ, bool HEADS, bool BACK>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kernel(const __grid_constant__ WalkView p) {
+  constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kSlots<P, BACK>, STEP = BACK ? 2 : 1, WEIGHT = 256 * P;
+  static_assert(kRingBytes<P, BACK> >= RPW * COLS * sizeof(float) || !BACK, "the sums take the rings' place");
+  extern __shared__ __align__(16) uint8_t smem[];  // weight | rings | angles
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR, warp = threadIdx.x >> 5;
   int cta = blockIdx.x;
   const int side = cta >= p.plan.chunks[0] * p.plan.ctas[0];
@@ -154,107 +98,149 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_bwd_kernel(const __grid
   const int chunk = cta / p.plan.ctas[side];
   const int q_first = chunk * p.plan.per, q_last = min(q_first + p.plan.per, p.passes[side]), H = p.H[side];
   const Lane at = lane_of<P, ADJ>(p.v, l);
-  const RowsView in = p.in[side], dout = p.dout[side], din = p.din[side];
-  const int64_t step = static_cast<int64_t>(p.plan.ctas[side]) * kWarps;
-  const int64_t tok0 = (cta - chunk * p.plan.ctas[side]) * kWarps + warp;
-  const Ring<P> ring(smem_u32(rings[warp]), lane);
+  const RowsView &x = p.x[side], &gr = p.g[side], &out = p.out[side];
+  const uint32_t step = p.plan.ctas[side] * kWarps, tok0 = (cta - chunk * p.plan.ctas[side]) * kWarps + warp;
+  const uint32_t base = smem_u32(smem), weight = base + lane * 16;
+  const Ring<P> ring(base + WEIGHT + warp * kRingBytes<P, BACK>, lane);
+  const uint32_t table = base + WEIGHT + kWarps * kRingBytes<P, BACK> + warp * (SLOTS + 1) * p.plan.table;
+  const int64_t by_x = RPW * x.st[2], by_g = BACK ? RPW * gr.st[2] : 0, by_out = RPW * out.st[2];
+  const int h_first = q_first * RPW + g, h_end = at.in ? H : 0;
+  const int64_t x_first = h_first * x.st[2] + at.ca, g_first = BACK ? h_first * gr.st[2] + at.ca : 0,
+                out_first = h_first * out.st[2] + at.ca;
+
   // what is fetched next
+  Token next{tok0, 0};
+  wrap(p.line, next);
   int64_t tok_next = tok0;
-  int q_next = q_first;
+  int pos_next = tok_next < p.line.tokens ? position_of(p.v, next.b, next.n) : 0;
+  int q_next = q_last, h_next = 0, row_next = 0;
+  uint32_t left_out = 0, begun = 0;  // bit t % 32: token t of the walk is left out; tokens begun
   const uint16_t *x_next = nullptr, *g_next = nullptr;
   auto start = [&](int slot) {
-    if (tok_next < p.line.tokens) {
-      if (q_next == q_first) {
-        int b, n;
-        split_token(p.line, tok_next, b, n);
-        x_next = token_rows(in, b, n);
-        g_next = token_rows(dout, b, n);
+    if (q_next == q_last && tok_next < p.line.tokens) {
+      const int pos = checked_position(p.v, pos_next, p.err);
+      const uint32_t bit = 1u << (begun & 31u);
+      left_out = pos < 0 ? left_out | bit : left_out & ~bit;
+      ++begun;
+      if (pos >= 0) {
+        const float* angles = p.v.rope + static_cast<int64_t>(pos) * p.v.rot;
+        for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(table + row_next * p.plan.table + 4 * i, angles + i, 16);
       }
-      const int h = q_next * RPW + g;
-      const bool real = at.in && h < H;
-      if (p.v.norm) ring.copy(2 * slot, x_next + (real ? h * in.st[2] : 0), at, real);
-      ring.copy(2 * slot + 1, g_next + (real ? h * dout.st[2] : 0), at, real);
-      if (++q_next == q_last) {
-        q_next = q_first;
-        tok_next += step;
-      }
+      row_next = row_next == SLOTS ? 0 : row_next + 1;
+      x_next = x.p + next.b * x.st[0] + next.n * x.st[1] + x_first;
+      if (BACK) g_next = gr.p + next.b * gr.st[0] + next.n * gr.st[1] + g_first;
+      h_next = pos < 0 ? h_end : h_first;
+      q_next = q_first;
+      tok_next += step;
+      next.n += step;
+      wrap(p.line, next);
+      if (tok_next < p.line.tokens) pos_next = position_of(p.v, next.b, next.n);
+    }
+    if (q_next < q_last) {
+      const bool real = h_next < h_end;
+      if (!BACK || p.v.norm) ring.copy(STEP * slot, x_next, at.apart, real);
+      if (BACK) ring.copy(STEP * slot + 1, g_next, at.apart, real);
+      x_next += by_x;
+      if (BACK) g_next += by_g;
+      h_next += RPW;
+      ++q_next;
     }
     cp_async_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < SLOTS; ++i) start(i);
+  if (warp == 0) put_weight<P>(weight, load_weight<P, ADJ>(p.v, side, HEADS ? min(h_first, H - 1) : 0, at));
+  __syncthreads();
+
   Pairs<P> acc;
 #pragma unroll
   for (int e = 0; e < P / 2; ++e) acc.a[e] = acc.b[e] = 0;
-  const Pairs<P> wt = load_weight<P, ADJ>(p.v, side, HEADS ? min(q_first * RPW + g, H - 1) : 0, at);
-  int slot = 0;
+  Token now{tok0, 0};
+  wrap(p.line, now);
+  int slot = 0, row = 0;
+  uint32_t done = 0;
   for (int64_t tok = tok0; tok < p.line.tokens; tok += step) {
-    int b, n;
-    split_token(p.line, tok, b, n);
-    const int pos = checked_position(p.v, position_of(p.v, b, n), p.err);
-    const Turn<P> t = load_turn<P>(p.v, max(pos, 0), l, at);
-    uint16_t* o_at = token_rows(din, b, n);
-    for (int q = q_first; q < q_last; ++q) {
-      const int h = q * RPW + g;
-      const bool real = at.in && h < H;
+    const bool left = (left_out >> (done & 31u)) & 1u;
+    const uint32_t angles = table + row * p.plan.table + 4 * P * l, half = 2 * p.v.rot;
+    uint16_t* to = out.p + now.b * out.st[0] + now.n * out.st[1] + out_first;
+    int h = h_first;
+#pragma unroll 1
+    for (int q = q_first; q < q_last; ++q, h += RPW, to += by_out) {
       cp_async_wait<SLOTS - 1>();
-      // a token that is left out has no gradient, whatever it holds
-      Pairs<P> d = widen<P, ADJ>(pos >= 0 ? ring.get(2 * slot + 1) : no_raw<P>());
-      if (p.v.norm) {
-        Pairs<P> x = widen<P, ADJ>(pos >= 0 ? ring.get(2 * slot) : no_raw<P>());
-        float by;
-        const float r = row_rsqrt<LPR>(p.v, x, by);
-        turn<true>(d, t, at);
-        // e = g r:  dw += e x,  dx = e w - x r^2 mean(e w x)   (of a scaled row: times `by`)
-        scale(d, r);
-#pragma unroll
-        for (int e = 0; e < P / 2; ++e) {
-          acc.a[e] = fma2(d.a[e], x.a[e], acc.a[e]);
-          acc.b[e] = fma2(d.b[e], x.b[e], acc.b[e]);
-        }
-        multiply(d, wt);
-        const float m = row_sum<LPR>(dot(d, x)) * p.v.inv_d * (-r * r);
-        const uint64_t m2 = f2(m, m);
-#pragma unroll
-        for (int e = 0; e < P / 2; ++e) {
-          d.a[e] = fma2(x.a[e], m2, d.a[e]);
-          d.b[e] = fma2(x.b[e], m2, d.b[e]);
-        }
-        if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
+      __syncwarp();  // the angles, which other lanes fetched
+      if (left) {
+        if (BACK && h < h_end) store_raw<P>(to, at.apart, no_raw<P>());
       } else {
-        turn<true>(d, t, at);
+        Pairs<P> d = widen<P, ADJ>(ring.get(STEP * slot + STEP - 1));
+        if constexpr (BACK) {
+          if (p.v.norm) {
+            Pairs<P> xs = widen<P, ADJ>(ring.get(STEP * slot));
+            float by;
+            const float r = row_rsqrt<LPR>(p.v, xs, by);
+            turn_shared<true>(d, angles, half, at);
+            scale(d, r);
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+              acc.a[e] = fma2(d.a[e], xs.a[e], acc.a[e]);
+              acc.b[e] = fma2(d.b[e], xs.b[e], acc.b[e]);
+            }
+            multiply_shared(d, weight);
+            const float m = row_sum<LPR>(dot(d, xs)) * p.v.inv_d * (-r * r);
+            const uint64_t m2 = f2(m, m);
+#pragma unroll
+            for (int e = 0; e < P / 2; ++e) {
+              d.a[e] = fma2(xs.a[e], m2, d.a[e]);
+              d.b[e] = fma2(xs.b[e], m2, d.b[e]);
+            }
+            if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
+          } else {
+            turn_shared<true>(d, angles, half, at);
+          }
+        } else {
+          if (p.v.norm) {
+            float by;
+            scale(d, row_rsqrt<LPR>(p.v, d, by));
+            multiply_shared(d, weight);
+          }
+          turn_shared<false>(d, angles, half, at);
+        }
+        if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
       }
-      if (real) store_raw<P>(o_at + h * din.st[2], at, pos < 0 ? no_raw<P>() : narrow<P, ADJ>(d));
+      __syncwarp();  // (the step that is begun now may take this one's place among the angles)
       start(slot);
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
+    row = row == SLOTS ? 0 : row + 1;
+    ++done;
+    now.n += step;
+    wrap(p.line, now);
   }
   cp_async_wait_all();
-  if (p.part == nullptr) return;
+  if (!BACK || p.part == nullptr) return;
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(rings);  // [warp][row of a pass][column]
+  float* sums = reinterpret_cast<float*>(smem + WEIGHT);  // [warp][row of a pass][column]
   if (at.in) put_columns(sums + (warp * RPW + g) * COLS, acc, at, ADJ);
   __syncthreads();
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.plan.rows * p.v.d;
-  for (int x = threadIdx.x; x < p.plan.rows * p.v.d; x += kThreads) {
-    const int row = x / p.v.d, c = x - row * p.v.d;
+  float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.plan.rows * p.v.d;
+  for (int i = threadIdx.x; i < p.plan.rows * p.v.d; i += kThreads) {
+    const int r = i / p.v.d, c = i - r * p.v.d;
     float sum = 0.f;
     for (int j = 0; j < kWarps; ++j) {
       if (HEADS) {
-        sum += sums[(j * RPW + row) * COLS + c];
+        sum += sums[(j * RPW + r) * COLS + c];
       } else {
 #pragma unroll
         for (int k = 0; k < RPW; ++k) sum += sums[(j * RPW + k) * COLS + c];
       }
     }
-    out[x] = sum;
+    part[i] = sum;
   }
 }
 
 struct WeightSumView {
   const float* part;
   float* dw[2];
-  BwdPlan plan;
+  WalkPlan plan;
   int d, H[2], heads, rpw;
 };
 
@@ -291,26 +277,49 @@ int passes_of(int H, int rows) { return (H + rows - 1) / rows; }
 
 bool by_head(const fdma_norm_rope_args& a) { return a.q_weight_head != 0 || a.k_weight_head != 0; }
 
-BwdPlan bwd_plan(const fdma_norm_rope_args& a) {
-  BwdPlan r{};
-  const int rot = a.rope != nullptr ? a.rot : 0, rpw = pass_rows(a.d, rot);
+WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
+  WalkPlan r{};
+  const int rot = a.rope != nullptr ? a.rot : 0, rpw = pass_rows(a.d, rot), piece = piece_of(a.d, rot);
+  const int slots = back ? 24 / piece : 32 / piece;
+  r.table = 4 * rot;
+  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (slots + 1) * r.table);
+  int per_sm = kSmemPerSm / (r.smem + 1024);
+  if (per_sm > ctas_per_sm(piece, back)) per_sm = ctas_per_sm(piece, back);
+  const int64_t ctas = 152 * per_sm;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
   const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
-  r.per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, kBwdCtas * kWarps).per;
+  r.per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
   int64_t cost = 0;  // of a token, the last chunks counted as whole ones
   for (int s = 0; s < 2; ++s) {
     r.chunks[s] = (q[s] + r.per - 1) / r.per;
     cost += static_cast<int64_t>(r.chunks[s]) * (q[s] < r.per ? q[s] : r.per);
   }
-  const int64_t most_ctas = (tokens + kWarps - 1) / kWarps;
+  const int64_t most = (tokens + kWarps - 1) / kWarps;
   for (int s = 0; s < 2; ++s) {
-    const int64_t n = kBwdCtas * static_cast<int64_t>(q[s] < r.per ? q[s] : r.per) / cost;
-    r.ctas[s] = static_cast<int>(n < 1 ? 1 : n > most_ctas ? most_ctas : n);
+    const int64_t n = ctas * static_cast<int64_t>(q[s] < r.per ? q[s] : r.per) / cost;
+    r.ctas[s] = static_cast<int>(n < 1 ? 1 : n > most ? most : n);
     r.grid += r.chunks[s] * r.ctas[s];
   }
   r.rows = by_head(a) ? r.per * rpw : 1;
-  r.bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
+  r.part_bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
   return r;
+}
+
+template <bool BACK>
+cudaError_t launch_walk(const fdma_norm_rope_args& a, const WalkView& p, cudaStream_t stream) {
+  const bool heads = by_head(a);
+  cudaError_t e = cudaSuccess;
+  with_layout(a.d, p.v.rot, a.interleaved != 0, [&](auto P, auto L, auto A) {
+    constexpr int kP = decltype(P)::value, kL = decltype(L)::value;
+    auto run = [&](auto* kern, std::atomic<uint64_t>& ready) {
+      e = set_up_once(ready, kern, kSmemPerSm / 2, 0);
+      if (e == cudaSuccess) kern<<<p.plan.grid, kThreads, p.plan.smem, stream>>>(p);
+    };
+    static std::atomic<uint64_t> ready[2];
+    if (heads) run(norm_rope_kernel<kP, kL, decltype(A)::value, true, BACK>, ready[1]);
+    else run(norm_rope_kernel<kP, kL, decltype(A)::value, false, BACK>, ready[0]);
+  });
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -387,6 +396,15 @@ int validate_positions(const fdma_norm_rope_args& a) {
   return a.first < 0 || static_cast<int64_t>(a.first) + a.N > a.rope_len ? FDMA_ERR_INVALID : FDMA_OK;
 }
 
+void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
+  p.v = norm_rope_view(a);
+  if (a.positions == nullptr && a.rope == nullptr) p.v.first = 0;
+  p.line = {a.N, a.B, static_cast<int64_t>(a.B) * a.N};
+  p.H[0] = a.Hq;
+  p.H[1] = a.Hk;
+  for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot));
+}
+
 int check_sides(const fdma_norm_rope_args& a, const fdma_rows* q, const fdma_rows* k, bool written) {
   const int64_t nq[3] = {a.B, a.N, a.Hq}, nk[3] = {a.B, a.N, a.Hk};
   const int st = validate_rows(q, nq, written);
@@ -411,35 +429,23 @@ int fdma_norm_rope(const fdma_norm_rope_args* a, const fdma_rows* q, const fdma_
   st = check_sides(*a, q, k, false);
   if (st == FDMA_OK) st = check_sides(*a, q_out, k_out, true);
   if (st != FDMA_OK) return st;
-  FwdView p{};
-  p.v = norm_rope_view(*a);
-  if (a->positions == nullptr && a->rope == nullptr) p.v.first = 0;
-  p.line = {a->N, a->B, tokens};
-  p.H[0] = a->Hq;
-  p.H[1] = a->Hk;
-  p.in[0] = rows_view(*q);
+  WalkView p{};
+  p.plan = walk_plan(*a, false);
+  set_sides(*a, p);
+  p.x[0] = rows_view(*q);
   p.out[0] = rows_view(*q_out);
   if (a->Hk > 0) {
-    p.in[1] = rows_view(*k);
+    p.x[1] = rows_view(*k);
     p.out[1] = rows_view(*k_out);
   }
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
-  const int rpw = pass_rows(a->d, p.v.rot);
-  p.passes_q = passes_of(a->Hq, rpw);
-  p.plan = plan_passes(p.passes_q + passes_of(a->Hk, rpw), tokens, 152 * 32);
-  const int64_t blocks = (tokens * p.plan.chunks + kWarps - 1) / kWarps;
-  if (blocks * kWarps > 0xffffffffll) return FDMA_ERR_UNSUPPORTED;
-  with_layout(a->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
-    norm_rope_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value>
-        <<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  });
-  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  return launch_walk<false>(*a, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 size_t fdma_norm_rope_bwd_workspace_size(const fdma_norm_rope_args* a) {
   if (validate_norm_rope(a) != FDMA_OK || static_cast<int64_t>(a->B) * a->N == 0) return 0;
-  return bwd_plan(*a).bytes;
+  return walk_plan(*a, true).part_bytes;
 }
 
 int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const fdma_rows* k, const fdma_rows* dq_out,
@@ -465,35 +471,23 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   if (st == FDMA_OK) st = check_sides(*a, dq, dk, true);
   if (st != FDMA_OK) return st;
   const bool want = dq_weight != nullptr || dk_weight != nullptr;
-  const BwdPlan plan = bwd_plan(*a);
-  if (want && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.bytes))
+  const WalkPlan plan = walk_plan(*a, true);
+  if (want && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < plan.part_bytes))
     return FDMA_ERR_WORKSPACE;
-  BwdView p{};
-  p.v = norm_rope_view(*a);
-  if (a->positions == nullptr && a->rope == nullptr) p.v.first = 0;
-  p.line = {a->N, a->B, tokens};
+  WalkView p{};
   p.plan = plan;
-  const int rpw = pass_rows(a->d, p.v.rot);
-  p.H[0] = a->Hq;
-  p.H[1] = a->Hk;
-  for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], rpw);
-  p.dout[0] = rows_view(*dq_out);
-  p.din[0] = rows_view(*dq);
-  if (a->norm) p.in[0] = rows_view(*q);
+  set_sides(*a, p);
+  p.g[0] = rows_view(*dq_out);
+  p.out[0] = rows_view(*dq);
+  if (a->norm) p.x[0] = rows_view(*q);
   if (a->Hk > 0) {
-    p.dout[1] = rows_view(*dk_out);
-    p.din[1] = rows_view(*dk);
-    if (a->norm) p.in[1] = rows_view(*k);
+    p.g[1] = rows_view(*dk_out);
+    p.out[1] = rows_view(*dk);
+    if (a->norm) p.x[1] = rows_view(*k);
   }
   p.part = want ? static_cast<float*>(workspace) : nullptr;
   p.err = paged_error_word();
-  if (p.err == nullptr) return FDMA_ERR_CUDA;
-  const bool heads = by_head(*a);
-  with_layout(a->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
-    if (heads) norm_rope_bwd_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value, true><<<plan.grid, kThreads, 0, cs>>>(p);
-    else norm_rope_bwd_kernel<decltype(P)::value, decltype(L)::value, decltype(A)::value, false><<<plan.grid, kThreads, 0, cs>>>(p);
-  });
-  if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
+  if (p.err == nullptr || launch_walk<true>(*a, p, cs) != cudaSuccess) return FDMA_ERR_CUDA;
   if (!want) return FDMA_OK;
   WeightSumView w{};
   w.part = p.part;
@@ -503,9 +497,9 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   w.d = a->d;
   w.H[0] = a->Hq;
   w.H[1] = a->Hk;
-  w.heads = heads;
-  w.rpw = rpw;
-  const dim3 grid(heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
+  w.heads = by_head(*a);
+  w.rpw = pass_rows(a->d, p.v.rot);
+  const dim3 grid(w.heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
   weight_sum_kernel<<<grid, 1024, 0, cs>>>(w);
   return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }

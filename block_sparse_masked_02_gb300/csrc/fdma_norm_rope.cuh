@@ -78,6 +78,7 @@ inline int pass_rows(int d, int rot) {
 // Where a lane's values lie in a row.
 struct Lane {
   int ca, cb;   // columns of its two pieces of P values
+  int apart;    // cb - ca
   bool in;      // 2 P l < d
   bool turned;  // its pairs are rotated
 };
@@ -89,6 +90,7 @@ __device__ __forceinline__ Lane lane_of(const NormRopeView& v, int l) {
   r.turned = 2 * P * l < v.rot;
   r.ca = !ADJ && r.turned ? P * l : 2 * P * l;
   r.cb = !ADJ && r.turned ? (v.rot >> 1) + P * l : 2 * P * l + P;
+  r.apart = r.cb - r.ca;
   return r;
 }
 
@@ -118,14 +120,15 @@ __device__ __forceinline__ Raw<P> load_raw(const uint16_t* row, const Lane& n) {
   }
   return r;
 }
+// (piece: where the first one lies, the second `apart` values behind it)
 template <int P>
-__device__ __forceinline__ void store_raw(uint16_t* row, const Lane& n, const Raw<P>& r) {
+__device__ __forceinline__ void store_raw(uint16_t* piece, int apart, const Raw<P>& r) {
   if constexpr (P == 8) {
-    *reinterpret_cast<uint4*>(row + n.ca) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
-    *reinterpret_cast<uint4*>(row + n.cb) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
+    *reinterpret_cast<uint4*>(piece) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    *reinterpret_cast<uint4*>(piece + apart) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
   } else {
-    *reinterpret_cast<uint2*>(row + n.ca) = make_uint2(r.w[0], r.w[1]);
-    *reinterpret_cast<uint2*>(row + n.cb) = make_uint2(r.w[2], r.w[3]);
+    *reinterpret_cast<uint2*>(piece) = make_uint2(r.w[0], r.w[1]);
+    *reinterpret_cast<uint2*>(piece + apart) = make_uint2(r.w[2], r.w[3]);
   }
 }
 
@@ -137,15 +140,15 @@ struct Ring {
   uint32_t at;                           // this lane's piece a of slot 0
 
   __device__ __forceinline__ Ring(uint32_t warp_base, int lane) : at(warp_base + lane * 2 * P) {}
-  // Starts a copy; with real false nothing is read and zeros are written.
-  __device__ __forceinline__ void copy(int slot, const uint16_t* row, const Lane& n, bool real) const {
+  // Starts a copy of a lane's pieces, `apart` values from each other; with real false nothing is read and zeros are written.
+  __device__ __forceinline__ void copy(int slot, const uint16_t* piece, int apart, bool real) const {
     const uint32_t to = at + slot * kSlot, bytes = real ? 2 * P : 0;
     if constexpr (P == 8) {
-      cp_async16(to, row + n.ca, bytes);
-      cp_async16(to + 64 * P, row + n.cb, bytes);
+      cp_async16(to, piece, bytes);
+      cp_async16(to + 64 * P, piece + apart, bytes);
     } else {
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(row + n.ca), "r"(bytes) : "memory");
-      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 64 * P), "l"(row + n.cb), "r"(bytes) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(piece), "r"(bytes) : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 64 * P), "l"(piece + apart), "r"(bytes) : "memory");
     }
   }
   __device__ __forceinline__ Raw<P> get(int slot) const {
@@ -263,18 +266,39 @@ __device__ __forceinline__ Turn<P> load_turn(const NormRopeView& v, int pos, int
   return t;
 }
 
-__device__ __forceinline__ uint64_t neg2(uint64_t x) { return x ^ 0x8000000080000000ull; }
+// Two pairs of fp32 values from 16 bytes of shared memory.
+__device__ __forceinline__ void shared_pairs(uint32_t at, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at) : "memory");
+}
 
-// Turns a lane's pairs (BACK: the other way).  Lanes that are not turned keep their values: a product with
-// a sine of 0 would carry an infinity of one column into another.
+// Turns a lane's pairs (BACK: the other way) by the angles i, i + 1 of c and s.
+template <bool BACK, int P>
+__device__ __forceinline__ void turn_pair(Pairs<P>& x, int i, uint64_t c, uint64_t s) {
+  const uint64_t a = x.a[i], b = x.b[i];
+  // (negative sines would take registers that are not there)
+  x.a[i] = BACK ? fma2(b, s, mul2(a, c)) : sub2(mul2(a, c), mul2(b, s));
+  x.b[i] = BACK ? sub2(mul2(b, c), mul2(a, s)) : fma2(a, s, mul2(b, c));
+}
+
+// Lanes that are not turned keep their values: a product with a sine of 0 would carry an infinity of one column into
+// another.
 template <bool BACK, int P>
 __device__ __forceinline__ void turn(Pairs<P>& x, const Turn<P>& t, const Lane& n) {
   if (!n.turned) return;
 #pragma unroll
-  for (int i = 0; i < P / 2; ++i) {
-    const uint64_t a = x.a[i], b = x.b[i], s = t.s[i], m = neg2(s);
-    x.a[i] = fma2(b, BACK ? s : m, mul2(a, t.c[i]));
-    x.b[i] = fma2(a, BACK ? m : s, mul2(b, t.c[i]));
+  for (int i = 0; i < P / 2; ++i) turn_pair<BACK>(x, i, t.c[i], t.s[i]);
+}
+// ... from a row of the table in shared memory (at: this lane's cosines, half: the sines' distance).
+template <bool BACK, int P>
+__device__ __forceinline__ void turn_shared(Pairs<P>& x, uint32_t at, uint32_t half, const Lane& n) {
+  if (!n.turned) return;
+#pragma unroll
+  for (int i = 0; i < P / 2; i += 2) {
+    uint64_t c0, c1, s0, s1;
+    shared_pairs(at + 8 * i, c0, c1);
+    shared_pairs(at + half + 8 * i, s0, s1);
+    turn_pair<BACK>(x, i, c0, s0);
+    turn_pair<BACK>(x, i + 1, c1, s1);
   }
 }
 
@@ -314,6 +338,29 @@ __device__ __forceinline__ void multiply(Pairs<P>& x, const Pairs<P>& w) {
   for (int i = 0; i < P / 2; ++i) {
     x.a[i] = mul2(x.a[i], w.a[i]);
     x.b[i] = mul2(x.b[i], w.b[i]);
+  }
+}
+
+// ... with a weight in shared memory, 16 bytes of it for every lane in turn.
+template <int P>
+__device__ __forceinline__ void multiply_shared(Pairs<P>& x, uint32_t at) {
+#pragma unroll
+  for (int i = 0; i < P / 2; i += 2) {
+    uint64_t w0, w1;
+    shared_pairs(at + 256 * i, w0, w1);
+    x.a[i] = mul2(x.a[i], w0);
+    x.a[i + 1] = mul2(x.a[i + 1], w1);
+    shared_pairs(at + 128 * P + 256 * i, w0, w1);
+    x.b[i] = mul2(x.b[i], w0);
+    x.b[i + 1] = mul2(x.b[i + 1], w1);
+  }
+}
+template <int P>
+__device__ __forceinline__ void put_weight(uint32_t at, const Pairs<P>& w) {
+#pragma unroll
+  for (int i = 0; i < P / 2; i += 2) {
+    asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + 256 * i), "l"(w.a[i]), "l"(w.a[i + 1]) : "memory");
+    asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(at + 128 * P + 256 * i), "l"(w.b[i]), "l"(w.b[i + 1]) : "memory");
   }
 }
 

@@ -88,12 +88,18 @@ def load() -> ctypes.CDLL:
     return _LIB
 
 
+_BF16, _FP32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _check_device(first, *ts):
-    dev = first.device
-    if dev.type != "cuda":
+    """The index of the device that all tensors of a call are on."""
+    dev = first.get_device()
+    if dev < 0:
         raise ValueError("libfdma takes CUDA tensors only (no CPU path)")
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors of a call are on one device")
     return dev
 
@@ -101,46 +107,43 @@ def _check_device(first, *ts):
 def _on(dev, stream):
     """(guard that makes the device and the launch stream current, or None; stream pointer): what is
     allocated for the call then belongs to the stream that it runs on."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream), stream.cuda_stream
-    guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    return guard, torch._C._cuda_getCurrentRawStream(dev.index)
+    if stream is None:
+        return (None if _current_device() == dev else torch.cuda.device(dev)), _raw_stream(dev)
+    if stream.device.index != dev:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream), stream.cuda_stream
 
 
-def _run(guard, call):
+def _run(guard, call, *args):
     if guard is None:
-        return call()
+        return call(*args)
     with guard:
-        return call()
+        return call(*args)
 
 
-def _rows(name, t, like=None):
+def _rows(name, t, shape=None):
     """fdma_rows of (B, N, H, d) or packed (T, H, d) rows, as packed bytes."""
     st = t.stride()
-    if t.dtype is not torch.bfloat16 or len(st) not in (3, 4) or (st[-1] != 1 and t.shape[-1] > 1):
+    n = len(st)
+    if t.dtype is not _BF16 or (n != 4 and n != 3) or (st[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be bf16 (B, N, H, d) or (T, H, d) with a contiguous head dim")
-    if like is not None and t.shape != like.shape:
-        raise ValueError(f"{name} must have the shape {tuple(like.shape)}")
-    return _PACK_ROWS(t.data_ptr(), *st[:3]) if len(st) == 4 else _PACK_ROWS(t.data_ptr(), 0, st[0], st[1])
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return _PACK_ROWS(t.data_ptr(), st[0], st[1], st[2]) if n == 4 else _PACK_ROWS(t.data_ptr(), 0, st[0], st[1])
 
 
 def _weight(name, w, H, d):
     """(pointer, head stride, type) of a weight (d) or (H, d)."""
-    if w is None:
-        return 0, 0, None
-    dt = FDMA_FP32 if w.dtype is torch.float32 else FDMA_BF16 if w.dtype is torch.bfloat16 else None
-    shape = w.shape
-    if dt is None or shape not in ((d,), (H, d)) or w.stride(-1) != 1:
+    dt = w.dtype
+    dt = FDMA_FP32 if dt is _FP32 else FDMA_BF16 if dt is _BF16 else None
+    shape, st = w.shape, w.stride()
+    if dt is None or shape[-1:] != (d,) or st[-1] != 1 or (len(shape) != 1 and shape != (H, d)):
         raise ValueError(f"{name} must be fp32 or bf16, ({d},) or ({H}, {d}), with a contiguous last dimension")
-    head = 0
-    if len(shape) == 2:
-        head = w.stride(0)
-        if H > 1 and head < d:
-            raise ValueError(f"the heads of {name} must not overlap")
-        head = max(head, d)
-    return w.data_ptr(), head, dt
+    if len(shape) == 1:
+        return w.data_ptr(), 0, dt
+    if H > 1 and st[0] < d:
+        raise ValueError(f"the heads of {name} must not overlap")
+    return w.data_ptr(), max(st[0], d), dt
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps):
@@ -154,35 +157,42 @@ def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleave
         raise ValueError("q must be (B, N, Hq, d) or (T, Hq, d)")
     Hk = 0
     if k is not None:
-        Hk = k.shape[-2]
-        if k.shape != (*shape[:-2], Hk, d):
+        ks = k.shape
+        Hk = ks[-2]
+        if ks[-1] != d or ks[:-2] != shape[:-2]:
             raise ValueError("k must have the tokens and the head dim of q")
     elif k_weight is not None:
         raise ValueError("a weight for keys without keys")
-    qw, qh, qt = _weight("q_weight", q_weight, Hq, d)
-    kw, kh, kt = _weight("k_weight", k_weight, Hk, d)
-    if qt is not None and kt is not None and qt != kt:
-        raise ValueError("q_weight and k_weight must have one type")
-    wt = qt if qt is not None else kt if kt is not None else FDMA_FP32
+    qw = qh = kw = kh = 0
+    wt = kt = None
+    if q_weight is not None:
+        qw, qh, wt = _weight("q_weight", q_weight, Hq, d)
+    if k_weight is not None:
+        kw, kh, kt = _weight("k_weight", k_weight, Hk, d)
+        if wt is None:
+            wt = kt
+        elif wt != kt:
+            raise ValueError("q_weight and k_weight must have one type")
     rp = length = rot = 0
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[1] != 2 or not rope.is_contiguous():
+        rs = rope.shape
+        if rope.dtype is not _FP32 or len(rs) != 3 or rs[1] != 2 or not rope.is_contiguous():
             raise ValueError("rope must be contiguous fp32 (length, 2, rot / 2)")
-        rp, length, rot = rope.data_ptr(), rope.shape[0], 2 * rope.shape[2]
+        rp, length, rot = rope.data_ptr(), rs[0], 2 * rs[2]
     pp = sb = sn = 0
     if positions is not None:
-        ps = positions.shape
-        if positions.dtype is not torch.int32 or ps not in ((N,), (B, N)):
+        ps, st = positions.shape, positions.stride()
+        if positions.dtype is not _I32 or (ps != (N,) and ps != (B, N)):
             raise ValueError(f"positions must be int32 ({N},) or ({B}, {N})")
-        pp, sn = positions.data_ptr(), positions.stride(-1)
-        sb = positions.stride(0) if len(ps) == 2 else 0
-    return _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt, qw, qh, kw, kh, rp, length, rot, 1 if interleaved else 0,
-                           first, pp, sb, sn)
+        pp, sn = positions.data_ptr(), st[-1]
+        sb = st[0] if len(st) == 2 else 0
+    return _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt or 0, qw, qh, kw, kh, rp, length, rot,
+                           1 if interleaved else 0, first, pp, sb, sn)
 
 
-def _as_given(t, dev):
+def _like(t):
     """An uninitialised contiguous tensor of t's shape."""
-    return torch.empty(t.shape, dtype=torch.bfloat16, device=dev)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def rope_table(length, rot, *, base=10000.0, device="cuda"):
@@ -191,6 +201,22 @@ def rope_table(length, rot, *, base=10000.0, device="cuda"):
     f = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
     a = torch.arange(length, dtype=torch.float64, device=device)[:, None] * f
     return torch.stack((a.cos(), a.sin()), 1).float()
+
+
+def _launch_norm_rope(args, q, k, q_out, k_out, sp):
+    qr = _rows("q", q)
+    if q_out is None:
+        q_out = _like(q)
+    kr = kor = None
+    if k is not None:
+        kr = _rows("k", k)
+        if k_out is None:
+            k_out = _like(k)
+        kor = _rows("k_out", k_out, k.shape)
+    st = load().fdma_norm_rope(args, qr, kr, _rows("q_out", q_out, q.shape), kor, sp)
+    if st:
+        _fdma._raise(st, "fdma_norm_rope")
+    return q_out, None if k is None else k_out
 
 
 def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=None, first=0, interleaved=False, norm=True,
@@ -206,18 +232,35 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=N
     table is left out too and reported by `fdma.device_error()`.  q_out and k_out may be q and k themselves."""
     dev = _check_device(q, k, q_weight, k_weight, rope, positions, q_out, k_out)
     args = _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps)
-    qr, kr = _rows("q", q), None if k is None else _rows("k", k)
     guard, sp = _on(dev, stream)
+    return _run(guard, _launch_norm_rope, args, q, k, q_out, k_out, sp)
 
-    def call():
-        qo = _as_given(q, dev) if q_out is None else q_out
-        ko = None if k is None else _as_given(k, dev) if k_out is None else k_out
-        return qo, ko, load().fdma_norm_rope(args, qr, kr, _rows("q_out", qo, q), None if k is None else _rows("k_out", ko, k), sp)
 
-    qo, ko, st = _run(guard, call)
+def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweight, ws, sp):
+    lib = load()
+    dq, dk, *dw = grads
+    if dq is None:
+        dq = _like(q)
+    kr = kg = ko = None
+    if k is not None:
+        if dk is None:
+            dk = _like(k)
+        kr, kg, ko = _rows("k", k), _rows("dk_out", dk_out, k.shape), _rows("dk", dk, k.shape)
+    n = wp = 0
+    if want_dweight:
+        dw = [torch.empty_like(w, dtype=_FP32, memory_format=torch.contiguous_format) if t is None and w is not None else t
+              for w, t in zip(weights, dw)]
+        if dw[0] is not None or dw[1] is not None:
+            if ws is None:
+                ws = torch.empty(lib.fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=q.device)
+            wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
+    else:
+        dw = (None, None)
+    st = lib.fdma_norm_rope_bwd(args, _rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, _rows("dq", dq, q.shape), ko,
+                                None if dw[0] is None else dw[0].data_ptr(), None if dw[1] is None else dw[1].data_ptr(), wp, n, sp)
     if st:
-        _fdma._raise(st, "fdma_norm_rope")
-    return qo, ko
+        _fdma._raise(st, "fdma_norm_rope_bwd")
+    return dq, None if k is None else dk, dw[0], dw[1]
 
 
 def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=None, positions=None, first=0,
@@ -235,44 +278,20 @@ def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=No
         raise ValueError("k and dk_out go together")
     dev = _check_device(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace, *g)
     args = _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps)
-    rows = (_rows("q", q), None if k is None else _rows("k", k), _rows("dq_out", dq_out, q),
-            None if k is None else _rows("dk_out", dk_out, k))
     for name, w, t in (("dq_weight", q_weight, g[2]), ("dk_weight", k_weight, g[3])):
-        if t is not None and (w is None or t.dtype is not torch.float32 or t.shape != w.shape or not t.is_contiguous()):
+        if t is not None and (w is None or t.dtype is not _FP32 or t.shape != w.shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous fp32 of its weight's shape")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     guard, sp = _on(dev, stream)
-
-    def call():
-        lib = load()
-        dq = _as_given(q, dev) if g[0] is None else g[0]
-        dk = None if k is None else _as_given(k, dev) if g[1] is None else g[1]
-        dw = [None, None]
-        if want_dweight:
-            dw = [t if t is not None or w is None else torch.empty(w.shape, dtype=torch.float32, device=dev)
-                  for w, t in ((q_weight, g[2]), (k_weight, g[3]))]
-        ws, n = None, 0
-        if dw[0] is not None or dw[1] is not None:
-            ws = workspace
-            if ws is None:
-                ws = torch.empty(lib.fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=dev)
-            n = ws.numel() * ws.element_size()
-        st = lib.fdma_norm_rope_bwd(args, *rows, _rows("dq", dq, q), None if k is None else _rows("dk", dk, k),
-                                    _fdma._ptr(dw[0]), _fdma._ptr(dw[1]), _fdma._ptr(ws), n, sp)
-        return (dq, dk, dw[0], dw[1]), st
-
-    out, st = _run(guard, call)
-    if st:
-        _fdma._raise(st, "fdma_norm_rope_bwd")
-    return out
+    return _run(guard, _launch_norm_rope_bwd, args, q, k, dq_out, dk_out, (q_weight, k_weight), g, want_dweight, workspace, sp)
 
 
-def norm_rope_bwd_workspace(q, k=None, *, q_weight=None, k_weight=None):
+def norm_rope_bwd_workspace(q, k=None, *, q_weight=None, k_weight=None, rope=None):
     """A workspace for `norm_rope_bwd` of these inputs."""
-    dev = _check_device(q, k, q_weight, k_weight)
-    args = _norm_rope_args(q, k, q_weight, k_weight, None, None, 0, False, True, 1.0)
-    return torch.empty(load().fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=dev)
+    _check_device(q, k, q_weight, k_weight, rope)
+    args = _norm_rope_args(q, k, q_weight, k_weight, rope, None, 0, False, True, 1.0)
+    return torch.empty(load().fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=q.device)
 
 
 def rel_starts(num_buckets, max_distance, *, bidirectional=True):
@@ -302,9 +321,18 @@ def _rel_args(H, Nq, Nk, starts, bidirectional, offset):
     n = len(starts)
     if not 0 < n <= MAX_BUCKETS:
         raise ValueError(f"1 to {MAX_BUCKETS} buckets a side")
-    a = struct.pack("%di" % n, *starts)
-    address = ctypes.cast(ctypes.c_char_p(a), ctypes.c_void_p).value
-    return _PACK_REL(H, Nq, Nk, n, address, 1 if bidirectional else 0, Nk - Nq if offset is None else offset), a
+    a = (ctypes.c_int32 * n)(*starts)
+    return _PACK_REL(H, Nq, Nk, n, ctypes.addressof(a), 1 if bidirectional else 0, Nk - Nq if offset is None else offset), a
+
+
+def _launch_rel_bias(args, table, dt, out, shape, sp):
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=table.device)
+    ts, os = table.stride(), out.stride()
+    st = load().fdma_rel_bias(args, table.data_ptr(), dt, _PACK_2Q(ts[0], ts[1]), out.data_ptr(), _PACK_2Q(os[1], os[2]), sp)
+    if st:
+        _fdma._raise(st, "fdma_rel_bias")
+    return out
 
 
 def rel_bias(table, Nq, Nk, starts, *, bidirectional=True, offset=None, out=None, stream=None):
@@ -314,24 +342,31 @@ def rel_bias(table, Nq, Nk, starts, *, bidirectional=True, offset=None, out=None
     have the second half of the table.  offset is the position of query row 0 among the keys, by default Nk - Nq (as
     `fdma.fwd`'s causal).  Nk is a multiple of 8.  `expand` it over a batch."""
     dev = _check_device(table, out)
-    dt = FDMA_FP32 if table.dtype is torch.float32 else FDMA_BF16 if table.dtype is torch.bfloat16 else None
-    if dt is None or table.dim() != 2 or table.shape[0] != (2 if bidirectional else 1) * len(starts):
+    dt, shape = table.dtype, table.shape
+    dt = FDMA_FP32 if dt is _FP32 else FDMA_BF16 if dt is _BF16 else None
+    if dt is None or len(shape) != 2 or shape[0] != (2 if bidirectional else 1) * len(starts):
         raise ValueError("table must be fp32 or bf16 (buckets, H), with len(starts) buckets (twice as many if bidirectional)")
-    H = table.shape[1]
-    args, keep = _rel_args(H, Nq, Nk, starts, bidirectional, offset)
-    if out is not None and (out.dtype is not torch.bfloat16 or out.shape != (1, H, Nq, Nk) or (Nk > 1 and out.stride(3) != 1)):
+    args, keep = _rel_args(shape[1], Nq, Nk, starts, bidirectional, offset)
+    shape = (1, shape[1], Nq, Nk)
+    if out is not None and (out.dtype is not _BF16 or out.shape != shape or (Nk > 1 and out.stride(3) != 1)):
         raise ValueError("out must be bf16 (1, H, Nq, Nk) with contiguous columns")
     guard, sp = _on(dev, stream)
+    return _run(guard, _launch_rel_bias, args, table, dt, out, shape, sp)
 
-    def call():
-        o = torch.empty((1, H, Nq, Nk), dtype=torch.bfloat16, device=dev) if out is None else out
-        return o, load().fdma_rel_bias(args, table.data_ptr(), dt, _PACK_2Q(*table.stride()), o.data_ptr(),
-                                       _PACK_2Q(o.stride(1), o.stride(2)), sp)
 
-    o, st = _run(guard, call)
+def _launch_rel_bias_bwd(args, dbias, causal, dtable, shape, ws, sp):
+    lib = load()
+    st, dev = dbias.stride(), dbias.device
+    if dtable is None:
+        dtable = torch.empty(shape, dtype=_FP32, device=dev)
+    B = dbias.shape[0]
+    if ws is None:
+        ws = torch.empty(lib.fdma_rel_bias_bwd_workspace_size(args, B), dtype=torch.uint8, device=dev)
+    st = lib.fdma_rel_bias_bwd(args, B, dbias.data_ptr(), _PACK_3Q(st[0], st[1], st[2]), 1 if causal else 0, dtable.data_ptr(),
+                               ws.data_ptr(), ws.numel() * ws.element_size(), sp)
     if st:
-        _fdma._raise(st, "fdma_rel_bias")
-    return o
+        _fdma._raise(st, "fdma_rel_bias_bwd")
+    return dtable
 
 
 def rel_bias_bwd(dbias, starts, *, bidirectional=True, offset=None, causal=False, dtable=None,
@@ -340,31 +375,17 @@ def rel_bias_bwd(dbias, starts, *, bidirectional=True, offset=None, causal=False
     over the batch too.  With causal=True keys behind the query count as zeros and most are not read.  A workspace
     passed in (uint8, `rel_bias_bwd_workspace`) serves one call at a time."""
     dev = _check_device(dbias, dtable, workspace)
-    st = dbias.stride()
-    if dbias.dtype is not torch.bfloat16 or len(st) != 4 or (st[3] != 1 and dbias.shape[3] > 1):
+    st, ds = dbias.stride(), dbias.shape
+    if dbias.dtype is not _BF16 or len(st) != 4 or (st[3] != 1 and ds[3] > 1):
         raise ValueError("dbias must be bf16 (B, H, Nq, Nk) with contiguous columns")
-    B, H, Nq, Nk = dbias.shape
-    args, keep = _rel_args(H, Nq, Nk, starts, bidirectional, offset)
-    shape = ((2 if bidirectional else 1) * len(starts), H)
-    if dtable is not None and (dtable.dtype is not torch.float32 or dtable.shape != shape or not dtable.is_contiguous()):
+    args, keep = _rel_args(ds[1], ds[2], ds[3], starts, bidirectional, offset)
+    shape = ((2 if bidirectional else 1) * len(starts), ds[1])
+    if dtable is not None and (dtable.dtype is not _FP32 or dtable.shape != shape or not dtable.is_contiguous()):
         raise ValueError(f"dtable must be contiguous fp32 {shape}")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     guard, sp = _on(dev, stream)
-
-    def call():
-        lib = load()
-        out = torch.empty(shape, dtype=torch.float32, device=dev) if dtable is None else dtable
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(lib.fdma_rel_bias_bwd_workspace_size(args, B), dtype=torch.uint8, device=dev)
-        return out, lib.fdma_rel_bias_bwd(args, B, dbias.data_ptr(), _PACK_3Q(*st[:3]), 1 if causal else 0, out.data_ptr(),
-                                          ws.data_ptr(), ws.numel() * ws.element_size(), sp)
-
-    out, status = _run(guard, call)
-    if status:
-        _fdma._raise(status, "fdma_rel_bias_bwd")
-    return out
+    return _run(guard, _launch_rel_bias_bwd, args, dbias, causal, dtable, shape, workspace, sp)
 
 
 def rel_bias_bwd_workspace(B, H, Nq, Nk, starts, *, bidirectional=True, device="cuda"):

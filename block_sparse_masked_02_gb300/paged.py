@@ -186,6 +186,17 @@ def kv_append(k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, k_exp=None, v
     _fdma._raise(st, "fdma_kv_append")
 
 
+def _launch_norm_rope_append(args, c, q, k, v, q_out, cu_q, sp):
+    rows = _inputs._rows
+    qr, kr, vr = rows("q", q), rows("k", k), rows("v", v)
+    if q_out is None:
+        q_out = _inputs._like(q)
+    st = _inputs.load().fdma_norm_rope_append(args, _PACK_CACHE(*c), qr, kr, vr, rows("q_out", q_out, q.shape), cu_q.data_ptr(), sp)
+    if st:
+        _fdma._raise(st, "fdma_norm_rope_append")
+    return q_out
+
+
 def norm_rope_append(q, k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, q_weight=None, k_weight=None, rope=None,
                      positions=None, interleaved=False, norm=True, eps=1e-6, k_exp=None, v_exp=None, q_out=None, stream=None):
     """`inputs.norm_rope` of the packed new tokens q (T, Hq, d) and k (T, Hkv, d), and `kv_append` of the keys with v
@@ -193,29 +204,19 @@ def norm_rope_append(q, k, v, k_cache, v_cache, page_table, k_lens, cu_q, *, q_w
     sequence, or positions[t] (int32 (T,)) where that is something else.  A float8_e4m3fn cache takes its codes from the
     fp32 values, rounded once.  Rows behind cu_q[B] and tokens at a negative position (padding) are left as they are, in
     q_out (uninitialised where it is allocated here) and in the cache."""
-    dev = _check_device(q, k, v, k_cache, v_cache, page_table, k_lens, cu_q, q_weight, k_weight, rope, positions, k_exp, v_exp,
-                        q_out)
+    dev = _inputs._check_device(q, k, v, k_cache, v_cache, page_table, k_lens, cu_q, q_weight, k_weight, rope, positions, k_exp,
+                                v_exp, q_out)
     c = _cache(k_cache, v_cache, page_table, k_lens, k_exp, v_exp)
     B, Hkv, d = c[:3]
     _check_int("cu_q", cu_q, B + 1)
-    T = q.shape[0]
-    if q.dim() != 3 or q.shape[2] != d or k.shape != (T, Hkv, d) or v.shape != k.shape:
+    qs = q.shape
+    if len(qs) != 3 or qs[2] != d or k.shape != (qs[0], Hkv, d) or v.shape != k.shape:
         raise ValueError("q, k and v must be (T, heads, d) with the kv heads and head dim of the cache")
     if positions is not None:
-        _check_int("positions", positions, T)
+        _check_int("positions", positions, qs[0])
     args = _inputs._norm_rope_args(q, k, q_weight, k_weight, rope, positions, 0, interleaved, norm, eps)
-    rows = (_inputs._rows("q", q), _inputs._rows("k", k), _inputs._rows("v", v))
-    guard, sp = _on(dev, stream)
-
-    def call():
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev) if q_out is None else q_out
-        return out, _inputs.load().fdma_norm_rope_append(args, _PACK_CACHE(*c), *rows, _inputs._rows("q_out", out, q),
-                                                         cu_q.data_ptr(), sp)
-
-    out, st = _inputs._run(guard, call)
-    if st:
-        _fdma._raise(st, "fdma_norm_rope_append")
-    return out
+    guard, sp = _inputs._on(dev, stream)
+    return _inputs._run(guard, _launch_norm_rope_append, args, c, q, k, v, q_out, cu_q, sp)
 
 
 def kv_gather(k_cache, v_cache, page_table, k_lens, cu_k, total, *, first=None, k_exp=None, v_exp=None, k_out=None,

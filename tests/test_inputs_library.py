@@ -237,7 +237,7 @@ def test_binding_refuses(I):
         with pytest.raises(ValueError):
             I._rows("x", bad)
     with pytest.raises(ValueError):
-        I._rows("x", x, x[:, :1])
+        I._rows("x", x, x[:, :1].shape)
     for bad in ((1, 128), (3, 128), (32, 8), (33, 128)):
         with pytest.raises(ValueError):
             I.rel_starts(*bad)
