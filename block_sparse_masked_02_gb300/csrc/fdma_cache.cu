@@ -398,7 +398,7 @@ __device__ __forceinline__ void store_codes(uint8_t* piece, int apart, const uin
 
 // A warp takes a token, or a run of its passes where there are few tokens: queries, keys, values, in this order.
 template <bool FP8, int P, int LPR, bool ADJ>
-__global__ void __launch_bounds__(kCacheThreads, 6) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
+__global__ void __launch_bounds__(kCacheThreads, 5) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
   constexpr int RPW = 32 / LPR, SLOTS = 48 / P;
   __shared__ __align__(16) uint8_t rings[kCacheThreads / 32][SLOTS * Ring<P>::kSlot];
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
@@ -477,7 +477,14 @@ __global__ void __launch_bounds__(kCacheThreads, 6) norm_rope_append_kernel(cons
       cp_async_wait<SLOTS - 1>();
       const Raw<P> raw = ring.get(slot);
       Pairs<P> x = widen<P, ADJ>(raw);
-      if (!is_v) norm_and_turn<LPR>(p.v, x, wt, t, at);
+      if (!is_v) {
+        if (p.v.norm) {
+          float by;
+          scale(x, row_rsqrt<LPR>(p.v, x, by));
+          multiply(x, wt);
+        }
+        turn<false>(x, t, at);
+      }
       if (!FP8 || is_q) {
         if (h < end) store_raw<P>(reinterpret_cast<uint16_t*>(to), at.apart, is_v ? raw : narrow<P, ADJ>(x));
       } else {

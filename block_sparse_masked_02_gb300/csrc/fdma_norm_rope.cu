@@ -4,6 +4,7 @@
 // With x a row, r = 1 / sqrt(mean(x^2) + eps) and g the gradient of the output turned back:
 //   forward   y = turned(x r w)
 //   backward  e = g r,  dx = e w - x r^2 mean(e w x),  dw = sum over tokens (and heads that share it) of e x.
+// (Both sums of a row can run together, as r may be taken into account last; that took more instructions and 3 % longer.)
 //
 // One kernel does either.  Bound by memory traffic, it keeps it going: a CTA has a chunk of one tensor's
 // heads (one pass where every head has a weight of its own) and its warps walk over tokens, a pass a step, with
@@ -25,7 +26,7 @@ constexpr int ctas_per_sm(int piece, bool back) { return back && piece == 8 ? 2 
 
 struct TokenLine {
   int N, batches;  // batches 1: tokens are one line
-  int64_t tokens;
+  uint32_t tokens;
 };
 
 // A token of a warp's walk.
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kSlots<P, BACK>, STEP = BACK ? 2 : 1, WEIGHT = 256 * P;
   static_assert(kRingBytes<P, BACK> >= RPW * COLS * sizeof(float) || !BACK, "the sums take the rings' place");
   extern __shared__ __align__(16) uint8_t smem[];  // weight | rings | angles
+  if (BACK) launch_dependents();
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR, warp = threadIdx.x >> 5;
   int cta = blockIdx.x;
   const int side = cta >= p.plan.chunks[0] * p.plan.ctas[0];
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   // what is fetched next
   Token next{tok0, 0};
   wrap(p.line, next);
-  int64_t tok_next = tok0;
+  uint32_t tok_next = tok0;
   int pos_next = tok_next < p.line.tokens ? position_of(p.v, next.b, next.n) : 0;
   int q_next = q_last, h_next = 0, row_next = 0;
   uint32_t left_out = 0, begun = 0;  // bit t % 32: token t of the walk is left out; tokens begun
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       const uint32_t bit = 1u << (begun & 31u);
       left_out = pos < 0 ? left_out | bit : left_out & ~bit;
       ++begun;
+      __syncwarp();  // (these angles may take the place of those that were read last)
       if (pos >= 0) {
         const float* angles = p.v.rope + static_cast<int64_t>(pos) * p.v.rot;
         for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(table + row_next * p.plan.table + 4 * i, angles + i, 16);
@@ -159,15 +162,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   wrap(p.line, now);
   int slot = 0, row = 0;
   uint32_t done = 0;
-  for (int64_t tok = tok0; tok < p.line.tokens; tok += step) {
+  for (uint32_t tok = tok0; tok < p.line.tokens; tok += step) {
     const bool left = (left_out >> (done & 31u)) & 1u;
     const uint32_t angles = table + row * p.plan.table + 4 * P * l, half = 2 * p.v.rot;
     uint16_t* to = out.p + now.b * out.st[0] + now.n * out.st[1] + out_first;
     int h = h_first;
+    cp_async_wait<SLOTS - 1>();
+    __syncwarp();  // the angles, which other lanes fetched
 #pragma unroll 1
     for (int q = q_first; q < q_last; ++q, h += RPW, to += by_out) {
       cp_async_wait<SLOTS - 1>();
-      __syncwarp();  // the angles, which other lanes fetched
       if (left) {
         if (BACK && h < h_end) store_raw<P>(to, at.apart, no_raw<P>());
       } else {
@@ -206,7 +210,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
         }
         if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
       }
-      __syncwarp();  // (the step that is begun now may take this one's place among the angles)
       start(slot);
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
@@ -247,6 +250,7 @@ struct WeightSumView {
 // Adds the CTAs' parts: block (row of the weights, 32 columns) of 32 x 32 threads.
 __global__ void __launch_bounds__(1024) weight_sum_kernel(const __grid_constant__ WeightSumView p) {
   __shared__ float s[32][33];
+  wait_for_primary();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.y * 32 + tx;
   int side, h = 0;
   if (p.heads) {
@@ -399,7 +403,7 @@ int validate_positions(const fdma_norm_rope_args& a) {
 void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
   p.v = norm_rope_view(a);
   if (a.positions == nullptr && a.rope == nullptr) p.v.first = 0;
-  p.line = {a.N, a.B, static_cast<int64_t>(a.B) * a.N};
+  p.line = {a.N, a.B, static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N)};
   p.H[0] = a.Hq;
   p.H[1] = a.Hk;
   for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot));
@@ -500,8 +504,7 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   w.heads = by_head(*a);
   w.rpw = pass_rows(a->d, p.v.rot);
   const dim3 grid(w.heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
-  weight_sum_kernel<<<grid, 1024, 0, cs>>>(w);
-  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  return launch_behind(weight_sum_kernel, grid, 1024, cs, w) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -369,29 +369,17 @@ __device__ __forceinline__ void put_weight(uint32_t at, const Pairs<P>& w) {
 // the scaled row.  Every lane of the warp calls it.
 template <int LPR, int P>
 __device__ __forceinline__ float row_rsqrt(const NormRopeView& v, Pairs<P>& x, float& by) {
-  constexpr float kDown = 0x1p-70f;
   float s = row_sum<LPR>(dot(x, x));
   by = 1.f;
   const bool over = s == __int_as_float(0x7f800000);
   if (__any_sync(0xffffffffu, over)) {
     if (over) {
-      by = kDown;
-      scale(x, kDown);
+      by = 0x1p-70f;
+      scale(x, by);
     }
     s = row_sum<LPR>(dot(x, x));
   }
   return rsqrtf(s * v.inv_d + v.eps * by * by);
-}
-
-// The forward of a row: x becomes what is stored.  Every lane of the warp calls it.
-template <int LPR, int P>
-__device__ __forceinline__ void norm_and_turn(const NormRopeView& v, Pairs<P>& x, const Pairs<P>& w, const Turn<P>& t, const Lane& n) {
-  if (v.norm) {
-    float by;
-    scale(x, row_rsqrt<LPR>(v, x, by));
-    multiply(x, w);
-  }
-  turn<false>(x, t, n);
 }
 
 // Position of a token, checked: -1 where it is left out.

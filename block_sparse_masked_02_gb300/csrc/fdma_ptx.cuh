@@ -474,6 +474,27 @@ __device__ __forceinline__ float add_bf16hi(uint32_t w, float c) {
   return r;
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel that a launch with launch_behind() follows says at its start that the follower's CTAs may be placed; they
+// wait for all of this kernel's (and of what came before it) writes before they read.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a kernel that calls wait_for_primary() so that its launch overlaps the end of the one before it in the stream.
+template <typename A>
+inline cudaError_t launch_behind(void (*kern)(A), dim3 grid, int threads, cudaStream_t stream, const A& args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, args);
+}
+
 // ---------------------------------------------------------------- packing
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

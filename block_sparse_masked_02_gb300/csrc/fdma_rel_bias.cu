@@ -12,6 +12,8 @@
 // over the matrix together and DRAM sees neighbouring rows.  A CTA's warps have eight parts of a band; it
 // joins their sums, adds up the diagonals of each bucket in a fixed order and writes one number for each bucket
 // that the band touches.  A second kernel adds those.
+#include <type_traits>
+
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
 #include "fdma_ptx.cuh"
@@ -24,37 +26,38 @@ constexpr int kMaxLen = 131072;  // as fdma_fwd's
 constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
 constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
 
+// CAP: most buckets of a side.  (A launch copies the arguments: with 256 it takes 2 us more on the host than with 32.)
+template <int CAP>
 struct RelView {
   int H, Nq, Nk, off;
   int n, two_sided;  // buckets of a side
-  int starts[FDMA_MAX_BUCKETS];
+  int starts[CAP];
 
   __host__ __device__ int buckets() const { return two_sided ? 2 * n : n; }
   __host__ __device__ int row_blocks() const { return (Nq + 7) >> 3; }
-  // The bucket of a distance, by its side's first distances.
-  __device__ __forceinline__ int side(const int* first, int a) const {
+  // The bucket of a distance on its side.
+  __device__ __forceinline__ int side(int a) const {
     int lo = 0, hi = n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (first[mid] <= a) lo = mid;
+      if (starts[mid] <= a) lo = mid;
       else hi = mid - 1;
     }
     return lo;
   }
-  __device__ __forceinline__ int side(int a) const { return side(starts, a); }
   // ... of a difference key - query.  It falls as delta rises to 0, and rises (from n, two-sided) or stays behind
   // it: where both ends of an interval have the same bucket, all of it has.
-  __device__ __forceinline__ int bucket(const int* first, int delta) const {
-    if (delta <= 0) return side(first, -delta);
-    return two_sided ? n + side(first, delta) : side(first, 0);
+  __device__ __forceinline__ int bucket(int delta) const {
+    if (delta <= 0) return side(-delta);
+    return two_sided ? n + side(delta) : side(0);
   }
-  __device__ __forceinline__ int bucket(int delta) const { return bucket(starts, delta); }
 };
 
 // ---- forward
 
+template <int CAP>
 struct FwdView {
-  RelView r;
+  RelView<CAP> r;
   const void* table;
   int table_bf16;
   int64_t ts[2];
@@ -63,7 +66,8 @@ struct FwdView {
   uint32_t ncc, units;  // warps along the columns; of all rows and heads
 };
 
-__device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, int h) {
+template <int CAP>
+__device__ __forceinline__ uint32_t table_value(const FwdView<CAP>& p, int bucket, int h) {
   const int64_t at = bucket * p.ts[0] + h * p.ts[1];
   if (p.table_bf16) return static_cast<const uint16_t*>(p.table)[at];
   return pack_bf16x2(static_cast<const float*>(p.table)[at], 0.f) & 0xffffu;
@@ -71,17 +75,19 @@ __device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, in
 
 // A warp writes 8 rows of 256 columns: with walks of 1, 2, 4, 8 or 16 blocks down the diagonal, which look up their values
 // once for all of them, four heads of 16384 x 16384 took 285, 310, 319, 330 or 353 us.
-__global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView p) {
-  __shared__ int first[FDMA_MAX_BUCKETS];  // (lanes look at different ones, which constant memory serves in turn)
-  const int lane = threadIdx.x & 31;
-  const uint32_t unit = blockIdx.x * kWarps + (threadIdx.x >> 5);
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView<CAP> p) {
+  __shared__ int first[CAP];  // (lanes look at different ones, which constant memory serves in turn)
+  __shared__ __align__(16) uint16_t values[kWarps][272];  // of a warp's diagonals
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t unit = blockIdx.x * kWarps + warp;
   const uint32_t hr = unit / p.ncc, nrb = p.r.row_blocks();
   const int cc = static_cast<int>(unit - hr * p.ncc), h = static_cast<int>(hr / nrb), rb = static_cast<int>(hr - h * nrb);
   const int lo = 256 * cc - 8 * rb - p.r.off - 7;
   const int b0 = p.r.bucket(lo);
   const bool one = b0 == p.r.bucket(lo + kSpan - 1) || unit >= p.units;
   if (__syncthreads_or(!one)) {
-    for (int i = threadIdx.x; i < p.r.n; i += kThreads) first[i] = p.r.starts[i];
+    for (int i = threadIdx.x; i < CAP; i += kThreads) first[i] = i < p.r.n ? p.r.starts[i] : 0x7fffffff;
     __syncthreads();
   }
   if (unit >= p.units) return;
@@ -91,11 +97,29 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < 14; ++i) w[i] = v;
   } else {
-    uint32_t v[15];
+    // nine diagonals a lane, looked up side by side: a search one after the other took 6 instead of 2 us
+    int a[9], s[9];
 #pragma unroll
-    for (int i = 0; i < 15; ++i) v[i] = table_value(p, p.r.bucket(first, lo + 8 * lane + i), h);
+    for (int k = 0; k < 9; ++k) {
+      const int delta = lo + 32 * k + lane;
+      a[k] = p.r.two_sided ? abs(delta) : max(-delta, 0);
+      s[k] = 0;
+    }
 #pragma unroll
-    for (int i = 0; i < 14; ++i) w[i] = v[i] | (v[i + 1] << 16);
+    for (int step = CAP / 2; step > 0; step >>= 1)
+#pragma unroll
+      for (int k = 0; k < 9; ++k)
+        if (first[s[k] + step] <= a[k]) s[k] += step;
+#pragma unroll
+    for (int k = 0; k < 9; ++k) {
+      const int i = 32 * k + lane;
+      if (i < 272) values[warp][i] = table_value(p, s[k] + (p.r.two_sided && lo + i > 0 ? p.r.n : 0), h);
+    }
+    __syncwarp();
+    const uint4 x = *reinterpret_cast<const uint4*>(&values[warp][8 * lane]), y = *reinterpret_cast<const uint4*>(&values[warp][8 * lane + 8]);
+    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int i = 0; i < 14; ++i) w[i] = i % 2 == 0 ? v[i / 2] : __byte_perm(v[i / 2], v[i / 2 + 1], 0x5432);
   }
   const int cb = 32 * cc + lane, rows = min(p.r.Nq - 8 * rb, 8);
   if (cb >= p.r.Nk >> 3) return;
@@ -107,8 +131,9 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
 
 // ---- backward
 
+template <int CAP>
 struct BwdView {
-  RelView r;
+  RelView<CAP> r;
   int B, causal;
   int bands, parts;  // bands with anything in them; parts is a multiple of 8
   const uint16_t* db;
@@ -122,15 +147,18 @@ struct Deltas {
   int lo, hi;
 };
 // Band 0 begins with the block in the matrix's lower left corner.
-__device__ __forceinline__ int first_delta(const RelView& r) { return -8 * (r.row_blocks() - 1) - r.off - 7; }
-__device__ __forceinline__ Deltas band_deltas(const BwdView& p, int band) {
+template <int CAP>
+__device__ __forceinline__ int first_delta(const RelView<CAP>& r) { return -8 * (r.row_blocks() - 1) - r.off - 7; }
+template <int CAP>
+__device__ __forceinline__ Deltas band_deltas(const BwdView<CAP>& p, int band) {
   Deltas d;
   d.lo = first_delta(p.r) + 256 * band;
   d.hi = d.lo + kSpan - 1;
   if (p.causal) d.hi = min(d.hi, 0);
   return d;
 }
-__device__ __forceinline__ Deltas bucket_deltas(const RelView& r, int bucket) {
+template <int CAP>
+__device__ __forceinline__ Deltas bucket_deltas(const RelView<CAP>& r, int bucket) {
   constexpr int kFar = 0x7fffffff;
   const bool right = bucket >= r.n;
   const int s = right ? bucket - r.n : bucket, a0 = r.starts[s], a1 = s + 1 < r.n ? r.starts[s + 1] - 1 : kFar;
@@ -151,7 +179,8 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-__global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView p) {
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView<CAP> p) {
   __shared__ float diag[kWarps][kSpan + 1];
   __shared__ float all[kSpan + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -236,8 +265,9 @@ __global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_
 }
 
 // Adds the CTAs' sums of one bucket and head.
-__global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView p) {
-  __shared__ double s[kThreads];
+template <int CAP>
+__global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView<CAP> p) {
+  __shared__ double s[kWarps];
   const int k = blockIdx.x % p.r.buckets(), h = blockIdx.x / p.r.buckets();
   const Deltas q = bucket_deltas(p.r, k);
   // the bands that have some of it
@@ -254,50 +284,61 @@ __global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_co
       sum += p.part[cta * p.r.buckets() + k];
     }
   }
-  s[threadIdx.x] = sum;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = sum;
   __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) s[threadIdx.x] += s[threadIdx.x + o];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) p.dtable[static_cast<int64_t>(k) * p.r.H + h] = static_cast<float>(s[0]);
+  if (threadIdx.x != 0) return;
+  for (int j = 1; j < kWarps; ++j) sum += s[j];
+  p.dtable[static_cast<int64_t>(k) * p.r.H + h] = static_cast<float>(sum);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int validate(const fdma_rel_args* a) {
   if (a == nullptr) return FDMA_ERR_INVALID;
-  if (a->H <= 0 || a->Nq < 0 || a->Nk < 0 || a->num_starts <= 0 || a->starts == nullptr) return FDMA_ERR_INVALID;
+  if (a->H <= 0 || a->Nq < 0 || a->Nk < 0 || a->num_starts <= 0) return FDMA_ERR_INVALID;
   if (a->two_sided != 0 && a->two_sided != 1) return FDMA_ERR_INVALID;
   if (a->offset > (1 << 30) || a->offset < -(1 << 30)) return FDMA_ERR_INVALID;
   if (a->num_starts > FDMA_MAX_BUCKETS || a->H > (1 << 20) || a->Nq > kMaxLen || a->Nk > kMaxLen || a->Nk % 8 != 0)
     return FDMA_ERR_UNSUPPORTED;
-  if (a->starts[0] != 0) return FDMA_ERR_INVALID;
-  for (int i = 1; i < a->num_starts; ++i)
-    if (a->starts[i] < a->starts[i - 1]) return FDMA_ERR_INVALID;
   return FDMA_OK;
 }
 
-RelView view(const fdma_rel_args& a) {
-  RelView r{};
+int validate_starts(const fdma_rel_args& a, const int32_t* starts) {
+  if (starts == nullptr || starts[0] != 0) return FDMA_ERR_INVALID;
+  for (int i = 1; i < a.num_starts; ++i)
+    if (starts[i] < starts[i - 1]) return FDMA_ERR_INVALID;
+  return FDMA_OK;
+}
+
+template <int CAP>
+void set_view(RelView<CAP>& r, const fdma_rel_args& a, const int32_t* starts) {
   r.H = a.H;
   r.Nq = a.Nq;
   r.Nk = a.Nk;
   r.off = a.offset;
   r.n = a.num_starts;
   r.two_sided = a.two_sided;
-  for (int i = 0; i < r.n; ++i) r.starts[i] = a.starts[i];
-  return r;
+  for (int i = 0; i < r.n; ++i) r.starts[i] = starts[i];
 }
+
+constexpr int kSmallCap = 32;
+template <typename F>
+int with_cap(int n, F&& f) {
+  return n <= kSmallCap ? f(std::integral_constant<int, kSmallCap>{}) : f(std::integral_constant<int, FDMA_MAX_BUCKETS>{});
+}
+
+int row_blocks(const fdma_rel_args& a) { return (a.Nq + 7) / 8; }
 
 struct BwdPlan {
   int bands, parts;
   int64_t ctas;
 };
 // Bands and parts of a call; what it needs of the workspace does not depend on `causal`.
-BwdPlan bwd_plan(const RelView& r, int64_t B, bool causal) {
+BwdPlan bwd_plan(const fdma_rel_args& r, int64_t B, bool causal) {
   BwdPlan p;
-  const int nrb = r.row_blocks(), ncb = r.Nk / 8, bands = (nrb + ncb - 1 + 31) / 32;
+  const int nrb = row_blocks(r), ncb = r.Nk / 8, bands = (nrb + ncb - 1 + 31) / 32;
   // groups of eight warps that share a band: walks of about kBwdSteps block rows, shorter ones where that is too few
   // CTAs for the machine
   const int64_t fill = (kBwdCtas + B * r.H * bands - 1) / (B * r.H * bands), most = (nrb + kWarps - 1) / kWarps;
@@ -306,7 +347,7 @@ BwdPlan bwd_plan(const RelView& r, int64_t B, bool causal) {
   p.parts = kWarps * static_cast<int>(groups);
   p.bands = bands;
   if (causal) {  // those that begin at a key that some query sees
-    const int64_t lo = -8ll * (nrb - 1) - r.off - 7;
+    const int64_t lo = -8ll * (nrb - 1) - r.offset - 7;
     const int64_t n = lo > 0 ? 0 : -lo / 256 + 1;
     if (n < bands) p.bands = static_cast<int>(n);
   }
@@ -321,9 +362,10 @@ using namespace fdma;
 
 extern "C" {
 
-int fdma_rel_bias(const fdma_rel_args* a, const void* table, int table_type, const int64_t ts[2], void* out,
-                  const int64_t os[2], void* stream) {
-  const int st = validate(a);
+int fdma_rel_bias(const fdma_rel_args* a, const int32_t* starts, const void* table, int table_type, const int64_t ts[2],
+                  void* out, const int64_t os[2], void* stream) {
+  int st = validate(a);
+  if (st == FDMA_OK) st = validate_starts(*a, starts);
   if (st != FDMA_OK) return st;
   if (table == nullptr || ts == nullptr || os == nullptr) return FDMA_ERR_INVALID;
   if (table_type != FDMA_FP32 && table_type != FDMA_BF16) return FDMA_ERR_INVALID;
@@ -334,34 +376,35 @@ int fdma_rel_bias(const fdma_rel_args* a, const void* table, int table_type, con
     return FDMA_ERR_INVALID;  // rows that overlap
   if (a->H > 1 && a->Nq == 1 && os[0] < a->Nk) return FDMA_ERR_INVALID;
   if (!aligned16(out) || (a->H > 1 && os[0] % 8 != 0) || (a->Nq > 1 && os[1] % 8 != 0)) return FDMA_ERR_UNSUPPORTED;
-  FwdView p{};
-  p.r = view(*a);
-  p.table = table;
-  p.table_bf16 = table_type == FDMA_BF16;
-  p.out = static_cast<uint16_t*>(out);
-  for (int i = 0; i < 2; ++i) {
-    p.ts[i] = ts[i];
-    p.os[i] = os[i];
-  }
-  p.ncc = (a->Nk / 8 + 31) / 32;
-  const int64_t units = static_cast<int64_t>(p.ncc) * p.r.row_blocks() * a->H;
+  const int64_t ncc = (a->Nk / 8 + 31) / 32, units = ncc * row_blocks(*a) * a->H;
   if (units > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
-  p.units = static_cast<uint32_t>(units);
-  const int64_t blocks = (units + kWarps - 1) / kWarps;
-  rel_bias_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  return with_cap(a->num_starts, [&](auto cap) {
+    FwdView<decltype(cap)::value> p;
+    set_view(p.r, *a, starts);
+    p.table = table;
+    p.table_bf16 = table_type == FDMA_BF16;
+    p.out = static_cast<uint16_t*>(out);
+    for (int i = 0; i < 2; ++i) {
+      p.ts[i] = ts[i];
+      p.os[i] = os[i];
+    }
+    p.ncc = static_cast<uint32_t>(ncc);
+    p.units = static_cast<uint32_t>(units);
+    rel_bias_kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  });
 }
 
 size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* a, int B) {
   if (validate(a) != FDMA_OK || B <= 0 || B > (1 << 20) || a->Nq == 0 || a->Nk == 0) return 0;
-  const RelView r = view(*a);
-  const BwdPlan plan = bwd_plan(r, B, false);
-  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * r.buckets() * sizeof(float);
+  const BwdPlan plan = bwd_plan(*a, B, false);
+  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * (a->two_sided ? 2 : 1) * a->num_starts * sizeof(float);
 }
 
-int fdma_rel_bias_bwd(const fdma_rel_args* a, int B, const void* dbias, const int64_t ds[3], int causal, float* dtable,
-                      void* workspace, size_t workspace_bytes, void* stream) {
-  const int st = validate(a);
+int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, const void* dbias, const int64_t ds[3], int causal,
+                      float* dtable, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate(a);
+  if (st == FDMA_OK) st = validate_starts(*a, starts);
   if (st != FDMA_OK) return st;
   if (B < 0 || (causal != 0 && causal != 1) || dtable == nullptr) return FDMA_ERR_INVALID;
   if (B > (1 << 20)) return FDMA_ERR_UNSUPPORTED;
@@ -378,27 +421,29 @@ int fdma_rel_bias_bwd(const fdma_rel_args* a, int B, const void* dbias, const in
     if (ds[i] % 8 != 0) return FDMA_ERR_UNSUPPORTED;
   }
   if (!aligned16(dbias)) return FDMA_ERR_UNSUPPORTED;
-  BwdView p{};
-  p.r = view(*a);
-  const BwdPlan whole = bwd_plan(p.r, B, false), plan = bwd_plan(p.r, B, causal != 0);
+  const BwdPlan whole = bwd_plan(*a, B, false), plan = bwd_plan(*a, B, causal != 0);
   if (whole.ctas > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < static_cast<size_t>(whole.ctas) * buckets * sizeof(float))
     return FDMA_ERR_WORKSPACE;
-  p.bands = plan.bands;
-  p.parts = plan.parts;
-  p.B = B;
-  p.causal = causal;
-  p.db = static_cast<const uint16_t*>(dbias);
-  for (int i = 0; i < 3; ++i) p.ds[i] = ds[i];
-  p.part = static_cast<float*>(workspace);
-  p.dtable = dtable;
-  if (plan.ctas > 0) {
-    rel_bias_bwd_kernel<<<static_cast<unsigned>(plan.ctas), kThreads, 0, cs>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
-  }
-  rel_bias_join_kernel<<<static_cast<unsigned>(buckets * a->H), kThreads, 0, cs>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  return with_cap(a->num_starts, [&](auto cap) {
+    BwdView<decltype(cap)::value> p;
+    set_view(p.r, *a, starts);
+    p.B = B;
+    p.causal = causal;
+    p.bands = plan.bands;
+    p.parts = plan.parts;
+    p.db = static_cast<const uint16_t*>(dbias);
+    for (int i = 0; i < 3; ++i) p.ds[i] = ds[i];
+    p.part = static_cast<float*>(workspace);
+    p.dtable = dtable;
+    if (plan.ctas > 0) {
+      rel_bias_bwd_kernel<<<static_cast<unsigned>(plan.ctas), kThreads, 0, cs>>>(p);
+      if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
+    }
+    rel_bias_join_kernel<<<static_cast<unsigned>(buckets * a->H), kThreads, 0, cs>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
+  });
 }
 
 }  // extern "C"

@@ -50,14 +50,14 @@ class FdmaNormRopeArgs(ctypes.Structure):
 class FdmaRelArgs(ctypes.Structure):
     _fields_ = [
         ("H", ctypes.c_int32), ("Nq", ctypes.c_int32), ("Nk", ctypes.c_int32), ("num_starts", ctypes.c_int32),
-        ("starts", ctypes.c_void_p), ("two_sided", ctypes.c_int32), ("offset", ctypes.c_int32),
+        ("two_sided", ctypes.c_int32), ("offset", ctypes.c_int32),
     ]
 
 
 # The structs as packed bytes (native alignment): a quarter of the time that ctypes fields take.
 _PACK_NORM_ROPE = struct.Struct("6ifiPqPqP4iP2q").pack
 _PACK_ROWS = struct.Struct("P3q").pack
-_PACK_REL = struct.Struct("4iP2i").pack
+_PACK_REL = struct.Struct("6i").pack
 _PACK_2Q = struct.Struct("2q").pack
 _PACK_3Q = struct.Struct("3q").pack
 
@@ -78,11 +78,11 @@ def load() -> ctypes.CDLL:
         lib.fdma_norm_rope_bwd.restype = I
         lib.fdma_norm_rope_append.argtypes = [S, S, S, S, S, S, P, P]
         lib.fdma_norm_rope_append.restype = I
-        lib.fdma_rel_bias.argtypes = [S, P, I, S, P, S, P]
+        lib.fdma_rel_bias.argtypes = [S, S, P, I, S, P, S, P]
         lib.fdma_rel_bias.restype = I
         lib.fdma_rel_bias_bwd_workspace_size.argtypes = [S, I]
         lib.fdma_rel_bias_bwd_workspace_size.restype = N
-        lib.fdma_rel_bias_bwd.argtypes = [S, I, P, S, I, P, P, N, P]
+        lib.fdma_rel_bias_bwd.argtypes = [S, S, I, P, S, I, P, P, N, P]
         lib.fdma_rel_bias_bwd.restype = I
         _LIB = lib
     return _LIB
@@ -317,19 +317,19 @@ def rel_starts(num_buckets, max_distance, *, bidirectional=True):
 
 
 def _rel_args(H, Nq, Nk, starts, bidirectional, offset):
-    """(fdma_rel_args as packed bytes, what they point to)."""
+    """(fdma_rel_args, starts) as packed bytes."""
     n = len(starts)
     if not 0 < n <= MAX_BUCKETS:
         raise ValueError(f"1 to {MAX_BUCKETS} buckets a side")
-    a = (ctypes.c_int32 * n)(*starts)
-    return _PACK_REL(H, Nq, Nk, n, ctypes.addressof(a), 1 if bidirectional else 0, Nk - Nq if offset is None else offset), a
+    return (_PACK_REL(H, Nq, Nk, n, 1 if bidirectional else 0, Nk - Nq if offset is None else offset),
+            struct.pack(f"{n}i", *starts))
 
 
-def _launch_rel_bias(args, table, dt, out, shape, sp):
+def _launch_rel_bias(args, first, table, dt, out, shape, sp):
     if out is None:
         out = torch.empty(shape, dtype=_BF16, device=table.device)
     ts, os = table.stride(), out.stride()
-    st = load().fdma_rel_bias(args, table.data_ptr(), dt, _PACK_2Q(ts[0], ts[1]), out.data_ptr(), _PACK_2Q(os[1], os[2]), sp)
+    st = load().fdma_rel_bias(args, first, table.data_ptr(), dt, _PACK_2Q(ts[0], ts[1]), out.data_ptr(), _PACK_2Q(os[1], os[2]), sp)
     if st:
         _fdma._raise(st, "fdma_rel_bias")
     return out
@@ -346,15 +346,15 @@ def rel_bias(table, Nq, Nk, starts, *, bidirectional=True, offset=None, out=None
     dt = FDMA_FP32 if dt is _FP32 else FDMA_BF16 if dt is _BF16 else None
     if dt is None or len(shape) != 2 or shape[0] != (2 if bidirectional else 1) * len(starts):
         raise ValueError("table must be fp32 or bf16 (buckets, H), with len(starts) buckets (twice as many if bidirectional)")
-    args, keep = _rel_args(shape[1], Nq, Nk, starts, bidirectional, offset)
+    args, first = _rel_args(shape[1], Nq, Nk, starts, bidirectional, offset)
     shape = (1, shape[1], Nq, Nk)
     if out is not None and (out.dtype is not _BF16 or out.shape != shape or (Nk > 1 and out.stride(3) != 1)):
         raise ValueError("out must be bf16 (1, H, Nq, Nk) with contiguous columns")
     guard, sp = _on(dev, stream)
-    return _run(guard, _launch_rel_bias, args, table, dt, out, shape, sp)
+    return _run(guard, _launch_rel_bias, args, first, table, dt, out, shape, sp)
 
 
-def _launch_rel_bias_bwd(args, dbias, causal, dtable, shape, ws, sp):
+def _launch_rel_bias_bwd(args, first, dbias, causal, dtable, shape, ws, sp):
     lib = load()
     st, dev = dbias.stride(), dbias.device
     if dtable is None:
@@ -362,7 +362,7 @@ def _launch_rel_bias_bwd(args, dbias, causal, dtable, shape, ws, sp):
     B = dbias.shape[0]
     if ws is None:
         ws = torch.empty(lib.fdma_rel_bias_bwd_workspace_size(args, B), dtype=torch.uint8, device=dev)
-    st = lib.fdma_rel_bias_bwd(args, B, dbias.data_ptr(), _PACK_3Q(st[0], st[1], st[2]), 1 if causal else 0, dtable.data_ptr(),
+    st = lib.fdma_rel_bias_bwd(args, first, B, dbias.data_ptr(), _PACK_3Q(st[0], st[1], st[2]), 1 if causal else 0, dtable.data_ptr(),
                                ws.data_ptr(), ws.numel() * ws.element_size(), sp)
     if st:
         _fdma._raise(st, "fdma_rel_bias_bwd")
@@ -378,17 +378,17 @@ def rel_bias_bwd(dbias, starts, *, bidirectional=True, offset=None, causal=False
     st, ds = dbias.stride(), dbias.shape
     if dbias.dtype is not _BF16 or len(st) != 4 or (st[3] != 1 and ds[3] > 1):
         raise ValueError("dbias must be bf16 (B, H, Nq, Nk) with contiguous columns")
-    args, keep = _rel_args(ds[1], ds[2], ds[3], starts, bidirectional, offset)
+    args, first = _rel_args(ds[1], ds[2], ds[3], starts, bidirectional, offset)
     shape = ((2 if bidirectional else 1) * len(starts), ds[1])
     if dtable is not None and (dtable.dtype is not _FP32 or dtable.shape != shape or not dtable.is_contiguous()):
         raise ValueError(f"dtable must be contiguous fp32 {shape}")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     guard, sp = _on(dev, stream)
-    return _run(guard, _launch_rel_bias_bwd, args, dbias, causal, dtable, shape, workspace, sp)
+    return _run(guard, _launch_rel_bias_bwd, args, first, dbias, causal, dtable, shape, workspace, sp)
 
 
 def rel_bias_bwd_workspace(B, H, Nq, Nk, starts, *, bidirectional=True, device="cuda"):
     """A workspace for `rel_bias_bwd` of these sizes."""
-    args, keep = _rel_args(H, Nq, Nk, starts, bidirectional, None)
+    args, _ = _rel_args(H, Nq, Nk, starts, bidirectional, None)
     return torch.empty(load().fdma_rel_bias_bwd_workspace_size(args, B), dtype=torch.uint8, device=device)

@@ -93,19 +93,19 @@ FDMA_API int fdma_norm_rope_append(const fdma_norm_rope_args* args, const fdma_k
 
 /* A learned bias by distance: bias[h, i, j] = table[bucket(j - i - offset), h] for query row i at position i + offset
    and key j.  One side (two_sided 0): the bucket of delta is that of the distance max(-delta, 0); two_sided: that of
-   |delta|, plus num_starts where delta > 0.  A distance a is in the last bucket s with starts[s] <= a. */
+   |delta|, plus num_starts where delta > 0.  A distance a is in the last bucket s with starts[s] <= a.  starts is a HOST
+   array of num_starts values, copied by the call: starts[0] = 0, none smaller than the one before. */
 typedef struct fdma_rel_args {
   int32_t H, Nq, Nk;  /* Nq, Nk at most 131072; Nk a multiple of 8 (as fdma_fwd wants it with a bias) */
   int32_t num_starts; /* buckets of a side, at most FDMA_MAX_BUCKETS; the table has them once, or twice if two_sided */
-  const int32_t* starts; /* HOST array: starts[0] = 0, none smaller than the one before; copied by the call */
   int32_t two_sided;
   int32_t offset; /* position of query row 0 in the key sequence; |offset| <= 2^30 */
 } fdma_rel_args;
 
 /* table: (buckets, H) of table_type, element strides table_stride (bucket, head), none negative.  out: (H, Nq, Nk)
    bf16, element strides (head, row), multiples of 8, rows not overlapping, base 16-byte aligned. */
-FDMA_API int fdma_rel_bias(const fdma_rel_args* args, const void* table, int table_type, const int64_t table_stride[2],
-                           void* out, const int64_t out_stride[2], void* stream);
+FDMA_API int fdma_rel_bias(const fdma_rel_args* args, const int32_t* starts, const void* table, int table_type,
+                           const int64_t table_stride[2], void* out, const int64_t out_stride[2], void* stream);
 
 /* Bytes of workspace that fdma_rel_bias_bwd needs for B batches (0: invalid sizes). */
 FDMA_API size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* args, int B);
@@ -116,8 +116,9 @@ FDMA_API size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* args, int 
    16-byte aligned.  causal 1: keys j > i + offset count as zeros, whatever is there, and most of them are not read
    (fdma_bwd writes zeros there for is_causal).  workspace: 256-byte aligned; calls that may run at the same time need one each.  Sums in fp32, the last
    ones in fp64, in a fixed order: the same call gives the same bits. */
-FDMA_API int fdma_rel_bias_bwd(const fdma_rel_args* args, int B, const void* dbias, const int64_t dbias_stride[3],
-                               int causal, float* dtable, void* workspace, size_t workspace_bytes, void* stream);
+FDMA_API int fdma_rel_bias_bwd(const fdma_rel_args* args, const int32_t* starts, int B, const void* dbias,
+                               const int64_t dbias_stride[3], int causal, float* dtable, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -41,8 +41,8 @@ def test_packed_bytes_are_the_structs(I):
     assert (a.rope, a.rope_len, a.rot, a.interleaved, a.first, a.positions, list(a.pos_stride)) == (13, 14, 15, 16, 17, 18, [19, 20])
     r = I.FdmaRows.from_buffer_copy(I._PACK_ROWS(1, 2, 3, 4))
     assert (r.p, list(r.stride)) == (1, [2, 3, 4])
-    s = I.FdmaRelArgs.from_buffer_copy(I._PACK_REL(1, 2, 3, 4, 5, 6, -7))
-    assert (s.H, s.Nq, s.Nk, s.num_starts, s.starts, s.two_sided, s.offset) == (1, 2, 3, 4, 5, 6, -7)
+    s = I.FdmaRelArgs.from_buffer_copy(I._PACK_REL(1, 2, 3, 4, 5, -6))
+    assert (s.H, s.Nq, s.Nk, s.num_starts, s.two_sided, s.offset) == (1, 2, 3, 4, 5, -6)
     assert ctypes.sizeof(I.FdmaNormRopeArgs) == len(I._PACK_NORM_ROPE(*[0] * 6, 0.0, *[0] * 13))
 
 
@@ -156,33 +156,37 @@ def test_append_arguments_are_refused(I):
     assert f(ok, _cache(P, B=0), None, None, None, None, None, None) == 0
 
 
-def _rel(I, firsts=(0, 1, 2, 4), **kw):
+STARTS = struct.pack("4i", 0, 1, 2, 4)
+
+
+def _rel(I, **kw):
     a = I.FdmaRelArgs()
-    keep = (ctypes.c_int32 * len(firsts))(*firsts)
-    a.H, a.Nq, a.Nk, a.num_starts, a.starts, a.two_sided, a.offset = 2, 16, 24, len(firsts), ctypes.addressof(keep), 0, 8
+    a.H, a.Nq, a.Nk, a.num_starts, a.two_sided, a.offset = 2, 16, 24, 4, 0, 8
     for k, v in kw.items():
         setattr(a, k, v)
-    return bytes(a), keep
+    return bytes(a)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(H=0), 1), (dict(Nq=-1), 1), (dict(Nk=-8), 1), (dict(num_starts=0), 1), (dict(starts=None), 1), (dict(two_sided=2), 1),
+    (dict(H=0), 1), (dict(Nq=-1), 1), (dict(Nk=-8), 1), (dict(num_starts=0), 1), (dict(two_sided=2), 1),
     (dict(offset=(1 << 30) + 1), 1), (dict(offset=-(1 << 30) - 1), 1), (dict(Nk=25), 2), (dict(Nq=131073), 2),
-    (dict(Nk=131080), 2), (dict(H=(1 << 20) + 1), 2), (dict(num_starts=257), 2), (dict(start=(1, 2)), 1), (dict(start=(0, 3, 2)), 1),
+    (dict(Nk=131080), 2), (dict(H=(1 << 20) + 1), 2), (dict(num_starts=257), 2),
 ])
 def test_bias_arguments_are_refused(I, kw, status):
     lib, two, three = I.load(), struct.pack("2q", 2, 1), struct.pack("2q", 384, 24)
-    kw = dict(kw)
-    a, keep = _rel(I, kw.pop("start", (0, 1, 2, 4)), **kw)
-    assert lib.fdma_rel_bias(a, FAKE, 0, two, FAKE, three, None) == status
-    assert lib.fdma_rel_bias_bwd(a, 1, FAKE, struct.pack("3q", 768, 384, 24), 0, FAKE, FAKE, 1 << 40, None) == status
+    a = _rel(I, **kw)
+    assert lib.fdma_rel_bias(a, STARTS, FAKE, 0, two, FAKE, three, None) == status
+    assert lib.fdma_rel_bias_bwd(a, STARTS, 1, FAKE, struct.pack("3q", 768, 384, 24), 0, FAKE, FAKE, 1 << 40, None) == status
     assert lib.fdma_rel_bias_bwd_workspace_size(a, 1) == 0
 
 
 def test_bias_buffers_are_checked(I):
-    lib, (a, keep), ts = I.load(), _rel(I), struct.pack("2q", 2, 1)
+    lib, a, ts = I.load(), _rel(I), struct.pack("2q", 2, 1)
     out = lambda h, r: struct.pack("2q", h, r)  # noqa: E731
-    f = lib.fdma_rel_bias
+    f = lambda a, *rest: lib.fdma_rel_bias(a, STARTS, *rest)  # noqa: E731
+    for bad in (None, struct.pack("4i", 1, 2, 3, 4), struct.pack("4i", 0, 3, 2, 4)):
+        assert lib.fdma_rel_bias(a, bad, FAKE, 0, ts, FAKE, out(384, 24), None) == 1
+        assert lib.fdma_rel_bias_bwd(a, bad, 1, FAKE, struct.pack("3q", 768, 384, 24), 0, FAKE, FAKE, 1 << 40, None) == 1
     assert f(a, None, 0, ts, FAKE, out(384, 24), None) == 1
     assert f(a, FAKE, 2, ts, FAKE, out(384, 24), None) == 1
     assert f(a, FAKE, 0, struct.pack("2q", -1, 1), FAKE, out(384, 24), None) == 1
@@ -191,9 +195,10 @@ def test_bias_buffers_are_checked(I):
     for h, r, status in ((0, 24, 1), (384, 16, 1), (380, 24, 1), (384, 28, 1), (388, 24, 2), (392, 24, 0), (24, 48, 0), (24, 40, 1)):
         if status:  # (those that are allowed are not launched here)
             assert f(a, FAKE, 0, ts, FAKE, out(h, r), None) == status, (h, r)
-    assert f(_rel(I, Nq=0)[0], FAKE, 0, ts, None, out(0, 0), None) == 0
-    assert f(_rel(I, Nk=0)[0], FAKE, 0, ts, None, out(0, 0), None) == 0
-    g, ds = lib.fdma_rel_bias_bwd, struct.pack("3q", 768, 384, 24)
+    assert f(_rel(I, Nq=0), FAKE, 0, ts, None, out(0, 0), None) == 0
+    assert f(_rel(I, Nk=0), FAKE, 0, ts, None, out(0, 0), None) == 0
+    g = lambda a, *rest: lib.fdma_rel_bias_bwd(a, STARTS, *rest)  # noqa: E731
+    ds = struct.pack("3q", 768, 384, 24)
     need = lib.fdma_rel_bias_bwd_workspace_size(a, 2)
     assert need > 0 and lib.fdma_rel_bias_bwd_workspace_size(a, 0) == 0 and lib.fdma_rel_bias_bwd_workspace_size(a, -1) == 0
     assert g(a, -1, FAKE, ds, 0, FAKE, FAKE, need, None) == 1
