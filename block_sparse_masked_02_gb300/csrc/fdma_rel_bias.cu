@@ -10,8 +10,8 @@
 // only at the end of the walk.  A band is the 32 neighbouring diagonals of blocks that a warp walks along; its block rows
 // are dealt out to `parts` warps in turn (warp p takes p, p + parts, ...), so that all warps sweep
 // over the matrix together and DRAM sees neighbouring rows.  A CTA's warps have eight parts of a band; it
-// joins their sums, adds up the diagonals of each bucket in a fixed order and writes one number for each bucket
-// that the band touches.  A second kernel adds those.
+// joins their sums and writes one number where the whole band is in one bucket, as far from the diagonal nearly all are,
+// else the sums of the band's diagonals.  A second kernel adds what each bucket has of those, in a fixed order.
 #include <type_traits>
 
 #include "../../include/fdma_inputs.h"
@@ -24,6 +24,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxLen = 131072;  // as fdma_fwd's
 constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
+constexpr int kPart = 264;
 constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
 
 // CAP: most buckets of a side.  (A launch copies the arguments: with 256 it takes 2 us more on the host than with 32.)
@@ -138,7 +139,7 @@ struct BwdView {
   int bands, parts;  // bands with anything in them; parts is a multiple of 8
   const uint16_t* db;
   int64_t ds[3];
-  float* part;  // [cta][bucket]: the sums of the buckets that the band has
+  float* part;  // [cta][kPart]: the sums of the band's diagonals, or the sum of all of them where they are in one bucket
   float* dtable;
 };
 
@@ -182,7 +183,8 @@ __device__ __forceinline__ float warp_sum(float x) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView<CAP> p) {
   __shared__ float diag[kWarps][kSpan + 1];
-  __shared__ float all[kSpan + 1];
+  __shared__ float sums[kWarps];
+  __shared__ int one_bucket;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the bands from right to left: a causal matrix's longest ones come first
   const uint32_t u = blockIdx.x / p.bands, groups = p.parts / kWarps;
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_
   const int h = static_cast<int>(hb / p.B), b = static_cast<int>(hb - h * p.B);
   const Deltas d = band_deltas(p, band);
   const int nrb = p.r.row_blocks(), ncb = p.r.Nk >> 3, db0 = 32 * band - (nrb - 1), db = db0 + lane;
+  if (threadIdx.x == 0) one_bucket = p.r.bucket(d.lo) == p.r.bucket(d.hi);
   float acc[15];
 #pragma unroll
   for (int i = 0; i < 15; ++i) acc[i] = 0.f;
@@ -234,63 +237,87 @@ __global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_
 #pragma unroll
   for (int i = 0; i < 7; ++i) x[8 * lane + i] += acc[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < kSpan; i += kThreads) {
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * kPart;
+  const bool one = one_bucket;
+  float total = 0.f;
+  for (int i = threadIdx.x; i <= d.hi - d.lo; i += kThreads) {  // (diagonals behind d.hi may hold anything)
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) s += diag[j][i];
-    all[i] = s;
+    total += s;
+    if (!one) out[i] = s;
   }
+  if (!one) return;
+  total = warp_sum(total);
+  if (lane == 0) sums[warp] = total;
   __syncthreads();
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * p.r.buckets();
-  // the buckets of the band, dealt out over the warps (diagonals behind d.hi belong to none: they may hold anything)
-  auto add_bucket = [&](int k) {
-    const Deltas q = bucket_deltas(p.r, k);
-    const int from = max(q.lo, d.lo) - d.lo, to = min(q.hi, d.hi) - d.lo;
-    if (from > to) return;
-    float s = 0.f;
-    for (int i = from + lane; i <= to; i += 32) s += all[i];
-    s = warp_sum(s);
-    if (lane == 0) out[k] = s;
-  };
-  if (d.lo <= 0) {
-    const int last = p.r.side(-d.lo);
-    for (int k = p.r.side(max(-d.hi, 0)) + warp; k <= last; k += kWarps) add_bucket(k);
-  } else if (!p.r.two_sided && warp == 0) {
-    add_bucket(p.r.side(0));
-  }
-  if (d.hi > 0 && p.r.two_sided) {
-    const int last = p.r.side(d.hi);
-    for (int k = p.r.side(max(d.lo, 1)) + warp; k <= last; k += kWarps) add_bucket(p.r.n + k);
-  }
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int j = 1; j < kWarps; ++j) total += sums[j];
+  out[0] = total;
 }
 
 // Adds the CTAs' sums of one bucket and head.
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView<CAP> p) {
-  __shared__ double s[kWarps];
+  __shared__ float s[kWarps];
   const int k = blockIdx.x % p.r.buckets(), h = blockIdx.x / p.r.buckets();
   const Deltas q = bucket_deltas(p.r, k);
   // the bands that have some of it
   const int64_t base = first_delta(p.r), hi = p.causal ? min(q.hi, 0) : q.hi;
-  const int64_t lo_band = max(int64_t{0}, (max(static_cast<int64_t>(q.lo), base) - base - (kSpan - 1) + 255) / 256);
-  const int64_t hi_band = hi < base ? -1 : min(static_cast<int64_t>(p.bands - 1), (hi - base) / 256);
-  double sum = 0.;
+  const int lo_band = static_cast<int>(max(int64_t{0}, (max(static_cast<int64_t>(q.lo), base) - base - (kSpan - 1) + 255) / 256));
+  const int hi_band = hi < base ? -1 : static_cast<int>(min(static_cast<int64_t>(p.bands - 1), (hi - base) / 256));
+  float sum = 0.f;
   if (q.lo <= hi && lo_band <= hi_band) {
-    const uint32_t n = static_cast<uint32_t>(hi_band - lo_band + 1);
-    const int64_t first = static_cast<int64_t>(h) * p.B * (p.parts / kWarps), count = n * static_cast<int64_t>(p.B) * (p.parts / kWarps);
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-      const int64_t u = i / n;
-      const int64_t cta = (first + u) * p.bands + (p.bands - 1 - (lo_band + (i - u * n)));
-      sum += p.part[cta * p.r.buckets() + k];
+    const uint32_t shares = static_cast<uint32_t>(p.B) * (p.parts / kWarps);  // CTAs of a band
+    const float* part = p.part + static_cast<int64_t>(h) * shares * p.bands * kPart;
+    auto of = [&](uint32_t u, int band) { return part + (static_cast<int64_t>(u) * p.bands + (p.bands - 1 - band)) * kPart; };
+    // those that it has whole, all but one or two at either end, give a number each, the others the diagonals that it has;
+    // all in one line, so that a thread's loads run together
+    int first = lo_band, last = hi_band;
+    auto whole = [&](int band) {
+      const Deltas d = band_deltas(p, band);
+      return d.lo >= q.lo && d.hi <= q.hi;
+    };
+    while (first <= last && !whole(first)) ++first;
+    while (last >= first && !whole(last)) --last;
+    const int left = first - lo_band, edges = left + (hi_band - last);
+    uint32_t n[5] = {static_cast<uint32_t>(last - first + 1), 0, 0, 0, 0}, end[5];
+    int band[5] = {first, 0, 0, 0, 0}, from[5] = {0, 0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 5; ++e) {
+      if (e > 0 && e <= edges) {
+        band[e] = e <= left ? lo_band + e - 1 : last + e - left;
+        const Deltas d = band_deltas(p, band[e]);
+        from[e] = max(q.lo, d.lo) - d.lo;
+        n[e] = static_cast<uint32_t>(min(q.hi, d.hi) - d.lo - from[e] + 1);
+      }
+      end[e] = (e > 0 ? end[e - 1] : 0u) + n[e] * shares;
+    }
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < end[4]; i += kThreads) {
+      uint32_t begin = 0, m = n[0];
+      int at = band[0], off = -1;
+#pragma unroll
+      for (int e = 1; e < 5; ++e) {
+        if (i >= end[e - 1]) {
+          begin = end[e - 1];
+          m = n[e];
+          at = band[e];
+          off = from[e];
+        }
+      }
+      const uint32_t u = (i - begin) / m;
+      const int x = static_cast<int>(i - begin - u * m);
+      sum += off < 0 ? *of(u, at + x) : of(u, at)[off + x];
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  sum = warp_sum(sum);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = sum;
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int j = 1; j < kWarps; ++j) sum += s[j];
-  p.dtable[static_cast<int64_t>(k) * p.r.H + h] = static_cast<float>(sum);
+  p.dtable[static_cast<int64_t>(k) * p.r.H + h] = sum;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -398,7 +425,7 @@ int fdma_rel_bias(const fdma_rel_args* a, const int32_t* starts, const void* tab
 size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* a, int B) {
   if (validate(a) != FDMA_OK || B <= 0 || B > (1 << 20) || a->Nq == 0 || a->Nk == 0) return 0;
   const BwdPlan plan = bwd_plan(*a, B, false);
-  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * (a->two_sided ? 2 : 1) * a->num_starts * sizeof(float);
+  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * kPart * sizeof(float);
 }
 
 int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, const void* dbias, const int64_t ds[3], int causal,
@@ -424,7 +451,7 @@ int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, cons
   const BwdPlan whole = bwd_plan(*a, B, false), plan = bwd_plan(*a, B, causal != 0);
   if (whole.ctas > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
-      workspace_bytes < static_cast<size_t>(whole.ctas) * buckets * sizeof(float))
+      workspace_bytes < static_cast<size_t>(whole.ctas) * kPart * sizeof(float))
     return FDMA_ERR_WORKSPACE;
   return with_cap(a->num_starts, [&](auto cap) {
     BwdView<decltype(cap)::value> p;

@@ -114,8 +114,8 @@ FDMA_API size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* args, int 
      dtable[s, h] = sum of dbias[b, h, i, j] over b and the (i, j) in bucket s.
    dbias: (B, H, Nq, Nk) bf16, element strides (batch, head, row), multiples of 8, none negative (0 repeats), base
    16-byte aligned.  causal 1: keys j > i + offset count as zeros, whatever is there, and most of them are not read
-   (fdma_bwd writes zeros there for is_causal).  workspace: 256-byte aligned; calls that may run at the same time need one each.  Sums in fp32, the last
-   ones in fp64, in a fixed order: the same call gives the same bits. */
+   (fdma_bwd writes zeros there for is_causal).  workspace: 256-byte aligned; calls that may run at the same time need one each.  Sums in fp32, in a
+   fixed order: the same call gives the same bits. */
 FDMA_API int fdma_rel_bias_bwd(const fdma_rel_args* args, const int32_t* starts, int B, const void* dbias,
                                const int64_t dbias_stride[3], int causal, float* dtable, void* workspace,
                                size_t workspace_bytes, void* stream);

@@ -10,9 +10,9 @@ dx by twice all that and its few products: (2 d + 64) u M, then 2^-8 for bf16.  
 off by (d / 2 + 14) u through the steps of a slot, the slots of a CTA and the CTAs' parts: at these sizes fewer than 256
 additions in a row, so (d + 300) u of the sum of magnitudes.
 
-The bias is table values rounded once, so it is compared by bits.  Its table's gradient adds at most 512 + 8 values of a
-diagonal, 15 diagonals or 9 of a bucket and 5 levels of a warp in fp32, the rest in fp64, and is rounded once: 600 u of the
-sum of magnitudes.  Half of bf16's least step, 2^-134, is added to every bound of a bf16 value.
+The bias is table values rounded once, so it is compared by bits.  Its table's gradient adds, in fp32 and one after the
+other, at most 8 values of each of at most 33 blocks of a diagonal, 2 neighbouring lanes', 8 warps', 2 diagonals of a thread
+and 5 + 8 in a CTA, and then at most 100 CTAs' and 5 + 8 again at these sizes: 600 u of the sum of magnitudes.  Half of bf16's least step, 2^-134, is added to every bound of a bf16 value.
 """
 import numpy as np
 import pytest
