@@ -91,6 +91,9 @@ def load() -> ctypes.CDLL:
 _BF16, _FP32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
+# A call's own workspace comes from the caching allocator without a tensor around it, which would cost 3 us.
+_raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_raw_delete = torch._C._cuda_cudaCachingAllocator_raw_delete
 
 
 def _check_device(first, *ts):
@@ -246,18 +249,24 @@ def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweig
         if dk is None:
             dk = _like(k)
         kr, kg, ko = _rows("k", k), _rows("dk_out", dk_out, k.shape), _rows("dk", dk, k.shape)
-    n = wp = 0
+    n = wp = own = 0
     if want_dweight:
         dw = [torch.empty_like(w, dtype=_FP32, memory_format=torch.contiguous_format) if t is None and w is not None else t
               for w, t in zip(weights, dw)]
         if dw[0] is not None or dw[1] is not None:
             if ws is None:
-                ws = torch.empty(lib.fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=q.device)
-            wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
+                n = lib.fdma_norm_rope_bwd_workspace_size(args)
+            else:
+                wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
     else:
         dw = (None, None)
-    st = lib.fdma_norm_rope_bwd(args, _rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, _rows("dq", dq, q.shape), ko,
-                                None if dw[0] is None else dw[0].data_ptr(), None if dw[1] is None else dw[1].data_ptr(), wp, n, sp)
+    rows = (_rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, _rows("dq", dq, q.shape), ko)
+    if n and ws is None:
+        wp = own = _raw_alloc(n, sp)
+    st = lib.fdma_norm_rope_bwd(args, *rows, None if dw[0] is None else dw[0].data_ptr(),
+                                None if dw[1] is None else dw[1].data_ptr(), wp, n, sp)
+    if own:  # (what is allocated next on this stream runs behind the kernels)
+        _raw_delete(own)
     if st:
         _fdma._raise(st, "fdma_norm_rope_bwd")
     return dq, None if k is None else dk, dw[0], dw[1]
@@ -356,14 +365,19 @@ def rel_bias(table, Nq, Nk, starts, *, bidirectional=True, offset=None, out=None
 
 def _launch_rel_bias_bwd(args, first, dbias, causal, dtable, shape, ws, sp):
     lib = load()
-    st, dev = dbias.stride(), dbias.device
+    st = dbias.stride()
     if dtable is None:
-        dtable = torch.empty(shape, dtype=_FP32, device=dev)
-    B = dbias.shape[0]
+        dtable = torch.empty(shape, dtype=_FP32, device=dbias.device)
+    B, own = dbias.shape[0], 0
     if ws is None:
-        ws = torch.empty(lib.fdma_rel_bias_bwd_workspace_size(args, B), dtype=torch.uint8, device=dev)
+        n = lib.fdma_rel_bias_bwd_workspace_size(args, B)
+        wp = own = _raw_alloc(n, sp) if n else 0
+    else:
+        wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
     st = lib.fdma_rel_bias_bwd(args, first, B, dbias.data_ptr(), _PACK_3Q(st[0], st[1], st[2]), 1 if causal else 0, dtable.data_ptr(),
-                               ws.data_ptr(), ws.numel() * ws.element_size(), sp)
+                               wp, n, sp)
+    if own:  # (what is allocated next on this stream runs behind the kernels)
+        _raw_delete(own)
     if st:
         _fdma._raise(st, "fdma_rel_bias_bwd")
     return dtable
