@@ -293,17 +293,34 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
   const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
   const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
   r.per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
-  int64_t cost = 0;  // of a token, the last chunks counted as whole ones
+  // A token costs a chunk its passes and two thirds of one for what is done once (190 of 284 instructions, backward; the last
+  // chunk counts as a whole one).  CTAs go by that, and, as a warp has whole tokens, by which of the two whole numbers
+  // next to the even share of q's leaves less to the last warp of either.
+  int64_t cost[2], all = 0;
   for (int s = 0; s < 2; ++s) {
     r.chunks[s] = (q[s] + r.per - 1) / r.per;
-    cost += static_cast<int64_t>(r.chunks[s]) * (q[s] < r.per ? q[s] : r.per);
+    cost[s] = 3 * (q[s] < r.per ? q[s] : r.per) + 2;
+    all += r.chunks[s] * cost[s];
   }
-  const int64_t most = (tokens + kWarps - 1) / kWarps;
-  for (int s = 0; s < 2; ++s) {
-    const int64_t n = ctas * static_cast<int64_t>(q[s] < r.per ? q[s] : r.per) / cost;
-    r.ctas[s] = static_cast<int>(n < 1 ? 1 : n > most ? most : n);
-    r.grid += r.chunks[s] * r.ctas[s];
+  auto share = [&](int64_t n) {  // tokens of a warp of n CTAs
+    return (tokens + n * kWarps - 1) / (n * kWarps);
+  };
+  auto least = [&](int64_t t) {  // CTAs whose warps have at most t
+    return (tokens + t * kWarps - 1) / (t * kWarps);
+  };
+  const int64_t even = ctas * cost[0] / all, up = share(even < 1 ? 1 : even);
+  int64_t best = -1;
+  for (int64_t t = up; t >= 1 && t >= up - 1; --t) {
+    const int64_t n = least(t), rest = r.chunks[1] > 0 ? (ctas - n * r.chunks[0]) / r.chunks[1] : 1;
+    if (t < up && (rest < 1 || n * r.chunks[0] > ctas)) continue;  // (the first one is taken whatever there is)
+    const int64_t m = r.chunks[1] > 0 ? least(share(rest < 1 ? 1 : rest)) : 0;
+    const int64_t last = r.chunks[1] > 0 && share(m) * cost[1] > t * cost[0] ? share(m) * cost[1] : t * cost[0];
+    if (best >= 0 && last >= best) continue;
+    best = last;
+    r.ctas[0] = static_cast<int>(n);
+    r.ctas[1] = static_cast<int>(m);
   }
+  r.grid = r.chunks[0] * r.ctas[0] + r.chunks[1] * r.ctas[1];
   r.rows = by_head(a) ? r.per * rpw : 1;
   r.part_bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
   return r;
