@@ -120,10 +120,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   const uint16_t *x_next = nullptr, *g_next = nullptr;
   auto start = [&](int slot) {
     if (q_next == q_last && tok_next < p.line.tokens) {
-      const int pos = checked_position(p.v, pos_next, p.err);
-      const uint32_t bit = 1u << (begun & 31u);
-      left_out = pos < 0 ? left_out | bit : left_out & ~bit;
-      ++begun;
+      int pos = pos_next;
+      if (p.v.pos != nullptr) {  // (else they are inside the table)
+        pos = checked_position(p.v, pos, p.err);
+        const uint32_t bit = 1u << (begun & 31u);
+        left_out = pos < 0 ? left_out | bit : left_out & ~bit;
+        ++begun;
+      }
       __syncwarp();  // (these angles may take the place of those that were read last)
       if (pos >= 0) {
         const float* angles = p.v.rope + static_cast<int64_t>(pos) * p.v.rot;
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
     row = row == SLOTS ? 0 : row + 1;
-    ++done;
+    if (p.v.pos != nullptr) ++done;
     now.n += step;
     wrap(p.line, now);
   }

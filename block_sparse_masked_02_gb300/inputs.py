@@ -135,18 +135,26 @@ def _rows(name, t, shape=None):
     return _PACK_ROWS(t.data_ptr(), st[0], st[1], st[2]) if n == 4 else _PACK_ROWS(t.data_ptr(), 0, st[0], st[1])
 
 
+def _new_rows(like):
+    """An uninitialised contiguous tensor of a tensor's shape, and its fdma_rows."""
+    t = torch.empty_like(like, memory_format=torch.contiguous_format)
+    shape = t.shape
+    hd = shape[-2] * shape[-1]
+    return t, _PACK_ROWS(t.data_ptr(), shape[-3] * hd, hd, shape[-1])
+
+
 def _weight(name, w, H, d):
     """(pointer, head stride, type) of a weight (d) or (H, d)."""
-    dt = w.dtype
+    dt, shape = w.dtype, w.shape
     dt = FDMA_FP32 if dt is _FP32 else FDMA_BF16 if dt is _BF16 else None
-    shape, st = w.shape, w.stride()
-    if dt is None or shape[-1:] != (d,) or st[-1] != 1 or (len(shape) != 1 and shape != (H, d)):
-        raise ValueError(f"{name} must be fp32 or bf16, ({d},) or ({H}, {d}), with a contiguous last dimension")
     if len(shape) == 1:
-        return w.data_ptr(), 0, dt
-    if H > 1 and st[0] < d:
-        raise ValueError(f"the heads of {name} must not overlap")
-    return w.data_ptr(), max(st[0], d), dt
+        if dt is not None and shape[0] == d and w.stride(0) == 1:
+            return w.data_ptr(), 0, dt
+    elif dt is not None and shape == (H, d):
+        head, one = w.stride()
+        if one == 1 and (H == 1 or head >= d):
+            return w.data_ptr(), max(head, d), dt
+    raise ValueError(f"{name} must be fp32 or bf16, ({d},) or ({H}, {d}), its heads apart and contiguous")
 
 
 def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps):
@@ -162,7 +170,7 @@ def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleave
     if k is not None:
         ks = k.shape
         Hk = ks[-2]
-        if ks[-1] != d or ks[:-2] != shape[:-2]:
+        if ks != ((B, N, Hk, d) if len(shape) == 4 else (N, Hk, d)):
             raise ValueError("k must have the tokens and the head dim of q")
     elif k_weight is not None:
         raise ValueError("a weight for keys without keys")
@@ -193,11 +201,6 @@ def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleave
                            1 if interleaved else 0, first, pp, sb, sn)
 
 
-def _like(t):
-    """An uninitialised contiguous tensor of t's shape."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
-
-
 def rope_table(length, rot, *, base=10000.0, device="cuda"):
     """The table that `norm_rope` takes: fp32 (length, 2, rot / 2), cosines and sines of p * base ** (-2 i / rot), formed in
     64 bits (in 32, the angles of far positions lose what matters)."""
@@ -207,19 +210,23 @@ def rope_table(length, rot, *, base=10000.0, device="cuda"):
 
 
 def _launch_norm_rope(args, q, k, q_out, k_out, sp):
-    qr = _rows("q", q)
-    if q_out is None:
-        q_out = _like(q)
     kr = kor = None
+    if q_out is None:
+        q_out, qor = _new_rows(q)
+    else:
+        qor = _rows("q_out", q_out, q.shape)
     if k is not None:
         kr = _rows("k", k)
         if k_out is None:
-            k_out = _like(k)
-        kor = _rows("k_out", k_out, k.shape)
-    st = load().fdma_norm_rope(args, qr, kr, _rows("q_out", q_out, q.shape), kor, sp)
+            k_out, kor = _new_rows(k)
+        else:
+            kor = _rows("k_out", k_out, k.shape)
+    else:
+        k_out = None
+    st = load().fdma_norm_rope(args, _rows("q", q), kr, qor, kor, sp)
     if st:
         _fdma._raise(st, "fdma_norm_rope")
-    return q_out, None if k is None else k_out
+    return q_out, k_out
 
 
 def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=None, first=0, interleaved=False, norm=True,
@@ -242,13 +249,19 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=N
 def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweight, ws, sp):
     lib = load()
     dq, dk, *dw = grads
-    if dq is None:
-        dq = _like(q)
     kr = kg = ko = None
+    if dq is None:
+        dq, qo = _new_rows(q)
+    else:
+        qo = _rows("dq", dq, q.shape)
     if k is not None:
         if dk is None:
-            dk = _like(k)
-        kr, kg, ko = _rows("k", k), _rows("dk_out", dk_out, k.shape), _rows("dk", dk, k.shape)
+            dk, ko = _new_rows(k)
+        else:
+            ko = _rows("dk", dk, k.shape)
+        kr, kg = _rows("k", k), _rows("dk_out", dk_out, k.shape)
+    else:
+        dk = None
     n = wp = own = 0
     if want_dweight:
         dw = [torch.empty_like(w, dtype=_FP32, memory_format=torch.contiguous_format) if t is None and w is not None else t
@@ -260,7 +273,7 @@ def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweig
                 wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
     else:
         dw = (None, None)
-    rows = (_rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, _rows("dq", dq, q.shape), ko)
+    rows = (_rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, qo, ko)
     if n and ws is None:
         wp = own = _raw_alloc(n, sp)
     st = lib.fdma_norm_rope_bwd(args, *rows, None if dw[0] is None else dw[0].data_ptr(),
@@ -269,7 +282,7 @@ def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweig
         _raw_delete(own)
     if st:
         _fdma._raise(st, "fdma_norm_rope_bwd")
-    return dq, None if k is None else dk, dw[0], dw[1]
+    return dq, dk, dw[0], dw[1]
 
 
 def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=None, positions=None, first=0,

@@ -190,8 +190,10 @@ def _launch_norm_rope_append(args, c, q, k, v, q_out, cu_q, sp):
     rows = _inputs._rows
     qr, kr, vr = rows("q", q), rows("k", k), rows("v", v)
     if q_out is None:
-        q_out = _inputs._like(q)
-    st = _inputs.load().fdma_norm_rope_append(args, _PACK_CACHE(*c), qr, kr, vr, rows("q_out", q_out, q.shape), cu_q.data_ptr(), sp)
+        q_out, qor = _inputs._new_rows(q)
+    else:
+        qor = rows("q_out", q_out, q.shape)
+    st = _inputs.load().fdma_norm_rope_append(args, _PACK_CACHE(*c), qr, kr, vr, qor, cu_q.data_ptr(), sp)
     if st:
         _fdma._raise(st, "fdma_norm_rope_append")
     return q_out
