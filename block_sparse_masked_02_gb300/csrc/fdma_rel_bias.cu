@@ -25,6 +25,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxLen = 131072;  // as fdma_fwd's
 constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
 constexpr int kPart = 264;
+constexpr int64_t kMostCtas = 1 << 28;  // of a backward (their parts take 283 GB)
 constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
 
 // CAP: most buckets of a side.  (A launch copies the arguments: with 256 it takes 2 us more on the host than with 32.)
@@ -425,7 +426,7 @@ int fdma_rel_bias(const fdma_rel_args* a, const int32_t* starts, const void* tab
 size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* a, int B) {
   if (validate(a) != FDMA_OK || B <= 0 || B > (1 << 20) || a->Nq == 0 || a->Nk == 0) return 0;
   const BwdPlan plan = bwd_plan(*a, B, false);
-  return plan.ctas > 0x7fffffff ? 0 : static_cast<size_t>(plan.ctas) * kPart * sizeof(float);
+  return plan.ctas > kMostCtas ? 0 : static_cast<size_t>(plan.ctas) * kPart * sizeof(float);
 }
 
 int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, const void* dbias, const int64_t ds[3], int causal,
@@ -449,7 +450,7 @@ int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, cons
   }
   if (!aligned16(dbias)) return FDMA_ERR_UNSUPPORTED;
   const BwdPlan whole = bwd_plan(*a, B, false), plan = bwd_plan(*a, B, causal != 0);
-  if (whole.ctas > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
+  if (whole.ctas > kMostCtas) return FDMA_ERR_UNSUPPORTED;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < static_cast<size_t>(whole.ctas) * kPart * sizeof(float))
     return FDMA_ERR_WORKSPACE;

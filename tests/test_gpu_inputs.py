@@ -636,6 +636,86 @@ def test_bias_refusals(I):
         I.rel_bias_bwd(db, (0, 1), workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
 
 
+# ------------------------------------------------------------------------------------------------ many shapes
+@pytest.mark.parametrize("seed", range(24))
+def test_random_rows(I, seed):
+    """Random sizes, layouts and options; rows that a warp's walk, a chunk of heads or a pass does not divide."""
+    r = np.random.default_rng(1000 + seed)
+    d = int(r.integers(1, 33)) * 8
+    rot = int(r.integers(0, d // 8 + 1)) * 8
+    B, N = int(r.integers(1, 5)), int(2 ** r.uniform(0, 9))
+    Hq, Hk = int(r.integers(1, 12)), int(r.integers(0, 6))
+    weight = [None, "shared", "head"][seed % 3]
+    inter = bool(r.integers(0, 2))
+    c = Case(I, B, N, Hq, Hk, d, rot, weight, [torch.float32, torch.bfloat16][seed % 2], length=N + 7, seed=seed)
+    pos = None
+    kw = dict(interleaved=inter, **c.kw)
+    if r.integers(0, 2):
+        pos = r.integers(-2, N + 7, (B, N))
+        kw["positions"] = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    _check_forward(c, I.norm_rope(c.q, c.k, **kw), inter, pos=pos)
+    grads = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **kw)
+    _check_backward(c, grads, inter, pos=pos)
+
+
+def test_walks_of_many_tokens(I):
+    """More than 32 tokens for every warp, some of them padding, of one and of many batches."""
+    for B, N, Hq, Hk in ((1, 150000, 1, 1), (50000, 3, 1, 0)):
+        c = Case(I, B, N, Hq, Hk, 16, 8, "shared", length=500, seed=N)
+        pos = np.random.default_rng(N).integers(-100, 500, (B, N))
+        pt = torch.tensor(pos, dtype=torch.int32, device="cuda")
+        _check_forward(c, I.norm_rope(c.q, c.k, positions=pt, **c.kw), pos=pos)
+        cos, sin = c.turns(pos)
+        keep = (pos >= 0)[..., None, None]
+        grads = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, positions=pt, **c.kw)
+        for x, do, w, got, gw in zip((c.q, c.k), (c.dq, c.dk), c.w, grads[:2], grads[2:]):
+            if x is None:
+                continue
+            ref, mag, dw, dwm = orc.norm_rope_bwd(np.where(keep, _np(x), 0), np.where(keep, _np(do), 0), _np(w), cos, sin, False, True, 1e-6)
+            _check_rows(got, ref, mag, 16, back=True)
+            # (every one of a slot's up to 100 tokens and of up to 152 CTAs one after the other)
+            assert (np.abs(_np(gw) - dw.sum(0)) <= (16 + 700) * U * dwm.sum(0)).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_of_many_tokens(I, fp8):
+    """So many that a warp takes whole tokens, with an empty sequence, a sequence of one and rows behind the last."""
+    s = Serving(I, [3000, 0, 1, 2100], [5, 9, 63, 640], 3, 2, 32, 64, fp8, rot=16, extra=9, seed=3)
+    got = s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, **s.kw, **s.ex)
+    (qr, qm), (kr, km) = s.exact()
+    n = 5101
+    _check_rows(got[:n], qr[:n], qm[:n], 32)
+    pg, sl = (torch.tensor(x, device="cuda") for x in s.slots())
+    if fp8:
+        vcode, vexp = porc.quantise(_np(s.v[:n]))
+        assert np.array_equal(s.vc.view(torch.uint8)[pg, sl].cpu().numpy(), vcode)
+        assert np.array_equal(s.ve[pg, sl].cpu().numpy(), vexp)
+    else:
+        _check_rows(s.kc[pg, sl], kr[:n], km[:n], 32)
+        assert torch.equal(s.vc[pg, sl], s.v[:n])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_biases(I, seed):
+    r = np.random.default_rng(2000 + seed)
+    H, B = int(r.integers(1, 5)), int(r.integers(1, 4))
+    Nq, Nk = int(2 ** r.uniform(0, 10)), 8 * int(2 ** r.uniform(0, 7))
+    two = bool(seed % 2)
+    n = int(r.integers(1, 257 if seed % 5 == 0 else 40))
+    starts = (0,) + tuple(int(x) for x in np.sort(r.integers(0, int(2 ** r.uniform(1, 11)), n - 1)))
+    offset = None if r.integers(0, 2) else int(r.integers(-700, 700))
+    off = Nk - Nq if offset is None else offset
+    table = torch.tensor(r.standard_normal((n * (2 if two else 1), H)), dtype=torch.float32, device="cuda")
+    at = torch.tensor(orc.buckets(Nq, Nk, starts, two, off), device="cuda")
+    got = I.rel_bias(table, Nq, Nk, starts, bidirectional=two, offset=offset)
+    assert torch.equal(got, table.bfloat16()[at].permute(2, 0, 1)[None])
+    db = torch.tensor(r.standard_normal((B, H, Nq, Nk)), dtype=torch.bfloat16, device="cuda")
+    for causal in (False, True):
+        ref, mag = orc.rel_bias_bwd(_np(db), starts, two, off, causal)
+        g = I.rel_bias_bwd(db, starts, bidirectional=two, offset=offset, causal=causal)
+        assert (np.abs(_np(g) - ref) <= 600 * U * mag).all()
+
+
 # ------------------------------------------------------------------------------------------------ together
 def test_a_training_step(I):
     """norm_rope, rel_bias, attention and their gradients against torch's in 64 bits: relative to the norm of each result, each
