@@ -399,7 +399,7 @@ __device__ __forceinline__ void store_codes(uint8_t* piece, int apart, const uin
 // A warp takes a token, or a run of its passes where there are few tokens: queries, keys, values, in this order.
 template <bool FP8, int P, int LPR, bool ADJ>
 __global__ void __launch_bounds__(kCacheThreads, 5) norm_rope_append_kernel(const __grid_constant__ NormAppendParams p) {
-  constexpr int RPW = 32 / LPR, SLOTS = 48 / P;
+  constexpr int RPW = 32 / LPR, SLOTS = 32 / P;
   __shared__ __align__(16) uint8_t rings[kCacheThreads / 32][SLOTS * Ring<P>::kSlot];
   const int lane = threadIdx.x & 31, l = lane % LPR, g = lane / LPR;
   const uint32_t w = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);

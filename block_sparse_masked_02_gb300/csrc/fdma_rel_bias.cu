@@ -12,8 +12,6 @@
 // over the matrix together and DRAM sees neighbouring rows.  A CTA's warps have eight parts of a band; it
 // joins their sums and writes one number where the whole band is in one bucket, as far from the diagonal nearly all are,
 // else the sums of the band's diagonals.  A second kernel adds what each bucket has of those, in a fixed order.
-#include <type_traits>
-
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
 #include "fdma_ptx.cuh"
@@ -28,12 +26,11 @@ constexpr int kPart = 264;
 constexpr int64_t kMostCtas = 1 << 28;  // of a backward (their parts take 283 GB)
 constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
 
-// CAP: most buckets of a side.  (A launch copies the arguments: with 256 it takes 2 us more on the host than with 32.)
-template <int CAP>
 struct RelView {
   int H, Nq, Nk, off;
   int n, two_sided;  // buckets of a side
-  int starts[CAP];
+  int top;           // the power of two that a search over them begins with
+  int starts[FDMA_MAX_BUCKETS];
 
   __host__ __device__ int buckets() const { return two_sided ? 2 * n : n; }
   __host__ __device__ int row_blocks() const { return (Nq + 7) >> 3; }
@@ -57,9 +54,8 @@ struct RelView {
 
 // ---- forward
 
-template <int CAP>
 struct FwdView {
-  RelView<CAP> r;
+  RelView r;
   const void* table;
   int table_bf16;
   int64_t ts[2];
@@ -68,8 +64,7 @@ struct FwdView {
   uint32_t ncc, units;  // warps along the columns; of all rows and heads
 };
 
-template <int CAP>
-__device__ __forceinline__ uint32_t table_value(const FwdView<CAP>& p, int bucket, int h) {
+__device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, int h) {
   const int64_t at = bucket * p.ts[0] + h * p.ts[1];
   if (p.table_bf16) return static_cast<const uint16_t*>(p.table)[at];
   return pack_bf16x2(static_cast<const float*>(p.table)[at], 0.f) & 0xffffu;
@@ -77,9 +72,8 @@ __device__ __forceinline__ uint32_t table_value(const FwdView<CAP>& p, int bucke
 
 // A warp writes 8 rows of 256 columns: with walks of 1, 2, 4, 8 or 16 blocks down the diagonal, which look up their values
 // once for all of them, four heads of 16384 x 16384 took 285, 310, 319, 330 or 353 us.
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView<CAP> p) {
-  __shared__ int first[CAP];  // (lanes look at different ones, which constant memory serves in turn)
+__global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView p) {
+  __shared__ int first[FDMA_MAX_BUCKETS];  // (lanes look at different ones, which constant memory serves in turn)
   __shared__ __align__(16) uint16_t values[kWarps][272];  // of a warp's diagonals
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t unit = blockIdx.x * kWarps + warp;
@@ -89,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
   const int b0 = p.r.bucket(lo);
   const bool one = b0 == p.r.bucket(lo + kSpan - 1) || unit >= p.units;
   if (__syncthreads_or(!one)) {
-    for (int i = threadIdx.x; i < CAP; i += kThreads) first[i] = i < p.r.n ? p.r.starts[i] : 0x7fffffff;
+    for (int i = threadIdx.x; i < FDMA_MAX_BUCKETS; i += kThreads) first[i] = i < p.r.n ? p.r.starts[i] : 0x7fffffff;
     __syncthreads();
   }
   if (unit >= p.units) return;
@@ -107,8 +101,7 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
       a[k] = p.r.two_sided ? abs(delta) : max(-delta, 0);
       s[k] = 0;
     }
-#pragma unroll
-    for (int step = CAP / 2; step > 0; step >>= 1)
+    for (int step = p.r.top; step > 0; step >>= 1)
 #pragma unroll
       for (int k = 0; k < 9; ++k)
         if (first[s[k] + step] <= a[k]) s[k] += step;
@@ -133,9 +126,8 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
 
 // ---- backward
 
-template <int CAP>
 struct BwdView {
-  RelView<CAP> r;
+  RelView r;
   int B, causal;
   int bands, parts;  // bands with anything in them; parts is a multiple of 8
   const uint16_t* db;
@@ -149,18 +141,15 @@ struct Deltas {
   int lo, hi;
 };
 // Band 0 begins with the block in the matrix's lower left corner.
-template <int CAP>
-__device__ __forceinline__ int first_delta(const RelView<CAP>& r) { return -8 * (r.row_blocks() - 1) - r.off - 7; }
-template <int CAP>
-__device__ __forceinline__ Deltas band_deltas(const BwdView<CAP>& p, int band) {
+__device__ __forceinline__ int first_delta(const RelView& r) { return -8 * (r.row_blocks() - 1) - r.off - 7; }
+__device__ __forceinline__ Deltas band_deltas(const BwdView& p, int band) {
   Deltas d;
   d.lo = first_delta(p.r) + 256 * band;
   d.hi = d.lo + kSpan - 1;
   if (p.causal) d.hi = min(d.hi, 0);
   return d;
 }
-template <int CAP>
-__device__ __forceinline__ Deltas bucket_deltas(const RelView<CAP>& r, int bucket) {
+__device__ __forceinline__ Deltas bucket_deltas(const RelView& r, int bucket) {
   constexpr int kFar = 0x7fffffff;
   const bool right = bucket >= r.n;
   const int s = right ? bucket - r.n : bucket, a0 = r.starts[s], a1 = s + 1 < r.n ? r.starts[s + 1] - 1 : kFar;
@@ -181,8 +170,7 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView<CAP> p) {
+__global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_constant__ BwdView p) {
   __shared__ float diag[kWarps][kSpan + 1];
   __shared__ float sums[kWarps];
   __shared__ int one_bucket;
@@ -259,8 +247,7 @@ __global__ void __launch_bounds__(kThreads, 4) rel_bias_bwd_kernel(const __grid_
 }
 
 // Adds the CTAs' sums of one bucket and head.
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView<CAP> p) {
+__global__ void __launch_bounds__(kThreads) rel_bias_join_kernel(const __grid_constant__ BwdView p) {
   __shared__ float s[kWarps];
   const int k = blockIdx.x % p.r.buckets(), h = blockIdx.x / p.r.buckets();
   const Deltas q = bucket_deltas(p.r, k);
@@ -340,21 +327,16 @@ int validate_starts(const fdma_rel_args& a, const int32_t* starts) {
   return FDMA_OK;
 }
 
-template <int CAP>
-void set_view(RelView<CAP>& r, const fdma_rel_args& a, const int32_t* starts) {
+void set_view(RelView& r, const fdma_rel_args& a, const int32_t* starts) {
   r.H = a.H;
   r.Nq = a.Nq;
   r.Nk = a.Nk;
   r.off = a.offset;
   r.n = a.num_starts;
   r.two_sided = a.two_sided;
+  r.top = 0;
+  while (2 * r.top < r.n && r.n > 1) r.top = r.top == 0 ? 1 : 2 * r.top;
   for (int i = 0; i < r.n; ++i) r.starts[i] = starts[i];
-}
-
-constexpr int kSmallCap = 32;
-template <typename F>
-int with_cap(int n, F&& f) {
-  return n <= kSmallCap ? f(std::integral_constant<int, kSmallCap>{}) : f(std::integral_constant<int, FDMA_MAX_BUCKETS>{});
 }
 
 int row_blocks(const fdma_rel_args& a) { return (a.Nq + 7) / 8; }
@@ -406,21 +388,19 @@ int fdma_rel_bias(const fdma_rel_args* a, const int32_t* starts, const void* tab
   if (!aligned16(out) || (a->H > 1 && os[0] % 8 != 0) || (a->Nq > 1 && os[1] % 8 != 0)) return FDMA_ERR_UNSUPPORTED;
   const int64_t ncc = (a->Nk / 8 + 31) / 32, units = ncc * row_blocks(*a) * a->H;
   if (units > 0x7fffffff) return FDMA_ERR_UNSUPPORTED;
-  return with_cap(a->num_starts, [&](auto cap) {
-    FwdView<decltype(cap)::value> p;
-    set_view(p.r, *a, starts);
-    p.table = table;
-    p.table_bf16 = table_type == FDMA_BF16;
-    p.out = static_cast<uint16_t*>(out);
-    for (int i = 0; i < 2; ++i) {
-      p.ts[i] = ts[i];
-      p.os[i] = os[i];
-    }
-    p.ncc = static_cast<uint32_t>(ncc);
-    p.units = static_cast<uint32_t>(units);
-    rel_bias_kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
-  });
+  FwdView p;
+  set_view(p.r, *a, starts);
+  p.table = table;
+  p.table_bf16 = table_type == FDMA_BF16;
+  p.out = static_cast<uint16_t*>(out);
+  for (int i = 0; i < 2; ++i) {
+    p.ts[i] = ts[i];
+    p.os[i] = os[i];
+  }
+  p.ncc = static_cast<uint32_t>(ncc);
+  p.units = static_cast<uint32_t>(units);
+  rel_bias_kernel<<<static_cast<unsigned>((units + kWarps - 1) / kWarps), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 size_t fdma_rel_bias_bwd_workspace_size(const fdma_rel_args* a, int B) {
@@ -454,24 +434,22 @@ int fdma_rel_bias_bwd(const fdma_rel_args* a, const int32_t* starts, int B, cons
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
       workspace_bytes < static_cast<size_t>(whole.ctas) * kPart * sizeof(float))
     return FDMA_ERR_WORKSPACE;
-  return with_cap(a->num_starts, [&](auto cap) {
-    BwdView<decltype(cap)::value> p;
-    set_view(p.r, *a, starts);
-    p.B = B;
-    p.causal = causal;
-    p.bands = plan.bands;
-    p.parts = plan.parts;
-    p.db = static_cast<const uint16_t*>(dbias);
-    for (int i = 0; i < 3; ++i) p.ds[i] = ds[i];
-    p.part = static_cast<float*>(workspace);
-    p.dtable = dtable;
-    if (plan.ctas > 0) {
-      rel_bias_bwd_kernel<<<static_cast<unsigned>(plan.ctas), kThreads, 0, cs>>>(p);
-      if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
-    }
-    rel_bias_join_kernel<<<static_cast<unsigned>(buckets * a->H), kThreads, 0, cs>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
-  });
+  BwdView p;
+  set_view(p.r, *a, starts);
+  p.B = B;
+  p.causal = causal;
+  p.bands = plan.bands;
+  p.parts = plan.parts;
+  p.db = static_cast<const uint16_t*>(dbias);
+  for (int i = 0; i < 3; ++i) p.ds[i] = ds[i];
+  p.part = static_cast<float*>(workspace);
+  p.dtable = dtable;
+  if (plan.ctas > 0) {
+    rel_bias_bwd_kernel<<<static_cast<unsigned>(plan.ctas), kThreads, 0, cs>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FDMA_ERR_CUDA;
+  }
+  rel_bias_join_kernel<<<static_cast<unsigned>(buckets * a->H), kThreads, 0, cs>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 
 }  // extern "C"
