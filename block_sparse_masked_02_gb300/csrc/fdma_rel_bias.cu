@@ -12,6 +12,9 @@
 // over the matrix together and DRAM sees neighbouring rows.  A CTA's warps have eight parts of a band; it
 // joins their sums and writes one number where the whole band is in one bucket, as far from the diagonal nearly all are,
 // else the sums of the band's diagonals.  A second kernel adds what each bucket has of those, in a fixed order.
+// Bound by reading: the causal half of four heads of 16384 x 16384 (1.07 GB) takes 170 us, 6.3 TB/s, 5 us of it the second kernel;
+// 55 MB in 3 x 6 heads 16 us, of which that is 3 and start and end of 540 CTAs of five block rows a warp most of the rest.
+// (Block rows of a unit one after the other, 512 rows of a matrix apart from the next unit's: 376 us.)
 #include "../../include/fdma_inputs.h"
 #include "fdma_internal.h"
 #include "fdma_ptx.cuh"
@@ -24,7 +27,9 @@ constexpr int kMaxLen = 131072;  // as fdma_fwd's
 constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
 constexpr int kPart = 264;
 constexpr int64_t kMostCtas = 1 << 28;  // of a backward (their parts take 283 GB)
-constexpr int kBwdSteps = 16, kBwdCtas = 456;  // of a backward walk; of a call
+// Block rows of a backward walk, and the CTAs that a call should have if its walks get shorter for it.  (Four causal heads of
+// 16384 x 16384 / 3 x 6 of 1001 x 1528, us: 8 steps 175 / 15.9, 16: 172 / 15.9, 24: 175 / 16.3; 600 CTAs 172 / 18.3, 150: 172 / 22.)
+constexpr int kBwdSteps = 16, kBwdCtas = 456;
 
 struct RelView {
   int H, Nq, Nk, off;
@@ -70,8 +75,10 @@ __device__ __forceinline__ uint32_t table_value(const FwdView& p, int bucket, in
   return pack_bf16x2(static_cast<const float*>(p.table)[at], 0.f) & 0xffffu;
 }
 
-// A warp writes 8 rows of 256 columns: with walks of 1, 2, 4, 8 or 16 blocks down the diagonal, which look up their values
-// once for all of them, four heads of 16384 x 16384 took 285, 310, 319, 330 or 353 us.
+// A warp writes 8 rows of 256 columns.  Bound by writing: four heads of 16384 x 16384 (2.1 GB) take 278 us, 7.7 TB/s, 94 % of
+// what DRAM has (a copy moves 6.8).  (Walks of 2, 4, 8 or 16 blocks down the diagonal, which look up their values once for all
+// of them, took 310, 319, 330 or 353 us: rows that are written at the same time should be neighbours.)  A few rows take 3 us,
+// most of it the launch and the searches near the diagonal.
 __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constant__ FwdView p) {
   __shared__ int first[FDMA_MAX_BUCKETS];  // (lanes look at different ones, which constant memory serves in turn)
   __shared__ __align__(16) uint16_t values[kWarps][272];  // of a warp's diagonals
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) rel_bias_kernel(const __grid_constan
 #pragma unroll
     for (int i = 0; i < 14; ++i) w[i] = v;
   } else {
-    // nine diagonals a lane, looked up side by side: a search one after the other took 6 instead of 2 us
+    // nine diagonals a lane, looked up side by side (one after the other, 5 rows of 4096 keys took 8.7 instead of 3.1 us)
     int a[9], s[9];
 #pragma unroll
     for (int k = 0; k < 9; ++k) {
