@@ -685,10 +685,10 @@ int fdma_norm_rope_append(const fdma_norm_rope_args* a, const fdma_kv_cache* c, 
   if (T == 0 || c->B == 0) return FDMA_OK;
   if (cu == nullptr) return FDMA_ERR_INVALID;
   const int64_t nq[3] = {1, T, a->Hq}, nk[3] = {1, T, a->Hk};
-  st = validate_rows(q, nq, false);
-  if (st == FDMA_OK) st = validate_rows(k, nk, false);
-  if (st == FDMA_OK) st = validate_rows(v, nk, false);
-  if (st == FDMA_OK) st = validate_rows(q_out, nq, true);
+  st = validate_rows(q, nq, a->d, false);
+  if (st == FDMA_OK) st = validate_rows(k, nk, a->d, false);
+  if (st == FDMA_OK) st = validate_rows(v, nk, a->d, false);
+  if (st == FDMA_OK) st = validate_rows(q_out, nq, a->d, true);
   if (st != FDMA_OK) return st;
   if (!distinct_slots(*c)) return FDMA_ERR_INVALID;
   NormAppendParams p{};

@@ -22,6 +22,7 @@
 // Steps that led here (the first case forward / backward, us): a row a lane group, addresses for each 52 / 102; a warp a token,
 // arithmetic on pairs, pieces of 16 bytes 39 / 80; rows on their way in shared memory 36 / 70; angles and weights there too 34
 // / 53; CTAs by what a token costs 31 / 46.
+#include <algorithm>
 #include <cmath>
 
 #include "fdma_norm_rope.cuh"
@@ -318,18 +319,14 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
     cost[s] = 3 * (q[s] < r.per ? q[s] : r.per) + 2;
     all += r.chunks[s] * cost[s];
   }
-  auto share = [&](int64_t n) {  // tokens of a warp of n CTAs
-    return (tokens + n * kWarps - 1) / (n * kWarps);
-  };
-  auto least = [&](int64_t t) {  // CTAs whose warps have at most t
-    return (tokens + t * kWarps - 1) / (t * kWarps);
-  };
+  // tokens of a warp of n CTAs, and as well the CTAs whose warps have at most n
+  auto share = [&](int64_t n) { return (tokens + n * kWarps - 1) / (n * kWarps); };
   const int64_t even = ctas * cost[0] / all, up = share(even < 1 ? 1 : even);
   int64_t best = -1;
   for (int64_t t = up; t >= 1 && t >= up - 1; --t) {
-    const int64_t n = least(t), rest = r.chunks[1] > 0 ? (ctas - n * r.chunks[0]) / r.chunks[1] : 1;
+    const int64_t n = share(t), rest = r.chunks[1] > 0 ? (ctas - n * r.chunks[0]) / r.chunks[1] : 1;
     if (t < up && (rest < 1 || n * r.chunks[0] > ctas)) continue;  // (the first one is taken whatever there is)
-    const int64_t m = r.chunks[1] > 0 ? least(share(rest < 1 ? 1 : rest)) : 0;
+    const int64_t m = r.chunks[1] > 0 ? share(share(rest < 1 ? 1 : rest)) : 0;
     const int64_t last = r.chunks[1] > 0 && share(m) * cost[1] > t * cost[0] ? share(m) * cost[1] : t * cost[0];
     if (best >= 0 && last >= best) continue;
     best = last;
@@ -409,13 +406,23 @@ NormRopeView norm_rope_view(const fdma_norm_rope_args& a) {
   return v;
 }
 
-int validate_rows(const fdma_rows* r, const int64_t n[3], bool written) {
+int validate_rows(const fdma_rows* r, const int64_t n[3], int d, bool written) {
   if (r == nullptr || r->p == nullptr) return FDMA_ERR_INVALID;
   if (!aligned16(r->p)) return FDMA_ERR_UNSUPPORTED;
   for (int i = 0; i < 3; ++i) {
     if (n[i] <= 1) continue;
-    if (r->stride[i] < 0 || (written && r->stride[i] == 0)) return FDMA_ERR_INVALID;
+    if (r->stride[i] < 0) return FDMA_ERR_INVALID;
     if (r->stride[i] % 8 != 0) return FDMA_ERR_UNSUPPORTED;
+  }
+  if (!written) return FDMA_OK;
+  // from the smallest stride to the largest, each steps over all that the ones before reach
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int i, int j) { return r->stride[i] < r->stride[j]; });
+  int64_t extent = d;
+  for (int i : order) {
+    if (n[i] <= 1) continue;
+    if (r->stride[i] < extent) return FDMA_ERR_INVALID;
+    extent += (n[i] - 1) * r->stride[i];
   }
   return FDMA_OK;
 }
@@ -444,9 +451,9 @@ void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
 
 int check_sides(const fdma_norm_rope_args& a, const fdma_rows* q, const fdma_rows* k, bool written) {
   const int64_t nq[3] = {a.B, a.N, a.Hq}, nk[3] = {a.B, a.N, a.Hk};
-  const int st = validate_rows(q, nq, written);
+  const int st = validate_rows(q, nq, a.d, written);
   if (st != FDMA_OK || a.Hk == 0) return st;
-  return validate_rows(k, nk, written);
+  return validate_rows(k, nk, a.d, written);
 }
 
 }  // namespace

@@ -46,8 +46,8 @@ struct NormRopeView {
 
 int validate_norm_rope(const fdma_norm_rope_args* a);
 NormRopeView norm_rope_view(const fdma_norm_rope_args& a);
-// Rows of n[0] batches, n[1] tokens and n[2] heads; those that are written have to be distinct.
-int validate_rows(const fdma_rows* r, const int64_t n[3], bool written);
+// Rows of n[0] batches, n[1] tokens and n[2] heads; those that are written must not overlap.
+int validate_rows(const fdma_rows* r, const int64_t n[3], int d, bool written);
 RowsView rows_view(const fdma_rows& r);
 
 // Pairs of a lane.

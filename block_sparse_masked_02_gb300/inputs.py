@@ -89,11 +89,12 @@ def load() -> ctypes.CDLL:
 
 
 _BF16, _FP32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (a torch built without CUDA has none of these; it can still import this)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 # A call's own workspace comes from the caching allocator without a tensor around it, which would cost 3 us.
-_raw_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
-_raw_delete = torch._C._cuda_cudaCachingAllocator_raw_delete
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
 
 def _check_device(first, *ts):
@@ -234,12 +235,13 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=N
     """Norm and rotation of q (B, N, Hq, d) and k (B, N, Hk, d) or None, or packed (T, H, d), bf16 with a contiguous head
     dim: (q_out, k_out), k_out None without k.
 
-    Each row is divided by sqrt(mean of its squares + eps) and multiplied with its weight, (d) or (heads, d), fp32 or
-    bf16, None for ones (norm=False leaves all of that out).  Then the first rot values are turned: rope is the table
-    of `rope_table` (None: no rotation), pairs are (i, i + rot / 2), or (2 i, 2 i + 1) if interleaved.  Token n of each
-    sequence is at position first + n, or at positions (int32 (N,) or (B, N)); a token at a negative position is padding
-    and its rows are left as they are (uninitialised where the outputs are allocated here).  A position behind the
-    table is left out too and reported by `fdma.device_error()`.  q_out and k_out may be q and k themselves."""
+    Each row is divided by sqrt(mean of its squares + eps) and multiplied with its weight, (d) or (heads, d) (both
+    weights of one form), fp32 or bf16, None for ones (norm=False leaves all of that out).  Then the first rot values
+    are turned: rope is the table of `rope_table` (None: no rotation), pairs are (i, i + rot / 2), or (2 i, 2 i + 1) if
+    interleaved.  Token n of each sequence is at position first + n, or at positions (int32 (N,) or (B, N)); a token
+    at a negative position is padding and its rows are left as they are (uninitialised where the outputs are
+    allocated here).  A position behind the table is left out too and reported by `fdma.device_error()`.  q_out and
+    k_out may be q and k themselves."""
     dev = _check_device(q, k, q_weight, k_weight, rope, positions, q_out, k_out)
     args = _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps)
     guard, sp = _on(dev, stream)

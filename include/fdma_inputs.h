@@ -21,7 +21,8 @@ extern "C" {
 typedef enum { FDMA_FP32 = 0, FDMA_BF16 = 1 } fdma_param_type;
 
 /* Rows of d contiguous bf16 values; strides (batch, token, head) in ELEMENTS, multiples of 8, none
-   negative; base 16-byte aligned.  A batch stride is not looked at with one batch, and so on. */
+   negative; base 16-byte aligned.  A batch stride is not looked at with one batch, and so on.  Rows that are
+   written must not overlap: sorted, each stride has to step over all that the smaller ones reach. */
 typedef struct fdma_rows {
   void* p;
   int64_t stride[3];
@@ -41,7 +42,7 @@ typedef struct fdma_norm_rope_args {
 
   int32_t weight_type; /* fdma_param_type of both weights */
   /* d values, 16-byte aligned, or NULL (ones); (H, d) with the head stride in elements (a multiple of 8,
-     at least d), or d for all heads with head stride 0 */
+     at least d), or d for all heads with head stride 0.  Both weights are of one form, or one of them is NULL */
   const void* q_weight;
   int64_t q_weight_head;
   const void* k_weight;

@@ -98,6 +98,8 @@ def test_rows_that_are_written_are_distinct(I):
     assert lib.fdma_norm_rope(a, r, r, same, r, None) == 1
     assert lib.fdma_norm_rope(a, r, r, r, same, None) == 1
     assert lib.fdma_norm_rope_bwd(a, r, r, r, r, same, r, None, None, None, 0, None) == 1
+    for st in ((2560, 512, 64), (2560, 448, 128), (2048, 512, 128), (0, 512, 128)):  # rows that overlap
+        assert lib.fdma_norm_rope(a, r, r, _rows(I, FAKE, st), r, None) == 1, st
     assert lib.fdma_norm_rope(a, None, r, r, r, None) == 1
     assert lib.fdma_norm_rope(None, r, r, r, r, None) == 1
 
