@@ -499,6 +499,30 @@ def test_append_to_nothing(I):
         s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, positions=torch.zeros(2, 2, dtype=torch.int32, device="cuda"), **s.kw)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_in_other_layouts_and_on_another_stream(I, fp8):
+    """Token-major pages with gaps, a page stride past 32 bits, q_out among other rows: as in the usual layout."""
+    s = Serving(I, [9, 3], [12, 30], 4, 2, 64, fp8=fp8)
+    want = s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, **s.kw, **s.ex)
+    num, dt = s.kc.shape[0], s.kc.dtype
+    kc = torch.empty(num, 16, 2, 96, dtype=dt, device="cuda")[..., :64]
+    step = ((1 << 31) + 4096) // (num - 1) // 128 * 128 + 128  # the last page begins behind 2^31 elements
+    vc = torch.empty(step * (num - 1) + 16 * 2 * 64, dtype=dt, device="cuda").as_strided((num, 16, 2, 64), (step, 128, 64, 1))
+    ke = torch.empty(num, 16, 3, dtype=torch.uint8, device="cuda")[..., 1:] if fp8 else None
+    ve = torch.empty(num, 2, 2, 16, dtype=torch.uint8, device="cuda")[:, :, 1].transpose(1, 2) if fp8 else None
+    rows = torch.empty(s.T, 9, 64, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = s.P.norm_rope_append(s.q, s.k, s.v, kc, vc, s.table, s.k_lens, s.cu, q_out=rows[:, 2:6], k_exp=ke, v_exp=ve,
+                               stream=side, **s.kw)
+    side.synchronize()
+    pg, sl = (torch.tensor(x, device="cuda") for x in s.slots())
+    n = 12
+    assert torch.equal(got[:n], want[:n])
+    for x, y in ((kc, s.kc), (vc, s.vc)) + (((ke, s.ke), (ve, s.ve)) if fp8 else ()):
+        assert torch.equal(x[pg, sl].view(torch.uint8), y[pg, sl].view(torch.uint8))
+
+
 def test_append_of_values_that_are_not_finite(I):
     for fp8 in (False, True):
         s = Serving(I, [8], [5], 2, 2, 64, fp8=fp8, extra=0)
