@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kCacheThreads, 5) norm_rope_append_kernel(cons
     cp_async_wait_all();
     return;
   }
-  const Turn<P> t = load_turn<P>(p.v, pos, l, at);
+  const Turn<P> t = load_turn<P, ADJ>(p.v, pos, at);
   int slot = 0;
 #pragma unroll 1
   for (int side = 0; side < 3; ++side) {
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kCacheThreads, 5) norm_rope_append_kernel(cons
           scale(x, row_rsqrt<LPR>(p.v, x, by));
           multiply(x, wt);
         }
-        turn<false>(x, t, at);
+        turn<false, ADJ>(x, t, at);
       }
       if (!FP8 || is_q) {
         if (h < end) store_raw<P>(reinterpret_cast<uint16_t*>(to), at.apart, is_v ? raw : narrow<P, ADJ>(x));

@@ -78,17 +78,20 @@ struct WalkView {
   int* err;
 };
 
-template <int P>
-__device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const Lane& at, bool adj) {
+template <int P, bool ADJ>
+__device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const Lane& at) {
 #pragma unroll
   for (int i = 0; i < P / 2; ++i) {
     float a0, a1, b0, b1;
     f2split(x.a[i], a0, a1);
     f2split(x.b[i], b0, b1);
-    s[adj ? at.ca + 4 * i : at.ca + 2 * i] = a0;
-    s[adj ? at.ca + 4 * i + 2 : at.ca + 2 * i + 1] = a1;
-    s[adj ? at.ca + 4 * i + 1 : at.cb + 2 * i] = b0;
-    s[adj ? at.ca + 4 * i + 3 : at.cb + 2 * i + 1] = b1;
+    if (ADJ) {
+      float* p = s + (i < P / 4 ? at.ca + 4 * i : at.cb + 4 * (i - P / 4));
+      p[0] = a0, p[1] = b0, p[2] = a1, p[3] = b1;
+    } else {
+      s[at.ca + 2 * i] = a0, s[at.ca + 2 * i + 1] = a1;
+      s[at.cb + 2 * i] = b0, s[at.cb + 2 * i + 1] = b1;
+    }
   }
 }
 
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   uint32_t done = 0;
   for (uint32_t tok = tok0; tok < p.line.tokens; tok += step) {
     const bool left = (left_out >> (done & 31u)) & 1u;
-    const uint32_t angles = table + row * p.plan.table + 4 * P * l, half = 2 * p.v.rot;
+    const uint32_t angles = table + row * p.plan.table, half = 2 * p.v.rot;
     uint16_t* to = out.p + now.b * out.st[0] + now.n * out.st[1] + out_first;
     int h = h_first;
     cp_async_wait<SLOTS - 1>();
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
             Pairs<P> xs = widen<P, ADJ>(ring.get(STEP * slot));
             float by;
             const float r = row_rsqrt<LPR>(p.v, xs, by);
-            turn_shared<true>(d, angles, half, at);
+            turn_shared<true, ADJ>(d, angles, half, at);
             scale(d, r);
 #pragma unroll
             for (int e = 0; e < P / 2; ++e) {
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
             }
             if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
           } else {
-            turn_shared<true>(d, angles, half, at);
+            turn_shared<true, ADJ>(d, angles, half, at);
           }
         } else {
           if (p.v.norm) {
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
             scale(d, row_rsqrt<LPR>(p.v, d, by));
             multiply_shared(d, weight);
           }
-          turn_shared<false>(d, angles, half, at);
+          turn_shared<false, ADJ>(d, angles, half, at);
         }
         if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
       }
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   if (!BACK || p.part == nullptr) return;
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem + WEIGHT);  // [warp][row of a pass][column]
-  if (at.in) put_columns(sums + (warp * RPW + g) * COLS, acc, at, ADJ);
+  if (at.in) put_columns<P, ADJ>(sums + (warp * RPW + g) * COLS, acc, at);
   __syncthreads();
   float* part = p.part + static_cast<int64_t>(blockIdx.x) * p.plan.rows * p.v.d;
   for (int i = threadIdx.x; i < p.plan.rows * p.v.d; i += kThreads) {

@@ -1,12 +1,15 @@
 // The norm of a row (one token's values of one head) and the rotation of its pairs, as the
 // kernels of fdma_norm_rope.cu and the cache write in fdma_cache.cu share them.
 //
-// A row is held by LPR lanes (a power of two), 2 P values a lane as P pairs (a[i], b[i]):
+// A row is held by LPR lanes, two pieces of P values a lane, P pairs (a[i], b[i]) in all.  The pieces a of a row's
+// lanes follow each other, and so do the pieces b (16 bytes of a lane beside those of the next: with both pieces of a lane side
+// by side, every store wrote half a sector, and adjacent pairs took 42 instead of 31 us forward, 68 instead of 46 backward):
 //   halves    lane l of the first rot / (2 P) holds columns P l + i and rot / 2 + P l + i, so both values
-//             of a pair are in one lane; the lanes behind hold columns 2 P l + i and 2 P l + P + i;
-//   adjacent  lane l holds columns 2 P l + 2 i and 2 P l + 2 i + 1.
-// Either way lane l turns its pairs by the angles P l + i.  Lanes with 2 P l >= d hold zeros.  A warp holds 32 / LPR rows
-// at once, all of one tensor: a pass.  Arithmetic is on pairs of fp32 values, one instruction for two.
+//             of a pair are in one lane; the m lanes behind hold, by their number u from 0 on, columns rot + P u + i and
+//             rot + P m + P u + i;
+//   adjacent  lane l holds columns P l + i and d / 2 + P l + i, P / 2 whole pairs each.
+// Lanes with 2 P l >= d hold zeros.  A warp holds 32 / LPR rows at once, all of one tensor: a pass.  Arithmetic is on
+// pairs of fp32 values, one instruction for two.
 //
 // P is 8, pieces of 16 bytes, where d and rot are multiples of 16, else 4, which other sizes need.  (With pieces of 4
 // for all, the long cases of rows of 128 take 37 instead of 31 us forward, 60 instead of 46 backward and 85 instead of 79 into
@@ -80,19 +83,32 @@ inline int pass_rows(int d, int rot) {
 
 // Where a lane's values lie in a row.
 struct Lane {
-  int ca, cb;   // columns of its two pieces of P values
-  int apart;    // cb - ca
-  bool in;      // 2 P l < d
-  bool turned;  // its pairs are rotated
+  int ca, cb;  // columns of its two pieces of P values
+  int apart;   // cb - ca
+  bool in;     // 2 P l < d
+  // whether the pairs of piece a (halves: all of them) and of piece b (adjacent) are turned, and where their angles begin
+  bool turned, turned_b;
+  int ta, tb;
 };
 
 template <int P, bool ADJ>
 __device__ __forceinline__ Lane lane_of(const NormRopeView& v, int l) {
   Lane r;
   r.in = 2 * P * l < v.d;
-  r.turned = 2 * P * l < v.rot;
-  r.ca = !ADJ && r.turned ? P * l : 2 * P * l;
-  r.cb = !ADJ && r.turned ? (v.rot >> 1) + P * l : 2 * P * l + P;
+  if (ADJ) {
+    r.ca = P * l;
+    r.cb = (v.d >> 1) + P * l;
+    r.turned = r.ca < v.rot;
+    r.turned_b = r.cb < v.rot;
+    r.ta = r.ca >> 1;
+    r.tb = r.cb >> 1;
+  } else {
+    r.turned = r.turned_b = 2 * P * l < v.rot;
+    const int first = r.turned ? 0 : v.rot, u = l - (r.turned ? 0 : v.rot / (2 * P));
+    r.ca = first + P * u;
+    r.cb = first + (((r.turned ? v.rot : v.d) - first) >> 1) + P * u;
+    r.ta = r.tb = P * l;
+  }
   r.apart = r.cb - r.ca;
   return r;
 }
@@ -250,31 +266,7 @@ template <int P>
 struct Turn {
   uint64_t c[P / 2], s[P / 2];
 };
-// Those of a lane's pairs at a position inside the table.
-template <int P>
-__device__ __forceinline__ Turn<P> load_turn(const NormRopeView& v, int pos, int l, const Lane& n) {
-  Turn<P> t;
-#pragma unroll
-  for (int i = 0; i < P / 2; ++i) t.c[i] = t.s[i] = 0;
-  if (!n.turned) return t;
-  const float* p = v.rope + static_cast<int64_t>(pos) * v.rot + P * l;
-#pragma unroll
-  for (int i = 0; i < P; i += 4) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(p + i)), s = __ldg(reinterpret_cast<const float4*>(p + (v.rot >> 1) + i));
-    t.c[i / 2] = f2(c.x, c.y);
-    t.c[i / 2 + 1] = f2(c.z, c.w);
-    t.s[i / 2] = f2(s.x, s.y);
-    t.s[i / 2 + 1] = f2(s.z, s.w);
-  }
-  return t;
-}
-
-// Two pairs of fp32 values from 16 bytes of shared memory.
-__device__ __forceinline__ void shared_pairs(uint32_t at, uint64_t& x, uint64_t& y) {
-  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at) : "memory");
-}
-
-// Turns a lane's pairs (BACK: the other way) by the angles i, i + 1 of c and s.
+// Turns a lane's pairs 2 i and 2 i + 1 (BACK: the other way).
 template <bool BACK, int P>
 __device__ __forceinline__ void turn_pair(Pairs<P>& x, int i, uint64_t c, uint64_t s) {
   const uint64_t a = x.a[i], b = x.b[i];
@@ -283,26 +275,65 @@ __device__ __forceinline__ void turn_pair(Pairs<P>& x, int i, uint64_t c, uint64
   x.b[i] = BACK ? sub2(mul2(b, c), mul2(a, s)) : fma2(a, s, mul2(b, c));
 }
 
-// Lanes that are not turned keep their values: a product with a sine of 0 would carry an infinity of one column into
-// another.
-template <bool BACK, int P>
+// The angles of a lane's pairs at a position inside the table.
+template <int P, bool ADJ>
+__device__ __forceinline__ Turn<P> load_turn(const NormRopeView& v, int pos, const Lane& n) {
+  Turn<P> t;
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) t.c[i] = t.s[i] = 0;
+  if (!n.turned) return t;
+  const float* row = v.rope + static_cast<int64_t>(pos) * v.rot;
+#pragma unroll
+  for (int i = 0; i < P / 2; ++i) {
+    const bool b = ADJ && i >= P / 4;
+    if (b && !n.turned_b) continue;
+    const float* p = row + (b ? n.tb + 2 * (i - P / 4) : n.ta + 2 * i);
+    const float2 c = __ldg(reinterpret_cast<const float2*>(p)), s = __ldg(reinterpret_cast<const float2*>(p + (v.rot >> 1)));
+    t.c[i] = f2(c.x, c.y);
+    t.s[i] = f2(s.x, s.y);
+  }
+  return t;
+}
+
+// Turns a lane's pairs.  Those that are not turned keep their values: a product with a sine of 0 would carry an
+// infinity of one column into another.
+template <bool BACK, bool ADJ, int P>
 __device__ __forceinline__ void turn(Pairs<P>& x, const Turn<P>& t, const Lane& n) {
   if (!n.turned) return;
 #pragma unroll
-  for (int i = 0; i < P / 2; ++i) turn_pair<BACK>(x, i, t.c[i], t.s[i]);
-}
-// ... from a row of the table in shared memory (at: this lane's cosines, half: the sines' distance).
-template <bool BACK, int P>
-__device__ __forceinline__ void turn_shared(Pairs<P>& x, uint32_t at, uint32_t half, const Lane& n) {
-  if (!n.turned) return;
-#pragma unroll
-  for (int i = 0; i < P / 2; i += 2) {
-    uint64_t c0, c1, s0, s1;
-    shared_pairs(at + 8 * i, c0, c1);
-    shared_pairs(at + half + 8 * i, s0, s1);
-    turn_pair<BACK>(x, i, c0, s0);
-    turn_pair<BACK>(x, i + 1, c1, s1);
+  for (int i = 0; i < P / 2; ++i) {
+    if (ADJ && i >= P / 4 && !n.turned_b) continue;
+    turn_pair<BACK>(x, i, t.c[i], t.s[i]);
   }
+}
+
+// Two pairs of fp32 values from 16 bytes of shared memory.
+__device__ __forceinline__ void shared_pairs(uint32_t at, uint64_t& x, uint64_t& y) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "r"(at) : "memory");
+}
+
+// ... by a row of the table in shared memory (half: from the cosines to the sines, in bytes).
+template <bool BACK, bool ADJ, int P>
+__device__ __forceinline__ void turn_shared(Pairs<P>& x, uint32_t row, uint32_t half, const Lane& n) {
+  if (!n.turned) return;
+  auto some = [&](int from, int count, uint32_t at) {  // count pairs of pairs
+#pragma unroll
+    for (int i = 0; i < count; i += 2) {
+      uint64_t c0, c1, s0, s1;
+      if (count > 1) {
+        shared_pairs(at + 8 * i, c0, c1);
+        shared_pairs(at + half + 8 * i, s0, s1);
+        turn_pair<BACK>(x, from + i, c0, s0);
+        turn_pair<BACK>(x, from + i + 1, c1, s1);
+      } else {
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(c0) : "r"(at) : "memory");
+        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s0) : "r"(at + half) : "memory");
+        turn_pair<BACK>(x, from, c0, s0);
+      }
+    }
+  };
+  some(0, ADJ ? P / 4 : P / 2, row + 4 * n.ta);
+  if (ADJ && n.turned_b) some(P / 4, P / 4, row + 4 * n.tb);
 }
 
 template <int LPR>
