@@ -373,8 +373,7 @@ __device__ __forceinline__ void quantise_pairs(const Pairs<P>& x, uint32_t (&cod
     const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
     m = max(m, a < 0x7f800000u ? a : 0u);
   }
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = row_all<LPR>(m, [](uint32_t a, uint32_t b) { return max(a, b); });
   const int E = static_cast<int>(m >> 23), up = (m & 0x7fffffu) > 0x600000u ? 1 : 0;
   const int b = min(max(E - 8 + up, 1), 246);
   be = static_cast<uint32_t>(b);
@@ -414,7 +413,7 @@ __global__ void __launch_bounds__(kCacheThreads, 5) norm_rope_append_kernel(cons
     c = w - tok * p.plan.chunks;
   }
   if (tok >= static_cast<uint32_t>(p.m.T)) return;  // (never a block's first warp)
-  const Lane at = lane_of<P, ADJ>(p.v, l);
+  const Lane at = lane_of<P, LPR, ADJ>(p.v, l, g);
   const Ring<P> ring(smem_u32(rings[threadIdx.x >> 5]), lane);
   const int q0 = static_cast<int>(c) * p.plan.per, q1 = min(q0 + p.plan.per, p.plan.passes);
   // what is fetched next: pass q_next, whose row of this lane is head h_next of the tensor that ends at pass q_turn
@@ -693,7 +692,7 @@ int fdma_norm_rope_append(const fdma_norm_rope_args* a, const fdma_kv_cache* c, 
   if (!distinct_slots(*c)) return FDMA_ERR_INVALID;
   NormAppendParams p{};
   p.v = norm_rope_view(*a);
-  const int rows = pass_rows(c->d, p.v.rot);
+  const int rows = pass_rows(c->d, p.v.rot, a->interleaved != 0);
   int at = 0;
   for (int i = 0; i < 3; ++i) {
     p.H[i] = i == 0 ? a->Hq : c->Hkv;

@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   if (side) cta -= p.plan.chunks[0] * p.plan.ctas[0];
   const int chunk = cta / p.plan.ctas[side];
   const int q_first = chunk * p.plan.per, q_last = min(q_first + p.plan.per, p.passes[side]), H = p.H[side];
-  const Lane at = lane_of<P, ADJ>(p.v, l);
+  const Lane at = lane_of<P, LPR, ADJ>(p.v, l, g);
   const RowsView &x = p.x[side], &gr = p.g[side], &out = p.out[side];
   const uint32_t step = p.plan.ctas[side] * kWarps, tok0 = (cta - chunk * p.plan.ctas[side]) * kWarps + warp;
   const uint32_t base = smem_u32(smem), weight = base + lane * 16;
@@ -302,7 +302,8 @@ bool by_head(const fdma_norm_rope_args& a) { return a.q_weight_head != 0 || a.k_
 
 WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
   WalkPlan r{};
-  const int rot = a.rope != nullptr ? a.rot : 0, rpw = pass_rows(a.d, rot), piece = piece_of(a.d, rot);
+  const int rot = a.rope != nullptr ? a.rot : 0, piece = piece_of(a.d, rot, a.interleaved != 0),
+            rpw = pass_rows(a.d, rot, a.interleaved != 0);
   const int slots = back ? 24 / piece : 32 / piece;
   r.table = 4 * rot;
   r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (slots + 1) * r.table);
@@ -449,7 +450,7 @@ void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
   p.line = {a.N, a.B, static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N)};
   p.H[0] = a.Hq;
   p.H[1] = a.Hk;
-  for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot));
+  for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot, a.interleaved != 0));
 }
 
 int check_sides(const fdma_norm_rope_args& a, const fdma_rows* q, const fdma_rows* k, bool written) {
@@ -545,7 +546,7 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   w.H[0] = a->Hq;
   w.H[1] = a->Hk;
   w.heads = by_head(*a);
-  w.rpw = pass_rows(a->d, p.v.rot);
+  w.rpw = pass_rows(a->d, p.v.rot, a->interleaved != 0);
   const dim3 grid(w.heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
   // (launched behind: 9.1 -> 8.4 us for 771 tokens of 5 + 5 heads)
   return launch_behind(weight_sum_kernel, grid, 1024, cs, w) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;

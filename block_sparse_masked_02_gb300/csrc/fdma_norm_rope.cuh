@@ -1,19 +1,20 @@
 // The norm of a row (one token's values of one head) and the rotation of its pairs, as the
 // kernels of fdma_norm_rope.cu and the cache write in fdma_cache.cu share them.
 //
-// A row is held by LPR lanes, two pieces of P values a lane, P pairs (a[i], b[i]) in all.  The pieces a of a row's
+// A row is held by LPR lanes (with pieces of 8 also five or six), two pieces of P values a lane, P pairs (a[i], b[i]) in all.  The pieces a of a row's
 // lanes follow each other, and so do the pieces b (16 bytes of a lane beside those of the next: with both pieces of a lane side
 // by side, every store wrote half a sector, and adjacent pairs took 42 instead of 31 us forward, 68 instead of 46 backward):
 //   halves    lane l of the first rot / (2 P) holds columns P l + i and rot / 2 + P l + i, so both values
 //             of a pair are in one lane; the m lanes behind hold, by their number u from 0 on, columns rot + P u + i and
 //             rot + P m + P u + i;
 //   adjacent  lane l holds columns P l + i and d / 2 + P l + i, P / 2 whole pairs each.
-// Lanes with 2 P l >= d hold zeros.  A warp holds 32 / LPR rows at once, all of one tensor: a pass.  Arithmetic is on
+// Lanes with 2 P l >= d hold zeros, as do the last two of a warp where LPR is five or six.  A warp holds 32 / LPR rows at
+// once, all of one tensor: a pass.  Arithmetic is on
 // pairs of fp32 values, one instruction for two.
 //
-// P is 8, pieces of 16 bytes, where d and rot are multiples of 16, else 4, which other sizes need.  (With pieces of 4
+// P is 8, pieces of 16 bytes, where d and (halves) rot are multiples of 16, else 4, which other sizes need.  (With pieces of 4
 // for all, the long cases of rows of 128 take 37 instead of 31 us forward, 60 instead of 46 backward and 85 instead of 79 into
-// the cache, a call of 771 tokens with rows of 80, of which pieces of 8 leave three lanes of eight idle, 7.8 instead of 8.5.)
+// the cache.)
 #pragma once
 
 #include <type_traits>
@@ -54,47 +55,52 @@ int validate_rows(const fdma_rows* r, const int64_t n[3], int d, bool written);
 RowsView rows_view(const fdma_rows& r);
 
 // Pairs of a lane.
-inline int piece_of(int d, int rot) { return d % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+inline int piece_of(int d, int rot, bool adj) { return d % 16 == 0 && (adj || rot % 16 == 0) ? 8 : 4; }
 
-// Calls f(P, LPR, ADJ) with the constants that a row of d values with rot turned ones takes.  (LPR is 4 to 16 with
-// pieces of 8, 8 to 32 with pieces of 4.)
+// Lanes of a row.  (16384 tokens of 20 + 5 heads, forward / backward, us: rows of 96 in six lanes 31 / 47, in eight 40 / 59; of 80
+// in five 32 / 51, in eight 39 / 60.  64 + 8 rows of 32 in two 32 / 54, in four 42 / 62.)
+inline int lanes_of(int d, int rot, bool adj) {
+  if (piece_of(d, rot, adj) == 8) return d <= 32 ? 2 : d <= 64 ? 4 : d <= 80 ? 5 : d <= 96 ? 6 : d <= 128 ? 8 : 16;
+  return d <= 64 ? 8 : d <= 128 ? 16 : 32;
+}
+// Calls f(P, LPR, ADJ) with the constants that a row of d values with rot turned ones takes.
 template <typename F>
 void with_layout(int d, int rot, bool adj, F&& f) {
   auto with = [&](auto P, auto L) {
+    if (lanes_of(d, rot, adj) != decltype(L)::value || piece_of(d, rot, adj) != decltype(P)::value) return;
     if (adj) f(P, L, std::true_type{});
     else f(P, L, std::false_type{});
   };
-  using std::integral_constant;
-  if (piece_of(d, rot) == 8) {
-    if (d <= 64) with(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-    else if (d <= 128) with(integral_constant<int, 8>{}, integral_constant<int, 8>{});
-    else with(integral_constant<int, 8>{}, integral_constant<int, 16>{});
-  } else {
-    if (d <= 64) with(integral_constant<int, 4>{}, integral_constant<int, 8>{});
-    else if (d <= 128) with(integral_constant<int, 4>{}, integral_constant<int, 16>{});
-    else with(integral_constant<int, 4>{}, integral_constant<int, 32>{});
-  }
+  using Eight = std::integral_constant<int, 8>;
+  using Four = std::integral_constant<int, 4>;
+  with(Eight{}, std::integral_constant<int, 2>{});
+  with(Eight{}, std::integral_constant<int, 4>{});
+  with(Eight{}, std::integral_constant<int, 5>{});
+  with(Eight{}, std::integral_constant<int, 6>{});
+  with(Eight{}, std::integral_constant<int, 8>{});
+  with(Eight{}, std::integral_constant<int, 16>{});
+  with(Four{}, std::integral_constant<int, 8>{});
+  with(Four{}, std::integral_constant<int, 16>{});
+  with(Four{}, std::integral_constant<int, 32>{});
 }
 // Rows of a pass.
-inline int pass_rows(int d, int rot) {
-  const int l = d <= 64 ? 4 : d <= 128 ? 8 : 16;
-  return 32 / (piece_of(d, rot) == 8 ? l : 2 * l);
-}
+inline int pass_rows(int d, int rot, bool adj) { return 32 / lanes_of(d, rot, adj); }
 
 // Where a lane's values lie in a row.
 struct Lane {
   int ca, cb;  // columns of its two pieces of P values
   int apart;   // cb - ca
-  bool in;     // 2 P l < d
+  bool in;     // 2 P l < d, and the row is one
   // whether the pairs of piece a (halves: all of them) and of piece b (adjacent) are turned, and where their angles begin
   bool turned, turned_b;
   int ta, tb;
 };
 
-template <int P, bool ADJ>
-__device__ __forceinline__ Lane lane_of(const NormRopeView& v, int l) {
+// Lane l of row g of a pass.
+template <int P, int LPR, bool ADJ>
+__device__ __forceinline__ Lane lane_of(const NormRopeView& v, int l, int g) {
   Lane r;
-  r.in = 2 * P * l < v.d;
+  r.in = 2 * P * l < v.d && g < 32 / LPR;
   if (ADJ) {
     r.ca = P * l;
     r.cb = (v.d >> 1) + P * l;
@@ -336,11 +342,30 @@ __device__ __forceinline__ void turn_shared(Pairs<P>& x, uint32_t row, uint32_t 
   if (ADJ && n.turned_b) some(P / 4, P / 4, row + 4 * n.tb);
 }
 
+// op over a row's lanes, the same in all of them.  Every lane of the warp calls it.
+template <int LPR, typename T, typename F>
+__device__ __forceinline__ T row_all(T x, F&& op) {
+  if constexpr ((LPR & (LPR - 1)) == 0) {
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  } else {
+    static_assert(LPR == 5 || LPR == 6, "lanes of a row");
+    const int lane = threadIdx.x & 31, l = lane % LPR, first = lane - l;
+    auto behind = [&](T y, int k) { return __shfl_sync(0xffffffffu, y, first + (l + k < LPR ? l + k : l + k - LPR)); };
+    if (LPR == 6) {
+      const T y = op(x, behind(x, 3));
+      x = op(op(y, behind(y, 1)), behind(y, 2));
+    } else {
+      const T y = op(x, behind(x, 1));
+      x = op(op(y, behind(y, 2)), behind(x, 4));
+    }
+    return __shfl_sync(0xffffffffu, x, first);  // (each lane has added in an order of its own)
+  }
+}
 template <int LPR>
 __device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  return row_all<LPR>(x, [](float a, float b) { return a + b; });
 }
 
 // The sum of a lane's products.

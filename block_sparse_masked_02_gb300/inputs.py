@@ -311,10 +311,10 @@ def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=No
     return _run(guard, _launch_norm_rope_bwd, args, q, k, dq_out, dk_out, (q_weight, k_weight), g, want_dweight, workspace, sp)
 
 
-def norm_rope_bwd_workspace(q, k=None, *, q_weight=None, k_weight=None, rope=None):
+def norm_rope_bwd_workspace(q, k=None, *, q_weight=None, k_weight=None, rope=None, interleaved=False):
     """A workspace for `norm_rope_bwd` of these inputs."""
     _check_device(q, k, q_weight, k_weight, rope)
-    args = _norm_rope_args(q, k, q_weight, k_weight, rope, None, 0, False, True, 1.0)
+    args = _norm_rope_args(q, k, q_weight, k_weight, rope, None, 0, interleaved, True, 1.0)
     return torch.empty(load().fdma_norm_rope_bwd_workspace_size(args), dtype=torch.uint8, device=q.device)
 
 

@@ -227,7 +227,7 @@ def test_in_place_and_strided_outputs(I, interleaved):
     wide[:, :, 6:8, :128] = 3
     assert (wide == 3).all()
     dq, dk = c.dq.clone(), c.dk.clone()
-    ws = I.norm_rope_bwd_workspace(c.q, c.k, q_weight=c.w[0], k_weight=c.w[1])
+    ws = I.norm_rope_bwd_workspace(c.q, c.k, interleaved=interleaved, **c.kw)
     dw = torch.full_like(c.w[0], 9.0)
     got = I.norm_rope_bwd(c.q, c.k, dq, dk, grads=(dq, dk, dw, None), workspace=ws, **kw)
     assert got[0] is dq and got[2] is dw
@@ -393,6 +393,8 @@ APPENDS = [  # news, olds, Hq, Hkv, d, page, rot, weight
     ([0, 7], [0, 9], 5, 5, 48, 64, 0, "shared"),
     ([130, 70], [1, 64], 16, 4, 128, 64, 64, None),
     ([2] * 40, list(range(40)), 4, 1, 16, 16, None, "head"),
+    ([20, 1], [7, 300], 13, 7, 80, 16, 48, "head"),
+    ([3, 9], [2, 30], 7, 2, 32, 32, 32, "shared"),
 ]
 
 
