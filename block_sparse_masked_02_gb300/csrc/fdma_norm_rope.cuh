@@ -1,14 +1,14 @@
 // The norm of a row (one token's values of one head) and the rotation of its pairs, as the
 // kernels of fdma_norm_rope.cu and the cache write in fdma_cache.cu share them.
 //
-// A row is held by LPR lanes (with pieces of 8 also five or six), two pieces of P values a lane, P pairs (a[i], b[i]) in all.  The pieces a of a row's
+// A row is held by LPR lanes (powers of two, five, six or ten), two pieces of P values a lane, P pairs (a[i], b[i]) in all.  The pieces a of a row's
 // lanes follow each other, and so do the pieces b (16 bytes of a lane beside those of the next: with both pieces of a lane side
 // by side, every store wrote half a sector, and adjacent pairs took 42 instead of 31 us forward, 68 instead of 46 backward):
 //   halves    lane l of the first rot / (2 P) holds columns P l + i and rot / 2 + P l + i, so both values
 //             of a pair are in one lane; the m lanes behind hold, by their number u from 0 on, columns rot + P u + i and
 //             rot + P m + P u + i;
 //   adjacent  lane l holds columns P l + i and d / 2 + P l + i, P / 2 whole pairs each.
-// Lanes with 2 P l >= d hold zeros, as do the last two of a warp where LPR is five or six.  A warp holds 32 / LPR rows at
+// Lanes with 2 P l >= d hold zeros, as do the last two of a warp where LPR is no power of two.  A warp holds 32 / LPR rows at
 // once, all of one tensor: a pass.  Arithmetic is on
 // pairs of fp32 values, one instruction for two.
 //
@@ -58,10 +58,11 @@ RowsView rows_view(const fdma_rows& r);
 inline int piece_of(int d, int rot, bool adj) { return d % 16 == 0 && (adj || rot % 16 == 0) ? 8 : 4; }
 
 // Lanes of a row.  (16384 tokens of 20 + 5 heads, forward / backward, us: rows of 96 in six lanes 31 / 47, in eight 40 / 59; of 80
-// in five 32 / 51, in eight 39 / 60.  64 + 8 rows of 32 in two 32 / 54, in four 42 / 62.)
+// in five 32 / 51, in eight 39 / 60; of 72 in ten (pieces of 4) 35 / 63, in sixteen 41 / 68.  64 + 8 rows of 32 in two 32 / 54, in
+// four 42 / 62.)
 inline int lanes_of(int d, int rot, bool adj) {
   if (piece_of(d, rot, adj) == 8) return d <= 32 ? 2 : d <= 64 ? 4 : d <= 80 ? 5 : d <= 96 ? 6 : d <= 128 ? 8 : 16;
-  return d <= 64 ? 8 : d <= 128 ? 16 : 32;
+  return d <= 64 ? 8 : d <= 80 ? 10 : d <= 128 ? 16 : 32;
 }
 // Calls f(P, LPR, ADJ) with the constants that a row of d values with rot turned ones takes.
 template <typename F>
@@ -80,6 +81,7 @@ void with_layout(int d, int rot, bool adj, F&& f) {
   with(Eight{}, std::integral_constant<int, 8>{});
   with(Eight{}, std::integral_constant<int, 16>{});
   with(Four{}, std::integral_constant<int, 8>{});
+  with(Four{}, std::integral_constant<int, 10>{});
   with(Four{}, std::integral_constant<int, 16>{});
   with(Four{}, std::integral_constant<int, 32>{});
 }
@@ -350,13 +352,14 @@ __device__ __forceinline__ T row_all(T x, F&& op) {
     for (int o = LPR / 2; o > 0; o >>= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
     return x;
   } else {
-    static_assert(LPR == 5 || LPR == 6, "lanes of a row");
+    static_assert(LPR == 5 || LPR == 6 || LPR == 10, "lanes of a row");
     const int lane = threadIdx.x & 31, l = lane % LPR, first = lane - l;
     auto behind = [&](T y, int k) { return __shfl_sync(0xffffffffu, y, first + (l + k < LPR ? l + k : l + k - LPR)); };
     if (LPR == 6) {
       const T y = op(x, behind(x, 3));
       x = op(op(y, behind(y, 1)), behind(y, 2));
     } else {
+      if (LPR == 10) x = op(x, behind(x, 5));
       const T y = op(x, behind(x, 1));
       x = op(op(y, behind(y, 2)), behind(x, 4));
     }
