@@ -356,10 +356,11 @@ struct BwdPlan {
 BwdPlan bwd_plan(const fdma_rel_args& r, int64_t B, bool causal) {
   BwdPlan p;
   const int nrb = row_blocks(r), ncb = r.Nk / 8, bands = (nrb + ncb - 1 + 31) / 32;
-  // groups of eight warps that share a band: walks of about kBwdSteps block rows, shorter ones where that is too few
-  // CTAs for the machine
-  const int64_t fill = (kBwdCtas + B * r.H * bands - 1) / (B * r.H * bands), most = (nrb + kWarps - 1) / kWarps;
-  int64_t groups = (nrb + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps);
+  // groups of eight warps that share a band, which runs through `rows` block rows at most: walks of about kBwdSteps of them,
+  // shorter ones where that is too few CTAs for the machine
+  const int rows = nrb < ncb + 31 ? nrb : ncb + 31;
+  const int64_t fill = (kBwdCtas + B * r.H * bands - 1) / (B * r.H * bands), most = (rows + kWarps - 1) / kWarps;
+  int64_t groups = (rows + kWarps * kBwdSteps - 1) / (kWarps * kBwdSteps);
   if (groups < fill) groups = fill < most ? fill : most;
   p.parts = kWarps * static_cast<int>(groups);
   p.bands = bands;
