@@ -15,9 +15,10 @@
 //
 // 16384 tokens of 16 + 4 heads of 128, one weight a tensor, inputs not in L2: forward 31 us (176 MB, 5.6 TB/s; a copy of
 // as much 26), backward 46 us (260 MB, 5.6 TB/s; 38), of which the sum of the weights' parts 2.  Two sequences of 4096 tokens of 32 + 8
-// heads with a weight each, backward: 58 us (253 MB, 4.4 TB/s): of some 420 instructions a pass 130 are then spent on a new
-// token.  What bounds both is issue and latency (issue slots 62 and 51 % busy at 24 and 16 warps an SM), no longer the
-// wait for memory (stalls on it: 0.1 of 7 cycles an instruction).
+// heads with a weight each, half of the columns turned, backward: 54 us (253 MB, 4.7 TB/s), as about 130 of 400 instructions a
+// pass are then spent on a new token.  What bounds both is issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an
+// SM), no longer the wait for memory (stalls on it: 0.3 of 8 cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1
+// take 35 and 56 us for 75 MB, as a key's row then has a pass to itself.
 //
 // Steps that led here (the first case forward / backward, us): a row a lane group, addresses for each 52 / 102; a warp a token,
 // arithmetic on pairs, pieces of 16 bytes 39 / 80; rows on their way in shared memory 36 / 70; angles and weights there too 34
@@ -548,7 +549,7 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   w.heads = by_head(*a);
   w.rpw = pass_rows(a->d, p.v.rot, a->interleaved != 0);
   const dim3 grid(w.heads ? a->Hq + a->Hk : 2, (a->d + 31) / 32);
-  // (launched behind: 9.1 -> 8.4 us for 771 tokens of 5 + 5 heads)
+  // (launched behind: 8.4 instead of 9.1 us for 771 tokens of 5 + 5 heads)
   return launch_behind(weight_sum_kernel, grid, 1024, cs, w) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
 }
 

@@ -28,7 +28,7 @@ constexpr int kSpan = 32 * 8 + 7;  // diagonals of a warp
 constexpr int kPart = 264;
 constexpr int64_t kMostCtas = 1 << 28;  // of a backward (their parts take 283 GB)
 // Block rows of a backward walk, and the CTAs that a call should have if its walks get shorter for it.  (Four causal heads of
-// 16384 x 16384 / 3 x 6 of 1001 x 1528, us: 8 steps 175 / 15.9, 16: 172 / 15.9, 24: 175 / 16.3; 600 CTAs 172 / 18.3, 150: 172 / 22.)
+// 16384 x 16384 / 3 x 6 of 1001 x 1528, us: 8 steps 175 / 15.9, 16: 171 / 15.9, 24: 175 / 16.3; 600 CTAs 172 / 18.3, 150: 172 / 22.)
 constexpr int kBwdSteps = 16, kBwdCtas = 456;
 
 struct RelView {
