@@ -15,8 +15,8 @@
 //
 // 16384 tokens of 16 + 4 heads of 128, one weight a tensor, inputs not in L2: forward 31 us (176 MB, 5.6 TB/s; a copy of
 // as much 26), backward 46 us (260 MB, 5.6 TB/s; 38), of which the sum of the weights' parts 2.  Two sequences of 4096 tokens of 32 + 8
-// heads with a weight each, half of the columns turned, backward: 54 us (253 MB, 4.7 TB/s), as about 130 of 400 instructions a
-// pass are then spent on a new token.  What bounds both is issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an
+// heads with a weight each, half of the columns turned, backward: 49 us (253 MB, 5.2 TB/s; 37), as every pass is then a new token's
+// (54 us where such a walk went through the loop over a token's passes, and found every row's address from its token's number).  What bounds both is issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an
 // SM), no longer the wait for memory (stalls on it: 0.3 of 8 cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1
 // take 35 and 56 us for 75 MB, as a key's row then has a pass to itself.
 //
@@ -47,12 +47,15 @@ struct Token {
   uint32_t n;
   int b;
 };
-__device__ __forceinline__ void wrap(const TokenLine& t, Token& k) {
-  if (t.batches > 1 && k.n >= static_cast<uint32_t>(t.N)) {
-    const uint32_t more = k.n / t.N;
-    k.b += more;
-    k.n -= more * t.N;
-  }
+__device__ __forceinline__ bool wrap(const TokenLine& t, Token& k) {
+  if (t.batches == 1 || k.n < static_cast<uint32_t>(t.N)) return false;
+  const uint32_t more = k.n / t.N;
+  k.b += more;
+  k.n -= more * t.N;
+  return true;
+}
+__device__ __forceinline__ uint16_t* row_of(const RowsView& r, const Token& k, int64_t first) {
+  return r.p + k.b * r.st[0] + k.n * r.st[1] + first;
 }
 
 // Position of a token before it is checked.
@@ -97,7 +100,8 @@ __device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const L
 }
 
 // Steps of a warp that are on their way at once: 4 KB of rows, backward 6 KB.  (Forward 3 and 6 KB: 31.1 and 32.4 us
-// against 31.2; backward 4 and 8: 48.2 and 46.7 against 46.0.)  Angles of a token more than steps.
+// against 31.2; backward 4 and 8: 48.2 and 46.7 against 46.0.)  There are angles of a token more than steps, where a token
+// has several (the last of one token and the first of the next share a slot's turn), else as many.
 template <int P, bool BACK>
 constexpr int kSlots = BACK ? 24 / P : 32 / P;
 template <int P, bool BACK>
@@ -106,7 +110,8 @@ constexpr int kRingBytes = kSlots<P, BACK> * (BACK ? 2 : 1) * Ring<P>::kSlot;
 // HEADS: every head has a weight of its own.
 template <int P, int LPR, bool ADJ, bool HEADS, bool BACK>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kernel(const __grid_constant__ WalkView p) {
-  constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kSlots<P, BACK>, STEP = BACK ? 2 : 1, WEIGHT = 256 * P;
+  constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kSlots<P, BACK>, STEP = BACK ? 2 : 1, WEIGHT = 256 * P,
+                TURNS = HEADS ? SLOTS : SLOTS + 1;
   static_assert(kRingBytes<P, BACK> >= RPW * COLS * sizeof(float) || !BACK, "the sums take the rings' place");
   extern __shared__ __align__(16) uint8_t smem[];  // weight | rings | angles
   if (BACK) launch_dependents();
@@ -121,13 +126,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   const uint32_t step = p.plan.ctas[side] * kWarps, tok0 = (cta - chunk * p.plan.ctas[side]) * kWarps + warp;
   const uint32_t base = smem_u32(smem), weight = base + lane * 16;
   const Ring<P> ring(base + WEIGHT + warp * kRingBytes<P, BACK>, lane);
-  const uint32_t table = base + WEIGHT + kWarps * kRingBytes<P, BACK> + warp * (SLOTS + 1) * p.plan.table;
+  const uint32_t table = base + WEIGHT + kWarps * kRingBytes<P, BACK> + warp * TURNS * p.plan.table;
   const int64_t by_x = RPW * x.st[2], by_g = BACK ? RPW * gr.st[2] : 0, by_out = RPW * out.st[2];
   const int h_first = q_first * RPW + g, h_end = at.in ? H : 0;
   const int64_t x_first = h_first * x.st[2] + at.ca, g_first = BACK ? h_first * gr.st[2] + at.ca : 0,
                 out_first = h_first * out.st[2] + at.ca;
 
-  // what is fetched next
+  // what is fetched next (HEADS: a token's one pass, `hop` values behind the last one's)
   Token next{tok0, 0};
   wrap(p.line, next);
   uint32_t tok_next = tok0;
@@ -135,8 +140,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   int q_next = q_last, h_next = 0, row_next = 0;
   uint32_t left_out = 0, begun = 0;  // bit t % 32: token t of the walk is left out; tokens begun
   const uint16_t *x_next = nullptr, *g_next = nullptr;
+  if (HEADS) {
+    x_next = row_of(x, next, x_first);
+    if (BACK) g_next = row_of(gr, next, g_first);
+  }
+  const int64_t hop_x = static_cast<int64_t>(step) * x.st[1], hop_g = BACK ? static_cast<int64_t>(step) * gr.st[1] : 0,
+                hop_out = static_cast<int64_t>(step) * out.st[1];
   auto start = [&](int slot) {
-    if (q_next == q_last && tok_next < p.line.tokens) {
+    if ((HEADS || q_next == q_last) && tok_next < p.line.tokens) {
       int pos = pos_next;
       if (p.v.pos != nullptr) {  // (else they are inside the table)
         pos = checked_position(p.v, pos, p.err);
@@ -147,19 +158,35 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       __syncwarp();  // (these angles may take the place of those that were read last)
       if (pos >= 0) {
         const float* angles = p.v.rope + static_cast<int64_t>(pos) * p.v.rot;
-        for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(table + row_next * p.plan.table + 4 * i, angles + i, 16);
+        const uint32_t to = table + (HEADS ? slot : row_next) * p.plan.table;
+        for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(to + 4 * i, angles + i, 16);
       }
-      row_next = row_next == SLOTS ? 0 : row_next + 1;
-      x_next = x.p + next.b * x.st[0] + next.n * x.st[1] + x_first;
-      if (BACK) g_next = gr.p + next.b * gr.st[0] + next.n * gr.st[1] + g_first;
-      h_next = pos < 0 ? h_end : h_first;
-      q_next = q_first;
+      if (HEADS) {
+        const bool real = pos >= 0 && h_first < h_end;
+        if (!BACK || p.v.norm) ring.copy(STEP * slot, x_next, at.apart, real);
+        if (BACK) ring.copy(STEP * slot + 1, g_next, at.apart, real);
+      } else {
+        row_next = row_next + 1 == TURNS ? 0 : row_next + 1;
+        x_next = row_of(x, next, x_first);
+        if (BACK) g_next = row_of(gr, next, g_first);
+        h_next = pos < 0 ? h_end : h_first;
+        q_next = q_first;
+      }
       tok_next += step;
       next.n += step;
-      wrap(p.line, next);
+      if (HEADS) {
+        x_next += hop_x;
+        if (BACK) g_next += hop_g;
+        if (wrap(p.line, next)) {
+          x_next = row_of(x, next, x_first);
+          if (BACK) g_next = row_of(gr, next, g_first);
+        }
+      } else {
+        wrap(p.line, next);
+      }
       if (tok_next < p.line.tokens) pos_next = position_of(p.v, next.b, next.n);
     }
-    if (q_next < q_last) {
+    if (!HEADS && q_next < q_last) {
       const bool real = h_next < h_end;
       if (!BACK || p.v.norm) ring.copy(STEP * slot, x_next, at.apart, real);
       if (BACK) ring.copy(STEP * slot + 1, g_next, at.apart, real);
@@ -182,61 +209,74 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   wrap(p.line, now);
   int slot = 0, row = 0;
   uint32_t done = 0;
+  // a pass of a token: this lane's row is head h, and goes to `to`
+  auto pass = [&](uint16_t* to, int h, uint32_t angles, bool left) {
+    const uint32_t half = 2 * p.v.rot;
+    if (left) {
+      if (BACK && h < h_end) store_raw<P>(to, at.apart, no_raw<P>());
+    } else {
+      Pairs<P> d = widen<P, ADJ>(ring.get(STEP * slot + STEP - 1));
+      if constexpr (BACK) {
+        if (p.v.norm) {
+          Pairs<P> xs = widen<P, ADJ>(ring.get(STEP * slot));
+          float by;
+          const float r = row_rsqrt<LPR>(p.v, xs, by);
+          turn_shared<true, ADJ>(d, angles, half, at);
+          scale(d, r);
+#pragma unroll
+          for (int e = 0; e < P / 2; ++e) {
+            acc.a[e] = fma2(d.a[e], xs.a[e], acc.a[e]);
+            acc.b[e] = fma2(d.b[e], xs.b[e], acc.b[e]);
+          }
+          multiply_shared(d, weight);
+          const float m = row_sum<LPR>(dot(d, xs)) * p.v.inv_d * (-r * r);
+          const uint64_t m2 = f2(m, m);
+#pragma unroll
+          for (int e = 0; e < P / 2; ++e) {
+            d.a[e] = fma2(xs.a[e], m2, d.a[e]);
+            d.b[e] = fma2(xs.b[e], m2, d.b[e]);
+          }
+          if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
+        } else {
+          turn_shared<true, ADJ>(d, angles, half, at);
+        }
+      } else {
+        if (p.v.norm) {
+          float by;
+          scale(d, row_rsqrt<LPR>(p.v, d, by));
+          multiply_shared(d, weight);
+        }
+        turn_shared<false, ADJ>(d, angles, half, at);
+      }
+      if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
+    }
+  };
+  uint16_t* to = HEADS ? row_of(out, now, out_first) : nullptr;
   for (uint32_t tok = tok0; tok < p.line.tokens; tok += step) {
     const bool left = (left_out >> (done & 31u)) & 1u;
-    const uint32_t angles = table + row * p.plan.table, half = 2 * p.v.rot;
-    uint16_t* to = out.p + now.b * out.st[0] + now.n * out.st[1] + out_first;
-    int h = h_first;
+    if (!HEADS) to = row_of(out, now, out_first);
     cp_async_wait<SLOTS - 1>();
     __syncwarp();  // the angles, which other lanes fetched
-#pragma unroll 1
-    for (int q = q_first; q < q_last; ++q, h += RPW, to += by_out) {
-      cp_async_wait<SLOTS - 1>();
-      if (left) {
-        if (BACK && h < h_end) store_raw<P>(to, at.apart, no_raw<P>());
-      } else {
-        Pairs<P> d = widen<P, ADJ>(ring.get(STEP * slot + STEP - 1));
-        if constexpr (BACK) {
-          if (p.v.norm) {
-            Pairs<P> xs = widen<P, ADJ>(ring.get(STEP * slot));
-            float by;
-            const float r = row_rsqrt<LPR>(p.v, xs, by);
-            turn_shared<true, ADJ>(d, angles, half, at);
-            scale(d, r);
-#pragma unroll
-            for (int e = 0; e < P / 2; ++e) {
-              acc.a[e] = fma2(d.a[e], xs.a[e], acc.a[e]);
-              acc.b[e] = fma2(d.b[e], xs.b[e], acc.b[e]);
-            }
-            multiply_shared(d, weight);
-            const float m = row_sum<LPR>(dot(d, xs)) * p.v.inv_d * (-r * r);
-            const uint64_t m2 = f2(m, m);
-#pragma unroll
-            for (int e = 0; e < P / 2; ++e) {
-              d.a[e] = fma2(xs.a[e], m2, d.a[e]);
-              d.b[e] = fma2(xs.b[e], m2, d.b[e]);
-            }
-            if (__any_sync(0xffffffffu, by != 1.f)) scale(d, by);
-          } else {
-            turn_shared<true, ADJ>(d, angles, half, at);
-          }
-        } else {
-          if (p.v.norm) {
-            float by;
-            scale(d, row_rsqrt<LPR>(p.v, d, by));
-            multiply_shared(d, weight);
-          }
-          turn_shared<false, ADJ>(d, angles, half, at);
-        }
-        if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
-      }
+    if (HEADS) {
+      pass(to, h_first, table + slot * p.plan.table, left);
       start(slot);
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    } else {
+      const uint32_t angles = table + row * p.plan.table;
+      int h = h_first;
+#pragma unroll 1
+      for (int q = q_first; q < q_last; ++q, h += RPW, to += by_out) {
+        cp_async_wait<SLOTS - 1>();
+        pass(to, h, angles, left);
+        start(slot);
+        slot = slot + 1 == SLOTS ? 0 : slot + 1;
+      }
+      row = row + 1 == TURNS ? 0 : row + 1;
     }
-    row = row == SLOTS ? 0 : row + 1;
     if (p.v.pos != nullptr) ++done;
     now.n += step;
-    wrap(p.line, now);
+    to += hop_out;
+    if (wrap(p.line, now)) to = row_of(out, now, out_first);
   }
   cp_async_wait_all();
   if (!BACK || p.part == nullptr) return;
@@ -307,7 +347,7 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
             rpw = pass_rows(a.d, rot, a.interleaved != 0);
   const int slots = back ? 24 / piece : 32 / piece;
   r.table = 4 * rot;
-  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (slots + 1) * r.table);
+  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (by_head(a) ? slots : slots + 1) * r.table);
   int per_sm = kSmemPerSm / (r.smem + 1024);
   if (per_sm > ctas_per_sm(piece, back)) per_sm = ctas_per_sm(piece, back);
   const int64_t ctas = 152 * per_sm;
