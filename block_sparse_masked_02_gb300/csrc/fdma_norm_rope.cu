@@ -63,6 +63,7 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
   return v.pos != nullptr ? v.pos[b * v.pos_st[0] + n * v.pos_st[1]] : v.first + n;
 }
 
+constexpr int kMostChunks = 16;
 // How the work is dealt out: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each with ctas[s]
 // CTAs.
 struct WalkPlan {
@@ -341,27 +342,17 @@ int passes_of(int H, int rows) { return (H + rows - 1) / rows; }
 
 bool by_head(const fdma_norm_rope_args& a) { return a.q_weight_head != 0 || a.k_weight_head != 0; }
 
-WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
-  WalkPlan r{};
-  const int rot = a.rope != nullptr ? a.rot : 0, piece = piece_of(a.d, rot, a.interleaved != 0),
-            rpw = pass_rows(a.d, rot, a.interleaved != 0);
-  const int slots = back ? 24 / piece : 32 / piece;
-  r.table = 4 * rot;
-  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (by_head(a) ? slots : slots + 1) * r.table);
-  int per_sm = kSmemPerSm / (r.smem + 1024);
-  if (per_sm > ctas_per_sm(piece, back)) per_sm = ctas_per_sm(piece, back);
-  const int64_t ctas = 152 * per_sm;
-  const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
-  const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
-  r.per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
+// The chunks of `per` passes with their CTAs, and what it costs the last warp (passes, times 3).
+int64_t deal(WalkPlan& r, const int (&q)[2], int per, int64_t tokens, int64_t ctas) {
+  r.per = per;
   // A token costs a chunk its passes and two thirds of one for what is done once (190 of 284 instructions, backward; the last
   // chunk counts as a whole one).  CTAs go by that, and, as a warp has whole tokens, by which of the two whole numbers
   // next to the even share of q's leaves less to the last warp of either.  (By passes alone: 34 and 53 us; with as much as a pass
   // for what is done once 33.6 and 48.9, against 31.2 and 46.)
   int64_t cost[2], all = 0;
   for (int s = 0; s < 2; ++s) {
-    r.chunks[s] = (q[s] + r.per - 1) / r.per;
-    cost[s] = 3 * (q[s] < r.per ? q[s] : r.per) + 2;
+    r.chunks[s] = (q[s] + per - 1) / per;
+    cost[s] = 3 * (q[s] < per ? q[s] : per) + 2;
     all += r.chunks[s] * cost[s];
   }
   // tokens of a warp of n CTAs, and as well the CTAs whose warps have at most n
@@ -379,6 +370,37 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
     r.ctas[1] = static_cast<int>(m);
   }
   r.grid = r.chunks[0] * r.ctas[0] + r.chunks[1] * r.ctas[1];
+  return best;
+}
+
+WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
+  WalkPlan r{};
+  const int rot = a.rope != nullptr ? a.rot : 0, piece = piece_of(a.d, rot, a.interleaved != 0),
+            rpw = pass_rows(a.d, rot, a.interleaved != 0);
+  const int slots = back ? 24 / piece : 32 / piece;
+  r.table = 4 * rot;
+  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (by_head(a) ? slots : slots + 1) * r.table);
+  int per_sm = kSmemPerSm / (r.smem + 1024);
+  if (per_sm > ctas_per_sm(piece, back)) per_sm = ctas_per_sm(piece, back);
+  const int64_t ctas = 152 * per_sm;
+  const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
+  const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
+  const int per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
+  int64_t best = deal(r, q, per, tokens, ctas);
+  // A warp has whole tokens of a chunk: where that is few, the last one can have twice the even share, and other chunks
+  // leave it less.  (1000 tokens of 64 + 8 heads of 128, forward / backward: 8.9 / 15.9 us, 9.6 / 18.4 without; 2500:
+  // 20.5 / 29.1, 22.9 / 37.6.  What is less than a sixteenth by this count is no gain: up to 5 % slower.)
+  const int64_t even = tokens * (3 * (q[0] + q[1]) + 4) / (ctas * kWarps);
+  if (per > 1 && best > even + even / 16) {
+    const int most = std::max(q[0], q[1]);
+    for (int c = 1; c <= kMostChunks && c <= most; ++c) {
+      WalkPlan other = r;
+      const int64_t last = deal(other, q, (most + c - 1) / c, tokens, ctas);
+      if (last + last / 16 >= best) continue;
+      best = last;
+      r = other;
+    }
+  }
   r.rows = by_head(a) ? r.per * rpw : 1;
   r.part_bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
   return r;

@@ -703,6 +703,30 @@ def test_walks_of_many_tokens(I):
             assert (np.abs(_np(gw) - dw.sum(0)) <= (16 + 700) * U * dwm.sum(0)).all()
 
 
+# Tokens that leave a warp one to three of them, whole or in chunks of heads.  (A weight's sum: a lane adds fewer than
+# 64 passes, a CTA 32 lanes, and fewer than 2 * 456 parts are added 32 side by side: under the 256 of the tolerance.)
+@pytest.mark.parametrize("B,N,Hq,Hk,d", [(1, 700, 64, 8, 128), (2, 401, 28, 4, 128), (3, 333, 36, 0, 128), (1, 1300, 48, 16, 64),
+                                         (1, 900, 5, 40, 256)])
+def test_tokens_in_chunks_of_heads(I, B, N, Hq, Hk, d):
+    c = Case(I, B, N, Hq, Hk, d, seed=N)
+    _check_forward(c, I.norm_rope(c.q, c.k, **c.kw))
+    _check_backward(c, I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **c.kw))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hk,d,rot", [(3, 1100, 40, 4, 64, 64), (700, 3, 5, 1, 128, 32), (2, 900, 21, 3, 72, 72)])
+def test_walks_with_a_weight_a_head(I, B, N, Hq, Hk, d, rot):
+    """Several tokens a warp, over the ends of batches, with padding; a warp has one pass of each."""
+    c = Case(I, B, N, Hq, Hk, d, rot, "head", length=N, seed=B)
+    pos = np.random.default_rng(B).integers(0, N, (B, N))
+    pos.flat[::5] = -1
+    pt = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    for kw, p in ((dict(), None), (dict(positions=pt), pos)):
+        qo, ko = torch.full_like(c.q, 7.0), torch.full_like(c.k, 7.0)
+        _check_forward(c, I.norm_rope(c.q, c.k, q_out=qo, k_out=ko, **kw, **c.kw), pos=p)
+        assert p is None or all((x[pt < 0] == 7).all() for x in (qo, ko))
+        _check_backward(c, I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **kw, **c.kw), pos=p)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_of_many_tokens(I, fp8):
     """So many that a warp takes whole tokens, with an empty sequence, a sequence of one and rows behind the last."""
