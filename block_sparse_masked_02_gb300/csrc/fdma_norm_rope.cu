@@ -16,9 +16,10 @@
 // 16384 tokens of 16 + 4 heads of 128, one weight a tensor, inputs not in L2: forward 31 us (176 MB, 5.6 TB/s; a copy of
 // as much 26), backward 46 us (260 MB, 5.6 TB/s; 38), of which the sum of the weights' parts 2.  Two sequences of 4096 tokens of 32 + 8
 // heads with a weight each, half of the columns turned, backward: 49 us (253 MB, 5.2 TB/s; 37), as every pass is then a new token's
-// (54 us where such a walk went through the loop over a token's passes, and found every row's address from its token's number).  What bounds both is issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an
-// SM), no longer the wait for memory (stalls on it: 0.3 of 8 cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1
-// take 35 and 56 us for 75 MB, as a key's row then has a pass to itself.
+// (54 us where such a walk went through the loop over a token's passes, and found every row's address from its token's number).  What bounds both is
+// issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an SM), no longer the wait for memory (stalls on it: 0.3 of 8
+// cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1 take 35 and 55 us for 75 MB, as a key's row then has a pass
+// to itself.
 //
 // Steps that led here (the first case forward / backward, us): a row a lane group, addresses for each 52 / 102; a warp a token,
 // arithmetic on pairs, pieces of 16 bytes 39 / 80; rows on their way in shared memory 36 / 70; angles and weights there too 34
