@@ -65,6 +65,12 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
 }
 
 constexpr int kMostChunks = 16;
+
+// Rows of more than L2 holds (129 MB) are read and written as what it drops first: of those written, the first ones would be gone
+// before a next kernel reads them, and the angles stay.  (336 MB of rows: 119 against 126 us.  84 MB: 31.7 either way, but an
+// attention that follows then finds the outputs in L2.  The backward has no registers for it: 51 against 46, 170 against 175.)
+constexpr int64_t kMostInL2 = 128 << 20;
+
 // How the work is dealt out: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each with ctas[s]
 // CTAs.
 struct WalkPlan {
@@ -82,6 +88,7 @@ struct WalkView {
   RowsView x[2], g[2], out[2];  // g: backward
   float* part;  // backward: [cta][plan.rows][d]; nullptr: no weight's gradient
   int* err;
+  bool pass_l2;  // forward: the rows do not displace what is in L2
 };
 
 template <int P, bool ADJ>
@@ -134,6 +141,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   const int64_t x_first = h_first * x.st[2] + at.ca, g_first = BACK ? h_first * gr.st[2] + at.ca : 0,
                 out_first = h_first * out.st[2] + at.ca;
 
+  uint64_t policy = 0;  // of the rows (forward), as they are read and as they are written
+  if (!BACK) {
+    if (p.pass_l2) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+  }
   // what is fetched next (HEADS: a token's one pass, `hop` values behind the last one's)
   Token next{tok0, 0};
   wrap(p.line, next);
@@ -148,6 +160,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   }
   const int64_t hop_x = static_cast<int64_t>(step) * x.st[1], hop_g = BACK ? static_cast<int64_t>(step) * gr.st[1] : 0,
                 hop_out = static_cast<int64_t>(step) * out.st[1];
+  auto copy = [&](int slot, bool real) {
+    if (!BACK) {
+      ring.copy(slot, x_next, at.apart, real, policy);
+    } else {
+      if (p.v.norm) ring.copy(2 * slot, x_next, at.apart, real);
+      ring.copy(2 * slot + 1, g_next, at.apart, real);
+    }
+  };
   auto start = [&](int slot) {
     if ((HEADS || q_next == q_last) && tok_next < p.line.tokens) {
       int pos = pos_next;
@@ -164,9 +184,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
         for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(to + 4 * i, angles + i, 16);
       }
       if (HEADS) {
-        const bool real = pos >= 0 && h_first < h_end;
-        if (!BACK || p.v.norm) ring.copy(STEP * slot, x_next, at.apart, real);
-        if (BACK) ring.copy(STEP * slot + 1, g_next, at.apart, real);
+        copy(slot, pos >= 0 && h_first < h_end);
       } else {
         row_next = row_next + 1 == TURNS ? 0 : row_next + 1;
         x_next = row_of(x, next, x_first);
@@ -189,9 +207,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       if (tok_next < p.line.tokens) pos_next = position_of(p.v, next.b, next.n);
     }
     if (!HEADS && q_next < q_last) {
-      const bool real = h_next < h_end;
-      if (!BACK || p.v.norm) ring.copy(STEP * slot, x_next, at.apart, real);
-      if (BACK) ring.copy(STEP * slot + 1, g_next, at.apart, real);
+      copy(slot, h_next < h_end);
       x_next += by_x;
       if (BACK) g_next += by_g;
       h_next += RPW;
@@ -250,7 +266,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
         }
         turn_shared<false, ADJ>(d, angles, half, at);
       }
-      if (h < h_end) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
+      if (h < h_end) {
+        if (BACK) store_raw<P>(to, at.apart, narrow<P, ADJ>(d));
+        else store_raw<P>(to, at.apart, narrow<P, ADJ>(d), policy);
+      }
     }
   };
   uint16_t* to = HEADS ? row_of(out, now, out_first) : nullptr;
@@ -514,6 +533,7 @@ void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
   p.line = {a.N, a.B, static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N)};
   p.H[0] = a.Hq;
   p.H[1] = a.Hk;
+  p.pass_l2 = static_cast<int64_t>(a.B) * a.N * (a.Hq + a.Hk) * a.d > kMostInL2 / 2;
   for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot, a.interleaved != 0));
 }
 

@@ -158,6 +158,19 @@ __device__ __forceinline__ void store_raw(uint16_t* piece, int apart, const Raw<
     *reinterpret_cast<uint2*>(piece + apart) = make_uint2(r.w[2], r.w[3]);
   }
 }
+// ... with a policy for L2.
+template <int P>
+__device__ __forceinline__ void store_raw(uint16_t* piece, int apart, const Raw<P>& r, uint64_t policy) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint16_t* to = piece + k * apart;
+    const uint32_t* w = r.w + k * P / 2;
+    if constexpr (P == 8)
+      asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "l"(policy) : "memory");
+    else
+      asm volatile("st.global.L2::cache_hint.v2.b32 [%0], {%1, %2}, %3;" ::"l"(to), "r"(w[0]), "r"(w[1]), "l"(policy) : "memory");
+  }
+}
 
 // Rows on their way, in shared memory: a slot holds a lane's two pieces of a pass, where only this lane writes and reads
 // them, so that a warp has many passes in flight without registers for them and without a barrier.
@@ -176,6 +189,17 @@ struct Ring {
     } else {
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(piece), "r"(bytes) : "memory");
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to + 64 * P), "l"(piece + apart), "r"(bytes) : "memory");
+    }
+  }
+  // ... with a policy for L2.
+  __device__ __forceinline__ void copy(int slot, const uint16_t* piece, int apart, bool real, uint64_t policy) const {
+    const uint32_t to = at + slot * kSlot, bytes = real ? 2 * P : 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (P == 8)
+        asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(to + k * 64 * P), "l"(piece + k * apart), "r"(bytes), "l"(policy) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global.L2::cache_hint [%0], [%1], 8, %2, %3;" ::"r"(to + k * 64 * P), "l"(piece + k * apart), "r"(bytes), "l"(policy) : "memory");
     }
   }
   __device__ __forceinline__ Raw<P> get(int slot) const {
