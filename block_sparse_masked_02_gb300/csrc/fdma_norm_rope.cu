@@ -68,8 +68,12 @@ constexpr int kMostChunks = 16;
 
 // Rows of more than L2 holds (129 MB) are read and written as what it drops first: of those written, the first ones would be gone
 // before a next kernel reads them, and the angles stay.  (336 MB of rows: 119 against 126 us.  84 MB: 31.7 either way, but an
-// attention that follows then finds the outputs in L2.  The backward has no registers for it: 51 against 46, 170 against 175.)
+// attention that follows then finds the outputs in L2.  The backward has no registers for it: 51 against 46, 170 against 175.
+// It takes one pass a chunk instead: 336 MB 162 against 175 us, 671 MB 314 against 355, but 84 MB 49 against 46.)
 constexpr int64_t kMostInL2 = 128 << 20;
+bool beyond_l2(const fdma_norm_rope_args& a) {
+  return static_cast<int64_t>(a.B) * a.N * (static_cast<int64_t>(a.Hq) + a.Hk) > kMostInL2 / (2 * a.d);
+}
 
 // How the work is dealt out: tensor s (q, k) has chunks[s] chunks of `per` passes (the last of fewer), each with ctas[s]
 // CTAs.
@@ -88,6 +92,7 @@ struct WalkView {
   RowsView x[2], g[2], out[2];  // g: backward
   float* part;  // backward: [cta][plan.rows][d]; nullptr: no weight's gradient
   int* err;
+  bool heads;    // every head has a weight of its own
   bool pass_l2;  // forward: the rows do not displace what is in L2
 };
 
@@ -116,11 +121,11 @@ constexpr int kSlots = BACK ? 24 / P : 32 / P;
 template <int P, bool BACK>
 constexpr int kRingBytes = kSlots<P, BACK> * (BACK ? 2 : 1) * Ring<P>::kSlot;
 
-// HEADS: every head has a weight of its own.
-template <int P, int LPR, bool ADJ, bool HEADS, bool BACK>
+// ONE: a chunk is one pass.
+template <int P, int LPR, bool ADJ, bool ONE, bool BACK>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kernel(const __grid_constant__ WalkView p) {
   constexpr int RPW = 32 / LPR, COLS = 2 * P * LPR, SLOTS = kSlots<P, BACK>, STEP = BACK ? 2 : 1, WEIGHT = 256 * P,
-                TURNS = HEADS ? SLOTS : SLOTS + 1;
+                TURNS = ONE ? SLOTS : SLOTS + 1;
   static_assert(kRingBytes<P, BACK> >= RPW * COLS * sizeof(float) || !BACK, "the sums take the rings' place");
   extern __shared__ __align__(16) uint8_t smem[];  // weight | rings | angles
   if (BACK) launch_dependents();
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
     if (p.pass_l2) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   }
-  // what is fetched next (HEADS: a token's one pass, `hop` values behind the last one's)
+  // what is fetched next (ONE: a token's one pass, `hop` values behind the last one's)
   Token next{tok0, 0};
   wrap(p.line, next);
   uint32_t tok_next = tok0;
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   int q_next = q_last, h_next = 0, row_next = 0;
   uint32_t left_out = 0, begun = 0;  // bit t % 32: token t of the walk is left out; tokens begun
   const uint16_t *x_next = nullptr, *g_next = nullptr;
-  if (HEADS) {
+  if (ONE) {
     x_next = row_of(x, next, x_first);
     if (BACK) g_next = row_of(gr, next, g_first);
   }
@@ -169,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
     }
   };
   auto start = [&](int slot) {
-    if ((HEADS || q_next == q_last) && tok_next < p.line.tokens) {
+    if ((ONE || q_next == q_last) && tok_next < p.line.tokens) {
       int pos = pos_next;
       if (p.v.pos != nullptr) {  // (else they are inside the table)
         pos = checked_position(p.v, pos, p.err);
@@ -180,10 +185,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       __syncwarp();  // (these angles may take the place of those that were read last)
       if (pos >= 0) {
         const float* angles = p.v.rope + static_cast<int64_t>(pos) * p.v.rot;
-        const uint32_t to = table + (HEADS ? slot : row_next) * p.plan.table;
+        const uint32_t to = table + (ONE ? slot : row_next) * p.plan.table;
         for (int i = 4 * lane; i < p.v.rot; i += 128) cp_async16(to + 4 * i, angles + i, 16);
       }
-      if (HEADS) {
+      if (ONE) {
         copy(slot, pos >= 0 && h_first < h_end);
       } else {
         row_next = row_next + 1 == TURNS ? 0 : row_next + 1;
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       }
       tok_next += step;
       next.n += step;
-      if (HEADS) {
+      if (ONE) {
         x_next += hop_x;
         if (BACK) g_next += hop_g;
         if (wrap(p.line, next)) {
@@ -206,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       }
       if (tok_next < p.line.tokens) pos_next = position_of(p.v, next.b, next.n);
     }
-    if (!HEADS && q_next < q_last) {
+    if (!ONE && q_next < q_last) {
       copy(slot, h_next < h_end);
       x_next += by_x;
       if (BACK) g_next += by_g;
@@ -217,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
   };
 #pragma unroll 1
   for (int i = 0; i < SLOTS; ++i) start(i);
-  if (warp == 0) put_weight<P>(weight, load_weight<P, ADJ>(p.v, side, HEADS ? min(h_first, H - 1) : 0, at));
+  if (warp == 0) put_weight<P>(weight, load_weight<P, ADJ>(p.v, side, min(h_first, H - 1), at));
   __syncthreads();
 
   Pairs<P> acc;
@@ -272,13 +277,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
       }
     }
   };
-  uint16_t* to = HEADS ? row_of(out, now, out_first) : nullptr;
+  uint16_t* to = ONE ? row_of(out, now, out_first) : nullptr;
   for (uint32_t tok = tok0; tok < p.line.tokens; tok += step) {
     const bool left = (left_out >> (done & 31u)) & 1u;
-    if (!HEADS) to = row_of(out, now, out_first);
+    if (!ONE) to = row_of(out, now, out_first);
     cp_async_wait<SLOTS - 1>();
     __syncwarp();  // the angles, which other lanes fetched
-    if (HEADS) {
+    if (ONE) {
       pass(to, h_first, table + slot * p.plan.table, left);
       start(slot);
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
@@ -310,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(P, BACK)) norm_rope_kern
     const int r = i / p.v.d, c = i - r * p.v.d;
     float sum = 0.f;
     for (int j = 0; j < kWarps; ++j) {
-      if (HEADS) {
+      if (p.heads) {
         sum += sums[(j * RPW + r) * COLS + c];
       } else {
 #pragma unroll
@@ -399,13 +404,14 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
             rpw = pass_rows(a.d, rot, a.interleaved != 0);
   const int slots = back ? 24 / piece : 32 / piece;
   r.table = 4 * rot;
-  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (by_head(a) ? slots : slots + 1) * r.table);
+  r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (slots + 1) * r.table);
   int per_sm = kSmemPerSm / (r.smem + 1024);
   if (per_sm > ctas_per_sm(piece, back)) per_sm = ctas_per_sm(piece, back);
   const int64_t ctas = 152 * per_sm;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
   const int q[2] = {passes_of(a.Hq, rpw), passes_of(a.Hk, rpw)};
-  const int per = by_head(a) ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
+  const bool one = by_head(a) || (back && beyond_l2(a));
+  const int per = one ? 1 : plan_passes(q[0] + q[1], tokens, ctas * kWarps).per;
   int64_t best = deal(r, q, per, tokens, ctas);
   // A warp has whole tokens of a chunk: where that is few, the last one can have twice the even share, and other chunks
   // leave it less.  (1000 tokens of 64 + 8 heads of 128, forward / backward: 8.9 / 15.9 us, 9.6 / 18.4 without; 2500:
@@ -421,6 +427,7 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
       r = other;
     }
   }
+  if (r.per == 1) r.smem -= kWarps * r.table;  // (as many rows of angles as steps)
   r.rows = by_head(a) ? r.per * rpw : 1;
   r.part_bytes = static_cast<size_t>(r.grid) * r.rows * a.d * sizeof(float);
   return r;
@@ -428,7 +435,6 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
 
 template <bool BACK>
 cudaError_t launch_walk(const fdma_norm_rope_args& a, const WalkView& p, cudaStream_t stream) {
-  const bool heads = by_head(a);
   cudaError_t e = cudaSuccess;
   with_layout(a.d, p.v.rot, a.interleaved != 0, [&](auto P, auto L, auto A) {
     constexpr int kP = decltype(P)::value, kL = decltype(L)::value;
@@ -437,7 +443,7 @@ cudaError_t launch_walk(const fdma_norm_rope_args& a, const WalkView& p, cudaStr
       if (e == cudaSuccess) kern<<<p.plan.grid, kThreads, p.plan.smem, stream>>>(p);
     };
     static std::atomic<uint64_t> ready[2];
-    if (heads) run(norm_rope_kernel<kP, kL, decltype(A)::value, true, BACK>, ready[1]);
+    if (p.plan.per == 1) run(norm_rope_kernel<kP, kL, decltype(A)::value, true, BACK>, ready[1]);
     else run(norm_rope_kernel<kP, kL, decltype(A)::value, false, BACK>, ready[0]);
   });
   return e != cudaSuccess ? e : cudaGetLastError();
@@ -533,7 +539,8 @@ void set_sides(const fdma_norm_rope_args& a, WalkView& p) {
   p.line = {a.N, a.B, static_cast<uint32_t>(a.B) * static_cast<uint32_t>(a.N)};
   p.H[0] = a.Hq;
   p.H[1] = a.Hk;
-  p.pass_l2 = static_cast<int64_t>(a.B) * a.N * (a.Hq + a.Hk) * a.d > kMostInL2 / 2;
+  p.heads = by_head(a);
+  p.pass_l2 = beyond_l2(a);
   for (int s = 0; s < 2; ++s) p.passes[s] = passes_of(p.H[s], pass_rows(a.d, p.v.rot, a.interleaved != 0));
 }
 

@@ -727,6 +727,33 @@ def test_walks_with_a_weight_a_head(I, B, N, Hq, Hk, d, rot):
         _check_backward(c, I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **kw, **c.kw), pos=p)
 
 
+@pytest.mark.parametrize("B,N,Hq,Hk,d", [(1, 40000, 16, 4, 128), (5, 6007, 21, 3, 96)])
+def test_rows_of_more_than_l2_holds(I, B, N, Hq, Hk, d):
+    """Row for row what calls of a few tokens give; the weights' gradients are those calls' sums.  (Each sum, and
+    that of the calls, is off by at most (d + 300) u of the magnitudes, as everywhere here; a turned value is at most the sum of
+    its pair.)"""
+    c = Case(I, B, N, Hq, Hk, d, length=N)
+    pos = torch.randint(-N // 8, N, (B, N), dtype=torch.int32, device="cuda")
+    qo, ko = torch.full_like(c.q, 7.0), torch.full_like(c.k, 7.0)
+    I.norm_rope(c.q, c.k, positions=pos, q_out=qo, k_out=ko, **c.kw)
+    dq, dk, *dw = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, positions=pos, **c.kw)
+    total, mag = [torch.zeros(d, dtype=torch.float64, device="cuda") for _ in range(2)], [0.0, 0.0]
+    for n in range(0, N, N // 5):
+        s = slice(n, n + N // 5)
+        p, a, b = pos[:, s].contiguous(), torch.full_like(qo[:, s], 7.0), torch.full_like(ko[:, s], 7.0)
+        I.norm_rope(c.q[:, s], c.k[:, s], positions=p, q_out=a, k_out=b, **c.kw)
+        assert torch.equal(a, qo[:, s]) and torch.equal(b, ko[:, s])
+        a, b, *w = I.norm_rope_bwd(c.q[:, s], c.k[:, s], c.dq[:, s], c.dk[:, s], positions=p, **c.kw)
+        assert torch.equal(a, dq[:, s]) and torch.equal(b, dk[:, s])
+        for i, (x, g) in enumerate(((c.q, c.dq), (c.k, c.dk))):
+            total[i] += w[i].double()
+            x, g = x[:, s].double(), g[:, s].double().abs() * (p >= 0)[..., None, None]
+            g = g + torch.cat((g[..., d // 2:], g[..., :d // 2]), -1)
+            mag[i] = mag[i] + (g * x.abs() * (x.square().mean(-1, keepdim=True) + 1e-6).rsqrt()).sum((0, 1, 2))
+    for i in range(2):
+        assert ((dw[i].double() - total[i]).abs() <= 2 * (d + 300) * U * mag[i]).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_of_many_tokens(I, fp8):
     """So many that a warp takes whole tokens, with an empty sequence, a sequence of one and rows behind the last."""
