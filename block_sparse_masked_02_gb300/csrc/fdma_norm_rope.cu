@@ -67,7 +67,7 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
 constexpr int kMostChunks = 16;
 
 // Rows of more than L2 holds (129 MB) are read and written as what it drops first: of those written, the first ones would be gone
-// before a next kernel reads them, and the angles stay.  (336 MB of rows: 119 against 126 us.  84 MB: 31.7 either way, but an
+// before a next kernel reads them, and the angles stay.  (336 MB of rows: 113 against 121 us.  84 MB: 31.3 either way, but an
 // attention that follows then finds the outputs in L2.  The backward has no registers for it: 51 against 46, 170 against 175.
 // It takes one pass a chunk instead: 336 MB 162 against 175 us, 671 MB 314 against 355, but 84 MB 49 against 46.)
 constexpr int64_t kMostInL2 = 128 << 20;
@@ -113,11 +113,12 @@ __device__ __forceinline__ void put_columns(float* s, const Pairs<P>& x, const L
   }
 }
 
-// Steps of a warp that are on their way at once: 4 KB of rows, backward 6 KB.  (Forward 3 and 6 KB: 31.1 and 32.4 us
-// against 31.2; backward 4 and 8: 48.2 and 46.7 against 46.0.)  There are angles of a token more than steps, where a token
+// Steps of a warp that are on their way at once: 2 KB of rows, backward 6 KB.  (Forward with 3, 4 and 6 KB: 31.1, 31.3 and 32.4 us
+// against 31.3, and 119, 119 to 124 against 112 to 114 for 65536 tokens: DRAM does better with less in flight; 1 KB with four CTAs an SM
+// 37 and 126.  Backward with 4 and 8: 48.2 and 46.7 against 46.0.)  There are angles of a token more than steps, where a token
 // has several (the last of one token and the first of the next share a slot's turn), else as many.
 template <int P, bool BACK>
-constexpr int kSlots = BACK ? 24 / P : 32 / P;
+constexpr int kSlots = BACK ? 24 / P : 16 / P;
 template <int P, bool BACK>
 constexpr int kRingBytes = kSlots<P, BACK> * (BACK ? 2 : 1) * Ring<P>::kSlot;
 
@@ -402,7 +403,7 @@ WalkPlan walk_plan(const fdma_norm_rope_args& a, bool back) {
   WalkPlan r{};
   const int rot = a.rope != nullptr ? a.rot : 0, piece = piece_of(a.d, rot, a.interleaved != 0),
             rpw = pass_rows(a.d, rot, a.interleaved != 0);
-  const int slots = back ? 24 / piece : 32 / piece;
+  const int slots = back ? 24 / piece : 16 / piece;
   r.table = 4 * rot;
   r.smem = 256 * piece + kWarps * (slots * (back ? 2 : 1) * 128 * piece + (slots + 1) * r.table);
   int per_sm = kSmemPerSm / (r.smem + 1024);
