@@ -707,10 +707,10 @@ int fdma_norm_rope_append(const fdma_norm_rope_args* a, const fdma_kv_cache* c, 
   p.m.check_blocks = (static_cast<unsigned>(c->B) + 31) / 32;
   p.m.err = paged_error_word();
   if (p.m.err == nullptr) return FDMA_ERR_CUDA;
-  p.in[0] = rows_view(*q);
-  p.in[1] = rows_view(*k);
-  p.in[2] = rows_view(*v);
-  p.q_out = rows_view(*q_out);
+  p.in[0] = rows_view(*q, nq);
+  p.in[1] = rows_view(*k, nk);
+  p.in[2] = rows_view(*v, nk);
+  p.q_out = rows_view(*q_out, nq);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   with_layout(c->d, p.v.rot, a->interleaved != 0, [&](auto P, auto L, auto A) {
     constexpr int kP = decltype(P)::value, kL = decltype(L)::value;

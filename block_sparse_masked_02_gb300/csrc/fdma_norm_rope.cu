@@ -521,8 +521,10 @@ int validate_rows(const fdma_rows* r, const int64_t n[3], int d, bool written) {
   return FDMA_OK;
 }
 
-RowsView rows_view(const fdma_rows& r) {
-  return {static_cast<uint16_t*>(r.p), {r.stride[0], r.stride[1], r.stride[2]}};
+RowsView rows_view(const fdma_rows& r, const int64_t n[3]) {
+  RowsView v{static_cast<uint16_t*>(r.p), {}};
+  for (int i = 0; i < 3; ++i) v.st[i] = n[i] > 1 ? r.stride[i] : 0;
+  return v;
 }
 
 namespace {
@@ -552,6 +554,12 @@ int check_sides(const fdma_norm_rope_args& a, const fdma_rows* q, const fdma_row
   return validate_rows(k, nk, a.d, written);
 }
 
+void set_rows(const fdma_norm_rope_args& a, RowsView (&to)[2], const fdma_rows* q, const fdma_rows* k) {
+  const int64_t nq[3] = {a.B, a.N, a.Hq}, nk[3] = {a.B, a.N, a.Hk};
+  to[0] = rows_view(*q, nq);
+  if (a.Hk > 0) to[1] = rows_view(*k, nk);
+}
+
 }  // namespace
 }  // namespace fdma
 
@@ -572,12 +580,8 @@ int fdma_norm_rope(const fdma_norm_rope_args* a, const fdma_rows* q, const fdma_
   WalkView p{};
   p.plan = walk_plan(*a, false);
   set_sides(*a, p);
-  p.x[0] = rows_view(*q);
-  p.out[0] = rows_view(*q_out);
-  if (a->Hk > 0) {
-    p.x[1] = rows_view(*k);
-    p.out[1] = rows_view(*k_out);
-  }
+  set_rows(*a, p.x, q, k);
+  set_rows(*a, p.out, q_out, k_out);
   p.err = paged_error_word();
   if (p.err == nullptr) return FDMA_ERR_CUDA;
   return launch_walk<false>(*a, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FDMA_OK : FDMA_ERR_CUDA;
@@ -617,14 +621,9 @@ int fdma_norm_rope_bwd(const fdma_norm_rope_args* a, const fdma_rows* q, const f
   WalkView p{};
   p.plan = plan;
   set_sides(*a, p);
-  p.g[0] = rows_view(*dq_out);
-  p.out[0] = rows_view(*dq);
-  if (a->norm) p.x[0] = rows_view(*q);
-  if (a->Hk > 0) {
-    p.g[1] = rows_view(*dk_out);
-    p.out[1] = rows_view(*dk);
-    if (a->norm) p.x[1] = rows_view(*k);
-  }
+  if (a->norm) set_rows(*a, p.x, q, k);
+  set_rows(*a, p.g, dq_out, dk_out);
+  set_rows(*a, p.out, dq, dk);
   p.part = want ? static_cast<float*>(workspace) : nullptr;
   p.err = paged_error_word();
   if (p.err == nullptr || launch_walk<true>(*a, p, cs) != cudaSuccess) return FDMA_ERR_CUDA;

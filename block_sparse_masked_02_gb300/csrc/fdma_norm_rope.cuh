@@ -52,7 +52,9 @@ int validate_norm_rope(const fdma_norm_rope_args* a);
 NormRopeView norm_rope_view(const fdma_norm_rope_args& a);
 // Rows of n[0] batches, n[1] tokens and n[2] heads; those that are written must not overlap.
 int validate_rows(const fdma_rows* r, const int64_t n[3], int d, bool written);
-RowsView rows_view(const fdma_rows& r);
+// ... as the kernels take them: the stride of a dimension of one is 0, whatever the caller has there.  Lanes without a row form
+// addresses too (copies of 0 bytes), and those have to be aligned like all others.
+RowsView rows_view(const fdma_rows& r, const int64_t n[3]);
 
 // Pairs of a lane.
 inline int piece_of(int d, int rot, bool adj) { return d % 16 == 0 && (adj || rot % 16 == 0) ? 8 : 4; }

@@ -286,6 +286,28 @@ def test_a_gradient_that_is_not_finite_stays_in_its_row(I):
     assert not torch.isfinite(got[2][100]) and torch.equal(got[2][:100], want[2][:100])
 
 
+def _loose(x):
+    """The same values with strides of 1 in the dimensions of one."""
+    return x.as_strided(x.shape, [1 if n == 1 else s for n, s in zip(x.shape, x.stride())])
+
+
+@pytest.mark.parametrize("d,rot", [(128, 128), (72, 72), (32, 16), (256, 0)])
+@pytest.mark.parametrize("B,N", [(1, 70), (1, 1), (5, 1), (3, 40)])
+def test_strides_of_dimensions_of_one_do_not_matter(I, B, N, d, rot):
+    """One head, token or batch: a pass has fewer rows than lanes for them, and the stride may be anything."""
+    for Hq, Hk, weight in ((1, 1, "shared"), (1, 1, "head"), (1, 3, "shared"), (3, 1, None)):
+        c = Case(I, B, N, Hq, Hk, d, rot, weight, seed=N)
+        q, k, dq, dk = (x.contiguous() for x in (c.q, c.k, c.dq, c.dk))
+        want, grads = I.norm_rope(q, k, **c.kw), I.norm_rope_bwd(q, k, dq, dk, **c.kw)
+        q, k, dq, dk = (_loose(x) for x in (q, k, dq, dk))
+        assert Hq > 1 or q.stride(2) == 1
+        out = [_loose(torch.empty_like(x)) for x in (q, k, dq, dk)]
+        got = I.norm_rope(q, k, q_out=out[0], k_out=out[1], **c.kw)
+        got += I.norm_rope_bwd(q, k, dq, dk, grads=(out[2], out[3], None, None), **c.kw)
+        for x, y in zip(got, want + grads):
+            assert (x is None and y is None) or torch.equal(x, y)
+
+
 def test_no_tokens(I):
     c = Case(I, 1, 3, 2, 1, 64)
     q, k = c.q[:, :0], c.k[:, :0]
@@ -523,6 +545,23 @@ def test_append_in_other_layouts_and_on_another_stream(I, fp8):
     assert torch.equal(got[:n], want[:n])
     for x, y in ((kc, s.kc), (vc, s.vc)) + (((ke, s.ke), (ve, s.ve)) if fp8 else ()):
         assert torch.equal(x[pg, sl].view(torch.uint8), y[pg, sl].view(torch.uint8))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("news", [[1], [9, 3], [700, 900]])
+def test_append_with_any_stride_of_one_head(I, fp8, news):
+    s = Serving(I, news, [12] * len(news), 1, 1, 64, fp8=fp8, extra=0)
+    q, k, v = (x.contiguous() for x in (s.q, s.k, s.v))
+    want = s.P.norm_rope_append(q, k, v, *s.at, s.cu, **s.kw, **s.ex)
+    kept = [x.clone() for x in (s.kc, s.vc, s.ke, s.ve) if x is not None]
+    for x in (s.kc, s.vc):
+        x.view(torch.uint8).fill_(0x55)
+    q, k, v = (_loose(x) for x in (q, k, v))
+    assert k.stride(1) == 1
+    got = s.P.norm_rope_append(q, k, v, *s.at, s.cu, q_out=_loose(torch.empty_like(q)), **s.kw, **s.ex)
+    assert torch.equal(got, want)
+    for x, y in zip([x for x in (s.kc, s.vc, s.ke, s.ve) if x is not None], kept):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
 
 
 def test_append_of_values_that_are_not_finite(I):
