@@ -452,22 +452,28 @@ __device__ __forceinline__ void put_weight(uint32_t at, const Pairs<P>& w) {
   }
 }
 
-// 1 / sqrt(mean(x^2) + eps) of the row.  Values above 2^64 have squares that fp32 does not hold: such a row is
-// multiplied by 2^-70 first (its squares then sum to less than 2^125), `by` says so, and what is returned belongs to
-// the scaled row.  Every lane of the warp calls it.
+// 1 / sqrt(z) of the row, z = mean(x^2) + eps.  fp32 does not hold all squares, and the backward multiplies with 1 / z: a row
+// whose z is not in [2^-64, 2^48) is multiplied by a power of two first, `by` says which, and what is returned belongs to the
+// scaled row (sqrt(z) times `by`).  2^40 leaves z below 2^16 and, as eps is at least 2^-149, above 2^-70; 2^-32 leaves what is
+// finite between 2^-16 and 2^64; 2^-70, where it is not, sums below 2^125.  What a scaled row loses of its smallest values is less
+// than bf16's least step in the output.  Ordinary rows are not touched, rows of zeros with an ordinary eps among them.  (Squares
+// that overflow alone: with rows of 2^60 and gradients of 2^-30, 1 / z times the mean was a subnormal and two thirds of the
+// gradient's projection were lost; with eps below 2^-128, 1 / z was infinite.)  Every lane of the warp calls it.
 template <int LPR, int P>
 __device__ __forceinline__ float row_rsqrt(const NormRopeView& v, Pairs<P>& x, float& by) {
-  float s = row_sum<LPR>(dot(x, x));
+  constexpr uint32_t kLeast = (127 - 64) << 23, kMost = (127 + 48) << 23;  // (as bits; NaN is above them)
+  float z = row_sum<LPR>(dot(x, x)) * v.inv_d + v.eps;
   by = 1.f;
-  const bool over = s == __int_as_float(0x7f800000);
-  if (__any_sync(0xffffffffu, over)) {
-    if (over) {
-      by = 0x1p-70f;
+  const uint32_t bits = __float_as_uint(z);
+  const bool out = bits - kLeast >= kMost - kLeast;
+  if (__any_sync(0xffffffffu, out)) {
+    if (out) {
+      by = bits < kLeast ? 0x1p40f : z == __int_as_float(0x7f800000) ? 0x1p-70f : 0x1p-32f;
       scale(x, by);
     }
-    s = row_sum<LPR>(dot(x, x));
+    z = row_sum<LPR>(dot(x, x)) * v.inv_d + v.eps * by * by;
   }
-  return rsqrtf(s * v.inv_d + v.eps * by * by);
+  return rsqrtf(z);
 }
 
 // Position of a token, checked: -1 where it is left out.

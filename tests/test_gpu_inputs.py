@@ -275,6 +275,30 @@ def test_rows_of_any_size(I):
         assert torch.isfinite(got).sum() == got.numel() - 2 and torch.isinf(got[0, 3, 0, 20]) and torch.isnan(got[0, 4, 0, 63])
 
 
+def test_rows_near_both_ends_of_fp32(I):
+    """Rows so large or small that the squares of their norms, or the norms' inverses, leave fp32, with small gradients.  The
+    bounds are those of all rows: they count relative roundings alone, so no step may leave fp32's normal range."""
+    c = Case(I, 1, 48, 2, 1, 128, 64)
+    at = 0
+    for power in (30, 45, 56, 60, 63, 66, 90):  # (their gradients are of 2^-power times those of the output)
+        for small in (0, 20, 30, 40):
+            c.q[0, at] *= 2.0 ** power
+            c.dq[0, at] *= 2.0 ** -small
+            at += 1
+    _check_forward(c, I.norm_rope(c.q, c.k, **c.kw))
+    _check_backward(c, I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **c.kw))
+    for eps in (1e-30, 1e-38, 1e-40, 2.0 ** -149):
+        eps = float(np.float32(eps))
+        c = Case(I, 1, 48, 2, 1, 128, 64, seed=1)
+        for i, power in enumerate((-30, -50, -60, -64, -70, -75, -80, -100, -120)):
+            c.q[0, 2 * i] *= 2.0 ** power
+            c.q[0, 2 * i + 1] *= 2.0 ** power
+            c.dq[0, 2 * i + 1] *= 2.0 ** 10
+        c.q[0, 20:30] = 0
+        _check_forward(c, I.norm_rope(c.q, c.k, eps=eps, **c.kw), eps=eps)
+        _check_backward(c, I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, eps=eps, **c.kw), eps=eps)
+
+
 def test_a_gradient_that_is_not_finite_stays_in_its_row(I):
     c = Case(I, 1, 40, 2, 1, 128, 64)
     want = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **c.kw)
