@@ -293,11 +293,13 @@ def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=No
     """The gradients (dq, dk, dq_weight, dk_weight) from those of `norm_rope`'s outputs, given its inputs: dq and dk bf16
     (zero for tokens that were left out), the weights' fp32, (d) or (heads, d) like the weights; None for what is not
     there or, with want_dweight=False, not wanted.  grads=(dq, dk, dq_weight, dk_weight) are written where they are not
-    None; dq and dk may be dq_out and dk_out themselves.  A workspace passed in (uint8, `norm_rope_bwd_workspace`)
-    serves one call at a time."""
+    None (one that the call would not write is refused); dq and dk may be dq_out and dk_out themselves.  A workspace
+    passed in (uint8, `norm_rope_bwd_workspace`) serves one call at a time."""
     g = (None,) * 4 if grads is None else tuple(grads)
     if len(g) != 4:
         raise ValueError("grads must be (dq, dk, dq_weight, dk_weight)")
+    if not want_dweight and (g[2] is not None or g[3] is not None):
+        raise ValueError("grads holds a weight's gradient that want_dweight=False leaves out")
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
     dev = _check_device(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace, *g)

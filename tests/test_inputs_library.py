@@ -259,3 +259,12 @@ def test_workspaces_depend_on_sizes_alone(I):
     size = lambda **kw: lib.fdma_norm_rope_bwd_workspace_size(bytes(_args(I, **kw)))  # noqa: E731
     assert size() == size(first=1, rope_len=11) == size(norm=1, rope=None, rot=0, rope_len=0)
     assert size(N=50000) < 2 ** 20 and size(q_weight_head=128, k_weight_head=128, N=50000) < 2 ** 23
+
+
+def test_weights_gradients_that_are_not_wanted_are_not_taken(I):
+    import torch
+
+    x, w = torch.zeros(1, 2, 64, dtype=torch.bfloat16), torch.ones(64)
+    for grads in ((None, None, w, None), (None, None, None, w)):
+        with pytest.raises(ValueError, match="want_dweight"):
+            I.norm_rope_bwd(x, x, x, x, q_weight=w, k_weight=w, want_dweight=False, grads=grads)
