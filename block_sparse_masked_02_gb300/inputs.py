@@ -222,8 +222,6 @@ def _launch_norm_rope(args, q, k, q_out, k_out, sp):
             k_out, kor = _new_rows(k)
         else:
             kor = _rows("k_out", k_out, k.shape)
-    else:
-        k_out = None
     st = load().fdma_norm_rope(args, _rows("q", q), kr, qor, kor, sp)
     if st:
         _fdma._raise(st, "fdma_norm_rope")
@@ -242,6 +240,8 @@ def norm_rope(q, k=None, *, q_weight=None, k_weight=None, rope=None, positions=N
     at a negative position is padding and its rows are left as they are (uninitialised where the outputs are
     allocated here).  A position behind the table is left out too and reported by `fdma.device_error()`.  q_out and
     k_out may be q and k themselves."""
+    if k is None and k_out is not None:
+        raise ValueError("an output for keys without keys")
     dev = _check_device(q, k, q_weight, k_weight, rope, positions, q_out, k_out)
     args = _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps)
     guard, sp = _on(dev, stream)
@@ -262,8 +262,6 @@ def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweig
         else:
             ko = _rows("dk", dk, k.shape)
         kr, kg = _rows("k", k), _rows("dk_out", dk_out, k.shape)
-    else:
-        dk = None
     n = wp = own = 0
     if want_dweight:
         dw = [torch.empty_like(w, dtype=_FP32, memory_format=torch.contiguous_format) if t is None and w is not None else t
@@ -302,6 +300,8 @@ def norm_rope_bwd(q, k, dq_out, dk_out, *, q_weight=None, k_weight=None, rope=No
         raise ValueError("grads holds a weight's gradient that want_dweight=False leaves out")
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
+    if k is None and g[1] is not None:
+        raise ValueError("an output for keys without keys")
     dev = _check_device(q, k, dq_out, dk_out, q_weight, k_weight, rope, positions, workspace, *g)
     args = _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleaved, norm, eps)
     for name, w, t in (("dq_weight", q_weight, g[2]), ("dk_weight", k_weight, g[3])):

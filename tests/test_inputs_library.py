@@ -268,3 +268,13 @@ def test_weights_gradients_that_are_not_wanted_are_not_taken(I):
     for grads in ((None, None, w, None), (None, None, None, w)):
         with pytest.raises(ValueError, match="want_dweight"):
             I.norm_rope_bwd(x, x, x, x, q_weight=w, k_weight=w, want_dweight=False, grads=grads)
+
+
+def test_outputs_for_keys_without_keys_are_not_taken(I):
+    import torch
+
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="without keys"):
+        I.norm_rope(x, k_out=x)
+    with pytest.raises(ValueError, match="without keys"):
+        I.norm_rope_bwd(x, None, x, None, grads=(None, x, None, None))
