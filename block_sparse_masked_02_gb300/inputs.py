@@ -154,7 +154,7 @@ def _weight(name, w, H, d):
     elif dt is not None and shape == (H, d):
         head, one = w.stride()
         if one == 1 and (H == 1 or head >= d):
-            return w.data_ptr(), max(head, d), dt
+            return w.data_ptr(), head if H > 1 else d, dt
     raise ValueError(f"{name} must be fp32 or bf16, ({d},) or ({H}, {d}), its heads apart and contiguous")
 
 

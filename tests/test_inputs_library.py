@@ -278,3 +278,14 @@ def test_outputs_for_keys_without_keys_are_not_taken(I):
         I.norm_rope(x, k_out=x)
     with pytest.raises(ValueError, match="without keys"):
         I.norm_rope_bwd(x, None, x, None, grads=(None, x, None, None))
+
+
+def test_a_weight_of_one_head_may_have_any_stride(I):
+    import torch
+
+    w = torch.ones(1, 129)[:, :128]
+    assert I._weight("w", w, 1, 128) == (w.data_ptr(), 128, I.FDMA_FP32)
+    w = w.as_strided((1, 128), (1, 1))
+    assert I._weight("w", w, 1, 128) == (w.data_ptr(), 128, I.FDMA_FP32)
+    w = torch.ones(2, 136)[:, :128]
+    assert I._weight("w", w, 2, 128) == (w.data_ptr(), 136, I.FDMA_FP32)
