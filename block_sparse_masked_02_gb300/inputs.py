@@ -198,8 +198,11 @@ def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleave
             raise ValueError(f"positions must be int32 ({N},) or ({B}, {N})")
         pp, sn = positions.data_ptr(), st[-1]
         sb = st[0] if len(st) == 2 else 0
-    return _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt or 0, qw, qh, kw, kh, rp, length, rot,
-                           1 if interleaved else 0, first, pp, sb, sn)
+    try:
+        return _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt or 0, qw, qh, kw, kh, rp, length, rot,
+                               1 if interleaved else 0, first, pp, sb, sn)
+    except (struct.error, OverflowError):
+        raise ValueError("sizes and first must be whole numbers of 32 bits, eps a number that fp32 holds") from None
 
 
 def rope_table(length, rot, *, base=10000.0, device="cuda"):
@@ -347,8 +350,11 @@ def _rel_args(H, Nq, Nk, starts, bidirectional, offset):
     n = len(starts)
     if not 0 < n <= MAX_BUCKETS:
         raise ValueError(f"1 to {MAX_BUCKETS} buckets a side")
-    return (_PACK_REL(H, Nq, Nk, n, 1 if bidirectional else 0, Nk - Nq if offset is None else offset),
-            struct.pack(f"{n}i", *starts))
+    try:
+        return (_PACK_REL(H, Nq, Nk, n, 1 if bidirectional else 0, Nk - Nq if offset is None else offset),
+                struct.pack(f"{n}i", *starts))
+    except struct.error:
+        raise ValueError("sizes, offset and starts must be whole numbers of 32 bits") from None
 
 
 def _launch_rel_bias(args, first, table, dt, out, shape, sp):

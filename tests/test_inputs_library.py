@@ -289,3 +289,15 @@ def test_a_weight_of_one_head_may_have_any_stride(I):
     assert I._weight("w", w, 1, 128) == (w.data_ptr(), 128, I.FDMA_FP32)
     w = torch.ones(2, 136)[:, :128]
     assert I._weight("w", w, 2, 128) == (w.data_ptr(), 136, I.FDMA_FP32)
+
+
+def test_numbers_that_the_structs_do_not_hold_are_refused(I):
+    import torch
+
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    for first, eps in ((1 << 31, 1e-6), (-(1 << 31) - 1, 1e-6), (0.5, 1e-6), (0, 1e39), (0, "1")):
+        with pytest.raises(ValueError):
+            I._norm_rope_args(x, None, None, None, None, None, first, False, True, eps)
+    for starts, Nq, offset in (((0, 1 << 31), 8, None), ((0, 1.5), 8, None), ((0, 1), 8, 1 << 31), ((0, 1), 1 << 31, 0), ((0, 1), 8, 0.5)):
+        with pytest.raises(ValueError):
+            I._rel_args(1, Nq, 8, starts, False, offset)
