@@ -89,6 +89,7 @@ def load() -> ctypes.CDLL:
 
 
 _BF16, _FP32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_FP32_MAX = torch.finfo(torch.float32).max
 # (a torch built without CUDA has none of these; it can still import this)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -199,10 +200,13 @@ def _norm_rope_args(q, k, q_weight, k_weight, rope, positions, first, interleave
         pp, sn = positions.data_ptr(), st[-1]
         sb = st[0] if len(st) == 2 else 0
     try:
-        return _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt or 0, qw, qh, kw, kh, rp, length, rot,
+        args = _PACK_NORM_ROPE(B, N, Hq, Hk, d, 1 if norm else 0, eps, wt or 0, qw, qh, kw, kh, rp, length, rot,
                                1 if interleaved else 0, first, pp, sb, sn)
-    except (struct.error, OverflowError):
-        raise ValueError("sizes and first must be whole numbers of 32 bits, eps a number that fp32 holds") from None
+    except struct.error:
+        args = None
+    if args is None or eps > _FP32_MAX:
+        raise ValueError("sizes and first must be whole numbers of 32 bits, eps a number that fp32 holds")
+    return args
 
 
 def rope_table(length, rot, *, base=10000.0, device="cuda"):
