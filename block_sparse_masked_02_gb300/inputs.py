@@ -91,9 +91,10 @@ def load() -> ctypes.CDLL:
 _BF16, _FP32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _FP32_MAX = torch.finfo(torch.float32).max
 # (a torch built without CUDA has none of these; it can still import this)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-# A call's own workspace comes from the caching allocator without a tensor around it, which would cost 3 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+# A call's own workspace comes from the caching allocator without a tensor around it, which would cost 3 us (a torch that does
+# not have these calls makes the tensor).
 _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
 _raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
 
@@ -117,6 +118,21 @@ def _on(dev, stream):
     if stream.device.index != dev:
         raise ValueError("the stream belongs to another device than the tensors")
     return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _workspace(n, dev, sp):
+    """(address of n bytes for a call on the stream sp, which is current; the raw block or the tensor that holds them)."""
+    if _raw_alloc is None or _raw_delete is None:
+        t = torch.empty(n, dtype=torch.uint8, device=dev)
+        return t.data_ptr(), t
+    p = _raw_alloc(n, sp)
+    return p, p
+
+
+def _release(own):
+    """Gives a workspace back: what is allocated next on its stream runs behind the kernels that were launched with it."""
+    if type(own) is int and own:
+        _raw_delete(own)
 
 
 def _run(guard, call, *args):
@@ -282,11 +298,10 @@ def _launch_norm_rope_bwd(args, q, k, dq_out, dk_out, weights, grads, want_dweig
         dw = (None, None)
     rows = (_rows("q", q), kr, _rows("dq_out", dq_out, q.shape), kg, qo, ko)
     if n and ws is None:
-        wp = own = _raw_alloc(n, sp)
+        wp, own = _workspace(n, q.device, sp)
     st = lib.fdma_norm_rope_bwd(args, *rows, None if dw[0] is None else dw[0].data_ptr(),
                                 None if dw[1] is None else dw[1].data_ptr(), wp, n, sp)
-    if own:  # (what is allocated next on this stream runs behind the kernels)
-        _raw_delete(own)
+    _release(own)
     if st:
         _fdma._raise(st, "fdma_norm_rope_bwd")
     return dq, dk, dw[0], dw[1]
@@ -395,16 +410,16 @@ def _launch_rel_bias_bwd(args, first, dbias, causal, dtable, shape, ws, sp):
     st = dbias.stride()
     if dtable is None:
         dtable = torch.empty(shape, dtype=_FP32, device=dbias.device)
-    B, own = dbias.shape[0], 0
+    B, wp, own = dbias.shape[0], 0, 0
     if ws is None:
         n = lib.fdma_rel_bias_bwd_workspace_size(args, B)
-        wp = own = _raw_alloc(n, sp) if n else 0
+        if n:
+            wp, own = _workspace(n, dbias.device, sp)
     else:
         wp, n = ws.data_ptr(), ws.numel() * ws.element_size()
     st = lib.fdma_rel_bias_bwd(args, first, B, dbias.data_ptr(), _PACK_3Q(st[0], st[1], st[2]), 1 if causal else 0, dtable.data_ptr(),
                                wp, n, sp)
-    if own:  # (what is allocated next on this stream runs behind the kernels)
-        _raw_delete(own)
+    _release(own)
     if st:
         _fdma._raise(st, "fdma_rel_bias_bwd")
     return dtable

@@ -998,3 +998,38 @@ def test_calls_on_another_stream(I):
     for o, w in zip(got, want + want):
         for x, y in zip(o, w):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_backward_passes_without_workspaces_in_a_captured_graph(I, raw, monkeypatch):
+    """What a call allocates for itself inside a capture lives as long as the graph: replays follow the inputs, and what is
+    allocated between them changes nothing.  Also with a torch that lends no memory without a tensor around it."""
+    if not raw:
+        monkeypatch.setattr(I, "_raw_alloc", None)
+    starts = I.rel_starts(32, 128)
+    cases = [Case(I, 1, 700, 4, 2, 128, seed=30 + i) for i in range(3)]
+    dbs = [torch.randn(1, 2, 512, 1024, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(3)]
+
+    def run(c, db):
+        return I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **c.kw) + (I.rel_bias_bwd(db, starts),)
+
+    want = [[x.clone() for x in run(c, db)] for c, db in zip(cases, dbs)]
+    now, db = Case(I, 1, 700, 4, 2, 128, seed=40), torch.zeros_like(dbs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(now, db)
+    for c, d, w in list(zip(cases, dbs, want)) * 2:
+        for x, y in ((now.q, c.q), (now.k, c.k), (now.dq, c.dq), (now.dk, c.dk), (now.w[0], c.w[0]), (now.w[1], c.w[1]), (db, d)):
+            x.copy_(y)
+        graph.replay()
+        other = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 10, 1 << 16, 1 << 20)]
+        for x, y in zip(out, w):
+            assert torch.equal(x, y)
+        del other
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    c = cases[0]
+    got = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, stream=side, **c.kw) + (I.rel_bias_bwd(dbs[0], starts, stream=side),)
+    side.synchronize()
+    for x, y in zip(got, want[0]):
+        assert torch.equal(x, y)
