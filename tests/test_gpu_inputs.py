@@ -1033,3 +1033,67 @@ def test_backward_passes_without_workspaces_in_a_captured_graph(I, raw, monkeypa
     side.synchronize()
     for x, y in zip(got, want[0]):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d,rot,interleaved", [(64, 64, False), (96, 32, False), (80, 80, True), (128, 24, False)])
+def test_append_without_a_norm(I, fp8, d, rot, interleaved):
+    s = Serving(I, [7, 1, 40], [9, 60, 0], 5, 3, d, fp8=fp8, rot=rot, weight=None, seed=d)
+    kw = dict(rope=s.rope, interleaved=interleaved, norm=False)
+    q_out = torch.full_like(s.q, 7.0)
+    s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, q_out=q_out, **kw, **s.ex)
+    n = 48
+    positions = torch.tensor(s.pos[:n], dtype=torch.int32, device="cuda")
+    q, k = I.norm_rope(s.q[:n], s.k[:n], positions=positions, **kw)
+    assert torch.equal(q_out[:n], q) and (q_out[n:] == 7).all()
+    t = _np(s.rope)[s.pos[:n]]
+    (qr, qm), (kr, km) = [orc.norm_rope(_np(x[:n]), None, t[:, None, 0], t[:, None, 1], interleaved, False, 1e-6) for x in (s.q, s.k)]
+    _check_rows(q, qr, qm, d)
+    pg, sl = (torch.tensor(x, device="cuda") for x in s.slots())
+    if not fp8:
+        assert torch.equal(s.kc[pg, sl], k) and torch.equal(s.vc[pg, sl], s.v[:n])
+        return
+    code, byte = porc.quantise(_np(s.v[:n]))
+    assert np.array_equal(s.vc.view(torch.uint8)[pg, sl].cpu().numpy(), code)
+    assert np.array_equal(s.ve[pg, sl].cpu().numpy(), byte)
+    # each code is the fp32 value rounded once: half a step of e4m3, of its least step where it has no normal code
+    delta = (d / 2 + 12) * U * km
+    e = s.ke[pg, sl].cpu().numpy().astype(np.float64)
+    val = porc.dequantise(s.kc.view(torch.uint8)[pg, sl].cpu().numpy(), e.astype(np.uint8))
+    tol = delta + np.maximum(2.0 ** -4 * (np.abs(kr) + delta), 2.0 ** -10 * 2.0 ** (e - 127)[..., None])
+    assert (np.abs(val - kr) <= tol).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("news", [[5, 1, 33], [3000, 2500]])
+def test_append_in_place(I, fp8, news):
+    """q_out being q: short runs of a token's rows a warp, and whole tokens."""
+    s = Serving(I, news, [9] * len(news), 6, 2, 64, fp8=fp8, rot=32)
+    n = sum(news)
+    q = s.q.clone()
+    want = s.P.norm_rope_append(q, s.k, s.v, *s.at, s.cu, **s.kw, **s.ex)
+    kc, vc = s.kc.clone(), s.vc.clone()
+    behind = s.q[n:].clone()
+    assert s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, q_out=s.q, **s.kw, **s.ex) is s.q
+    assert torch.equal(s.q[:n], want[:n]) and torch.equal(s.q[n:], behind)
+    pg, sl = (torch.tensor(x, device="cuda") for x in s.slots())
+    for x, y in ((s.kc, kc), (s.vc, vc)):
+        assert torch.equal(x[pg, sl].view(torch.uint8), y[pg, sl].view(torch.uint8))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("N,Hq,Hk,d,rot", [(40000, 16, 4, 128, 128), (30000, 21, 3, 104, 40)])
+def test_rows_of_more_than_l2_holds_in_place(I, N, Hq, Hk, d, rot, interleaved):
+    c = Case(I, 1, N, Hq, Hk, d, rot)
+    pos = torch.randint(-N // 8, N, (N,), dtype=torch.int32, device="cuda")
+    kw = dict(interleaved=interleaved, positions=pos, **c.kw)
+    qo, ko = c.q.clone(), c.k.clone()
+    I.norm_rope(c.q, c.k, q_out=qo, k_out=ko, **kw)
+    grads = I.norm_rope_bwd(c.q, c.k, c.dq, c.dk, **kw)
+    dq, dk = c.dq.clone(), c.dk.clone()
+    got = I.norm_rope_bwd(c.q, c.k, dq, dk, grads=(dq, dk, None, None), **kw)
+    assert got[0] is dq and got[1] is dk
+    for x, y in zip(got, grads):
+        assert torch.equal(x, y)
+    I.norm_rope(c.q, c.k, q_out=c.q, k_out=c.k, **kw)
+    assert torch.equal(c.q, qo) and torch.equal(c.k, ko)
