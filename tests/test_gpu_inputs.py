@@ -1097,3 +1097,50 @@ def test_rows_of_more_than_l2_holds_in_place(I, N, Hq, Hk, d, rot, interleaved):
         assert torch.equal(x, y)
     I.norm_rope(c.q, c.k, q_out=c.q, k_out=c.k, **kw)
     assert torch.equal(c.q, qo) and torch.equal(c.k, ko)
+
+
+@pytest.mark.parametrize("seed", range(32))
+def test_random_appends(I, seed):
+    """Every width of a cache's rows, any part of it turned, random batches and layouts: bit for bit what norm_rope and
+    kv_append give (an e4m3 cache's keys, which take their codes from values that are rounded once less: within that of
+    the codes' own bound)."""
+    r = np.random.default_rng(3000 + seed)
+    fp8 = seed % 4 == 3
+    d = 16 * int(r.integers(1, 9)) if fp8 else 8 * (seed % 16 + 1)
+    rot = 8 * int(r.integers(0, d // 8 + 1))
+    Hq, Hkv = int(r.integers(1, 14)), int(r.integers(1, 7))
+    inter, norm = bool(r.integers(0, 2)), bool(rot == 0 or r.integers(0, 4))
+    weight = [None, "shared", "head"][seed % 3] if norm else None
+    news = [int(2 ** r.uniform(0, 8)) - 1 for _ in range(int(r.integers(1, 8)))]
+    olds = [int(r.integers(0, 100)) for _ in news]
+    s = Serving(I, news, olds, Hq, Hkv, d, [16, 64][seed % 2], fp8, rot, weight, seed=seed, wdtype=[torch.float32, torch.bfloat16][seed % 2])
+    kw, n = dict(interleaved=inter, norm=norm, **s.kw), sum(news)
+    q_out = torch.full_like(s.q, 7.0)
+    s.P.norm_rope_append(s.q, s.k, s.v, *s.at, s.cu, q_out=q_out, **kw, **s.ex)
+    pos = torch.tensor(s.pos, dtype=torch.int32, device="cuda")
+    q2, k2 = torch.full_like(s.q, 7.0), torch.zeros_like(s.k)
+    I.norm_rope(s.q, s.k, positions=pos, q_out=q2, k_out=k2, **kw)
+    assert torch.equal(q_out, q2)
+    got = [x.clone() for x in (s.kc, s.vc, s.ke, s.ve) if x is not None]
+    for x in (s.kc, s.vc):
+        x.view(torch.uint8).fill_(0x55)
+    if fp8:
+        s.ke.fill_(9)
+        s.ve.fill_(9)
+    s.P.kv_append(k2, s.v, *s.at, s.cu, **s.ex)
+    assert torch.equal(got[1].view(torch.uint8), s.vc.view(torch.uint8))
+    if not fp8:
+        assert torch.equal(got[0].view(torch.uint8), s.kc.view(torch.uint8))
+        return
+    assert torch.equal(got[3], s.ve)
+    pg, sl = s.slots()
+    keep = np.ones(s.kc.shape[:2], dtype=bool)
+    keep[pg, sl] = False
+    assert np.array_equal(got[0].view(torch.uint8).cpu().numpy()[keep], s.kc.view(torch.uint8).cpu().numpy()[keep])
+    assert np.array_equal(got[2].cpu().numpy()[keep], s.ke.cpu().numpy()[keep])
+    code, e = got[0].view(torch.uint8).cpu().numpy()[pg, sl], got[2].cpu().numpy()[pg, sl]
+    # k2 is the fp32 value y to half a step of bf16: |y| <= |k2| (1 + 2^-7); the code is y to half a step of e4m3
+    k = np.abs(_np(k2[:n])) * (1 + 2.0 ** -7) + 2.0 ** -133
+    step = 2.0 ** (e.astype(np.float64) - 127)[..., None]
+    tol = 2.0 ** -7 * k + 2.0 ** -133 + np.maximum(2.0 ** -4 * k, 2.0 ** -10 * step)
+    assert (np.abs(porc.dequantise(code, e) - _np(k2[:n])) <= tol).all()
