@@ -17,9 +17,9 @@
 // as much 26), backward 46 us (260 MB, 5.6 TB/s; 38), of which the sum of the weights' parts 2.  Two sequences of 4096 tokens of 32 + 8
 // heads with a weight each, half of the columns turned, backward: 49 us (253 MB, 5.2 TB/s; 37), as every pass is then a new token's
 // (54 us where such a walk went through the loop over a token's passes, and found every row's address from its token's number).  What bounds both is
-// issue and latency (issue slots 63 and 51 % busy at 24 and 16 warps an SM), no longer the wait for memory (stalls on it: 0.3 of 8
-// cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1 take 35 and 55 us for 75 MB, as a key's row then has a pass
-// to itself.
+// issue and latency (issue slots 63 and 52 % busy at 24 and 16 warps an SM), no longer the wait for memory (stalls on it: 0.3 of 8
+// cycles an instruction).  Few heads cost more: 32768 tokens of 8 + 1 take 33 us for 168 MB and 55 for 243 (25 and 36 at a copy's
+// rate), as a key's row then has a pass to itself.
 //
 // Steps that led here (the first case forward / backward, us): a row a lane group, addresses for each 52 / 102; a warp a token,
 // arithmetic on pairs, pieces of 16 bytes 39 / 80; rows on their way in shared memory 36 / 70; angles and weights there too 34
@@ -66,10 +66,13 @@ __device__ __forceinline__ int position_of(const NormRopeView& v, int b, int n) 
 
 constexpr int kMostChunks = 16;
 
-// Rows of more than L2 holds (129 MB) are read and written as what it drops first: of those written, the first ones would be gone
-// before a next kernel reads them, and the angles stay.  (336 MB of rows: 113 against 121 us.  84 MB: 31.3 either way, but an
-// attention that follows then finds the outputs in L2.  The backward has no registers for it: 51 against 46, 170 against 175.
-// It takes one pass a chunk instead: 336 MB 162 against 175 us, 671 MB 314 against 355, but 84 MB 49 against 46.)
+// Where the input's rows, of q and k together, are more than 134 MB, the forward reads and writes rows as what L2 (129 MB) drops first:
+// there are as many bytes of output, and the first of them would be gone before a next kernel reads them, while the angles stay.
+// (MB of rows, of heads of 16 + 4: us usual / so.  84: 30.2 / 28.3, 105: 37.6 / 37.2, 126: 43.5 / 42.6, 147: 50.6 / 49.8, 168: 56.6 / 55.6, 252:
+// 87.7 / 83.5, 336: 118 / 111.  So alone it would pay from 84 MB on, but the attention that follows then does not find the outputs in L2.)
+// The backward has no registers for it (51 against 46 us, 170 against 175).  It takes one pass a chunk there instead: 84 MB 45.0 / 48.4,
+// 105: 56.0 / 57.2, 126: 65.4 / 66.8, 147: 75.0 / 76.2, 168: 85.4 / 85.6, 252: 127 / 124, 336: 173 / 163, 671: 355 / 314.  (That crosses at about
+// 180 MB: from 134 MB to there the common limit costs up to 1.6 %.)
 constexpr int64_t kMostInL2 = 128 << 20;
 bool beyond_l2(const fdma_norm_rope_args& a) {
   return static_cast<int64_t>(a.B) * a.N * (static_cast<int64_t>(a.Hq) + a.Hk) > kMostInL2 / (2 * a.d);

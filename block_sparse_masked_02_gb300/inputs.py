@@ -390,8 +390,10 @@ def rel_bias(table, Nq, Nk, starts, *, bidirectional=True, offset=None, out=None
     """The bias (1, H, Nq, Nk) bf16 of a learned table (buckets, H), fp32 or bf16: table[bucket(j - (i + offset)), h] for
     query row i and key j.  starts holds the first distance of each bucket of one side (`rel_starts`): a distance is in the
     last bucket that begins at it or before.  One-sided, keys behind the query are at distance 0; bidirectional, they
-    have the second half of the table.  offset is the position of query row 0 among the keys, by default Nk - Nq (as
-    `fdma.fwd`'s causal).  Nk is a multiple of 8.  `expand` it over a batch."""
+    have the second half of the table.  H is the number of kv heads, as `fdma.fwd` takes a bias (B, Hkv, Nq, Nk) (or 1, to
+    be expanded over them; the gradient is then the sum of `rel_bias_bwd`'s columns): query heads that share a kv head share
+    its bias.  offset is the position of query row 0 among the keys, by default Nk - Nq (as `fdma.fwd`'s causal).  Nk is a
+    multiple of 8.  `expand` it over a batch."""
     dev = _check_device(table, out)
     dt, shape = table.dtype, table.shape
     dt = FDMA_FP32 if dt is _FP32 else FDMA_BF16 if dt is _BF16 else None

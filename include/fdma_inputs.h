@@ -93,7 +93,7 @@ FDMA_API int fdma_norm_rope_append(const fdma_norm_rope_args* args, const fdma_k
 #define FDMA_MAX_BUCKETS 256 /* of one side */
 
 /* A learned bias by distance: bias[h, i, j] = table[bucket(j - i - offset), h] for query row i at position i + offset
-   and key j.  One side (two_sided 0): the bucket of delta is that of the distance max(-delta, 0); two_sided: that of
+   and key j; h runs over kv heads, as in the bias that fdma_fwd takes.  One side (two_sided 0): the bucket of delta is that of the distance max(-delta, 0); two_sided: that of
    |delta|, plus num_starts where delta > 0.  A distance a is in the last bucket s with starts[s] <= a.  starts is a HOST
    array of num_starts values, copied by the call: starts[0] = 0, none smaller than the one before. */
 typedef struct fdma_rel_args {

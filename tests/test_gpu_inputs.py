@@ -895,6 +895,26 @@ def test_a_training_step(I):
         assert rel <= 1e-2 + 3 * 2.0 ** -8, rel
 
 
+def test_a_bias_of_one_head_for_all(I):
+    """A table of one head, its bias expanded over batch and kv heads: as a table with that column for each kv head."""
+    from block_sparse_masked_02_gb300 import fdma
+
+    B, N, Hq, Hk, d = 2, 160, 4, 2, 64
+    g = torch.Generator().manual_seed(6)
+    q, k, v, do = (_rows(g, B, N, H, d) for H in (Hq, Hk, Hk, Hq))
+    starts = I.rel_starts(16, 64, bidirectional=False)
+    table = torch.randn(16, 1, generator=g).cuda()
+    res = []
+    for t in (table, table.expand(16, Hk)):
+        bias = I.rel_bias(t, N, N, starts, bidirectional=False).expand(B, Hk, -1, -1)
+        out, lse = fdma.fwd(q, k, v, bias=bias, causal=True)
+        db = fdma.bwd(q, k, v, out, do, lse, bias=bias, causal=True)[3]
+        res.append((out, lse, I.rel_bias_bwd(db, starts, bidirectional=False, causal=True)))
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+    assert res[0][2].shape == (16, Hk)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_serving_steps_from_a_captured_graph(I, fp8):
     """norm_rope_append and the attention over the cache, captured once and replayed for several steps: bit for bit what
